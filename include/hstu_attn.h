@@ -313,6 +313,164 @@ HSTU_API hstu_status_t hstu_attn_build_func(const hstu_func_spec_t* spec, const 
 HSTU_API hstu_status_t hstu_attn_build_func_candidates(const int32_t* seq_offsets, int32_t batch, int32_t nfunc,
                                                        int32_t* func_c, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Serving: rotary positions, a paged K/V cache, and candidate rows against it.
+ * These are additions of this library; the pages have no counterpart. The
+ * attention kernels take no positional bias, so positions reach the scores
+ * through q and k. A server keeps each user's K/V rows between requests in
+ * pages, appends the rows of a new request (hstu_attn_cache_write) and scores
+ * candidate rows against all of them (hstu_attn_fwd_paged).
+ * ------------------------------------------------------------------------ */
+
+/* How the frequencies f_i = base^(-2i/R) of the R/2 pairs are changed for
+ * contexts `factor` times as long as the trained one. */
+#define HSTU_ROPE_NONE 0   /* not at all; factor is ignored */
+#define HSTU_ROPE_LINEAR 1 /* f_i / factor (position interpolation) */
+#define HSTU_ROPE_NTK 2    /* base * factor^(R/(R-2)) in place of base (R > 2) */
+#define HSTU_ROPE_YARN 3   /* with r_i = original_len f_i / 2 pi turns over the
+                              trained length: f_i if r_i >= fast_turns, f_i /
+                              factor if r_i <= slow_turns, the linear blend
+                              between; rotated values are multiplied by
+                              0.1 ln(factor) + 1 */
+typedef struct {
+  int32_t rotary_dim;   /* R: leading columns of a head that are rotated, a
+                           multiple of 16 from 16 to 128 */
+  int32_t scaling;      /* HSTU_ROPE_* */
+  double base;          /* > 1 */
+  double factor;        /* >= 1 */
+  double original_len;  /* YARN: the trained length, >= 1 */
+  double fast_turns;    /* YARN: > slow_turns */
+  double slow_turns;    /* YARN: > 0 */
+} hstu_rope_spec_t;
+
+/* A rotation as the kernels take it. */
+typedef struct {
+  const uint64_t* turns; /* DEVICE (R/2), 8-byte aligned: the frequencies in
+                            turns a position, as fractions of 2^64 */
+  int32_t rotary_dim;    /* R */
+  int32_t interleaved;   /* 0: pairs (i, i + R/2); 1: pairs (2i, 2i + 1) */
+  float magnitude;       /* multiplies the rotated columns */
+} hstu_rope_t;
+
+/* Host-only: fills turns (HOST uint64 (R/2)) and magnitude from the spec; the
+ * caller copies turns to the device once. The phase of a position is the low
+ * 64 bits of position * turns, so it stays exact at any position; a product
+ * of 32-bit floats is 1e-3 of a turn off at position 10^5. Returns
+ * HSTU_ERR_INVALID_ARG for null pointers or values out of the ranges above,
+ * HSTU_ERR_UNSUPPORTED for a rotary_dim or scaling there is no kernel for. */
+HSTU_API hstu_status_t hstu_attn_rope_table(const hstu_rope_spec_t* spec, uint64_t* turns, float* magnitude);
+
+/* Rotates the first R columns of every head of q, and of k if it is not NULL,
+ * by its row's position; columns R and up are copied. For a pair (a, b) of
+ * angle t:  a' = m (a cos t - b sin t),  b' = m (b cos t + a sin t).
+ * backward != 0 applies the transposed rotation instead: given the gradients
+ * of the rotated rows it returns those of the rows.
+ *   q, k, q_out, k_out  DEVICE (tokens, H, D), heads and columns contiguous,
+ *            rows *_stride elements apart (>= H D and a multiple of 8), 16-byte
+ *            aligned. An output may be its own input (same pointer and
+ *            stride); otherwise outputs overlap no input.
+ *   positions  DEVICE int32 (tokens), any value; angles are computed from
+ *            exact phases (see hstu_attn_rope_table).
+ *   head_dim  32, 64 or 128, >= R; dtype HSTU_DTYPE_BF16 or HSTU_DTYPE_F16.
+ * Computed in fp32 and rounded once. */
+HSTU_API hstu_status_t hstu_attn_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, void* q_out,
+                                      int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                                      const int32_t* positions, int64_t tokens, int32_t num_heads, int32_t head_dim,
+                                      int32_t dtype, const hstu_rope_t* rope, int32_t backward, void* stream);
+
+/* A paged K/V cache, DEVICE memory owned by the caller. Row `pos` of sequence
+ * b lives in page page_table[b][pos / page_size], slot pos % page_size. A
+ * page keeps each head's rows together, so that one (page, head) is one
+ * contiguous block. */
+typedef struct {
+  void* k;             /* (num_pages, H, page_size, D_qk), 16-byte aligned */
+  void* v;             /* (num_pages, H, page_size, D_v), 16-byte aligned */
+  uint8_t* k_scale;    /* e4m3 only: (num_pages, H, page_size) scale bytes */
+  uint8_t* v_scale;
+  int64_t num_pages;   /* 1 .. 2^31 - 1 */
+  int32_t page_size;   /* 16, 32, 64, 128 or 256 */
+  int32_t num_heads;
+  int32_t head_dim;    /* D_qk: 32, 64 or 128 */
+  int32_t head_dim_v;  /* D_v: 32, 64 or 128; 0 means D_qk */
+  int32_t dtype;       /* type of rows written, read back, q_c and o_c */
+  int32_t e4m3;        /* 0: pages hold rows of dtype. 1: 8-bit floats (4
+                          exponent, 3 mantissa bits) under a power-of-two
+                          scale for each row and head: value = code *
+                          2^(byte - 127), the smallest power (2^-127 at the
+                          least) that brings the row's finite values to 448 or
+                          below. A power of two keeps the scaling exact in
+                          both directions, so the code's rounding is the only
+                          one. A value that is not finite is stored as NaN. */
+} hstu_cache_t;
+
+/* Appends rows to the cache: row i of sequence b (rows seq_offsets[b] ..
+ * seq_offsets[b+1] of k and v) goes to position cache_lens[b] + i.
+ *   k, v     DEVICE (rows, H, D_qk / D_v) of cache->dtype, strides as for
+ *            hstu_attn_rope
+ *   seq_offsets  DEVICE int32 (batch+1): 0, non-decreasing, last = rows
+ *   cache_lens   DEVICE int32 (batch): rows already cached; not changed (the
+ *            caller adds the new counts after the call)
+ *   page_table   DEVICE int32 (batch, max_pages); entries of pages that no
+ *            row falls in are not read
+ *   rope     HOST pointer or NULL: rotates k on its way, by positions[row]
+ *            (DEVICE int32 (rows)) or, where positions is NULL, by the row's
+ *            place in the cache
+ *   ws       NULL, or DEVICE, 256-byte aligned, >= 256 bytes: its error word
+ *            is cleared and receives HSTU_ERR_DEVICE_INPUT where a row is
+ *            skipped (read it with hstu_attn_get_device_status)
+ * A negative length, a position past max_pages * page_size and a page outside
+ * [0, num_pages) skip the rows that they concern. Offsets that do not run from
+ * 0 to rows, or out of order, are reported; rows that they bring to a valid
+ * place are written there. Nothing is written out of bounds. Two rows of one
+ * call must not share a slot. */
+HSTU_API hstu_status_t hstu_attn_cache_write(const hstu_cache_t* cache, const void* k, int64_t k_stride,
+                                             const void* v, int64_t v_stride, const int32_t* seq_offsets,
+                                             int32_t batch, int64_t rows, const int32_t* cache_lens,
+                                             const int32_t* page_table, int32_t max_pages, const hstu_rope_t* rope,
+                                             const int32_t* positions, void* ws, size_t ws_bytes, void* stream);
+
+/* Reads cached rows back into jagged tensors for the contiguous kernels: row i
+ * of sequence b (output rows seq_offsets[b] .. seq_offsets[b+1]) is position
+ * starts[b] + i (starts DEVICE int32 (batch), NULL: 0). k (rows, H, D_qk) and
+ * v (rows, H, D_v) are written, contiguous, of cache->dtype; e4m3 rows are
+ * multiplied out and rounded once. Rows that the checks of
+ * hstu_attn_cache_write skip are left as they were; ws as there. */
+HSTU_API hstu_status_t hstu_attn_cache_read(const hstu_cache_t* cache, void* k, void* v, const int32_t* seq_offsets,
+                                            int32_t batch, int64_t rows, const int32_t* starts,
+                                            const int32_t* page_table, int32_t max_pages, void* ws, size_t ws_bytes,
+                                            void* stream);
+
+/* Bytes of workspace that hstu_attn_fwd_paged needs; 0 if an argument is out
+ * of range. */
+HSTU_API size_t hstu_attn_paged_workspace_size(const hstu_cache_t* cache, int32_t batch, int64_t num_candidates,
+                                               int32_t max_seqlen);
+
+/* Candidate rows against cached rows: for candidate c of sequence b
+ *     o_c[c] = sum over visible positions j of silu(alpha q_c[c] . k_j) / N * v_j
+ * over the positions [0, cache_lens[b]) of its sequence, N = max_seqlen. New
+ * tokens that are to see themselves are written to the cache before the call.
+ *   q_c      DEVICE (num_candidates, H, D_qk), rows q_stride elements apart
+ *            (as for hstu_attn_rope); o_c (num_candidates, H, D_v) contiguous
+ *   cache_lens   DEVICE int32 (batch), each in [0, max_seqlen]
+ *   cand_offsets DEVICE int32 (batch+1) as for hstu_attn_fwd_targets, or NULL:
+ *            one candidate a sequence (num_candidates = batch)
+ *   func_c   DEVICE int32 (nfunc, num_candidates), intervals as everywhere,
+ *            or NULL: every cached position is visible (nfunc is ignored)
+ *   max_seqlen   N, 1 .. 2^24 (the pages take longer histories than the
+ *            contiguous kernels)
+ *   ws       hstu_attn_paged_workspace_size() bytes, 256-byte aligned
+ * Slots past a sequence's length and positions that a candidate does not see
+ * do not reach it, whatever they hold (NaN and infinities too). A candidate
+ * that sees nothing gets 0. The cache's length is split over CTAs, whose sums
+ * are joined in a fixed order (bitwise repeatable). A sequence with bad
+ * offsets, length or page sets HSTU_ERR_DEVICE_INPUT in the error word of ws;
+ * its rows of o_c are left as they were. */
+HSTU_API hstu_status_t hstu_attn_fwd_paged(const void* q_c, int64_t q_stride, void* o_c, const hstu_cache_t* cache,
+                                           const int32_t* cache_lens, int32_t batch, const int32_t* page_table,
+                                           int32_t max_pages, const int32_t* cand_offsets, int64_t num_candidates,
+                                           const int32_t* func_c, int32_t nfunc, int32_t max_seqlen, float alpha,
+                                           void* ws, size_t ws_bytes, void* stream);
+
 /* Synchronises the stream, then returns the status recorded in the
  * workspace error word (HSTU_OK, HSTU_ERR_DEVICE_INPUT, HSTU_ERR_TIMEOUT,
  * and in the checked build HSTU_ERR_DEVICE_CHECK) or HSTU_ERR_CUDA if the

@@ -36,7 +36,8 @@ EXPORTED = (
     "hstu_attn_shard_sequences", "hstu_attn_test_wait_timeout", "hstu_attn_build_func",
     "hstu_attn_build_func_candidates", "hstu_attn_targets_workspace_size", "hstu_attn_fwd_targets",
     "hstu_attn_bwd_targets", "hstu_attn_project_workspace_size", "hstu_attn_project_rows",
-    "hstu_attn_project_rows_bwd", "hstu_attn_test_set_handoff_limit",
+    "hstu_attn_project_rows_bwd", "hstu_attn_test_set_handoff_limit", "hstu_attn_rope_table", "hstu_attn_rope",
+    "hstu_attn_cache_write", "hstu_attn_cache_read", "hstu_attn_paged_workspace_size", "hstu_attn_fwd_paged",
 )
 FUNC_CAUSAL, FUNC_SLA, FUNC_ONERANK = 0, 1, 2
 NOALLOC_SCRATCH_BYTES = 8 << 20
@@ -72,6 +73,43 @@ class Shape(ctypes.Structure):
     ]
 
 
+class RopeSpec(ctypes.Structure):
+    _fields_ = [
+        ("rotary_dim", ctypes.c_int32),
+        ("scaling", ctypes.c_int32),
+        ("base", ctypes.c_double),
+        ("factor", ctypes.c_double),
+        ("original_len", ctypes.c_double),
+        ("fast_turns", ctypes.c_double),
+        ("slow_turns", ctypes.c_double),
+    ]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [
+        ("turns", ctypes.c_void_p),
+        ("rotary_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("magnitude", ctypes.c_float),
+    ]
+
+
+class Cache(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("num_pages", ctypes.c_int64),
+        ("page_size", ctypes.c_int32),
+        ("num_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("head_dim_v", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("e4m3", ctypes.c_int32),
+    ]
+
+
 _libs = {}
 _active = LIB_PATH
 
@@ -96,7 +134,8 @@ def load(path: str = None) -> ctypes.CDLL:
             "(python -c 'import __graft_entry__ as g; g.build()')")
     lib = ctypes.CDLL(path)
     vp, i32, u32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint32, ctypes.c_size_t
-    sp = ctypes.POINTER(Shape)
+    i64, sp = ctypes.c_int64, ctypes.POINTER(Shape)
+    cp, rp = ctypes.POINTER(Cache), ctypes.POINTER(Rope)
     sig = {
         "hstu_attn_nfunc_supported": (ctypes.c_int, [i32]),
         "hstu_attn_workspace_size": (sz, [sp, i32]),
@@ -123,6 +162,14 @@ def load(path: str = None) -> ctypes.CDLL:
         "hstu_attn_fwd_targets": (ctypes.c_int, [vp, vp, vp, vp, vp, vp, ctypes.c_int64, vp, sp, vp, sz, vp]),
         "hstu_attn_bwd_targets": (ctypes.c_int, [vp, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_int64, vp, sp, vp,
                                                  sz, vp]),
+        "hstu_attn_rope_table": (ctypes.c_int, [ctypes.POINTER(RopeSpec), vp, ctypes.POINTER(ctypes.c_float)]),
+        "hstu_attn_rope": (ctypes.c_int, [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i32, i32, i32, rp, i32, vp]),
+        "hstu_attn_cache_write": (ctypes.c_int, [cp, vp, i64, vp, i64, vp, i32, i64, vp, vp, i32, rp, vp, vp, sz,
+                                                 vp]),
+        "hstu_attn_cache_read": (ctypes.c_int, [cp, vp, vp, vp, i32, i64, vp, vp, i32, vp, sz, vp]),
+        "hstu_attn_paged_workspace_size": (sz, [cp, i32, i64, i32]),
+        "hstu_attn_fwd_paged": (ctypes.c_int, [vp, i64, vp, cp, vp, i32, vp, i32, vp, i64, vp, i32, i32,
+                                               ctypes.c_float, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -483,3 +530,267 @@ def set_handoff_limit_for_tests(limit_ns: int) -> None:
     """Test hook (hstu_attn_test_set_handoff_limit): shortens the attention
     kernels' accumulator hand-off wait; 0 restores the normal limit."""
     _check(load().hstu_attn_test_set_handoff_limit(int(limit_ns)), "hstu_attn_test_set_handoff_limit")
+
+
+_ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+class RopeTable:
+    """A rotation of the first ``rotary_dim`` columns of each head: the pairs'
+    frequencies on the device, as ``rope`` and ``cache_write`` take it (see
+    hstu_rope_t). Made by ``rope_table``."""
+
+    def __init__(self, turns: torch.Tensor, interleaved: bool, magnitude: float):
+        self.turns = turns
+        self.rotary_dim = 2 * turns.numel()
+        self.interleaved = bool(interleaved)
+        self.magnitude = magnitude
+        self.device = turns.device
+        self._c = Rope(turns.data_ptr(), self.rotary_dim, int(self.interleaved), magnitude)
+
+
+def rope_table(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+               original_len: float = 0.0, fast_turns: float = 32.0, slow_turns: float = 1.0,
+               interleaved: bool = False, device="cuda") -> RopeTable:
+    """The frequencies of a rotation (hstu_attn_rope_table), made once and
+    kept. ``scaling`` is "none", "linear", "ntk" or "yarn"; ``factor`` is how
+    many times longer than trained the contexts are, ``original_len`` the
+    trained length (yarn only)."""
+    if scaling not in _ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(_ROPE_SCALINGS)}")
+    spec = RopeSpec(int(rotary_dim), _ROPE_SCALINGS[scaling], base, factor, original_len, fast_turns, slow_turns)
+    turns = torch.zeros(max(int(rotary_dim) // 2, 1), dtype=torch.int64)
+    magnitude = ctypes.c_float()
+    _check(load().hstu_attn_rope_table(ctypes.byref(spec), _ptr(turns), ctypes.byref(magnitude)),
+           "hstu_attn_rope_table")
+    return RopeTable(turns.to(device), interleaved, magnitude.value)
+
+
+def _need_rows(t: torch.Tensor, dtype, name: str) -> int:
+    """Checks a (rows, H, D) tensor whose rows may lie apart (a slice of a
+    wider projection); returns the distance between rows in elements."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be (rows, heads, width), got {tuple(t.shape)}")
+    rows, heads, width = t.shape
+    stride, sh, sw = t.stride()
+    if (sw != 1 and width > 1) or (sh != width and heads > 1):
+        raise ValueError(f"{name}: heads and columns of a row must be contiguous")
+    if rows <= 1:
+        return heads * width
+    if stride < heads * width:
+        raise ValueError(f"{name}: rows overlap")
+    return stride
+
+
+def _need_here(device, **tensors):
+    """Every tensor on ``device``, and that the current one: the library
+    launches on the current device."""
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _need_int32(t: torch.Tensor, name: str, shape):
+    _need(t, torch.int32, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def rope(q, k, positions, table: RopeTable, backward: bool = False, outs=None, stream=None):
+    """(q', k') with the leading columns of every head rotated by the row's
+    position (hstu_attn_rope). q and k are (T, H, D), bf16 or fp16, and may be
+    slices of a wider projection; k may be None. ``backward=True`` takes the
+    gradients of q' and k' to those of q and k. ``outs`` may be (q, k) itself:
+    the rows are then rotated in place."""
+    if q.dtype not in DTYPES:
+        raise ValueError(f"q must be one of {_FLOATS}, got {q.dtype}")
+    qs = _need_rows(q, q.dtype, "q")
+    T, H, D = q.shape
+    ks = 0
+    if k is not None:
+        ks = _need_rows(k, q.dtype, "k")
+        if k.shape != q.shape:
+            raise ValueError(f"k must have q's shape {tuple(q.shape)}, got {tuple(k.shape)}")
+    _need_int32(positions, "positions", (T,))
+    _need_here(q.device, k=k, positions=positions, table=table)
+    if outs is None:
+        qo = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+        ko = None if k is None else torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+        qos = kos = H * D
+    else:
+        qo, ko = outs
+        qos, kos = _need_rows(qo, q.dtype, "outs[0]"), 0
+        if qo.shape != q.shape or (ko is None) != (k is None):
+            raise ValueError("outs must match q and k")
+        if ko is not None:
+            kos = _need_rows(ko, q.dtype, "outs[1]")
+            if ko.shape != q.shape:
+                raise ValueError("outs must match q and k")
+        _need_here(q.device, qo=qo, ko=ko)
+    _check(load().hstu_attn_rope(_ptr(q), qs, _ptr(k), ks, _ptr(qo), qos, _ptr(ko), kos, _ptr(positions), T, H, D,
+                                 DTYPES[q.dtype], ctypes.byref(table._c), 1 if backward else 0, _stream(stream)),
+           "hstu_attn_rope")
+    return qo, ko
+
+
+class PagedCache:
+    """K/V pages on the device (hstu_cache_t). ``k`` is (pages, H, page, D_qk)
+    and ``v`` (pages, H, page, D_v): bf16 or fp16, or uint8 holding 8-bit
+    floats under the power-of-two scales ``k_scale`` and ``v_scale`` (uint8,
+    (pages, H, page)). ``dtype`` is the type of the rows written, read back
+    and multiplied (16-bit pages hold it as it is)."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None, dtype=None):
+        e4m3 = k_scale is not None
+        dtype = dtype if dtype is not None else k.dtype
+        if dtype not in DTYPES:
+            raise ValueError(f"dtype must be one of {_FLOATS}, got {dtype}")
+        for t, n in ((k, "k"), (v, "v")):
+            _need(t, torch.uint8 if e4m3 else dtype, n)
+            if t.dim() != 4:
+                raise ValueError(f"{n} must be (pages, heads, page, width), got {tuple(t.shape)}")
+        if k.shape[:3] != v.shape[:3]:
+            raise ValueError("k and v must have the same pages, heads and page size")
+        if (v_scale is not None) != e4m3:
+            raise ValueError("k_scale and v_scale come together")
+        if e4m3:
+            for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+                _need(t, torch.uint8, n)
+                if t.shape != k.shape[:3]:
+                    raise ValueError(f"{n} must have shape {tuple(k.shape[:3])}, got {tuple(t.shape)}")
+        for t in (v, k_scale, v_scale):
+            if t is not None and t.device != k.device:
+                raise ValueError("the cache's tensors must be on one device")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.dtype, self.device, self.quantised = dtype, k.device, e4m3
+        self.num_pages, self.heads, self.page_size, self.dim = k.shape
+        self.dim_v = v.shape[3]
+        addr = lambda t: None if t is None else t.data_ptr()
+        self._c = Cache(addr(k), addr(v), addr(k_scale), addr(v_scale), self.num_pages, self.page_size, self.heads,
+                        self.dim, self.dim_v, DTYPES[dtype], int(e4m3))
+
+
+def alloc_cache(num_pages: int, page_size: int, heads: int, dim: int, dim_v: int = 0, dtype=torch.bfloat16,
+                quantised: bool = False, device="cuda") -> PagedCache:
+    """An empty paged cache; its slots hold anything until rows are written."""
+    shape = (num_pages, heads, page_size)
+    kind = torch.uint8 if quantised else dtype
+    new = lambda *s: torch.empty(s, dtype=kind, device=device)
+    k, v = new(*shape, dim), new(*shape, dim_v or dim)
+    return PagedCache(k, v, new(*shape) if quantised else None, new(*shape) if quantised else None, dtype=dtype)
+
+
+def _need_pages(cache: PagedCache, page_table, batch: int):
+    _need(page_table, torch.int32, "page_table")
+    if page_table.dim() != 2 or page_table.shape[0] != batch or page_table.shape[1] < 1:
+        raise ValueError(f"page_table must be (batch = {batch}, pages), got {tuple(page_table.shape)}")
+
+
+def _ws_args(ws):
+    return (None, 0) if ws is None else (_ptr(ws), ws.numel() * ws.element_size())
+
+
+def cache_write(cache: PagedCache, k, v, seq_offsets, cache_lens, page_table, rope: Optional[RopeTable] = None,
+                positions=None, ws: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Appends the jagged rows k (T, H, D_qk) and v (T, H, D_v) to their
+    sequences' pages behind the ``cache_lens`` rows already there
+    (hstu_attn_cache_write); ``rope`` rotates k on its way, by ``positions``
+    or by its place in the cache. ``cache_lens`` is not changed. With a ``ws``
+    (256 bytes) skipped rows are reported by ``device_status``."""
+    ks, vs = _need_rows(k, cache.dtype, "k"), _need_rows(v, cache.dtype, "v")
+    T = k.shape[0]
+    if k.shape[1:] != (cache.heads, cache.dim) or v.shape != (T, cache.heads, cache.dim_v):
+        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} do not fit the cache's heads and widths")
+    _need(seq_offsets, torch.int32, "seq_offsets")
+    B = seq_offsets.numel() - 1
+    _need_int32(cache_lens, "cache_lens", (B,))
+    _need_pages(cache, page_table, B)
+    if positions is not None:
+        _need_int32(positions, "positions", (T,))
+    _need_here(cache.device, k=k, v=v, seq_offsets=seq_offsets, cache_lens=cache_lens, page_table=page_table,
+               positions=positions, rope=rope, ws=ws)
+    _check(load().hstu_attn_cache_write(ctypes.byref(cache._c), _ptr(k), ks, _ptr(v), vs, _ptr(seq_offsets), B, T,
+                                        _ptr(cache_lens), _ptr(page_table), page_table.shape[1],
+                                        None if rope is None else ctypes.byref(rope._c), _ptr(positions),
+                                        *_ws_args(ws), _stream(stream)), "hstu_attn_cache_write")
+
+
+def cache_read(cache: PagedCache, seq_offsets, rows: int, page_table, starts=None, outs=None,
+               ws: Optional[torch.Tensor] = None, stream=None):
+    """(k, v) of cached rows, jagged and contiguous, in the cache's dtype
+    (hstu_attn_cache_read): ``rows`` rows, those of sequence b from position
+    ``starts[b]`` (0 without ``starts``)."""
+    _need(seq_offsets, torch.int32, "seq_offsets")
+    B = seq_offsets.numel() - 1
+    _need_pages(cache, page_table, B)
+    if starts is not None:
+        _need_int32(starts, "starts", (B,))
+    if outs is None:
+        new = lambda w: torch.empty((rows, cache.heads, w), dtype=cache.dtype, device=cache.device)
+        k, v = new(cache.dim), new(cache.dim_v)
+    else:
+        k, v = outs
+        for t, n, w in ((k, "outs[0]", cache.dim), (v, "outs[1]", cache.dim_v)):
+            _need(t, cache.dtype, n)
+            if t.shape != (rows, cache.heads, w):
+                raise ValueError(f"{n} must have shape {(rows, cache.heads, w)}, got {tuple(t.shape)}")
+    _need_here(cache.device, seq_offsets=seq_offsets, page_table=page_table, starts=starts, k=k, v=v, ws=ws)
+    _check(load().hstu_attn_cache_read(ctypes.byref(cache._c), _ptr(k), _ptr(v), _ptr(seq_offsets), B, rows,
+                                       _ptr(starts), _ptr(page_table), page_table.shape[1], *_ws_args(ws),
+                                       _stream(stream)), "hstu_attn_cache_read")
+    return k, v
+
+
+def paged_workspace(cache: PagedCache, batch: int, num_candidates: int, max_seqlen: int) -> torch.Tensor:
+    """Workspace of ``fwd_paged``."""
+    n = int(load().hstu_attn_paged_workspace_size(ctypes.byref(cache._c), batch, num_candidates, max_seqlen))
+    if n == 0:
+        raise HstuError(2, "hstu_attn_paged_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+
+
+def fwd_paged(q_c, cache: PagedCache, cache_lens, page_table, max_seqlen: int, alpha: Optional[float] = None,
+              cand_offsets=None, func_c=None, ws: Optional[torch.Tensor] = None, out=None, stream=None):
+    """o_c (C, H, D_v): candidate rows q_c (C, H, D_qk) against the
+    ``cache_lens[b]`` cached rows of their sequences (hstu_attn_fwd_paged).
+    One candidate a sequence without ``cand_offsets``; all cached rows are
+    visible without ``func_c`` (nfunc, C)."""
+    qs = _need_rows(q_c, cache.dtype, "q_c")
+    C, H, D = q_c.shape
+    if (H, D) != (cache.heads, cache.dim):
+        raise ValueError(f"q_c {tuple(q_c.shape)} does not fit the cache's heads and width")
+    _need(cache_lens, torch.int32, "cache_lens")
+    B = cache_lens.numel()
+    _need_pages(cache, page_table, B)
+    nfunc = 0
+    if cand_offsets is not None:
+        _need_int32(cand_offsets, "cand_offsets", (B + 1,))
+    if func_c is not None:
+        nfunc = func_c.shape[0]
+        _need_int32(func_c, "func_c", (nfunc, C))
+    if alpha is None:
+        alpha = 1.0 / math.sqrt(D)
+    if out is None:
+        out = torch.empty((C, H, cache.dim_v), dtype=cache.dtype, device=cache.device)
+    else:
+        _need(out, cache.dtype, "out")
+        if out.shape != (C, H, cache.dim_v):
+            raise ValueError(f"out must have shape {(C, H, cache.dim_v)}, got {tuple(out.shape)}")
+    _need_here(cache.device, q_c=q_c, cache_lens=cache_lens, page_table=page_table, cand_offsets=cand_offsets,
+               func_c=func_c, out=out, ws=ws)
+    own_ws = ws is None
+    if own_ws:
+        ws = paged_workspace(cache, B, C, max_seqlen)
+    _check(load().hstu_attn_fwd_paged(_ptr(q_c), qs, _ptr(out), ctypes.byref(cache._c), _ptr(cache_lens), B,
+                                      _ptr(page_table), page_table.shape[1], _ptr(cand_offsets), C, _ptr(func_c),
+                                      nfunc, max_seqlen, alpha, _ptr(ws), ws.numel(), _stream(stream)),
+           "hstu_attn_fwd_paged")
+    if own_ws and stream is not None:
+        ws.record_stream(stream)
+    return out

@@ -29,7 +29,8 @@ VARIANTS = {
     "checked": (CHECKED_LIB_PATH, os.path.join(BUILD_DIR, "checked"), ["-DHSTU_CHECKED"]),
 }
 SOURCES = ["plan.cu", "attn_fwd_bf16.cu", "attn_fwd_f16.cu", "attn_bwd_bf16.cu", "attn_bwd_f16.cu", "targets_only.cu", "api.cu", "noalloc.cu", "selftest.cu", "func_build.cu", "project.cu",
-           "shard.cpp"]
+           "rope.cu", "cache.cu", "paged.cu", "paged_bf16.cu", "paged_f16.cu", "paged_bf16_e4m3.cu",
+           "paged_f16_e4m3.cu", "shard.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

@@ -1,0 +1,110 @@
+// Entry points of the paged attention (declared in include/hstu_attn.h):
+// argument checks, the split of the cache's length, workspace, dispatch.
+#include <algorithm>
+
+#include "paged.cuh"
+
+namespace hstu {
+
+// Keys of a split. Splits of up to 4096 keys while the sequences and heads
+// alone give every SM several CTAs; shorter ones, down to 256 keys, where
+// they do not. It follows from the arguments alone, so that the workspace and
+// the order of the sums are the same on every device.
+static int paged_split(int batch, int heads, int max_seqlen) {
+  constexpr int64_t kCtas = 152 * 4 * 2;  // SMs x resident CTAs x waves
+  const int64_t want = static_cast<int64_t>(max_seqlen) * batch * heads / kCtas;
+  return static_cast<int>(std::min<int64_t>(kPagedMaxSplit, std::max<int64_t>(256, (want + 255) / 256 * 256)));
+}
+
+struct PagedLayout {
+  int split = 0, nsplit = 0;
+  size_t counters = 0, counter_bytes = 0, partial = 0, total = 0;
+};
+static PagedLayout paged_layout(const CacheView& c, int batch, int64_t num_cand, int max_seqlen) {
+  PagedLayout l;
+  l.split = paged_split(batch, c.heads, max_seqlen);
+  l.nsplit = (max_seqlen + l.split - 1) / l.split;
+  l.counters = kHdrWords * 4;
+  l.partial = l.counters;
+  l.total = l.partial;
+  if (l.nsplit > 1) {
+    l.counter_bytes = static_cast<size_t>(batch) * c.heads * 4;
+    l.partial = l.counters + align_up(l.counter_bytes, 256);
+    l.total = l.partial + align_up(static_cast<size_t>(num_cand) * c.heads * l.nsplit * c.dim_v * 4, 256);
+  }
+  return l;
+}
+
+static hstu_status_t check_paged(const hstu_cache_t* cache, int32_t batch, int64_t num_cand, int32_t max_seqlen,
+                                 CacheView* view) {
+  const hstu_status_t st = check_cache(cache, view);
+  if (st != HSTU_OK) return st;
+  if (batch < 1 || num_cand < 0 || num_cand > INT32_MAX || max_seqlen < 1) return HSTU_ERR_INVALID_ARG;
+  if (max_seqlen > (1 << 24)) return HSTU_ERR_UNSUPPORTED;
+  const PagedLayout l = paged_layout(*view, batch, num_cand, max_seqlen);
+  const int64_t bh = static_cast<int64_t>(batch) * view->heads;
+  if (bh > INT32_MAX / l.nsplit) return HSTU_ERR_UNSUPPORTED;  // CTAs of a launch
+  return HSTU_OK;
+}
+
+}  // namespace hstu
+
+extern "C" {
+
+HSTU_API size_t hstu_attn_paged_workspace_size(const hstu_cache_t* cache, int32_t batch, int64_t num_candidates,
+                                               int32_t max_seqlen) {
+  hstu::CacheView view;
+  if (hstu::check_paged(cache, batch, num_candidates, max_seqlen, &view) != HSTU_OK) return 0;
+  return hstu::paged_layout(view, batch, num_candidates, max_seqlen).total;
+}
+
+HSTU_API hstu_status_t hstu_attn_fwd_paged(const void* q_c, int64_t q_stride, void* o_c, const hstu_cache_t* cache,
+                                           const int32_t* cache_lens, int32_t batch, const int32_t* page_table,
+                                           int32_t max_pages, const int32_t* cand_offsets, int64_t num_candidates,
+                                           const int32_t* func_c, int32_t nfunc, int32_t max_seqlen, float alpha,
+                                           void* ws, size_t ws_bytes, void* stream) {
+  hstu::PagedParams p{};
+  const hstu_status_t st = hstu::check_paged(cache, batch, num_candidates, max_seqlen, &p.cache);
+  if (st != HSTU_OK) return st;
+  if (func_c && !hstu_attn_nfunc_supported(nfunc)) return HSTU_ERR_UNSUPPORTED;
+  if (max_pages < 1 || !(alpha == alpha) || (!cand_offsets && num_candidates != batch)) return HSTU_ERR_INVALID_ARG;
+  const auto bad4 = [](const void* q) { return reinterpret_cast<uintptr_t>(q) % 4 != 0; };
+  if (!cache_lens || !page_table || bad4(cache_lens) || bad4(page_table) || bad4(cand_offsets) || bad4(func_c))
+    return HSTU_ERR_INVALID_ARG;
+  if (num_candidates > 0 && (!hstu::rows_ok(q_c, q_stride, p.cache.heads, p.cache.dim) || !o_c ||
+                             reinterpret_cast<uintptr_t>(o_c) % 16 != 0))
+    return HSTU_ERR_INVALID_ARG;
+  const hstu::PagedLayout l = hstu::paged_layout(p.cache, batch, num_candidates, max_seqlen);
+  if (!ws || reinterpret_cast<uintptr_t>(ws) % 256 != 0 || ws_bytes < l.total) return HSTU_ERR_WORKSPACE;
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  p.q = q_c;
+  p.o = o_c;
+  p.q_stride = q_stride;
+  p.lens = cache_lens;
+  p.page_table = page_table;
+  p.cand_offsets = cand_offsets;
+  p.func = func_c;
+  p.partial = reinterpret_cast<float*>(base + l.partial);
+  p.header = reinterpret_cast<int32_t*>(base);
+  p.counters = reinterpret_cast<int32_t*>(base + l.counters);
+  p.batch = batch;
+  p.max_pages = max_pages;
+  p.num_cand = static_cast<int32_t>(num_candidates);
+  p.nfunc = nfunc;
+  p.max_seqlen = max_seqlen;
+  p.split = l.split;
+  p.nsplit = l.nsplit;
+  p.alpha = alpha;
+  p.inv_n = 1.0f / static_cast<float>(max_seqlen);
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  // The error word and the counters start at zero.
+  if (cudaMemsetAsync(ws, 0, l.counters + l.counter_bytes, cs) != cudaSuccess) return HSTU_ERR_CUDA;
+  const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(batch) * p.cache.heads * l.nsplit);
+  const bool half = cache->dtype == HSTU_DTYPE_F16;
+  cudaError_t e;
+  if (cache->e4m3) e = half ? hstu::launch_paged_f16_e4m3(p, blocks, cs) : hstu::launch_paged_bf16_e4m3(p, blocks, cs);
+  else e = half ? hstu::launch_paged_f16(p, blocks, cs) : hstu::launch_paged_bf16(p, blocks, cs);
+  return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+}
+
+}  // extern "C"
