@@ -385,7 +385,8 @@ HSTU_API hstu_status_t hstu_attn_rope(const void* q, int64_t q_stride, const voi
 typedef struct {
   void* k;             /* (num_pages, H, page_size, D_qk), 16-byte aligned */
   void* v;             /* (num_pages, H, page_size, D_v), 16-byte aligned */
-  uint8_t* k_scale;    /* e4m3 only: (num_pages, H, page_size) scale bytes */
+  uint8_t* k_scale;    /* e4m3 only: (num_pages, H, page_size) scale bytes,
+                          16-byte aligned */
   uint8_t* v_scale;
   int64_t num_pages;   /* 1 .. 2^31 - 1 */
   int32_t page_size;   /* 16, 32, 64, 128 or 256 */

@@ -77,7 +77,7 @@ inline hstu_status_t check_cache(const hstu_cache_t* c, CacheView* out) {
   if (c->num_heads < 1 || c->num_heads > 65535) return c->num_heads < 1 ? HSTU_ERR_INVALID_ARG : HSTU_ERR_UNSUPPORTED;
   if (c->num_pages < 1 || c->num_pages > INT32_MAX || (c->e4m3 != 0 && c->e4m3 != 1)) return HSTU_ERR_INVALID_ARG;
   const auto bad = [](const void* p) { return !p || reinterpret_cast<uintptr_t>(p) % 16 != 0; };
-  if (bad(c->k) || bad(c->v) || (c->e4m3 && (!c->k_scale || !c->v_scale))) return HSTU_ERR_INVALID_ARG;
+  if (bad(c->k) || bad(c->v) || (c->e4m3 && (bad(c->k_scale) || bad(c->v_scale)))) return HSTU_ERR_INVALID_ARG;
   *out = CacheView{c->k,     c->v,         c->k_scale,    c->v_scale, c->num_pages,
                    shift,    c->num_heads, c->head_dim,   dv};
   return HSTU_OK;

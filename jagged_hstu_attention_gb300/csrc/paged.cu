@@ -6,14 +6,14 @@
 
 namespace hstu {
 
-// Keys of a split. Splits of up to 4096 keys while the sequences and heads
-// alone give every SM several CTAs; shorter ones, down to 256 keys, where
-// they do not. It follows from the arguments alone, so that the workspace and
-// the order of the sums are the same on every device.
+// Keys of a split: as many as leave 2400 CTAs (eight waves of two an SM) at
+// the longest length, which balances ragged lengths, from 512 to 4096. It
+// follows from the arguments alone, so that the workspace and the order of the
+// sums are the same on every device.
 static int paged_split(int batch, int heads, int max_seqlen) {
-  constexpr int64_t kCtas = 152 * 4 * 2;  // SMs x resident CTAs x waves
+  constexpr int64_t kCtas = 2400;
   const int64_t want = static_cast<int64_t>(max_seqlen) * batch * heads / kCtas;
-  return static_cast<int>(std::min<int64_t>(kPagedMaxSplit, std::max<int64_t>(256, (want + 255) / 256 * 256)));
+  return static_cast<int>(std::min<int64_t>(kPagedMaxSplit, std::max<int64_t>(512, (want + 255) / 256 * 256)));
 }
 
 struct PagedLayout {

@@ -8,8 +8,11 @@
 // instructions (m16n8k16), whose operands a warp can take straight from the
 // cache's rows.
 //
-// A CTA takes one (sequence, head) and one split of its length; a warp takes
-// every fourth tile of 16 keys. Per tile:
+// A CTA takes one (sequence, head) and one split of its length. Its four warps
+// form slices of 1, 2 or 4 warps, as many as the sequence has groups of eight
+// candidates; a slice reads every (4 / warps)-th step of 16 keys a warp into
+// its ring of shared memory with asynchronous copies, and each of its warps
+// multiplies all of the step's keys with its own eight candidates. Per 16 keys:
 //   S = Q K^T   16 x 8 tiles, rows = 8 candidates (rows 8..15 see below)
 //   P = silu(alpha S), zero where not visible, split into two 16-bit parts
 //   O += P V    rows 0..7 hold the high part of P, rows 8..15 its low part
@@ -37,6 +40,7 @@
 #include <type_traits>
 
 #include "cache.cuh"
+#include "internal.h"
 #include "rope.cuh"
 
 namespace hstu {
@@ -84,18 +88,27 @@ __device__ __forceinline__ void mma16816<__half>(float (&d)[4], uint32_t a0, uin
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// B (bytes) of a lane's piece: 16, 8 or 4.
+// B bytes (16, 8 or 4) of a lane's piece, from shared memory.
 template <int B>
-__device__ __forceinline__ void load_piece(const void* p, bool live, uint32_t* w) {
-  if (B == 16) {
-    const uint4 u = live ? __ldg(static_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
-    w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
-  } else if (B == 8) {
-    const uint2 u = live ? __ldg(static_cast<const uint2*>(p)) : make_uint2(0, 0);
-    w[0] = u.x; w[1] = u.y;
-  } else {
-    w[0] = live ? __ldg(static_cast<const uint32_t*>(p)) : 0u;
-  }
+__device__ __forceinline__ void load_piece(uint32_t addr, uint32_t* w) {
+  if (B == 16)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(addr));
+  else if (B == 8)
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+  else
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+}
+
+// Asynchronous copy of 16 bytes; zeros where not live (src is not read then).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
 }
 
 __device__ __forceinline__ float silu_exact(float x) { return x * sigmoidf_fast(x); }
@@ -107,11 +120,14 @@ __device__ __forceinline__ float cached_value(const void* base, int64_t i) {
   return Elem<T>::lo(static_cast<const uint16_t*>(base)[i]);
 }
 
-// The sum of one candidate over the keys of one warp that it sees, in fp32,
-// one key after the other: the way out for sums that are not finite.
+// The sum of one candidate over the steps of one slice, in fp32, one visible
+// key after the other: the way out for sums that are not finite. The slice
+// takes entries [first, first + count), and so on every `stride` entries, of
+// the split's list of 16-key tiles (the tiles themselves without a list).
 template <typename T, int DQ, int DV, bool E4M3, int NI>
-__device__ __noinline__ void paged_scalar_sum(const PagedParams& p, int cand, int h, int warp, int lane, int k0,
-                                              int k1, int len, const int* pages, float* out) {
+__device__ __noinline__ void paged_scalar_sum(const PagedParams& p, int cand, int h, int lane, int first, int count,
+                                              int stride, int entries, const uint8_t* list, int k0, int k1, int len,
+                                              const int* pages, float* out) {
   int lo[NI], hi[NI];
   if (p.func) {
     load_row_intervals<NI>(p.func, p.num_cand, cand, len, true, lo, hi, (1u << ((p.nfunc + 1) / 2)) - 1u);
@@ -124,7 +140,8 @@ __device__ __noinline__ void paged_scalar_sum(const PagedParams& p, int cand, in
   const int page0 = k0 >> p.cache.page_shift;
   float sum[DV / 32];
   for (int i = 0; i < DV / 32; ++i) sum[i] = 0.0f;
-  for (int key0 = k0 + warp * kPagedTile; key0 < k1; key0 += kPagedWarps * kPagedTile) {
+  for (int e = first; e < entries; e = (e + 1 - first) % stride < count ? e + 1 : e + 1 + stride - count) {
+    const int key0 = k0 + (p.func ? list[e] : e) * kPagedTile;
     const int64_t row0 = cache_row(p.cache, pages[(key0 >> p.cache.page_shift) - page0], h,
                                    key0 & ((1 << p.cache.page_shift) - 1));
     for (int key = key0; key < min(key0 + kPagedTile, k1); ++key) {
@@ -146,28 +163,48 @@ __device__ __noinline__ void paged_scalar_sum(const PagedParams& p, int cand, in
   for (int i = 0; i < DV / 32; ++i) out[lane + 32 * i] = sum[i];
 }
 
+// Sizes that follow from the types and widths.
+template <int DQ, int DV, bool E4M3>
+struct PagedSizes {
+  static constexpr int ES = E4M3 ? 1 : 2;               // bytes of a cached element
+  static constexpr int KROW = DQ * ES, VROW = DV * ES;  // bytes of a cached row
+  static constexpr int KC = KROW / 16, VC = VROW / 16;  // 16-byte pieces of a row
+  // One warp's step: 16 rows of k, of v, and their scale bytes.
+  static constexpr int kStep = kPagedTile * (KROW + VROW) + (E4M3 ? 32 : 0);
+  // Steps in flight: enough bytes of the SM's CTAs together to cover HBM's
+  // latency (48 KB an SM), within 227 KB of shared memory.
+  static constexpr int kStages = kStep >= 8192 ? 3 : 4;
+  static constexpr int kRing = kPagedWarps * kStages * kStep;
+  static constexpr int kRed = kPagedWarps * kPagedGroup * DV * 4;  // the warps' sums, after the ring's use
+  static constexpr int kSmem = kRing > kRed ? kRing : kRed;
+  static constexpr int kResident = kSmem > 72 * 1024 ? 2 : 3;  // CTAs of an SM
+};
+
 // T: type of q, o and 16-bit pages. E4M3: 8-bit pages. NI: intervals a
 // candidate may have.
 template <typename T, int DQ, int DV, bool E4M3, int NI>
-__global__ void __launch_bounds__(kPagedThreads) paged_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(kPagedThreads, PagedSizes<DQ, DV, E4M3>::kResident) paged_kernel(const PagedParams p) {
+  using Z = PagedSizes<DQ, DV, E4M3>;
   constexpr bool kHalf = E4M3 || std::is_same<T, __half>::value;  // products in fp16
   constexpr bool kSplitQ = E4M3 && !std::is_same<T, __half>::value;
   using M = typename std::conditional<kHalf, __half, __nv_bfloat16>::type;
-  constexpr int ES = E4M3 ? 1 : 2;              // bytes of a cached element
-  constexpr int KROW = DQ * ES, VROW = DV * ES;  // bytes of a cached row
+  constexpr int KROW = Z::KROW, VROW = Z::VROW, KC = Z::KC, VC = Z::VC;
   // k pieces: a lane reads DQ / 4 columns of a key row
   constexpr int KB = (KROW / 4) < 16 ? KROW / 4 : 16;  // bytes of a piece
   constexpr int KP = KROW / 4 / KB;                    // pieces
   // v pieces: a lane reads DV / 8 columns of a key row
   constexpr int VB = (VROW / 8) < 16 ? VROW / 8 : 16;
   constexpr int VP = VROW / 8 / VB;
-  constexpr int VE = VB / ES;  // columns of a v piece
+  constexpr int VE = VB / Z::ES;  // columns of a v piece
   constexpr int KSTEPS = DQ / 16, VTILES = DV / 8;
   constexpr float kLow = 2048.0f, kLowInv = 1.0f / 2048.0f;  // scale of the low parts in fp16
+  constexpr float kMaxFinite = 3.402823466e38f;
 
-  __shared__ float red[kPagedWarps][kPagedGroup][DV];
+  extern __shared__ __align__(128) uint8_t ring[];
   __shared__ int pages[kPagedMaxSplit / kPagedTile];
-  __shared__ int sh_flag;
+  __shared__ uint32_t tile_bits[kPagedMaxSplit / kPagedTile / 32];
+  __shared__ uint8_t list[kPagedMaxSplit / kPagedTile];
+  __shared__ int sh_flag, sh_entries;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int64_t bid = blockIdx.x;
@@ -216,25 +253,99 @@ __global__ void __launch_bounds__(kPagedThreads) paged_kernel(const PagedParams 
 
   const char* kbase = static_cast<const char*>(p.cache.k);
   const char* vbase = static_cast<const char*>(p.cache.v);
+  const uint32_t ring_addr = smem_u32(ring);
+  float* red = reinterpret_cast<float*>(ring);
 
-  for (int c0 = cb; c0 < ce; c0 += kPagedGroup) {
-    const int ncand = min(kPagedGroup, ce - c0);
+  for (int c0 = cb; c0 < ce;) {
+    // Slices of `wg` warps; warp `gi` of its slice has candidates cg .. cg + 7.
+    const int groups = (ce - c0 + kPagedGroup - 1) / kPagedGroup;
+    const int wg = groups == 1 ? 1 : (groups == 2 ? 2 : 4);
+    const int nslices = kPagedWarps / wg, slice = warp / wg, gi = warp % wg;
+    const int cg = c0 + gi * kPagedGroup;
+    const int ncand = max(0, min(kPagedGroup, ce - cg));
     const bool has = g < ncand;
     // Intervals of candidate g.
     int lo[NI], hi[NI];
+    int entries = ntiles;
     if (p.func) {
-      load_row_intervals<NI>(p.func, p.num_cand, c0 + g, len, has, lo, hi, (1u << ((p.nfunc + 1) / 2)) - 1u);
+      load_row_intervals<NI>(p.func, p.num_cand, cg + g, len, has, lo, hi, (1u << ((p.nfunc + 1) / 2)) - 1u);
+      // The tiles that some candidate of this pass sees.
+      if (tid < kPagedMaxSplit / kPagedTile / 32) tile_bits[tid] = 0;
+      __syncthreads();
+      if (slice == 0 && t == 0) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const int a = max(lo[i], k0) - k0, e = min(hi[i], k1) - k0;
+          if (e <= a) continue;
+          const int first = a / kPagedTile, last = (e - 1) / kPagedTile;
+          for (int w = first >> 5; w <= last >> 5; ++w) {
+            uint32_t bits = 0xffffffffu;
+            if (w == first >> 5) bits &= 0xffffffffu << (first & 31);
+            if (w == last >> 5) bits &= 0xffffffffu >> (31 - (last & 31));
+            atomicOr(&tile_bits[w], bits);
+          }
+        }
+      }
+      __syncthreads();
+      if (warp == 0) {
+        const uint32_t mine = (tile_bits[lane >> 2] >> (8 * (lane & 3))) & 0xffu;  // tiles 8 lane .. 8 lane + 7
+        int at = __popc(mine);
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const int o = __shfl_up_sync(0xffffffffu, at, off);
+          if (lane >= off) at += o;
+        }
+        if (lane == 31) sh_entries = bad ? 0 : at;
+        at -= __popc(mine);
+        for (int i = 0; i < 8; ++i)
+          if ((mine >> i) & 1u) list[at++] = static_cast<uint8_t>(8 * lane + i);
+      }
+      __syncthreads();
+      entries = sh_entries;
     } else {
 #pragma unroll
       for (int i = 0; i < NI; ++i) lo[i] = hi[i] = 0;
       if (has) hi[0] = len;
     }
+    const int iters = (entries + kPagedWarps - 1) / kPagedWarps;
+
+    // Copies this warp's tile of iteration `it` of its slice.
+    const auto issue = [&](int it) {
+      const int e = (it * nslices + slice) * wg + gi;
+      if (it < iters && e < entries) {
+        const int key0 = k0 + (p.func ? list[e] : e) * kPagedTile;
+        const int page = pages[(key0 >> p.cache.page_shift) - page0];
+        const int64_t row0 = cache_row(p.cache, page, h, key0 & (page_size - 1));
+        const int nkeys = k1 - key0;
+        const uint32_t dst = ring_addr + ((slice * Z::kStages + it % Z::kStages) * wg + gi) * Z::kStep;
+        const char* ksrc = kbase + row0 * KROW;
+        const char* vsrc = vbase + row0 * VROW;
+#pragma unroll
+        for (int i = 0; i < KROW / 32; ++i) {
+          const int u = i * 32 + lane, r = u / KC, c = u % KC;
+          const int sw = KC >= 8 ? (r & 1) << 2 : 0;
+          copy16(dst + r * KROW + (c ^ sw) * 16, ksrc + u * 16, r < nkeys);
+        }
+#pragma unroll
+        for (int i = 0; i < VROW / 32; ++i) {
+          const int u = i * 32 + lane, r = u / VC, c = u % VC;
+          const int sw = VC >= 8 ? r & 6 : (VC == 4 ? (r >> 1) & 3 : 0);
+          copy16(dst + kPagedTile * KROW + r * VROW + (c ^ sw) * 16, vsrc + u * 16, r < nkeys);
+        }
+        if (E4M3 && lane < 2)
+          copy16(dst + kPagedTile * (KROW + VROW) + 16 * lane, (lane ? p.cache.v_scale : p.cache.k_scale) + row0, true);
+      }
+      copies_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < Z::kStages - 1; ++i) issue(i);
+
     // Q fragments: rows 0..7 the candidates, rows 8..15 zero or low parts.
     uint32_t qa[KSTEPS][2], ql[kSplitQ ? KSTEPS : 1][2];
     float qscale = p.alpha;
     {
-      const T* qrow = static_cast<const T*>(p.q) + static_cast<int64_t>(c0 + g) * p.q_stride + h * DQ;
-      constexpr int KE = KB / ES;  // columns of a k piece: 16, 8
+      const T* qrow = static_cast<const T*>(p.q) + static_cast<int64_t>(has ? cg + g : c0) * p.q_stride + h * DQ;
+      constexpr int KE = KB / Z::ES;  // columns of a k piece: 16, 8
       float f[KSTEPS][4];
 #pragma unroll
       for (int i = 0; i < KP; ++i) {
@@ -284,141 +395,143 @@ __global__ void __launch_bounds__(kPagedThreads) paged_kernel(const PagedParams 
       for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
     int erun = 30;  // biased exponent that this candidate's P is scaled to (fp16 products)
 
-    for (int tile = warp; tile < ntiles; tile += kPagedWarps) {
-      const int key0 = k0 + tile * kPagedTile;
-      bool hit = false;
-#pragma unroll
-      for (int i = 0; i < NI; ++i) hit |= lo[i] < key0 + kPagedTile && hi[i] > key0;
-      if (!__any_sync(0xffffffffu, hit)) continue;
-      const int page = pages[(key0 >> p.cache.page_shift) - page0];
-      const int64_t row0 = cache_row(p.cache, page, h, key0 & (page_size - 1));
-      const int nkeys = min(kPagedTile, k1 - key0);
+    for (int it = 0; it < iters; ++it) {
+      copies_wait<Z::kStages - 2>();  // this warp's copies of iteration `it` have landed
+      if (wg == 1) __syncwarp();
+      else asm volatile("bar.sync %0, %1;" ::"r"(1 + slice), "r"(32 * wg) : "memory");
+      issue(it + Z::kStages - 1);  // into the stage that the slice used last
+      if (ncand == 0) continue;
+      for (int j = 0; j < wg; ++j) {
+        const int entry = (it * nslices + slice) * wg + j;
+        if (entry >= entries) break;
+        const int key0 = k0 + (p.func ? list[entry] : entry) * kPagedTile;
+        const uint32_t kt = ring_addr + ((slice * Z::kStages + it % Z::kStages) * wg + j) * Z::kStep;
+        const uint32_t vt = kt + kPagedTile * KROW;
 
-      // K: rows g and g + 8.
-      uint32_t kw[2][KP][KB / 4];
+        // S: key tile r holds keys 8r .. 8r + 7; this lane's columns are keys
+        // 8r + 2t and 8r + 2t + 1 of candidate g.
+        float s[2][4];
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
+        for (int r = 0; r < 2; ++r) {
+          s[r][0] = s[r][1] = s[r][2] = s[r][3] = 0.0f;
+          const int row = g + 8 * r;
+          const int sw = KC >= 8 ? (row & 1) << 2 : 0;
 #pragma unroll
-        for (int i = 0; i < KP; ++i)
-          load_piece<KB>(kbase + (row0 + g + 8 * r) * KROW + i * 4 * KB + t * KB, g + 8 * r < nkeys, kw[r][i]);
-      // V: rows 2t, 2t+1, 2t+8, 2t+9.
-      uint32_t vw[4][VP][VB / 4];
+          for (int i = 0; i < KP; ++i) {
+            uint32_t kw[KB / 4];
+            const int byte = i * 4 * KB + t * KB;
+            load_piece<KB>(kt + row * KROW + ((byte >> 4) ^ sw) * 16 + (byte & 15), kw);
+            if (E4M3) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int key = 2 * t + (r & 1) + 8 * (r >> 1);
+              for (int w = 0; w < KB / 4; ++w) {
+                const int st = i * (KB / 4) + w;
+                mma16816<M>(s[r], qa[st][0], kSplitQ ? ql[kSplitQ ? st : 0][0] : 0u, qa[st][1],
+                            kSplitQ ? ql[kSplitQ ? st : 0][1] : 0u, e4m3x2_to_f16x2(kw[w]),
+                            e4m3x2_to_f16x2(kw[w] >> 16));
+              }
+            } else {
 #pragma unroll
-        for (int i = 0; i < VP; ++i)
-          load_piece<VB>(vbase + (row0 + key) * VROW + i * 8 * VB + g * VB, key < nkeys, vw[r][i]);
-      }
-      float ks[4], vs[4];  // scales of keys 2t, 2t+1, 2t+8, 2t+9
-      if (E4M3) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int key = 2 * t + (r & 1) + 8 * (r >> 1);
-          ks[r] = key < nkeys ? scale_value(__ldg(p.cache.k_scale + row0 + key)) : 0.0f;
-          vs[r] = key < nkeys ? scale_value(__ldg(p.cache.v_scale + row0 + key)) : 0.0f;
-        }
-      }
-
-      // S: key tile r holds keys 8r .. 8r + 7; this lane's columns are keys
-      // 8r + 2t and 8r + 2t + 1 of candidate g.
-      float s[2][4];
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        s[r][0] = s[r][1] = s[r][2] = s[r][3] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < KP; ++i) {
-          if (E4M3) {
-#pragma unroll
-            for (int j = 0; j < KB / 4; ++j) {
-              const int st = i * (KB / 4) + j;
-              const uint32_t w = kw[r][i][j];
-              mma16816<M>(s[r], qa[st][0], kSplitQ ? ql[kSplitQ ? st : 0][0] : 0u, qa[st][1],
-                          kSplitQ ? ql[kSplitQ ? st : 0][1] : 0u, e4m3x2_to_f16x2(w), e4m3x2_to_f16x2(w >> 16));
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < KB / 8; ++j) {
-              const int st = i * (KB / 8) + j;
-              mma16816<M>(s[r], qa[st][0], 0u, qa[st][1], 0u, kw[r][i][2 * j], kw[r][i][2 * j + 1]);
+              for (int w = 0; w < KB / 8; ++w) {
+                const int st = i * (KB / 8) + w;
+                mma16816<M>(s[r], qa[st][0], 0u, qa[st][1], 0u, kw[2 * w], kw[2 * w + 1]);
+              }
             }
           }
         }
-      }
 
-      // P of candidate g at keys 2t, 2t+1, 2t+8, 2t+9.
-      float pr[4];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int key = key0 + 2 * t + (r & 1) + 8 * (r >> 1);
-        float x = s[r >> 1][r & 1];
-        if (kSplitQ) x = fmaf(s[r >> 1][2 + (r & 1)], kLowInv, x);
-        x *= qscale;
-        if (E4M3) x *= ks[r];
-        float v = silu_exact(x);
-        if (E4M3) v *= vs[r];
-        bool vis = false;
-#pragma unroll
-        for (int i = 0; i < NI; ++i) vis |= lo[i] <= key && key < hi[i];
-        pr[r] = vis ? v : 0.0f;
-      }
-      uint32_t pa[2], pl[2];
-      if (kHalf) {
-        // Largest magnitude of the candidate in this tile: its four lanes.
-        float top = fmaxf(fmaxf(fabsf(pr[0]), fabsf(pr[1])), fmaxf(fabsf(pr[2]), fabsf(pr[3])));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int e = static_cast<int>(__float_as_uint(top) >> 23);
-        if (e > erun) {
-          const float down = e - erun < 127 ? __uint_as_float(static_cast<uint32_t>(127 - (e - erun)) << 23) : 0.0f;
-#pragma unroll
-          for (int j = 0; j < VTILES; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[j][i] *= down;
-          erun = e;
-        }
-        const float up = __uint_as_float(static_cast<uint32_t>(268 - erun) << 23);  // 2^14 at the largest
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float x = pr[2 * r] * up, y = pr[2 * r + 1] * up;
-          pa[r] = pack_f16x2(x, y);
-          pl[r] = pack_f16x2((x - Elem<__half>::lo(pa[r])) * kLow, (y - Elem<__half>::hi(pa[r])) * kLow);
-        }
-      } else {
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float x = pr[2 * r], y = pr[2 * r + 1];
-          pa[r] = pack_bf16x2(x, y);
-          pl[r] = pack_bf16x2(x - Elem<__nv_bfloat16>::lo(pa[r]), y - Elem<__nv_bfloat16>::hi(pa[r]));
-        }
-      }
-
-      // O += P V: column tile (i, e) holds column e of the lanes' pieces i.
-#pragma unroll
-      for (int i = 0; i < VP; ++i) {
+        // P of candidate g at keys 2t, 2t+1, 2t+8, 2t+9.
+        float pr[4];
+        uint32_t scales[4];  // k and v scale bytes of keys 2t, 2t+1 and 2t+8, 2t+9
         if (E4M3) {
+          const uint32_t sc = vt + kPagedTile * VROW + 2 * t;
 #pragma unroll
-          for (int w = 0; w < VB / 4; ++w) {
-            // bytes (row 0, row 1) of columns 4w, 4w+1 and 4w+2, 4w+3
-            const uint32_t x0 = __byte_perm(vw[0][i][w], vw[1][i][w], 0x5140);
-            const uint32_t x1 = __byte_perm(vw[0][i][w], vw[1][i][w], 0x7362);
-            const uint32_t y0 = __byte_perm(vw[2][i][w], vw[3][i][w], 0x5140);
-            const uint32_t y1 = __byte_perm(vw[2][i][w], vw[3][i][w], 0x7362);
-            mma16816<M>(acc[i * VE + 4 * w], pa[0], pl[0], pa[1], pl[1], e4m3x2_to_f16x2(x0), e4m3x2_to_f16x2(y0));
-            mma16816<M>(acc[i * VE + 4 * w + 1], pa[0], pl[0], pa[1], pl[1], e4m3x2_to_f16x2(x0 >> 16),
-                        e4m3x2_to_f16x2(y0 >> 16));
-            mma16816<M>(acc[i * VE + 4 * w + 2], pa[0], pl[0], pa[1], pl[1], e4m3x2_to_f16x2(x1),
-                        e4m3x2_to_f16x2(y1));
-            mma16816<M>(acc[i * VE + 4 * w + 3], pa[0], pl[0], pa[1], pl[1], e4m3x2_to_f16x2(x1 >> 16),
-                        e4m3x2_to_f16x2(y1 >> 16));
+          for (int r = 0; r < 4; ++r) {
+            uint16_t u;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(u) : "r"(sc + 8 * r));
+            scales[r] = u;
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int key = key0 + 2 * t + (r & 1) + 8 * (r >> 1);
+          float x = s[r >> 1][r & 1];
+          if (kSplitQ) x = fmaf(s[r >> 1][2 + (r & 1)], kLowInv, x);
+          x *= qscale;
+          if (E4M3) x *= scale_value((scales[r >> 1] >> (8 * (r & 1))) & 0xffu);
+          float v = silu_exact(x);
+          if (E4M3) v *= scale_value((scales[2 + (r >> 1)] >> (8 * (r & 1))) & 0xffu);
+          bool vis = false;
+#pragma unroll
+          for (int i = 0; i < NI; ++i) vis |= lo[i] <= key && key < hi[i];
+          pr[r] = vis ? v : 0.0f;
+        }
+        uint32_t pa[2], pl[2];
+        if (kHalf) {
+          // Largest magnitude of the candidate in this tile: its four lanes.
+          float top = fmaxf(fmaxf(fabsf(pr[0]), fabsf(pr[1])), fmaxf(fabsf(pr[2]), fabsf(pr[3])));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const int e = static_cast<int>(__float_as_uint(top) >> 23);
+          if (e > erun) {
+            const float down = e - erun < 127 ? __uint_as_float(static_cast<uint32_t>(127 - (e - erun)) << 23) : 0.0f;
+#pragma unroll
+            for (int n = 0; n < VTILES; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) acc[n][i] *= down;
+            erun = e;
+          }
+          __syncwarp();
+          const float up = __uint_as_float(static_cast<uint32_t>(268 - erun) << 23);  // 2^14 at the largest
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float x = pr[2 * r] * up, y = pr[2 * r + 1] * up;
+            pa[r] = pack_f16x2(x, y);
+            pl[r] = pack_f16x2((x - Elem<__half>::lo(pa[r])) * kLow, (y - Elem<__half>::hi(pa[r])) * kLow);
           }
         } else {
 #pragma unroll
-          for (int w = 0; w < VB / 4; ++w) {
-            mma16816<M>(acc[i * VE + 2 * w], pa[0], pl[0], pa[1], pl[1], __byte_perm(vw[0][i][w], vw[1][i][w], 0x5410),
-                        __byte_perm(vw[2][i][w], vw[3][i][w], 0x5410));
-            mma16816<M>(acc[i * VE + 2 * w + 1], pa[0], pl[0], pa[1], pl[1],
-                        __byte_perm(vw[0][i][w], vw[1][i][w], 0x7632), __byte_perm(vw[2][i][w], vw[3][i][w], 0x7632));
+          for (int r = 0; r < 2; ++r) {
+            const float x = pr[2 * r], y = pr[2 * r + 1];
+            pa[r] = pack_bf16x2(x, y);
+            pl[r] = pack_bf16x2(x - Elem<__nv_bfloat16>::lo(pa[r]), y - Elem<__nv_bfloat16>::hi(pa[r]));
+          }
+        }
+
+        // O += P V: column tile (i, e) holds column e of the lanes' pieces i.
+        // V rows 2t, 2t+1, 2t+8, 2t+9.
+#pragma unroll
+        for (int i = 0; i < VP; ++i) {
+          uint32_t vw[4][VB / 4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int row = 2 * t + (r & 1) + 8 * (r >> 1);
+            const int sw = VC >= 8 ? row & 6 : (VC == 4 ? (row >> 1) & 3 : 0);
+            const int byte = i * 8 * VB + g * VB;
+            load_piece<VB>(vt + row * VROW + ((byte >> 4) ^ sw) * 16 + (byte & 15), vw[r]);
+          }
+          if (E4M3) {
+#pragma unroll
+            for (int w = 0; w < VB / 4; ++w) {
+              // bytes (row 0, row 1) of columns 4w, 4w+1 and 4w+2, 4w+3
+              const uint32_t x0 = __byte_perm(vw[0][w], vw[1][w], 0x5140);
+              const uint32_t x1 = __byte_perm(vw[0][w], vw[1][w], 0x7362);
+              const uint32_t y0 = __byte_perm(vw[2][w], vw[3][w], 0x5140);
+              const uint32_t y1 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
+              float(*o)[4] = acc + i * VE + 4 * w;
+              mma16816<M>(o[0], pa[0], pl[0], pa[1], pl[1], e4m3x2_to_f16x2(x0), e4m3x2_to_f16x2(y0));
+              mma16816<M>(o[1], pa[0], pl[0], pa[1], pl[1], e4m3x2_to_f16x2(x0 >> 16), e4m3x2_to_f16x2(y0 >> 16));
+              mma16816<M>(o[2], pa[0], pl[0], pa[1], pl[1], e4m3x2_to_f16x2(x1), e4m3x2_to_f16x2(y1));
+              mma16816<M>(o[3], pa[0], pl[0], pa[1], pl[1], e4m3x2_to_f16x2(x1 >> 16), e4m3x2_to_f16x2(y1 >> 16));
+            }
+          } else {
+#pragma unroll
+            for (int w = 0; w < VB / 4; ++w) {
+              float(*o)[4] = acc + i * VE + 2 * w;
+              mma16816<M>(o[0], pa[0], pl[0], pa[1], pl[1], __byte_perm(vw[0][w], vw[1][w], 0x5410),
+                          __byte_perm(vw[2][w], vw[3][w], 0x5410));
+              mma16816<M>(o[1], pa[0], pl[0], pa[1], pl[1], __byte_perm(vw[0][w], vw[1][w], 0x7632),
+                          __byte_perm(vw[2][w], vw[3][w], 0x7632));
+            }
           }
         }
       }
@@ -426,7 +539,9 @@ __global__ void __launch_bounds__(kPagedThreads) paged_kernel(const PagedParams 
 
     // This warp's sums: candidate g, columns (2t, 2t+1) of each column tile,
     // i.e. columns [2t VE, 2t VE + 2 VE) of piece group i.
-    const float back = kHalf ? __uint_as_float(static_cast<uint32_t>(max(erun - 14, 0)) << 23) : 1.0f;
+    __syncthreads();  // the ring is free: the sums take its place
+    float* mine = red + warp * kPagedGroup * DV;
+    const float back = kHalf ? __uint_as_float(static_cast<uint32_t>(erun - 14) << 23) : 1.0f;
     bool finite = true;
 #pragma unroll
     for (int i = 0; i < VP; ++i)
@@ -435,28 +550,28 @@ __global__ void __launch_bounds__(kPagedThreads) paged_kernel(const PagedParams 
         const float(&a)[4] = acc[i * VE + e];
         const float x = (kHalf ? fmaf(a[2], kLowInv, a[0]) : a[0] + a[2]) * back;
         const float y = (kHalf ? fmaf(a[3], kLowInv, a[1]) : a[1] + a[3]) * back;
-        finite = finite && fabsf(x) <= 3.402823466e38f && fabsf(y) <= 3.402823466e38f;
-        red[warp][g][i * 8 * VE + 2 * t * VE + e] = x;
-        red[warp][g][i * 8 * VE + (2 * t + 1) * VE + e] = y;
+        finite = finite && fabsf(x) <= kMaxFinite && fabsf(y) <= kMaxFinite;
+        mine[g * DV + i * 8 * VE + 2 * t * VE + e] = x;
+        mine[g * DV + i * 8 * VE + (2 * t + 1) * VE + e] = y;
       }
     // A sum that is not finite may have met a value that its candidate does
     // not see (zero times infinity): those candidates are summed again, key by
     // key, over what they see alone.
     const uint32_t odd = __ballot_sync(0xffffffffu, has && !finite);
     if (odd != 0) {
-      __syncwarp();
-      for (int r = 0; r < ncand; ++r) {
-        if (((odd >> (4 * r)) & 15u) == 0) continue;
-        paged_scalar_sum<T, DQ, DV, E4M3, NI>(p, c0 + r, h, warp, lane, k0, k1, len, pages, red[warp][r]);
-      }
+      for (int r = 0; r < ncand; ++r)
+        if (((odd >> (4 * r)) & 15u) != 0)
+          paged_scalar_sum<T, DQ, DV, E4M3, NI>(p, cg + r, h, lane, slice * wg, wg, kPagedWarps, entries, list, k0, k1,
+                                                len, pages, mine + r * DV);
     }
     __syncthreads();
-    // The warps' sums in warp order.
-    for (int i = tid; i < ncand * DV; i += kPagedThreads) {
+    // The slices' sums in slice order.
+    const int taken = min(ce - c0, wg * kPagedGroup);
+    for (int i = tid; i < taken * DV; i += kPagedThreads) {
       const int r = i / DV, d = i % DV;
-      float sum = red[0][r][d];
-#pragma unroll
-      for (int w = 1; w < kPagedWarps; ++w) sum += red[w][r][d];
+      const float* from = red + r * DV + d;  // group r / 8 is warp r / 8 of each slice
+      float sum = from[0];
+      for (int w = 1; w < nslices; ++w) sum += from[w * wg * kPagedGroup * DV];
       const int64_t at = static_cast<int64_t>(c0 + r) * p.cache.heads + h;
       if (splits > 1) {
         p.partial[(at * p.nsplit + split) * DV + d] = sum;
@@ -466,12 +581,13 @@ __global__ void __launch_bounds__(kPagedThreads) paged_kernel(const PagedParams 
       }
     }
     __syncthreads();
+    c0 += taken;
   }
   if (splits == 1) return;
 
   // The last CTA of this (sequence, head) to arrive joins the splits' sums in
-  // split order. A split with a bad page marks the counter, and nothing is
-  // written then.
+  // a fixed order: a quarter of the splits for each warp, then the quarters.
+  // A split with a bad page marks the counter, and nothing is written then.
   __threadfence();
   __syncthreads();
   if (tid == 0) sh_flag = atomicAdd(p.counters + bh, bad ? 1 + (1 << 20) : 1) + (bad ? 1 << 20 : 0);
@@ -479,23 +595,50 @@ __global__ void __launch_bounds__(kPagedThreads) paged_kernel(const PagedParams 
   const int seen = sh_flag;
   if ((seen & 0xfffff) != splits - 1 || seen >> 20 != 0) return;
   __threadfence();
-  for (int64_t i = tid; i < static_cast<int64_t>(ce - cb) * DV; i += kPagedThreads) {
-    const int64_t at = (cb + i / DV) * p.cache.heads + h;
-    const int d = static_cast<int>(i % DV);
-    float sum = 0.0f;
-    for (int s = 0; s < splits; ++s) sum += __ldcg(p.partial + (at * p.nsplit + s) * DV + d);
-    const uint32_t w = Elem<T>::pack2(sum * p.inv_n, 0.0f);
-    static_cast<T*>(p.o)[at * DV + d] = *reinterpret_cast<const T*>(&w);
+  const int quarter = (splits + kPagedWarps - 1) / kPagedWarps;
+  for (int c0 = cb; c0 < ce; c0 += kPagedGroup) {
+    const int n = min(kPagedGroup, ce - c0);
+    for (int item = warp; item < n * kPagedWarps; item += kPagedWarps) {
+      const int r = item / kPagedWarps, qt = item % kPagedWarps;
+      const float* from = p.partial + (static_cast<int64_t>(c0 + r) * p.cache.heads + h) * p.nsplit * DV;
+      float sum[DV / 32];
+#pragma unroll
+      for (int i = 0; i < DV / 32; ++i) sum[i] = 0.0f;
+#pragma unroll 4
+      for (int s = qt * quarter; s < min(splits, (qt + 1) * quarter); ++s)
+#pragma unroll
+        for (int i = 0; i < DV / 32; ++i) sum[i] += __ldcg(from + s * DV + 32 * i + lane);
+#pragma unroll
+      for (int i = 0; i < DV / 32; ++i) red[(qt * kPagedGroup + r) * DV + 32 * i + lane] = sum[i];
+    }
+    __syncthreads();
+    for (int i = tid; i < n * DV; i += kPagedThreads) {
+      float sum = red[i];
+#pragma unroll
+      for (int qt = 1; qt < kPagedWarps; ++qt) sum += red[qt * kPagedGroup * DV + i];
+      const int64_t at = static_cast<int64_t>(c0 + i / DV) * p.cache.heads + h;
+      const uint32_t w = Elem<T>::pack2(sum * p.inv_n, 0.0f);
+      static_cast<T*>(p.o)[at * DV + i % DV] = *reinterpret_cast<const T*>(&w);
+    }
+    __syncthreads();
   }
 }
 
 // Launches the kernel for the widths of p.cache (one function for each type,
 // in a translation unit of its own so that they compile in parallel).
+template <typename T, bool E4M3, int DQ, int DV, int NI>
+cudaError_t launch_paged_one(const PagedParams& p, unsigned blocks, cudaStream_t stream) {
+  constexpr int kSmem = PagedSizes<DQ, DV, E4M3>::kSmem;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = ensure_smem_limit(paged_kernel<T, DQ, DV, E4M3, NI>, kSmem, done);
+  if (e != cudaSuccess) return e;
+  paged_kernel<T, DQ, DV, E4M3, NI><<<blocks, kPagedThreads, kSmem, stream>>>(p);
+  return cudaGetLastError();
+}
 template <typename T, bool E4M3, int DQ, int DV>
 cudaError_t launch_paged_widths(const PagedParams& p, unsigned blocks, cudaStream_t stream) {
-  if (!p.func || p.nfunc == 1) paged_kernel<T, DQ, DV, E4M3, 1><<<blocks, kPagedThreads, 0, stream>>>(p);
-  else paged_kernel<T, DQ, DV, E4M3, kMaxIntervals><<<blocks, kPagedThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  if (!p.func || p.nfunc == 1) return launch_paged_one<T, E4M3, DQ, DV, 1>(p, blocks, stream);
+  return launch_paged_one<T, E4M3, DQ, DV, kMaxIntervals>(p, blocks, stream);
 }
 template <typename T, bool E4M3, int DQ>
 cudaError_t launch_paged_dv(const PagedParams& p, unsigned blocks, cudaStream_t stream) {
