@@ -37,9 +37,9 @@ __device__ __forceinline__ bool find_sequence(const int32_t* __restrict__ offset
   return first >= 0 && first <= t && t < __ldg(offsets + lo + 1);
 }
 
-// 2^(byte - 127).
+// 2^(byte - 127); 2^-127 is below the normal numbers, hence the maximum.
 __device__ __forceinline__ float scale_value(uint32_t byte) {
-  return __uint_as_float(byte == 0 ? 0x00400000u : byte << 23);
+  return __uint_as_float(max(byte << 23, 0x00400000u));
 }
 
 // Scale byte of a row whose largest finite magnitude is `top`: the smallest
@@ -61,6 +61,13 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(w)));
+  return r;
+}
+
+// The high two codes of w.
+__device__ __forceinline__ uint32_t e4m3x2_hi_to_f16x2(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(r) : "r"(w));
   return r;
 }
 

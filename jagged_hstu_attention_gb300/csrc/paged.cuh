@@ -9,28 +9,34 @@
 // cache's rows.
 //
 // A CTA takes one (sequence, head) and one split of its length. Its four warps
-// form slices of 1, 2 or 4 warps, as many as the sequence has groups of eight
-// candidates; a slice reads every (4 / warps)-th step of 16 keys a warp into
-// its ring of shared memory with asynchronous copies, and each of its warps
-// multiplies all of the step's keys with its own eight candidates. Per 16 keys:
-//   S = Q K^T   16 x 8 tiles, rows = 8 candidates (rows 8..15 see below)
-//   P = silu(alpha S), zero where not visible, split into two 16-bit parts
-//   O += P V    rows 0..7 hold the high part of P, rows 8..15 its low part
-// With eight candidates in a 16-row operand the low part of P costs no extra
-// instruction, and P V is as exact as with P in fp32 (rounding P to 16 bits
-// instead would be as large an error as that of the output's own type).
+// form slices of 1, 2 or 4 warps, as many as the sequence's candidates need; a
+// warp reads tiles of 16 keys into its ring of shared memory with asynchronous
+// copies, and each warp of a slice multiplies all of the slice's tiles with
+// its own candidates. Per tile, keys and value columns as the 16 rows of the
+// products and candidates as their 8 columns:
+//   S^T = K Q^T    P = silu(alpha S), zero where not visible
+//   O^T += V^T P^T P in two 16-bit parts, so that P V is as exact as with P in
+//                  fp32 (rounding P to 16 bits instead would be as large an
+//                  error as that of the output's own type)
+// Up to four candidates ("pair") have two columns each, one for each part of
+// P, so that one instruction adds both. More ("full") take a column each, in
+// one or two groups of eight, and an instruction for each part: a piece of K
+// and V that is brought into operand form then serves up to 16 candidates.
 //
 // Operand layout. The order of the columns inside a contraction is free as
 // long as both operands share it, so each lane reads whole 16-byte pieces of
 // a row: lane (g, t) = (lane / 4, lane % 4) takes columns [8t, 8t + 8) of
-// each 32 of key row g, which are its parts of two k = 16 steps, and the same
-// columns of candidate row g. For P V lane (g, t) reads piece g of the key
+// each 32 of key rows g and g + 8, which are its parts of two k = 16 steps,
+// and the same columns of candidate row g. For V^T it reads piece g of the key
 // rows 2t, 2t+1, 2t+8, 2t+9 and pairs the rows' columns with byte
-// permutations.
+// permutations. P^T comes out of the first product with keys along g and is
+// turned by movmatrix, 8 x 8 values an instruction. In shared memory the
+// 16-byte pieces of a row are permuted by bits of the row's index so that the
+// eight lanes of a load phase meet different banks.
 //
 // Types. 16-bit caches multiply in their own type. 8-bit codes become fp16
 // (exact); a bf16 candidate row is then scaled by a power of two and split
-// into two fp16 parts in the same way as P (rows 8..15). A key's scale
+// into two fp16 parts in the same way as P. A key's scale
 // multiplies its column of S, a value row's scale its column of P, both exact
 // powers of two. In fp16 the range of P needs care: a candidate's P is scaled
 // by a power of two that follows its running maximum (when it grows, the sums
@@ -48,7 +54,7 @@ namespace hstu {
 constexpr int kPagedWarps = 4;
 constexpr int kPagedThreads = 32 * kPagedWarps;
 constexpr int kPagedTile = 16;     // keys of a warp's step
-constexpr int kPagedGroup = 8;     // candidates of a pass
+constexpr int kPagedPass = 64;     // candidates of a pass, at most
 constexpr int kPagedMaxSplit = 4096;  // keys of a split, at most
 
 struct PagedParams {
@@ -111,7 +117,15 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
 }
 
-__device__ __forceinline__ float silu_exact(float x) { return x * sigmoidf_fast(x); }
+// x sigmoid(x) with the hardware's exponential and reciprocal (relative error
+// about |x| 2^-24 + 2^-22). Far below zero the exponential is infinite and the
+// result -0.
+__device__ __forceinline__ float silu_exact(float x) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return x * r;
+}
 
 // Column `i` of a cached matrix as fp32 (8-bit codes without their scale).
 template <typename T, bool E4M3>
@@ -120,34 +134,138 @@ __device__ __forceinline__ float cached_value(const void* base, int64_t i) {
   return Elem<T>::lo(static_cast<const uint16_t*>(base)[i]);
 }
 
-// The sum of one candidate over the steps of one slice, in fp32, one visible
-// key after the other: the way out for sums that are not finite. The slice
-// takes entries [first, first + count), and so on every `stride` entries, of
-// the split's list of 16-key tiles (the tiles themselves without a list).
-template <typename T, int DQ, int DV, bool E4M3, int NI>
-__device__ __noinline__ void paged_scalar_sum(const PagedParams& p, int cand, int h, int lane, int first, int count,
-                                              int stride, int entries, const uint8_t* list, int k0, int k1, int len,
-                                              const int* pages, float* out) {
-  int lo[NI], hi[NI];
-  if (p.func) {
-    load_row_intervals<NI>(p.func, p.num_cand, cand, len, true, lo, hi, (1u << ((p.nfunc + 1) / 2)) - 1u);
-  } else {
-    for (int i = 0; i < NI; ++i) lo[i] = hi[i] = 0;
-    hi[0] = len;
+// Sizes that follow from the types and widths. MANY: the kernel for any number
+// of candidates; otherwise the one for a single candidate a sequence.
+template <int DQ, int DV, bool E4M3, bool MANY>
+struct PagedSizes {
+  static constexpr int ES = E4M3 ? 1 : 2;               // bytes of a cached element
+  static constexpr int KROW = DQ * ES, VROW = DV * ES;  // bytes of a cached row
+  static constexpr int KC = KROW / 16, VC = VROW / 16;  // 16-byte pieces of a row
+  // k pieces: a lane reads KP of KB bytes, DQ / 4 columns of a key row;
+  // v pieces: VP of VB bytes (VE columns), DV / 8 columns of a key row
+  static constexpr int KB = KROW / 4 < 16 ? KROW / 4 : 16, KP = KROW / 4 / KB;
+  static constexpr int VB = VROW / 8 < 16 ? VROW / 8 : 16, VP = VROW / 8 / VB, VE = VB / ES;
+  // One warp's tile: 16 rows of k, of v, and their scale bytes.
+  static constexpr int kStep = kPagedTile * (KROW + VROW) + (E4M3 ? 32 : 0);
+  // Tiles of a warp's ring: enough in flight on an SM to cover HBM's latency
+  // (48 KB); two stages where the warps of a slice share tiles, whose products
+  // take longer than the copies.
+  static constexpr int kStages = kStep <= 2080 ? 4 : (MANY && kStep >= 4096 ? 2 : 3);
+  static constexpr int kRing = kPagedWarps * kStages * kStep;
+  // The warps' sums, after the ring's use. A lane (g, t) writes VE columns of
+  // each piece of row t: blocks of VE + 1 and rows of 8 (mod 32) put the
+  // lanes' stores into different banks.
+  static constexpr int kBlock = VE + 1;
+  static constexpr int kRedRow = (VP * 8 * kBlock + 31) / 32 * 32 + 8;
+  static constexpr int kRedRows = MANY ? 16 : 4;  // of a warp
+  static constexpr int kRed = kPagedWarps * kRedRows * kRedRow * 4;
+  static constexpr int kSmem = kRing > kRed ? kRing : kRed;
+  static constexpr int kFit = 227 * 1024 / (kSmem + 6144);  // CTAs that shared memory has room for
+  static constexpr int kResident = kFit < 1 ? 1 : (kFit > (MANY ? 3 : 4) ? (MANY ? 3 : 4) : kFit);
+  static __device__ __forceinline__ int red_column(int d) { return d / VE * kBlock + d % VE; }
+};
+
+// What a CTA's passes share.
+struct PagedSplit {
+  int h, k0, k1, len, page0, tiles;
+  int c0, ce;         // candidates still to do
+  const int* pages;   // shared memory: pages of the split,
+  uint32_t* bits;     // tiles that some candidate sees, tiles that some does not see whole,
+  uint16_t* list;     // the seen tiles (bit 15: not seen whole by all)
+  int* iv;            // and the candidates' intervals
+  int* entries;
+  uint32_t ring;      // shared-memory address of the ring
+  float* red;
+};
+constexpr int kPagedWords = kPagedMaxSplit / kPagedTile / 32;
+constexpr int kPagedIv = 2 * kMaxIntervals + 1;  // ints of a candidate's intervals (odd: different banks)
+
+// Lists the tiles that the pass's candidates see.
+__device__ __forceinline__ int paged_list(const PagedParams& p, const PagedSplit& sp, int ncand) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (tid < 2 * kPagedWords) sp.bits[tid] = 0;
+  __syncthreads();
+  if (tid < ncand) {
+    int lo[kMaxIntervals], hi[kMaxIntervals];
+    load_row_intervals<kMaxIntervals>(p.func, p.num_cand, sp.c0 + tid, sp.len, true, lo, hi,
+                                      (1u << ((p.nfunc + 1) / 2)) - 1u);
+    uint32_t whole[kPagedWords];
+#pragma unroll
+    for (int w = 0; w < kPagedWords; ++w) whole[w] = 0;
+#pragma unroll
+    for (int i = 0; i < kMaxIntervals; ++i) {
+      sp.iv[tid * kPagedIv + 2 * i] = lo[i];
+      sp.iv[tid * kPagedIv + 2 * i + 1] = hi[i];
+      const int a = max(lo[i], sp.k0) - sp.k0, e = min(hi[i], sp.k1) - sp.k0;
+      if (e <= a) continue;
+      const int first = a / kPagedTile, last = (e - 1) / kPagedTile;              // tiles it touches
+      const int wfirst = (a + kPagedTile - 1) / kPagedTile, wlast = e / kPagedTile - 1;  // and covers
+#pragma unroll
+      for (int w = 0; w < kPagedWords; ++w) {
+        const auto span = [w](int x, int y) {  // bits of word w in [x, y]
+          const int u = max(x - 32 * w, 0), v = min(y - 32 * w, 31);
+          return u > v ? 0u : (0xffffffffu << u) & (0xffffffffu >> (31 - v));
+        };
+        const uint32_t seen = span(first, last);
+        if (seen) atomicOr(sp.bits + w, seen);
+        whole[w] |= span(wfirst, wlast);
+      }
+    }
+#pragma unroll
+    for (int w = 0; w < kPagedWords; ++w)
+      if (~whole[w]) atomicOr(sp.bits + kPagedWords + w, ~whole[w]);
   }
-  const uint16_t* q =
-      static_cast<const uint16_t*>(p.q) + static_cast<int64_t>(cand) * p.q_stride + static_cast<int64_t>(h) * DQ;
-  const int page0 = k0 >> p.cache.page_shift;
+  __syncthreads();
+  if (tid < 32) {
+    const int shift = 8 * (lane & 3);
+    const uint32_t mine = (sp.bits[lane >> 2] >> shift) & 0xffu;  // tiles 8 lane .. 8 lane + 7
+    const uint32_t part = (sp.bits[kPagedWords + (lane >> 2)] >> shift) & 0xffu;
+    int at = __popc(mine);
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, at, off);
+      if (lane >= off) at += o;
+    }
+    if (lane == 31) *sp.entries = sp.tiles > 0 ? at : 0;
+    at -= __popc(mine);
+    for (int i = 0; i < 8; ++i)
+      if ((mine >> i) & 1u) sp.list[at++] = static_cast<uint16_t>((8 * lane + i) | (((part >> i) & 1u) << 15));
+  }
+  __syncthreads();
+  return *sp.entries;
+}
+
+// Whether candidate r of the pass sees `key`.
+__device__ __forceinline__ bool paged_sees(const PagedParams& p, const PagedSplit& sp, int r, int key) {
+  if (!p.func) return key < sp.k1;
+  bool vis = false;
+  const int n = (p.nfunc + 1) / 2;
+  for (int i = 0; i < n; ++i) vis |= sp.iv[r * kPagedIv + 2 * i] <= key && key < sp.iv[r * kPagedIv + 2 * i + 1];
+  return vis;
+}
+
+__device__ __forceinline__ int paged_key(const PagedParams& p, const PagedSplit& sp, int entry) {
+  return sp.k0 + (p.func ? sp.list[entry] & 0x7fff : entry) * kPagedTile;
+}
+
+// The sum of candidate r of the pass over the tiles of one slice, in fp32, one
+// visible key after the other: the way out for sums that are not finite. The
+// slice takes entries [first, first + count), and so on every four entries.
+template <typename T, int DQ, int DV, bool E4M3, typename Z>
+__device__ __noinline__ void paged_scalar_sum(const PagedParams& p, const PagedSplit& sp, int r, int first, int count,
+                                              int entries, float* out) {
+  const int lane = threadIdx.x & 31;
+  const uint16_t* q = static_cast<const uint16_t*>(p.q) + static_cast<int64_t>(sp.c0 + r) * p.q_stride +
+                      static_cast<int64_t>(sp.h) * DQ;
   float sum[DV / 32];
   for (int i = 0; i < DV / 32; ++i) sum[i] = 0.0f;
-  for (int e = first; e < entries; e = (e + 1 - first) % stride < count ? e + 1 : e + 1 + stride - count) {
-    const int key0 = k0 + (p.func ? list[e] : e) * kPagedTile;
-    const int64_t row0 = cache_row(p.cache, pages[(key0 >> p.cache.page_shift) - page0], h,
+  for (int e = first; e < entries;
+       e = (e + 1 - first) % kPagedWarps < count ? e + 1 : e + 1 + kPagedWarps - count) {
+    const int key0 = paged_key(p, sp, e);
+    const int64_t row0 = cache_row(p.cache, sp.pages[(key0 >> p.cache.page_shift) - sp.page0], sp.h,
                                    key0 & ((1 << p.cache.page_shift) - 1));
-    for (int key = key0; key < min(key0 + kPagedTile, k1); ++key) {
-      bool vis = false;
-      for (int i = 0; i < NI; ++i) vis |= lo[i] <= key && key < hi[i];
-      if (!vis) continue;
+    for (int key = key0; key < min(key0 + kPagedTile, sp.k1); ++key) {
+      if (!paged_sees(p, sp, r, key)) continue;
       const int64_t row = row0 + key - key0;
       float dot = 0.0f;
       for (int i = lane; i < DQ; i += 32)
@@ -160,63 +278,408 @@ __device__ __noinline__ void paged_scalar_sum(const PagedParams& p, int cand, in
         sum[i] = fmaf(w, cached_value<T, E4M3>(p.cache.v, row * DV + lane + 32 * i), sum[i]);
     }
   }
-  for (int i = 0; i < DV / 32; ++i) out[lane + 32 * i] = sum[i];
+  for (int i = 0; i < DV / 32; ++i) out[Z::red_column(lane + 32 * i)] = sum[i];
 }
 
-// Sizes that follow from the types and widths.
-template <int DQ, int DV, bool E4M3>
-struct PagedSizes {
-  static constexpr int ES = E4M3 ? 1 : 2;               // bytes of a cached element
-  static constexpr int KROW = DQ * ES, VROW = DV * ES;  // bytes of a cached row
-  static constexpr int KC = KROW / 16, VC = VROW / 16;  // 16-byte pieces of a row
-  // One warp's step: 16 rows of k, of v, and their scale bytes.
-  static constexpr int kStep = kPagedTile * (KROW + VROW) + (E4M3 ? 32 : 0);
-  // Steps in flight: enough bytes of the SM's CTAs together to cover HBM's
-  // latency (48 KB an SM), within 227 KB of shared memory.
-  static constexpr int kStages = kStep >= 8192 ? 3 : 4;
-  static constexpr int kRing = kPagedWarps * kStages * kStep;
-  static constexpr int kRed = kPagedWarps * kPagedGroup * DV * 4;  // the warps' sums, after the ring's use
-  static constexpr int kSmem = kRing > kRed ? kRing : kRed;
-  static constexpr int kResident = kSmem > 72 * 1024 ? 2 : 3;  // CTAs of an SM
-};
+// 8 x 8 16-bit values, row g columns 2t, 2t+1 in lane (g, t), transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t w) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(w));
+  return r;
+}
 
-// T: type of q, o and 16-bit pages. E4M3: 8-bit pages. NI: intervals a
-// candidate may have.
-template <typename T, int DQ, int DV, bool E4M3, int NI>
-__global__ void __launch_bounds__(kPagedThreads, PagedSizes<DQ, DV, E4M3>::kResident) paged_kernel(const PagedParams p) {
-  using Z = PagedSizes<DQ, DV, E4M3>;
+// One pass over the split's keys: the sums of candidates c0 .. of this
+// sequence, as many as fit, in the CTA's shared memory. CG = 0: pair columns
+// (up to 4 candidates a warp), 1 or 2: groups of eight columns. Returns the
+// warps of a slice.
+template <typename T, int DQ, int DV, bool E4M3, bool MANY, int CG>
+__device__ __forceinline__ int paged_pass(const PagedParams& p, const PagedSplit& sp) {
+  using Z = PagedSizes<DQ, DV, E4M3, MANY>;
+  constexpr bool kPair = CG == 0;
   constexpr bool kHalf = E4M3 || std::is_same<T, __half>::value;  // products in fp16
   constexpr bool kSplitQ = E4M3 && !std::is_same<T, __half>::value;
   using M = typename std::conditional<kHalf, __half, __nv_bfloat16>::type;
   constexpr int KROW = Z::KROW, VROW = Z::VROW, KC = Z::KC, VC = Z::VC;
-  // k pieces: a lane reads DQ / 4 columns of a key row
-  constexpr int KB = (KROW / 4) < 16 ? KROW / 4 : 16;  // bytes of a piece
-  constexpr int KP = KROW / 4 / KB;                    // pieces
-  // v pieces: a lane reads DV / 8 columns of a key row
-  constexpr int VB = (VROW / 8) < 16 ? VROW / 8 : 16;
-  constexpr int VP = VROW / 8 / VB;
-  constexpr int VE = VB / Z::ES;  // columns of a v piece
-  constexpr int KSTEPS = DQ / 16, VTILES = DV / 8;
-  constexpr float kLow = 2048.0f, kLowInv = 1.0f / 2048.0f;  // scale of the low parts in fp16
+  constexpr int KB = Z::KB, KP = Z::KP, VB = Z::VB, VP = Z::VP, VE = Z::VE;
+  constexpr int KSTEPS = DQ / 16, VTILES = DV / 16, S = Z::kStages;
+  constexpr int NG = kPair ? 1 : CG;         // column groups
+  constexpr int NC = kPair ? 1 : 2 * CG;     // candidates of a lane
+  constexpr int ROWS = kPair ? 4 : 8 * CG;   // candidates of a warp
   constexpr float kMaxFinite = 3.402823466e38f;
 
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int total = sp.ce - sp.c0;
+  const int wg = kPair || total <= ROWS ? 1 : (total <= 2 * ROWS ? 2 : 4);
+  const int nslices = kPagedWarps / wg, slice = warp / wg, gi = warp % wg;
+  const int cg = gi * ROWS;                                        // this warp's first candidate in the pass
+  const int ncand = max(0, min(ROWS, total - cg));
+  const int entries = p.func ? paged_list(p, sp, min(total, wg * ROWS)) : sp.tiles;
+  // Copy n of this warp is list entry (n nslices + slice) wg + gi.
+  const int iters = (entries + kPagedWarps - 1) / kPagedWarps;
+
+  const uint32_t ring = sp.ring + slice * S * wg * Z::kStep;  // the slice's stages
+  const auto issue = [&](int n, int stage) {
+    const int e = (n * nslices + slice) * wg + gi;
+    if (n < iters && e < entries) {
+      const int key0 = paged_key(p, sp, e);
+      const int page = sp.pages[(key0 >> p.cache.page_shift) - sp.page0];
+      const int64_t row0 = cache_row(p.cache, page, sp.h, key0 & ((1 << p.cache.page_shift) - 1));
+      const int nkeys = sp.k1 - key0;
+      const uint32_t dst = ring + (stage * wg + gi) * Z::kStep;
+      const char* ksrc = static_cast<const char*>(p.cache.k) + row0 * KROW + lane * 16;
+      const char* vsrc = static_cast<const char*>(p.cache.v) + row0 * VROW + lane * 16;
+      const auto copy = [&](auto whole) {
+#pragma unroll
+        for (int i = 0; i < KROW / 32; ++i) {
+          const int u = i * 32 + lane, r = u / KC, c = u % KC;
+          const int sw = KC >= 8 ? (r & 1) << 2 : 0;
+          copy16(dst + r * KROW + (c ^ sw) * 16, ksrc + i * 512, whole || r < nkeys);
+        }
+#pragma unroll
+        for (int i = 0; i < VROW / 32; ++i) {
+          const int u = i * 32 + lane, r = u / VC, c = u % VC;
+          const int sw = VC >= 8 ? r & 6 : (VC == 4 ? (r >> 1) & 3 : 0);
+          copy16(dst + kPagedTile * KROW + r * VROW + (c ^ sw) * 16, vsrc + i * 512, whole || r < nkeys);
+        }
+      };
+      if (nkeys >= kPagedTile) copy(std::true_type{});
+      else copy(std::false_type{});  // zeros behind the last key
+      if (E4M3 && lane < 2)
+        copy16(dst + kPagedTile * (KROW + VROW) + 16 * lane, (lane ? p.cache.v_scale : p.cache.k_scale) + row0, true);
+    }
+    copies_commit();
+  };
+  // A warp that reads alone refills a stage as soon as it has used it; the
+  // warps of a slice refill it after the barrier of the next step.
+#pragma unroll
+  for (int n = 0; n < S - 1; ++n) issue(n, n);
+  if (wg == 1) issue(S - 1, S - 1);
+
+  // Q fragments, column g of each group. 8-bit caches with bf16 rows: two fp16
+  // parts of the row scaled to a largest magnitude of 2^14 to 2^15, which is
+  // put right in qscale (of this lane's candidates in the scores).
+  uint32_t qa[NG][KSTEPS][2], ql[kSplitQ && !kPair ? NG : 1][kSplitQ && !kPair ? KSTEPS : 1][2];
+  float qscale[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) qscale[c] = p.alpha;
+#pragma unroll
+  for (int n = 0; n < NG; ++n) {
+    const int r = kPair ? g >> 1 : 8 * n + g;
+    const bool has = r < ncand && (!kPair || kSplitQ || (g & 1) == 0);
+    const T* qrow = static_cast<const T*>(p.q) + static_cast<int64_t>(sp.c0 + (has ? cg + r : 0)) * p.q_stride +
+                    static_cast<int64_t>(sp.h) * DQ;
+    constexpr int KE = KB / Z::ES;  // columns of a k piece
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < KP; ++i) {
+#pragma unroll
+      for (int j = 0; j < KE / 4; ++j) {
+        // columns of this lane in step st: two for k 0..7, two for 8..15
+        const int st = i * (KE / 4) + j;
+        const uint2 u =
+            has ? __ldg(reinterpret_cast<const uint2*>(qrow + i * 4 * KE + t * KE + 4 * j)) : make_uint2(0, 0);
+        qa[n][st][0] = u.x;
+        qa[n][st][1] = u.y;
+        if (kSplitQ)
+          top = max(max(top, max((u.x << 16) & 0x7fff0000u, u.x & 0x7fff0000u)),
+                    max((u.y << 16) & 0x7fff0000u, u.y & 0x7fff0000u));
+      }
+    }
+    if (kSplitQ) {
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int e = min(max(static_cast<int>(top >> 23), 27), 254);            // biased exponent
+      const float up = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);  // 2^(14 - (e - 127))
+      const float back = p.alpha * __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+#pragma unroll
+      for (int st = 0; st < KSTEPS; ++st)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float x = Elem<T>::lo(qa[n][st][i]) * up, y = Elem<T>::hi(qa[n][st][i]) * up;
+          const uint32_t high = pack_f16x2(x, y);
+          const uint32_t low = pack_f16x2(x - Elem<__half>::lo(high), y - Elem<__half>::hi(high));
+          qa[n][st][i] = kPair && (g & 1) ? low : high;
+          if (!kPair) ql[kPair ? 0 : n][kPair ? 0 : st][i] = low;
+        }
+      // The scores' columns 2t (and 2t + 1) were loaded by lanes of row 2t (and 2t + 1).
+      if (kPair) {
+        qscale[0] = __shfl_sync(0xffffffffu, back, 8 * t);
+      } else {
+        qscale[NC > 1 ? 2 * n : 0] = __shfl_sync(0xffffffffu, back, 8 * t);
+        qscale[NC > 1 ? 2 * n + 1 : 0] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
+      }
+    }
+  }
+
+  float acc[NG][VTILES][4];
+#pragma unroll
+  for (int n = 0; n < NG; ++n)
+#pragma unroll
+    for (int j = 0; j < VTILES; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[n][j][e] = 0.0f;
+  int erun[NC];  // biased exponents that the candidates' P are scaled to (fp16 products)
+#pragma unroll
+  for (int c = 0; c < NC; ++c) erun[c] = 30;
+
+  const int krow_sw = KC >= 8 ? (g & 1) << 2 : 0;  // rows g and g + 8 alike
+  int stage = 0;
+  for (int n0 = 0; n0 < iters; ++n0) {
+    if (wg > 1) {
+      copies_wait<S - 2>();
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + slice), "r"(32 * wg) : "memory");
+      issue(n0 + S - 1, stage == 0 ? S - 1 : stage - 1);  // into the stage that the slice used last
+    } else {
+      copies_wait<S - 1>();
+      __syncwarp();
+    }
+    for (int j = 0; j < wg; ++j) {
+      const int entry = (n0 * nslices + slice) * wg + j;
+      if (entry >= entries || ncand == 0) break;
+      const uint32_t kt = ring + (stage * wg + j) * Z::kStep;
+      const uint32_t vt = kt + kPagedTile * KROW;
+
+      // Scores of keys g (values 0, 1 of a group) and g + 8 (2, 3), two sums
+      // each, halves of a dependent chain.
+      float s[2][NG][4];
+#pragma unroll
+      for (int n = 0; n < NG; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[0][n][e] = s[1][n][e] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < KP; ++i) {
+        uint32_t kw[2][KB / 4];
+        const int byte = i * 4 * KB + t * KB;
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          load_piece<KB>(kt + (g + 8 * r) * KROW + ((byte >> 4) ^ krow_sw) * 16 + (byte & 15), kw[r]);
+        constexpr int kPer = E4M3 ? KB / 4 : KB / 8;  // k = 16 steps of a piece
+#pragma unroll
+        for (int w = 0; w < kPer; ++w) {
+          const int st = i * kPer + w;
+          uint32_t a[4];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            a[r] = E4M3 ? e4m3x2_to_f16x2(kw[r][E4M3 ? w : 0]) : kw[r][E4M3 ? 0 : 2 * w];
+            a[2 + r] = E4M3 ? e4m3x2_hi_to_f16x2(kw[r][E4M3 ? w : 0]) : kw[r][E4M3 ? 0 : 2 * w + 1];
+          }
+#pragma unroll
+          for (int n = 0; n < NG; ++n) {
+            if (kSplitQ && !kPair) {
+              mma16816<M>(s[0][n], a[0], a[1], a[2], a[3], qa[n][st][0], qa[n][st][1]);
+              mma16816<M>(s[1][n], a[0], a[1], a[2], a[3], ql[kPair ? 0 : n][kSplitQ && !kPair ? st : 0][0],
+                          ql[kPair ? 0 : n][kSplitQ && !kPair ? st : 0][1]);
+            } else {
+              mma16816<M>(s[st & 1][n], a[0], a[1], a[2], a[3], qa[n][st][0], qa[n][st][1]);
+            }
+          }
+        }
+      }
+
+      // P of this lane's candidates at keys g and g + 8.
+      const int key0 = paged_key(p, sp, entry);
+      const bool part = p.func ? (sp.list[entry] & 0x8000) != 0 : key0 + kPagedTile > sp.k1;
+      float ks[2], vs[2];
+      if (E4M3) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          uint32_t u, v;
+          asm volatile("ld.shared.u8 %0, [%1];" : "=r"(u) : "r"(vt + kPagedTile * VROW + g + 8 * r));
+          asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(vt + kPagedTile * VROW + 16 + g + 8 * r));
+          ks[r] = scale_value(u);
+          vs[r] = scale_value(v);
+        }
+      }
+      float pr[NC][2];
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float x;
+          if (kPair) {
+            x = s[0][0][2 * r] + s[1][0][2 * r];
+            if (kSplitQ) x += s[0][0][2 * r + 1] + s[1][0][2 * r + 1];
+          } else {
+            x = s[0][kPair ? 0 : c / 2][2 * r + (c & 1)] + s[1][kPair ? 0 : c / 2][2 * r + (c & 1)];
+          }
+          x *= qscale[c];
+          if (E4M3) x *= ks[r];
+          x = silu_exact(x);
+          if (E4M3) x *= vs[r];
+          pr[c][r] = x;
+        }
+      if (part) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int cand = cg + (kPair ? t : c / 2 * 8 + 2 * t + (c & 1));
+            if (!(cand < cg + ncand && paged_sees(p, sp, cand, key0 + g + 8 * r))) pr[c][r] = 0.0f;
+          }
+        __syncwarp();
+      }
+      if (kHalf) {
+        // A candidate's scale follows the largest magnitude it has met.
+        bool grow = false;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+          grow |= static_cast<int>(__float_as_uint(fmaxf(fabsf(pr[c][0]), fabsf(pr[c][1]))) >> 23) > erun[c];
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            float top = fmaxf(fabsf(pr[c][0]), fabsf(pr[c][1]));
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            const int more = max(static_cast<int>(__float_as_uint(top) >> 23) - erun[c], 0);
+            const float down = more < 127 ? __uint_as_float(static_cast<uint32_t>(127 - more) << 23) : 0.0f;
+            erun[c] += more;
+#pragma unroll
+            for (int m = 0; m < VTILES; ++m)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (kPair || (e & 1) == (c & 1)) acc[kPair ? 0 : c / 2][m][e] *= down;
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const float up = __uint_as_float(static_cast<uint32_t>(268 - erun[c]) << 23);  // below 2^15 at the largest
+          pr[c][0] *= up;
+          pr[c][1] *= up;
+        }
+      }
+      // P^T operands: high and low parts in one (pair), or one each.
+      uint32_t bh[NG][2], bl[NG][2];
+      if (kPair) {
+        const uint32_t h = Elem<M>::pack2(pr[0][0], pr[0][1]);
+        bh[0][0] = transpose8(Elem<M>::pack2(pr[0][0], pr[0][0] - Elem<M>::lo(h)));
+        bh[0][1] = transpose8(Elem<M>::pack2(pr[0][1], pr[0][1] - Elem<M>::hi(h)));
+      } else {
+#pragma unroll
+        for (int n = 0; n < NG; ++n)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float x = pr[kPair ? 0 : 2 * n][r], y = pr[kPair ? 0 : 2 * n + 1][r];
+            const uint32_t h = Elem<M>::pack2(x, y);
+            bh[n][r] = transpose8(h);
+            bl[n][r] = transpose8(Elem<M>::pack2(x - Elem<M>::lo(h), y - Elem<M>::hi(h)));
+          }
+      }
+
+      // O^T += V^T P^T: rows g and g + 8 of a product are columns e and e + 1
+      // of the lanes' pieces.
+      const auto add = [&](int m, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+          mma16816<M>(acc[n][m], a0, a1, a2, a3, bh[n][0], bh[n][1]);
+          if (!kPair) mma16816<M>(acc[n][m], a0, a1, a2, a3, bl[n][0], bl[n][1]);
+        }
+      };
+#pragma unroll
+      for (int i = 0; i < VP; ++i) {
+        uint32_t vw[4][VB / 4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = 2 * t + (r & 1) + 8 * (r >> 1);
+          const int sw = VC >= 8 ? row & 6 : (VC == 4 ? (row >> 1) & 3 : 0);
+          const int byte = i * 8 * VB + g * VB;
+          load_piece<VB>(vt + row * VROW + ((byte >> 4) ^ sw) * 16 + (byte & 15), vw[r]);
+        }
+#pragma unroll
+        for (int w = 0; w < VB / 4; ++w) {
+          if (E4M3) {
+            // bytes (row 0, row 1) of columns 4w, 4w+1 and 4w+2, 4w+3
+            const uint32_t x0 = __byte_perm(vw[0][w], vw[1][w], 0x5140);
+            const uint32_t x1 = __byte_perm(vw[0][w], vw[1][w], 0x7362);
+            const uint32_t y0 = __byte_perm(vw[2][w], vw[3][w], 0x5140);
+            const uint32_t y1 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
+            const int m = i * VE / 2 + 2 * w;
+            add(m, e4m3x2_to_f16x2(x0), e4m3x2_hi_to_f16x2(x0), e4m3x2_to_f16x2(y0), e4m3x2_hi_to_f16x2(y0));
+            add(E4M3 ? m + 1 : m, e4m3x2_to_f16x2(x1), e4m3x2_hi_to_f16x2(x1), e4m3x2_to_f16x2(y1),
+                e4m3x2_hi_to_f16x2(y1));
+          } else {
+            add(i * VE / 2 + w, __byte_perm(vw[0][w], vw[1][w], 0x5410), __byte_perm(vw[0][w], vw[1][w], 0x7632),
+                __byte_perm(vw[2][w], vw[3][w], 0x5410), __byte_perm(vw[2][w], vw[3][w], 0x7632));
+          }
+        }
+      }
+    }
+    if (wg == 1) {
+      __syncwarp();
+      issue(n0 + S, stage);  // into the stage just used
+    }
+    stage = stage + 1 == S ? 0 : stage + 1;
+  }
+
+  // This warp's sums.
+  copies_wait<0>();
+  __syncthreads();  // the ring is free: the sums take its place
+  float* mine = sp.red + warp * ROWS * Z::kRedRow;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int r = kPair ? t : c / 2 * 8 + 2 * t + (c & 1);
+    const float back = kHalf ? __uint_as_float(static_cast<uint32_t>(erun[c] - 14) << 23) : 1.0f;
+    bool finite = true;
+    if (r < ncand) {
+      float* row = mine + r * Z::kRedRow + g * Z::kBlock;
+#pragma unroll
+      for (int i = 0; i < VP; ++i)
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          const float(&a)[4] = acc[kPair ? 0 : c / 2][i * VE / 2 + e / 2];
+          const float u = (kPair ? a[2 * (e & 1)] + a[2 * (e & 1) + 1] : a[2 * (e & 1) + (c & 1)]) * back;
+          finite = finite && fabsf(u) <= kMaxFinite;
+          row[i * 8 * Z::kBlock + e] = u;
+        }
+    }
+    // A sum that is not finite may have met a value that its candidate does
+    // not see (zero times infinity): those candidates are summed again, key by
+    // key, over what they see alone.
+    const uint32_t odd = __ballot_sync(0xffffffffu, !finite);
+    for (int l = 0; odd != 0 && l < 4; ++l) {
+      if ((odd & (0x11111111u << l)) == 0) continue;
+      const int again = kPair ? l : c / 2 * 8 + 2 * l + (c & 1);
+      paged_scalar_sum<T, DQ, DV, E4M3, Z>(p, sp, cg + again, slice * wg, wg, entries, mine + again * Z::kRedRow);
+    }
+  }
+  return wg;
+}
+
+// T: type of q, o and 16-bit pages. E4M3: 8-bit pages. MANY: any number of
+// candidates, else one a sequence.
+template <typename T, int DQ, int DV, bool E4M3, bool MANY>
+__global__ void __launch_bounds__(kPagedThreads, PagedSizes<DQ, DV, E4M3, MANY>::kResident)
+    paged_kernel(const PagedParams p) {
+  using Z = PagedSizes<DQ, DV, E4M3, MANY>;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ int pages[kPagedMaxSplit / kPagedTile];
-  __shared__ uint32_t tile_bits[kPagedMaxSplit / kPagedTile / 32];
-  __shared__ uint8_t list[kPagedMaxSplit / kPagedTile];
-  __shared__ int sh_flag, sh_entries;
+  __shared__ uint32_t bits[2 * kPagedWords];
+  __shared__ uint16_t list[kPagedMaxSplit / kPagedTile];
+  __shared__ int iv[(MANY ? kPagedPass : 1) * kPagedIv];
+  __shared__ int sh_entries, sh_seen;
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t bid = blockIdx.x;
   const int split = static_cast<int>(bid % p.nsplit);
   const int bh = static_cast<int>(bid / p.nsplit);
   const int h = bh % p.cache.heads, b = bh / p.cache.heads;
-  const int page_size = 1 << p.cache.page_shift;
+  const int k0 = split * p.split;
+
+  // Pages of this split, read before the length is known (entries past the
+  // length are not looked at).
+  const int page0 = k0 >> p.cache.page_shift;
+  const int most_pages = min((p.split + (1 << p.cache.page_shift) - 1) >> p.cache.page_shift, p.max_pages - page0);
+  constexpr int kPageLoads = kPagedMaxSplit / kPagedTile / kPagedThreads;
+  int page[kPageLoads];
+#pragma unroll
+  for (int i = 0; i < kPageLoads; ++i) {
+    const int at = i * kPagedThreads + tid;
+    page[i] = at < most_pages ? __ldg(p.page_table + static_cast<int64_t>(b) * p.max_pages + page0 + at) : -1;
+  }
 
   // Checks of this sequence (every CTA of it comes to the same answer).
   int cb = b, ce = b + 1;
   bool ok = true;
-  if (p.cand_offsets) {
+  if (MANY) {
     cb = p.cand_offsets[b];
     ce = p.cand_offsets[b + 1];
     ok = cb >= 0 && cb <= ce && ce <= p.num_cand && p.cand_offsets[0] == 0 &&
@@ -232,346 +695,57 @@ __global__ void __launch_bounds__(kPagedThreads, PagedSizes<DQ, DV, E4M3>::kResi
   if (cb == ce) return;
   const int splits = max(1, (len + p.split - 1) / p.split);
   if (split >= splits) return;
-  const int k0 = split * p.split, k1 = min(len, k0 + p.split);
-
-  // Pages of this split.
-  const int page0 = k0 >> p.cache.page_shift;
+  const int k1 = min(len, k0 + p.split);
   const int npages = k1 > k0 ? ((k1 - 1) >> p.cache.page_shift) - page0 + 1 : 0;
-  if (tid == 0) sh_flag = 0;
-  __syncthreads();
   bool bad_page = false;
-  for (int i = tid; i < npages; i += kPagedThreads) {
-    const int pg = p.page_table[static_cast<int64_t>(b) * p.max_pages + page0 + i];
-    pages[i] = pg;
-    bad_page |= pg < 0 || pg >= p.cache.num_pages;
+#pragma unroll
+  for (int i = 0; i < kPageLoads; ++i) {
+    const int at = i * kPagedThreads + tid;
+    if (at < npages) {
+      pages[at] = page[i];
+      bad_page |= page[i] < 0 || page[i] >= p.cache.num_pages;
+    }
   }
-  if (bad_page) sh_flag = 1;
-  __syncthreads();
-  const bool bad = sh_flag != 0;
-  const int ntiles = bad ? 0 : (k1 - k0 + kPagedTile - 1) / kPagedTile;
+  const bool bad = __syncthreads_or(bad_page) != 0;
   if (bad && tid == 0) atomicOr(p.header + kHdrErr, kErrInput);
 
-  const char* kbase = static_cast<const char*>(p.cache.k);
-  const char* vbase = static_cast<const char*>(p.cache.v);
-  const uint32_t ring_addr = smem_u32(ring);
   float* red = reinterpret_cast<float*>(ring);
-
+  PagedSplit sp;
+  sp.h = h;
+  sp.k0 = k0;
+  sp.k1 = k1;
+  sp.len = len;
+  sp.page0 = page0;
+  sp.tiles = bad ? 0 : (k1 - k0 + kPagedTile - 1) / kPagedTile;
+  sp.ce = ce;
+  sp.pages = pages;
+  sp.bits = bits;
+  sp.list = list;
+  sp.iv = iv;
+  sp.entries = &sh_entries;
+  sp.ring = smem_u32(ring);
+  sp.red = red;
   for (int c0 = cb; c0 < ce;) {
-    // Slices of `wg` warps; warp `gi` of its slice has candidates cg .. cg + 7.
-    const int groups = (ce - c0 + kPagedGroup - 1) / kPagedGroup;
-    const int wg = groups == 1 ? 1 : (groups == 2 ? 2 : 4);
-    const int nslices = kPagedWarps / wg, slice = warp / wg, gi = warp % wg;
-    const int cg = c0 + gi * kPagedGroup;
-    const int ncand = max(0, min(kPagedGroup, ce - cg));
-    const bool has = g < ncand;
-    // Intervals of candidate g.
-    int lo[NI], hi[NI];
-    int entries = ntiles;
-    if (p.func) {
-      load_row_intervals<NI>(p.func, p.num_cand, cg + g, len, has, lo, hi, (1u << ((p.nfunc + 1) / 2)) - 1u);
-      // The tiles that some candidate of this pass sees.
-      if (tid < kPagedMaxSplit / kPagedTile / 32) tile_bits[tid] = 0;
-      __syncthreads();
-      if (slice == 0 && t == 0) {
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          const int a = max(lo[i], k0) - k0, e = min(hi[i], k1) - k0;
-          if (e <= a) continue;
-          const int first = a / kPagedTile, last = (e - 1) / kPagedTile;
-          for (int w = first >> 5; w <= last >> 5; ++w) {
-            uint32_t bits = 0xffffffffu;
-            if (w == first >> 5) bits &= 0xffffffffu << (first & 31);
-            if (w == last >> 5) bits &= 0xffffffffu >> (31 - (last & 31));
-            atomicOr(&tile_bits[w], bits);
-          }
-        }
-      }
-      __syncthreads();
-      if (warp == 0) {
-        const uint32_t mine = (tile_bits[lane >> 2] >> (8 * (lane & 3))) & 0xffu;  // tiles 8 lane .. 8 lane + 7
-        int at = __popc(mine);
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const int o = __shfl_up_sync(0xffffffffu, at, off);
-          if (lane >= off) at += o;
-        }
-        if (lane == 31) sh_entries = bad ? 0 : at;
-        at -= __popc(mine);
-        for (int i = 0; i < 8; ++i)
-          if ((mine >> i) & 1u) list[at++] = static_cast<uint8_t>(8 * lane + i);
-      }
-      __syncthreads();
-      entries = sh_entries;
+    sp.c0 = c0;
+    int wg, rows;
+    if (!MANY || ce - c0 <= 4) {
+      wg = paged_pass<T, DQ, DV, E4M3, MANY, 0>(p, sp);
+      rows = 4;
+    } else if (MANY && ce - c0 <= 8) {
+      wg = paged_pass<T, DQ, DV, E4M3, MANY, MANY ? 1 : 0>(p, sp);
+      rows = 8;
     } else {
-#pragma unroll
-      for (int i = 0; i < NI; ++i) lo[i] = hi[i] = 0;
-      if (has) hi[0] = len;
-    }
-    const int iters = (entries + kPagedWarps - 1) / kPagedWarps;
-
-    // Copies this warp's tile of iteration `it` of its slice.
-    const auto issue = [&](int it) {
-      const int e = (it * nslices + slice) * wg + gi;
-      if (it < iters && e < entries) {
-        const int key0 = k0 + (p.func ? list[e] : e) * kPagedTile;
-        const int page = pages[(key0 >> p.cache.page_shift) - page0];
-        const int64_t row0 = cache_row(p.cache, page, h, key0 & (page_size - 1));
-        const int nkeys = k1 - key0;
-        const uint32_t dst = ring_addr + ((slice * Z::kStages + it % Z::kStages) * wg + gi) * Z::kStep;
-        const char* ksrc = kbase + row0 * KROW;
-        const char* vsrc = vbase + row0 * VROW;
-#pragma unroll
-        for (int i = 0; i < KROW / 32; ++i) {
-          const int u = i * 32 + lane, r = u / KC, c = u % KC;
-          const int sw = KC >= 8 ? (r & 1) << 2 : 0;
-          copy16(dst + r * KROW + (c ^ sw) * 16, ksrc + u * 16, r < nkeys);
-        }
-#pragma unroll
-        for (int i = 0; i < VROW / 32; ++i) {
-          const int u = i * 32 + lane, r = u / VC, c = u % VC;
-          const int sw = VC >= 8 ? r & 6 : (VC == 4 ? (r >> 1) & 3 : 0);
-          copy16(dst + kPagedTile * KROW + r * VROW + (c ^ sw) * 16, vsrc + u * 16, r < nkeys);
-        }
-        if (E4M3 && lane < 2)
-          copy16(dst + kPagedTile * (KROW + VROW) + 16 * lane, (lane ? p.cache.v_scale : p.cache.k_scale) + row0, true);
-      }
-      copies_commit();
-    };
-#pragma unroll
-    for (int i = 0; i < Z::kStages - 1; ++i) issue(i);
-
-    // Q fragments: rows 0..7 the candidates, rows 8..15 zero or low parts.
-    uint32_t qa[KSTEPS][2], ql[kSplitQ ? KSTEPS : 1][2];
-    float qscale = p.alpha;
-    {
-      const T* qrow = static_cast<const T*>(p.q) + static_cast<int64_t>(has ? cg + g : c0) * p.q_stride + h * DQ;
-      constexpr int KE = KB / Z::ES;  // columns of a k piece: 16, 8
-      float f[KSTEPS][4];
-#pragma unroll
-      for (int i = 0; i < KP; ++i) {
-#pragma unroll
-        for (int j = 0; j < KE / 4; ++j) {
-          // columns of this lane in step (i * KE + 4 j) / 4: two for k 0..7, two for 8..15
-          const int col = i * 4 * KE + t * KE + 4 * j;
-          const uint2 u = has ? __ldg(reinterpret_cast<const uint2*>(qrow + col)) : make_uint2(0, 0);
-          const int s = i * (KE / 4) + j;
-          qa[s][0] = u.x;
-          qa[s][1] = u.y;
-          if (kSplitQ) {
-            f[s][0] = Elem<T>::lo(u.x);
-            f[s][1] = Elem<T>::hi(u.x);
-            f[s][2] = Elem<T>::lo(u.y);
-            f[s][3] = Elem<T>::hi(u.y);
-          }
-        }
-      }
-      if (kSplitQ) {
-        uint32_t top = 0;  // largest magnitude of the row
-#pragma unroll
-        for (int s = 0; s < KSTEPS; ++s)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(f[s][e]) & 0x7fffffffu);
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int e = min(max(static_cast<int>(top >> 23), 27), 254);  // biased exponent
-        const float up = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);  // 2^(14 - (e - 127))
-        qscale = p.alpha * __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
-#pragma unroll
-        for (int s = 0; s < KSTEPS; ++s)
-#pragma unroll
-          for (int e2 = 0; e2 < 2; ++e2) {
-            const float x = f[s][2 * e2] * up, y = f[s][2 * e2 + 1] * up;
-            const uint32_t w = pack_f16x2(x, y);
-            qa[s][e2] = w;
-            ql[s][e2] = pack_f16x2((x - Elem<__half>::lo(w)) * kLow, (y - Elem<__half>::hi(w)) * kLow);
-          }
-      }
-    }
-
-    float acc[VTILES][4];
-#pragma unroll
-    for (int j = 0; j < VTILES; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
-    int erun = 30;  // biased exponent that this candidate's P is scaled to (fp16 products)
-
-    for (int it = 0; it < iters; ++it) {
-      copies_wait<Z::kStages - 2>();  // this warp's copies of iteration `it` have landed
-      if (wg == 1) __syncwarp();
-      else asm volatile("bar.sync %0, %1;" ::"r"(1 + slice), "r"(32 * wg) : "memory");
-      issue(it + Z::kStages - 1);  // into the stage that the slice used last
-      if (ncand == 0) continue;
-      for (int j = 0; j < wg; ++j) {
-        const int entry = (it * nslices + slice) * wg + j;
-        if (entry >= entries) break;
-        const int key0 = k0 + (p.func ? list[entry] : entry) * kPagedTile;
-        const uint32_t kt = ring_addr + ((slice * Z::kStages + it % Z::kStages) * wg + j) * Z::kStep;
-        const uint32_t vt = kt + kPagedTile * KROW;
-
-        // S: key tile r holds keys 8r .. 8r + 7; this lane's columns are keys
-        // 8r + 2t and 8r + 2t + 1 of candidate g.
-        float s[2][4];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          s[r][0] = s[r][1] = s[r][2] = s[r][3] = 0.0f;
-          const int row = g + 8 * r;
-          const int sw = KC >= 8 ? (row & 1) << 2 : 0;
-#pragma unroll
-          for (int i = 0; i < KP; ++i) {
-            uint32_t kw[KB / 4];
-            const int byte = i * 4 * KB + t * KB;
-            load_piece<KB>(kt + row * KROW + ((byte >> 4) ^ sw) * 16 + (byte & 15), kw);
-            if (E4M3) {
-#pragma unroll
-              for (int w = 0; w < KB / 4; ++w) {
-                const int st = i * (KB / 4) + w;
-                mma16816<M>(s[r], qa[st][0], kSplitQ ? ql[kSplitQ ? st : 0][0] : 0u, qa[st][1],
-                            kSplitQ ? ql[kSplitQ ? st : 0][1] : 0u, e4m3x2_to_f16x2(kw[w]),
-                            e4m3x2_to_f16x2(kw[w] >> 16));
-              }
-            } else {
-#pragma unroll
-              for (int w = 0; w < KB / 8; ++w) {
-                const int st = i * (KB / 8) + w;
-                mma16816<M>(s[r], qa[st][0], 0u, qa[st][1], 0u, kw[2 * w], kw[2 * w + 1]);
-              }
-            }
-          }
-        }
-
-        // P of candidate g at keys 2t, 2t+1, 2t+8, 2t+9.
-        float pr[4];
-        uint32_t scales[4];  // k and v scale bytes of keys 2t, 2t+1 and 2t+8, 2t+9
-        if (E4M3) {
-          const uint32_t sc = vt + kPagedTile * VROW + 2 * t;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            uint16_t u;
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(u) : "r"(sc + 8 * r));
-            scales[r] = u;
-          }
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int key = key0 + 2 * t + (r & 1) + 8 * (r >> 1);
-          float x = s[r >> 1][r & 1];
-          if (kSplitQ) x = fmaf(s[r >> 1][2 + (r & 1)], kLowInv, x);
-          x *= qscale;
-          if (E4M3) x *= scale_value((scales[r >> 1] >> (8 * (r & 1))) & 0xffu);
-          float v = silu_exact(x);
-          if (E4M3) v *= scale_value((scales[2 + (r >> 1)] >> (8 * (r & 1))) & 0xffu);
-          bool vis = false;
-#pragma unroll
-          for (int i = 0; i < NI; ++i) vis |= lo[i] <= key && key < hi[i];
-          pr[r] = vis ? v : 0.0f;
-        }
-        uint32_t pa[2], pl[2];
-        if (kHalf) {
-          // Largest magnitude of the candidate in this tile: its four lanes.
-          float top = fmaxf(fmaxf(fabsf(pr[0]), fabsf(pr[1])), fmaxf(fabsf(pr[2]), fabsf(pr[3])));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          const int e = static_cast<int>(__float_as_uint(top) >> 23);
-          if (e > erun) {
-            const float down = e - erun < 127 ? __uint_as_float(static_cast<uint32_t>(127 - (e - erun)) << 23) : 0.0f;
-#pragma unroll
-            for (int n = 0; n < VTILES; ++n)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) acc[n][i] *= down;
-            erun = e;
-          }
-          __syncwarp();
-          const float up = __uint_as_float(static_cast<uint32_t>(268 - erun) << 23);  // 2^14 at the largest
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const float x = pr[2 * r] * up, y = pr[2 * r + 1] * up;
-            pa[r] = pack_f16x2(x, y);
-            pl[r] = pack_f16x2((x - Elem<__half>::lo(pa[r])) * kLow, (y - Elem<__half>::hi(pa[r])) * kLow);
-          }
-        } else {
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const float x = pr[2 * r], y = pr[2 * r + 1];
-            pa[r] = pack_bf16x2(x, y);
-            pl[r] = pack_bf16x2(x - Elem<__nv_bfloat16>::lo(pa[r]), y - Elem<__nv_bfloat16>::hi(pa[r]));
-          }
-        }
-
-        // O += P V: column tile (i, e) holds column e of the lanes' pieces i.
-        // V rows 2t, 2t+1, 2t+8, 2t+9.
-#pragma unroll
-        for (int i = 0; i < VP; ++i) {
-          uint32_t vw[4][VB / 4];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int row = 2 * t + (r & 1) + 8 * (r >> 1);
-            const int sw = VC >= 8 ? row & 6 : (VC == 4 ? (row >> 1) & 3 : 0);
-            const int byte = i * 8 * VB + g * VB;
-            load_piece<VB>(vt + row * VROW + ((byte >> 4) ^ sw) * 16 + (byte & 15), vw[r]);
-          }
-          if (E4M3) {
-#pragma unroll
-            for (int w = 0; w < VB / 4; ++w) {
-              // bytes (row 0, row 1) of columns 4w, 4w+1 and 4w+2, 4w+3
-              const uint32_t x0 = __byte_perm(vw[0][w], vw[1][w], 0x5140);
-              const uint32_t x1 = __byte_perm(vw[0][w], vw[1][w], 0x7362);
-              const uint32_t y0 = __byte_perm(vw[2][w], vw[3][w], 0x5140);
-              const uint32_t y1 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
-              float(*o)[4] = acc + i * VE + 4 * w;
-              mma16816<M>(o[0], pa[0], pl[0], pa[1], pl[1], e4m3x2_to_f16x2(x0), e4m3x2_to_f16x2(y0));
-              mma16816<M>(o[1], pa[0], pl[0], pa[1], pl[1], e4m3x2_to_f16x2(x0 >> 16), e4m3x2_to_f16x2(y0 >> 16));
-              mma16816<M>(o[2], pa[0], pl[0], pa[1], pl[1], e4m3x2_to_f16x2(x1), e4m3x2_to_f16x2(y1));
-              mma16816<M>(o[3], pa[0], pl[0], pa[1], pl[1], e4m3x2_to_f16x2(x1 >> 16), e4m3x2_to_f16x2(y1 >> 16));
-            }
-          } else {
-#pragma unroll
-            for (int w = 0; w < VB / 4; ++w) {
-              float(*o)[4] = acc + i * VE + 2 * w;
-              mma16816<M>(o[0], pa[0], pl[0], pa[1], pl[1], __byte_perm(vw[0][w], vw[1][w], 0x5410),
-                          __byte_perm(vw[2][w], vw[3][w], 0x5410));
-              mma16816<M>(o[1], pa[0], pl[0], pa[1], pl[1], __byte_perm(vw[0][w], vw[1][w], 0x7632),
-                          __byte_perm(vw[2][w], vw[3][w], 0x7632));
-            }
-          }
-        }
-      }
-    }
-
-    // This warp's sums: candidate g, columns (2t, 2t+1) of each column tile,
-    // i.e. columns [2t VE, 2t VE + 2 VE) of piece group i.
-    __syncthreads();  // the ring is free: the sums take its place
-    float* mine = red + warp * kPagedGroup * DV;
-    const float back = kHalf ? __uint_as_float(static_cast<uint32_t>(erun - 14) << 23) : 1.0f;
-    bool finite = true;
-#pragma unroll
-    for (int i = 0; i < VP; ++i)
-#pragma unroll
-      for (int e = 0; e < VE; ++e) {
-        const float(&a)[4] = acc[i * VE + e];
-        const float x = (kHalf ? fmaf(a[2], kLowInv, a[0]) : a[0] + a[2]) * back;
-        const float y = (kHalf ? fmaf(a[3], kLowInv, a[1]) : a[1] + a[3]) * back;
-        finite = finite && fabsf(x) <= kMaxFinite && fabsf(y) <= kMaxFinite;
-        mine[g * DV + i * 8 * VE + 2 * t * VE + e] = x;
-        mine[g * DV + i * 8 * VE + (2 * t + 1) * VE + e] = y;
-      }
-    // A sum that is not finite may have met a value that its candidate does
-    // not see (zero times infinity): those candidates are summed again, key by
-    // key, over what they see alone.
-    const uint32_t odd = __ballot_sync(0xffffffffu, has && !finite);
-    if (odd != 0) {
-      for (int r = 0; r < ncand; ++r)
-        if (((odd >> (4 * r)) & 15u) != 0)
-          paged_scalar_sum<T, DQ, DV, E4M3, NI>(p, cg + r, h, lane, slice * wg, wg, kPagedWarps, entries, list, k0, k1,
-                                                len, pages, mine + r * DV);
+      wg = paged_pass<T, DQ, DV, E4M3, MANY, MANY ? 2 : 0>(p, sp);
+      rows = 16;
     }
     __syncthreads();
     // The slices' sums in slice order.
-    const int taken = min(ce - c0, wg * kPagedGroup);
+    const int taken = min(ce - c0, wg * rows);
     for (int i = tid; i < taken * DV; i += kPagedThreads) {
       const int r = i / DV, d = i % DV;
-      const float* from = red + r * DV + d;  // group r / 8 is warp r / 8 of each slice
+      const float* from = red + r * Z::kRedRow + Z::red_column(d);  // warp r / rows of each slice
       float sum = from[0];
-      for (int w = 1; w < nslices; ++w) sum += from[w * wg * kPagedGroup * DV];
+      for (int w = wg; w < kPagedWarps; w += wg) sum += from[w * rows * Z::kRedRow];
       const int64_t at = static_cast<int64_t>(c0 + r) * p.cache.heads + h;
       if (splits > 1) {
         p.partial[(at * p.nsplit + split) * DV + d] = sum;
@@ -586,59 +760,77 @@ __global__ void __launch_bounds__(kPagedThreads, PagedSizes<DQ, DV, E4M3>::kResi
   if (splits == 1) return;
 
   // The last CTA of this (sequence, head) to arrive joins the splits' sums in
-  // a fixed order: a quarter of the splits for each warp, then the quarters.
-  // A split with a bad page marks the counter, and nothing is written then.
+  // a fixed order. A split with a bad page marks the counter, and nothing is
+  // written then.
   __threadfence();
   __syncthreads();
-  if (tid == 0) sh_flag = atomicAdd(p.counters + bh, bad ? 1 + (1 << 20) : 1) + (bad ? 1 << 20 : 0);
+  if (tid == 0) sh_seen = atomicAdd(p.counters + bh, bad ? 1 + (1 << 20) : 1) + (bad ? 1 << 20 : 0);
   __syncthreads();
-  const int seen = sh_flag;
+  const int seen = sh_seen;
   if ((seen & 0xfffff) != splits - 1 || seen >> 20 != 0) return;
   __threadfence();
-  const int quarter = (splits + kPagedWarps - 1) / kPagedWarps;
-  for (int c0 = cb; c0 < ce; c0 += kPagedGroup) {
-    const int n = min(kPagedGroup, ce - c0);
-    for (int item = warp; item < n * kPagedWarps; item += kPagedWarps) {
-      const int r = item / kPagedWarps, qt = item % kPagedWarps;
-      const float* from = p.partial + (static_cast<int64_t>(c0 + r) * p.cache.heads + h) * p.nsplit * DV;
+  const auto at_of = [&](int c) { return (static_cast<int64_t>(c) * p.cache.heads + h); };
+  if (ce - cb < kPagedWarps) {
+    // Few candidates, many splits: a quarter of the splits for each warp, then
+    // the quarters.
+    const int quarter = (splits + kPagedWarps - 1) / kPagedWarps;
+    for (int c = cb; c < ce; ++c) {
+      const float* from = p.partial + at_of(c) * p.nsplit * DV;
       float sum[DV / 32];
 #pragma unroll
       for (int i = 0; i < DV / 32; ++i) sum[i] = 0.0f;
-#pragma unroll 4
-      for (int s = qt * quarter; s < min(splits, (qt + 1) * quarter); ++s)
+#pragma unroll 8
+      for (int s = warp * quarter; s < min(splits, (warp + 1) * quarter); ++s)
 #pragma unroll
         for (int i = 0; i < DV / 32; ++i) sum[i] += __ldcg(from + s * DV + 32 * i + lane);
 #pragma unroll
-      for (int i = 0; i < DV / 32; ++i) red[(qt * kPagedGroup + r) * DV + 32 * i + lane] = sum[i];
-    }
-    __syncthreads();
-    for (int i = tid; i < n * DV; i += kPagedThreads) {
-      float sum = red[i];
+      for (int i = 0; i < DV / 32; ++i) red[warp * DV + 32 * i + lane] = sum[i];
+      __syncthreads();
+      for (int d = tid; d < DV; d += kPagedThreads) {
+        float all = red[d];
 #pragma unroll
-      for (int qt = 1; qt < kPagedWarps; ++qt) sum += red[qt * kPagedGroup * DV + i];
-      const int64_t at = static_cast<int64_t>(c0 + i / DV) * p.cache.heads + h;
-      const uint32_t w = Elem<T>::pack2(sum * p.inv_n, 0.0f);
-      static_cast<T*>(p.o)[at * DV + i % DV] = *reinterpret_cast<const T*>(&w);
+        for (int w = 1; w < kPagedWarps; ++w) all += red[w * DV + d];
+        const uint32_t w = Elem<T>::pack2(all * p.inv_n, 0.0f);
+        static_cast<T*>(p.o)[at_of(c) * DV + d] = *reinterpret_cast<const T*>(&w);
+      }
+      __syncthreads();
     }
-    __syncthreads();
+    return;
+  }
+  // Many candidates: four columns of one for each thread.
+#pragma unroll 4
+  for (int i = tid; i < (ce - cb) * (DV / 4); i += kPagedThreads) {
+    const int64_t at = at_of(cb + i / (DV / 4));
+    const int d = i % (DV / 4) * 4;
+    const float* from = p.partial + at * p.nsplit * DV + d;
+    float4 sum = __ldcg(reinterpret_cast<const float4*>(from));
+    for (int s = 1; s < splits; ++s) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(from + s * DV));
+      sum.x += v.x;
+      sum.y += v.y;
+      sum.z += v.z;
+      sum.w += v.w;
+    }
+    *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + at * DV + d) =
+        make_uint2(Elem<T>::pack2(sum.x * p.inv_n, sum.y * p.inv_n), Elem<T>::pack2(sum.z * p.inv_n, sum.w * p.inv_n));
   }
 }
 
 // Launches the kernel for the widths of p.cache (one function for each type,
 // in a translation unit of its own so that they compile in parallel).
-template <typename T, bool E4M3, int DQ, int DV, int NI>
+template <typename T, bool E4M3, int DQ, int DV, bool MANY>
 cudaError_t launch_paged_one(const PagedParams& p, unsigned blocks, cudaStream_t stream) {
-  constexpr int kSmem = PagedSizes<DQ, DV, E4M3>::kSmem;
+  constexpr int kSmem = PagedSizes<DQ, DV, E4M3, MANY>::kSmem;
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = ensure_smem_limit(paged_kernel<T, DQ, DV, E4M3, NI>, kSmem, done);
+  const cudaError_t e = ensure_smem_limit(paged_kernel<T, DQ, DV, E4M3, MANY>, kSmem, done);
   if (e != cudaSuccess) return e;
-  paged_kernel<T, DQ, DV, E4M3, NI><<<blocks, kPagedThreads, kSmem, stream>>>(p);
+  paged_kernel<T, DQ, DV, E4M3, MANY><<<blocks, kPagedThreads, kSmem, stream>>>(p);
   return cudaGetLastError();
 }
 template <typename T, bool E4M3, int DQ, int DV>
 cudaError_t launch_paged_widths(const PagedParams& p, unsigned blocks, cudaStream_t stream) {
-  if (!p.func || p.nfunc == 1) return launch_paged_one<T, E4M3, DQ, DV, 1>(p, blocks, stream);
-  return launch_paged_one<T, E4M3, DQ, DV, kMaxIntervals>(p, blocks, stream);
+  return p.cand_offsets ? launch_paged_one<T, E4M3, DQ, DV, true>(p, blocks, stream)
+                        : launch_paged_one<T, E4M3, DQ, DV, false>(p, blocks, stream);
 }
 template <typename T, bool E4M3, int DQ>
 cudaError_t launch_paged_dv(const PagedParams& p, unsigned blocks, cudaStream_t stream) {
