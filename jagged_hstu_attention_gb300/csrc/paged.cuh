@@ -289,22 +289,23 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t w) {
 }
 
 // One pass over the split's keys: the sums of candidates c0 .. of this
-// sequence, as many as fit, in the CTA's shared memory. CG = 0: pair columns
-// (up to 4 candidates a warp), 1 or 2: groups of eight columns. Returns the
-// warps of a slice.
-template <typename T, int DQ, int DV, bool E4M3, bool MANY, int CG>
+// sequence, as many as fit, in the CTA's shared memory. PAIR: two columns for
+// each of up to 4 candidates; otherwise two groups of eight columns a warp (the
+// second idle where a warp has 8 candidates or fewer). Returns the warps of a
+// slice.
+template <typename T, int DQ, int DV, bool E4M3, bool MANY, bool PAIR>
 __device__ __forceinline__ int paged_pass(const PagedParams& p, const PagedSplit& sp) {
   using Z = PagedSizes<DQ, DV, E4M3, MANY>;
-  constexpr bool kPair = CG == 0;
+  constexpr bool kPair = PAIR;
   constexpr bool kHalf = E4M3 || std::is_same<T, __half>::value;  // products in fp16
   constexpr bool kSplitQ = E4M3 && !std::is_same<T, __half>::value;
   using M = typename std::conditional<kHalf, __half, __nv_bfloat16>::type;
   constexpr int KROW = Z::KROW, VROW = Z::VROW, KC = Z::KC, VC = Z::VC;
   constexpr int KB = Z::KB, KP = Z::KP, VB = Z::VB, VP = Z::VP, VE = Z::VE;
   constexpr int KSTEPS = DQ / 16, VTILES = DV / 16, S = Z::kStages;
-  constexpr int NG = kPair ? 1 : CG;         // column groups
-  constexpr int NC = kPair ? 1 : 2 * CG;     // candidates of a lane
-  constexpr int ROWS = kPair ? 4 : 8 * CG;   // candidates of a warp
+  constexpr int NG = kPair ? 1 : 2;      // column groups
+  constexpr int NC = kPair ? 1 : 4;      // candidates of a lane
+  constexpr int ROWS = kPair ? 4 : 16;   // candidates of a warp
   constexpr float kMaxFinite = 3.402823466e38f;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -313,6 +314,7 @@ __device__ __forceinline__ int paged_pass(const PagedParams& p, const PagedSplit
   const int nslices = kPagedWarps / wg, slice = warp / wg, gi = warp % wg;
   const int cg = gi * ROWS;                                        // this warp's first candidate in the pass
   const int ncand = max(0, min(ROWS, total - cg));
+  const int groups = kPair ? 1 : (ncand > 8 ? 2 : 1);              // column groups in use
   const int entries = p.func ? paged_list(p, sp, min(total, wg * ROWS)) : sp.tiles;
   // Copy n of this warp is list entry (n nslices + slice) wg + gi.
   const int iters = (entries + kPagedWarps - 1) / kPagedWarps;
@@ -324,36 +326,30 @@ __device__ __forceinline__ int paged_pass(const PagedParams& p, const PagedSplit
       const int key0 = paged_key(p, sp, e);
       const int page = sp.pages[(key0 >> p.cache.page_shift) - sp.page0];
       const int64_t row0 = cache_row(p.cache, page, sp.h, key0 & ((1 << p.cache.page_shift) - 1));
-      const int nkeys = sp.k1 - key0;
+      const int nkeys = sp.k1 - key0;  // zeros behind the last key
       const uint32_t dst = ring + (stage * wg + gi) * Z::kStep;
       const char* ksrc = static_cast<const char*>(p.cache.k) + row0 * KROW + lane * 16;
       const char* vsrc = static_cast<const char*>(p.cache.v) + row0 * VROW + lane * 16;
-      const auto copy = [&](auto whole) {
 #pragma unroll
-        for (int i = 0; i < KROW / 32; ++i) {
-          const int u = i * 32 + lane, r = u / KC, c = u % KC;
-          const int sw = KC >= 8 ? (r & 1) << 2 : 0;
-          copy16(dst + r * KROW + (c ^ sw) * 16, ksrc + i * 512, whole || r < nkeys);
-        }
+      for (int i = 0; i < KROW / 32; ++i) {
+        const int u = i * 32 + lane, r = u / KC, c = u % KC;
+        const int sw = KC >= 8 ? (r & 1) << 2 : 0;
+        copy16(dst + r * KROW + (c ^ sw) * 16, ksrc + i * 512, r < nkeys);
+      }
 #pragma unroll
-        for (int i = 0; i < VROW / 32; ++i) {
-          const int u = i * 32 + lane, r = u / VC, c = u % VC;
-          const int sw = VC >= 8 ? r & 6 : (VC == 4 ? (r >> 1) & 3 : 0);
-          copy16(dst + kPagedTile * KROW + r * VROW + (c ^ sw) * 16, vsrc + i * 512, whole || r < nkeys);
-        }
-      };
-      if (nkeys >= kPagedTile) copy(std::true_type{});
-      else copy(std::false_type{});  // zeros behind the last key
+      for (int i = 0; i < VROW / 32; ++i) {
+        const int u = i * 32 + lane, r = u / VC, c = u % VC;
+        const int sw = VC >= 8 ? r & 6 : (VC == 4 ? (r >> 1) & 3 : 0);
+        copy16(dst + kPagedTile * KROW + r * VROW + (c ^ sw) * 16, vsrc + i * 512, r < nkeys);
+      }
       if (E4M3 && lane < 2)
         copy16(dst + kPagedTile * (KROW + VROW) + 16 * lane, (lane ? p.cache.v_scale : p.cache.k_scale) + row0, true);
     }
     copies_commit();
   };
-  // A warp that reads alone refills a stage as soon as it has used it; the
-  // warps of a slice refill it after the barrier of the next step.
-#pragma unroll
+  // The first S - 1 copies run while Q is loaded.
+#pragma unroll 1
   for (int n = 0; n < S - 1; ++n) issue(n, n);
-  if (wg == 1) issue(S - 1, S - 1);
 
   // Q fragments, column g of each group. 8-bit caches with bf16 rows: two fp16
   // parts of the row scaled to a largest magnitude of 2^14 to 2^15, which is
@@ -425,14 +421,10 @@ __device__ __forceinline__ int paged_pass(const PagedParams& p, const PagedSplit
   const int krow_sw = KC >= 8 ? (g & 1) << 2 : 0;  // rows g and g + 8 alike
   int stage = 0;
   for (int n0 = 0; n0 < iters; ++n0) {
-    if (wg > 1) {
-      copies_wait<S - 2>();
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + slice), "r"(32 * wg) : "memory");
-      issue(n0 + S - 1, stage == 0 ? S - 1 : stage - 1);  // into the stage that the slice used last
-    } else {
-      copies_wait<S - 1>();
-      __syncwarp();
-    }
+    copies_wait<S - 2>();
+    if (wg > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + slice), "r"(32 * wg) : "memory");
+    else __syncwarp();
+    issue(n0 + S - 1, stage == 0 ? S - 1 : stage - 1);  // into the stage that the slice used last
     for (int j = 0; j < wg; ++j) {
       const int entry = (n0 * nslices + slice) * wg + j;
       if (entry >= entries || ncand == 0) break;
@@ -465,6 +457,7 @@ __device__ __forceinline__ int paged_pass(const PagedParams& p, const PagedSplit
           }
 #pragma unroll
           for (int n = 0; n < NG; ++n) {
+            if (n >= groups) break;
             if (kSplitQ && !kPair) {
               mma16816<M>(s[0][n], a[0], a[1], a[2], a[3], qa[n][st][0], qa[n][st][1]);
               mma16816<M>(s[1][n], a[0], a[1], a[2], a[3], ql[kPair ? 0 : n][kSplitQ && !kPair ? st : 0][0],
@@ -495,6 +488,8 @@ __device__ __forceinline__ int paged_pass(const PagedParams& p, const PagedSplit
       for (int c = 0; c < NC; ++c)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
+          pr[c][r] = 0.0f;
+          if (c / 2 >= groups) continue;
           float x;
           if (kPair) {
             x = s[0][0][2 * r] + s[1][0][2 * r];
@@ -558,6 +553,7 @@ __device__ __forceinline__ int paged_pass(const PagedParams& p, const PagedSplit
         for (int n = 0; n < NG; ++n)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
+            if (n >= groups) break;
             const float x = pr[kPair ? 0 : 2 * n][r], y = pr[kPair ? 0 : 2 * n + 1][r];
             const uint32_t h = Elem<M>::pack2(x, y);
             bh[n][r] = transpose8(h);
@@ -570,6 +566,7 @@ __device__ __forceinline__ int paged_pass(const PagedParams& p, const PagedSplit
       const auto add = [&](int m, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
+          if (n >= groups) break;
           mma16816<M>(acc[n][m], a0, a1, a2, a3, bh[n][0], bh[n][1]);
           if (!kPair) mma16816<M>(acc[n][m], a0, a1, a2, a3, bl[n][0], bl[n][1]);
         }
@@ -602,10 +599,6 @@ __device__ __forceinline__ int paged_pass(const PagedParams& p, const PagedSplit
           }
         }
       }
-    }
-    if (wg == 1) {
-      __syncwarp();
-      issue(n0 + S, stage);  // into the stage just used
     }
     stage = stage + 1 == S ? 0 : stage + 1;
   }
@@ -667,7 +660,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedSizes<DQ, DV, E4M3, MANY>:
   // Pages of this split, read before the length is known (entries past the
   // length are not looked at).
   const int page0 = k0 >> p.cache.page_shift;
-  const int most_pages = min((p.split + (1 << p.cache.page_shift) - 1) >> p.cache.page_shift, p.max_pages - page0);
+  const int most_pages = min(((k0 + p.split - 1) >> p.cache.page_shift) - page0 + 1, p.max_pages - page0);
   constexpr int kPageLoads = kPagedMaxSplit / kPagedTile / kPagedThreads;
   int page[kPageLoads];
 #pragma unroll
@@ -729,13 +722,10 @@ __global__ void __launch_bounds__(kPagedThreads, PagedSizes<DQ, DV, E4M3, MANY>:
     sp.c0 = c0;
     int wg, rows;
     if (!MANY || ce - c0 <= 4) {
-      wg = paged_pass<T, DQ, DV, E4M3, MANY, 0>(p, sp);
+      wg = paged_pass<T, DQ, DV, E4M3, MANY, true>(p, sp);
       rows = 4;
-    } else if (MANY && ce - c0 <= 8) {
-      wg = paged_pass<T, DQ, DV, E4M3, MANY, MANY ? 1 : 0>(p, sp);
-      rows = 8;
     } else {
-      wg = paged_pass<T, DQ, DV, E4M3, MANY, MANY ? 2 : 0>(p, sp);
+      wg = paged_pass<T, DQ, DV, E4M3, MANY, !MANY>(p, sp);
       rows = 16;
     }
     __syncthreads();
