@@ -459,7 +459,9 @@ HSTU_API size_t hstu_attn_paged_workspace_size(const hstu_cache_t* cache, int32_
  *            or NULL: every cached position is visible (nfunc is ignored)
  *   max_seqlen   N, 1 .. 2^24 (the pages take longer histories than the
  *            contiguous kernels)
- *   ws       hstu_attn_paged_workspace_size() bytes, 256-byte aligned
+ *   ws       hstu_attn_paged_workspace_size() bytes, 256-byte aligned; NULL is
+ *            taken where that size is 256 (one split: nothing but the error
+ *            word), and bad sequences are then not reported
  * Slots past a sequence's length and positions that a candidate does not see
  * do not reach it, whatever they hold (NaN and infinities too). A candidate
  * that sees nothing gets 0. The cache's length is split over CTAs, whose sums

@@ -135,7 +135,6 @@ def load(path: str = None) -> ctypes.CDLL:
     lib = ctypes.CDLL(path)
     vp, i32, u32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint32, ctypes.c_size_t
     i64, sp = ctypes.c_int64, ctypes.POINTER(Shape)
-    cp, rp = ctypes.POINTER(Cache), ctypes.POINTER(Rope)
     sig = {
         "hstu_attn_nfunc_supported": (ctypes.c_int, [i32]),
         "hstu_attn_workspace_size": (sz, [sp, i32]),
@@ -163,12 +162,12 @@ def load(path: str = None) -> ctypes.CDLL:
         "hstu_attn_bwd_targets": (ctypes.c_int, [vp, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_int64, vp, sp, vp,
                                                  sz, vp]),
         "hstu_attn_rope_table": (ctypes.c_int, [ctypes.POINTER(RopeSpec), vp, ctypes.POINTER(ctypes.c_float)]),
-        "hstu_attn_rope": (ctypes.c_int, [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i32, i32, i32, rp, i32, vp]),
-        "hstu_attn_cache_write": (ctypes.c_int, [cp, vp, i64, vp, i64, vp, i32, i64, vp, vp, i32, rp, vp, vp, sz,
+        "hstu_attn_rope": (ctypes.c_int, [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i32, i32, i32, vp, i32, vp]),
+        "hstu_attn_cache_write": (ctypes.c_int, [vp, vp, i64, vp, i64, vp, i32, i64, vp, vp, i32, vp, vp, vp, sz,
                                                  vp]),
-        "hstu_attn_cache_read": (ctypes.c_int, [cp, vp, vp, vp, i32, i64, vp, vp, i32, vp, sz, vp]),
-        "hstu_attn_paged_workspace_size": (sz, [cp, i32, i64, i32]),
-        "hstu_attn_fwd_paged": (ctypes.c_int, [vp, i64, vp, cp, vp, i32, vp, i32, vp, i64, vp, i32, i32,
+        "hstu_attn_cache_read": (ctypes.c_int, [vp, vp, vp, vp, i32, i64, vp, vp, i32, vp, sz, vp]),
+        "hstu_attn_paged_workspace_size": (sz, [vp, i32, i64, i32]),
+        "hstu_attn_fwd_paged": (ctypes.c_int, [vp, i64, vp, vp, vp, i32, vp, i32, vp, i64, vp, i32, i32,
                                                ctypes.c_float, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
@@ -532,6 +531,10 @@ def set_handoff_limit_for_tests(limit_ns: int) -> None:
     _check(load().hstu_attn_test_set_handoff_limit(int(limit_ns)), "hstu_attn_test_set_handoff_limit")
 
 
+# ---------------------------------------------------------------- serving
+# A decode step is a few microseconds on the GPU, so these wrappers keep to one
+# pass of cheap checks and hand plain integers to ctypes.
+
 _ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 
@@ -545,8 +548,9 @@ class RopeTable:
         self.rotary_dim = 2 * turns.numel()
         self.interleaved = bool(interleaved)
         self.magnitude = magnitude
-        self.device = turns.device
         self._c = Rope(turns.data_ptr(), self.rotary_dim, int(self.interleaved), magnitude)
+        self._addr = ctypes.addressof(self._c)
+        self._device = turns.get_device()
 
 
 def rope_table(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -561,45 +565,60 @@ def rope_table(rotary_dim: int, base: float = 10000.0, scaling: str = "none", fa
     spec = RopeSpec(int(rotary_dim), _ROPE_SCALINGS[scaling], base, factor, original_len, fast_turns, slow_turns)
     turns = torch.zeros(max(int(rotary_dim) // 2, 1), dtype=torch.int64)
     magnitude = ctypes.c_float()
-    _check(load().hstu_attn_rope_table(ctypes.byref(spec), _ptr(turns), ctypes.byref(magnitude)),
+    _check(load().hstu_attn_rope_table(ctypes.byref(spec), turns.data_ptr(), ctypes.byref(magnitude)),
            "hstu_attn_rope_table")
     return RopeTable(turns.to(device), interleaved, magnitude.value)
 
 
-def _need_rows(t: torch.Tensor, dtype, name: str) -> int:
-    """Checks a (rows, H, D) tensor whose rows may lie apart (a slice of a
-    wider projection); returns the distance between rows in elements."""
-    if not t.is_cuda:
+def _here(index: int, name: str) -> None:
+    """Tensors on device ``index``, and that the current one: the library
+    launches on the current device."""
+    if index < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
+    current = torch._C._cuda_getDevice()
+    if index != current:
+        raise ValueError(f"{name} is on cuda:{index}, the current device is cuda:{current}")
+
+
+def _raw_stream(stream, index: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
+def _device_of(t: torch.Tensor, index: int, name: str) -> None:
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be a CUDA tensor" if t.get_device() < 0 else
+                         f"{name} is on cuda:{t.get_device()}, not on cuda:{index}")
+
+
+def _rows(t: torch.Tensor, dtype, heads: int, width: int, index: int, name: str) -> int:
+    """Checks a (rows, heads, width) tensor whose rows may lie apart (a slice
+    of a wider projection); returns the distance between rows in elements."""
+    _device_of(t, index, name)
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be (rows, heads, width), got {tuple(t.shape)}")
-    rows, heads, width = t.shape
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != width:
+        raise ValueError(f"{name} must be (rows, {heads}, {width}), got {tuple(shape)}")
     stride, sh, sw = t.stride()
-    if (sw != 1 and width > 1) or (sh != width and heads > 1):
+    if shape[0] <= 1:
+        stride = heads * width
+    if sw != 1 or (sh != width and heads > 1):
         raise ValueError(f"{name}: heads and columns of a row must be contiguous")
-    if rows <= 1:
-        return heads * width
     if stride < heads * width:
         raise ValueError(f"{name}: rows overlap")
     return stride
 
 
-def _need_here(device, **tensors):
-    """Every tensor on ``device``, and that the current one: the library
-    launches on the current device."""
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
-
-
-def _need_int32(t: torch.Tensor, name: str, shape):
-    _need(t, torch.int32, name)
-    if tuple(t.shape) != tuple(shape):
+def _ints(t: torch.Tensor, shape, index: int, name: str) -> int:
+    """Checks an int32 tensor of the given shape; returns its address."""
+    _device_of(t, index, name)
+    if t.dtype != torch.int32:
+        raise ValueError(f"{name} must be {torch.int32}, got {t.dtype}")
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def rope(q, k, positions, table: RopeTable, backward: bool = False, outs=None, stream=None):
@@ -608,34 +627,41 @@ def rope(q, k, positions, table: RopeTable, backward: bool = False, outs=None, s
     slices of a wider projection; k may be None. ``backward=True`` takes the
     gradients of q' and k' to those of q and k. ``outs`` may be (q, k) itself:
     the rows are then rotated in place."""
-    if q.dtype not in DTYPES:
-        raise ValueError(f"q must be one of {_FLOATS}, got {q.dtype}")
-    qs = _need_rows(q, q.dtype, "q")
-    T, H, D = q.shape
-    ks = 0
+    dtype, index = q.dtype, q.get_device()
+    if dtype not in DTYPES:
+        raise ValueError(f"q must be one of {_FLOATS}, got {dtype}")
+    _here(index, "q")
+    if q.dim() != 3:
+        raise ValueError(f"q must be (rows, heads, width), got {tuple(q.shape)}")
+    shape = q.shape
+    T, H, D = shape
+    qs, ks, kos, kp, kop = _rows(q, dtype, H, D, index, "q"), 0, 0, 0, 0
     if k is not None:
-        ks = _need_rows(k, q.dtype, "k")
-        if k.shape != q.shape:
-            raise ValueError(f"k must have q's shape {tuple(q.shape)}, got {tuple(k.shape)}")
-    _need_int32(positions, "positions", (T,))
-    _need_here(q.device, k=k, positions=positions, table=table)
+        ks, kp = _rows(k, dtype, H, D, index, "k"), k.data_ptr()
+        if k.shape[0] != T:
+            raise ValueError(f"k must have q's shape {tuple(shape)}, got {tuple(k.shape)}")
+    if table._device != index:
+        raise ValueError("table is on another device")
     if outs is None:
-        qo = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
-        ko = None if k is None else torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+        qo = torch.empty(shape, dtype=dtype, device=q.device)
+        ko = None if k is None else torch.empty(shape, dtype=dtype, device=q.device)
         qos = kos = H * D
     else:
         qo, ko = outs
-        qos, kos = _need_rows(qo, q.dtype, "outs[0]"), 0
-        if qo.shape != q.shape or (ko is None) != (k is None):
+        if (ko is None) != (k is None):
             raise ValueError("outs must match q and k")
+        qos = _rows(qo, dtype, H, D, index, "outs[0]")
         if ko is not None:
-            kos = _need_rows(ko, q.dtype, "outs[1]")
-            if ko.shape != q.shape:
-                raise ValueError("outs must match q and k")
-        _need_here(q.device, qo=qo, ko=ko)
-    _check(load().hstu_attn_rope(_ptr(q), qs, _ptr(k), ks, _ptr(qo), qos, _ptr(ko), kos, _ptr(positions), T, H, D,
-                                 DTYPES[q.dtype], ctypes.byref(table._c), 1 if backward else 0, _stream(stream)),
-           "hstu_attn_rope")
+            kos = _rows(ko, dtype, H, D, index, "outs[1]")
+        if qo.shape[0] != T or (ko is not None and ko.shape[0] != T):
+            raise ValueError("outs must match q and k")
+    if ko is not None:
+        kop = ko.data_ptr()
+    st = load().hstu_attn_rope(q.data_ptr(), qs, kp, ks, qo.data_ptr(), qos, kop, kos,
+                               _ints(positions, (T,), index, "positions"), T, H, D, DTYPES[dtype], table._addr,
+                               1 if backward else 0, _raw_stream(stream, index))
+    if st != HSTU_OK:
+        _check(st, "hstu_attn_rope")
     return qo, ko
 
 
@@ -674,6 +700,8 @@ class PagedCache:
         addr = lambda t: None if t is None else t.data_ptr()
         self._c = Cache(addr(k), addr(v), addr(k_scale), addr(v_scale), self.num_pages, self.page_size, self.heads,
                         self.dim, self.dim_v, DTYPES[dtype], int(e4m3))
+        self._addr = ctypes.addressof(self._c)
+        self._device = k.get_device()
 
 
 def alloc_cache(num_pages: int, page_size: int, heads: int, dim: int, dim_v: int = 0, dtype=torch.bfloat16,
@@ -686,14 +714,19 @@ def alloc_cache(num_pages: int, page_size: int, heads: int, dim: int, dim_v: int
     return PagedCache(k, v, new(*shape) if quantised else None, new(*shape) if quantised else None, dtype=dtype)
 
 
-def _need_pages(cache: PagedCache, page_table, batch: int):
-    _need(page_table, torch.int32, "page_table")
-    if page_table.dim() != 2 or page_table.shape[0] != batch or page_table.shape[1] < 1:
-        raise ValueError(f"page_table must be (batch = {batch}, pages), got {tuple(page_table.shape)}")
+def _pages(page_table, batch: int, index: int):
+    """Checks a page table; returns its address and width."""
+    shape = page_table.shape
+    if len(shape) != 2 or shape[0] != batch or shape[1] < 1:
+        raise ValueError(f"page_table must be (batch = {batch}, pages), got {tuple(shape)}")
+    return _ints(page_table, shape, index, "page_table"), shape[1]
 
 
-def _ws_args(ws):
-    return (None, 0) if ws is None else (_ptr(ws), ws.numel() * ws.element_size())
+def _ws_args(ws, index: int):
+    if ws is None:
+        return 0, 0
+    _device_of(ws, index, "ws")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def cache_write(cache: PagedCache, k, v, seq_offsets, cache_lens, page_table, rope: Optional[RopeTable] = None,
@@ -703,22 +736,24 @@ def cache_write(cache: PagedCache, k, v, seq_offsets, cache_lens, page_table, ro
     (hstu_attn_cache_write); ``rope`` rotates k on its way, by ``positions``
     or by its place in the cache. ``cache_lens`` is not changed. With a ``ws``
     (256 bytes) skipped rows are reported by ``device_status``."""
-    ks, vs = _need_rows(k, cache.dtype, "k"), _need_rows(v, cache.dtype, "v")
-    T = k.shape[0]
-    if k.shape[1:] != (cache.heads, cache.dim) or v.shape != (T, cache.heads, cache.dim_v):
-        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} do not fit the cache's heads and widths")
-    _need(seq_offsets, torch.int32, "seq_offsets")
-    B = seq_offsets.numel() - 1
-    _need_int32(cache_lens, "cache_lens", (B,))
-    _need_pages(cache, page_table, B)
-    if positions is not None:
-        _need_int32(positions, "positions", (T,))
-    _need_here(cache.device, k=k, v=v, seq_offsets=seq_offsets, cache_lens=cache_lens, page_table=page_table,
-               positions=positions, rope=rope, ws=ws)
-    _check(load().hstu_attn_cache_write(ctypes.byref(cache._c), _ptr(k), ks, _ptr(v), vs, _ptr(seq_offsets), B, T,
-                                        _ptr(cache_lens), _ptr(page_table), page_table.shape[1],
-                                        None if rope is None else ctypes.byref(rope._c), _ptr(positions),
-                                        *_ws_args(ws), _stream(stream)), "hstu_attn_cache_write")
+    index = cache._device
+    _here(index, "cache")
+    ks = _rows(k, cache.dtype, cache.heads, cache.dim, index, "k")
+    vs = _rows(v, cache.dtype, cache.heads, cache.dim_v, index, "v")
+    T, B = k.shape[0], seq_offsets.numel() - 1
+    if v.shape[0] != T:
+        raise ValueError(f"k has {T} rows, v {v.shape[0]}")
+    if rope is not None and rope._device != index:
+        raise ValueError("rope is on another device")
+    table, width = _pages(page_table, B, index)
+    st = load().hstu_attn_cache_write(cache._addr, k.data_ptr(), ks, v.data_ptr(), vs,
+                                      _ints(seq_offsets, (B + 1,), index, "seq_offsets"), B, T,
+                                      _ints(cache_lens, (B,), index, "cache_lens"), table, width,
+                                      0 if rope is None else rope._addr,
+                                      0 if positions is None else _ints(positions, (T,), index, "positions"),
+                                      *_ws_args(ws, index), _raw_stream(stream, index))
+    if st != HSTU_OK:
+        _check(st, "hstu_attn_cache_write")
 
 
 def cache_read(cache: PagedCache, seq_offsets, rows: int, page_table, starts=None, outs=None,
@@ -726,30 +761,31 @@ def cache_read(cache: PagedCache, seq_offsets, rows: int, page_table, starts=Non
     """(k, v) of cached rows, jagged and contiguous, in the cache's dtype
     (hstu_attn_cache_read): ``rows`` rows, those of sequence b from position
     ``starts[b]`` (0 without ``starts``)."""
-    _need(seq_offsets, torch.int32, "seq_offsets")
+    index = cache._device
+    _here(index, "cache")
     B = seq_offsets.numel() - 1
-    _need_pages(cache, page_table, B)
-    if starts is not None:
-        _need_int32(starts, "starts", (B,))
     if outs is None:
-        new = lambda w: torch.empty((rows, cache.heads, w), dtype=cache.dtype, device=cache.device)
-        k, v = new(cache.dim), new(cache.dim_v)
+        k = torch.empty((rows, cache.heads, cache.dim), dtype=cache.dtype, device=cache.device)
+        v = torch.empty((rows, cache.heads, cache.dim_v), dtype=cache.dtype, device=cache.device)
     else:
         k, v = outs
         for t, n, w in ((k, "outs[0]", cache.dim), (v, "outs[1]", cache.dim_v)):
-            _need(t, cache.dtype, n)
-            if t.shape != (rows, cache.heads, w):
-                raise ValueError(f"{n} must have shape {(rows, cache.heads, w)}, got {tuple(t.shape)}")
-    _need_here(cache.device, seq_offsets=seq_offsets, page_table=page_table, starts=starts, k=k, v=v, ws=ws)
-    _check(load().hstu_attn_cache_read(ctypes.byref(cache._c), _ptr(k), _ptr(v), _ptr(seq_offsets), B, rows,
-                                       _ptr(starts), _ptr(page_table), page_table.shape[1], *_ws_args(ws),
-                                       _stream(stream)), "hstu_attn_cache_read")
+            _rows(t, cache.dtype, cache.heads, w, index, n)
+            if t.shape[0] != rows or not t.is_contiguous():
+                raise ValueError(f"{n} must be contiguous and have {rows} rows")
+    table, width = _pages(page_table, B, index)
+    st = load().hstu_attn_cache_read(cache._addr, k.data_ptr(), v.data_ptr(),
+                                     _ints(seq_offsets, (B + 1,), index, "seq_offsets"), B, rows,
+                                     0 if starts is None else _ints(starts, (B,), index, "starts"), table, width,
+                                     *_ws_args(ws, index), _raw_stream(stream, index))
+    if st != HSTU_OK:
+        _check(st, "hstu_attn_cache_read")
     return k, v
 
 
 def paged_workspace(cache: PagedCache, batch: int, num_candidates: int, max_seqlen: int) -> torch.Tensor:
     """Workspace of ``fwd_paged``."""
-    n = int(load().hstu_attn_paged_workspace_size(ctypes.byref(cache._c), batch, num_candidates, max_seqlen))
+    n = load().hstu_attn_paged_workspace_size(cache._addr, batch, num_candidates, max_seqlen)
     if n == 0:
         raise HstuError(2, "hstu_attn_paged_workspace_size")
     return torch.empty(n, dtype=torch.uint8, device=cache.device)
@@ -760,37 +796,37 @@ def fwd_paged(q_c, cache: PagedCache, cache_lens, page_table, max_seqlen: int, a
     """o_c (C, H, D_v): candidate rows q_c (C, H, D_qk) against the
     ``cache_lens[b]`` cached rows of their sequences (hstu_attn_fwd_paged).
     One candidate a sequence without ``cand_offsets``; all cached rows are
-    visible without ``func_c`` (nfunc, C)."""
-    qs = _need_rows(q_c, cache.dtype, "q_c")
-    C, H, D = q_c.shape
-    if (H, D) != (cache.heads, cache.dim):
-        raise ValueError(f"q_c {tuple(q_c.shape)} does not fit the cache's heads and width")
-    _need(cache_lens, torch.int32, "cache_lens")
-    B = cache_lens.numel()
-    _need_pages(cache, page_table, B)
-    nfunc = 0
-    if cand_offsets is not None:
-        _need_int32(cand_offsets, "cand_offsets", (B + 1,))
+    visible without ``func_c`` (nfunc, C). With a ``ws`` (``paged_workspace``)
+    of its own a caller can read ``device_status``."""
+    index, dtype = cache._device, cache.dtype
+    _here(index, "cache")
+    qs = _rows(q_c, dtype, cache.heads, cache.dim, index, "q_c")
+    C, B = q_c.shape[0], cache_lens.numel()
+    table, width = _pages(page_table, B, index)
+    nfunc = func = 0
     if func_c is not None:
         nfunc = func_c.shape[0]
-        _need_int32(func_c, "func_c", (nfunc, C))
+        func = _ints(func_c, (nfunc, C), index, "func_c")
     if alpha is None:
-        alpha = 1.0 / math.sqrt(D)
+        alpha = 1.0 / math.sqrt(cache.dim)
     if out is None:
-        out = torch.empty((C, H, cache.dim_v), dtype=cache.dtype, device=cache.device)
+        out = torch.empty((C, cache.heads, cache.dim_v), dtype=dtype, device=cache.device)
     else:
-        _need(out, cache.dtype, "out")
-        if out.shape != (C, H, cache.dim_v):
-            raise ValueError(f"out must have shape {(C, H, cache.dim_v)}, got {tuple(out.shape)}")
-    _need_here(cache.device, q_c=q_c, cache_lens=cache_lens, page_table=page_table, cand_offsets=cand_offsets,
-               func_c=func_c, out=out, ws=ws)
-    own_ws = ws is None
-    if own_ws:
-        ws = paged_workspace(cache, B, C, max_seqlen)
-    _check(load().hstu_attn_fwd_paged(_ptr(q_c), qs, _ptr(out), ctypes.byref(cache._c), _ptr(cache_lens), B,
-                                      _ptr(page_table), page_table.shape[1], _ptr(cand_offsets), C, _ptr(func_c),
-                                      nfunc, max_seqlen, alpha, _ptr(ws), ws.numel(), _stream(stream)),
-           "hstu_attn_fwd_paged")
-    if own_ws and stream is not None:
-        ws.record_stream(stream)
+        _rows(out, dtype, cache.heads, cache.dim_v, index, "out")
+        if out.shape[0] != C or not out.is_contiguous():
+            raise ValueError(f"out must be contiguous and have {C} rows")
+    lib = load()
+    own_ws = None
+    if ws is None:
+        n = lib.hstu_attn_paged_workspace_size(cache._addr, B, C, max_seqlen)
+        if n > 256:  # sums of splits; without them nothing but the error word
+            own_ws = ws = torch.empty(n, dtype=torch.uint8, device=cache.device)
+    st = lib.hstu_attn_fwd_paged(q_c.data_ptr(), qs, out.data_ptr(), cache._addr,
+                                 _ints(cache_lens, (B,), index, "cache_lens"), B, table, width,
+                                 0 if cand_offsets is None else _ints(cand_offsets, (B + 1,), index, "cand_offsets"),
+                                 C, func, nfunc, max_seqlen, alpha, *_ws_args(ws, index), _raw_stream(stream, index))
+    if st != HSTU_OK:
+        _check(st, "hstu_attn_fwd_paged")
+    if own_ws is not None and stream is not None:
+        own_ws.record_stream(stream)
     return out

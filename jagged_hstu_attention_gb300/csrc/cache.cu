@@ -1,16 +1,18 @@
 // Writing rows into the paged K/V cache and reading them back.
 //
-// Both kernels move each row once. A thread holds one slot (16 columns) of
-// one (row, head) of k or of v; the threads of a row are neighbours in a
-// warp, so that a row's largest magnitude, which sets the scale of its 8-bit
-// codes, is a few shuffles away. The blocks of the k rows come first in the
-// grid, those of the v rows after them.
+// Both kernels move each row once. A thread holds one slot (two 8-column
+// chunks) of the k and v rows of one token, for several heads: the token's
+// sequence, its page and the slot's cosines and sines are found once for all
+// of them. The threads of a row are neighbours in a warp, so that a row's
+// largest magnitude, which sets the scale of its 8-bit codes, is a few
+// shuffles away.
 #include "cache.cuh"
 #include "rope.cuh"
 
 namespace hstu {
 
 constexpr int kCacheThreads = 256;
+constexpr int kCacheHeads = 4;  // heads of a thread where there are rows enough to fill the GPU
 
 struct CacheParams {
   CacheView cache;
@@ -23,16 +25,20 @@ struct CacheParams {
   const int32_t* positions;  // for the rotation; null: the row's position
   const uint64_t* turns;     // null: k is not rotated
   int32_t* header;           // null: skipped rows are not reported
-  int64_t rows, k_blocks;
+  int64_t rows;
   int32_t batch, max_pages, rotary;
+  int32_t slots;  // threads of a token: those of the wider of k and v
+  bool one_head;  // heads of a thread: 1 or kCacheHeads
   float magnitude;
 };
 
 // Page-table lookup of jagged row t: its position and its (page, slot).
-// False (and the error word set) where the row has no valid place.
+// False (and the error word set) where the row has no valid place. Every lane
+// of the warp calls it; rows past the last are nobody's.
 __device__ __forceinline__ bool place_row(const CacheParams& p, int64_t t, int64_t& pos, int64_t& page, int& slot) {
   int b, first;
   bool ok = find_sequence(p.seq_offsets, p.batch, t, b, first);
+  if (t >= p.rows) return false;
   if (ok) {
     const int start = p.starts ? __ldg(p.starts + b) : 0;
     pos = t - first + start;
@@ -56,147 +62,176 @@ __device__ __forceinline__ void check_offsets(const CacheParams& p) {
   if (bad) atomicOr(p.header + kHdrErr, kErrInput);
 }
 
-// The unit (row, head, slot) of this thread in the k or v part of the grid.
-struct CacheUnit {
-  int64_t row;
-  int head, slot, width;
-  bool is_v, live;
+// One head's 16 columns, in registers.
+struct Chunks {
+  uint4 a, b;
 };
-__device__ __forceinline__ CacheUnit cache_unit(const CacheParams& p) {
-  CacheUnit u;
-  u.is_v = blockIdx.x >= p.k_blocks;
-  u.width = u.is_v ? p.cache.dim_v : p.cache.dim;
-  const int slots = u.width / 16;
-  const int64_t unit =
-      (static_cast<int64_t>(blockIdx.x) - (u.is_v ? p.k_blocks : 0)) * kCacheThreads + threadIdx.x;
-  u.slot = static_cast<int>(unit) & (slots - 1);
-  const int64_t rh = unit / slots;
-  u.row = rh / p.cache.heads;
-  u.head = static_cast<int>(rh - u.row * p.cache.heads);
-  u.live = u.row < p.rows;
-  return u;
+template <typename T>
+__device__ __forceinline__ Chunks load_chunks(const T* row, const SlotColumns& k) {
+  return Chunks{*reinterpret_cast<const uint4*>(row + k.c0), *reinterpret_cast<const uint4*>(row + k.c1)};
 }
 
-// ROPE: 0 none, 1 half layout, 2 interleaved.
+// Writes one head's slot into the cache at row `at` of `out`. Every thread of
+// the row calls it; those without a part of it (`live` false) only take part
+// in the shuffles.
 template <typename T, bool E4M3, int ROPE>
-__global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheParams p) {
-  check_offsets(p);
-  const CacheUnit u = cache_unit(p);
-  int64_t pos = 0, page = 0;
-  int slot_in_page = 0;
-  const bool ok = u.live && place_row(p, u.row, pos, page, slot_in_page);
-  const bool turned = ROPE != 0 && !u.is_v && 16 * u.slot < p.rotary;
-  int c0 = 16 * u.slot, c1 = c0 + 8;
-  if (ROPE != 0 && !u.is_v) slot_columns(u.slot, p.rotary, ROPE == 2, c0, c1);
-  uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
-  if (ok) {
-    const T* row = static_cast<const T*>(u.is_v ? p.v : p.k) + u.row * (u.is_v ? p.v_stride : p.k_stride) +
-                   static_cast<int64_t>(u.head) * u.width;
-    u0 = *reinterpret_cast<const uint4*>(row + c0);
-    u1 = *reinterpret_cast<const uint4*>(row + c1);
-  }
+__device__ __forceinline__ void write_chunks(Chunks u, const SlotColumns& k, bool turned, const float (&c)[8],
+                                             const float (&s)[8], bool live, int slots, void* out, uint8_t* scales,
+                                             int64_t at, int width, bool first) {
   float a[8], b[8];
-  if (E4M3 || turned) {
-    unpack8<T>(u0, a);
-    unpack8<T>(u1, b);
+  if (E4M3 || ROPE != 0) {
+    unpack8<T>(u.a, a);
+    unpack8<T>(u.b, b);
   }
-  if (turned && ok) {
-    float c[8], s[8];
-    rope_factors(p.turns, 8 * u.slot, p.positions ? __ldg(p.positions + u.row) : pos, p.magnitude,
-                 1.0f, c, s);
-    rotate_pairs<ROPE == 2>(a, b, c, s);
-  }
-  const int64_t at = ok ? cache_row(p.cache, page, u.head, slot_in_page) : 0;
+  if (ROPE != 0 && turned) rotate_pairs<ROPE == 2>(a, b, c, s);
   if (!E4M3) {
-    if (!ok) return;
-    if (turned) {
-      u0 = pack8<T>(a);
-      u1 = pack8<T>(b);
-    }
-    T* out = static_cast<T*>(u.is_v ? p.cache.v : p.cache.k) + at * u.width;
-    *reinterpret_cast<uint4*>(out + c0) = u0;
-    *reinterpret_cast<uint4*>(out + c1) = u1;
+    if (!live) return;
+    if (ROPE != 0 && turned) u = Chunks{pack8<T>(a), pack8<T>(b)};
+    T* row = static_cast<T*>(out) + at * width;
+    *reinterpret_cast<uint4*>(row + k.c0) = u.a;
+    *reinterpret_cast<uint4*>(row + k.c1) = u.b;
     return;
   }
   // Largest finite magnitude of the row: this thread's 16 values, then the
   // row's 2, 4 or 8 threads.
+  constexpr float kMaxFinite = 3.402823466e38f;
   float top = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float x = fabsf(a[i]), y = fabsf(b[i]);
-    top = fmaxf(top, x <= 3.402823466e38f ? x : 0.0f);
-    top = fmaxf(top, y <= 3.402823466e38f ? y : 0.0f);
+    top = fmaxf(top, x <= kMaxFinite ? x : 0.0f);
+    top = fmaxf(top, y <= kMaxFinite ? y : 0.0f);
   }
-  const int slots = u.width / 16;
+  if (!live) top = 0.0f;
 #pragma unroll
   for (int off = 1; off < 8; off <<= 1) {
     const float o = __shfl_xor_sync(0xffffffffu, top, off);
     if (off < slots) top = fmaxf(top, o);
   }
-  if (!ok) return;
+  if (!live) return;
   const uint32_t byte = scale_byte(top);
   const float inv = __uint_as_float((254u - byte) << 23);  // 2^(127 - byte), exact
-  uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    a[i] = fabsf(a[i]) <= 3.402823466e38f ? a[i] * inv : __uint_as_float(0x7fc00000u);
-    b[i] = fabsf(b[i]) <= 3.402823466e38f ? b[i] * inv : __uint_as_float(0x7fc00000u);
+    a[i] = fabsf(a[i]) <= kMaxFinite ? a[i] * inv : __uint_as_float(0x7fc00000u);
+    b[i] = fabsf(b[i]) <= kMaxFinite ? b[i] * inv : __uint_as_float(0x7fc00000u);
   }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    w[i] = e4m3x2(a[4 * i], a[4 * i + 1]) | (e4m3x2(a[4 * i + 2], a[4 * i + 3]) << 16);
-    w[2 + i] = e4m3x2(b[4 * i], b[4 * i + 1]) | (e4m3x2(b[4 * i + 2], b[4 * i + 3]) << 16);
-  }
-  uint8_t* out = static_cast<uint8_t*>(u.is_v ? p.cache.v : p.cache.k) + at * u.width;
-  if (c1 == c0 + 8) {
-    *reinterpret_cast<uint4*>(out + c0) = make_uint4(w[0], w[1], w[2], w[3]);
-  } else {
-    *reinterpret_cast<uint2*>(out + c0) = make_uint2(w[0], w[1]);
-    *reinterpret_cast<uint2*>(out + c1) = make_uint2(w[2], w[3]);
-  }
-  if (u.slot == 0) (u.is_v ? p.cache.v_scale : p.cache.k_scale)[at] = static_cast<uint8_t>(byte);
+  uint8_t* row = static_cast<uint8_t*>(out) + at * width;
+  *reinterpret_cast<uint2*>(row + k.c0) = make_uint2(e4m3x2(a[0], a[1]) | (e4m3x2(a[2], a[3]) << 16),
+                                                     e4m3x2(a[4], a[5]) | (e4m3x2(a[6], a[7]) << 16));
+  *reinterpret_cast<uint2*>(row + k.c1) = make_uint2(e4m3x2(b[0], b[1]) | (e4m3x2(b[2], b[3]) << 16),
+                                                     e4m3x2(b[4], b[5]) | (e4m3x2(b[6], b[7]) << 16));
+  if (first) scales[at] = static_cast<uint8_t>(byte);
 }
 
-template <typename T, bool E4M3>
+// ROPE: 0 none, 1 half layout, 2 interleaved.
+template <typename T, bool E4M3, int ROPE, int HEADS>
+__global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheParams p) {
+  check_offsets(p);
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kCacheThreads + threadIdx.x;
+  const int slot = static_cast<int>(unit) & (p.slots - 1);
+  const int64_t row = unit / p.slots;
+  const int h0 = blockIdx.y * HEADS, heads = min(HEADS, p.cache.heads - h0);
+  const bool in = row < p.rows;
+  const bool has_k = in && 16 * slot < p.cache.dim, has_v = in && 16 * slot < p.cache.dim_v;
+  const SlotColumns kc = slot_columns(slot, p.cache.dim, ROPE != 0 ? p.rotary : 0, ROPE == 2);
+  const SlotColumns vc = slot_columns(slot, p.cache.dim_v, 0, false);
+  // The rows' loads do not wait for the search of their place.
+  const T* krow = static_cast<const T*>(p.k) + row * p.k_stride + static_cast<int64_t>(h0) * p.cache.dim;
+  const T* vrow = static_cast<const T*>(p.v) + row * p.v_stride + static_cast<int64_t>(h0) * p.cache.dim_v;
+  Chunks ku[HEADS], vu[HEADS];
+#pragma unroll
+  for (int i = 0; i < HEADS; ++i) {
+    ku[i] = vu[i] = Chunks{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (i >= heads) continue;
+    if (has_k) ku[i] = load_chunks(krow + i * p.cache.dim, kc);
+    if (has_v) vu[i] = load_chunks(vrow + i * p.cache.dim_v, vc);
+  }
+  int64_t pos = 0, page = 0;
+  int slot_in_page = 0;
+  const bool ok = place_row(p, row, pos, page, slot_in_page);
+  float c[8], s[8];
+  const bool turned = ROPE != 0 && has_k && kc.turned;
+  if (turned && ok)
+    rope_factors(p.turns, kc.first, kc.second, p.positions ? __ldg(p.positions + row) : pos, p.magnitude, 1.0f, c, s);
+#pragma unroll
+  for (int i = 0; i < HEADS; ++i) {
+    if (i >= heads) break;
+    const int64_t at = cache_row(p.cache, page, h0 + i, slot_in_page);
+    write_chunks<T, E4M3, ROPE>(ku[i], kc, turned && ok, c, s, ok && has_k, p.cache.dim / 16, p.cache.k,
+                                p.cache.k_scale, at, p.cache.dim, slot == 0);
+    write_chunks<T, E4M3, 0>(vu[i], vc, false, c, s, ok && has_v, p.cache.dim_v / 16, p.cache.v, p.cache.v_scale, at,
+                             p.cache.dim_v, slot == 0);
+  }
+}
+
+// Eight codes times their scale, rounded to T.
+template <typename T>
+__device__ __forceinline__ uint4 decode8(const uint2 codes, float scale) {
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t w = i ? codes.y : codes.x;
+    const uint32_t lo = e4m3x2_to_f16x2(w), hi = e4m3x2_hi_to_f16x2(w);
+    f[4 * i] = Elem<__half>::lo(lo) * scale;
+    f[4 * i + 1] = Elem<__half>::hi(lo) * scale;
+    f[4 * i + 2] = Elem<__half>::lo(hi) * scale;
+    f[4 * i + 3] = Elem<__half>::hi(hi) * scale;
+  }
+  return pack8<T>(f);
+}
+
+template <typename T, bool E4M3, int HEADS>
 __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CacheParams p) {
   check_offsets(p);
-  const CacheUnit u = cache_unit(p);
-  if (!u.live) return;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kCacheThreads + threadIdx.x;
+  const int slot = static_cast<int>(unit) & (p.slots - 1);
+  const int64_t row = unit / p.slots;
   int64_t pos, page;
   int slot_in_page;
-  if (!place_row(p, u.row, pos, page, slot_in_page)) return;
-  const int64_t at = cache_row(p.cache, page, u.head, slot_in_page);
-  T* out = static_cast<T*>(u.is_v ? p.v : p.k) + (u.row * p.cache.heads + u.head) * u.width + 16 * u.slot;
-  const void* base = u.is_v ? p.cache.v : p.cache.k;
-  uint4 u0, u1;
-  if (E4M3) {
-    const uint4 codes =
-        __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + at * u.width + 16 * u.slot));
-    const float scale = scale_value(__ldg((u.is_v ? p.cache.v_scale : p.cache.k_scale) + at));
-    const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-    float f[16];
+  if (!place_row(p, row, pos, page, slot_in_page)) return;
+  const int h0 = blockIdx.y * HEADS, heads = min(HEADS, p.cache.heads - h0);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t h = e4m3x2_to_f16x2(w[i / 2] >> (16 * (i & 1)));
-      f[2 * i] = Elem<__half>::lo(h) * scale;
-      f[2 * i + 1] = Elem<__half>::hi(h) * scale;
+  for (int part = 0; part < 2; ++part) {
+    const int width = part ? p.cache.dim_v : p.cache.dim;
+    if (16 * slot >= width) continue;
+    const SlotColumns k = slot_columns(slot, width, 0, false);
+    const void* base = part ? p.cache.v : p.cache.k;
+    const uint8_t* scales = part ? p.cache.v_scale : p.cache.k_scale;
+    T* out = static_cast<T*>(part ? p.v : p.k) + (row * p.cache.heads + h0) * width;
+    Chunks u[HEADS];
+    uint32_t byte[HEADS];
+#pragma unroll
+    for (int i = 0; i < HEADS; ++i) {
+      if (i >= heads) break;
+      const int64_t at = cache_row(p.cache, page, h0 + i, slot_in_page);
+      if (E4M3) {
+        const uint8_t* codes = static_cast<const uint8_t*>(base) + at * width;
+        const uint2 x = __ldg(reinterpret_cast<const uint2*>(codes + k.c0));
+        const uint2 y = __ldg(reinterpret_cast<const uint2*>(codes + k.c1));
+        u[i].a = make_uint4(x.x, x.y, y.x, y.y);
+        byte[i] = __ldg(scales + at);
+      } else {
+        u[i] = load_chunks(static_cast<const T*>(base) + at * width, k);
+      }
     }
-    u0 = make_uint4(Elem<T>::pack2(f[0], f[1]), Elem<T>::pack2(f[2], f[3]), Elem<T>::pack2(f[4], f[5]),
-                    Elem<T>::pack2(f[6], f[7]));
-    u1 = make_uint4(Elem<T>::pack2(f[8], f[9]), Elem<T>::pack2(f[10], f[11]), Elem<T>::pack2(f[12], f[13]),
-                    Elem<T>::pack2(f[14], f[15]));
-  } else {
-    const T* in = static_cast<const T*>(base) + at * u.width + 16 * u.slot;
-    u0 = __ldg(reinterpret_cast<const uint4*>(in));
-    u1 = __ldg(reinterpret_cast<const uint4*>(in) + 1);
+#pragma unroll
+    for (int i = 0; i < HEADS; ++i) {
+      if (i >= heads) break;
+      if (E4M3) {
+        const float scale = scale_value(byte[i]);
+        u[i].b = decode8<T>(make_uint2(u[i].a.z, u[i].a.w), scale);
+        u[i].a = decode8<T>(make_uint2(u[i].a.x, u[i].a.y), scale);
+      }
+      *reinterpret_cast<uint4*>(out + i * width + k.c0) = u[i].a;
+      *reinterpret_cast<uint4*>(out + i * width + k.c1) = u[i].b;
+    }
   }
-  *reinterpret_cast<uint4*>(out) = u0;
-  *reinterpret_cast<uint4*>(out + 8) = u1;
 }
 
 static hstu_status_t cache_common(const hstu_cache_t* cache, const int32_t* seq_offsets, int32_t batch, int64_t rows,
                                   const int32_t* starts, const int32_t* page_table, int32_t max_pages, void* ws,
-                                  size_t ws_bytes, CacheParams* p, int64_t* blocks) {
+                                  size_t ws_bytes, CacheParams* p, dim3* grid) {
   *p = CacheParams{};
   const hstu_status_t st = check_cache(cache, &p->cache);
   if (st != HSTU_OK) return st;
@@ -205,12 +240,13 @@ static hstu_status_t cache_common(const hstu_cache_t* cache, const int32_t* seq_
   if (!seq_offsets || !page_table || bad4(seq_offsets) || bad4(starts) || bad4(page_table))
     return HSTU_ERR_INVALID_ARG;
   if (ws && (reinterpret_cast<uintptr_t>(ws) % 256 != 0 || ws_bytes < kHdrWords * 4)) return HSTU_ERR_WORKSPACE;
-  const auto blocks_of = [&](int width) {
-    return (rows * p->cache.heads * (width / 16) + kCacheThreads - 1) / kCacheThreads;
-  };
-  p->k_blocks = blocks_of(p->cache.dim);
-  *blocks = p->k_blocks + blocks_of(p->cache.dim_v);
-  if (*blocks > INT32_MAX) return HSTU_ERR_UNSUPPORTED;
+  p->slots = (p->cache.dim > p->cache.dim_v ? p->cache.dim : p->cache.dim_v) / 16;
+  const int64_t blocks = (rows * p->slots + kCacheThreads - 1) / kCacheThreads;
+  // A thread for each head while that does not fill the GPU (152 SMs of four
+  // such blocks): the heads of a call with few rows are then moved at once.
+  p->one_head = blocks * p->cache.heads <= 152 * 4;
+  *grid = dim3(static_cast<unsigned>(blocks),
+               p->one_head ? p->cache.heads : (p->cache.heads + kCacheHeads - 1) / kCacheHeads);
   p->seq_offsets = seq_offsets;
   p->starts = starts;
   p->page_table = page_table;
@@ -225,23 +261,35 @@ static cudaError_t clear_header(void* ws, cudaStream_t stream) {
   return ws ? cudaMemsetAsync(ws, 0, kHdrWords * 4, stream) : cudaSuccess;
 }
 
+template <typename T, bool E4M3, int HEADS>
+static void launch_write(const CacheParams& p, dim3 grid, int rope, cudaStream_t stream) {
+  if (rope == 0) cache_write_kernel<T, E4M3, 0, HEADS><<<grid, kCacheThreads, 0, stream>>>(p);
+  else if (rope == 1) cache_write_kernel<T, E4M3, 1, HEADS><<<grid, kCacheThreads, 0, stream>>>(p);
+  else cache_write_kernel<T, E4M3, 2, HEADS><<<grid, kCacheThreads, 0, stream>>>(p);
+}
+
 template <typename T, bool E4M3>
-static void launch_write(const CacheParams& p, unsigned blocks, int rope, cudaStream_t stream) {
-  if (rope == 0) cache_write_kernel<T, E4M3, 0><<<blocks, kCacheThreads, 0, stream>>>(p);
-  else if (rope == 1) cache_write_kernel<T, E4M3, 1><<<blocks, kCacheThreads, 0, stream>>>(p);
-  else cache_write_kernel<T, E4M3, 2><<<blocks, kCacheThreads, 0, stream>>>(p);
+static void launch_write_heads(const CacheParams& p, dim3 grid, int rope, cudaStream_t stream) {
+  if (p.one_head) launch_write<T, E4M3, 1>(p, grid, rope, stream);
+  else launch_write<T, E4M3, kCacheHeads>(p, grid, rope, stream);
 }
 
 template <typename T>
-static void launch_write_typed(const CacheParams& p, unsigned blocks, bool e4m3, int rope, cudaStream_t stream) {
-  if (e4m3) launch_write<T, true>(p, blocks, rope, stream);
-  else launch_write<T, false>(p, blocks, rope, stream);
+static void launch_write_typed(const CacheParams& p, dim3 grid, bool e4m3, int rope, cudaStream_t stream) {
+  if (e4m3) launch_write_heads<T, true>(p, grid, rope, stream);
+  else launch_write_heads<T, false>(p, grid, rope, stream);
+}
+
+template <typename T, bool E4M3>
+static void launch_read_heads(const CacheParams& p, dim3 grid, cudaStream_t stream) {
+  if (p.one_head) cache_read_kernel<T, E4M3, 1><<<grid, kCacheThreads, 0, stream>>>(p);
+  else cache_read_kernel<T, E4M3, kCacheHeads><<<grid, kCacheThreads, 0, stream>>>(p);
 }
 
 template <typename T>
-static void launch_read_typed(const CacheParams& p, unsigned blocks, bool e4m3, cudaStream_t stream) {
-  if (e4m3) cache_read_kernel<T, true><<<blocks, kCacheThreads, 0, stream>>>(p);
-  else cache_read_kernel<T, false><<<blocks, kCacheThreads, 0, stream>>>(p);
+static void launch_read_typed(const CacheParams& p, dim3 grid, bool e4m3, cudaStream_t stream) {
+  if (e4m3) launch_read_heads<T, true>(p, grid, stream);
+  else launch_read_heads<T, false>(p, grid, stream);
 }
 
 }  // namespace hstu
@@ -254,9 +302,9 @@ HSTU_API hstu_status_t hstu_attn_cache_write(const hstu_cache_t* cache, const vo
                                              const int32_t* page_table, int32_t max_pages, const hstu_rope_t* rope,
                                              const int32_t* positions, void* ws, size_t ws_bytes, void* stream) {
   hstu::CacheParams p;
-  int64_t blocks = 0;
+  dim3 grid;
   hstu_status_t st =
-      hstu::cache_common(cache, seq_offsets, batch, rows, cache_lens, page_table, max_pages, ws, ws_bytes, &p, &blocks);
+      hstu::cache_common(cache, seq_offsets, batch, rows, cache_lens, page_table, max_pages, ws, ws_bytes, &p, &grid);
   if (st != HSTU_OK) return st;
   if (!cache_lens || reinterpret_cast<uintptr_t>(positions) % 4 != 0 || (positions && !rope))
     return HSTU_ERR_INVALID_ARG;
@@ -280,9 +328,9 @@ HSTU_API hstu_status_t hstu_attn_cache_write(const hstu_cache_t* cache, const vo
   if (rows == 0) return HSTU_OK;
   const int mode = rope ? (rope->interleaved ? 2 : 1) : 0;
   if (cache->dtype == HSTU_DTYPE_F16)
-    hstu::launch_write_typed<__half>(p, static_cast<unsigned>(blocks), cache->e4m3 != 0, mode, cs);
+    hstu::launch_write_typed<__half>(p, grid, cache->e4m3 != 0, mode, cs);
   else
-    hstu::launch_write_typed<__nv_bfloat16>(p, static_cast<unsigned>(blocks), cache->e4m3 != 0, mode, cs);
+    hstu::launch_write_typed<__nv_bfloat16>(p, grid, cache->e4m3 != 0, mode, cs);
   return cudaGetLastError() == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
 }
 
@@ -291,9 +339,9 @@ HSTU_API hstu_status_t hstu_attn_cache_read(const hstu_cache_t* cache, void* k, 
                                             const int32_t* page_table, int32_t max_pages, void* ws, size_t ws_bytes,
                                             void* stream) {
   hstu::CacheParams p;
-  int64_t blocks = 0;
+  dim3 grid;
   const hstu_status_t st =
-      hstu::cache_common(cache, seq_offsets, batch, rows, starts, page_table, max_pages, ws, ws_bytes, &p, &blocks);
+      hstu::cache_common(cache, seq_offsets, batch, rows, starts, page_table, max_pages, ws, ws_bytes, &p, &grid);
   if (st != HSTU_OK) return st;
   const auto bad = [](const void* q) { return !q || reinterpret_cast<uintptr_t>(q) % 16 != 0; };
   if (rows > 0 && (bad(k) || bad(v))) return HSTU_ERR_INVALID_ARG;
@@ -303,9 +351,9 @@ HSTU_API hstu_status_t hstu_attn_cache_read(const hstu_cache_t* cache, void* k, 
   if (hstu::clear_header(ws, cs) != cudaSuccess) return HSTU_ERR_CUDA;
   if (rows == 0) return HSTU_OK;
   if (cache->dtype == HSTU_DTYPE_F16)
-    hstu::launch_read_typed<__half>(p, static_cast<unsigned>(blocks), cache->e4m3 != 0, cs);
+    hstu::launch_read_typed<__half>(p, grid, cache->e4m3 != 0, cs);
   else
-    hstu::launch_read_typed<__nv_bfloat16>(p, static_cast<unsigned>(blocks), cache->e4m3 != 0, cs);
+    hstu::launch_read_typed<__nv_bfloat16>(p, grid, cache->e4m3 != 0, cs);
   return cudaGetLastError() == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
 }
 

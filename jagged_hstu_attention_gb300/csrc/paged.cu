@@ -75,7 +75,8 @@ HSTU_API hstu_status_t hstu_attn_fwd_paged(const void* q_c, int64_t q_stride, vo
                              reinterpret_cast<uintptr_t>(o_c) % 16 != 0))
     return HSTU_ERR_INVALID_ARG;
   const hstu::PagedLayout l = hstu::paged_layout(p.cache, batch, num_candidates, max_seqlen);
-  if (!ws || reinterpret_cast<uintptr_t>(ws) % 256 != 0 || ws_bytes < l.total) return HSTU_ERR_WORKSPACE;
+  if (!ws && l.nsplit > 1) return HSTU_ERR_WORKSPACE;
+  if (ws && (reinterpret_cast<uintptr_t>(ws) % 256 != 0 || ws_bytes < l.total)) return HSTU_ERR_WORKSPACE;
   uint8_t* base = static_cast<uint8_t*>(ws);
   p.q = q_c;
   p.o = o_c;
@@ -98,7 +99,7 @@ HSTU_API hstu_status_t hstu_attn_fwd_paged(const void* q_c, int64_t q_stride, vo
   p.inv_n = 1.0f / static_cast<float>(max_seqlen);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   // The error word and the counters start at zero.
-  if (cudaMemsetAsync(ws, 0, l.counters + l.counter_bytes, cs) != cudaSuccess) return HSTU_ERR_CUDA;
+  if (ws && cudaMemsetAsync(ws, 0, l.counters + l.counter_bytes, cs) != cudaSuccess) return HSTU_ERR_CUDA;
   const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(batch) * p.cache.heads * l.nsplit);
   const bool half = cache->dtype == HSTU_DTYPE_F16;
   cudaError_t e;

@@ -67,7 +67,7 @@ struct PagedParams {
   const int32_t* cand_offsets;  // null: candidate b belongs to sequence b
   const int32_t* func;          // null: everything cached is visible
   float* partial;
-  int32_t* header;
+  int32_t* header;    // null: bad sequences are not reported
   int32_t* counters;  // (batch, heads), zero at launch
   int32_t batch, max_pages, num_cand, nfunc, max_seqlen;
   int32_t split, nsplit;  // keys of a split; splits of max_seqlen
@@ -682,7 +682,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedSizes<DQ, DV, E4M3, MANY>:
   ok = ok && len >= 0 && len <= p.max_seqlen &&
        static_cast<int64_t>(len) <= (static_cast<int64_t>(p.max_pages) << p.cache.page_shift);
   if (!ok) {
-    if (split == 0 && h == 0 && tid == 0) atomicOr(p.header + kHdrErr, kErrInput);
+    if (p.header && split == 0 && h == 0 && tid == 0) atomicOr(p.header + kHdrErr, kErrInput);
     return;
   }
   if (cb == ce) return;
@@ -700,7 +700,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedSizes<DQ, DV, E4M3, MANY>:
     }
   }
   const bool bad = __syncthreads_or(bad_page) != 0;
-  if (bad && tid == 0) atomicOr(p.header + kHdrErr, kErrInput);
+  if (bad && p.header && tid == 0) atomicOr(p.header + kHdrErr, kErrInput);
 
   float* red = reinterpret_cast<float*>(ring);
   PagedSplit sp;

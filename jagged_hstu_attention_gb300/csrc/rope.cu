@@ -13,7 +13,7 @@
 namespace hstu {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeHeads = 4;  // heads a thread takes when there are enough tokens
+constexpr int kRopeHeads = 4;  // heads of a thread where there are tokens enough to fill the GPU
 
 struct RopeParams {
   const void* in[2];
@@ -33,11 +33,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
   const int64_t token = unit / kSlots;
   const int slot = static_cast<int>(unit % kSlots);
   if (token >= p.tokens) return;
-  const bool turned = 16 * slot < p.rotary;
-  int c0, c1;
-  slot_columns(slot, p.rotary, INTERLEAVED, c0, c1);
+  const SlotColumns k = slot_columns(slot, D, p.rotary, INTERLEAVED);
   float c[8], s[8];
-  if (turned) rope_factors(p.turns, 8 * slot, p.positions[token], p.magnitude, p.sign, c, s);
+  if (k.turned) rope_factors(p.turns, k.first, k.second, p.positions[token], p.magnitude, p.sign, c, s);
   const int h0 = blockIdx.y * HPT;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
@@ -48,13 +46,13 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
 #pragma unroll
     for (int i = 0; i < HPT; ++i) {
       if (h0 + i >= p.heads) break;
-      u0[i] = *reinterpret_cast<const uint4*>(in + (h0 + i) * D + c0);
-      u1[i] = *reinterpret_cast<const uint4*>(in + (h0 + i) * D + c1);
+      u0[i] = *reinterpret_cast<const uint4*>(in + (h0 + i) * D + k.c0);
+      u1[i] = *reinterpret_cast<const uint4*>(in + (h0 + i) * D + k.c1);
     }
 #pragma unroll
     for (int i = 0; i < HPT; ++i) {
       if (h0 + i >= p.heads) break;
-      if (turned) {
+      if (k.turned) {
         float a[8], b[8];
         unpack8<T>(u0[i], a);
         unpack8<T>(u1[i], b);
@@ -62,8 +60,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
         u0[i] = pack8<T>(a);
         u1[i] = pack8<T>(b);
       }
-      *reinterpret_cast<uint4*>(out + (h0 + i) * D + c0) = u0[i];
-      *reinterpret_cast<uint4*>(out + (h0 + i) * D + c1) = u1[i];
+      *reinterpret_cast<uint4*>(out + (h0 + i) * D + k.c0) = u0[i];
+      *reinterpret_cast<uint4*>(out + (h0 + i) * D + k.c1) = u1[i];
     }
   }
 }
@@ -79,6 +77,10 @@ static cudaError_t launch_rope(const RopeParams& p, bool interleaved, cudaStream
 
 template <typename T, int D>
 static cudaError_t launch_rope_heads(const RopeParams& p, bool interleaved, cudaStream_t stream) {
+  // A thread for each head while that does not fill the GPU (152 SMs of four
+  // such blocks).
+  const int64_t blocks = (p.tokens * (D / 16) + kRopeThreads - 1) / kRopeThreads;
+  if (blocks * p.heads <= 152 * 4) return launch_rope<T, D, 1>(p, interleaved, stream);
   return launch_rope<T, D, kRopeHeads>(p, interleaved, stream);
 }
 

@@ -31,14 +31,15 @@ __device__ __forceinline__ void phase_cos_sin(uint32_t phase, float& c, float& s
   s = (quarter & 2u) ? -b : b;
 }
 
-// m cos and m sin of the 8 pairs from `first` on at position pos; sign = -1
-// for the transposed rotation. pos * turns wraps modulo one turn in 64-bit
-// integers, so the phase is exact at any position, negative ones included.
-__device__ __forceinline__ void rope_factors(const uint64_t* __restrict__ turns, int first, int64_t pos, float magnitude,
-                                             float sign, float (&c)[8], float (&s)[8]) {
+// m cos and m sin of pairs first .. first + 3 and second .. second + 3 at
+// position pos; sign = -1 for the transposed rotation. pos * turns wraps modulo
+// one turn in 64-bit integers, so the phase is exact at any position, negative
+// ones included.
+__device__ __forceinline__ void rope_factors(const uint64_t* __restrict__ turns, int first, int second, int64_t pos,
+                                             float magnitude, float sign, float (&c)[8], float (&s)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const uint64_t phase = static_cast<uint64_t>(pos) * __ldg(turns + first + i);
+    const uint64_t phase = static_cast<uint64_t>(pos) * __ldg(turns + (i < 4 ? first + i : second + i - 4));
     phase_cos_sin(static_cast<uint32_t>(phase >> 32), c[i], s[i]);
     c[i] *= magnitude;
     s[i] *= magnitude * sign;
@@ -59,15 +60,25 @@ __device__ __forceinline__ void rotate_pairs(float (&a)[8], float (&b)[8], const
   }
 }
 
-// Columns of the two 8-column chunks of slot j of a row: slots below R/16
-// hold 8 pairs, the others 16 columns that are copied.
-__device__ __forceinline__ void slot_columns(int j, int rotary, bool interleaved, int& c0, int& c1) {
-  c0 = 16 * j;
-  c1 = c0 + 8;
-  if (!interleaved && 16 * j < rotary) {
-    c0 = 8 * j;
-    c1 = rotary / 2 + 8 * j;
-  }
+// A row of `width` columns, the first `rotary` of them rotated, is dealt to
+// width / 16 slots of two 8-column chunks: those of the rotated columns first.
+// The chunks lie half of their part apart, so that the slots' neighbouring
+// 16-byte loads and stores fill whole sectors, and the half layout finds both
+// members of its pairs.
+struct SlotColumns {
+  int c0, c1;         // columns of the chunks
+  int first, second;  // pairs of the factors (rotated slots)
+  bool turned;
+};
+__device__ __forceinline__ SlotColumns slot_columns(int slot, int width, int rotary, bool interleaved) {
+  SlotColumns k;
+  k.turned = 16 * slot < rotary;
+  const int base = k.turned ? 0 : rotary, part = k.turned ? rotary : width - rotary;
+  k.c0 = base + 8 * (slot - base / 16);
+  k.c1 = k.c0 + part / 2;
+  k.first = interleaved ? k.c0 / 2 : k.c0;
+  k.second = interleaved ? k.c1 / 2 : k.c0 + 4;
+  return k;
 }
 
 template <typename T>
