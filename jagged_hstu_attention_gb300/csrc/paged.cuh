@@ -96,15 +96,20 @@ __device__ __forceinline__ void mma16816<__half>(float (&d)[4], uint32_t a0, uin
 
 // B bytes (16, 8 or 4) of a lane's piece, from shared memory.
 template <int B>
-__device__ __forceinline__ void load_piece(uint32_t addr, uint32_t* w) {
-  if (B == 16)
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                 : "r"(addr));
-  else if (B == 8)
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
-  else
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+__device__ __forceinline__ void load_piece(const uint8_t* p, uint32_t* w) {
+  if (B == 16) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    w[0] = u.x;
+    w[1] = u.y;
+    w[2] = u.z;
+    w[3] = u.w;
+  } else if (B == 8) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    w[0] = u.x;
+    w[1] = u.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
 }
 
 // Asynchronous copy of 16 bytes; zeros where not live (src is not read then).
@@ -164,6 +169,8 @@ struct PagedSizes {
   static constexpr int kResident = kFit < 1 ? 1 : (kFit > (MANY ? 3 : 4) ? (MANY ? 3 : 4) : kFit);
   static __device__ __forceinline__ int red_column(int d) { return d / VE * kBlock + d % VE; }
 };
+
+extern __shared__ __align__(128) uint8_t paged_ring[];
 
 // What a CTA's passes share.
 struct PagedSplit {
@@ -284,7 +291,7 @@ __device__ __noinline__ void paged_scalar_sum(const PagedParams& p, const PagedS
 // 8 x 8 16-bit values, row g columns 2t, 2t+1 in lane (g, t), transposed.
 __device__ __forceinline__ uint32_t transpose8(uint32_t w) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(w));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(w));
   return r;
 }
 
@@ -428,8 +435,8 @@ __device__ __forceinline__ int paged_pass(const PagedParams& p, const PagedSplit
     for (int j = 0; j < wg; ++j) {
       const int entry = (n0 * nslices + slice) * wg + j;
       if (entry >= entries || ncand == 0) break;
-      const uint32_t kt = ring + (stage * wg + j) * Z::kStep;
-      const uint32_t vt = kt + kPagedTile * KROW;
+      const uint8_t* kt = paged_ring + (slice * S * wg + stage * wg + j) * Z::kStep;
+      const uint8_t* vt = kt + kPagedTile * KROW;
 
       // Scores of keys g (values 0, 1 of a group) and g + 8 (2, 3), two sums
       // each, halves of a dependent chain.
@@ -476,11 +483,8 @@ __device__ __forceinline__ int paged_pass(const PagedParams& p, const PagedSplit
       if (E4M3) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          uint32_t u, v;
-          asm volatile("ld.shared.u8 %0, [%1];" : "=r"(u) : "r"(vt + kPagedTile * VROW + g + 8 * r));
-          asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(vt + kPagedTile * VROW + 16 + g + 8 * r));
-          ks[r] = scale_value(u);
-          vs[r] = scale_value(v);
+          ks[r] = scale_value(vt[kPagedTile * VROW + g + 8 * r]);
+          vs[r] = scale_value(vt[kPagedTile * VROW + 16 + g + 8 * r]);
         }
       }
       float pr[NC][2];
@@ -643,7 +647,6 @@ template <typename T, int DQ, int DV, bool E4M3, bool MANY>
 __global__ void __launch_bounds__(kPagedThreads, PagedSizes<DQ, DV, E4M3, MANY>::kResident)
     paged_kernel(const PagedParams p) {
   using Z = PagedSizes<DQ, DV, E4M3, MANY>;
-  extern __shared__ __align__(128) uint8_t ring[];
   __shared__ int pages[kPagedMaxSplit / kPagedTile];
   __shared__ uint32_t bits[2 * kPagedWords];
   __shared__ uint16_t list[kPagedMaxSplit / kPagedTile];
@@ -702,7 +705,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedSizes<DQ, DV, E4M3, MANY>:
   const bool bad = __syncthreads_or(bad_page) != 0;
   if (bad && p.header && tid == 0) atomicOr(p.header + kHdrErr, kErrInput);
 
-  float* red = reinterpret_cast<float*>(ring);
+  float* red = reinterpret_cast<float*>(paged_ring);
   PagedSplit sp;
   sp.h = h;
   sp.k0 = k0;
@@ -716,7 +719,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedSizes<DQ, DV, E4M3, MANY>:
   sp.list = list;
   sp.iv = iv;
   sp.entries = &sh_entries;
-  sp.ring = smem_u32(ring);
+  sp.ring = smem_u32(paged_ring);
   sp.red = red;
   for (int c0 = cb; c0 < ce;) {
     sp.c0 = c0;
