@@ -104,12 +104,15 @@ typedef struct {
 #define HSTU_WS_FULL 0    /* plan + hstu_attn_fwd + hstu_attn_bwd */
 #define HSTU_WS_TARGETS 1 /* hstu_attn_{fwd,bwd}_targets_only */
 
-/* Flags for hstu_attn_fwd / hstu_attn_bwd. */
+/* Flags for hstu_attn_fwd / hstu_attn_bwd / hstu_attn_fwd_paged. */
 #define HSTU_FLAG_NONE 0
 /* The workspace already holds the plan that hstu_attn_plan (or an earlier
  * fwd/bwd call without this flag) built for the same seq_offsets, func and
  * shape; skip rebuilding it. The caller guarantees that none changed. */
 #define HSTU_FLAG_REUSE_PLAN 1
+/* hstu_attn_fwd_paged: the error word of ws is neither cleared nor set, which
+ * saves a launch. Bad sequences are left out as without the flag. */
+#define HSTU_FLAG_NO_STATUS 2
 
 /* 1 if the library has kernels for that nfunc (1, 3, 5, 7, 9), else 0. The pages'
  * wheel bakes NFUNC in at compile time (TorchEasyRec PR #670 review thread on
@@ -460,8 +463,9 @@ HSTU_API size_t hstu_attn_paged_workspace_size(const hstu_cache_t* cache, int32_
  *   max_seqlen   N, 1 .. 2^24 (the pages take longer histories than the
  *            contiguous kernels)
  *   ws       hstu_attn_paged_workspace_size() bytes, 256-byte aligned; NULL is
- *            taken where that size is 256 (one split: nothing but the error
- *            word), and bad sequences are then not reported
+ *            taken with HSTU_FLAG_NO_STATUS where that size is 256 (one split:
+ *            nothing but the error word)
+ *   flags    HSTU_FLAG_NONE or HSTU_FLAG_NO_STATUS
  * Slots past a sequence's length and positions that a candidate does not see
  * do not reach it, whatever they hold (NaN and infinities too). A candidate
  * that sees nothing gets 0. The cache's length is split over CTAs, whose sums
@@ -472,7 +476,7 @@ HSTU_API hstu_status_t hstu_attn_fwd_paged(const void* q_c, int64_t q_stride, vo
                                            const int32_t* cache_lens, int32_t batch, const int32_t* page_table,
                                            int32_t max_pages, const int32_t* cand_offsets, int64_t num_candidates,
                                            const int32_t* func_c, int32_t nfunc, int32_t max_seqlen, float alpha,
-                                           void* ws, size_t ws_bytes, void* stream);
+                                           void* ws, size_t ws_bytes, uint32_t flags, void* stream);
 
 /* Synchronises the stream, then returns the status recorded in the
  * workspace error word (HSTU_OK, HSTU_ERR_DEVICE_INPUT, HSTU_ERR_TIMEOUT,

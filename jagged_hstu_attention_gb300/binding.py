@@ -28,6 +28,7 @@ STATUS_NAMES = {
 WS_FULL = 0
 WS_TARGETS = 1
 FLAG_REUSE_PLAN = 1
+FLAG_NO_STATUS = 2
 
 EXPORTED = (
     "hstu_attn_nfunc_supported", "hstu_attn_workspace_size", "hstu_attn_plan", "hstu_attn_fwd",
@@ -168,7 +169,7 @@ def load(path: str = None) -> ctypes.CDLL:
         "hstu_attn_cache_read": (ctypes.c_int, [vp, vp, vp, vp, i32, i64, vp, vp, i32, vp, sz, vp]),
         "hstu_attn_paged_workspace_size": (sz, [vp, i32, i64, i32]),
         "hstu_attn_fwd_paged": (ctypes.c_int, [vp, i64, vp, vp, vp, i32, vp, i32, vp, i64, vp, i32, i32,
-                                               ctypes.c_float, vp, sz, vp]),
+                                               ctypes.c_float, vp, sz, u32, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -816,15 +817,17 @@ def fwd_paged(q_c, cache: PagedCache, cache_lens, page_table, max_seqlen: int, a
         if out.shape[0] != C or not out.is_contiguous():
             raise ValueError(f"out must be contiguous and have {C} rows")
     lib = load()
-    own_ws = None
+    own_ws, flags = None, 0
     if ws is None:
+        flags = FLAG_NO_STATUS  # nobody could read it
         n = lib.hstu_attn_paged_workspace_size(cache._addr, B, C, max_seqlen)
         if n > 256:  # sums of splits; without them nothing but the error word
             own_ws = ws = torch.empty(n, dtype=torch.uint8, device=cache.device)
     st = lib.hstu_attn_fwd_paged(q_c.data_ptr(), qs, out.data_ptr(), cache._addr,
                                  _ints(cache_lens, (B,), index, "cache_lens"), B, table, width,
                                  0 if cand_offsets is None else _ints(cand_offsets, (B + 1,), index, "cand_offsets"),
-                                 C, func, nfunc, max_seqlen, alpha, *_ws_args(ws, index), _raw_stream(stream, index))
+                                 C, func, nfunc, max_seqlen, alpha, *_ws_args(ws, index), flags,
+                                 _raw_stream(stream, index))
     if st != HSTU_OK:
         _check(st, "hstu_attn_fwd_paged")
     if own_ws is not None and stream is not None:

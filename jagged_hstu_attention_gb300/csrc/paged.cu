@@ -18,18 +18,15 @@ static int paged_split(int batch, int heads, int max_seqlen) {
 
 struct PagedLayout {
   int split = 0, nsplit = 0;
-  size_t counters = 0, counter_bytes = 0, partial = 0, total = 0;
+  size_t states = 0, partial = 0, total = 0;
 };
 static PagedLayout paged_layout(const CacheView& c, int batch, int64_t num_cand, int max_seqlen) {
   PagedLayout l;
   l.split = paged_split(batch, c.heads, max_seqlen);
   l.nsplit = (max_seqlen + l.split - 1) / l.split;
-  l.counters = kHdrWords * 4;
-  l.partial = l.counters;
-  l.total = l.partial;
+  l.states = l.partial = l.total = kHdrWords * 4;
   if (l.nsplit > 1) {
-    l.counter_bytes = static_cast<size_t>(batch) * c.heads * 4;
-    l.partial = l.counters + align_up(l.counter_bytes, 256);
+    l.partial = l.states + align_up(static_cast<size_t>(batch) * c.heads * l.nsplit * 4, 256);
     l.total = l.partial + align_up(static_cast<size_t>(num_cand) * c.heads * l.nsplit * c.dim_v * 4, 256);
   }
   return l;
@@ -43,7 +40,7 @@ static hstu_status_t check_paged(const hstu_cache_t* cache, int32_t batch, int64
   if (max_seqlen > (1 << 24)) return HSTU_ERR_UNSUPPORTED;
   const PagedLayout l = paged_layout(*view, batch, num_cand, max_seqlen);
   const int64_t bh = static_cast<int64_t>(batch) * view->heads;
-  if (bh > INT32_MAX / l.nsplit) return HSTU_ERR_UNSUPPORTED;  // CTAs of a launch
+  if (bh > INT32_MAX / l.nsplit || num_cand * view->heads > INT32_MAX) return HSTU_ERR_UNSUPPORTED;  // CTAs of a launch
   return HSTU_OK;
 }
 
@@ -62,7 +59,7 @@ HSTU_API hstu_status_t hstu_attn_fwd_paged(const void* q_c, int64_t q_stride, vo
                                            const int32_t* cache_lens, int32_t batch, const int32_t* page_table,
                                            int32_t max_pages, const int32_t* cand_offsets, int64_t num_candidates,
                                            const int32_t* func_c, int32_t nfunc, int32_t max_seqlen, float alpha,
-                                           void* ws, size_t ws_bytes, void* stream) {
+                                           void* ws, size_t ws_bytes, uint32_t flags, void* stream) {
   hstu::PagedParams p{};
   const hstu_status_t st = hstu::check_paged(cache, batch, num_candidates, max_seqlen, &p.cache);
   if (st != HSTU_OK) return st;
@@ -75,7 +72,8 @@ HSTU_API hstu_status_t hstu_attn_fwd_paged(const void* q_c, int64_t q_stride, vo
                              reinterpret_cast<uintptr_t>(o_c) % 16 != 0))
     return HSTU_ERR_INVALID_ARG;
   const hstu::PagedLayout l = hstu::paged_layout(p.cache, batch, num_candidates, max_seqlen);
-  if (!ws && l.nsplit > 1) return HSTU_ERR_WORKSPACE;
+  const bool report = !(flags & HSTU_FLAG_NO_STATUS);
+  if (!ws && (l.nsplit > 1 || report)) return HSTU_ERR_WORKSPACE;
   if (ws && (reinterpret_cast<uintptr_t>(ws) % 256 != 0 || ws_bytes < l.total)) return HSTU_ERR_WORKSPACE;
   uint8_t* base = static_cast<uint8_t*>(ws);
   p.q = q_c;
@@ -86,8 +84,8 @@ HSTU_API hstu_status_t hstu_attn_fwd_paged(const void* q_c, int64_t q_stride, vo
   p.cand_offsets = cand_offsets;
   p.func = func_c;
   p.partial = reinterpret_cast<float*>(base + l.partial);
-  p.header = reinterpret_cast<int32_t*>(base);
-  p.counters = reinterpret_cast<int32_t*>(base + l.counters);
+  p.header = report ? reinterpret_cast<int32_t*>(base) : nullptr;
+  p.states = reinterpret_cast<int32_t*>(base + l.states);
   p.batch = batch;
   p.max_pages = max_pages;
   p.num_cand = static_cast<int32_t>(num_candidates);
@@ -98,8 +96,7 @@ HSTU_API hstu_status_t hstu_attn_fwd_paged(const void* q_c, int64_t q_stride, vo
   p.alpha = alpha;
   p.inv_n = 1.0f / static_cast<float>(max_seqlen);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  // The error word and the counters start at zero.
-  if (ws && cudaMemsetAsync(ws, 0, l.counters + l.counter_bytes, cs) != cudaSuccess) return HSTU_ERR_CUDA;
+  if (report && cudaMemsetAsync(ws, 0, hstu::kHdrWords * 4, cs) != cudaSuccess) return HSTU_ERR_CUDA;
   const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(batch) * p.cache.heads * l.nsplit);
   const bool half = cache->dtype == HSTU_DTYPE_F16;
   cudaError_t e;

@@ -68,7 +68,7 @@ struct PagedParams {
   const int32_t* func;          // null: everything cached is visible
   float* partial;
   int32_t* header;    // null: bad sequences are not reported
-  int32_t* counters;  // (batch, heads), zero at launch
+  int32_t* states;    // (batch, heads, nsplit): 1 where a split's sums are good
   int32_t batch, max_pages, num_cand, nfunc, max_seqlen;
   int32_t split, nsplit;  // keys of a split; splits of max_seqlen
   float alpha, inv_n;
@@ -192,35 +192,34 @@ __device__ __forceinline__ int paged_list(const PagedParams& p, const PagedSplit
   const int tid = threadIdx.x, lane = tid & 31;
   if (tid < 2 * kPagedWords) sp.bits[tid] = 0;
   __syncthreads();
+  const int words = (sp.tiles + 31) / 32, n = (p.nfunc + 1) / 2;
   if (tid < ncand) {
     int lo[kMaxIntervals], hi[kMaxIntervals];
-    load_row_intervals<kMaxIntervals>(p.func, p.num_cand, sp.c0 + tid, sp.len, true, lo, hi,
-                                      (1u << ((p.nfunc + 1) / 2)) - 1u);
-    uint32_t whole[kPagedWords];
+    load_row_intervals<kMaxIntervals>(p.func, p.num_cand, sp.c0 + tid, sp.len, true, lo, hi, (1u << n) - 1u);
+    for (int w = 0; w < words; ++w) {
+      const int base = sp.k0 + w * 32 * kPagedTile;
+      const auto span = [](int x, int y) {  // bits [x, y), cut to the word
+        const int u = max(x, 0), v = min(y, 32);
+        return u >= v ? 0u : (0xffffffffu << u) & (0xffffffffu >> (32 - v));
+      };
+      uint32_t seen = 0, whole = 0;
 #pragma unroll
-    for (int w = 0; w < kPagedWords; ++w) whole[w] = 0;
-#pragma unroll
-    for (int i = 0; i < kMaxIntervals; ++i) {
-      sp.iv[tid * kPagedIv + 2 * i] = lo[i];
-      sp.iv[tid * kPagedIv + 2 * i + 1] = hi[i];
-      const int a = max(lo[i], sp.k0) - sp.k0, e = min(hi[i], sp.k1) - sp.k0;
-      if (e <= a) continue;
-      const int first = a / kPagedTile, last = (e - 1) / kPagedTile;              // tiles it touches
-      const int wfirst = (a + kPagedTile - 1) / kPagedTile, wlast = e / kPagedTile - 1;  // and covers
-#pragma unroll
-      for (int w = 0; w < kPagedWords; ++w) {
-        const auto span = [w](int x, int y) {  // bits of word w in [x, y]
-          const int u = max(x - 32 * w, 0), v = min(y - 32 * w, 31);
-          return u > v ? 0u : (0xffffffffu << u) & (0xffffffffu >> (31 - v));
-        };
-        const uint32_t seen = span(first, last);
-        if (seen) atomicOr(sp.bits + w, seen);
-        whole[w] |= span(wfirst, wlast);
+      for (int i = 0; i < kMaxIntervals; ++i) {
+        if (i >= n) break;
+        const int a = max(lo[i], sp.k0) - base, e = min(hi[i], sp.k1) - base;  // in keys of this word's first tile
+        if (e <= a) continue;
+        seen |= span(a >> 4, (e + kPagedTile - 1) >> 4);   // the tiles it touches
+        whole |= span((a + kPagedTile - 1) >> 4, e >> 4);  // and covers
       }
+      if (seen) atomicOr(sp.bits + w, seen);
+      if (~whole) atomicOr(sp.bits + kPagedWords + w, ~whole);
     }
 #pragma unroll
-    for (int w = 0; w < kPagedWords; ++w)
-      if (~whole[w]) atomicOr(sp.bits + kPagedWords + w, ~whole[w]);
+    for (int i = 0; i < kMaxIntervals; ++i) {
+      if (i >= n) break;
+      sp.iv[tid * kPagedIv + 2 * i] = lo[i];
+      sp.iv[tid * kPagedIv + 2 * i + 1] = hi[i];
+    }
   }
   __syncthreads();
   if (tid < 32) {
@@ -651,9 +650,10 @@ __global__ void __launch_bounds__(kPagedThreads, PagedSizes<DQ, DV, E4M3, MANY>:
   __shared__ uint32_t bits[2 * kPagedWords];
   __shared__ uint16_t list[kPagedMaxSplit / kPagedTile];
   __shared__ int iv[(MANY ? kPagedPass : 1) * kPagedIv];
-  __shared__ int sh_entries, sh_seen;
+  __shared__ int sh_entries;
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x;
   const int64_t bid = blockIdx.x;
   const int split = static_cast<int>(bid % p.nsplit);
   const int bh = static_cast<int>(bid / p.nsplit);
@@ -732,81 +732,89 @@ __global__ void __launch_bounds__(kPagedThreads, PagedSizes<DQ, DV, E4M3, MANY>:
       rows = 16;
     }
     __syncthreads();
-    // The slices' sums in slice order.
+    // The slices' sums in slice order, four columns a thread.
     const int taken = min(ce - c0, wg * rows);
-    for (int i = tid; i < taken * DV; i += kPagedThreads) {
-      const int r = i / DV, d = i % DV;
+    for (int i = tid; i < taken * (DV / 4); i += kPagedThreads) {
+      const int r = i / (DV / 4), d = i % (DV / 4) * 4;
       const float* from = red + r * Z::kRedRow + Z::red_column(d);  // warp r / rows of each slice
-      float sum = from[0];
-      for (int w = wg; w < kPagedWarps; w += wg) sum += from[w * rows * Z::kRedRow];
-      const int64_t at = static_cast<int64_t>(c0 + r) * p.cache.heads + h;
-      if (splits > 1) {
-        p.partial[(at * p.nsplit + split) * DV + d] = sum;
-      } else if (!bad) {
-        const uint32_t w = Elem<T>::pack2(sum * p.inv_n, 0.0f);
-        static_cast<T*>(p.o)[at * DV + d] = *reinterpret_cast<const T*>(&w);
+      float sum[4] = {from[0], from[1], from[2], from[3]};
+      for (int w = wg; w < kPagedWarps; w += wg) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e] += from[w * rows * Z::kRedRow + e];
       }
+      const int64_t at = static_cast<int64_t>(c0 + r) * p.cache.heads + h;
+      if (splits > 1)
+        *reinterpret_cast<float4*>(p.partial + (at * p.nsplit + split) * DV + d) =
+            make_float4(sum[0], sum[1], sum[2], sum[3]);
+      else if (!bad)
+        *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + at * DV + d) =
+            make_uint2(Elem<T>::pack2(sum[0] * p.inv_n, sum[1] * p.inv_n),
+                       Elem<T>::pack2(sum[2] * p.inv_n, sum[3] * p.inv_n));
     }
     __syncthreads();
     c0 += taken;
   }
-  if (splits == 1) return;
+  if (splits > 1 && tid == 0) p.states[static_cast<int64_t>(bh) * p.nsplit + split] = bad ? 0 : 1;
+}
 
-  // The last CTA of this (sequence, head) to arrive joins the splits' sums in
-  // a fixed order. A split with a bad page marks the counter, and nothing is
-  // written then.
-  __threadfence();
-  __syncthreads();
-  if (tid == 0) sh_seen = atomicAdd(p.counters + bh, bad ? 1 + (1 << 20) : 1) + (bad ? 1 << 20 : 0);
-  __syncthreads();
-  const int seen = sh_seen;
-  if ((seen & 0xfffff) != splits - 1 || seen >> 20 != 0) return;
-  __threadfence();
-  const auto at_of = [&](int c) { return (static_cast<int64_t>(c) * p.cache.heads + h); };
-  if (ce - cb < kPagedWarps) {
-    // Few candidates, many splits: a quarter of the splits for each warp, then
-    // the quarters.
-    const int quarter = (splits + kPagedWarps - 1) / kPagedWarps;
-    for (int c = cb; c < ce; ++c) {
-      const float* from = p.partial + at_of(c) * p.nsplit * DV;
-      float sum[DV / 32];
-#pragma unroll
-      for (int i = 0; i < DV / 32; ++i) sum[i] = 0.0f;
-#pragma unroll 8
-      for (int s = warp * quarter; s < min(splits, (warp + 1) * quarter); ++s)
-#pragma unroll
-        for (int i = 0; i < DV / 32; ++i) sum[i] += __ldcg(from + s * DV + 32 * i + lane);
-#pragma unroll
-      for (int i = 0; i < DV / 32; ++i) red[warp * DV + 32 * i + lane] = sum[i];
-      __syncthreads();
-      for (int d = tid; d < DV; d += kPagedThreads) {
-        float all = red[d];
-#pragma unroll
-        for (int w = 1; w < kPagedWarps; ++w) all += red[w * DV + d];
-        const uint32_t w = Elem<T>::pack2(all * p.inv_n, 0.0f);
-        static_cast<T*>(p.o)[at_of(c) * DV + d] = *reinterpret_cast<const T*>(&w);
-      }
-      __syncthreads();
-    }
-    return;
+// Joins the splits' sums of each (candidate, head), in a fixed order: WARPS
+// warps take a share of the splits each, and their sums are added in warp
+// order. Its blocks start while the last CTAs of paged_kernel run and wait for
+// them. A sequence with one split was written there, and one with a bad split
+// is left alone.
+template <typename T, int DV, int WARPS>
+__global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int kUnits = 8 / WARPS;  // (candidate, head) of a block
+  __shared__ float4 red[8][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kUnits + warp / WARPS;
+  const int64_t c = unit / p.cache.heads;
+  const int h = static_cast<int>(unit - c * p.cache.heads);
+  bool live = c < p.num_cand;
+  int b = static_cast<int>(c), first;
+  if (p.cand_offsets) {  // lanes of a warp ask for the same candidate
+    live = find_sequence(p.cand_offsets, p.batch, live ? c : 0, b, first) && live && p.cand_offsets[0] == 0 &&
+           p.cand_offsets[p.batch] == p.num_cand && p.cand_offsets[b + 1] <= p.num_cand;  // as paged_kernel has it
   }
-  // Many candidates: four columns of one for each thread.
-#pragma unroll 4
-  for (int i = tid; i < (ce - cb) * (DV / 4); i += kPagedThreads) {
-    const int64_t at = at_of(cb + i / (DV / 4));
-    const int d = i % (DV / 4) * 4;
-    const float* from = p.partial + at * p.nsplit * DV + d;
-    float4 sum = __ldcg(reinterpret_cast<const float4*>(from));
-    for (int s = 1; s < splits; ++s) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(from + s * DV));
+  const int len = live ? p.lens[b] : 0;
+  live = live && len > p.split && len <= p.max_seqlen &&
+         static_cast<int64_t>(len) <= (static_cast<int64_t>(p.max_pages) << p.cache.page_shift);
+  const int splits = live ? (len + p.split - 1) / p.split : 0;
+  const int32_t* states = p.states + (static_cast<int64_t>(b) * p.cache.heads + h) * p.nsplit;
+  bool good = true;
+  for (int s = lane; s < splits; s += 32) good = good && states[s] == 1;
+  live = __all_sync(0xffffffffu, good) && live;
+
+  const int share = (splits + WARPS - 1) / WARPS, s0 = warp % WARPS * share, s1 = min(splits, s0 + share);
+  float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (live && lane < DV / 4) {
+    const float4* from = reinterpret_cast<const float4*>(p.partial + unit * p.nsplit * DV) + lane;
+#pragma unroll 8
+    for (int s = s0; s < s1; ++s) {
+      const float4 v = from[s * (DV / 4)];
       sum.x += v.x;
       sum.y += v.y;
       sum.z += v.z;
       sum.w += v.w;
     }
-    *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + at * DV + d) =
-        make_uint2(Elem<T>::pack2(sum.x * p.inv_n, sum.y * p.inv_n), Elem<T>::pack2(sum.z * p.inv_n, sum.w * p.inv_n));
   }
+  if (WARPS > 1) {
+    red[warp][lane] = sum;
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll
+    for (int w = 1; w < WARPS; ++w) {
+      const float4 v = red[w][lane];
+      sum.x += v.x;
+      sum.y += v.y;
+      sum.z += v.z;
+      sum.w += v.w;
+    }
+  }
+  if (live && lane < DV / 4)
+    *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + unit * DV + 4 * lane) =
+        make_uint2(Elem<T>::pack2(sum.x * p.inv_n, sum.y * p.inv_n), Elem<T>::pack2(sum.z * p.inv_n, sum.w * p.inv_n));
 }
 
 // Launches the kernel for the widths of p.cache (one function for each type,
@@ -820,10 +828,29 @@ cudaError_t launch_paged_one(const PagedParams& p, unsigned blocks, cudaStream_t
   paged_kernel<T, DQ, DV, E4M3, MANY><<<blocks, kPagedThreads, kSmem, stream>>>(p);
   return cudaGetLastError();
 }
+
+template <typename T, int DV, int WARPS>
+cudaError_t launch_paged_join(const PagedParams& p, cudaStream_t stream) {
+  const int64_t units = static_cast<int64_t>(p.num_cand) * p.cache.heads;
+  cudaLaunchAttribute overlap{};
+  overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  overlap.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t config{};
+  config.gridDim = dim3(static_cast<unsigned>((units + 8 / WARPS - 1) / (8 / WARPS)));
+  config.blockDim = dim3(256);
+  config.stream = stream;
+  config.attrs = &overlap;
+  config.numAttrs = 1;
+  return cudaLaunchKernelEx(&config, paged_join_kernel<T, DV, WARPS>, p);
+}
 template <typename T, bool E4M3, int DQ, int DV>
 cudaError_t launch_paged_widths(const PagedParams& p, unsigned blocks, cudaStream_t stream) {
-  return p.cand_offsets ? launch_paged_one<T, E4M3, DQ, DV, true>(p, blocks, stream)
-                        : launch_paged_one<T, E4M3, DQ, DV, false>(p, blocks, stream);
+  const cudaError_t e = p.cand_offsets ? launch_paged_one<T, E4M3, DQ, DV, true>(p, blocks, stream)
+                                       : launch_paged_one<T, E4M3, DQ, DV, false>(p, blocks, stream);
+  if (e != cudaSuccess || p.nsplit == 1 || p.num_cand == 0) return e;
+  // A warp for each (candidate, head), or a block where those are few.
+  if (static_cast<int64_t>(p.num_cand) * p.cache.heads <= 1216) return launch_paged_join<T, DV, 8>(p, stream);
+  return launch_paged_join<T, DV, 1>(p, stream);
 }
 template <typename T, bool E4M3, int DQ>
 cudaError_t launch_paged_dv(const PagedParams& p, unsigned blocks, cudaStream_t stream) {

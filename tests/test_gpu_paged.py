@@ -219,6 +219,36 @@ def test_bad_sequences_are_left_as_they_were():
     assert st == hb.HSTU_OK and torch.equal(out, good)
 
 
+def test_bad_offsets_of_long_sequences_leave_their_rows():
+    """Sequences of several splits: a refused one wrote no sums to join, and the
+    workspace may hold those of an earlier call."""
+    lens, counts, H, D, N = [100, 1500, 1400], [2, 1, 3], 2, 64, 1500
+    pages = su.Pages(lens, H, D, D, 32, torch.bfloat16, False)
+    pages.fill(np.random.default_rng(2))
+    q = su.rows_of((6, H, D), torch.Generator().manual_seed(2), torch.bfloat16)
+    ws = hb.paged_workspace(pages.cache, 3, 6, N)
+    assert ws.numel() > 256  # several splits
+
+    def run(offsets, table=None):
+        out = torch.full((6, H, D), 55.0, dtype=torch.bfloat16, device="cuda")
+        hb.fwd_paged(q, pages.cache, pages.d_lens, pages.d_table if table is None else table, N,
+                     cand_offsets=_int32(offsets), ws=ws, out=out)
+        return hb.device_status(ws), out
+
+    st, good = run(_offsets(counts))
+    assert st == hb.HSTU_OK
+    st, out = run([0, 2, 9, 6])  # sequence 1 ends past the candidates, sequence 2 before it begins
+    assert st == 5 and torch.equal(out[:2], good[:2]) and (out[2:] == 55.0).all()
+    st, out = run([0, 2, 3, 5])
+    assert st == 5 and (out == 55.0).all()
+    table = pages.d_table.clone()
+    table[1, 40] = -1  # in the third split of sequence 1
+    st, out = run(_offsets(counts), table)
+    assert st == 5 and (out[2] == 55.0).all() and torch.equal(out[:2], good[:2]) and torch.equal(out[3:], good[3:])
+    st, out = run(_offsets(counts))
+    assert st == hb.HSTU_OK and torch.equal(out, good)
+
+
 def test_captured_and_replayed_with_longer_histories():
     """One graph serves every length up to its N; two graphs with workspaces of
     their own may share the cache."""

@@ -127,10 +127,10 @@ def test_cache_read_refusals(lib):
 
 def test_paged_refusals(lib):
     def paged(cache=None, q=FAKE, qs=256, o=FAKE, lens=FAKE, B=3, table=FAKE, width=4, coff=FAKE, C=7, func=None,
-              nfunc=0, N=1000, alpha=0.1, ws=FAKE, wsb=1 << 30):
+              nfunc=0, N=1000, alpha=0.1, ws=FAKE, wsb=1 << 30, flags=0):
         c = cache if cache is not None else _cache()
         return lib.hstu_attn_fwd_paged(q, qs, o, ctypes.byref(c), lens, B, table, width, coff, C, func, nfunc, N,
-                                       alpha, ws, wsb, None)
+                                       alpha, ws, wsb, flags, None)
     for kw, want in BAD_CACHES:
         assert paged(cache=_cache(**kw)) == want, kw
         assert lib.hstu_attn_paged_workspace_size(ctypes.byref(_cache(**kw)), 3, 7, 1000) == 0
@@ -142,7 +142,7 @@ def test_paged_refusals(lib):
     for kw in (dict(func=FAKE, nfunc=2), dict(func=FAKE, nfunc=11), dict(N=(1 << 24) + 1),
                dict(cache=_cache(H=60000), B=1 << 20)):
         assert paged(**kw) == 2, kw
-    assert paged(ws=None) == 3 and paged(ws=vp((1 << 20) + 64)) == 3 and paged(wsb=64) == 3
+    assert paged(ws=None, flags=2) == 3 and paged(ws=None, N=100) == 3 and paged(ws=None) == 3 and paged(ws=vp((1 << 20) + 64)) == 3 and paged(wsb=64) == 3
     size = lib.hstu_attn_paged_workspace_size(ctypes.byref(_cache()), 3, 7, 1000)
     assert size > 256 and paged(wsb=size - 1) == 3  # the sums of several splits
     assert lib.hstu_attn_paged_workspace_size(ctypes.byref(_cache()), 3, 7, 100) == 256
