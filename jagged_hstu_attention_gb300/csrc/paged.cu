@@ -6,24 +6,29 @@
 
 namespace hstu {
 
-// Keys of a split: as many as leave 2400 CTAs (eight waves of two an SM) at
-// the longest length, which balances ragged lengths, from 512 to 4096. It
-// follows from the arguments alone, so that the workspace and the order of the
-// sums are the same on every device.
-static int paged_split(int batch, int heads, int max_seqlen) {
-  constexpr int64_t kCtas = 2400;
-  const int64_t want = static_cast<int64_t>(max_seqlen) * batch * heads / kCtas;
-  return static_cast<int>(std::min<int64_t>(kPagedMaxSplit, std::max<int64_t>(512, (want + 255) / 256 * 256)));
-}
-
+// The split of the cache's length. It follows from the arguments alone, so
+// that the workspace and the order of the sums are the same on every device.
+//   - As many keys as leave 2400 CTAs (eight waves of two an SM) at the longest
+//     length, which balances ragged lengths, from 512 to 4096.
+//   - With more than 8 candidates a sequence on average, 1024 keys at the least,
+//     which paged_split_keys cuts to a half or a quarter where a sequence has
+//     many: 64 users of 512 to 2048 rows and 0 to 48 candidates took 71 us so and
+//     79 us with 512 keys for all. With fewer the short splits that no
+//     sequence uses would cost more than they give.
 struct PagedLayout {
   int split = 0, nsplit = 0;
+  bool shorter = false;
   size_t states = 0, partial = 0, total = 0;
 };
 static PagedLayout paged_layout(const CacheView& c, int batch, int64_t num_cand, int max_seqlen) {
+  constexpr int64_t kCtas = 2400;
   PagedLayout l;
-  l.split = paged_split(batch, c.heads, max_seqlen);
-  l.nsplit = (max_seqlen + l.split - 1) / l.split;
+  l.shorter = num_cand > 8 * static_cast<int64_t>(batch);
+  const int64_t want = static_cast<int64_t>(max_seqlen) * batch * c.heads / kCtas;
+  l.split = static_cast<int>(
+      std::min<int64_t>(kPagedMaxSplit, std::max<int64_t>(l.shorter ? 1024 : 512, (want + 255) / 256 * 256)));
+  const int least = l.shorter ? l.split / paged_slice(kPagedPass) : l.split;
+  l.nsplit = (max_seqlen + least - 1) / least;
   l.states = l.partial = l.total = kHdrWords * 4;
   if (l.nsplit > 1) {
     l.partial = l.states + align_up(static_cast<size_t>(batch) * c.heads * l.nsplit * 4, 256);
@@ -93,11 +98,19 @@ HSTU_API hstu_status_t hstu_attn_fwd_paged(const void* q_c, int64_t q_stride, vo
   p.max_seqlen = max_seqlen;
   p.split = l.split;
   p.nsplit = l.nsplit;
+  if (func_c && !cand_offsets && l.split < hstu::kPagedMaxSplit) {
+    // A mask leaves a CTA less to read than its keys and makes it list its
+    // tiles first, so splits are twice as long: one row for each of 128 users
+    // under the SLA mask took 25.7 us so and 29.1 us without.
+    p.split = std::min(2 * l.split, hstu::kPagedMaxSplit);
+    p.nsplit = (max_seqlen + p.split - 1) / p.split;
+  }
+  p.shorter = l.shorter;
   p.alpha = alpha;
   p.inv_n = 1.0f / static_cast<float>(max_seqlen);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (report && cudaMemsetAsync(ws, 0, hstu::kHdrWords * 4, cs) != cudaSuccess) return HSTU_ERR_CUDA;
-  const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(batch) * p.cache.heads * l.nsplit);
+  const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(batch) * p.cache.heads * p.nsplit);
   const bool half = cache->dtype == HSTU_DTYPE_F16;
   cudaError_t e;
   if (cache->e4m3) e = half ? hstu::launch_paged_f16_e4m3(p, blocks, cs) : hstu::launch_paged_bf16_e4m3(p, blocks, cs);

@@ -70,7 +70,8 @@ struct PagedParams {
   int32_t* header;    // null: bad sequences are not reported
   int32_t* states;    // (batch, heads, nsplit): 1 where a split's sums are good
   int32_t batch, max_pages, num_cand, nfunc, max_seqlen;
-  int32_t split, nsplit;  // keys of a split; splits of max_seqlen
+  int32_t split, nsplit;  // keys of a split (of sequences with few candidates); splits of max_seqlen, at most
+  bool shorter;           // splits get shorter with a sequence's candidates (paged_split_keys)
   float alpha, inv_n;
 };
 
@@ -155,7 +156,7 @@ struct PagedSizes {
   // Tiles of a warp's ring: enough in flight on an SM to cover HBM's latency
   // (48 KB); two stages where the warps of a slice share tiles, whose products
   // take longer than the copies.
-  static constexpr int kStages = kStep <= 2080 ? 4 : (MANY && kStep >= 4096 ? 2 : 3);
+  static constexpr int kStages = kStep <= 2080 ? 4 : (MANY && kStep >= 4096) || kStep == 6144 ? 2 : 3;
   static constexpr int kRing = kPagedWarps * kStages * kStep;
   // The warps' sums, after the ring's use. A lane (g, t) writes VE columns of
   // each piece of row t: blocks of VE + 1 and rows of 8 (mod 32) put the
@@ -187,33 +188,62 @@ struct PagedSplit {
 constexpr int kPagedWords = kPagedMaxSplit / kPagedTile / 32;
 constexpr int kPagedIv = 2 * kMaxIntervals + 1;  // ints of a candidate's intervals (odd: different banks)
 
-// Lists the tiles that the pass's candidates see.
-__device__ __forceinline__ int paged_list(const PagedParams& p, const PagedSplit& sp, int ncand) {
-  const int tid = threadIdx.x, lane = tid & 31;
-  if (tid < 2 * kPagedWords) sp.bits[tid] = 0;
-  __syncthreads();
-  const int words = (sp.tiles + 31) / 32, n = (p.nfunc + 1) / 2;
-  if (tid < ncand) {
-    int lo[kMaxIntervals], hi[kMaxIntervals];
-    load_row_intervals<kMaxIntervals>(p.func, p.num_cand, sp.c0 + tid, sp.len, true, lo, hi, (1u << n) - 1u);
-    for (int w = 0; w < words; ++w) {
-      const int base = sp.k0 + w * 32 * kPagedTile;
-      const auto span = [](int x, int y) {  // bits [x, y), cut to the word
-        const int u = max(x, 0), v = min(y, 32);
-        return u >= v ? 0u : (0xffffffffu << u) & (0xffffffffu >> (32 - v));
-      };
-      uint32_t seen = 0, whole = 0;
+// The bits of a word of 32 tiles whose tiles lie in [x, y).
+__device__ __forceinline__ uint32_t tile_span(int x, int y) {
+  const int u = max(x, 0), v = min(y, 32);
+  return u >= v ? 0u : (0xffffffffu << u) & (0xffffffffu >> (32 - v));
+}
+
+// Tiles of word w that the intervals touch (seen) and that one of them covers.
+__device__ __forceinline__ void tile_words(const PagedSplit& sp, int w, const int (&lo)[kMaxIntervals],
+                                           const int (&hi)[kMaxIntervals], int n, uint32_t& seen, uint32_t& whole) {
+  const int base = sp.k0 + w * 32 * kPagedTile;
+  seen = whole = 0;
 #pragma unroll
-      for (int i = 0; i < kMaxIntervals; ++i) {
-        if (i >= n) break;
-        const int a = max(lo[i], sp.k0) - base, e = min(hi[i], sp.k1) - base;  // in keys of this word's first tile
-        if (e <= a) continue;
-        seen |= span(a >> 4, (e + kPagedTile - 1) >> 4);   // the tiles it touches
-        whole |= span((a + kPagedTile - 1) >> 4, e >> 4);  // and covers
+  for (int i = 0; i < kMaxIntervals; ++i) {
+    if (i >= n) break;
+    const int a = max(lo[i], sp.k0) - base, e = min(hi[i], sp.k1) - base;  // in keys of the word's first tile
+    if (e <= a) continue;
+    seen |= tile_span(a >> 4, (e + kPagedTile - 1) >> 4);
+    whole |= tile_span((a + kPagedTile - 1) >> 4, e >> 4);
+  }
+}
+
+// Lists the tiles that the pass's candidates see. A single candidate's raw
+// intervals are in every thread's registers.
+template <bool MANY>
+__device__ __forceinline__ int paged_list(const PagedParams& p, const PagedSplit& sp, int ncand,
+                                          const int (&raw)[2 * kMaxIntervals - 1]) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int words = (sp.tiles + 31) / 32, n = (p.nfunc + 1) / 2;
+  int lo[kMaxIntervals], hi[kMaxIntervals];
+  if (MANY) {
+    if (tid < 2 * kPagedWords) sp.bits[tid] = 0;
+    __syncthreads();
+    if (tid < ncand) {
+      load_row_intervals<kMaxIntervals>(p.func, p.num_cand, sp.c0 + tid, sp.len, true, lo, hi, (1u << n) - 1u);
+      for (int w = 0; w < words; ++w) {
+        uint32_t seen, whole;
+        tile_words(sp, w, lo, hi, n, seen, whole);
+        if (seen) atomicOr(sp.bits + w, seen);
+        if (~whole) atomicOr(sp.bits + kPagedWords + w, ~whole);
       }
-      if (seen) atomicOr(sp.bits + w, seen);
-      if (~whole) atomicOr(sp.bits + kPagedWords + w, ~whole);
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kMaxIntervals; ++i) {  // as load_row_intervals has them
+      lo[i] = i == 0 ? 0 : min(max(raw[i > 0 ? 2 * i - 1 : 0], 0), sp.len);
+      hi[i] = min(max(raw[2 * i], 0), sp.len);
+      if (i >= n || hi[i] <= lo[i]) lo[i] = hi[i] = 0;
+    }
+    if (tid < kPagedWords) {
+      uint32_t seen = 0, whole = 0;
+      if (tid < words) tile_words(sp, tid, lo, hi, n, seen, whole);
+      sp.bits[tid] = seen;
+      sp.bits[kPagedWords + tid] = ~whole;
+    }
+  }
+  if (tid < ncand) {
 #pragma unroll
     for (int i = 0; i < kMaxIntervals; ++i) {
       if (i >= n) break;
@@ -248,6 +278,16 @@ __device__ __forceinline__ bool paged_sees(const PagedParams& p, const PagedSpli
   const int n = (p.nfunc + 1) / 2;
   for (int i = 0; i < n; ++i) vis |= sp.iv[r * kPagedIv + 2 * i] <= key && key < sp.iv[r * kPagedIv + 2 * i + 1];
   return vis;
+}
+
+// Warps of a slice for `total` candidates of a pass.
+__host__ __device__ __forceinline__ int paged_slice(int total) { return total <= 16 ? 1 : (total <= 32 ? 2 : 4); }
+
+// Keys of a split of a sequence with `total` candidates: where the warps of a
+// slice share their tiles, each takes all of them, so the split is shorter by
+// as much and CTAs take about the same time.
+__device__ __forceinline__ int paged_split_keys(const PagedParams& p, int total) {
+  return p.shorter ? p.split / paged_slice(total) : p.split;
 }
 
 __device__ __forceinline__ int paged_key(const PagedParams& p, const PagedSplit& sp, int entry) {
@@ -300,7 +340,8 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t w) {
 // second idle where a warp has 8 candidates or fewer). Returns the warps of a
 // slice.
 template <typename T, int DQ, int DV, bool E4M3, bool MANY, bool PAIR>
-__device__ __forceinline__ int paged_pass(const PagedParams& p, const PagedSplit& sp) {
+__device__ __forceinline__ int paged_pass(const PagedParams& p, const PagedSplit& sp,
+                                          const int (&raw)[2 * kMaxIntervals - 1]) {
   using Z = PagedSizes<DQ, DV, E4M3, MANY>;
   constexpr bool kPair = PAIR;
   constexpr bool kHalf = E4M3 || std::is_same<T, __half>::value;  // products in fp16
@@ -316,12 +357,12 @@ __device__ __forceinline__ int paged_pass(const PagedParams& p, const PagedSplit
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int total = sp.ce - sp.c0;
-  const int wg = kPair || total <= ROWS ? 1 : (total <= 2 * ROWS ? 2 : 4);
+  const int wg = kPair ? 1 : paged_slice(total);
   const int nslices = kPagedWarps / wg, slice = warp / wg, gi = warp % wg;
   const int cg = gi * ROWS;                                        // this warp's first candidate in the pass
   const int ncand = max(0, min(ROWS, total - cg));
   const int groups = kPair ? 1 : (ncand > 8 ? 2 : 1);              // column groups in use
-  const int entries = p.func ? paged_list(p, sp, min(total, wg * ROWS)) : sp.tiles;
+  const int entries = p.func ? paged_list<MANY>(p, sp, min(total, wg * ROWS), raw) : sp.tiles;
   // Copy n of this warp is list entry (n nslices + slice) wg + gi.
   const int iters = (entries + kPagedWarps - 1) / kPagedWarps;
 
@@ -658,12 +699,18 @@ __global__ void __launch_bounds__(kPagedThreads, PagedSizes<DQ, DV, E4M3, MANY>:
   const int split = static_cast<int>(bid % p.nsplit);
   const int bh = static_cast<int>(bid / p.nsplit);
   const int h = bh % p.cache.heads, b = bh / p.cache.heads;
-  const int k0 = split * p.split;
+  int cb = b, ce = b + 1;
+  if (MANY) {
+    cb = p.cand_offsets[b];
+    ce = p.cand_offsets[b + 1];
+  }
+  const int keys = MANY ? paged_split_keys(p, ce - cb) : p.split;
+  const int k0 = static_cast<int>(min(static_cast<int64_t>(split) * keys, static_cast<int64_t>(p.max_seqlen)));
 
   // Pages of this split, read before the length is known (entries past the
   // length are not looked at).
   const int page0 = k0 >> p.cache.page_shift;
-  const int most_pages = min(((k0 + p.split - 1) >> p.cache.page_shift) - page0 + 1, p.max_pages - page0);
+  const int most_pages = min(((k0 + keys - 1) >> p.cache.page_shift) - page0 + 1, p.max_pages - page0);
   constexpr int kPageLoads = kPagedMaxSplit / kPagedTile / kPagedThreads;
   int page[kPageLoads];
 #pragma unroll
@@ -671,13 +718,15 @@ __global__ void __launch_bounds__(kPagedThreads, PagedSizes<DQ, DV, E4M3, MANY>:
     const int at = i * kPagedThreads + tid;
     page[i] = at < most_pages ? __ldg(p.page_table + static_cast<int64_t>(b) * p.max_pages + page0 + at) : -1;
   }
+  // A single candidate's intervals likewise.
+  int raw[2 * kMaxIntervals - 1];
+#pragma unroll
+  for (int i = 0; i < 2 * kMaxIntervals - 1; ++i)
+    raw[i] = !MANY && p.func && i < p.nfunc ? __ldg(p.func + static_cast<int64_t>(i) * p.num_cand + b) : 0;
 
   // Checks of this sequence (every CTA of it comes to the same answer).
-  int cb = b, ce = b + 1;
   bool ok = true;
   if (MANY) {
-    cb = p.cand_offsets[b];
-    ce = p.cand_offsets[b + 1];
     ok = cb >= 0 && cb <= ce && ce <= p.num_cand && p.cand_offsets[0] == 0 &&
          p.cand_offsets[p.batch] == p.num_cand;
   }
@@ -689,9 +738,9 @@ __global__ void __launch_bounds__(kPagedThreads, PagedSizes<DQ, DV, E4M3, MANY>:
     return;
   }
   if (cb == ce) return;
-  const int splits = max(1, (len + p.split - 1) / p.split);
+  const int splits = max(1, (len + keys - 1) / keys);
   if (split >= splits) return;
-  const int k1 = min(len, k0 + p.split);
+  const int k1 = min(len, k0 + keys);
   const int npages = k1 > k0 ? ((k1 - 1) >> p.cache.page_shift) - page0 + 1 : 0;
   bool bad_page = false;
 #pragma unroll
@@ -725,10 +774,10 @@ __global__ void __launch_bounds__(kPagedThreads, PagedSizes<DQ, DV, E4M3, MANY>:
     sp.c0 = c0;
     int wg, rows;
     if (!MANY || ce - c0 <= 4) {
-      wg = paged_pass<T, DQ, DV, E4M3, MANY, true>(p, sp);
+      wg = paged_pass<T, DQ, DV, E4M3, MANY, true>(p, sp, raw);
       rows = 4;
     } else {
-      wg = paged_pass<T, DQ, DV, E4M3, MANY, !MANY>(p, sp);
+      wg = paged_pass<T, DQ, DV, E4M3, MANY, !MANY>(p, sp, raw);
       rows = 16;
     }
     __syncthreads();
@@ -772,15 +821,16 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p) {
   const int64_t c = unit / p.cache.heads;
   const int h = static_cast<int>(unit - c * p.cache.heads);
   bool live = c < p.num_cand;
-  int b = static_cast<int>(c), first;
+  int b = static_cast<int>(c), first, keys = p.split;
   if (p.cand_offsets) {  // lanes of a warp ask for the same candidate
     live = find_sequence(p.cand_offsets, p.batch, live ? c : 0, b, first) && live && p.cand_offsets[0] == 0 &&
            p.cand_offsets[p.batch] == p.num_cand && p.cand_offsets[b + 1] <= p.num_cand;  // as paged_kernel has it
+    keys = live ? paged_split_keys(p, p.cand_offsets[b + 1] - first) : p.split;
   }
   const int len = live ? p.lens[b] : 0;
-  live = live && len > p.split && len <= p.max_seqlen &&
+  live = live && len > keys && len <= p.max_seqlen &&
          static_cast<int64_t>(len) <= (static_cast<int64_t>(p.max_pages) << p.cache.page_shift);
-  const int splits = live ? (len + p.split - 1) / p.split : 0;
+  const int splits = live ? (len + keys - 1) / keys : 0;
   const int32_t* states = p.states + (static_cast<int64_t>(b) * p.cache.heads + h) * p.nsplit;
   bool good = true;
   for (int s = lane; s < splits; s += 32) good = good && states[s] == 1;
