@@ -31,6 +31,10 @@ VARIANTS = {
 SOURCES = ["plan.cu", "attn_fwd_bf16.cu", "attn_fwd_f16.cu", "attn_bwd_bf16.cu", "attn_bwd_f16.cu", "targets_only.cu", "api.cu", "noalloc.cu", "selftest.cu", "func_build.cu", "project.cu",
            "rope.cu", "cache.cu", "paged.cu", "paged_bf16.cu", "paged_f16.cu", "paged_bf16_e4m3.cu",
            "paged_f16_e4m3.cu", "shard.cpp"]
+# Sources without HSTU_CHECKED code: the checked library links the release's
+# objects of them.
+SHARED = {"rope.cu", "cache.cu", "paged.cu", "paged_bf16.cu", "paged_f16.cu", "paged_bf16_e4m3.cu",
+          "paged_f16_e4m3.cu"}
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]
@@ -79,15 +83,16 @@ def build(force: bool = False, verbose: bool = False, variants=("release", "chec
             raise RuntimeError(f"nvcc failed on {src} ({variant}):\n{r.stdout}\n{r.stderr}")
         return obj
 
-    for v in todo:
+    job_of = lambda v, src: ("release" if src in SHARED else v, src)
+    jobs = sorted({job_of(v, src) for v in todo for src in SOURCES})
+    for v, _ in jobs:
         os.makedirs(VARIANTS[v][1], exist_ok=True)
-    jobs = [(v, src) for v in todo for src in SOURCES]
     with ThreadPoolExecutor(max_workers=min(len(jobs), max(os.cpu_count() or 1, len(SOURCES)))) as ex:
-        objs = list(ex.map(compile_one, jobs))
+        objs = dict(zip(jobs, ex.map(compile_one, jobs)))
     for v in todo:
         lib = VARIANTS[v][0]
         tmp = lib + ".tmp"
-        cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *[o for (vv, _), o in zip(jobs, objs) if vv == v]]
+        cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *[objs[job_of(v, src)] for src in SOURCES]]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed ({v}):\n{r.stdout}\n{r.stderr}")

@@ -612,6 +612,10 @@ __device__ __forceinline__ int paged_pass(const PagedParams& p, const PagedSplit
         for (int n = 0; n < NG; ++n) {
           if (n >= groups) break;
           mma16816<M>(acc[n][m], a0, a1, a2, a3, bh[n][0], bh[n][1]);
+        }
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+          if (n >= groups) break;
           if (!kPair) mma16816<M>(acc[n][m], a0, a1, a2, a3, bl[n][0], bl[n][1]);
         }
       };

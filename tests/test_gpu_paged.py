@@ -310,3 +310,89 @@ def test_serving_steps_together():
         o2 = hb.fwd_targets_only(qr, k, v, _int32(off), func, N)
         assert np.linalg.norm(su.f64(o2) - su.f64(o)) <= 5e-3 * np.linalg.norm(su.f64(o))
     assert lens.cpu().tolist() == [p + steps for p in prompts]
+
+
+def test_a_history_past_the_contiguous_kernels_limit():
+    H, D, L = 1, 32, 70001
+    pages = su.Pages([L, 40], H, D, D, 256, torch.float16, True)
+    rows = pages.fill(np.random.default_rng(4))
+    _run(pages, rows, [1, 1], None, 1 << 20, single=True)
+    func = np.array([[20000, 39999, 70000], [3, 50, 60]]).T
+    _run(pages, rows, [1, 1], func, 1 << 17, single=True)
+
+
+def test_many_candidates_take_several_passes():
+    """More than one pass (64 candidates), and every way of sharing tiles."""
+    lens, counts = [700, 1100, 90, 300, 40], [130, 65, 33, 17, 9]
+    full = [n + c for n, c in zip(lens, counts)]
+    func = np.array([(n, n + j, n + j + 1) for n, c in zip(lens, counts) for j in range(c)]).T
+    for dtype, quantised in ((torch.bfloat16, True), (torch.float16, False)):
+        pages = su.Pages(full, 2, 64, 64, 64, dtype, quantised)
+        rows = pages.fill(np.random.default_rng(8))
+        _run(pages, rows, counts, func, max(full))
+        _run(pages, rows, counts, None, max(full))
+
+
+def test_a_length_past_the_page_table_is_refused():
+    pages = su.Pages([40, 40], 1, 32, 32, 16, torch.bfloat16, False)
+    pages.fill(np.random.default_rng(0))
+    q = su.rows_of((2, 1, 32), torch.Generator().manual_seed(0), torch.bfloat16)
+    out = torch.full((2, 1, 32), 9.0, dtype=torch.bfloat16, device="cuda")
+    ws = hb.paged_workspace(pages.cache, 2, 2, 500)
+    hb.fwd_paged(q, pages.cache, _int32([49, 40]), pages.d_table, 500, ws=ws, out=out)  # 3 pages of 16
+    assert hb.device_status(ws) == 5 and (out[0] == 9.0).all() and (out[1] != 9.0).any()
+
+
+def test_no_candidates():
+    pages = su.Pages([40, 4000], 1, 32, 32, 16, torch.bfloat16, False)
+    q = torch.empty((0, 1, 32), dtype=torch.bfloat16, device="cuda")
+    o = hb.fwd_paged(q, pages.cache, pages.d_lens, pages.d_table, 4000, cand_offsets=_int32([0, 0, 0]))
+    torch.cuda.synchronize()
+    assert o.shape == (0, 1, 32)
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with its own workspace, over one cache."""
+    pages = su.Pages([3000, 2100, 900], 2, 64, 64, 64, torch.bfloat16, False)
+    pages.fill(np.random.default_rng(0))
+    qs = [su.rows_of((3, 2, 64), torch.Generator().manual_seed(i), torch.bfloat16) for i in range(2)]
+    want = [hb.fwd_paged(q, pages.cache, pages.d_lens, pages.d_table, 3000) for q in qs]
+    streams = [torch.cuda.Stream() for _ in qs]
+    ws = [hb.paged_workspace(pages.cache, 3, 3, 3000) for _ in qs]
+    outs = [torch.zeros_like(w) for w in want]
+    torch.cuda.synchronize()
+    for _ in range(50):
+        for q, s, w, o in zip(qs, streams, ws, outs):
+            hb.fwd_paged(q, pages.cache, pages.d_lens, pages.d_table, 3000, ws=w, out=o, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+def test_the_binding_refuses_what_does_not_fit():
+    pages = su.Pages([40], 2, 64, 32, 16, torch.bfloat16, False)
+    c, lens, table = pages.cache, pages.d_lens, pages.d_table
+    q = torch.zeros((1, 2, 64), dtype=torch.bfloat16, device="cuda")
+    for bad in (dict(q_c=q.half()), dict(q_c=q[:, :1]), dict(q_c=q.transpose(1, 2).contiguous().transpose(1, 2)),
+                dict(q_c=q.cpu()), dict(cache_lens=lens.long()), dict(page_table=table[:, ::2]),
+                dict(page_table=table[0]), dict(cand_offsets=lens), dict(func_c=torch.zeros((3, 2), device="cuda").int()),
+                dict(out=torch.zeros((1, 2, 64), dtype=torch.bfloat16, device="cuda")), dict(ws=torch.zeros(512).byte())):
+        args = dict(q_c=q, cache=c, cache_lens=lens, page_table=table, max_seqlen=40)
+        args.update(bad)
+        with pytest.raises(ValueError):
+            hb.fwd_paged(**args)
+    with pytest.raises(hb.HstuError):  # an even number of interval rows
+        hb.fwd_paged(q, c, lens, table, 40, func_c=torch.zeros((2, 1), device="cuda").int())
+    k, v = q.new_zeros((3, 2, 64)), q.new_zeros((3, 2, 32))
+    off = _int32([0, 3])
+    for bad in (dict(k=v), dict(v=v[:2]), dict(k=k.half()), dict(seq_offsets=off.long()), dict(cache_lens=off),
+                dict(positions=off), dict(rope=hb.rope_table(64, device="cpu"))):
+        args = dict(cache=c, k=k, v=v, seq_offsets=off, cache_lens=lens, page_table=table)
+        args.update(bad)
+        with pytest.raises(ValueError):
+            hb.cache_write(**args)
+    with pytest.raises(hb.HstuError):  # the rotation is wider than the head
+        hb.cache_write(c, k, v, off, lens, table, rope=hb.rope_table(128))
+    with pytest.raises(ValueError):
+        hb.cache_read(c, off, 3, table, outs=(k, k))
+    with pytest.raises(ValueError, match="current device"):
+        hb._here(torch.cuda.device_count(), "q")
