@@ -703,6 +703,18 @@ class PagedCache:
                         self.dim, self.dim_v, DTYPES[dtype], int(e4m3))
         self._addr = ctypes.addressof(self._c)
         self._device = k.get_device()
+        self._ws_bytes = {}  # workspace sizes already asked for, by (batch, candidates, max_seqlen)
+
+    def workspace_bytes(self, batch: int, num_candidates: int, max_seqlen: int) -> int:
+        """hstu_attn_paged_workspace_size; a server asks for few different sizes."""
+        key = (batch, num_candidates, max_seqlen)
+        n = self._ws_bytes.get(key)
+        if n is None:
+            n = load().hstu_attn_paged_workspace_size(self._addr, batch, num_candidates, max_seqlen)
+            if len(self._ws_bytes) >= 1024:
+                self._ws_bytes.clear()
+            self._ws_bytes[key] = n
+        return n
 
 
 def alloc_cache(num_pages: int, page_size: int, heads: int, dim: int, dim_v: int = 0, dtype=torch.bfloat16,
@@ -786,7 +798,7 @@ def cache_read(cache: PagedCache, seq_offsets, rows: int, page_table, starts=Non
 
 def paged_workspace(cache: PagedCache, batch: int, num_candidates: int, max_seqlen: int) -> torch.Tensor:
     """Workspace of ``fwd_paged``."""
-    n = load().hstu_attn_paged_workspace_size(cache._addr, batch, num_candidates, max_seqlen)
+    n = cache.workspace_bytes(batch, num_candidates, max_seqlen)
     if n == 0:
         raise HstuError(2, "hstu_attn_paged_workspace_size")
     return torch.empty(n, dtype=torch.uint8, device=cache.device)
@@ -820,7 +832,7 @@ def fwd_paged(q_c, cache: PagedCache, cache_lens, page_table, max_seqlen: int, a
     own_ws, flags = None, 0
     if ws is None:
         flags = FLAG_NO_STATUS  # nobody could read it
-        n = lib.hstu_attn_paged_workspace_size(cache._addr, B, C, max_seqlen)
+        n = cache.workspace_bytes(B, C, max_seqlen)
         if n > 256:  # sums of splits; without them nothing but the error word
             own_ws = ws = torch.empty(n, dtype=torch.uint8, device=cache.device)
     st = lib.hstu_attn_fwd_paged(q_c.data_ptr(), qs, out.data_ptr(), cache._addr,

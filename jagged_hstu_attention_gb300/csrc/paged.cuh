@@ -166,8 +166,12 @@ struct PagedSizes {
   static constexpr int kRedRows = MANY ? 16 : 4;  // of a warp
   static constexpr int kRed = kPagedWarps * kRedRows * kRedRow * 4;
   static constexpr int kSmem = kRing > kRed ? kRing : kRed;
-  static constexpr int kFit = 227 * 1024 / (kSmem + 6144);  // CTAs that shared memory has room for
-  static constexpr int kResident = kFit < 1 ? 1 : (kFit > (MANY ? 3 : 4) ? (MANY ? 3 : 4) : kFit);
+  // CTAs of an SM: as many as shared memory has room for, up to 4 (3 to 5 for
+  // many candidates, whose sums and fragments are most of the registers).
+  static constexpr int kFit = 227 * 1024 / (kSmem + 6144);
+  static constexpr int kRegisters = 80 + DV / 2 + DQ / 4 * (E4M3 ? 2 : 1);
+  static constexpr int kWant = !MANY ? 4 : (kRegisters <= 102 ? 5 : (kRegisters <= 128 ? 4 : 3));
+  static constexpr int kResident = kFit < 1 ? 1 : (kFit > kWant ? kWant : kFit);
   static __device__ __forceinline__ int red_column(int d) { return d / VE * kBlock + d % VE; }
 };
 
@@ -548,14 +552,34 @@ __device__ __forceinline__ int paged_pass(const PagedParams& p, const PagedSplit
           pr[c][r] = x;
         }
       if (part) {
+        // Interval by interval, all of this lane's candidates and keys at once.
+        bool vis[NC][2];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) vis[c][0] = vis[c][1] = false;
+        if (p.func) {
+          const int n = (p.nfunc + 1) / 2;
+#pragma unroll 1
+          for (int i = 0; i < n; ++i) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+              const int cand = kPair ? t : c / 2 * 8 + 2 * t + (c & 1);
+              const int* iv = sp.iv + (cg + (cand < ncand ? cand : 0)) * kPagedIv + 2 * i;
+              const int lo = iv[0], hi = iv[1];
+#pragma unroll
+              for (int r = 0; r < 2; ++r) vis[c][r] |= lo <= key0 + g + 8 * r && key0 + g + 8 * r < hi;
+            }
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            vis[c][0] = key0 + g < sp.k1;
+            vis[c][1] = key0 + g + 8 < sp.k1;
+          }
+        }
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const int cand = cg + (kPair ? t : c / 2 * 8 + 2 * t + (c & 1));
-            if (!(cand < cg + ncand && paged_sees(p, sp, cand, key0 + g + 8 * r))) pr[c][r] = 0.0f;
-          }
-        __syncwarp();
+          for (int r = 0; r < 2; ++r) pr[c][r] = vis[c][r] ? pr[c][r] : 0.0f;
       }
       if (kHalf) {
         // A candidate's scale follows the largest magnitude it has met.
