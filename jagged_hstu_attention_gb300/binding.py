@@ -585,26 +585,32 @@ def _raw_stream(stream, index: int) -> int:
     return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
-def _device_of(t: torch.Tensor, index: int, name: str) -> None:
+_INT32 = torch.int32
+
+
+def _refuse(t: torch.Tensor, dtype, shape, index: int, name: str) -> None:
+    """The error for a tensor that one of the quick checks below turned down."""
     if t.get_device() != index:
         raise ValueError(f"{name} must be a CUDA tensor" if t.get_device() < 0 else
                          f"{name} is on cuda:{t.get_device()}, not on cuda:{index}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous (rows of heads x width may lie apart)")
 
 
 def _rows(t: torch.Tensor, dtype, heads: int, width: int, index: int, name: str) -> int:
     """Checks a (rows, heads, width) tensor whose rows may lie apart (a slice
     of a wider projection); returns the distance between rows in elements."""
-    _device_of(t, index, name)
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     shape = t.shape
-    if len(shape) != 3 or shape[1] != heads or shape[2] != width:
-        raise ValueError(f"{name} must be (rows, {heads}, {width}), got {tuple(shape)}")
+    if t.get_device() != index or t.dtype is not dtype or len(shape) != 3 or shape[1] != heads or shape[2] != width:
+        _refuse(t, dtype, ("rows", heads, width), index, name)
     stride, sh, sw = t.stride()
-    if shape[0] <= 1:
-        stride = heads * width
     if sw != 1 or (sh != width and heads > 1):
-        raise ValueError(f"{name}: heads and columns of a row must be contiguous")
+        _refuse(t, None, None, index, name)
+    if shape[0] <= 1:
+        return heads * width
     if stride < heads * width:
         raise ValueError(f"{name}: rows overlap")
     return stride
@@ -612,13 +618,8 @@ def _rows(t: torch.Tensor, dtype, heads: int, width: int, index: int, name: str)
 
 def _ints(t: torch.Tensor, shape, index: int, name: str) -> int:
     """Checks an int32 tensor of the given shape; returns its address."""
-    _device_of(t, index, name)
-    if t.dtype != torch.int32:
-        raise ValueError(f"{name} must be {torch.int32}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != index or t.dtype is not _INT32 or t.shape != shape or not t.is_contiguous():
+        _refuse(t, _INT32, shape, index, name)
     return t.data_ptr()
 
 
@@ -738,7 +739,8 @@ def _pages(page_table, batch: int, index: int):
 def _ws_args(ws, index: int):
     if ws is None:
         return 0, 0
-    _device_of(ws, index, "ws")
+    if ws.get_device() != index:
+        _refuse(ws, None, None, index, "ws")
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
