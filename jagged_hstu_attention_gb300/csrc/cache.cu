@@ -6,6 +6,12 @@
 // of them. The threads of a row are neighbours in a warp, so that a row's
 // largest magnitude, which sets the scale of its 8-bit codes, is a few
 // shuffles away.
+//
+// Bound by memory: 86000 rows (4 heads of 128) into 16-bit pages, k rotated, take
+// 59 us, 6.0 TB/s; with a thread for each (row, head, slot), which searched its
+// sequence and computed its cosines alone, they took 100 us. A chunk of 3500 rows
+// into 8-bit pages and 90000 rows read back from them take 50 us, 5.7 TB/s, of
+// which the read is 43 us.
 #include "cache.cuh"
 #include "rope.cuh"
 

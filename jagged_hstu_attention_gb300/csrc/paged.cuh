@@ -1,12 +1,24 @@
 // Candidate rows against a paged K/V cache: the kernel (instantiated by
-// paged_{bf16,f16}.cu, launched from paged.cu).
+// paged_{bf16,f16}{,_e4m3}.cu, launched from paged.cu).
 //
 // For candidate c of sequence b: o = sum_j silu(alpha q.k_j) / N v_j over the
 // visible cached positions j. Every cached row is read once and takes part in
 // as many products as its sequence has candidates, few of them, so the bytes
 // of the cache bound the kernel; the products run on warp-level matrix
 // instructions (m16n8k16), whose operands a warp can take straight from the
-// cache's rows.
+// cache's rows. (A tcgen05 product has 128 rows of which a handful of
+// candidates would fill a few, and wants its operands in canonical
+// shared-memory tiles and P back in shared memory; what remains of the time
+// with many candidates is silu and the operands' conversion, not the products:
+// the matrix pipe is 26% busy with 24 of them.)
+//
+// Measured, H = 4, D_qk = D_v = 128, histories of 1332 to 3994 rows: one
+// candidate for each of 256 users over 16-bit pages 207 us, 6.8 TB/s, the rate of
+// a plain copy; over 8-bit pages 119 us, 5.9 TB/s, with the issue slots half
+// used by the codes' conversion and two waves of latency at the ends. 0 to 48
+// candidates for each of 64 users of 512 to 2048 rows: 67 us against 25 us for
+// the bytes, bound by the latency of the chain from scores to weights in the
+// twelve warps that registers leave an SM.
 //
 // A CTA takes one (sequence, head) and one split of its length. Its four warps
 // form slices of 1, 2 or 4 warps, as many as the sequence's candidates need; a
@@ -724,8 +736,14 @@ __global__ void __launch_bounds__(kPagedThreads, PagedSizes<DQ, DV, E4M3, MANY>:
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x;
   const int64_t bid = blockIdx.x;
-  const int split = static_cast<int>(bid % p.nsplit);
-  const int bh = static_cast<int>(bid / p.nsplit);
+  // One candidate a sequence: first splits first, so that the last CTAs to start
+  // are those of the sequences' ends, the shorter ones (8-bit pages, 256 users:
+  // 118.9 us so, 120.4 us with a sequence's splits side by side). Splits that
+  // follow the candidates take about the same time as they are, and are
+  // better off side by side (67 us against 70).
+  const int pairs = p.batch * p.cache.heads;
+  const int split = static_cast<int>(MANY ? bid % p.nsplit : bid / pairs);
+  const int bh = static_cast<int>(MANY ? bid / p.nsplit : bid % pairs);
   const int h = bh % p.cache.heads, b = bh / p.cache.heads;
   int cb = b, ce = b + 1;
   if (MANY) {
