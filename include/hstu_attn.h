@@ -454,7 +454,8 @@ HSTU_API size_t hstu_attn_paged_workspace_size(const hstu_cache_t* cache, int32_
  * over the positions [0, cache_lens[b]) of its sequence, N = max_seqlen. New
  * tokens that are to see themselves are written to the cache before the call.
  *   q_c      DEVICE (num_candidates, H, D_qk), rows q_stride elements apart
- *            (as for hstu_attn_rope); o_c (num_candidates, H, D_v) contiguous
+ *            (as for hstu_attn_rope); o_c (num_candidates, H, D_v) contiguous,
+ *            not overlapping q_c
  *   cache_lens   DEVICE int32 (batch), each in [0, max_seqlen]
  *   cand_offsets DEVICE int32 (batch+1) as for hstu_attn_fwd_targets, or NULL:
  *            one candidate a sequence (num_candidates = batch)
@@ -462,7 +463,8 @@ HSTU_API size_t hstu_attn_paged_workspace_size(const hstu_cache_t* cache, int32_
  *            or NULL: every cached position is visible (nfunc is ignored)
  *   max_seqlen   N, 1 .. 2^24 (the pages take longer histories than the
  *            contiguous kernels)
- *   ws       hstu_attn_paged_workspace_size() bytes, 256-byte aligned; NULL is
+ *   ws       hstu_attn_paged_workspace_size() bytes, 256-byte aligned, one for
+ *            each of the calls that may run at the same time; NULL is
  *            taken with HSTU_FLAG_NO_STATUS where that size is 256 (one split:
  *            nothing but the error word)
  *   flags    HSTU_FLAG_NONE or HSTU_FLAG_NO_STATUS

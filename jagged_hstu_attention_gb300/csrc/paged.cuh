@@ -712,6 +712,7 @@ __device__ __forceinline__ int paged_pass(const PagedParams& p, const PagedSplit
     // not see (zero times infinity): those candidates are summed again, key by
     // key, over what they see alone.
     const uint32_t odd = __ballot_sync(0xffffffffu, !finite);
+    if (odd != 0) __syncwarp();  // the lanes' stores above come before those of the second sum
     for (int l = 0; odd != 0 && l < 4; ++l) {
       if ((odd & (0x11111111u << l)) == 0) continue;
       const int again = kPair ? l : c / 2 * 8 + 2 * l + (c & 1);

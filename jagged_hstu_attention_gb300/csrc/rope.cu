@@ -151,6 +151,7 @@ HSTU_API hstu_status_t hstu_attn_rope(const void* q, int64_t q_stride, const voi
     return HSTU_ERR_INVALID_ARG;
   if ((q == q_out && q_stride != q_out_stride) || (k && k == k_out && k_stride != k_out_stride))
     return HSTU_ERR_INVALID_ARG;
+  if (k && (q_out == k_out || q_out == k || k_out == q)) return HSTU_ERR_INVALID_ARG;
   hstu::RopeParams p{};
   p.in[0] = q;
   p.in[1] = k;

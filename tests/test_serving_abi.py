@@ -56,7 +56,8 @@ def test_rope_table_refusals(lib):
         hb.rope_table(64, scaling="cubic", device="cpu")
 
 
-def _rope(lib, rope=None, q=FAKE, qs=256, k=FAKE, ks=256, qo=FAKE, qos=256, ko=FAKE, kos=256, pos=FAKE, tokens=5, H=4,
+def _rope(lib, rope=None, q=vp(1 << 21), qs=256, k=vp(1 << 22), ks=256, qo=vp(1 << 23), qos=256, ko=vp(1 << 24),
+          kos=256, pos=FAKE, tokens=5, H=4,
           D=64, dtype=0, R=64, inter=0, mag=1.0, turns=1 << 20):
     r = hb.Rope(turns, R, inter, mag) if rope is None else rope
     return lib.hstu_attn_rope(q, qs, k, ks, qo, qos, ko, kos, pos, tokens, H, D, dtype,
@@ -69,7 +70,9 @@ def test_rope_refusals(lib):
     for kw in (dict(rope=False), dict(turns=0), dict(turns=(1 << 20) + 4), dict(inter=2), dict(mag=float("nan")),
                dict(q=None), dict(q=vp((1 << 20) + 8)), dict(qs=248), dict(qs=260), dict(qo=None), dict(ko=None),
                dict(kos=128), dict(ks=257), dict(pos=None), dict(pos=vp((1 << 20) + 2)), dict(tokens=-1),
-               dict(tokens=1 << 31), dict(H=0), dict(qos=512)):
+               dict(tokens=1 << 31), dict(H=0), dict(qo=vp(1 << 21), qos=512),
+               # outputs that another input or output shares
+               dict(ko=vp(1 << 23)), dict(qo=vp(1 << 22)), dict(ko=vp(1 << 21))):
         assert _rope(lib, **kw) == 1, kw
     assert _rope(lib, tokens=0, q=None, qo=None, k=None, pos=None) == 0
 
@@ -126,7 +129,7 @@ def test_cache_read_refusals(lib):
 
 
 def test_paged_refusals(lib):
-    def paged(cache=None, q=FAKE, qs=256, o=FAKE, lens=FAKE, B=3, table=FAKE, width=4, coff=FAKE, C=7, func=None,
+    def paged(cache=None, q=FAKE, qs=256, o=vp(1 << 21), lens=FAKE, B=3, table=FAKE, width=4, coff=FAKE, C=7, func=None,
               nfunc=0, N=1000, alpha=0.1, ws=FAKE, wsb=1 << 30, flags=0):
         c = cache if cache is not None else _cache()
         return lib.hstu_attn_fwd_paged(q, qs, o, ctypes.byref(c), lens, B, table, width, coff, C, func, nfunc, N,
@@ -134,7 +137,7 @@ def test_paged_refusals(lib):
     for kw, want in BAD_CACHES:
         assert paged(cache=_cache(**kw)) == want, kw
         assert lib.hstu_attn_paged_workspace_size(ctypes.byref(_cache(**kw)), 3, 7, 1000) == 0
-    for kw in (dict(q=None), dict(q=vp((1 << 20) + 8)), dict(qs=254), dict(qs=260), dict(o=None),
+    for kw in (dict(q=vp(1 << 21)), dict(q=None), dict(q=vp((1 << 20) + 8)), dict(qs=254), dict(qs=260), dict(o=None),
                dict(o=vp((1 << 20) + 4)), dict(lens=None), dict(lens=vp((1 << 20) + 2)), dict(B=0), dict(table=None),
                dict(width=0), dict(coff=None), dict(coff=vp((1 << 20) + 2)), dict(C=-1), dict(C=1 << 31),
                dict(func=vp((1 << 20) + 2), nfunc=3), dict(N=0), dict(alpha=float("nan"))):
