@@ -533,8 +533,36 @@ def set_handoff_limit_for_tests(limit_ns: int) -> None:
 
 
 # ---------------------------------------------------------------- serving
-# A decode step is a few microseconds on the GPU, so these wrappers keep to one
-# pass of cheap checks and hand plain integers to ctypes.
+# A decode step is a few microseconds on the GPU. The calls below go through
+# the extension of csrc/serving_ext.cpp, which checks the tensors, allocates the
+# outputs and calls the selected library's entry points; ctypes and checks in
+# Python take three times as long as the step.
+
+EXT_PATH = os.path.join(_HERE, "_serving.so")
+_ext_module = None
+_ext_library = None  # the library that the extension calls
+
+
+def _ext():
+    """The extension, bound to the selected library. Raises if it has not been
+    built."""
+    global _ext_module, _ext_library
+    if _ext_library != _active:
+        lib = load()
+        if _ext_module is None:
+            if not os.path.exists(EXT_PATH):
+                raise RuntimeError(f"extension {EXT_PATH} is missing: build it first "
+                                   "(python -c 'import __graft_entry__ as g; g.build()')")
+            from . import _serving
+            _ext_module = _serving
+        names = ("rope", "cache_write", "cache_read", "paged_workspace_size", "fwd_paged")
+        _ext_module.bind(*(ctypes.cast(getattr(lib, "hstu_attn_" + n), ctypes.c_void_p).value for n in names))
+        _ext_library = _active
+    return _ext_module
+
+
+def _raw_stream(stream):
+    return None if stream is None else stream.cuda_stream
 
 _ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
@@ -571,100 +599,17 @@ def rope_table(rotary_dim: int, base: float = 10000.0, scaling: str = "none", fa
     return RopeTable(turns.to(device), interleaved, magnitude.value)
 
 
-def _here(index: int, name: str) -> None:
-    """Tensors on device ``index``, and that the current one: the library
-    launches on the current device."""
-    if index < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    current = torch._C._cuda_getDevice()
-    if index != current:
-        raise ValueError(f"{name} is on cuda:{index}, the current device is cuda:{current}")
-
-
-def _raw_stream(stream, index: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-
-
-_INT32 = torch.int32
-
-
-def _refuse(t: torch.Tensor, dtype, shape, index: int, name: str) -> None:
-    """The error for a tensor that one of the quick checks below turned down."""
-    if t.get_device() != index:
-        raise ValueError(f"{name} must be a CUDA tensor" if t.get_device() < 0 else
-                         f"{name} is on cuda:{t.get_device()}, not on cuda:{index}")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    raise ValueError(f"{name} must be contiguous (rows of heads x width may lie apart)")
-
-
-def _rows(t: torch.Tensor, dtype, heads: int, width: int, index: int, name: str) -> int:
-    """Checks a (rows, heads, width) tensor whose rows may lie apart (a slice
-    of a wider projection); returns the distance between rows in elements."""
-    shape = t.shape
-    if t.get_device() != index or t.dtype is not dtype or len(shape) != 3 or shape[1] != heads or shape[2] != width:
-        _refuse(t, dtype, ("rows", heads, width), index, name)
-    stride, sh, sw = t.stride()
-    if sw != 1 or (sh != width and heads > 1):
-        _refuse(t, None, None, index, name)
-    if shape[0] <= 1:
-        return heads * width
-    if stride < heads * width:
-        raise ValueError(f"{name}: rows overlap")
-    return stride
-
-
-def _ints(t: torch.Tensor, shape, index: int, name: str) -> int:
-    """Checks an int32 tensor of the given shape; returns its address."""
-    if t.get_device() != index or t.dtype is not _INT32 or t.shape != shape or not t.is_contiguous():
-        _refuse(t, _INT32, shape, index, name)
-    return t.data_ptr()
-
-
 def rope(q, k, positions, table: RopeTable, backward: bool = False, outs=None, stream=None):
     """(q', k') with the leading columns of every head rotated by the row's
     position (hstu_attn_rope). q and k are (T, H, D), bf16 or fp16, and may be
     slices of a wider projection; k may be None. ``backward=True`` takes the
     gradients of q' and k' to those of q and k. ``outs`` may be (q, k) itself:
     the rows are then rotated in place."""
-    dtype, index = q.dtype, q.get_device()
-    if dtype not in DTYPES:
-        raise ValueError(f"q must be one of {_FLOATS}, got {dtype}")
-    _here(index, "q")
-    if q.dim() != 3:
-        raise ValueError(f"q must be (rows, heads, width), got {tuple(q.shape)}")
-    shape = q.shape
-    T, H, D = shape
-    qs, ks, kos, kp, kop = _rows(q, dtype, H, D, index, "q"), 0, 0, 0, 0
-    if k is not None:
-        ks, kp = _rows(k, dtype, H, D, index, "k"), k.data_ptr()
-        if k.shape[0] != T:
-            raise ValueError(f"k must have q's shape {tuple(shape)}, got {tuple(k.shape)}")
-    if table._device != index:
-        raise ValueError("table is on another device")
-    if outs is None:
-        qo = torch.empty(shape, dtype=dtype, device=q.device)
-        ko = None if k is None else torch.empty(shape, dtype=dtype, device=q.device)
-        qos = kos = H * D
-    else:
-        qo, ko = outs
-        if (ko is None) != (k is None):
-            raise ValueError("outs must match q and k")
-        qos = _rows(qo, dtype, H, D, index, "outs[0]")
-        if ko is not None:
-            kos = _rows(ko, dtype, H, D, index, "outs[1]")
-        if qo.shape[0] != T or (ko is not None and ko.shape[0] != T):
-            raise ValueError("outs must match q and k")
-    if ko is not None:
-        kop = ko.data_ptr()
-    st = load().hstu_attn_rope(q.data_ptr(), qs, kp, ks, qo.data_ptr(), qos, kop, kos,
-                               _ints(positions, (T,), index, "positions"), T, H, D, DTYPES[dtype], table._addr,
-                               1 if backward else 0, _raw_stream(stream, index))
-    if st != HSTU_OK:
-        _check(st, "hstu_attn_rope")
-    return qo, ko
+    qo, ko = (None, None) if outs is None else outs
+    r = _ext().rope(q, k, positions, table._addr, table._device, bool(backward), qo, ko, _raw_stream(stream))
+    if type(r) is int:
+        _check(r, "hstu_attn_rope")
+    return r
 
 
 class PagedCache:
@@ -704,18 +649,6 @@ class PagedCache:
                         self.dim, self.dim_v, DTYPES[dtype], int(e4m3))
         self._addr = ctypes.addressof(self._c)
         self._device = k.get_device()
-        self._ws_bytes = {}  # workspace sizes already asked for, by (batch, candidates, max_seqlen)
-
-    def workspace_bytes(self, batch: int, num_candidates: int, max_seqlen: int) -> int:
-        """hstu_attn_paged_workspace_size; a server asks for few different sizes."""
-        key = (batch, num_candidates, max_seqlen)
-        n = self._ws_bytes.get(key)
-        if n is None:
-            n = load().hstu_attn_paged_workspace_size(self._addr, batch, num_candidates, max_seqlen)
-            if len(self._ws_bytes) >= 1024:
-                self._ws_bytes.clear()
-            self._ws_bytes[key] = n
-        return n
 
 
 def alloc_cache(num_pages: int, page_size: int, heads: int, dim: int, dim_v: int = 0, dtype=torch.bfloat16,
@@ -728,22 +661,6 @@ def alloc_cache(num_pages: int, page_size: int, heads: int, dim: int, dim_v: int
     return PagedCache(k, v, new(*shape) if quantised else None, new(*shape) if quantised else None, dtype=dtype)
 
 
-def _pages(page_table, batch: int, index: int):
-    """Checks a page table; returns its address and width."""
-    shape = page_table.shape
-    if len(shape) != 2 or shape[0] != batch or shape[1] < 1:
-        raise ValueError(f"page_table must be (batch = {batch}, pages), got {tuple(shape)}")
-    return _ints(page_table, shape, index, "page_table"), shape[1]
-
-
-def _ws_args(ws, index: int):
-    if ws is None:
-        return 0, 0
-    if ws.get_device() != index:
-        _refuse(ws, None, None, index, "ws")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
-
-
 def cache_write(cache: PagedCache, k, v, seq_offsets, cache_lens, page_table, rope: Optional[RopeTable] = None,
                 positions=None, ws: Optional[torch.Tensor] = None, stream=None) -> None:
     """Appends the jagged rows k (T, H, D_qk) and v (T, H, D_v) to their
@@ -751,22 +668,9 @@ def cache_write(cache: PagedCache, k, v, seq_offsets, cache_lens, page_table, ro
     (hstu_attn_cache_write); ``rope`` rotates k on its way, by ``positions``
     or by its place in the cache. ``cache_lens`` is not changed. With a ``ws``
     (256 bytes) skipped rows are reported by ``device_status``."""
-    index = cache._device
-    _here(index, "cache")
-    ks = _rows(k, cache.dtype, cache.heads, cache.dim, index, "k")
-    vs = _rows(v, cache.dtype, cache.heads, cache.dim_v, index, "v")
-    T, B = k.shape[0], seq_offsets.numel() - 1
-    if v.shape[0] != T:
-        raise ValueError(f"k has {T} rows, v {v.shape[0]}")
-    if rope is not None and rope._device != index:
-        raise ValueError("rope is on another device")
-    table, width = _pages(page_table, B, index)
-    st = load().hstu_attn_cache_write(cache._addr, k.data_ptr(), ks, v.data_ptr(), vs,
-                                      _ints(seq_offsets, (B + 1,), index, "seq_offsets"), B, T,
-                                      _ints(cache_lens, (B,), index, "cache_lens"), table, width,
-                                      0 if rope is None else rope._addr,
-                                      0 if positions is None else _ints(positions, (T,), index, "positions"),
-                                      *_ws_args(ws, index), _raw_stream(stream, index))
+    st = _ext().cache_write(cache._addr, cache._device, k, v, seq_offsets, cache_lens, page_table,
+                            0 if rope is None else rope._addr, 0 if rope is None else rope._device, positions, ws,
+                            _raw_stream(stream))
     if st != HSTU_OK:
         _check(st, "hstu_attn_cache_write")
 
@@ -776,31 +680,17 @@ def cache_read(cache: PagedCache, seq_offsets, rows: int, page_table, starts=Non
     """(k, v) of cached rows, jagged and contiguous, in the cache's dtype
     (hstu_attn_cache_read): ``rows`` rows, those of sequence b from position
     ``starts[b]`` (0 without ``starts``)."""
-    index = cache._device
-    _here(index, "cache")
-    B = seq_offsets.numel() - 1
-    if outs is None:
-        k = torch.empty((rows, cache.heads, cache.dim), dtype=cache.dtype, device=cache.device)
-        v = torch.empty((rows, cache.heads, cache.dim_v), dtype=cache.dtype, device=cache.device)
-    else:
-        k, v = outs
-        for t, n, w in ((k, "outs[0]", cache.dim), (v, "outs[1]", cache.dim_v)):
-            _rows(t, cache.dtype, cache.heads, w, index, n)
-            if t.shape[0] != rows or not t.is_contiguous():
-                raise ValueError(f"{n} must be contiguous and have {rows} rows")
-    table, width = _pages(page_table, B, index)
-    st = load().hstu_attn_cache_read(cache._addr, k.data_ptr(), v.data_ptr(),
-                                     _ints(seq_offsets, (B + 1,), index, "seq_offsets"), B, rows,
-                                     0 if starts is None else _ints(starts, (B,), index, "starts"), table, width,
-                                     *_ws_args(ws, index), _raw_stream(stream, index))
-    if st != HSTU_OK:
-        _check(st, "hstu_attn_cache_read")
-    return k, v
+    k, v = (None, None) if outs is None else outs
+    r = _ext().cache_read(cache._addr, cache._device, seq_offsets, rows, page_table, starts, k, v, ws,
+                          _raw_stream(stream))
+    if type(r) is int:
+        _check(r, "hstu_attn_cache_read")
+    return r
 
 
 def paged_workspace(cache: PagedCache, batch: int, num_candidates: int, max_seqlen: int) -> torch.Tensor:
     """Workspace of ``fwd_paged``."""
-    n = cache.workspace_bytes(batch, num_candidates, max_seqlen)
+    n = load().hstu_attn_paged_workspace_size(cache._addr, batch, num_candidates, max_seqlen)
     if n == 0:
         raise HstuError(2, "hstu_attn_paged_workspace_size")
     return torch.empty(n, dtype=torch.uint8, device=cache.device)
@@ -813,37 +703,17 @@ def fwd_paged(q_c, cache: PagedCache, cache_lens, page_table, max_seqlen: int, a
     One candidate a sequence without ``cand_offsets``; all cached rows are
     visible without ``func_c`` (nfunc, C). With a ``ws`` (``paged_workspace``)
     of its own a caller can read ``device_status``."""
-    index, dtype = cache._device, cache.dtype
-    _here(index, "cache")
-    qs = _rows(q_c, dtype, cache.heads, cache.dim, index, "q_c")
-    C, B = q_c.shape[0], cache_lens.numel()
-    table, width = _pages(page_table, B, index)
-    nfunc = func = 0
-    if func_c is not None:
-        nfunc = func_c.shape[0]
-        func = _ints(func_c, (nfunc, C), index, "func_c")
-    if alpha is None:
-        alpha = 1.0 / math.sqrt(cache.dim)
-    if out is None:
-        out = torch.empty((C, cache.heads, cache.dim_v), dtype=dtype, device=cache.device)
-    else:
-        _rows(out, dtype, cache.heads, cache.dim_v, index, "out")
-        if out.shape[0] != C or not out.is_contiguous():
-            raise ValueError(f"out must be contiguous and have {C} rows")
-    lib = load()
-    own_ws, flags = None, 0
-    if ws is None:
-        flags = FLAG_NO_STATUS  # nobody could read it
-        n = cache.workspace_bytes(B, C, max_seqlen)
-        if n > 256:  # sums of splits; without them nothing but the error word
-            own_ws = ws = torch.empty(n, dtype=torch.uint8, device=cache.device)
-    st = lib.hstu_attn_fwd_paged(q_c.data_ptr(), qs, out.data_ptr(), cache._addr,
-                                 _ints(cache_lens, (B,), index, "cache_lens"), B, table, width,
-                                 0 if cand_offsets is None else _ints(cand_offsets, (B + 1,), index, "cand_offsets"),
-                                 C, func, nfunc, max_seqlen, alpha, *_ws_args(ws, index), flags,
-                                 _raw_stream(stream, index))
-    if st != HSTU_OK:
-        _check(st, "hstu_attn_fwd_paged")
-    if own_ws is not None and stream is not None:
-        own_ws.record_stream(stream)
-    return out
+    flags = 0
+    own = None
+    if stream is not None and ws is None:
+        # Allocated here, on the current stream, and used on another.
+        own = ws = paged_workspace(cache, cache_lens.numel(), q_c.shape[0], max_seqlen)
+        flags = FLAG_NO_STATUS
+    r = _ext().fwd_paged(cache._addr, cache._device, q_c, cache_lens, page_table, max_seqlen,
+                         1.0 / math.sqrt(cache.dim) if alpha is None else alpha, cand_offsets, func_c, ws, flags, out,
+                         _raw_stream(stream))
+    if own is not None:
+        own.record_stream(stream)
+    if type(r) is int:
+        _check(r, "hstu_attn_fwd_paged")
+    return r

@@ -5,8 +5,9 @@ same sources compiled with ``HSTU_CHECKED``: its kernels validate every
 work-list entry before using it (a debugging aid, results bit-identical).
 Every translation unit of both is compiled by nvcc in one parallel pool, then
 each set is linked into one shared library next to this file (the CUDA
-runtime is linked statically). A library newer than every source is not
-rebuilt.
+runtime is linked statically). ``_serving.so`` is the CPython extension of the
+serving calls, compiled beside them against the installed torch. A library
+newer than every source is not rebuilt.
 """
 from __future__ import annotations
 
@@ -23,6 +24,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_NAME = "libhstu_attn.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 CHECKED_LIB_PATH = os.path.join(PKG, "libhstu_attn_checked.so")
+EXT_SOURCE = "serving_ext.cpp"
+EXT_PATH = os.path.join(PKG, "_serving.so")
 # variant -> (library, object directory, extra nvcc flags)
 VARIANTS = {
     "release": (LIB_PATH, BUILD_DIR, []),
@@ -64,10 +67,30 @@ def up_to_date(lib: str = LIB_PATH) -> bool:
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
+def _build_extension() -> None:
+    import sysconfig
+
+    import torch
+    torch_dir = os.path.dirname(torch.__file__)
+    include = os.path.join(torch_dir, "include")
+    tmp = EXT_PATH + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", include, "-isystem", os.path.join(include, "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"),
+           "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, EXT_SOURCE), "-o", tmp,
+           "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {EXT_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, EXT_PATH)
+
+
 def build(force: bool = False, verbose: bool = False, variants=("release", "checked")) -> str:
     """Builds the requested variants; returns the release library's path."""
     todo = [v for v in variants if force or not up_to_date(VARIANTS[v][0])]
-    if not todo:
+    extension = force or not up_to_date(EXT_PATH)
+    if not todo and not extension:
         return LIB_PATH
     nvcc = _nvcc()
 
@@ -87,8 +110,11 @@ def build(force: bool = False, verbose: bool = False, variants=("release", "chec
     jobs = sorted({job_of(v, src) for v in todo for src in SOURCES})
     for v, _ in jobs:
         os.makedirs(VARIANTS[v][1], exist_ok=True)
-    with ThreadPoolExecutor(max_workers=min(len(jobs), max(os.cpu_count() or 1, len(SOURCES)))) as ex:
+    with ThreadPoolExecutor(max_workers=min(len(jobs), max(os.cpu_count() or 1, len(SOURCES))) + 1) as ex:
+        ext = ex.submit(_build_extension) if extension else None
         objs = dict(zip(jobs, ex.map(compile_one, jobs)))
+        if ext is not None:
+            ext.result()
     for v in todo:
         lib = VARIANTS[v][0]
         tmp = lib + ".tmp"

@@ -394,5 +394,7 @@ def test_the_binding_refuses_what_does_not_fit():
         hb.cache_write(c, k, v, off, lens, table, rope=hb.rope_table(128))
     with pytest.raises(ValueError):
         hb.cache_read(c, off, 3, table, outs=(k, k))
+    elsewhere = hb.alloc_cache(2, 16, 2, 64, 32)
+    elsewhere._device = torch.cuda.device_count()  # as if its tensors were on another device
     with pytest.raises(ValueError, match="current device"):
-        hb._here(torch.cuda.device_count(), "q")
+        hb.fwd_paged(q, elsewhere, lens, table, 40)
