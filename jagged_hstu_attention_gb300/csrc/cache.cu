@@ -13,6 +13,7 @@
 // into 8-bit pages and 90000 rows read back from them take 50 us, 5.7 TB/s, of
 // which the read is 43 us.
 #include "cache.cuh"
+#include "internal.h"
 #include "rope.cuh"
 
 namespace hstu {
@@ -133,6 +134,7 @@ __device__ __forceinline__ void write_chunks(Chunks u, const SlotColumns& k, boo
 // ROPE: 0 none, 1 half layout, 2 interleaved.
 template <typename T, bool E4M3, int ROPE, int HEADS>
 __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheParams p) {
+  chain();
   check_offsets(p);
   const int64_t unit = static_cast<int64_t>(blockIdx.x) * kCacheThreads + threadIdx.x;
   const int slot = static_cast<int>(unit) & (p.slots - 1);
@@ -189,6 +191,7 @@ __device__ __forceinline__ uint4 decode8(const uint2 codes, float scale) {
 
 template <typename T, bool E4M3, int HEADS>
 __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CacheParams p) {
+  chain();
   check_offsets(p);
   const int64_t unit = static_cast<int64_t>(blockIdx.x) * kCacheThreads + threadIdx.x;
   const int slot = static_cast<int>(unit) & (p.slots - 1);
@@ -268,34 +271,27 @@ static cudaError_t clear_header(void* ws, cudaStream_t stream) {
 }
 
 template <typename T, bool E4M3, int HEADS>
-static void launch_write(const CacheParams& p, dim3 grid, int rope, cudaStream_t stream) {
-  if (rope == 0) cache_write_kernel<T, E4M3, 0, HEADS><<<grid, kCacheThreads, 0, stream>>>(p);
-  else if (rope == 1) cache_write_kernel<T, E4M3, 1, HEADS><<<grid, kCacheThreads, 0, stream>>>(p);
-  else cache_write_kernel<T, E4M3, 2, HEADS><<<grid, kCacheThreads, 0, stream>>>(p);
-}
-
-template <typename T, bool E4M3>
-static void launch_write_heads(const CacheParams& p, dim3 grid, int rope, cudaStream_t stream) {
-  if (p.one_head) launch_write<T, E4M3, 1>(p, grid, rope, stream);
-  else launch_write<T, E4M3, kCacheHeads>(p, grid, rope, stream);
+static cudaError_t launch_write(const CacheParams& p, dim3 grid, int rope, cudaStream_t stream) {
+  void (*kernel)(CacheParams) = rope == 0   ? cache_write_kernel<T, E4M3, 0, HEADS>
+                                : rope == 1 ? cache_write_kernel<T, E4M3, 1, HEADS>
+                                            : cache_write_kernel<T, E4M3, 2, HEADS>;
+  return launch_chained(kernel, grid, kCacheThreads, 0, stream, p);
 }
 
 template <typename T>
-static void launch_write_typed(const CacheParams& p, dim3 grid, bool e4m3, int rope, cudaStream_t stream) {
-  if (e4m3) launch_write_heads<T, true>(p, grid, rope, stream);
-  else launch_write_heads<T, false>(p, grid, rope, stream);
-}
-
-template <typename T, bool E4M3>
-static void launch_read_heads(const CacheParams& p, dim3 grid, cudaStream_t stream) {
-  if (p.one_head) cache_read_kernel<T, E4M3, 1><<<grid, kCacheThreads, 0, stream>>>(p);
-  else cache_read_kernel<T, E4M3, kCacheHeads><<<grid, kCacheThreads, 0, stream>>>(p);
+static cudaError_t launch_write_typed(const CacheParams& p, dim3 grid, bool e4m3, int rope, cudaStream_t stream) {
+  if (p.one_head)
+    return e4m3 ? launch_write<T, true, 1>(p, grid, rope, stream) : launch_write<T, false, 1>(p, grid, rope, stream);
+  return e4m3 ? launch_write<T, true, kCacheHeads>(p, grid, rope, stream)
+              : launch_write<T, false, kCacheHeads>(p, grid, rope, stream);
 }
 
 template <typename T>
-static void launch_read_typed(const CacheParams& p, dim3 grid, bool e4m3, cudaStream_t stream) {
-  if (e4m3) launch_read_heads<T, true>(p, grid, stream);
-  else launch_read_heads<T, false>(p, grid, stream);
+static cudaError_t launch_read_typed(const CacheParams& p, dim3 grid, bool e4m3, cudaStream_t stream) {
+  void (*kernel)(CacheParams) =
+      p.one_head ? (e4m3 ? cache_read_kernel<T, true, 1> : cache_read_kernel<T, false, 1>)
+                 : (e4m3 ? cache_read_kernel<T, true, kCacheHeads> : cache_read_kernel<T, false, kCacheHeads>);
+  return launch_chained(kernel, grid, kCacheThreads, 0, stream, p);
 }
 
 }  // namespace hstu
@@ -333,11 +329,10 @@ HSTU_API hstu_status_t hstu_attn_cache_write(const hstu_cache_t* cache, const vo
   if (hstu::clear_header(ws, cs) != cudaSuccess) return HSTU_ERR_CUDA;
   if (rows == 0) return HSTU_OK;
   const int mode = rope ? (rope->interleaved ? 2 : 1) : 0;
-  if (cache->dtype == HSTU_DTYPE_F16)
-    hstu::launch_write_typed<__half>(p, grid, cache->e4m3 != 0, mode, cs);
-  else
-    hstu::launch_write_typed<__nv_bfloat16>(p, grid, cache->e4m3 != 0, mode, cs);
-  return cudaGetLastError() == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+  const cudaError_t e = cache->dtype == HSTU_DTYPE_F16
+                            ? hstu::launch_write_typed<__half>(p, grid, cache->e4m3 != 0, mode, cs)
+                            : hstu::launch_write_typed<__nv_bfloat16>(p, grid, cache->e4m3 != 0, mode, cs);
+  return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
 }
 
 HSTU_API hstu_status_t hstu_attn_cache_read(const hstu_cache_t* cache, void* k, void* v, const int32_t* seq_offsets,
@@ -356,11 +351,10 @@ HSTU_API hstu_status_t hstu_attn_cache_read(const hstu_cache_t* cache, void* k, 
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (hstu::clear_header(ws, cs) != cudaSuccess) return HSTU_ERR_CUDA;
   if (rows == 0) return HSTU_OK;
-  if (cache->dtype == HSTU_DTYPE_F16)
-    hstu::launch_read_typed<__half>(p, grid, cache->e4m3 != 0, cs);
-  else
-    hstu::launch_read_typed<__nv_bfloat16>(p, grid, cache->e4m3 != 0, cs);
-  return cudaGetLastError() == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+  const cudaError_t e = cache->dtype == HSTU_DTYPE_F16
+                            ? hstu::launch_read_typed<__half>(p, grid, cache->e4m3 != 0, cs)
+                            : hstu::launch_read_typed<__nv_bfloat16>(p, grid, cache->e4m3 != 0, cs);
+  return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -25,6 +25,29 @@ cudaError_t ensure_smem_limit(Kernel kernel, int smem, std::atomic<uint64_t>& do
   return e;
 }
 
+// Serving kernels follow one another in a stream, each a few microseconds long.
+// They are launched so that a kernel's blocks may be placed while the one
+// before it ends; every block begins with chain(), which waits until that one
+// has completed and its writes are visible, and lets the next launch begin.
+template <typename... Params, typename... Args>
+cudaError_t launch_chained(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t stream,
+                           const Args&... args) {
+  cudaLaunchAttribute overlap{};
+  overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  overlap.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t config{};
+  config.gridDim = grid;
+  config.blockDim = dim3(threads);
+  config.dynamicSmemBytes = smem;
+  config.stream = stream;
+  config.attrs = &overlap;
+  config.numAttrs = 1;
+  return cudaLaunchKernelEx(&config, kernel, args...);
+}
+__device__ __forceinline__ void chain() {
+  asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+}
+
 cudaError_t launch_plan(const PlanParams& p, cudaStream_t stream);
 // grid_items: upper bound on the number of work items (CTAs = items * heads).
 // One translation unit per input type keeps the many kernel variants

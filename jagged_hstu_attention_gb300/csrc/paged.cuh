@@ -734,7 +734,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedSizes<DQ, DV, E4M3, MANY>:
   __shared__ int iv[(MANY ? kPagedPass : 1) * kPagedIv];
   __shared__ int sh_entries;
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  chain();
   const int tid = threadIdx.x;
   const int64_t bid = blockIdx.x;
   // One candidate a sequence: first splits first, so that the last CTAs to start
@@ -860,7 +860,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedSizes<DQ, DV, E4M3, MANY>:
 // is left alone.
 template <typename T, int DV, int WARPS>
 __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  chain();
   constexpr int kUnits = 8 / WARPS;  // (candidate, head) of a block
   __shared__ float4 red[8][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -922,23 +922,14 @@ cudaError_t launch_paged_one(const PagedParams& p, unsigned blocks, cudaStream_t
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = ensure_smem_limit(paged_kernel<T, DQ, DV, E4M3, MANY>, kSmem, done);
   if (e != cudaSuccess) return e;
-  paged_kernel<T, DQ, DV, E4M3, MANY><<<blocks, kPagedThreads, kSmem, stream>>>(p);
-  return cudaGetLastError();
+  return launch_chained(paged_kernel<T, DQ, DV, E4M3, MANY>, dim3(blocks), kPagedThreads, kSmem, stream, p);
 }
 
 template <typename T, int DV, int WARPS>
 cudaError_t launch_paged_join(const PagedParams& p, cudaStream_t stream) {
   const int64_t units = static_cast<int64_t>(p.num_cand) * p.cache.heads;
-  cudaLaunchAttribute overlap{};
-  overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  overlap.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t config{};
-  config.gridDim = dim3(static_cast<unsigned>((units + 8 / WARPS - 1) / (8 / WARPS)));
-  config.blockDim = dim3(256);
-  config.stream = stream;
-  config.attrs = &overlap;
-  config.numAttrs = 1;
-  return cudaLaunchKernelEx(&config, paged_join_kernel<T, DV, WARPS>, p);
+  const dim3 grid(static_cast<unsigned>((units + 8 / WARPS - 1) / (8 / WARPS)));
+  return launch_chained(paged_join_kernel<T, DV, WARPS>, grid, 256, 0, stream, p);
 }
 template <typename T, bool E4M3, int DQ, int DV>
 cudaError_t launch_paged_widths(const PagedParams& p, unsigned blocks, cudaStream_t stream) {

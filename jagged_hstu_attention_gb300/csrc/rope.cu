@@ -15,6 +15,7 @@
 // (6.3 TB/s). A step of 64 tokens takes 2.6 us, the time of an empty launch.
 #include <cmath>
 
+#include "internal.h"
 #include "rope.cuh"
 
 namespace hstu {
@@ -35,6 +36,7 @@ struct RopeParams {
 
 template <typename T, int D, int HPT, bool INTERLEAVED>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
+  chain();
   constexpr int kSlots = D / 16;
   const int64_t unit = static_cast<int64_t>(blockIdx.x) * kRopeThreads + threadIdx.x;
   const int64_t token = unit / kSlots;
@@ -77,9 +79,8 @@ template <typename T, int D, int HPT>
 static cudaError_t launch_rope(const RopeParams& p, bool interleaved, cudaStream_t stream) {
   const int64_t blocks = (p.tokens * (D / 16) + kRopeThreads - 1) / kRopeThreads;
   const dim3 grid(static_cast<unsigned>(blocks), (p.heads + HPT - 1) / HPT);
-  if (interleaved) rope_kernel<T, D, HPT, true><<<grid, kRopeThreads, 0, stream>>>(p);
-  else rope_kernel<T, D, HPT, false><<<grid, kRopeThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_chained(interleaved ? rope_kernel<T, D, HPT, true> : rope_kernel<T, D, HPT, false>, grid, kRopeThreads,
+                        0, stream, p);
 }
 
 template <typename T, int D>
