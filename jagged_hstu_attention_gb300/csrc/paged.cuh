@@ -125,6 +125,14 @@ __device__ __forceinline__ void load_piece(const uint8_t* p, uint32_t* w) {
   }
 }
 
+// Four 8 x 8 blocks of 16-bit values, each transposed: lane l gives the address
+// of row l % 8 of block l / 8.
+__device__ __forceinline__ void load_transposed(uint32_t addr, uint32_t (&w)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "r"(addr));
+}
+
 // Asynchronous copy of 16 bytes; zeros where not live (src is not read then).
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
@@ -173,8 +181,9 @@ struct PagedSizes {
   // The warps' sums, after the ring's use. A lane (g, t) writes VE columns of
   // each piece of row t: blocks of VE + 1 and rows of 8 (mod 32) put the
   // lanes' stores into different banks.
+  // (16-bit pages: columns g and g + 8 of each 16, no padding needed.)
   static constexpr int kBlock = VE + 1;
-  static constexpr int kRedRow = (VP * 8 * kBlock + 31) / 32 * 32 + 8;
+  static constexpr int kRedRow = E4M3 ? (VP * 8 * kBlock + 31) / 32 * 32 + 8 : DV + 8;
   static constexpr int kRedRows = MANY ? 16 : 4;  // of a warp
   static constexpr int kRed = kPagedWarps * kRedRows * kRedRow * 4;
   static constexpr int kSmem = kRing > kRed ? kRing : kRed;
@@ -184,7 +193,12 @@ struct PagedSizes {
   static constexpr int kRegisters = 80 + DV / 2 + DQ / 4 * (E4M3 ? 2 : 1);
   static constexpr int kWant = !MANY ? 4 : (kRegisters <= 102 ? 5 : (kRegisters <= 128 ? 4 : 3));
   static constexpr int kResident = kFit < 1 ? 1 : (kFit > kWant ? kWant : kFit);
-  static __device__ __forceinline__ int red_column(int d) { return d / VE * kBlock + d % VE; }
+  static __device__ __forceinline__ int red_column(int d) { return E4M3 ? d / VE * kBlock + d % VE : d; }
+  // Permutation of the 16-byte pieces of v row r.
+  static __device__ __forceinline__ int v_swizzle(int r) {
+    if (!E4M3) return VC >= 8 ? r & 7 : (r >> 1) & 3;
+    return VC >= 8 ? r & 6 : (VC == 4 ? (r >> 1) & 3 : 0);
+  }
 };
 
 extern __shared__ __align__(128) uint8_t paged_ring[];
@@ -402,8 +416,7 @@ __device__ __forceinline__ int paged_pass(const PagedParams& p, const PagedSplit
 #pragma unroll
       for (int i = 0; i < VROW / 32; ++i) {
         const int u = i * 32 + lane, r = u / VC, c = u % VC;
-        const int sw = VC >= 8 ? r & 6 : (VC == 4 ? (r >> 1) & 3 : 0);
-        copy16(dst + kPagedTile * KROW + r * VROW + (c ^ sw) * 16, vsrc + i * 512, r < nkeys);
+        copy16(dst + kPagedTile * KROW + r * VROW + (c ^ Z::v_swizzle(r)) * 16, vsrc + i * 512, r < nkeys);
       }
       if (E4M3 && lane < 2)
         copy16(dst + kPagedTile * (KROW + VROW) + 16 * lane, (lane ? p.cache.v_scale : p.cache.k_scale) + row0, true);
@@ -655,32 +668,39 @@ __device__ __forceinline__ int paged_pass(const PagedParams& p, const PagedSplit
           if (!kPair) mma16816<M>(acc[n][m], a0, a1, a2, a3, bl[n][0], bl[n][1]);
         }
       };
+      if (E4M3) {
 #pragma unroll
-      for (int i = 0; i < VP; ++i) {
-        uint32_t vw[4][VB / 4];
+        for (int i = 0; i < VP; ++i) {
+          uint32_t vw[4][VB / 4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = 2 * t + (r & 1) + 8 * (r >> 1);
-          const int sw = VC >= 8 ? row & 6 : (VC == 4 ? (row >> 1) & 3 : 0);
-          const int byte = i * 8 * VB + g * VB;
-          load_piece<VB>(vt + row * VROW + ((byte >> 4) ^ sw) * 16 + (byte & 15), vw[r]);
-        }
+          for (int r = 0; r < 4; ++r) {
+            const int row = 2 * t + (r & 1) + 8 * (r >> 1);
+            const int byte = i * 8 * VB + g * VB;
+            load_piece<VB>(vt + row * VROW + ((byte >> 4) ^ Z::v_swizzle(row)) * 16 + (byte & 15), vw[r]);
+          }
 #pragma unroll
-        for (int w = 0; w < VB / 4; ++w) {
-          if (E4M3) {
+          for (int w = 0; w < VB / 4; ++w) {
             // bytes (row 0, row 1) of columns 4w, 4w+1 and 4w+2, 4w+3
             const uint32_t x0 = __byte_perm(vw[0][w], vw[1][w], 0x5140);
             const uint32_t x1 = __byte_perm(vw[0][w], vw[1][w], 0x7362);
             const uint32_t y0 = __byte_perm(vw[2][w], vw[3][w], 0x5140);
             const uint32_t y1 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
-            const int m = i * VE / 2 + 2 * w;
+            const int m = E4M3 ? i * VE / 2 + 2 * w : 0;
             add(m, e4m3x2_to_f16x2(x0), e4m3x2_hi_to_f16x2(x0), e4m3x2_to_f16x2(y0), e4m3x2_hi_to_f16x2(y0));
-            add(E4M3 ? m + 1 : m, e4m3x2_to_f16x2(x1), e4m3x2_hi_to_f16x2(x1), e4m3x2_to_f16x2(y1),
+            add(E4M3 ? m + 1 : 0, e4m3x2_to_f16x2(x1), e4m3x2_hi_to_f16x2(x1), e4m3x2_to_f16x2(y1),
                 e4m3x2_hi_to_f16x2(y1));
-          } else {
-            add(i * VE / 2 + w, __byte_perm(vw[0][w], vw[1][w], 0x5410), __byte_perm(vw[0][w], vw[1][w], 0x7632),
-                __byte_perm(vw[2][w], vw[3][w], 0x5410), __byte_perm(vw[2][w], vw[3][w], 0x7632));
           }
+        }
+      } else {
+        // Columns 16m .. 16m + 15 of the 16 rows, transposed on their way: lane
+        // l gives row (l & 7) + 8 (l >> 4), columns 8 ((l >> 3) & 1) on.
+        const int row = (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
+        const uint32_t from = smem_u32(vt) + row * VROW;
+#pragma unroll
+        for (int m = 0; m < VTILES; ++m) {
+          uint32_t v[4];
+          load_transposed(from + ((2 * m + half) ^ Z::v_swizzle(row)) * 16, v);
+          add(m, v[0], v[1], v[2], v[3]);
         }
       }
     }
@@ -697,15 +717,17 @@ __device__ __forceinline__ int paged_pass(const PagedParams& p, const PagedSplit
     const float back = kHalf ? __uint_as_float(static_cast<uint32_t>(erun[c] - 14) << 23) : 1.0f;
     bool finite = true;
     if (r < ncand) {
-      float* row = mine + r * Z::kRedRow + g * Z::kBlock;
+      float* row = mine + r * Z::kRedRow;
 #pragma unroll
-      for (int i = 0; i < VP; ++i)
+      for (int m = 0; m < VTILES; ++m)
 #pragma unroll
-        for (int e = 0; e < VE; ++e) {
-          const float(&a)[4] = acc[kPair ? 0 : c / 2][i * VE / 2 + e / 2];
-          const float u = (kPair ? a[2 * (e & 1)] + a[2 * (e & 1) + 1] : a[2 * (e & 1) + (c & 1)]) * back;
+        for (int e = 0; e < 2; ++e) {
+          const float(&a)[4] = acc[kPair ? 0 : c / 2][m];
+          const float u = (kPair ? a[2 * e] + a[2 * e + 1] : a[2 * e + (c & 1)]) * back;
           finite = finite && fabsf(u) <= kMaxFinite;
-          row[i * 8 * Z::kBlock + e] = u;
+          // 8-bit pages: column 2 (m % (VE / 2)) + e of this lane's piece m / (VE / 2)
+          const int at = E4M3 ? (m / (VE / 2) * 8 + g) * Z::kBlock + m % (VE / 2) * 2 + e : 16 * m + 8 * e + g;
+          row[at] = u;
         }
     }
     // A sum that is not finite may have met a value that its candidate does
