@@ -8,7 +8,7 @@
 // shuffles away.
 //
 // Bound by memory: 86000 rows (4 heads of 128) into 16-bit pages, k rotated, take
-// 59 us, 6.0 TB/s; with a thread for each (row, head, slot), which searched its
+// 56 us, 6.2 TB/s; with a thread for each (row, head, slot), which searched its
 // sequence and computed its cosines alone, they took 100 us. A chunk of 3500 rows
 // into 8-bit pages and 90000 rows read back from them take 50 us, 5.7 TB/s, of
 // which the read is 43 us.
@@ -18,7 +18,10 @@
 
 namespace hstu {
 
-constexpr int kCacheThreads = 256;
+// Threads of a block. (86000 rows written take 56 us with 128 threads and 58
+// us with 256, whose registers leave an SM two blocks; 90000 rows read back take
+// 2 us less with 256.)
+constexpr int kWriteThreads = 128, kReadThreads = 256;
 constexpr int kCacheHeads = 4;  // heads of a thread where there are rows enough to fill the GPU
 
 struct CacheParams {
@@ -65,7 +68,7 @@ __device__ __forceinline__ bool place_row(const CacheParams& p, int64_t t, int64
 __device__ __forceinline__ void check_offsets(const CacheParams& p) {
   if (!p.header || blockIdx.x != 0) return;
   bool bad = p.seq_offsets[0] != 0 || static_cast<int64_t>(p.seq_offsets[p.batch]) != p.rows;
-  for (int b = threadIdx.x; b < p.batch; b += kCacheThreads) bad |= p.seq_offsets[b] > p.seq_offsets[b + 1];
+  for (int b = threadIdx.x; b < p.batch; b += blockDim.x) bad |= p.seq_offsets[b] > p.seq_offsets[b + 1];
   if (bad) atomicOr(p.header + kHdrErr, kErrInput);
 }
 
@@ -133,10 +136,10 @@ __device__ __forceinline__ void write_chunks(Chunks u, const SlotColumns& k, boo
 
 // ROPE: 0 none, 1 half layout, 2 interleaved.
 template <typename T, bool E4M3, int ROPE, int HEADS>
-__global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheParams p) {
+__global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(const CacheParams p) {
   chain();
   check_offsets(p);
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kCacheThreads + threadIdx.x;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   const int slot = static_cast<int>(unit) & (p.slots - 1);
   const int64_t row = unit / p.slots;
   const int h0 = blockIdx.y * HEADS, heads = min(HEADS, p.cache.heads - h0);
@@ -190,10 +193,10 @@ __device__ __forceinline__ uint4 decode8(const uint2 codes, float scale) {
 }
 
 template <typename T, bool E4M3, int HEADS>
-__global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CacheParams p) {
+__global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const CacheParams p) {
   chain();
   check_offsets(p);
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kCacheThreads + threadIdx.x;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   const int slot = static_cast<int>(unit) & (p.slots - 1);
   const int64_t row = unit / p.slots;
   int64_t pos, page;
@@ -240,7 +243,7 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CachePa
 
 static hstu_status_t cache_common(const hstu_cache_t* cache, const int32_t* seq_offsets, int32_t batch, int64_t rows,
                                   const int32_t* starts, const int32_t* page_table, int32_t max_pages, void* ws,
-                                  size_t ws_bytes, CacheParams* p, dim3* grid) {
+                                  size_t ws_bytes, int threads, CacheParams* p, dim3* grid) {
   *p = CacheParams{};
   const hstu_status_t st = check_cache(cache, &p->cache);
   if (st != HSTU_OK) return st;
@@ -250,10 +253,10 @@ static hstu_status_t cache_common(const hstu_cache_t* cache, const int32_t* seq_
     return HSTU_ERR_INVALID_ARG;
   if (ws && (reinterpret_cast<uintptr_t>(ws) % 256 != 0 || ws_bytes < kHdrWords * 4)) return HSTU_ERR_WORKSPACE;
   p->slots = (p->cache.dim > p->cache.dim_v ? p->cache.dim : p->cache.dim_v) / 16;
-  const int64_t blocks = (rows * p->slots + kCacheThreads - 1) / kCacheThreads;
-  // A thread for each head while that does not fill the GPU (152 SMs of four
-  // such blocks): the heads of a call with few rows are then moved at once.
-  p->one_head = blocks * p->cache.heads <= 152 * 4;
+  const int64_t blocks = (rows * p->slots + threads - 1) / threads;
+  // A thread for each head while that does not fill the GPU (1024 threads on each
+  // of 152 SMs): the heads of a call with few rows are then moved at once.
+  p->one_head = blocks * p->cache.heads * threads <= 152 * 1024;
   *grid = dim3(static_cast<unsigned>(blocks),
                p->one_head ? p->cache.heads : (p->cache.heads + kCacheHeads - 1) / kCacheHeads);
   p->seq_offsets = seq_offsets;
@@ -275,7 +278,7 @@ static cudaError_t launch_write(const CacheParams& p, dim3 grid, int rope, cudaS
   void (*kernel)(CacheParams) = rope == 0   ? cache_write_kernel<T, E4M3, 0, HEADS>
                                 : rope == 1 ? cache_write_kernel<T, E4M3, 1, HEADS>
                                             : cache_write_kernel<T, E4M3, 2, HEADS>;
-  return launch_chained(kernel, grid, kCacheThreads, 0, stream, p);
+  return launch_chained(kernel, grid, kWriteThreads, 0, stream, p);
 }
 
 template <typename T>
@@ -291,7 +294,7 @@ static cudaError_t launch_read_typed(const CacheParams& p, dim3 grid, bool e4m3,
   void (*kernel)(CacheParams) =
       p.one_head ? (e4m3 ? cache_read_kernel<T, true, 1> : cache_read_kernel<T, false, 1>)
                  : (e4m3 ? cache_read_kernel<T, true, kCacheHeads> : cache_read_kernel<T, false, kCacheHeads>);
-  return launch_chained(kernel, grid, kCacheThreads, 0, stream, p);
+  return launch_chained(kernel, grid, kReadThreads, 0, stream, p);
 }
 
 }  // namespace hstu
@@ -306,7 +309,8 @@ HSTU_API hstu_status_t hstu_attn_cache_write(const hstu_cache_t* cache, const vo
   hstu::CacheParams p;
   dim3 grid;
   hstu_status_t st =
-      hstu::cache_common(cache, seq_offsets, batch, rows, cache_lens, page_table, max_pages, ws, ws_bytes, &p, &grid);
+      hstu::cache_common(cache, seq_offsets, batch, rows, cache_lens, page_table, max_pages, ws, ws_bytes,
+                         hstu::kWriteThreads, &p, &grid);
   if (st != HSTU_OK) return st;
   if (!cache_lens || reinterpret_cast<uintptr_t>(positions) % 4 != 0 || (positions && !rope))
     return HSTU_ERR_INVALID_ARG;
@@ -342,7 +346,8 @@ HSTU_API hstu_status_t hstu_attn_cache_read(const hstu_cache_t* cache, void* k, 
   hstu::CacheParams p;
   dim3 grid;
   const hstu_status_t st =
-      hstu::cache_common(cache, seq_offsets, batch, rows, starts, page_table, max_pages, ws, ws_bytes, &p, &grid);
+      hstu::cache_common(cache, seq_offsets, batch, rows, starts, page_table, max_pages, ws, ws_bytes,
+                         hstu::kReadThreads, &p, &grid);
   if (st != HSTU_OK) return st;
   const auto bad = [](const void* q) { return !q || reinterpret_cast<uintptr_t>(q) % 16 != 0; };
   if (rows > 0 && (bad(k) || bad(v))) return HSTU_ERR_INVALID_ARG;

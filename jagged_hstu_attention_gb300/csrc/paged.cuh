@@ -14,9 +14,9 @@
 //
 // Measured, H = 4, D_qk = D_v = 128, histories of 1332 to 3994 rows: one
 // candidate for each of 256 users over 16-bit pages 207 us, 6.8 TB/s, the rate of
-// a plain copy; over 8-bit pages 119 us, 5.9 TB/s, with the issue slots half
-// used by the codes' conversion and two waves of latency at the ends. 0 to 48
-// candidates for each of 64 users of 512 to 2048 rows: 67 us against 25 us for
+// a plain copy; over 8-bit pages 118 us, 6.0 TB/s, with the issue slots half
+// used by the codes' conversion and the latency of the first and last CTAs. 0 to 48
+// candidates for each of 64 users of 512 to 2048 rows: 66 us against 25 us for
 // the bytes, bound by the latency of the chain from scores to weights in the
 // twelve warps that registers leave an SM.
 //
@@ -38,13 +38,14 @@
 // Operand layout. The order of the columns inside a contraction is free as
 // long as both operands share it, so each lane reads whole 16-byte pieces of
 // a row: lane (g, t) = (lane / 4, lane % 4) takes columns [8t, 8t + 8) of
-// each 32 of key rows g and g + 8, which are its parts of two k = 16 steps,
-// and the same columns of candidate row g. For V^T it reads piece g of the key
-// rows 2t, 2t+1, 2t+8, 2t+9 and pairs the rows' columns with byte
-// permutations. P^T comes out of the first product with keys along g and is
-// turned by movmatrix, 8 x 8 values an instruction. In shared memory the
-// 16-byte pieces of a row are permuted by bits of the row's index so that the
-// eight lanes of a load phase meet different banks.
+// each 32 of key rows g and g + 8, which are its parts of two k = 16 steps, and
+// the same columns of candidate row g. 16-bit value rows are transposed by
+// ldmatrix. Of 8-bit ones the lane reads piece g of the key rows 2t, 2t+1, 2t+8,
+// 2t+9 and pairs the rows' columns with byte permutations. P^T comes out of the
+// first product with keys along g and is turned by movmatrix, 8 x 8 values an
+// instruction. In shared memory the 16-byte pieces of a row are permuted by
+// bits of the row's index so that the lanes of a load phase meet different
+// banks.
 //
 // Types. 16-bit caches multiply in their own type. 8-bit codes become fp16
 // (exact); a bf16 candidate row is then scaled by a power of two and split
@@ -52,7 +53,7 @@
 // multiplies its column of S, a value row's scale its column of P, both exact
 // powers of two. In fp16 the range of P needs care: a candidate's P is scaled
 // by a power of two that follows its running maximum (when it grows, the sums
-// so far are scaled down), which leaves 50 bits below the largest term.
+// so far are scaled down), which leaves 39 bits below the largest term.
 #pragma once
 
 #include <type_traits>

@@ -10,9 +10,9 @@
 // its cosine and sine.
 //
 // Bound by memory: q and k of 81920 tokens (4 heads of 128), forward and
-// backward, take 103 us, 6.5 TB/s, 96% of a plain copy; 32749 tokens of 8 heads
-// in fp16, half of each head rotated, read from rows four times as long, 43 us
-// (6.3 TB/s). A step of 64 tokens takes 2.6 us, the time of an empty launch.
+// backward, take 101.5 us, 6.6 TB/s, 97% of a plain copy; 32749 tokens of 8 heads
+// in fp16, half of each head rotated, read from rows four times as long, 42 us
+// (6.4 TB/s). A step of 64 tokens takes 2.2 us, about the time of an empty launch.
 #include <cmath>
 
 #include "internal.h"
@@ -20,7 +20,7 @@
 
 namespace hstu {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 constexpr int kRopeHeads = 4;  // heads of a thread where there are tokens enough to fill the GPU
 
 struct RopeParams {
@@ -85,10 +85,10 @@ static cudaError_t launch_rope(const RopeParams& p, bool interleaved, cudaStream
 
 template <typename T, int D>
 static cudaError_t launch_rope_heads(const RopeParams& p, bool interleaved, cudaStream_t stream) {
-  // A thread for each head while that does not fill the GPU (152 SMs of four
-  // such blocks).
+  // A thread for each head while that does not fill the GPU (1024 threads on each
+  // of 152 SMs).
   const int64_t blocks = (p.tokens * (D / 16) + kRopeThreads - 1) / kRopeThreads;
-  if (blocks * p.heads <= 152 * 4) return launch_rope<T, D, 1>(p, interleaved, stream);
+  if (blocks * p.heads * kRopeThreads <= 152 * 1024) return launch_rope<T, D, 1>(p, interleaved, stream);
   return launch_rope<T, D, kRopeHeads>(p, interleaved, stream);
 }
 
