@@ -64,8 +64,8 @@
 
 namespace hstu {
 
-constexpr int kPagedWarps = 4;
-constexpr int kPagedThreads = 32 * kPagedWarps;
+constexpr int kPagedWarps = 4;       // of a CTA
+constexpr int kPagedWarpsWide = 8;  // and where there is no more than one CTA an SM
 constexpr int kPagedTile = 16;     // keys of a warp's step
 constexpr int kPagedPass = 64;     // candidates of a pass, at most
 constexpr int kPagedMaxSplit = 4096;  // keys of a split, at most
@@ -163,8 +163,9 @@ __device__ __forceinline__ float cached_value(const void* base, int64_t i) {
 
 // Sizes that follow from the types and widths. MANY: the kernel for any number
 // of candidates; otherwise the one for a single candidate a sequence.
-template <int DQ, int DV, bool E4M3, bool MANY>
+template <int DQ, int DV, bool E4M3, bool MANY, int W = kPagedWarps>
 struct PagedSizes {
+  static constexpr int kWarps = W, kThreads = 32 * W;
   static constexpr int ES = E4M3 ? 1 : 2;               // bytes of a cached element
   static constexpr int KROW = DQ * ES, VROW = DV * ES;  // bytes of a cached row
   static constexpr int KC = KROW / 16, VC = VROW / 16;  // 16-byte pieces of a row
@@ -178,7 +179,7 @@ struct PagedSizes {
   // (48 KB); two stages where the warps of a slice share tiles, whose products
   // take longer than the copies.
   static constexpr int kStages = kStep <= 2080 ? 4 : (MANY && kStep >= 4096) || kStep == 6144 ? 2 : 3;
-  static constexpr int kRing = kPagedWarps * kStages * kStep;
+  static constexpr int kRing = W * kStages * kStep;
   // The warps' sums, after the ring's use. A lane (g, t) writes VE columns of
   // each piece of row t: blocks of VE + 1 and rows of 8 (mod 32) put the
   // lanes' stores into different banks.
@@ -186,13 +187,13 @@ struct PagedSizes {
   static constexpr int kBlock = VE + 1;
   static constexpr int kRedRow = E4M3 ? (VP * 8 * kBlock + 31) / 32 * 32 + 8 : DV + 8;
   static constexpr int kRedRows = MANY ? 16 : 4;  // of a warp
-  static constexpr int kRed = kPagedWarps * kRedRows * kRedRow * 4;
+  static constexpr int kRed = W * kRedRows * kRedRow * 4;
   static constexpr int kSmem = kRing > kRed ? kRing : kRed;
   // CTAs of an SM: as many as shared memory has room for, up to 4 (3 to 5 for
   // many candidates, whose sums and fragments are most of the registers).
   static constexpr int kFit = 227 * 1024 / (kSmem + 6144);
   static constexpr int kRegisters = 80 + DV / 2 + DQ / 4 * (E4M3 ? 2 : 1);
-  static constexpr int kWant = !MANY ? 4 : (kRegisters <= 102 ? 5 : (kRegisters <= 128 ? 4 : 3));
+  static constexpr int kWant = !MANY ? (W == kPagedWarps ? 4 : 2) : (kRegisters <= 102 ? 5 : (kRegisters <= 128 ? 4 : 3));
   static constexpr int kResident = kFit < 1 ? 1 : (kFit > kWant ? kWant : kFit);
   static __device__ __forceinline__ int red_column(int d) { return E4M3 ? d / VE * kBlock + d % VE : d; }
   // Permutation of the 16-byte pieces of v row r.
@@ -327,7 +328,7 @@ __device__ __forceinline__ int paged_key(const PagedParams& p, const PagedSplit&
 
 // The sum of candidate r of the pass over the tiles of one slice, in fp32, one
 // visible key after the other: the way out for sums that are not finite. The
-// slice takes entries [first, first + count), and so on every four entries.
+// slice takes entries [first, first + count), and so on every `Z::kWarps` entries.
 template <typename T, int DQ, int DV, bool E4M3, typename Z>
 __device__ __noinline__ void paged_scalar_sum(const PagedParams& p, const PagedSplit& sp, int r, int first, int count,
                                               int entries, float* out) {
@@ -337,7 +338,7 @@ __device__ __noinline__ void paged_scalar_sum(const PagedParams& p, const PagedS
   float sum[DV / 32];
   for (int i = 0; i < DV / 32; ++i) sum[i] = 0.0f;
   for (int e = first; e < entries;
-       e = (e + 1 - first) % kPagedWarps < count ? e + 1 : e + 1 + kPagedWarps - count) {
+       e = (e + 1 - first) % Z::kWarps < count ? e + 1 : e + 1 + Z::kWarps - count) {
     const int key0 = paged_key(p, sp, e);
     const int64_t row0 = cache_row(p.cache, sp.pages[(key0 >> p.cache.page_shift) - sp.page0], sp.h,
                                    key0 & ((1 << p.cache.page_shift) - 1));
@@ -370,10 +371,10 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t w) {
 // each of up to 4 candidates; otherwise two groups of eight columns a warp (the
 // second idle where a warp has 8 candidates or fewer). Returns the warps of a
 // slice.
-template <typename T, int DQ, int DV, bool E4M3, bool MANY, bool PAIR>
+template <typename T, int DQ, int DV, bool E4M3, bool MANY, int W, bool PAIR>
 __device__ __forceinline__ int paged_pass(const PagedParams& p, const PagedSplit& sp,
                                           const int (&raw)[2 * kMaxIntervals - 1]) {
-  using Z = PagedSizes<DQ, DV, E4M3, MANY>;
+  using Z = PagedSizes<DQ, DV, E4M3, MANY, W>;
   constexpr bool kPair = PAIR;
   constexpr bool kHalf = E4M3 || std::is_same<T, __half>::value;  // products in fp16
   constexpr bool kSplitQ = E4M3 && !std::is_same<T, __half>::value;
@@ -389,13 +390,13 @@ __device__ __forceinline__ int paged_pass(const PagedParams& p, const PagedSplit
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int total = sp.ce - sp.c0;
   const int wg = kPair ? 1 : paged_slice(total);
-  const int nslices = kPagedWarps / wg, slice = warp / wg, gi = warp % wg;
+  const int nslices = W / wg, slice = warp / wg, gi = warp % wg;
   const int cg = gi * ROWS;                                        // this warp's first candidate in the pass
   const int ncand = max(0, min(ROWS, total - cg));
   const int groups = kPair ? 1 : (ncand > 8 ? 2 : 1);              // column groups in use
   const int entries = p.func ? paged_list<MANY>(p, sp, min(total, wg * ROWS), raw) : sp.tiles;
   // Copy n of this warp is list entry (n nslices + slice) wg + gi.
-  const int iters = (entries + kPagedWarps - 1) / kPagedWarps;
+  const int iters = (entries + W - 1) / W;
 
   const uint32_t ring = sp.ring + slice * S * wg * Z::kStep;  // the slice's stages
   const auto issue = [&](int n, int stage) {
@@ -747,10 +748,10 @@ __device__ __forceinline__ int paged_pass(const PagedParams& p, const PagedSplit
 
 // T: type of q, o and 16-bit pages. E4M3: 8-bit pages. MANY: any number of
 // candidates, else one a sequence.
-template <typename T, int DQ, int DV, bool E4M3, bool MANY>
-__global__ void __launch_bounds__(kPagedThreads, PagedSizes<DQ, DV, E4M3, MANY>::kResident)
+template <typename T, int DQ, int DV, bool E4M3, bool MANY, int W>
+__global__ void __launch_bounds__(32 * W, PagedSizes<DQ, DV, E4M3, MANY, W>::kResident)
     paged_kernel(const PagedParams p) {
-  using Z = PagedSizes<DQ, DV, E4M3, MANY>;
+  using Z = PagedSizes<DQ, DV, E4M3, MANY, W>;
   __shared__ int pages[kPagedMaxSplit / kPagedTile];
   __shared__ uint32_t bits[2 * kPagedWords];
   __shared__ uint16_t list[kPagedMaxSplit / kPagedTile];
@@ -781,11 +782,11 @@ __global__ void __launch_bounds__(kPagedThreads, PagedSizes<DQ, DV, E4M3, MANY>:
   // length are not looked at).
   const int page0 = k0 >> p.cache.page_shift;
   const int most_pages = min(((k0 + keys - 1) >> p.cache.page_shift) - page0 + 1, p.max_pages - page0);
-  constexpr int kPageLoads = kPagedMaxSplit / kPagedTile / kPagedThreads;
+  constexpr int kPageLoads = kPagedMaxSplit / kPagedTile / Z::kThreads;
   int page[kPageLoads];
 #pragma unroll
   for (int i = 0; i < kPageLoads; ++i) {
-    const int at = i * kPagedThreads + tid;
+    const int at = i * Z::kThreads + tid;
     page[i] = at < most_pages ? __ldg(p.page_table + static_cast<int64_t>(b) * p.max_pages + page0 + at) : -1;
   }
   // A single candidate's intervals likewise.
@@ -815,7 +816,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedSizes<DQ, DV, E4M3, MANY>:
   bool bad_page = false;
 #pragma unroll
   for (int i = 0; i < kPageLoads; ++i) {
-    const int at = i * kPagedThreads + tid;
+    const int at = i * Z::kThreads + tid;
     if (at < npages) {
       pages[at] = page[i];
       bad_page |= page[i] < 0 || page[i] >= p.cache.num_pages;
@@ -844,20 +845,20 @@ __global__ void __launch_bounds__(kPagedThreads, PagedSizes<DQ, DV, E4M3, MANY>:
     sp.c0 = c0;
     int wg, rows;
     if (!MANY || ce - c0 <= 4) {
-      wg = paged_pass<T, DQ, DV, E4M3, MANY, true>(p, sp, raw);
+      wg = paged_pass<T, DQ, DV, E4M3, MANY, W, true>(p, sp, raw);
       rows = 4;
     } else {
-      wg = paged_pass<T, DQ, DV, E4M3, MANY, !MANY>(p, sp, raw);
+      wg = paged_pass<T, DQ, DV, E4M3, MANY, W, !MANY>(p, sp, raw);
       rows = 16;
     }
     __syncthreads();
     // The slices' sums in slice order, four columns a thread.
     const int taken = min(ce - c0, wg * rows);
-    for (int i = tid; i < taken * (DV / 4); i += kPagedThreads) {
+    for (int i = tid; i < taken * (DV / 4); i += Z::kThreads) {
       const int r = i / (DV / 4), d = i % (DV / 4) * 4;
       const float* from = red + r * Z::kRedRow + Z::red_column(d);  // warp r / rows of each slice
       float sum[4] = {from[0], from[1], from[2], from[3]};
-      for (int w = wg; w < kPagedWarps; w += wg) {
+      for (int w = wg; w < W; w += wg) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum[e] += from[w * rows * Z::kRedRow + e];
       }
@@ -939,13 +940,13 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p) {
 
 // Launches the kernel for the widths of p.cache (one function for each type,
 // in a translation unit of its own so that they compile in parallel).
-template <typename T, bool E4M3, int DQ, int DV, bool MANY>
+template <typename T, bool E4M3, int DQ, int DV, bool MANY, int W>
 cudaError_t launch_paged_one(const PagedParams& p, unsigned blocks, cudaStream_t stream) {
-  constexpr int kSmem = PagedSizes<DQ, DV, E4M3, MANY>::kSmem;
+  constexpr int kSmem = PagedSizes<DQ, DV, E4M3, MANY, W>::kSmem;
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = ensure_smem_limit(paged_kernel<T, DQ, DV, E4M3, MANY>, kSmem, done);
+  const cudaError_t e = ensure_smem_limit(paged_kernel<T, DQ, DV, E4M3, MANY, W>, kSmem, done);
   if (e != cudaSuccess) return e;
-  return launch_chained(paged_kernel<T, DQ, DV, E4M3, MANY>, dim3(blocks), kPagedThreads, kSmem, stream, p);
+  return launch_chained(paged_kernel<T, DQ, DV, E4M3, MANY, W>, dim3(blocks), 32 * W, kSmem, stream, p);
 }
 
 template <typename T, int DV, int WARPS>
@@ -956,8 +957,14 @@ cudaError_t launch_paged_join(const PagedParams& p, cudaStream_t stream) {
 }
 template <typename T, bool E4M3, int DQ, int DV>
 cudaError_t launch_paged_widths(const PagedParams& p, unsigned blocks, cudaStream_t stream) {
-  const cudaError_t e = p.cand_offsets ? launch_paged_one<T, E4M3, DQ, DV, true>(p, blocks, stream)
-                                       : launch_paged_one<T, E4M3, DQ, DV, false>(p, blocks, stream);
+  // Eight warps a CTA where there is at most a CTA for each of 152 SMs: each warp
+  // has half the tiles to go through. (One row for each of 8 users of 700 to 1400
+  // rows: 7.2 us so, 8.2 us with four. With 200 to 256 CTAs it made no
+  // difference or cost 2%; 128 keys are two tiles a warp either way.)
+  const bool wide = blocks <= 152u && p.max_seqlen > 128;
+  const cudaError_t e = p.cand_offsets ? launch_paged_one<T, E4M3, DQ, DV, true, kPagedWarps>(p, blocks, stream)
+                        : wide ? launch_paged_one<T, E4M3, DQ, DV, false, kPagedWarpsWide>(p, blocks, stream)
+                               : launch_paged_one<T, E4M3, DQ, DV, false, kPagedWarps>(p, blocks, stream);
   if (e != cudaSuccess || p.nsplit == 1 || p.num_cand == 0) return e;
   // A warp for each (candidate, head), or a block where those are few.
   if (static_cast<int64_t>(p.num_cand) * p.cache.heads <= 1216) return launch_paged_join<T, DV, 8>(p, stream);
