@@ -543,7 +543,7 @@ _ext_module = None
 _ext_library = None  # the library that the extension calls
 
 
-def _ext():
+def load_extension():
     """The extension, bound to the selected library. Raises if it has not been
     built."""
     global _ext_module, _ext_library
@@ -606,7 +606,8 @@ def rope(q, k, positions, table: RopeTable, backward: bool = False, outs=None, s
     gradients of q' and k' to those of q and k. ``outs`` may be (q, k) itself:
     the rows are then rotated in place."""
     qo, ko = (None, None) if outs is None else outs
-    r = _ext().rope(q, k, positions, table._addr, table._device, bool(backward), qo, ko, _raw_stream(stream))
+    r = load_extension().rope(q, k, positions, table._addr, table._device, bool(backward), qo, ko,
+                              _raw_stream(stream))
     if type(r) is int:
         _check(r, "hstu_attn_rope")
     return r
@@ -668,9 +669,9 @@ def cache_write(cache: PagedCache, k, v, seq_offsets, cache_lens, page_table, ro
     (hstu_attn_cache_write); ``rope`` rotates k on its way, by ``positions``
     or by its place in the cache. ``cache_lens`` is not changed. With a ``ws``
     (256 bytes) skipped rows are reported by ``device_status``."""
-    st = _ext().cache_write(cache._addr, cache._device, k, v, seq_offsets, cache_lens, page_table,
-                            0 if rope is None else rope._addr, 0 if rope is None else rope._device, positions, ws,
-                            _raw_stream(stream))
+    st = load_extension().cache_write(cache._addr, cache._device, k, v, seq_offsets, cache_lens, page_table,
+                                      0 if rope is None else rope._addr, 0 if rope is None else rope._device, positions, ws,
+                                      _raw_stream(stream))
     if st != HSTU_OK:
         _check(st, "hstu_attn_cache_write")
 
@@ -681,8 +682,8 @@ def cache_read(cache: PagedCache, seq_offsets, rows: int, page_table, starts=Non
     (hstu_attn_cache_read): ``rows`` rows, those of sequence b from position
     ``starts[b]`` (0 without ``starts``)."""
     k, v = (None, None) if outs is None else outs
-    r = _ext().cache_read(cache._addr, cache._device, seq_offsets, rows, page_table, starts, k, v, ws,
-                          _raw_stream(stream))
+    r = load_extension().cache_read(cache._addr, cache._device, seq_offsets, rows, page_table, starts, k, v, ws,
+                                    _raw_stream(stream))
     if type(r) is int:
         _check(r, "hstu_attn_cache_read")
     return r
@@ -709,9 +710,9 @@ def fwd_paged(q_c, cache: PagedCache, cache_lens, page_table, max_seqlen: int, a
         # Allocated here, on the current stream, and used on another.
         own = ws = paged_workspace(cache, cache_lens.numel(), q_c.shape[0], max_seqlen)
         flags = FLAG_NO_STATUS
-    r = _ext().fwd_paged(cache._addr, cache._device, q_c, cache_lens, page_table, max_seqlen,
-                         1.0 / math.sqrt(cache.dim) if alpha is None else alpha, cand_offsets, func_c, ws, flags, out,
-                         _raw_stream(stream))
+    r = load_extension().fwd_paged(cache._addr, cache._device, q_c, cache_lens, page_table, max_seqlen,
+                                   1.0 / math.sqrt(cache.dim) if alpha is None else alpha, cand_offsets, func_c, ws, flags, out,
+                                   _raw_stream(stream))
     if own is not None:
         own.record_stream(stream)
     if type(r) is int:

@@ -31,6 +31,7 @@ CASES = [
     ([0, 15, 16, 17, 0], [33, 0, 1, 64, 7], 3, 64, 128, 16),
     ([250, 0, 3], [300, 513, 0], 2, 128, 32, 256),
     ([63, 1], [2, 700], 5, 32, 64, 64),
+    ([0, 40, 0, 1000], [3001, 1999, 0, 2503], 5, 64, 128, 128),  # enough rows for four heads a thread
 ]
 
 
@@ -86,8 +87,9 @@ def test_8_bit_rows_are_the_nearest_codes(hist, new, H, D, Dv, page, dtype):
 @pytest.mark.parametrize("quantised", [False, True])
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("D,R", [(128, 128), (64, 32), (32, 16), (128, 48)])
-def test_rotation_on_the_way_in(D, R, interleaved, quantised):
-    hist, new, H, dtype = [100, 0, 7], [3, 150, 40], 3, torch.bfloat16
+@pytest.mark.parametrize("hist,new,H", [([100, 0, 7], [3, 150, 40], 3), ([5, 0, 300], [5000, 1, 2999], 6)])
+def test_rotation_on_the_way_in(hist, new, H, D, R, interleaved, quantised):
+    dtype = torch.bfloat16
     pages, k, v = _setup(hist, new, H, D, 64, 32, dtype, quantised, seed=R)
     off, table = _offsets(new), hb.rope_table(R, interleaved=interleaved)
     f, m = su.frequencies(R)

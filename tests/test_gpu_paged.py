@@ -63,6 +63,21 @@ def test_one_new_token_a_sequence(lens, H, D, Dv, page, dtype, quantised):
 
 @pytest.mark.parametrize("quantised", [False, True])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("D,Dv", [(128, 128), (64, 32), (32, 128)])
+def test_more_ctas_than_sms(D, Dv, dtype, quantised):
+    """One row for each of many sequences: four warps a CTA, one split and several."""
+    rng = np.random.default_rng(D + Dv)
+    lens = rng.integers(0, 700, size=90).tolist()
+    pages = su.Pages(lens, 2, D, Dv, 32, dtype, quantised)
+    rows = pages.fill(rng)
+    _run(pages, rows, [1] * 90, None, 700, single=True)
+    func = np.array([(min(60, n), max(0, n - 33), n) for n in lens]).T
+    _run(pages, rows, [1] * 90, func, 700, single=True)
+    _run(pages, rows, [1] * 90, None, 400000, single=True)  # N far above the lengths
+
+
+@pytest.mark.parametrize("quantised", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("nfunc", [1, 3, 5, 9])
 @pytest.mark.parametrize("D,Dv", [(128, 128), (32, 64)])
 def test_several_candidates_with_masks(nfunc, D, Dv, dtype, quantised):

@@ -27,7 +27,9 @@ def _check(x, got, pos, f, m, interleaved, backward, dtype):
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("T,H,D,R", [(1, 1, 32, 32), (1, 4, 128, 128), (7, 3, 64, 48), (129, 2, 128, 16),
-                                     (1000, 5, 32, 16), (4097, 4, 128, 96), (333, 9, 64, 64)])
+                                     (1000, 5, 32, 16), (4097, 4, 128, 96), (333, 9, 64, 64),
+                                     # enough tokens for four heads a thread
+                                     (20011, 5, 32, 32), (10007, 6, 64, 48), (5003, 4, 128, 128)])
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_rotation_and_its_transpose(T, H, D, R, interleaved, dtype):
     rng, g = np.random.default_rng(T + R), torch.Generator().manual_seed(T)
