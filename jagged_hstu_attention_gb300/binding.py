@@ -28,7 +28,6 @@ STATUS_NAMES = {
 WS_FULL = 0
 WS_TARGETS = 1
 FLAG_REUSE_PLAN = 1
-FLAG_NO_STATUS = 2
 
 EXPORTED = (
     "hstu_attn_nfunc_supported", "hstu_attn_workspace_size", "hstu_attn_plan", "hstu_attn_fwd",
@@ -561,8 +560,20 @@ def load_extension():
     return _ext_module
 
 
-def _raw_stream(stream):
-    return None if stream is None else stream.cuda_stream
+def _serve(name, stream, *args):
+    """One call of the extension. It launches on the current stream and allocates
+    from that stream's memory, so a ``stream`` given is made the current one: an
+    output of another stream's memory could still be in use there."""
+    call = getattr(load_extension(), name)
+    if stream is None:
+        r = call(*args)
+    else:
+        with torch.cuda.stream(stream):
+            r = call(*args)
+    if type(r) is int:
+        _check(r, "hstu_attn_" + name)
+    return r
+
 
 _ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
@@ -606,11 +617,7 @@ def rope(q, k, positions, table: RopeTable, backward: bool = False, outs=None, s
     gradients of q' and k' to those of q and k. ``outs`` may be (q, k) itself:
     the rows are then rotated in place."""
     qo, ko = (None, None) if outs is None else outs
-    r = load_extension().rope(q, k, positions, table._addr, table._device, bool(backward), qo, ko,
-                              _raw_stream(stream))
-    if type(r) is int:
-        _check(r, "hstu_attn_rope")
-    return r
+    return _serve("rope", stream, q, k, positions, table._addr, table._device, bool(backward), qo, ko)
 
 
 class PagedCache:
@@ -669,11 +676,8 @@ def cache_write(cache: PagedCache, k, v, seq_offsets, cache_lens, page_table, ro
     (hstu_attn_cache_write); ``rope`` rotates k on its way, by ``positions``
     or by its place in the cache. ``cache_lens`` is not changed. With a ``ws``
     (256 bytes) skipped rows are reported by ``device_status``."""
-    st = load_extension().cache_write(cache._addr, cache._device, k, v, seq_offsets, cache_lens, page_table,
-                                      0 if rope is None else rope._addr, 0 if rope is None else rope._device, positions, ws,
-                                      _raw_stream(stream))
-    if st != HSTU_OK:
-        _check(st, "hstu_attn_cache_write")
+    _serve("cache_write", stream, cache._addr, cache._device, k, v, seq_offsets, cache_lens, page_table,
+           0 if rope is None else rope._addr, 0 if rope is None else rope._device, positions, ws)
 
 
 def cache_read(cache: PagedCache, seq_offsets, rows: int, page_table, starts=None, outs=None,
@@ -682,11 +686,7 @@ def cache_read(cache: PagedCache, seq_offsets, rows: int, page_table, starts=Non
     (hstu_attn_cache_read): ``rows`` rows, those of sequence b from position
     ``starts[b]`` (0 without ``starts``)."""
     k, v = (None, None) if outs is None else outs
-    r = load_extension().cache_read(cache._addr, cache._device, seq_offsets, rows, page_table, starts, k, v, ws,
-                                    _raw_stream(stream))
-    if type(r) is int:
-        _check(r, "hstu_attn_cache_read")
-    return r
+    return _serve("cache_read", stream, cache._addr, cache._device, seq_offsets, rows, page_table, starts, k, v, ws)
 
 
 def paged_workspace(cache: PagedCache, batch: int, num_candidates: int, max_seqlen: int) -> torch.Tensor:
@@ -704,17 +704,5 @@ def fwd_paged(q_c, cache: PagedCache, cache_lens, page_table, max_seqlen: int, a
     One candidate a sequence without ``cand_offsets``; all cached rows are
     visible without ``func_c`` (nfunc, C). With a ``ws`` (``paged_workspace``)
     of its own a caller can read ``device_status``."""
-    flags = 0
-    own = None
-    if stream is not None and ws is None:
-        # Allocated here, on the current stream, and used on another.
-        own = ws = paged_workspace(cache, cache_lens.numel(), q_c.shape[0], max_seqlen)
-        flags = FLAG_NO_STATUS
-    r = load_extension().fwd_paged(cache._addr, cache._device, q_c, cache_lens, page_table, max_seqlen,
-                                   1.0 / math.sqrt(cache.dim) if alpha is None else alpha, cand_offsets, func_c, ws, flags, out,
-                                   _raw_stream(stream))
-    if own is not None:
-        own.record_stream(stream)
-    if type(r) is int:
-        _check(r, "hstu_attn_fwd_paged")
-    return r
+    return _serve("fwd_paged", stream, cache._addr, cache._device, q_c, cache_lens, page_table, max_seqlen,
+                  1.0 / math.sqrt(cache.dim) if alpha is None else alpha, cand_offsets, func_c, ws, out)

@@ -104,6 +104,7 @@ const int32_t* check_ints(const at::Tensor& t, std::initializer_list<int64_t> sh
 const int32_t* check_pages(const at::Tensor& t, int64_t batch, int index) {
   if (t.dim() != 2 || t.size(0) != batch || t.size(1) < 1)
     throw Refused{"page_table must be (batch = " + std::to_string(batch) + ", pages), got " + shape_text(t.sizes())};
+  if (batch > INT32_MAX || t.size(1) > INT32_MAX) throw Refused{"page_table is too large"};
   return check_ints(t, {batch, t.size(1)}, index, "page_table");
 }
 
@@ -137,9 +138,8 @@ void* address(PyObject* o) {
   return p;
 }
 
-// The stream to launch on: an address, or None for the device's current one.
-void* stream_of(PyObject* o, int index) {
-  if (o != Py_None) return address(o);
+// The stream to launch on, whose memory the outputs are allocated from.
+void* current_stream(int index) {
   return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(index)).stream();
 }
 
@@ -177,9 +177,9 @@ void need_args(Py_ssize_t got, Py_ssize_t want) {
   if (got != want || !g_rope) throw Refused{"called by the wrappers of binding.py only"};
 }
 
-// rope(q, k, positions, table, table_device, backward, q_out, k_out, stream)
+// rope(q, k, positions, table, table_device, backward, q_out, k_out)
 PyObject* rope(PyObject* const* a, Py_ssize_t n) {
-  need_args(n, 9);
+  need_args(n, 8);
   const at::Tensor& q = tensor(a[0], "q");
   const at::Tensor* k = tensor_or_none(a[1], "k");
   const at::ScalarType type = q.scalar_type();
@@ -216,7 +216,7 @@ PyObject* rope(PyObject* const* a, Py_ssize_t n) {
     qo = new_rows(T, H, D, type, index);
     if (k) ko = new_rows(T, H, D, type, index);
   }
-  void* stream = stream_of(a[8], index);
+  void* stream = current_stream(index);
   const int backward = a[5] == Py_True;
   const hstu_status_t st = without_lock([&] {
     return g_rope(q.data_ptr(), qs, k ? k->data_ptr() : nullptr, ks, qo.data_ptr(), qos, ko ? ko->data_ptr() : nullptr,
@@ -228,9 +228,9 @@ PyObject* rope(PyObject* const* a, Py_ssize_t n) {
 }
 
 // cache_write(cache, cache_device, k, v, seq_offsets, cache_lens, page_table,
-//             rope, rope_device, positions, ws, stream)
+//             rope, rope_device, positions, ws)
 PyObject* cache_write(PyObject* const* a, Py_ssize_t n) {
-  need_args(n, 12);
+  need_args(n, 11);
   const auto* cache = static_cast<const hstu_cache_t*>(address(a[0]));
   const int index = static_cast<int>(integer(a[1]));
   check_current(index, "cache");
@@ -251,18 +251,19 @@ PyObject* cache_write(PyObject* const* a, Py_ssize_t n) {
   const at::Tensor* positions = tensor_or_none(a[9], "positions");
   const int32_t* pos = positions ? check_ints(*positions, {T}, index, "positions") : nullptr;
   const Workspace ws = check_ws(tensor_or_none(a[10], "ws"), index);
-  void* stream = stream_of(a[11], index);
+  void* stream = current_stream(index);
   const hstu_status_t st = without_lock([&] {
     return g_cache_write(cache, k.data_ptr(), ks, v.data_ptr(), vs, off, static_cast<int32_t>(B), T, lens, pages,
                          static_cast<int32_t>(table.size(1)), rope, pos, ws.ptr, ws.bytes, stream);
   });
-  return PyLong_FromLong(st);
+  if (st != HSTU_OK) return PyLong_FromLong(st);
+  Py_RETURN_NONE;
 }
 
 // cache_read(cache, cache_device, seq_offsets, rows, page_table, starts, k_out,
-//            v_out, ws, stream)
+//            v_out, ws)
 PyObject* cache_read(PyObject* const* a, Py_ssize_t n) {
-  need_args(n, 10);
+  need_args(n, 9);
   const auto* cache = static_cast<const hstu_cache_t*>(address(a[0]));
   const int index = static_cast<int>(integer(a[1]));
   check_current(index, "cache");
@@ -288,7 +289,7 @@ PyObject* cache_read(PyObject* const* a, Py_ssize_t n) {
     v = new_rows(rows, H, cache->head_dim_v, type, index);
   }
   const Workspace ws = check_ws(tensor_or_none(a[8], "ws"), index);
-  void* stream = stream_of(a[9], index);
+  void* stream = current_stream(index);
   const hstu_status_t st = without_lock([&] {
     return g_cache_read(cache, k.data_ptr(), v.data_ptr(), off, static_cast<int32_t>(B), rows, first, pages,
                         static_cast<int32_t>(table.size(1)), ws.ptr, ws.bytes, stream);
@@ -298,9 +299,9 @@ PyObject* cache_read(PyObject* const* a, Py_ssize_t n) {
 }
 
 // fwd_paged(cache, cache_device, q_c, cache_lens, page_table, max_seqlen, alpha,
-//           cand_offsets, func_c, ws, flags, out, stream)
+//           cand_offsets, func_c, ws, out)
 PyObject* fwd_paged(PyObject* const* a, Py_ssize_t n) {
-  need_args(n, 13);
+  need_args(n, 11);
   const auto* cache = static_cast<const hstu_cache_t*>(address(a[0]));
   const int index = static_cast<int>(integer(a[1]));
   check_current(index, "cache");
@@ -320,7 +321,7 @@ PyObject* fwd_paged(PyObject* const* a, Py_ssize_t n) {
   const at::Tensor* func = tensor_or_none(a[8], "func_c");
   const int64_t nfunc = func && func->dim() > 0 ? func->size(0) : 0;
   const int32_t* intervals = func ? check_ints(*func, {nfunc, C}, index, "func_c") : nullptr;
-  const at::Tensor* given = tensor_or_none(a[11], "out");
+  const at::Tensor* given = tensor_or_none(a[10], "out");
   at::Tensor out;
   if (given) {
     check_output(*given, type, C, H, cache->head_dim_v, index, "out");
@@ -329,7 +330,7 @@ PyObject* fwd_paged(PyObject* const* a, Py_ssize_t n) {
     out = new_rows(C, H, cache->head_dim_v, type, index);
   }
   Workspace ws = check_ws(tensor_or_none(a[9], "ws"), index);
-  uint32_t flags = static_cast<uint32_t>(integer(a[10]));
+  uint32_t flags = 0;
   at::Tensor own;  // freed on return, for the allocator to reuse behind this call on its stream
   if (!ws.ptr) {
     flags |= HSTU_FLAG_NO_STATUS;  // nobody could read the error word
@@ -340,7 +341,7 @@ PyObject* fwd_paged(PyObject* const* a, Py_ssize_t n) {
       ws = {own.data_ptr(), bytes};
     }
   }
-  void* stream = stream_of(a[12], index);
+  void* stream = current_stream(index);
   const hstu_status_t st = without_lock([&] {
     return g_fwd_paged(q.data_ptr(), qs, out.data_ptr(), cache, len, static_cast<int32_t>(B), pages,
                        static_cast<int32_t>(table.size(1)), cand, C, intervals, static_cast<int32_t>(nfunc),

@@ -191,6 +191,37 @@ def test_repeatable_and_on_another_stream():
         assert torch.equal(again, first)
 
 
+def _stream_of(t):
+    """The stream whose memory the tensor lies in."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+    return None
+
+
+def test_outputs_belong_to_the_stream_of_the_call():
+    """Memory of another stream could still be in use there."""
+    pages = su.Pages([3000, 2100], 2, 128, 128, 64, torch.bfloat16, True)
+    pages.fill(np.random.default_rng(0))
+    q = su.rows_of((2, 2, 128), torch.Generator().manual_seed(0), torch.bfloat16)
+    off, pos, table = _int32([0, 3000, 5100]), _int32([5, 7]), hb.rope_table(128)
+    side = torch.cuda.Stream()
+    first = hb.fwd_paged(q, pages.cache, pages.d_lens, pages.d_table, 3000)
+    turned = hb.rope(q, None, pos, table)[0]
+    k, v = hb.cache_read(pages.cache, off, 5100, pages.d_table)
+    torch.cuda.synchronize()
+    outs = [hb.fwd_paged(q, pages.cache, pages.d_lens, pages.d_table, 3000, stream=side),
+            hb.rope(q, None, pos, table, stream=side)[0],
+            *hb.cache_read(pages.cache, off, 5100, pages.d_table, stream=side)]
+    torch.cuda.synchronize()
+    for got, want in zip(outs, (first, turned, k, v)):
+        assert torch.equal(got, want)
+        assert _stream_of(got) == side.cuda_stream and _stream_of(want) != side.cuda_stream
+    with pytest.raises(ValueError):  # a refusal leaves the current stream as it was
+        hb.rope(q.cpu(), None, pos, table, stream=side)
+    assert torch.cuda.current_stream() != side
+
+
 def test_bad_sequences_are_left_as_they_were():
     lens, counts, H, D = [600, 50, 90], [2, 1, 3], 2, 32
     pages = su.Pages(lens, H, D, D, 16, torch.bfloat16, False, extra_pages=1)
