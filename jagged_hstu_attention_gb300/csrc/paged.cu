@@ -2,7 +2,7 @@
 // argument checks, the split of the cache's length, workspace, dispatch.
 #include <algorithm>
 
-#include "paged.cuh"
+#include "paged_many.cuh"
 
 namespace hstu {
 
@@ -10,20 +10,25 @@ namespace hstu {
 // that the workspace and the order of the sums are the same on every device.
 //   - As many keys as leave 2400 CTAs (eight waves of two an SM) at the longest
 //     length, which balances ragged lengths, from 512 to 4096.
-//   - With more than 8 candidates a sequence on average, 1024 keys at the least,
-//     which paged_split_keys cuts to a half or a quarter where a sequence has
-//     many: 64 users of 512 to 2048 rows and 0 to 48 candidates took 71 us so and
-//     79 us with 512 keys for all. With fewer the short splits that no
-//     sequence uses would cost more than they give.
+//   - With more than 8 candidates a sequence on average in paged_kernel, 1024 keys at
+//     the least, which paged_split_keys cuts to a half or a quarter where a sequence
+//     has many: 64 users of 512 to 2048 rows and 0 to 48 candidates took 64 us so and
+//     72 us with 512 keys for all. With fewer the short splits that no sequence uses
+//     would cost more than they give.
+//   - paged_many_kernel (more than 16 on average) takes 59 us of them with 512 keys
+//     at the least, 61 with 1024 and 58 with 2048; 16 users of 20000 rows 172 with 512.
 struct PagedLayout {
   int split = 0, nsplit = 0;
-  bool shorter = false;
+  bool tensor = false, shorter = false;
   size_t states = 0, partial = 0, total = 0;
 };
-static PagedLayout paged_layout(const CacheView& c, int batch, int64_t num_cand, int max_seqlen) {
+static PagedLayout paged_layout(const CacheView& c, const hstu_cache_t* cache, int batch, int64_t num_cand,
+                                int max_seqlen) {
   constexpr int64_t kCtas = 2400;
   PagedLayout l;
-  l.shorter = num_cand > 8 * static_cast<int64_t>(batch);
+  l.tensor = c.dim == kManyDim && c.dim_v == kManyDim && (cache->e4m3 || cache->dtype != HSTU_DTYPE_F16) &&
+             num_cand > 16 * static_cast<int64_t>(batch);
+  l.shorter = !l.tensor && num_cand > 8 * static_cast<int64_t>(batch);
   const int64_t want = static_cast<int64_t>(max_seqlen) * batch * c.heads / kCtas;
   l.split = static_cast<int>(
       std::min<int64_t>(kPagedMaxSplit, std::max<int64_t>(l.shorter ? 1024 : 512, (want + 255) / 256 * 256)));
@@ -43,7 +48,7 @@ static hstu_status_t check_paged(const hstu_cache_t* cache, int32_t batch, int64
   if (st != HSTU_OK) return st;
   if (batch < 1 || num_cand < 0 || num_cand > INT32_MAX || max_seqlen < 1) return HSTU_ERR_INVALID_ARG;
   if (max_seqlen > (1 << 24)) return HSTU_ERR_UNSUPPORTED;
-  const PagedLayout l = paged_layout(*view, batch, num_cand, max_seqlen);
+  const PagedLayout l = paged_layout(*view, cache, batch, num_cand, max_seqlen);
   const int64_t bh = static_cast<int64_t>(batch) * view->heads;
   if (bh > INT32_MAX / l.nsplit || num_cand * view->heads > INT32_MAX) return HSTU_ERR_UNSUPPORTED;  // CTAs of a launch
   return HSTU_OK;
@@ -57,7 +62,7 @@ HSTU_API size_t hstu_attn_paged_workspace_size(const hstu_cache_t* cache, int32_
                                                int32_t max_seqlen) {
   hstu::CacheView view;
   if (hstu::check_paged(cache, batch, num_candidates, max_seqlen, &view) != HSTU_OK) return 0;
-  return hstu::paged_layout(view, batch, num_candidates, max_seqlen).total;
+  return hstu::paged_layout(view, cache, batch, num_candidates, max_seqlen).total;
 }
 
 HSTU_API hstu_status_t hstu_attn_fwd_paged(const void* q_c, int64_t q_stride, void* o_c, const hstu_cache_t* cache,
@@ -76,7 +81,8 @@ HSTU_API hstu_status_t hstu_attn_fwd_paged(const void* q_c, int64_t q_stride, vo
   if (num_candidates > 0 && (!hstu::rows_ok(q_c, q_stride, p.cache.heads, p.cache.dim) || !o_c ||
                              reinterpret_cast<uintptr_t>(o_c) % 16 != 0 || o_c == q_c))
     return HSTU_ERR_INVALID_ARG;
-  const hstu::PagedLayout l = hstu::paged_layout(p.cache, batch, num_candidates, max_seqlen);
+  const bool half = cache->dtype == HSTU_DTYPE_F16;
+  const hstu::PagedLayout l = hstu::paged_layout(p.cache, cache, batch, num_candidates, max_seqlen);
   const bool report = !(flags & HSTU_FLAG_NO_STATUS);
   if (!ws && (l.nsplit > 1 || report)) return HSTU_ERR_WORKSPACE;
   if (ws && (reinterpret_cast<uintptr_t>(ws) % 256 != 0 || ws_bytes < l.total)) return HSTU_ERR_WORKSPACE;
@@ -105,13 +111,13 @@ HSTU_API hstu_status_t hstu_attn_fwd_paged(const void* q_c, int64_t q_stride, vo
     p.split = std::min(2 * l.split, hstu::kPagedMaxSplit);
     p.nsplit = (max_seqlen + p.split - 1) / p.split;
   }
+  p.tensor = l.tensor;
   p.shorter = l.shorter;
   p.alpha = alpha;
   p.inv_n = 1.0f / static_cast<float>(max_seqlen);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (report && cudaMemsetAsync(ws, 0, hstu::kHdrWords * 4, cs) != cudaSuccess) return HSTU_ERR_CUDA;
   const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(batch) * p.cache.heads * p.nsplit);
-  const bool half = cache->dtype == HSTU_DTYPE_F16;
   cudaError_t e;
   if (cache->e4m3) e = half ? hstu::launch_paged_f16_e4m3(p, blocks, cs) : hstu::launch_paged_bf16_e4m3(p, blocks, cs);
   else e = half ? hstu::launch_paged_f16(p, blocks, cs) : hstu::launch_paged_bf16(p, blocks, cs);

@@ -6,19 +6,16 @@
 // as many products as its sequence has candidates, few of them, so the bytes
 // of the cache bound the kernel; the products run on warp-level matrix
 // instructions (m16n8k16), whose operands a warp can take straight from the
-// cache's rows. (A tcgen05 product has 128 rows of which a handful of
-// candidates would fill a few, and wants its operands in canonical
-// shared-memory tiles and P back in shared memory; what remains of the time
-// with many candidates is silu and the operands' conversion, not the products:
-// the matrix pipe is 26% busy with 24 of them.)
+// cache's rows. (Where a sequence has more than 16 candidates the products are
+// worth tcgen05's operand tiles in shared memory: paged_many.cuh.)
 //
 // Measured, H = 4, D_qk = D_v = 128, histories of 1332 to 3994 rows: one
 // candidate for each of 256 users over 16-bit pages 207 us, 6.8 TB/s, the rate of
 // a plain copy; over 8-bit pages 118 us, 6.0 TB/s, with the issue slots half
-// used by the codes' conversion and the latency of the first and last CTAs. 0 to 48
-// candidates for each of 64 users of 512 to 2048 rows: 66 us against 25 us for
-// the bytes, bound by the latency of the chain from scores to weights in the
-// twelve warps that registers leave an SM.
+// used by the codes' conversion and the latency of the first and last CTAs. 16
+// candidates for each of 64 users of 512 to 2048 rows: 47 us against 25 us for the
+// bytes, bound by the latency of the chain from scores to weights in the twelve
+// warps that registers leave an SM and by the CTAs' first loads.
 //
 // A CTA takes one (sequence, head) and one split of its length. Its four warps
 // form slices of 1, 2 or 4 warps, as many as the sequence's candidates need; a
@@ -84,6 +81,7 @@ struct PagedParams {
   int32_t* states;    // (batch, heads, nsplit): 1 where a split's sums are good
   int32_t batch, max_pages, num_cand, nfunc, max_seqlen;
   int32_t split, nsplit;  // keys of a split (of sequences with few candidates); splits of max_seqlen, at most
+  bool tensor;            // many candidates: paged_many_kernel
   bool shorter;           // splits get shorter with a sequence's candidates (paged_split_keys)
   float alpha, inv_n;
 };
@@ -324,6 +322,79 @@ __device__ __forceinline__ int paged_split_keys(const PagedParams& p, int total)
 
 __device__ __forceinline__ int paged_key(const PagedParams& p, const PagedSplit& sp, int entry) {
   return sp.k0 + (p.func ? sp.list[entry] & 0x7fff : entry) * kPagedTile;
+}
+
+// What a CTA keeps in shared memory besides its tiles.
+template <bool MANY>
+struct PagedTables {
+  int pages[kPagedMaxSplit / kPagedTile];
+  uint32_t bits[2 * kPagedWords];
+  uint16_t list[kPagedMaxSplit / kPagedTile];
+  int iv[(MANY ? kPagedPass : 1) * kPagedIv];
+  int entries;
+};
+
+// Opens one split, of `keys` keys, of sequence b for candidates [cb, ce): reads its
+// pages and checks the sequence. False where there is nothing to do; `bad`
+// where a page of the split is no page of the cache (it has no tiles then).
+template <bool MANY, int THREADS>
+__device__ __forceinline__ bool paged_open(const PagedParams& p, PagedTables<MANY>& tables, int b, int h, int split,
+                                           int cb, int ce, int keys, PagedSplit& sp, int& splits, bool& bad) {
+  const int tid = threadIdx.x;
+  // Loads that depend on nothing, all under way at once.
+  const int len = p.lens[b];
+  const int offsets0 = MANY ? p.cand_offsets[0] : 0, offsets1 = MANY ? p.cand_offsets[p.batch] : p.num_cand;
+  const int k0 = static_cast<int>(min(static_cast<int64_t>(split) * keys, static_cast<int64_t>(p.max_seqlen)));
+
+  // Pages of this split, read before the length is known (entries past the
+  // length are not looked at).
+  const int page0 = k0 >> p.cache.page_shift;
+  const int most_pages = min(((k0 + keys - 1) >> p.cache.page_shift) - page0 + 1, p.max_pages - page0);
+  constexpr int kPageLoads = (kPagedMaxSplit / kPagedTile + THREADS - 1) / THREADS;
+  int page[kPageLoads];
+#pragma unroll
+  for (int i = 0; i < kPageLoads; ++i) {
+    const int at = i * THREADS + tid;
+    page[i] = at < most_pages ? __ldg(p.page_table + static_cast<int64_t>(b) * p.max_pages + page0 + at) : -1;
+  }
+  // Checks of this sequence (every CTA of it comes to the same answer).
+  bool ok = true;
+  if (MANY) ok = (cb >= 0) & (cb <= ce) & (ce <= p.num_cand) & (offsets0 == 0) & (offsets1 == p.num_cand);
+  ok = ok && len >= 0 && len <= p.max_seqlen &&
+       static_cast<int64_t>(len) <= (static_cast<int64_t>(p.max_pages) << p.cache.page_shift);
+  if (!ok) {
+    if (p.header && split == 0 && h == 0 && tid == 0) atomicOr(p.header + kHdrErr, kErrInput);
+    return false;
+  }
+  if (cb == ce) return false;
+  splits = max(1, (len + keys - 1) / keys);
+  if (split >= splits) return false;
+  const int k1 = min(len, k0 + keys);
+  const int npages = k1 > k0 ? ((k1 - 1) >> p.cache.page_shift) - page0 + 1 : 0;
+  bool bad_page = false;
+#pragma unroll
+  for (int i = 0; i < kPageLoads; ++i) {
+    const int at = i * THREADS + tid;
+    if (at < npages) {
+      tables.pages[at] = page[i];
+      bad_page |= page[i] < 0 || page[i] >= p.cache.num_pages;
+    }
+  }
+  bad = __syncthreads_or(bad_page) != 0;
+  if (bad && p.header && tid == 0) atomicOr(p.header + kHdrErr, kErrInput);
+  sp.h = h;
+  sp.k0 = k0;
+  sp.k1 = k1;
+  sp.len = len;
+  sp.page0 = page0;
+  sp.tiles = bad ? 0 : (k1 - k0 + kPagedTile - 1) / kPagedTile;
+  sp.ce = ce;
+  sp.pages = tables.pages;
+  sp.bits = tables.bits;
+  sp.list = tables.list;
+  sp.iv = tables.iv;
+  sp.entries = &tables.entries;
+  return true;
 }
 
 // The sum of candidate r of the pass over the tiles of one slice, in fp32, one
@@ -752,11 +823,7 @@ template <typename T, int DQ, int DV, bool E4M3, bool MANY, int W>
 __global__ void __launch_bounds__(32 * W, PagedSizes<DQ, DV, E4M3, MANY, W>::kResident)
     paged_kernel(const PagedParams p) {
   using Z = PagedSizes<DQ, DV, E4M3, MANY, W>;
-  __shared__ int pages[kPagedMaxSplit / kPagedTile];
-  __shared__ uint32_t bits[2 * kPagedWords];
-  __shared__ uint16_t list[kPagedMaxSplit / kPagedTile];
-  __shared__ int iv[(MANY ? kPagedPass : 1) * kPagedIv];
-  __shared__ int sh_entries;
+  __shared__ PagedTables<MANY> tables;
 
   chain();
   const int tid = threadIdx.x;
@@ -776,69 +843,18 @@ __global__ void __launch_bounds__(32 * W, PagedSizes<DQ, DV, E4M3, MANY, W>::kRe
     ce = p.cand_offsets[b + 1];
   }
   const int keys = MANY ? paged_split_keys(p, ce - cb) : p.split;
-  const int k0 = static_cast<int>(min(static_cast<int64_t>(split) * keys, static_cast<int64_t>(p.max_seqlen)));
 
-  // Pages of this split, read before the length is known (entries past the
-  // length are not looked at).
-  const int page0 = k0 >> p.cache.page_shift;
-  const int most_pages = min(((k0 + keys - 1) >> p.cache.page_shift) - page0 + 1, p.max_pages - page0);
-  constexpr int kPageLoads = kPagedMaxSplit / kPagedTile / Z::kThreads;
-  int page[kPageLoads];
-#pragma unroll
-  for (int i = 0; i < kPageLoads; ++i) {
-    const int at = i * Z::kThreads + tid;
-    page[i] = at < most_pages ? __ldg(p.page_table + static_cast<int64_t>(b) * p.max_pages + page0 + at) : -1;
-  }
-  // A single candidate's intervals likewise.
+  // A single candidate's intervals, read before the length is known.
   int raw[2 * kMaxIntervals - 1];
 #pragma unroll
   for (int i = 0; i < 2 * kMaxIntervals - 1; ++i)
     raw[i] = !MANY && p.func && i < p.nfunc ? __ldg(p.func + static_cast<int64_t>(i) * p.num_cand + b) : 0;
 
-  // Checks of this sequence (every CTA of it comes to the same answer).
-  bool ok = true;
-  if (MANY) {
-    ok = cb >= 0 && cb <= ce && ce <= p.num_cand && p.cand_offsets[0] == 0 &&
-         p.cand_offsets[p.batch] == p.num_cand;
-  }
-  const int len = p.lens[b];
-  ok = ok && len >= 0 && len <= p.max_seqlen &&
-       static_cast<int64_t>(len) <= (static_cast<int64_t>(p.max_pages) << p.cache.page_shift);
-  if (!ok) {
-    if (p.header && split == 0 && h == 0 && tid == 0) atomicOr(p.header + kHdrErr, kErrInput);
-    return;
-  }
-  if (cb == ce) return;
-  const int splits = max(1, (len + keys - 1) / keys);
-  if (split >= splits) return;
-  const int k1 = min(len, k0 + keys);
-  const int npages = k1 > k0 ? ((k1 - 1) >> p.cache.page_shift) - page0 + 1 : 0;
-  bool bad_page = false;
-#pragma unroll
-  for (int i = 0; i < kPageLoads; ++i) {
-    const int at = i * Z::kThreads + tid;
-    if (at < npages) {
-      pages[at] = page[i];
-      bad_page |= page[i] < 0 || page[i] >= p.cache.num_pages;
-    }
-  }
-  const bool bad = __syncthreads_or(bad_page) != 0;
-  if (bad && p.header && tid == 0) atomicOr(p.header + kHdrErr, kErrInput);
-
-  float* red = reinterpret_cast<float*>(paged_ring);
   PagedSplit sp;
-  sp.h = h;
-  sp.k0 = k0;
-  sp.k1 = k1;
-  sp.len = len;
-  sp.page0 = page0;
-  sp.tiles = bad ? 0 : (k1 - k0 + kPagedTile - 1) / kPagedTile;
-  sp.ce = ce;
-  sp.pages = pages;
-  sp.bits = bits;
-  sp.list = list;
-  sp.iv = iv;
-  sp.entries = &sh_entries;
+  int splits;
+  bool bad;
+  if (!paged_open<MANY, Z::kThreads>(p, tables, b, h, split, cb, ce, keys, sp, splits, bad)) return;
+  float* red = reinterpret_cast<float*>(paged_ring);
   sp.ring = smem_u32(paged_ring);
   sp.red = red;
   for (int c0 = cb; c0 < ce;) {
@@ -936,51 +952,6 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p) {
   if (live && lane < DV / 4)
     *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + unit * DV + 4 * lane) =
         make_uint2(Elem<T>::pack2(sum.x * p.inv_n, sum.y * p.inv_n), Elem<T>::pack2(sum.z * p.inv_n, sum.w * p.inv_n));
-}
-
-// Launches the kernel for the widths of p.cache (one function for each type,
-// in a translation unit of its own so that they compile in parallel).
-template <typename T, bool E4M3, int DQ, int DV, bool MANY, int W>
-cudaError_t launch_paged_one(const PagedParams& p, unsigned blocks, cudaStream_t stream) {
-  constexpr int kSmem = PagedSizes<DQ, DV, E4M3, MANY, W>::kSmem;
-  static std::atomic<uint64_t> done{0};
-  const cudaError_t e = ensure_smem_limit(paged_kernel<T, DQ, DV, E4M3, MANY, W>, kSmem, done);
-  if (e != cudaSuccess) return e;
-  return launch_chained(paged_kernel<T, DQ, DV, E4M3, MANY, W>, dim3(blocks), 32 * W, kSmem, stream, p);
-}
-
-template <typename T, int DV, int WARPS>
-cudaError_t launch_paged_join(const PagedParams& p, cudaStream_t stream) {
-  const int64_t units = static_cast<int64_t>(p.num_cand) * p.cache.heads;
-  const dim3 grid(static_cast<unsigned>((units + 8 / WARPS - 1) / (8 / WARPS)));
-  return launch_chained(paged_join_kernel<T, DV, WARPS>, grid, 256, 0, stream, p);
-}
-template <typename T, bool E4M3, int DQ, int DV>
-cudaError_t launch_paged_widths(const PagedParams& p, unsigned blocks, cudaStream_t stream) {
-  // Eight warps a CTA where there is at most a CTA for each of 152 SMs: each warp
-  // has half the tiles to go through. (One row for each of 8 users of 700 to 1400
-  // rows: 7.2 us so, 8.2 us with four. With 200 to 256 CTAs it made no
-  // difference or cost 2%; 128 keys are two tiles a warp either way.)
-  const bool wide = blocks <= 152u && p.max_seqlen > 128;
-  const cudaError_t e = p.cand_offsets ? launch_paged_one<T, E4M3, DQ, DV, true, kPagedWarps>(p, blocks, stream)
-                        : wide ? launch_paged_one<T, E4M3, DQ, DV, false, kPagedWarpsWide>(p, blocks, stream)
-                               : launch_paged_one<T, E4M3, DQ, DV, false, kPagedWarps>(p, blocks, stream);
-  if (e != cudaSuccess || p.nsplit == 1 || p.num_cand == 0) return e;
-  // A warp for each (candidate, head), or a block where those are few.
-  if (static_cast<int64_t>(p.num_cand) * p.cache.heads <= 1216) return launch_paged_join<T, DV, 8>(p, stream);
-  return launch_paged_join<T, DV, 1>(p, stream);
-}
-template <typename T, bool E4M3, int DQ>
-cudaError_t launch_paged_dv(const PagedParams& p, unsigned blocks, cudaStream_t stream) {
-  if (p.cache.dim_v == 128) return launch_paged_widths<T, E4M3, DQ, 128>(p, blocks, stream);
-  if (p.cache.dim_v == 64) return launch_paged_widths<T, E4M3, DQ, 64>(p, blocks, stream);
-  return launch_paged_widths<T, E4M3, DQ, 32>(p, blocks, stream);
-}
-template <typename T, bool E4M3>
-cudaError_t launch_paged_typed(const PagedParams& p, unsigned blocks, cudaStream_t stream) {
-  if (p.cache.dim == 128) return launch_paged_dv<T, E4M3, 128>(p, blocks, stream);
-  if (p.cache.dim == 64) return launch_paged_dv<T, E4M3, 64>(p, blocks, stream);
-  return launch_paged_dv<T, E4M3, 32>(p, blocks, stream);
 }
 
 cudaError_t launch_paged_bf16(const PagedParams& p, unsigned blocks, cudaStream_t stream);

@@ -1,5 +1,5 @@
 // Paged attention kernels for bf16 rows and pages.
-#include "paged.cuh"
+#include "paged_many.cuh"
 
 namespace hstu {
 

@@ -1,5 +1,5 @@
 // Paged attention kernels for fp16 rows, 8-bit pages.
-#include "paged.cuh"
+#include "paged_many.cuh"
 
 namespace hstu {
 

@@ -379,6 +379,108 @@ def test_many_candidates_take_several_passes():
         _run(pages, rows, counts, None, max(full))
 
 
+# More than 16 candidates a sequence on average, widths of 128: the kernel whose
+# products are tcgen05's (bf16 and 8-bit pages).
+MANY_TYPES = [(torch.bfloat16, False), (torch.bfloat16, True), (torch.float16, True), (torch.float16, False)]
+MANY_SIZES = [
+    # lens, counts, H, page
+    ([300, 0, 1, 129, 2100], [40, 5, 17, 33, 70], 2, 64),
+    ([15, 16, 17, 700], [20, 16, 64, 65], 3, 16),
+    ([1537], [17], 1, 256),
+    ([128, 127, 640], [200, 0, 1], 1, 32),
+]
+
+
+@pytest.mark.parametrize("dtype,quantised", MANY_TYPES)
+@pytest.mark.parametrize("nfunc", [0, 1, 3, 9])
+@pytest.mark.parametrize("lens,counts,H,page", MANY_SIZES)
+def test_crowds_of_candidates(lens, counts, H, page, nfunc, dtype, quantised):
+    pages = su.Pages(lens, H, 128, 128, page, dtype, quantised, seed=nfunc)
+    rng = np.random.default_rng(nfunc + H)
+    rows = pages.fill(rng)
+    C = sum(counts)
+    func = None
+    if nfunc:
+        func = np.zeros((nfunc, C), dtype=np.int32)
+        for b, L in enumerate(lens):
+            for c in range(sum(counts[:b]), sum(counts[:b + 1])):
+                func[0, c] = rng.integers(0, L + 1) if c % 3 else 0
+                for i in range(1, nfunc):
+                    func[i, c] = rng.integers(-5, L + 6)
+        func[:, 4] = 0
+    _, o = _run(pages, rows, counts, func, max(lens))
+    assert func is None or (o[4] == 0).all()
+    if func is None:
+        _run(pages, rows, counts, None, max(lens), alpha=-3.0)
+        _run(pages, rows, counts, None, 3 * max(lens), alpha=1e-6)
+
+
+@pytest.mark.parametrize("dtype,quantised", MANY_TYPES)
+def test_crowds_of_candidates_and_rows_that_hold_anything(dtype, quantised):
+    lens, counts, H, D = [700, 90], [35, 5], 2, 128
+    pages = su.Pages(lens, H, D, D, 16, dtype, quantised)
+    rows = pages.fill(np.random.default_rng(5))
+    c = pages.cache
+    for b, pos in ((0, 5), (0, 300), (1, 88)):
+        page, slot = (int(x[0]) for x in pages.places(b, pos, 1))
+        c.k[page, :, slot] = c.v[page, :, slot] = 0x7f if quantised else float("nan")
+        for x in rows[b]:
+            x[pos] = float("nan")
+    func = np.zeros((3, 40), dtype=np.int32)
+    func[:, :35] = np.array([[5, 6, 300], [0, 301, 700], [5, 6, 200], [0, 100, 290], [0, 0, 0]] * 7).T
+    func[:, 35:] = np.array([[88, 89, 90]] * 5).T
+    _run(pages, rows, counts, func, 700)
+    func[:, 33] = [302, 0, 0]  # sees two of them; its neighbours are not touched
+    q = su.rows_of((40, H, D), torch.Generator().manual_seed(0), dtype)
+    o = hb.fwd_paged(q, c, pages.d_lens, pages.d_table, 700, cand_offsets=_int32(_offsets(counts)), func_c=_int32(func))
+    func[:, 33] = 0
+    want, tol = su.paged_reference(su.f64(q), rows, counts, func, 700, D ** -0.5, dtype)
+    keep = np.arange(40) != 33
+    assert np.all(np.abs(su.f64(o) - want)[keep] <= tol[keep])
+    assert not torch.isfinite(o[33]).any()
+
+
+@pytest.mark.parametrize("quantised", [False, True])
+def test_crowds_of_candidates_refused_replayed_and_on_two_streams(quantised):
+    lens, counts, H, D, N = [100, 1500, 1400], [20, 40, 66], 2, 128, 1500
+    pages = su.Pages(lens, H, D, D, 32, torch.bfloat16, quantised)
+    pages.fill(np.random.default_rng(2))
+    q = su.rows_of((126, H, D), torch.Generator().manual_seed(2), torch.bfloat16)
+    off = _int32(_offsets(counts))
+    ws = hb.paged_workspace(pages.cache, 3, 126, N)
+
+    def run(offsets, table=None):
+        out = torch.full((126, H, D), 55.0, dtype=torch.bfloat16, device="cuda")
+        hb.fwd_paged(q, pages.cache, pages.d_lens, pages.d_table if table is None else table, N,
+                     cand_offsets=offsets, ws=ws, out=out)
+        return hb.device_status(ws), out
+
+    st, good = run(off)
+    assert st == hb.HSTU_OK
+    table = pages.d_table.clone()
+    table[1, 40] = -1
+    table[0, 2] = pages.num_pages
+    st, out = run(off, table)
+    assert st == 5 and (out[:60] == 55.0).all() and torch.equal(out[60:], good[60:])
+    for bad in ([0, 20, 60, 125], [1, 20, 60, 126]):
+        st, out = run(_int32(bad))
+        assert st == 5 and (out == 55.0).all()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    outs = [hb.fwd_paged(q, pages.cache, pages.d_lens, pages.d_table, N, cand_offsets=off, stream=s)
+            for _ in range(10) for s in streams]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, good) for o in outs)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = hb.fwd_paged(q, pages.cache, pages.d_lens, pages.d_table, N, cand_offsets=off)
+    for _ in range(5):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, good)
+
+
 def test_a_length_past_the_page_table_is_refused():
     pages = su.Pages([40, 40], 1, 32, 32, 16, torch.bfloat16, False)
     pages.fill(np.random.default_rng(0))
