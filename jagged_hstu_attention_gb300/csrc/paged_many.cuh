@@ -32,8 +32,8 @@
 // Measured against paged_kernel, H = 4, 16-bit pages, us: 256 users of 1332 to 3994
 // rows with 24 candidates each 254 (311), with 40 each 327 (533; the bytes alone take
 // 206), 16 users of 20000 rows with 40 each 172 (294), 64 users of 512 to 2048 rows with
-// 0 to 48 each 59 (64), with 16 each 49 (47). 8-bit pages: 40 each 423 (791), 0 to 48
-// each 69 (85). With widths of 64, 0 to 48 each took 52 (45): a step's copies are
+// 0 to 48 each 59 (64), with 16 each 49 (47). 8-bit pages: 40 each 397 (791), 0 to 48
+// each 66 (85). With widths of 64, 0 to 48 each took 52 (45): a step's copies are
 // too small there for its waits.
 #pragma once
 
@@ -263,6 +263,11 @@ __global__ void __launch_bounds__(256, 2) paged_many_kernel(const PagedParams p)
       // This thread's key.
       const int mine = t * Z::kWarps + 2 * quarter + (lane >> 4);
       const float ks = E4M3 ? scale_value(kbyte) * p.alpha : p.alpha, vs = E4M3 ? scale_value(vbyte) : 1.0f;
+      if (E4M3) {  // the next copies' registers are free as soon as the operands are written
+        fetch_k(t + 1);
+        if (t * Z::kWarps + warp < entries) vc.settle(v_tile, lane);
+        fetch_v(t + 1);
+      }
       int key = sp.k1;
       bool part = true;
       if (mine < entries) {
@@ -270,11 +275,10 @@ __global__ void __launch_bounds__(256, 2) paged_many_kernel(const PagedParams p)
         key = key0 + (lane & 15);
         part = p.func ? (sp.list[mine] & 0x8000) != 0 : key0 + kPagedTile > sp.k1;
       }
-      if (E4M3 && t * Z::kWarps + warp < entries) vc.settle(v_tile, lane);
       ok = mbar_wait(s_bar, s_phase, abort_flag);
       s_phase ^= 1;
       tc_fence_after();
-      fetch_k(t + 1);  // K is free
+      if (!E4M3) fetch_k(t + 1);  // K is free
       for (int g = 0; g < groups; ++g) {
         const int first = g * Z::kGroup + 16 * half;  // candidates of this warp
         const bool busy = first < total && t * Z::kWarps + 2 * quarter < entries;
@@ -344,7 +348,7 @@ __global__ void __launch_bounds__(256, 2) paged_many_kernel(const PagedParams p)
       if (!ok) break;
       ok = mbar_wait(o_bar, o_phase, abort_flag);
       o_phase ^= 1;
-      fetch_v(t + 1);  // V is free
+      if (!E4M3) fetch_v(t + 1);  // V is free
     }
     if (!E4M3) copies_wait<0>();
     ok = __syncthreads_and(ok);
