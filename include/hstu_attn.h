@@ -445,7 +445,8 @@ HSTU_API hstu_status_t hstu_attn_cache_read(const hstu_cache_t* cache, void* k, 
                                             void* stream);
 
 /* Bytes of workspace that hstu_attn_fwd_paged needs; 0 if an argument is out
- * of range. */
+ * of range. They serve calls with fewer candidates too (the other arguments
+ * alike). */
 HSTU_API size_t hstu_attn_paged_workspace_size(const hstu_cache_t* cache, int32_t batch, int64_t num_candidates,
                                                int32_t max_seqlen);
 
@@ -473,7 +474,8 @@ HSTU_API size_t hstu_attn_paged_workspace_size(const hstu_cache_t* cache, int32_
  * that sees nothing gets 0. The cache's length is split over CTAs, whose sums
  * are joined in a fixed order (bitwise repeatable). A sequence with bad
  * offsets, length or page sets HSTU_ERR_DEVICE_INPUT in the error word of ws;
- * its rows of o_c are left as they were. */
+ * its rows of o_c are left as they were, and so are those of a sequence whose
+ * products do not end in time (HSTU_ERR_TIMEOUT). */
 HSTU_API hstu_status_t hstu_attn_fwd_paged(const void* q_c, int64_t q_stride, void* o_c, const hstu_cache_t* cache,
                                            const int32_t* cache_lens, int32_t batch, const int32_t* page_table,
                                            int32_t max_pages, const int32_t* cand_offsets, int64_t num_candidates,

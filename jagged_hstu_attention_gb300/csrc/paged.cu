@@ -39,6 +39,10 @@ static PagedLayout paged_layout(const CacheView& c, const hstu_cache_t* cache, i
     l.partial = l.states + align_up(static_cast<size_t>(batch) * c.heads * l.nsplit * 4, 256);
     l.total = l.partial + align_up(static_cast<size_t>(num_cand) * c.heads * l.nsplit * c.dim_v * 4, 256);
   }
+  // paged_kernel's shorter splits can take more room for fewer candidates: a
+  // workspace serves every call with as many or fewer.
+  if (l.tensor)
+    l.total = std::max(l.total, paged_layout(c, cache, batch, 16 * static_cast<int64_t>(batch), max_seqlen).total);
   return l;
 }
 

@@ -152,6 +152,16 @@ def test_paged_refusals(lib):
     assert lib.hstu_attn_paged_workspace_size(None, 3, 7, 1000) == 0
 
 
+def test_a_paged_workspace_serves_fewer_candidates(lib):
+    for kw in (dict(), dict(D=128, Dv=128), dict(D=128, Dv=128, dtype=1), dict(D=128, Dv=32),
+               dict(D=128, e4m3=1, ks=1 << 20, vs=1 << 20, dtype=1)):
+        for B in (1, 7, 300):
+            for N in (1, 256, 300, 512, 513, 1100, 20000, 1 << 20):
+                sizes = [lib.hstu_attn_paged_workspace_size(ctypes.byref(_cache(**kw)), B, C, N)
+                         for C in (0, B, 8 * B, 8 * B + 1, 16 * B, 16 * B + 1, 17 * B + 3, 40 * B, 64 * B)]
+                assert sizes[0] >= 256 and sizes == sorted(sizes), (kw, B, N, sizes)
+
+
 def test_binding_checks_its_tensors(lib):
     q = torch.zeros((4, 2, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
