@@ -191,7 +191,8 @@ struct PagedSizes {
   // many candidates, whose sums and fragments are most of the registers).
   static constexpr int kFit = 227 * 1024 / (kSmem + 6144);
   static constexpr int kRegisters = 80 + DV / 2 + DQ / 4 * (E4M3 ? 2 : 1);
-  static constexpr int kWant = !MANY ? (W == kPagedWarps ? 4 : 2) : (kRegisters <= 102 ? 5 : (kRegisters <= 128 ? 4 : 3));
+  static constexpr int kWant =
+      !MANY ? (W == kPagedWarps ? 4 : 2) : (kRegisters <= 102 ? 5 : (kRegisters <= 128 ? 4 : 3));
   static constexpr int kResident = kFit < 1 ? 1 : (kFit > kWant ? kWant : kFit);
   static __device__ __forceinline__ int red_column(int d) { return E4M3 ? d / VE * kBlock + d % VE : d; }
   // Permutation of the 16-byte pieces of v row r.

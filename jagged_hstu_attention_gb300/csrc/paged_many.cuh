@@ -114,20 +114,21 @@ struct TileCopy {
   }
   // 8-bit rows: from registers into the operand.
   __device__ __forceinline__ void settle(uint32_t dst, int lane) {
-    if (!E4M3) return;
+    if constexpr (E4M3) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int u = i * 32 + lane, r = u / C, c = u % C;
-      const uint4 x = w[E4M3 ? i : 0];
-      const uint32_t words[4] = {x.x, x.y, x.z, x.w};
-      uint32_t f[8];
+      for (int i = 0; i < N; ++i) {
+        const int u = i * 32 + lane, r = u / C, c = u % C;
+        const uint4 x = w[i];
+        const uint32_t words[4] = {x.x, x.y, x.z, x.w};
+        uint32_t f[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        f[2 * j] = pair(e4m3x2_to_f16x2(words[j]));
-        f[2 * j + 1] = pair(e4m3x2_hi_to_f16x2(words[j]));
+        for (int j = 0; j < 4; ++j) {
+          f[2 * j] = pair(e4m3x2_to_f16x2(words[j]));
+          f[2 * j + 1] = pair(e4m3x2_hi_to_f16x2(words[j]));
+        }
+        store16(dst + piece_at<Z::kBlock64>(r, 2 * c), f[0], f[1], f[2], f[3]);
+        store16(dst + piece_at<Z::kBlock64>(r, 2 * c + 1), f[4], f[5], f[6], f[7]);
       }
-      store16(dst + piece_at<Z::kBlock64>(r, 2 * c), f[0], f[1], f[2], f[3]);
-      store16(dst + piece_at<Z::kBlock64>(r, 2 * c + 1), f[4], f[5], f[6], f[7]);
     }
   }
 };

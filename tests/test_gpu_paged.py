@@ -481,6 +481,43 @@ def test_crowds_of_candidates_refused_replayed_and_on_two_streams(quantised):
         assert torch.equal(out, good)
 
 
+def test_crowds_of_candidates_beside_kernels_that_hold_tensor_memory():
+    """The attention and the projection kernels on another stream: all take
+    tensor memory, whichever gets an SM first."""
+    lens, counts, H, D, N = [900, 1500, 300, 2000] * 8, [20, 30, 17, 40] * 8, 4, 128, 2000
+    pages = su.Pages(lens, H, D, D, 64, torch.bfloat16, False)
+    pages.fill(np.random.default_rng(4))
+    g = torch.Generator().manual_seed(4)
+    qc = su.rows_of((sum(counts), H, D), g, torch.bfloat16)
+    off = _int32(_offsets(counts))
+    n = [700, 1024, 333, 64] * 8
+    x = [su.rows_of((sum(n), H, D), g, torch.bfloat16) for _ in range(3)]
+    seq = _int32(_offsets(n))
+    func = _int32(np.concatenate([np.arange(1, m + 1) for m in n])[None])
+    w = su.rows_of((1, 512, H * D), g, torch.bfloat16)[0]
+
+    def paged():
+        return hb.fwd_paged(qc, pages.cache, pages.d_lens, pages.d_table, N, cand_offsets=off)
+
+    def others():
+        return hb.fwd(*x, seq, func, 1024), hb.project_rows(x[0].view(-1, H * D), w)[0]
+
+    want, want_others = paged(), others()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got, got_others = [], []
+    for _ in range(10):
+        for s in streams:
+            with torch.cuda.stream(s):
+                if s is streams[1]:
+                    got_others.append(others())
+                else:
+                    got.append(paged())
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in got)
+    assert all(torch.equal(a, b) for o in got_others for a, b in zip(o, want_others))
+
+
 def test_a_length_past_the_page_table_is_refused():
     pages = su.Pages([40, 40], 1, 32, 32, 16, torch.bfloat16, False)
     pages.fill(np.random.default_rng(0))
