@@ -535,7 +535,9 @@ def set_handoff_limit_for_tests(limit_ns: int) -> None:
 # A decode step is a few microseconds on the GPU. The calls below go through
 # the extension of csrc/serving_ext.cpp, which checks the tensors, allocates the
 # outputs and calls the selected library's entry points; ctypes and checks in
-# Python take three times as long as the step.
+# Python take three times as long as the step. It launches on the current stream
+# and allocates from that stream's memory, so a ``stream`` given is made the
+# current one: an output of another stream's memory could still be in use there.
 
 EXT_PATH = os.path.join(_HERE, "_serving.so")
 _ext_module = None
@@ -558,21 +560,6 @@ def load_extension():
         _ext_module.bind(*(ctypes.cast(getattr(lib, "hstu_attn_" + n), ctypes.c_void_p).value for n in names))
         _ext_library = _active
     return _ext_module
-
-
-def _serve(name, stream, *args):
-    """One call of the extension. It launches on the current stream and allocates
-    from that stream's memory, so a ``stream`` given is made the current one: an
-    output of another stream's memory could still be in use there."""
-    call = getattr(load_extension(), name)
-    if stream is None:
-        r = call(*args)
-    else:
-        with torch.cuda.stream(stream):
-            r = call(*args)
-    if type(r) is int:
-        _check(r, "hstu_attn_" + name)
-    return r
 
 
 _ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
@@ -616,8 +603,14 @@ def rope(q, k, positions, table: RopeTable, backward: bool = False, outs=None, s
     slices of a wider projection; k may be None. ``backward=True`` takes the
     gradients of q' and k' to those of q and k. ``outs`` may be (q, k) itself:
     the rows are then rotated in place."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return rope(q, k, positions, table, backward, outs)
     qo, ko = (None, None) if outs is None else outs
-    return _serve("rope", stream, q, k, positions, table._addr, table._device, bool(backward), qo, ko)
+    r = load_extension().rope(q, k, positions, table._addr, table._device, bool(backward), qo, ko)
+    if type(r) is int:
+        _check(r, "hstu_attn_rope")
+    return r
 
 
 class PagedCache:
@@ -676,8 +669,14 @@ def cache_write(cache: PagedCache, k, v, seq_offsets, cache_lens, page_table, ro
     (hstu_attn_cache_write); ``rope`` rotates k on its way, by ``positions``
     or by its place in the cache. ``cache_lens`` is not changed. With a ``ws``
     (256 bytes) skipped rows are reported by ``device_status``."""
-    _serve("cache_write", stream, cache._addr, cache._device, k, v, seq_offsets, cache_lens, page_table,
-           0 if rope is None else rope._addr, 0 if rope is None else rope._device, positions, ws)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return cache_write(cache, k, v, seq_offsets, cache_lens, page_table, rope, positions, ws)
+    st = load_extension().cache_write(cache._addr, cache._device, k, v, seq_offsets, cache_lens, page_table,
+                                      0 if rope is None else rope._addr, 0 if rope is None else rope._device,
+                                      positions, ws)
+    if st is not None:
+        _check(st, "hstu_attn_cache_write")
 
 
 def cache_read(cache: PagedCache, seq_offsets, rows: int, page_table, starts=None, outs=None,
@@ -685,8 +684,14 @@ def cache_read(cache: PagedCache, seq_offsets, rows: int, page_table, starts=Non
     """(k, v) of cached rows, jagged and contiguous, in the cache's dtype
     (hstu_attn_cache_read): ``rows`` rows, those of sequence b from position
     ``starts[b]`` (0 without ``starts``)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return cache_read(cache, seq_offsets, rows, page_table, starts, outs, ws)
     k, v = (None, None) if outs is None else outs
-    return _serve("cache_read", stream, cache._addr, cache._device, seq_offsets, rows, page_table, starts, k, v, ws)
+    r = load_extension().cache_read(cache._addr, cache._device, seq_offsets, rows, page_table, starts, k, v, ws)
+    if type(r) is int:
+        _check(r, "hstu_attn_cache_read")
+    return r
 
 
 def paged_workspace(cache: PagedCache, batch: int, num_candidates: int, max_seqlen: int) -> torch.Tensor:
@@ -704,5 +709,12 @@ def fwd_paged(q_c, cache: PagedCache, cache_lens, page_table, max_seqlen: int, a
     One candidate a sequence without ``cand_offsets``; all cached rows are
     visible without ``func_c`` (nfunc, C). With a ``ws`` (``paged_workspace``)
     of its own a caller can read ``device_status``."""
-    return _serve("fwd_paged", stream, cache._addr, cache._device, q_c, cache_lens, page_table, max_seqlen,
-                  1.0 / math.sqrt(cache.dim) if alpha is None else alpha, cand_offsets, func_c, ws, out)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return fwd_paged(q_c, cache, cache_lens, page_table, max_seqlen, alpha, cand_offsets, func_c, ws, out)
+    r = load_extension().fwd_paged(cache._addr, cache._device, q_c, cache_lens, page_table, max_seqlen,
+                                   1.0 / math.sqrt(cache.dim) if alpha is None else alpha, cand_offsets, func_c, ws,
+                                   out)
+    if type(r) is int:
+        _check(r, "hstu_attn_fwd_paged")
+    return r
