@@ -15,7 +15,7 @@ namespace hstu {
 //     has many: 64 users of 512 to 2048 rows and 0 to 48 candidates took 64 us so and
 //     72 us with 512 keys for all. With fewer the short splits that no sequence uses
 //     would cost more than they give.
-//   - paged_many_kernel (more than 16 on average) takes 59 us of them with 512 keys
+//   - paged_many_kernel (more than 16 on average, lengths past 256) takes 59 us of them with 512 keys
 //     at the least, 61 with 1024 and 58 with 2048; 16 users of 20000 rows 172 with 512.
 struct PagedLayout {
   int split = 0, nsplit = 0;
@@ -27,7 +27,7 @@ static PagedLayout paged_layout(const CacheView& c, const hstu_cache_t* cache, i
   constexpr int64_t kCtas = 2400;
   PagedLayout l;
   l.tensor = c.dim == kManyDim && c.dim_v == kManyDim && (cache->e4m3 || cache->dtype != HSTU_DTYPE_F16) &&
-             num_cand > 16 * static_cast<int64_t>(batch);
+             num_cand > 16 * static_cast<int64_t>(batch) && max_seqlen > 256;
   l.shorter = !l.tensor && num_cand > 8 * static_cast<int64_t>(batch);
   const int64_t want = static_cast<int64_t>(max_seqlen) * batch * c.heads / kCtas;
   l.split = static_cast<int>(

@@ -1,6 +1,6 @@
 // Candidate rows against a paged K/V cache where sequences have many of them: the
-// kernel for bf16 and 8-bit pages with D_qk = D_v = 128 and more than 16 candidates a
-// sequence on average (paged_kernel takes the rest).
+// kernel for bf16 and 8-bit pages with D_qk = D_v = 128, more than 16 candidates a
+// sequence on average and N above 256 (paged_kernel takes the rest).
 //
 // The formula is paged.cuh's: o = sum_j silu(alpha q.k_j) / N v_j. With this many
 // candidates paged_kernel is bound by its matrix instructions and the operands it
@@ -34,7 +34,8 @@
 // 206), 16 users of 20000 rows with 40 each 172 (294), 64 users of 512 to 2048 rows with
 // 0 to 48 each 59 (64), with 16 each 49 (47). 8-bit pages: 40 each 397 (791), 0 to 48
 // each 66 (85). With widths of 64, 0 to 48 each took 52 (45): a step's copies are
-// too small there for its waits.
+// too small there for its waits. 200 users with 8 to 48 each, N up to 304: 44 (55); N
+// up to 176, a step or two a CTA, of which an SM holds two here and three there: 38 (34).
 #pragma once
 
 #include "paged.cuh"

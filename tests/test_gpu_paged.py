@@ -379,7 +379,7 @@ def test_many_candidates_take_several_passes():
         _run(pages, rows, counts, None, max(full))
 
 
-# More than 16 candidates a sequence on average, widths of 128: the kernel whose
+# More than 16 candidates a sequence on average, widths of 128, N above 256: the kernel whose
 # products are tcgen05's (bf16 and 8-bit pages).
 MANY_TYPES = [(torch.bfloat16, False), (torch.bfloat16, True), (torch.float16, True), (torch.float16, False)]
 MANY_SIZES = [
