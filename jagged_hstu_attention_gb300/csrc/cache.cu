@@ -50,12 +50,12 @@ __device__ __forceinline__ bool place_row(const CacheParams& p, int64_t t, int64
   bool ok = find_sequence(p.seq_offsets, p.batch, t, b, first);
   if (t >= p.rows) return false;
   if (ok) {
-    const int start = p.starts ? __ldg(p.starts + b) : 0;
+    const int start = p.starts ? p.starts[b] : 0;
     pos = t - first + start;
     ok = start >= 0 && pos < (static_cast<int64_t>(p.max_pages) << p.cache.page_shift);
   }
   if (ok) {
-    page = __ldg(p.page_table + static_cast<int64_t>(b) * p.max_pages + (pos >> p.cache.page_shift));
+    page = p.page_table[static_cast<int64_t>(b) * p.max_pages + (pos >> p.cache.page_shift)];
     slot = static_cast<int>(pos & ((1 << p.cache.page_shift) - 1));
     ok = page >= 0 && page < p.cache.num_pages;
   }
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(const CacheP
   float c[8], s[8];
   const bool turned = ROPE != 0 && has_k && kc.turned;
   if (turned && ok)
-    rope_factors(p.turns, kc.first, kc.second, p.positions ? __ldg(p.positions + row) : pos, p.magnitude, 1.0f, c, s);
+    rope_factors(p.turns, kc.first, kc.second, p.positions ? p.positions[row] : pos, p.magnitude, 1.0f, c, s);
 #pragma unroll
   for (int i = 0; i < HEADS; ++i) {
     if (i >= heads) break;
@@ -219,10 +219,10 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const CachePar
       const int64_t at = cache_row(p.cache, page, h0 + i, slot_in_page);
       if (E4M3) {
         const uint8_t* codes = static_cast<const uint8_t*>(base) + at * width;
-        const uint2 x = __ldg(reinterpret_cast<const uint2*>(codes + k.c0));
-        const uint2 y = __ldg(reinterpret_cast<const uint2*>(codes + k.c1));
+        const uint2 x = *reinterpret_cast<const uint2*>(codes + k.c0);
+        const uint2 y = *reinterpret_cast<const uint2*>(codes + k.c1);
         u[i].a = make_uint4(x.x, x.y, y.x, y.y);
-        byte[i] = __ldg(scales + at);
+        byte[i] = scales[at];
       } else {
         u[i] = load_chunks(static_cast<const T*>(base) + at * width, k);
       }

@@ -27,25 +27,24 @@ __device__ __forceinline__ int64_t cache_row(const CacheView& c, int64_t page, i
 // finds the sequence of its first row together, 32 offsets a step, and each
 // lane goes on from there. (A search by halving takes 6 to 10 dependent loads,
 // most of the time of a call with few rows.) Every lane of the warp calls it.
-__device__ __forceinline__ bool find_sequence(const int32_t* __restrict__ offsets, int batch, int64_t t, int& b,
-                                              int& first) {
+__device__ __forceinline__ bool find_sequence(const int32_t* offsets, int batch, int64_t t, int& b, int& first) {
   const int lane = threadIdx.x & 31;
   const int64_t t0 = __shfl_sync(0xffffffffu, t, 0);
   int lo = 0, n = batch;
   while (n > 1) {
     const int step = (n + 31) / 32, at = lane * step;
-    const uint32_t below = __ballot_sync(0xffffffffu, at < n && __ldg(offsets + lo + at) <= t0);
+    const uint32_t below = __ballot_sync(0xffffffffu, at < n && offsets[lo + at] <= t0);
     const int k = max(31 - __clz(below), 0);  // the last probe at or below t0
     lo += k * step;
     n = min(step, n - k * step);
   }
   b = lo;
-  first = __ldg(offsets + b);
-  int next = __ldg(offsets + b + 1);
+  first = offsets[b];
+  int next = offsets[b + 1];
   while (next <= t && b + 1 < batch) {
     ++b;
     first = next;
-    next = __ldg(offsets + b + 1);
+    next = offsets[b + 1];
   }
   return first >= 0 && first <= t && t < next;
 }

@@ -29,6 +29,10 @@ cudaError_t ensure_smem_limit(Kernel kernel, int smem, std::atomic<uint64_t>& do
 // They are launched so that a kernel's blocks may be placed while the one
 // before it ends; every block begins with chain(), which waits until that one
 // has completed and its writes are visible, and lets the next launch begin.
+// A chained kernel so begins while others still write what it will read: its
+// loads are ordinary ones, after chain(). (Loads through the read-only path,
+// __ldg or const __restrict__, are for memory that nothing writes while the
+// kernel lives, and the compiler may move them in front of chain().)
 template <typename... Params, typename... Args>
 cudaError_t launch_chained(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t stream,
                            const Args&... args) {

@@ -240,6 +240,18 @@ __device__ __forceinline__ void tile_words(const PagedSplit& sp, int w, const in
   }
 }
 
+// The n intervals of a candidate from its raw values, cut to [0, len); empty
+// ones are [0, 0).
+__device__ __forceinline__ void paged_intervals(const int (&raw)[2 * kMaxIntervals - 1], int len, int n,
+                                                int (&lo)[kMaxIntervals], int (&hi)[kMaxIntervals]) {
+#pragma unroll
+  for (int i = 0; i < kMaxIntervals; ++i) {
+    lo[i] = i == 0 ? 0 : min(max(raw[i > 0 ? 2 * i - 1 : 0], 0), len);
+    hi[i] = min(max(raw[2 * i], 0), len);
+    if (i >= n || hi[i] <= lo[i]) lo[i] = hi[i] = 0;
+  }
+}
+
 // Lists the tiles that the pass's candidates see. A single candidate's raw
 // intervals are in every thread's registers.
 template <bool MANY>
@@ -252,7 +264,11 @@ __device__ __forceinline__ int paged_list(const PagedParams& p, const PagedSplit
     if (tid < 2 * kPagedWords) sp.bits[tid] = 0;
     __syncthreads();
     if (tid < ncand) {
-      load_row_intervals<kMaxIntervals>(p.func, p.num_cand, sp.c0 + tid, sp.len, true, lo, hi, (1u << n) - 1u);
+      int mine[2 * kMaxIntervals - 1];
+#pragma unroll
+      for (int i = 0; i < 2 * kMaxIntervals - 1; ++i)
+        mine[i] = i < p.nfunc ? p.func[static_cast<int64_t>(i) * p.num_cand + sp.c0 + tid] : 0;
+      paged_intervals(mine, sp.len, n, lo, hi);
       for (int w = 0; w < words; ++w) {
         uint32_t seen, whole;
         tile_words(sp, w, lo, hi, n, seen, whole);
@@ -261,12 +277,7 @@ __device__ __forceinline__ int paged_list(const PagedParams& p, const PagedSplit
       }
     }
   } else {
-#pragma unroll
-    for (int i = 0; i < kMaxIntervals; ++i) {  // as load_row_intervals has them
-      lo[i] = i == 0 ? 0 : min(max(raw[i > 0 ? 2 * i - 1 : 0], 0), sp.len);
-      hi[i] = min(max(raw[2 * i], 0), sp.len);
-      if (i >= n || hi[i] <= lo[i]) lo[i] = hi[i] = 0;
-    }
+    paged_intervals(raw, sp.len, n, lo, hi);
     if (tid < kPagedWords) {
       uint32_t seen = 0, whole = 0;
       if (tid < words) tile_words(sp, tid, lo, hi, n, seen, whole);
@@ -356,7 +367,7 @@ __device__ __forceinline__ bool paged_open(const PagedParams& p, PagedTables<MAN
 #pragma unroll
   for (int i = 0; i < kPageLoads; ++i) {
     const int at = i * THREADS + tid;
-    page[i] = at < most_pages ? __ldg(p.page_table + static_cast<int64_t>(b) * p.max_pages + page0 + at) : -1;
+    page[i] = at < most_pages ? p.page_table[static_cast<int64_t>(b) * p.max_pages + page0 + at] : -1;
   }
   // Checks of this sequence (every CTA of it comes to the same answer).
   bool ok = true;
@@ -523,7 +534,7 @@ __device__ __forceinline__ int paged_pass(const PagedParams& p, const PagedSplit
         // columns of this lane in step st: two for k 0..7, two for 8..15
         const int st = i * (KE / 4) + j;
         const uint2 u =
-            has ? __ldg(reinterpret_cast<const uint2*>(qrow + i * 4 * KE + t * KE + 4 * j)) : make_uint2(0, 0);
+            has ? *reinterpret_cast<const uint2*>(qrow + i * 4 * KE + t * KE + 4 * j) : make_uint2(0, 0);
         qa[n][st][0] = u.x;
         qa[n][st][1] = u.y;
         if (kSplitQ)
@@ -849,7 +860,7 @@ __global__ void __launch_bounds__(32 * W, PagedSizes<DQ, DV, E4M3, MANY, W>::kRe
   int raw[2 * kMaxIntervals - 1];
 #pragma unroll
   for (int i = 0; i < 2 * kMaxIntervals - 1; ++i)
-    raw[i] = !MANY && p.func && i < p.nfunc ? __ldg(p.func + static_cast<int64_t>(i) * p.num_cand + b) : 0;
+    raw[i] = !MANY && p.func && i < p.nfunc ? p.func[static_cast<int64_t>(i) * p.num_cand + b] : 0;
 
   PagedSplit sp;
   int splits;

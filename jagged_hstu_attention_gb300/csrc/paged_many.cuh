@@ -105,7 +105,7 @@ struct TileCopy {
     for (int i = 0; i < N; ++i) {
       const int u = i * 32 + lane, r = u / C, c = u % C;
       if (E4M3)
-        w[i] = r < nkeys ? __ldg(reinterpret_cast<const uint4*>(src + i * 512)) : make_uint4(0, 0, 0, 0);
+        w[i] = r < nkeys ? *reinterpret_cast<const uint4*>(src + i * 512) : make_uint4(0, 0, 0, 0);
       else
         copy16(dst + piece_at<Z::kBlock64>(r, c), src + i * 512, r < nkeys);
     }
@@ -201,8 +201,8 @@ __global__ void __launch_bounds__(256, 2) paged_many_kernel(const PagedParams p)
         if (mine < entries) {
           int nkeys;
           const int64_t row = tile_row(mine, nkeys) + (lane & 15);
-          kbyte = __ldg(p.cache.k_scale + row);
-          vbyte = __ldg(p.cache.v_scale + row);
+          kbyte = p.cache.k_scale[row];
+          vbyte = p.cache.v_scale[row];
         }
       } else {
         copies_commit();
@@ -222,9 +222,8 @@ __global__ void __launch_bounds__(256, 2) paged_many_kernel(const PagedParams p)
 
     for (int i = tid; i < total * (DQ / 8); i += Z::kThreads) {
       const int r = i / (DQ / 8), c = i % (DQ / 8);
-      const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) +
-                                                           static_cast<int64_t>(c0 + r) * p.q_stride +
-                                                           static_cast<int64_t>(h) * DQ) + c);
+      const T* qrow = static_cast<const T*>(p.q) + static_cast<int64_t>(c0 + r) * p.q_stride + static_cast<int64_t>(h) * DQ;
+      const uint4 u = reinterpret_cast<const uint4*>(qrow)[c];
       store16(q_at + piece_at<Z::kQBlock>(r, c), u.x, u.y, u.z, u.w);
     }
     if (tid < 2) odd[tid] = 0;

@@ -35,11 +35,11 @@ __device__ __forceinline__ void phase_cos_sin(uint32_t phase, float& c, float& s
 // position pos; sign = -1 for the transposed rotation. pos * turns wraps modulo
 // one turn in 64-bit integers, so the phase is exact at any position, negative
 // ones included.
-__device__ __forceinline__ void rope_factors(const uint64_t* __restrict__ turns, int first, int second, int64_t pos,
-                                             float magnitude, float sign, float (&c)[8], float (&s)[8]) {
+__device__ __forceinline__ void rope_factors(const uint64_t* turns, int first, int second, int64_t pos, float magnitude,
+                                             float sign, float (&c)[8], float (&s)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const uint64_t phase = static_cast<uint64_t>(pos) * __ldg(turns + (i < 4 ? first + i : second + i - 4));
+    const uint64_t phase = static_cast<uint64_t>(pos) * turns[i < 4 ? first + i : second + i - 4];
     phase_cos_sin(static_cast<uint32_t>(phase >> 32), c[i], s[i]);
     c[i] *= magnitude;
     s[i] *= magnitude * sign;
