@@ -474,8 +474,12 @@ HSTU_API size_t hstu_attn_paged_workspace_size(const hstu_cache_t* cache, int32_
  * that sees nothing gets 0. The cache's length is split over CTAs, whose sums
  * are joined in a fixed order (bitwise repeatable). A sequence with bad
  * offsets, length or page sets HSTU_ERR_DEVICE_INPUT in the error word of ws;
- * its rows of o_c are left as they were, and so are those of a sequence whose
- * products do not end in time (HSTU_ERR_TIMEOUT). */
+ * its rows of o_c are left as they were (where offsets are out of order, rows
+ * that another sequence claims too may hold its results).
+ * Where the products of one head of a sequence do not end in time
+ * (HSTU_ERR_TIMEOUT), that head's part of the sequence's rows is left as it
+ * was; but with one split of the length, the head's earlier groups of 64
+ * candidates have been written by then. Other heads are written. */
 HSTU_API hstu_status_t hstu_attn_fwd_paged(const void* q_c, int64_t q_stride, void* o_c, const hstu_cache_t* cache,
                                            const int32_t* cache_lens, int32_t batch, const int32_t* page_table,
                                            int32_t max_pages, const int32_t* cand_offsets, int64_t num_candidates,
@@ -520,6 +524,9 @@ HSTU_API hstu_status_t hstu_attn_test_wait_timeout(void* ws, int32_t limit_ms, v
  * then raises its abort flag, every role drains what it issued (bounded
  * waits), TMEM is freed and the workspace error word gets HSTU_ERR_TIMEOUT --
  * no fault, no hang, the context stays usable.
+ * The limit also holds for hstu_attn_fwd_paged's waits for the scores of many
+ * candidates (its products on tensor memory); with 1 ns the wait of each
+ * sequence's last group of 64 candidates gives up at once.
  *   limit_ns: 1 .. 2e9; 0 restores the kernels' normal limit (2 s).
  * Process-wide and meant for tests only; returns HSTU_ERR_INVALID_ARG above
  * 2e9. */

@@ -100,11 +100,6 @@ hstu_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? HSTU_OK : HST
 // kernels' normal limit. Only hstu_attn_test_set_handoff_limit changes it.
 std::atomic<uint64_t> g_handoff_limit_ns{0};
 
-uint64_t handoff_limit() {
-  const uint64_t v = g_handoff_limit_ns.load(std::memory_order_relaxed);
-  return v != 0 ? v : hstu::kWaitLimitNs;
-}
-
 // Upper bound on the number of (sequence, tile) work items.
 int grid_items(const hstu_attn_shape_t* s, int nt) {
   const int64_t by_tokens = (s->total + kBlock - 1) / kBlock + s->batch;
@@ -157,6 +152,13 @@ hstu_status_t run_plan(const int32_t* seq_offsets, const int32_t* func, const hs
 }
 
 }  // namespace
+
+namespace hstu {
+uint64_t handoff_limit() {
+  const uint64_t v = g_handoff_limit_ns.load(std::memory_order_relaxed);
+  return v != 0 ? v : kWaitLimitNs;
+}
+}  // namespace hstu
 
 extern "C" {
 
@@ -222,7 +224,7 @@ hstu_status_t hstu_attn_fwd(const void* q, const void* k, const void* v, void* o
   p.max_seqlen = shape->max_seqlen;
   p.alpha = shape->alpha;
   p.inv_n = 1.0f / static_cast<float>(shape->max_seqlen);
-  p.handoff_limit_ns = handoff_limit();
+  p.handoff_limit_ns = hstu::handoff_limit();
   return from_cuda(hstu::launch_fwd(p, (shape->nfunc + 1) / 2, dt, grid_items(shape, l.nt), cs));
 }
 
@@ -271,7 +273,7 @@ hstu_status_t hstu_attn_bwd(const void* dout, const void* q, const void* k, cons
   p.max_seqlen = shape->max_seqlen;
   p.alpha = shape->alpha;
   p.inv_n = 1.0f / static_cast<float>(shape->max_seqlen);
-  p.handoff_limit_ns = handoff_limit();
+  p.handoff_limit_ns = hstu::handoff_limit();
   return from_cuda(hstu::launch_bwd(p, (shape->nfunc + 1) / 2, dt, grid_items(shape, l.nt), cs));
 }
 

@@ -52,6 +52,9 @@ __device__ __forceinline__ void chain() {
   asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Limit of the wait that a test shortens (hstu_attn_test_set_handoff_limit), in ns.
+uint64_t handoff_limit();
+
 cudaError_t launch_plan(const PlanParams& p, cudaStream_t stream);
 // grid_items: upper bound on the number of work items (CTAs = items * heads).
 // One translation unit per input type keeps the many kernel variants

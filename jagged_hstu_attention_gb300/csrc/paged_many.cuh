@@ -276,7 +276,10 @@ __global__ void __launch_bounds__(256, 2) paged_many_kernel(const PagedParams p)
         key = key0 + (lane & 15);
         part = p.func ? (sp.list[mine] & 0x8000) != 0 : key0 + kPagedTile > sp.k1;
       }
-      ok = mbar_wait(s_bar, s_phase, abort_flag);
+      // A limit of 1 ns, set only by a test, gives up at once, in the last pass, so
+      // that the way out runs with a product and copies in flight.
+      ok = !(p.wait_limit_ns <= 1 && ce - c0 <= kPagedPass) &&
+           mbar_wait(s_bar, s_phase, abort_flag, p.wait_limit_ns > 1 ? p.wait_limit_ns : kWaitLimitNs);
       s_phase ^= 1;
       tc_fence_after();
       if (!E4M3) fetch_k(t + 1);  // K is free
