@@ -524,9 +524,9 @@ HSTU_API hstu_status_t hstu_attn_test_wait_timeout(void* ws, int32_t limit_ms, v
  * then raises its abort flag, every role drains what it issued (bounded
  * waits), TMEM is freed and the workspace error word gets HSTU_ERR_TIMEOUT --
  * no fault, no hang, the context stays usable.
- * The limit also holds for hstu_attn_fwd_paged's waits for the scores of many
- * candidates (its products on tensor memory); with 1 ns the wait of each
- * sequence's last group of 64 candidates gives up at once.
+ * With 1 ns hstu_attn_fwd_paged's waits for products on tensor memory give up
+ * too, in each sequence's last group of 64 candidates; longer limits leave
+ * them as they are.
  *   limit_ns: 1 .. 2e9; 0 restores the kernels' normal limit (2 s).
  * Process-wide and meant for tests only; returns HSTU_ERR_INVALID_ARG above
  * 2e9. */

@@ -119,7 +119,7 @@ HSTU_API hstu_status_t hstu_attn_fwd_paged(const void* q_c, int64_t q_stride, vo
   p.shorter = l.shorter;
   p.alpha = alpha;
   p.inv_n = 1.0f / static_cast<float>(max_seqlen);
-  p.wait_limit_ns = hstu::handoff_limit();
+  p.give_up = hstu::handoff_limit() <= 1;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (report && cudaMemsetAsync(ws, 0, hstu::kHdrWords * 4, cs) != cudaSuccess) return HSTU_ERR_CUDA;
   const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(batch) * p.cache.heads * p.nsplit);

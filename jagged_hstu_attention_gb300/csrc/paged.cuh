@@ -84,7 +84,7 @@ struct PagedParams {
   bool tensor;            // many candidates: paged_many_kernel
   bool shorter;           // splits get shorter with a sequence's candidates (paged_split_keys)
   float alpha, inv_n;
-  uint64_t wait_limit_ns;  // of paged_many_kernel's waits for the scores; a test sets 1
+  bool give_up;  // set by a test: paged_many_kernel takes its way out of a wait that ran out
 };
 
 template <typename M>
