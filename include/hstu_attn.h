@@ -113,6 +113,9 @@ typedef struct {
 /* hstu_attn_fwd_paged: the error word of ws is neither cleared nor set, which
  * saves a launch. Bad sequences are left out as without the flag. */
 #define HSTU_FLAG_NO_STATUS 2
+/* hstu_attn_fwd_paged: rows of o_c that would be left as they were are set to
+ * 0, for an o_c that held nothing yet. */
+#define HSTU_FLAG_ZERO_SKIPPED 4
 
 /* 1 if the library has kernels for that nfunc (1, 3, 5, 7, 9), else 0. The pages'
  * wheel bakes NFUNC in at compile time (TorchEasyRec PR #670 review thread on
@@ -438,11 +441,17 @@ HSTU_API hstu_status_t hstu_attn_cache_write(const hstu_cache_t* cache, const vo
  * starts[b] + i (starts DEVICE int32 (batch), NULL: 0). k (rows, H, D_qk) and
  * v (rows, H, D_v) are written, contiguous, of cache->dtype; e4m3 rows are
  * multiplied out and rounded once. Rows that the checks of
- * hstu_attn_cache_write skip are left as they were; ws as there. */
+ * hstu_attn_cache_write skip are left as they were by hstu_attn_cache_read and
+ * set to 0 by hstu_attn_cache_read_zeroed, for a k and v that held nothing
+ * yet; ws as there. */
 HSTU_API hstu_status_t hstu_attn_cache_read(const hstu_cache_t* cache, void* k, void* v, const int32_t* seq_offsets,
                                             int32_t batch, int64_t rows, const int32_t* starts,
                                             const int32_t* page_table, int32_t max_pages, void* ws, size_t ws_bytes,
                                             void* stream);
+HSTU_API hstu_status_t hstu_attn_cache_read_zeroed(const hstu_cache_t* cache, void* k, void* v,
+                                                   const int32_t* seq_offsets, int32_t batch, int64_t rows,
+                                                   const int32_t* starts, const int32_t* page_table,
+                                                   int32_t max_pages, void* ws, size_t ws_bytes, void* stream);
 
 /* Bytes of workspace that hstu_attn_fwd_paged needs; 0 if an argument is out
  * of range. They serve calls with fewer candidates too (the other arguments
@@ -468,14 +477,15 @@ HSTU_API size_t hstu_attn_paged_workspace_size(const hstu_cache_t* cache, int32_
  *            each of the calls that may run at the same time; NULL is
  *            taken with HSTU_FLAG_NO_STATUS where that size is 256 (one split:
  *            nothing but the error word)
- *   flags    HSTU_FLAG_NONE or HSTU_FLAG_NO_STATUS
+ *   flags    HSTU_FLAG_NONE, or HSTU_FLAG_NO_STATUS and HSTU_FLAG_ZERO_SKIPPED
  * Slots past a sequence's length and positions that a candidate does not see
  * do not reach it, whatever they hold (NaN and infinities too). A candidate
  * that sees nothing gets 0. The cache's length is split over CTAs, whose sums
  * are joined in a fixed order (bitwise repeatable). A sequence with bad
  * offsets, length or page sets HSTU_ERR_DEVICE_INPUT in the error word of ws;
  * its rows of o_c are left as they were (where offsets are out of order, rows
- * that another sequence claims too may hold its results).
+ * that another sequence claims too may hold its results, or 0 with
+ * HSTU_FLAG_ZERO_SKIPPED).
  * Where the products of one head of a sequence do not end in time
  * (HSTU_ERR_TIMEOUT), that head's part of the sequence's rows is left as it
  * was; but with one split of the length, the head's earlier groups of 64

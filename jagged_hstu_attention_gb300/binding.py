@@ -38,6 +38,7 @@ EXPORTED = (
     "hstu_attn_bwd_targets", "hstu_attn_project_workspace_size", "hstu_attn_project_rows",
     "hstu_attn_project_rows_bwd", "hstu_attn_test_set_handoff_limit", "hstu_attn_rope_table", "hstu_attn_rope",
     "hstu_attn_cache_write", "hstu_attn_cache_read", "hstu_attn_paged_workspace_size", "hstu_attn_fwd_paged",
+    "hstu_attn_cache_read_zeroed",
 )
 FUNC_CAUSAL, FUNC_SLA, FUNC_ONERANK = 0, 1, 2
 NOALLOC_SCRATCH_BYTES = 8 << 20
@@ -166,6 +167,7 @@ def load(path: str = None) -> ctypes.CDLL:
         "hstu_attn_cache_write": (ctypes.c_int, [vp, vp, i64, vp, i64, vp, i32, i64, vp, vp, i32, vp, vp, vp, sz,
                                                  vp]),
         "hstu_attn_cache_read": (ctypes.c_int, [vp, vp, vp, vp, i32, i64, vp, vp, i32, vp, sz, vp]),
+        "hstu_attn_cache_read_zeroed": (ctypes.c_int, [vp, vp, vp, vp, i32, i64, vp, vp, i32, vp, sz, vp]),
         "hstu_attn_paged_workspace_size": (sz, [vp, i32, i64, i32]),
         "hstu_attn_fwd_paged": (ctypes.c_int, [vp, i64, vp, vp, vp, i32, vp, i32, vp, i64, vp, i32, i32,
                                                ctypes.c_float, vp, sz, u32, vp]),
@@ -556,7 +558,7 @@ def load_extension():
                                    "(python -c 'import __graft_entry__ as g; g.build()')")
             from . import _serving
             _ext_module = _serving
-        names = ("rope", "cache_write", "cache_read", "paged_workspace_size", "fwd_paged")
+        names = ("rope", "cache_write", "cache_read", "paged_workspace_size", "fwd_paged", "cache_read_zeroed")
         _ext_module.bind(*(ctypes.cast(getattr(lib, "hstu_attn_" + n), ctypes.c_void_p).value for n in names))
         _ext_library = _active
     return _ext_module
@@ -683,7 +685,8 @@ def cache_read(cache: PagedCache, seq_offsets, rows: int, page_table, starts=Non
                ws: Optional[torch.Tensor] = None, stream=None):
     """(k, v) of cached rows, jagged and contiguous, in the cache's dtype
     (hstu_attn_cache_read): ``rows`` rows, those of sequence b from position
-    ``starts[b]`` (0 without ``starts``)."""
+    ``starts[b]`` (0 without ``starts``). Rows without a valid place are left
+    as they were in ``outs`` and are zeros in new tensors."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return cache_read(cache, seq_offsets, rows, page_table, starts, outs, ws)
@@ -708,7 +711,8 @@ def fwd_paged(q_c, cache: PagedCache, cache_lens, page_table, max_seqlen: int, a
     ``cache_lens[b]`` cached rows of their sequences (hstu_attn_fwd_paged).
     One candidate a sequence without ``cand_offsets``; all cached rows are
     visible without ``func_c`` (nfunc, C). With a ``ws`` (``paged_workspace``)
-    of its own a caller can read ``device_status``."""
+    of its own a caller can read ``device_status``. Rows of bad sequences are
+    left as they were in ``out`` and are zeros in a new tensor."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return fwd_paged(q_c, cache, cache_lens, page_table, max_seqlen, alpha, cand_offsets, func_c, ws, out)

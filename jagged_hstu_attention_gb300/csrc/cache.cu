@@ -39,6 +39,7 @@ struct CacheParams {
   int32_t batch, max_pages, rotary;
   int32_t slots;  // threads of a token: those of the wider of k and v
   bool one_head;  // heads of a thread: 1 or kCacheHeads
+  bool zero;      // reader: skipped rows become zeros
   float magnitude;
 };
 
@@ -192,6 +193,14 @@ __device__ __forceinline__ uint4 decode8(const uint2 codes, float scale) {
   return pack8<T>(f);
 }
 
+// A skipped row's slot, 16 columns of the row that begins at `at`.
+template <typename T>
+__device__ __forceinline__ void zero_slot(void* out, int64_t at, int slot, int width) {
+  if (16 * slot >= width) return;
+  uint4* to = reinterpret_cast<uint4*>(static_cast<T*>(out) + at + 16 * slot);
+  to[0] = to[1] = make_uint4(0, 0, 0, 0);
+}
+
 template <typename T, bool E4M3, int HEADS>
 __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const CacheParams p) {
   chain();
@@ -199,10 +208,18 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const CachePar
   const int64_t unit = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   const int slot = static_cast<int>(unit) & (p.slots - 1);
   const int64_t row = unit / p.slots;
+  const int h0 = blockIdx.y * HEADS, heads = min(HEADS, p.cache.heads - h0);
   int64_t pos, page;
   int slot_in_page;
-  if (!place_row(p, row, pos, page, slot_in_page)) return;
-  const int h0 = blockIdx.y * HEADS, heads = min(HEADS, p.cache.heads - h0);
+  if (!place_row(p, row, pos, page, slot_in_page)) {
+    if (p.zero && row < p.rows) {
+      for (int i = 0; i < heads; ++i) {
+        zero_slot<T>(p.k, (row * p.cache.heads + h0 + i) * p.cache.dim, slot, p.cache.dim);
+        zero_slot<T>(p.v, (row * p.cache.heads + h0 + i) * p.cache.dim_v, slot, p.cache.dim_v);
+      }
+    }
+    return;
+  }
 #pragma unroll
   for (int part = 0; part < 2; ++part) {
     const int width = part ? p.cache.dim_v : p.cache.dim;
@@ -297,6 +314,27 @@ static cudaError_t launch_read_typed(const CacheParams& p, dim3 grid, bool e4m3,
   return launch_chained(kernel, grid, kReadThreads, 0, stream, p);
 }
 
+static hstu_status_t cache_read(const hstu_cache_t* cache, void* k, void* v, const int32_t* seq_offsets, int32_t batch,
+                                int64_t rows, const int32_t* starts, const int32_t* page_table, int32_t max_pages,
+                                void* ws, size_t ws_bytes, bool zero, cudaStream_t stream) {
+  CacheParams p;
+  dim3 grid;
+  const hstu_status_t st = cache_common(cache, seq_offsets, batch, rows, starts, page_table, max_pages, ws, ws_bytes,
+                                        kReadThreads, &p, &grid);
+  if (st != HSTU_OK) return st;
+  const auto bad = [](const void* q) { return !q || reinterpret_cast<uintptr_t>(q) % 16 != 0; };
+  if (rows > 0 && (bad(k) || bad(v))) return HSTU_ERR_INVALID_ARG;
+  p.k = k;
+  p.v = v;
+  p.zero = zero;
+  if (clear_header(ws, stream) != cudaSuccess) return HSTU_ERR_CUDA;
+  if (rows == 0) return HSTU_OK;
+  const cudaError_t e = cache->dtype == HSTU_DTYPE_F16
+                            ? launch_read_typed<__half>(p, grid, cache->e4m3 != 0, stream)
+                            : launch_read_typed<__nv_bfloat16>(p, grid, cache->e4m3 != 0, stream);
+  return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+}
+
 }  // namespace hstu
 
 extern "C" {
@@ -343,23 +381,16 @@ HSTU_API hstu_status_t hstu_attn_cache_read(const hstu_cache_t* cache, void* k, 
                                             int32_t batch, int64_t rows, const int32_t* starts,
                                             const int32_t* page_table, int32_t max_pages, void* ws, size_t ws_bytes,
                                             void* stream) {
-  hstu::CacheParams p;
-  dim3 grid;
-  const hstu_status_t st =
-      hstu::cache_common(cache, seq_offsets, batch, rows, starts, page_table, max_pages, ws, ws_bytes,
-                         hstu::kReadThreads, &p, &grid);
-  if (st != HSTU_OK) return st;
-  const auto bad = [](const void* q) { return !q || reinterpret_cast<uintptr_t>(q) % 16 != 0; };
-  if (rows > 0 && (bad(k) || bad(v))) return HSTU_ERR_INVALID_ARG;
-  p.k = k;
-  p.v = v;
-  cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  if (hstu::clear_header(ws, cs) != cudaSuccess) return HSTU_ERR_CUDA;
-  if (rows == 0) return HSTU_OK;
-  const cudaError_t e = cache->dtype == HSTU_DTYPE_F16
-                            ? hstu::launch_read_typed<__half>(p, grid, cache->e4m3 != 0, cs)
-                            : hstu::launch_read_typed<__nv_bfloat16>(p, grid, cache->e4m3 != 0, cs);
-  return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+  return hstu::cache_read(cache, k, v, seq_offsets, batch, rows, starts, page_table, max_pages, ws, ws_bytes, false,
+                          static_cast<cudaStream_t>(stream));
+}
+
+HSTU_API hstu_status_t hstu_attn_cache_read_zeroed(const hstu_cache_t* cache, void* k, void* v,
+                                                   const int32_t* seq_offsets, int32_t batch, int64_t rows,
+                                                   const int32_t* starts, const int32_t* page_table,
+                                                   int32_t max_pages, void* ws, size_t ws_bytes, void* stream) {
+  return hstu::cache_read(cache, k, v, seq_offsets, batch, rows, starts, page_table, max_pages, ws, ws_bytes, true,
+                          static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

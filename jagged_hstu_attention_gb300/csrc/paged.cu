@@ -116,6 +116,7 @@ HSTU_API hstu_status_t hstu_attn_fwd_paged(const void* q_c, int64_t q_stride, vo
     p.nsplit = (max_seqlen + p.split - 1) / p.split;
   }
   p.tensor = l.tensor;
+  p.zero = (flags & HSTU_FLAG_ZERO_SKIPPED) != 0;
   p.shorter = l.shorter;
   p.alpha = alpha;
   p.inv_n = 1.0f / static_cast<float>(max_seqlen);

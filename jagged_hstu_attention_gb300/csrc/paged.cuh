@@ -82,6 +82,7 @@ struct PagedParams {
   int32_t batch, max_pages, num_cand, nfunc, max_seqlen;
   int32_t split, nsplit;  // keys of a split (of sequences with few candidates); splits of max_seqlen, at most
   bool tensor;            // many candidates: paged_many_kernel
+  bool zero;              // rows that would be left as they were become zeros
   bool shorter;           // splits get shorter with a sequence's candidates (paged_split_keys)
   float alpha, inv_n;
   bool give_up;  // set by a test: paged_many_kernel takes its way out of a wait that ran out
@@ -347,6 +348,13 @@ struct PagedTables {
   int entries;
 };
 
+// Zeros in head h of candidate rows [first, last), by all threads of the CTA.
+inline __device__ __noinline__ void paged_zero_rows(void* o, int heads, int dim_v, int h, int64_t first, int64_t last) {
+  const int pieces = dim_v / 8;  // of 16 bytes
+  for (int64_t i = threadIdx.x; i < (last - first) * pieces; i += blockDim.x)
+    static_cast<uint4*>(o)[((first + i / pieces) * heads + h) * pieces + i % pieces] = make_uint4(0, 0, 0, 0);
+}
+
 // Opens one split, of `keys` keys, of sequence b for candidates [cb, ce): reads its
 // pages and checks the sequence. False where there is nothing to do; `bad`
 // where a page of the split is no page of the cache (it has no tiles then).
@@ -377,6 +385,15 @@ __device__ __forceinline__ bool paged_open(const PagedParams& p, PagedTables<MAN
        static_cast<int64_t>(len) <= (static_cast<int64_t>(p.max_pages) << p.cache.page_shift);
   if (!ok) {
     if (p.header && split == 0 && h == 0 && tid == 0) atomicOr(p.header + kHdrErr, kErrInput);
+    if (p.zero && split == 0) {
+      // Offsets with a wrong end make every sequence bad, and each takes a share
+      // of all rows. With right ends every row lies between the offsets of some
+      // sequence, a bad one among them reaching past the ends at the most.
+      const bool ends = offsets0 == 0 && offsets1 == p.num_cand;
+      const int64_t rows = p.num_cand;
+      paged_zero_rows(p.o, p.cache.heads, p.cache.dim_v, h, ends ? max(cb, 0) : rows * b / p.batch,
+                      ends ? min(ce, p.num_cand) : rows * (b + 1) / p.batch);
+    }
     return false;
   }
   if (cb == ce) return false;
@@ -895,7 +912,7 @@ __global__ void __launch_bounds__(32 * W, PagedSizes<DQ, DV, E4M3, MANY, W>::kRe
       if (splits > 1)
         *reinterpret_cast<float4*>(p.partial + (at * p.nsplit + split) * DV + d) =
             make_float4(sum[0], sum[1], sum[2], sum[3]);
-      else if (!bad)
+      else if (!bad || p.zero)  // the sums of a bad sequence are zeros: it has no tiles
         *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + at * DV + d) =
             make_uint2(Elem<T>::pack2(sum[0] * p.inv_n, sum[1] * p.inv_n),
                        Elem<T>::pack2(sum[2] * p.inv_n, sum[3] * p.inv_n));
@@ -910,7 +927,8 @@ __global__ void __launch_bounds__(32 * W, PagedSizes<DQ, DV, E4M3, MANY, W>::kRe
 // warps take a share of the splits each, and their sums are added in warp
 // order. Its blocks start while the last CTAs of paged_kernel run and wait for
 // them. A sequence with one split was written there, and one with a bad split
-// is left alone.
+// is left alone or becomes zeros, as are rows that no sequence is found for
+// (offsets out of order).
 template <typename T, int DV, int WARPS>
 __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p) {
   chain();
@@ -920,11 +938,13 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p) {
   const int64_t unit = static_cast<int64_t>(blockIdx.x) * kUnits + warp / WARPS;
   const int64_t c = unit / p.cache.heads;
   const int h = static_cast<int>(unit - c * p.cache.heads);
-  bool live = c < p.num_cand;
+  const bool row = c < p.num_cand;
+  bool live = row, found = row;
   int b = static_cast<int>(c), first, keys = p.split;
   if (p.cand_offsets) {  // lanes of a warp ask for the same candidate
-    live = find_sequence(p.cand_offsets, p.batch, live ? c : 0, b, first) && live && p.cand_offsets[0] == 0 &&
-           p.cand_offsets[p.batch] == p.num_cand && p.cand_offsets[b + 1] <= p.num_cand;  // as paged_kernel has it
+    found = find_sequence(p.cand_offsets, p.batch, row ? c : 0, b, first) && row;
+    live = found && p.cand_offsets[0] == 0 && p.cand_offsets[p.batch] == p.num_cand &&
+           p.cand_offsets[b + 1] <= p.num_cand;  // as paged_kernel has it
     keys = live ? paged_split_keys(p, p.cand_offsets[b + 1] - first) : p.split;
   }
   const int len = live ? p.lens[b] : 0;
@@ -934,7 +954,9 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p) {
   const int32_t* states = p.states + (static_cast<int64_t>(b) * p.cache.heads + h) * p.nsplit;
   bool good = true;
   for (int s = lane; s < splits; s += 32) good = good && states[s] == 1;
-  live = __all_sync(0xffffffffu, good) && live;
+  good = __all_sync(0xffffffffu, good);
+  const bool blank = p.zero && row && (!found || (live && !good));
+  live = good && live;
 
   const int share = (splits + WARPS - 1) / WARPS, s0 = warp % WARPS * share, s1 = min(splits, s0 + share);
   float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -962,7 +984,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p) {
       sum.w += v.w;
     }
   }
-  if (live && lane < DV / 4)
+  if ((live || blank) && lane < DV / 4)  // zeros where blank
     *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + unit * DV + 4 * lane) =
         make_uint2(Elem<T>::pack2(sum.x * p.inv_n, sum.y * p.inv_n), Elem<T>::pack2(sum.z * p.inv_n, sum.w * p.inv_n));
 }

@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(256, 2) paged_many_kernel(const PagedParams p)
       const int64_t at = static_cast<int64_t>(c0 + r) * p.cache.heads + h;
       if (splits > 1)
         *reinterpret_cast<float4*>(p.partial + (at * p.nsplit + split) * DV + d) = sum;
-      else if (!bad)
+      else if (!bad || p.zero)
         *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + at * DV + d) =
             make_uint2(Elem<T>::pack2(sum.x * p.inv_n, sum.y * p.inv_n),
                        Elem<T>::pack2(sum.z * p.inv_n, sum.w * p.inv_n));
@@ -406,6 +406,7 @@ __global__ void __launch_bounds__(256, 2) paged_many_kernel(const PagedParams p)
   }
 
   if (!ok) {  // a product did not end in time: leave none in flight
+    if (p.zero && splits == 1) paged_zero_rows(p.o, p.cache.heads, DV, sp.h, sp.c0, sp.ce);
     if (!E4M3) copies_wait<0>();
     if (tid == 0) {
       umma_commit(smem_u32(&bar_drain));

@@ -30,6 +30,7 @@ namespace {
 decltype(&hstu_attn_rope) g_rope = nullptr;
 decltype(&hstu_attn_cache_write) g_cache_write = nullptr;
 decltype(&hstu_attn_cache_read) g_cache_read = nullptr;
+decltype(&hstu_attn_cache_read) g_cache_read_zeroed = nullptr;
 decltype(&hstu_attn_paged_workspace_size) g_paged_size = nullptr;
 decltype(&hstu_attn_fwd_paged) g_fwd_paged = nullptr;
 
@@ -278,7 +279,8 @@ PyObject* cache_read(PyObject* const* a, Py_ssize_t n) {
   const at::Tensor* k_given = tensor_or_none(a[6], "outs[0]");
   const at::Tensor* v_given = tensor_or_none(a[7], "outs[1]");
   at::Tensor k, v;
-  if (k_given || v_given) {
+  const bool given = k_given || v_given;
+  if (given) {
     if (!k_given || !v_given) throw Refused{"outs must hold k and v"};
     check_output(*k_given, type, rows, H, cache->head_dim, index, "outs[0]");
     check_output(*v_given, type, rows, H, cache->head_dim_v, index, "outs[1]");
@@ -291,7 +293,8 @@ PyObject* cache_read(PyObject* const* a, Py_ssize_t n) {
   const Workspace ws = check_ws(tensor_or_none(a[8], "ws"), index);
   void* stream = current_stream(index);
   const hstu_status_t st = without_lock([&] {
-    return g_cache_read(cache, k.data_ptr(), v.data_ptr(), off, static_cast<int32_t>(B), rows, first, pages,
+    // Rows that are skipped hold zeros in new memory, not what was there before.
+    return (given ? g_cache_read : g_cache_read_zeroed)(cache, k.data_ptr(), v.data_ptr(), off, static_cast<int32_t>(B), rows, first, pages,
                         static_cast<int32_t>(table.size(1)), ws.ptr, ws.bytes, stream);
   });
   if (st != HSTU_OK) return PyLong_FromLong(st);
@@ -323,14 +326,15 @@ PyObject* fwd_paged(PyObject* const* a, Py_ssize_t n) {
   const int32_t* intervals = func ? check_ints(*func, {nfunc, C}, index, "func_c") : nullptr;
   const at::Tensor* given = tensor_or_none(a[10], "out");
   at::Tensor out;
+  uint32_t flags = 0;
   if (given) {
     check_output(*given, type, C, H, cache->head_dim_v, index, "out");
     out = *given;
   } else {
     out = new_rows(C, H, cache->head_dim_v, type, index);
+    flags |= HSTU_FLAG_ZERO_SKIPPED;  // not what the memory held before
   }
   Workspace ws = check_ws(tensor_or_none(a[9], "ws"), index);
-  uint32_t flags = 0;
   at::Tensor own;  // freed on return, for the allocator to reuse behind this call on its stream
   if (!ws.ptr) {
     flags |= HSTU_FLAG_NO_STATUS;  // nobody could read the error word
@@ -353,15 +357,16 @@ PyObject* fwd_paged(PyObject* const* a, Py_ssize_t n) {
   return r;
 }
 
-// bind(rope, cache_write, cache_read, paged_workspace_size, fwd_paged):
-// addresses of the entry points.
+// bind(rope, cache_write, cache_read, paged_workspace_size, fwd_paged,
+// cache_read_zeroed): addresses of the entry points.
 PyObject* bind(PyObject* const* a, Py_ssize_t n) {
-  if (n != 5) throw Refused{"five addresses"};
+  if (n != 6) throw Refused{"six addresses"};
   g_rope = reinterpret_cast<decltype(g_rope)>(address(a[0]));
   g_cache_write = reinterpret_cast<decltype(g_cache_write)>(address(a[1]));
   g_cache_read = reinterpret_cast<decltype(g_cache_read)>(address(a[2]));
   g_paged_size = reinterpret_cast<decltype(g_paged_size)>(address(a[3]));
   g_fwd_paged = reinterpret_cast<decltype(g_fwd_paged)>(address(a[4]));
+  g_cache_read_zeroed = reinterpret_cast<decltype(g_cache_read_zeroed)>(address(a[5]));
   Py_RETURN_NONE;
 }
 
