@@ -45,10 +45,10 @@ struct CacheParams {
 
 // Page-table lookup of jagged row t: its position and its (page, slot).
 // False (and the error word set) where the row has no valid place. Every lane
-// of the warp calls it; rows past the last are nobody's.
+// of the warp calls it; rows past the last are nobody's and search as the last.
 __device__ __forceinline__ bool place_row(const CacheParams& p, int64_t t, int64_t& pos, int64_t& page, int& slot) {
   int b, first;
-  bool ok = find_sequence(p.seq_offsets, p.batch, t, b, first);
+  bool ok = find_sequence(p.seq_offsets, p.batch, min(t, p.rows - 1), b, first);
   if (t >= p.rows) return false;
   if (ok) {
     const int start = p.starts ? p.starts[b] : 0;

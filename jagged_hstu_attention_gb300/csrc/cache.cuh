@@ -25,14 +25,18 @@ __device__ __forceinline__ int64_t cache_row(const CacheView& c, int64_t page, i
 // The sequence of jagged row t, the last b with offsets[b] <= t; false where
 // the offsets do not bracket t. The rows of a warp are neighbours: the warp
 // finds the sequence of its first row together, 32 offsets a step, and each
-// lane goes on from there. (A search by halving takes 6 to 10 dependent loads,
-// most of the time of a call with few rows.) Every lane of the warp calls it.
+// lane goes on from there: four sequences one by one, which is where the rows of
+// a step lie, then in steps that double and halve again, so that a run of
+// empty sequences costs two loads for each doubling of its length. (A search by
+// halving from the start takes 6 to 10 dependent loads, most of the time of a
+// call with few rows.) Every lane of the warp calls it, those without a row of
+// their own with a row of the batch.
 __device__ __forceinline__ bool find_sequence(const int32_t* offsets, int batch, int64_t t, int& b, int& first) {
   const int lane = threadIdx.x & 31;
   const int64_t t0 = __shfl_sync(0xffffffffu, t, 0);
   int lo = 0, n = batch;
   while (n > 1) {
-    const int step = (n + 31) / 32, at = lane * step;
+    const int step = (n - 1) / 32 + 1, at = lane * step;
     const uint32_t below = __ballot_sync(0xffffffffu, at < n && offsets[lo + at] <= t0);
     const int k = max(31 - __clz(below), 0);  // the last probe at or below t0
     lo += k * step;
@@ -41,9 +45,24 @@ __device__ __forceinline__ bool find_sequence(const int32_t* offsets, int batch,
   b = lo;
   first = offsets[b];
   int next = offsets[b + 1];
-  while (next <= t && b + 1 < batch) {
+  for (int i = 0; i < 4 && next <= t && b + 1 < batch; ++i) {
     ++b;
     first = next;
+    next = offsets[b + 1];
+  }
+  if (next <= t && b + 1 < batch) {
+    uint32_t step = 1, end = b + 1;  // offsets[end] <= t so far
+    while (end < batch && offsets[end] <= t) {
+      b = end;
+      step *= 2;
+      end = b + min(step, batch - b);
+    }
+    while (end - b > 1) {
+      const int mid = b + (end - b) / 2;
+      if (offsets[mid] <= t) b = mid;
+      else end = mid;
+    }
+    first = offsets[b];
     next = offsets[b + 1];
   }
   return first >= 0 && first <= t && t < next;
