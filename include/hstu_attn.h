@@ -440,7 +440,8 @@ HSTU_API hstu_status_t hstu_attn_cache_write(const hstu_cache_t* cache, const vo
  * of sequence b (output rows seq_offsets[b] .. seq_offsets[b+1]) is position
  * starts[b] + i (starts DEVICE int32 (batch), NULL: 0). k (rows, H, D_qk) and
  * v (rows, H, D_v) are written, contiguous, of cache->dtype; e4m3 rows are
- * multiplied out and rounded once. Rows that the checks of
+ * multiplied out and rounded once; values past the largest finite one of the
+ * type, which a code near it may stand for, come back as that. Rows that the checks of
  * hstu_attn_cache_write skip are left as they were by hstu_attn_cache_read and
  * set to 0 by hstu_attn_cache_read_zeroed, for a k and v that held nothing
  * yet; ws as there. */

@@ -12,6 +12,8 @@
 // sequence and computed its cosines alone, they took 100 us. A chunk of 3500 rows
 // into 8-bit pages and 90000 rows read back from them take 50 us, 5.7 TB/s, of
 // which the read is 43 us.
+#include <type_traits>
+
 #include "cache.cuh"
 #include "internal.h"
 #include "rope.cuh"
@@ -177,7 +179,18 @@ __global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(const CacheP
   }
 }
 
-// Eight codes times their scale, rounded to T.
+// x cut to [-top, top]; NaN stays.
+__device__ __forceinline__ float cut(float x, float top) {
+  float r;
+  asm("{\n\t.reg .f32 low;\n\tmax.NaN.f32 low, %1, %3;\n\tmin.NaN.f32 %0, low, %2;\n\t}"
+      : "=f"(r)
+      : "f"(x), "f"(top), "f"(-top));
+  return r;
+}
+
+// Eight codes times their scale, rounded to T. The largest values of T may have
+// been rounded up to a code above them (fp16: 63488 and up to 65536): those come
+// back as T's largest, not as infinity.
 template <typename T>
 __device__ __forceinline__ uint4 decode8(const uint2 codes, float scale) {
   float f[8];
@@ -190,6 +203,9 @@ __device__ __forceinline__ uint4 decode8(const uint2 codes, float scale) {
     f[4 * i + 2] = Elem<__half>::lo(hi) * scale;
     f[4 * i + 3] = Elem<__half>::hi(hi) * scale;
   }
+  constexpr float kTop = std::is_same<T, __half>::value ? 65504.0f : 3.38953139e38f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = cut(f[i], kTop);
   return pack8<T>(f);
 }
 
