@@ -290,7 +290,7 @@ static hstu_status_t cache_common(const hstu_cache_t* cache, const int32_t* seq_
   // A thread for each head while that does not fill the GPU (1024 threads on each
   // of 152 SMs): the heads of a call with few rows are then moved at once.
   p->one_head = blocks * p->cache.heads * threads <= 152 * 1024;
-  *grid = dim3(static_cast<unsigned>(blocks),
+  *grid = dim3(static_cast<unsigned>(blocks > 0 ? blocks : 1),
                p->one_head ? p->cache.heads : (p->cache.heads + kCacheHeads - 1) / kCacheHeads);
   p->seq_offsets = seq_offsets;
   p->starts = starts;
@@ -344,7 +344,7 @@ static hstu_status_t cache_read(const hstu_cache_t* cache, void* k, void* v, con
   p.v = v;
   p.zero = zero;
   if (clear_header(ws, stream) != cudaSuccess) return HSTU_ERR_CUDA;
-  if (rows == 0) return HSTU_OK;
+  if (rows == 0 && !ws) return HSTU_OK;  // with an error word, the offsets are checked all the same
   const cudaError_t e = cache->dtype == HSTU_DTYPE_F16
                             ? launch_read_typed<__half>(p, grid, cache->e4m3 != 0, stream)
                             : launch_read_typed<__nv_bfloat16>(p, grid, cache->e4m3 != 0, stream);
@@ -385,7 +385,7 @@ HSTU_API hstu_status_t hstu_attn_cache_write(const hstu_cache_t* cache, const vo
   p.positions = positions;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (hstu::clear_header(ws, cs) != cudaSuccess) return HSTU_ERR_CUDA;
-  if (rows == 0) return HSTU_OK;
+  if (rows == 0 && !ws) return HSTU_OK;  // with an error word, the offsets are checked all the same
   const int mode = rope ? (rope->interleaved ? 2 : 1) : 0;
   const cudaError_t e = cache->dtype == HSTU_DTYPE_F16
                             ? hstu::launch_write_typed<__half>(p, grid, cache->e4m3 != 0, mode, cs)
