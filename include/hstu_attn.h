@@ -374,7 +374,8 @@ HSTU_API hstu_status_t hstu_attn_rope_table(const hstu_rope_spec_t* spec, uint64
  *   q, k, q_out, k_out  DEVICE (tokens, H, D), heads and columns contiguous,
  *            rows *_stride elements apart (>= H D and a multiple of 8), 16-byte
  *            aligned. An output may be its own input (same pointer and
- *            stride); otherwise outputs overlap no input.
+ *            stride); otherwise no row of an output may share memory with one
+ *            of an input or of the other output (HSTU_ERR_INVALID_ARG).
  *   positions  DEVICE int32 (tokens), any value; angles are computed from
  *            exact phases (see hstu_attn_rope_table).
  *   head_dim  32, 64 or 128, >= R; dtype HSTU_DTYPE_BF16 or HSTU_DTYPE_F16.
@@ -439,7 +440,8 @@ HSTU_API hstu_status_t hstu_attn_cache_write(const hstu_cache_t* cache, const vo
 /* Reads cached rows back into jagged tensors for the contiguous kernels: row i
  * of sequence b (output rows seq_offsets[b] .. seq_offsets[b+1]) is position
  * starts[b] + i (starts DEVICE int32 (batch), NULL: 0). k (rows, H, D_qk) and
- * v (rows, H, D_v) are written, contiguous, of cache->dtype; e4m3 rows are
+ * v (rows, H, D_v) are written, contiguous, of cache->dtype, and may not overlap
+ * (HSTU_ERR_INVALID_ARG); e4m3 rows are
  * multiplied out and rounded once; values past the largest finite one of the
  * type, which a code near it may stand for, come back as that. Rows that the checks of
  * hstu_attn_cache_write skip are left as they were by hstu_attn_cache_read and
@@ -466,7 +468,7 @@ HSTU_API size_t hstu_attn_paged_workspace_size(const hstu_cache_t* cache, int32_
  * tokens that are to see themselves are written to the cache before the call.
  *   q_c      DEVICE (num_candidates, H, D_qk), rows q_stride elements apart
  *            (as for hstu_attn_rope); o_c (num_candidates, H, D_v) contiguous,
- *            not overlapping q_c
+ *            not overlapping q_c (HSTU_ERR_INVALID_ARG)
  *   cache_lens   DEVICE int32 (batch), each in [0, max_seqlen]
  *   cand_offsets DEVICE int32 (batch+1) as for hstu_attn_fwd_targets, or NULL:
  *            one candidate a sequence (num_candidates = batch)

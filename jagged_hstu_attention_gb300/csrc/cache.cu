@@ -340,6 +340,8 @@ static hstu_status_t cache_read(const hstu_cache_t* cache, void* k, void* v, con
   if (st != HSTU_OK) return st;
   const auto bad = [](const void* q) { return !q || reinterpret_cast<uintptr_t>(q) % 16 != 0; };
   if (rows > 0 && (bad(k) || bad(v))) return HSTU_ERR_INVALID_ARG;
+  const int64_t k_row = 2ll * p.cache.heads * p.cache.dim, v_row = 2ll * p.cache.heads * p.cache.dim_v;
+  if (rows_meet(k, k_row, k_row, v, v_row, v_row, rows)) return HSTU_ERR_INVALID_ARG;
   p.k = k;
   p.v = v;
   p.zero = zero;

@@ -83,8 +83,10 @@ HSTU_API hstu_status_t hstu_attn_fwd_paged(const void* q_c, int64_t q_stride, vo
   if (!cache_lens || !page_table || bad4(cache_lens) || bad4(page_table) || bad4(cand_offsets) || bad4(func_c))
     return HSTU_ERR_INVALID_ARG;
   if (num_candidates > 0 && (!hstu::rows_ok(q_c, q_stride, p.cache.heads, p.cache.dim) || !o_c ||
-                             reinterpret_cast<uintptr_t>(o_c) % 16 != 0 || o_c == q_c))
+                             reinterpret_cast<uintptr_t>(o_c) % 16 != 0))
     return HSTU_ERR_INVALID_ARG;
+  const int64_t q_row = 2ll * p.cache.heads * p.cache.dim, o_row = 2ll * p.cache.heads * p.cache.dim_v;
+  if (hstu::rows_meet(o_c, o_row, o_row, q_c, 2 * q_stride, q_row, num_candidates)) return HSTU_ERR_INVALID_ARG;
   const bool half = cache->dtype == HSTU_DTYPE_F16;
   const hstu::PagedLayout l = hstu::paged_layout(p.cache, cache, batch, num_candidates, max_seqlen);
   const bool report = !(flags & HSTU_FLAG_NO_STATUS);

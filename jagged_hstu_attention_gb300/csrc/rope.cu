@@ -152,7 +152,14 @@ HSTU_API hstu_status_t hstu_attn_rope(const void* q, int64_t q_stride, const voi
     return HSTU_ERR_INVALID_ARG;
   if ((q == q_out && q_stride != q_out_stride) || (k && k == k_out && k_stride != k_out_stride))
     return HSTU_ERR_INVALID_ARG;
-  if (k && (q_out == k_out || q_out == k || k_out == q)) return HSTU_ERR_INVALID_ARG;
+  const int64_t row = static_cast<int64_t>(num_heads) * head_dim * 2;
+  const auto meet = [&](const void* a, int64_t sa, const void* b, int64_t sb) {
+    return hstu::rows_meet(a, 2 * sa, row, b, 2 * sb, row, tokens);
+  };
+  if (q_out != q && meet(q_out, q_out_stride, q, q_stride)) return HSTU_ERR_INVALID_ARG;
+  if (k && ((k_out != k && meet(k_out, k_out_stride, k, k_stride)) || meet(q_out, q_out_stride, k, k_stride) ||
+            meet(k_out, k_out_stride, q, q_stride) || meet(q_out, q_out_stride, k_out, k_out_stride)))
+    return HSTU_ERR_INVALID_ARG;
   hstu::RopeParams p{};
   p.in[0] = q;
   p.in[1] = k;

@@ -3,6 +3,8 @@
 // writer, which rotates k on its way into the pages).
 #pragma once
 
+#include <algorithm>
+
 #include "../../include/hstu_attn.h"
 #include "common.cuh"
 
@@ -109,6 +111,23 @@ inline hstu_status_t check_rope(const hstu_rope_t* r, int dim) {
 inline bool rows_ok(const void* p, int64_t stride, int heads, int dim) {
   return p && reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride >= static_cast<int64_t>(heads) * dim &&
          stride % 8 == 0;
+}
+
+// Whether one of n rows of `wa` bytes, `sa` bytes apart from a on, shares memory
+// with one of n rows of b. (The rows of two slices of one projection lie
+// between each other without meeting.)
+inline bool rows_meet(const void* a, int64_t sa, int64_t wa, const void* b, int64_t sb, int64_t wb, int64_t n) {
+  const int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
+  if (n <= 0 || d >= (n - 1) * sa + wa || -d >= (n - 1) * sb + wb) return false;
+  const auto floor_div = [](int64_t x, int64_t y) { return x >= 0 ? x / y : -((-x + y - 1) / y); };
+  // Rows of b, of which row j begins at d + j sb, that meet [x, x + wa): -wb < d + j sb - x < wa.
+  const auto first = [&](int64_t x) { return floor_div(x - d - wb, sb) + 1; };
+  const auto last = [&](int64_t x) { return floor_div(x - d + wa - 1, sb); };
+  if (sa == sb)  // the same for every row of a, but for the ends
+    return std::max(first(0), 1 - n) <= std::min(last(0), n - 1);
+  for (int64_t i = 0; i < n; ++i)
+    if (std::max<int64_t>(first(i * sa), 0) <= std::min(last(i * sa), n - 1)) return true;
+  return false;
 }
 
 inline bool head_width_ok(int d) { return d == 32 || d == 64 || d == 128; }
