@@ -125,6 +125,7 @@ Workspace check_ws(const at::Tensor* t, int index) {
   if (!t) return {};
   check_device(*t, index, "ws");
   if (!t->is_contiguous()) throw Refused{"ws must be contiguous"};
+  if (t->nbytes() == 0) throw Refused{"ws is empty"};  // its address is null, as if none had been given
   return {t->data_ptr(), static_cast<size_t>(t->nbytes())};
 }
 
