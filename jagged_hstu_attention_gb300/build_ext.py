@@ -6,14 +6,19 @@ work-list entry before using it (a debugging aid, results bit-identical).
 Every translation unit of both is compiled by nvcc in one parallel pool, then
 each set is linked into one shared library next to this file (the CUDA
 runtime is linked statically). ``_serving.so`` is the CPython extension of the
-serving calls, compiled beside them against the installed torch. A library
-newer than every source is not rebuilt.
+serving calls, compiled beside them against the installed torch; the libraries
+need neither torch nor Python's headers, and are built where it cannot be. A
+library newer than every source is not rebuilt, the extension only while torch
+and Python are those it was compiled against.
 """
 from __future__ import annotations
 
+import importlib.metadata
 import os
 import shutil
 import subprocess
+import sys
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -26,6 +31,7 @@ LIB_PATH = os.path.join(PKG, LIB_NAME)
 CHECKED_LIB_PATH = os.path.join(PKG, "libhstu_attn_checked.so")
 EXT_SOURCE = "serving_ext.cpp"
 EXT_PATH = os.path.join(PKG, "_serving.so")
+EXT_STAMP = os.path.join(BUILD_DIR, "serving_built_against.txt")
 # variant -> (library, object directory, extra nvcc flags)
 VARIANTS = {
     "release": (LIB_PATH, BUILD_DIR, []),
@@ -67,6 +73,22 @@ def up_to_date(lib: str = LIB_PATH) -> bool:
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
+def _extension_against() -> str:
+    """What the extension's binary depends on besides its sources."""
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        version = "none"
+    return f"torch {version}, python {sys.version}"
+
+
+def extension_up_to_date() -> bool:
+    if not up_to_date(EXT_PATH) or not os.path.exists(EXT_STAMP):
+        return False
+    with open(EXT_STAMP) as f:
+        return f.read() == _extension_against()
+
+
 def _build_extension() -> None:
     import sysconfig
 
@@ -84,12 +106,17 @@ def _build_extension() -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {EXT_SOURCE}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, EXT_PATH)
+    os.makedirs(os.path.dirname(EXT_STAMP), exist_ok=True)
+    with open(EXT_STAMP, "w") as f:
+        f.write(_extension_against())
 
 
 def build(force: bool = False, verbose: bool = False, variants=("release", "checked")) -> str:
-    """Builds the requested variants; returns the release library's path."""
+    """Builds the requested variants; returns the release library's path. Where
+    the extension cannot be built there is a warning and none is left, so that
+    the serving calls of binding.py raise; everything else is whole."""
     todo = [v for v in variants if force or not up_to_date(VARIANTS[v][0])]
-    extension = force or not up_to_date(EXT_PATH)
+    extension = force or not extension_up_to_date()
     if not todo and not extension:
         return LIB_PATH
     nvcc = _nvcc()
@@ -113,8 +140,7 @@ def build(force: bool = False, verbose: bool = False, variants=("release", "chec
     with ThreadPoolExecutor(max_workers=min(len(jobs), max(os.cpu_count() or 1, len(SOURCES))) + 1) as ex:
         ext = ex.submit(_build_extension) if extension else None
         objs = dict(zip(jobs, ex.map(compile_one, jobs)))
-        if ext is not None:
-            ext.result()
+        failed = None if ext is None else ext.exception()
     for v in todo:
         lib = VARIANTS[v][0]
         tmp = lib + ".tmp"
@@ -123,6 +149,10 @@ def build(force: bool = False, verbose: bool = False, variants=("release", "chec
         if r.returncode != 0:
             raise RuntimeError(f"link failed ({v}):\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, lib)
+    if failed is not None:
+        if os.path.exists(EXT_PATH):  # an older one, of other sources or another torch
+            os.remove(EXT_PATH)
+        warnings.warn(f"{os.path.basename(EXT_PATH)} has not been built: {failed}", RuntimeWarning, stacklevel=2)
     return LIB_PATH
 
 
