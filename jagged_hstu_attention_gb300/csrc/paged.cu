@@ -15,8 +15,10 @@ namespace hstu {
 //     has many: 64 users of 512 to 2048 rows and 0 to 48 candidates took 64 us so and
 //     72 us with 512 keys for all. With fewer the short splits that no sequence uses
 //     would cost more than they give.
-//   - paged_many_kernel (more than 16 on average, lengths past 256) takes 59 us of them with 512 keys
-//     at the least, 61 with 1024 and 58 with 2048; 16 users of 20000 rows 172 with 512.
+//   - paged_many_kernel (widths of 128, bf16 or 8-bit pages, more than 16 candidates
+//     on average, N above 256; its header has both kernels' times) takes 60 us of
+//     them with 512 keys at the least, 61 with 1024 and 58 with 2048; 16 users of
+//     20000 rows 176 with 512.
 struct PagedLayout {
   int split = 0, nsplit = 0;
   bool tensor = false, shorter = false;

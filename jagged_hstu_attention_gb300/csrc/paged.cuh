@@ -2,12 +2,14 @@
 // paged_{bf16,f16}{,_e4m3}.cu, launched from paged.cu).
 //
 // For candidate c of sequence b: o = sum_j silu(alpha q.k_j) / N v_j over the
-// visible cached positions j. Every cached row is read once and takes part in
-// as many products as its sequence has candidates, few of them, so the bytes
-// of the cache bound the kernel; the products run on warp-level matrix
-// instructions (m16n8k16), whose operands a warp can take straight from the
-// cache's rows. (Where a sequence has more than 16 candidates the products are
-// worth tcgen05's operand tiles in shared memory: paged_many.cuh.)
+// visible cached positions j. A cached row is read once for each 64 candidates of
+// its sequence (a pass) and takes part in as many products as the pass has
+// candidates, few of them, so the bytes of the cache bound the kernel; the
+// products run on warp-level matrix instructions (m16n8k16), whose operands a
+// warp can take straight from the cache's rows. (Where sequences have more than
+// 16 candidates on average the products are worth tcgen05's operand tiles in
+// shared memory, for the types, widths and lengths that paged.cu's
+// paged_layout names: paged_many.cuh.)
 //
 // Measured, H = 4, D_qk = D_v = 128, histories of 1332 to 3994 rows: one
 // candidate for each of 256 users over 16-bit pages 207 us, 6.8 TB/s, the rate of
@@ -24,9 +26,10 @@
 // its own candidates. Per tile, keys and value columns as the 16 rows of the
 // products and candidates as their 8 columns:
 //   S^T = K Q^T    P = silu(alpha S), zero where not visible
-//   O^T += V^T P^T P in two 16-bit parts, so that P V is as exact as with P in
-//                  fp32 (rounding P to 16 bits instead would be as large an
-//                  error as that of the output's own type)
+//   O^T += V^T P^T P in two 16-bit parts, which leave a relative error of 2^-17 in
+//                  bf16 and 2^-23 in fp16 (fp32: 2^-24); one part alone would be
+//                  off by as much as the output's own rounding to that type
+//                  (2^-8, 2^-11)
 // Up to four candidates ("pair") have two columns each, one for each part of
 // P, so that one instruction adds both. More ("full") take a column each, in
 // one or two groups of eight, and an instruction for each part: a piece of K

@@ -10,11 +10,13 @@
 //   S^T (keys x cands)  = K Q^T       K and Q from shared memory
 //   P = silu(alpha S), zero where not visible, in two 16-bit parts
 //   O^T (Dv x cands)   += V^T [P_hi | P_lo]
-// The sums of the two parts lie side by side in TMEM and are added at the end, so
-// that P V is as exact as with P in fp32. Thread r of a group of four warps has key
-// r: its scores are one TMEM lane, its 8-bit scales two scalars, and its row of P
-// one 128-byte row of shared memory, which is the layout that the second product
-// reads P in (candidates along the row, keys down).
+// The sums of the two parts lie side by side in TMEM and are added at the end. Two
+// bf16 parts leave a relative error of 2^-17 in P (fp32: 2^-24), against the
+// output's rounding of 2^-8 (bf16) or 2^-11 (fp16). Thread r of a group of four
+// warps has key r: its scores are one TMEM lane, its 8-bit scales two scalars, and
+// its row of P one 128-byte row of shared memory, which is the layout that the
+// second product reads P in (candidates along the row, keys down). A pass takes 64
+// candidates, and each further pass reads the split's keys again.
 //
 // A step is eight 16-key tiles, listed as in paged_kernel: keys that no
 // candidate sees are left out, and the second product skips tiles past the
@@ -30,11 +32,11 @@
 // pages have no such exact form, which is why they are not taken here.
 //
 // Measured against paged_kernel, H = 4, 16-bit pages, us: 256 users of 1332 to 3994
-// rows with 24 candidates each 254 (311), with 40 each 327 (533; the bytes alone take
-// 206), 16 users of 20000 rows with 40 each 172 (294), 64 users of 512 to 2048 rows with
-// 0 to 48 each 59 (64), with 16 each 49 (47). 8-bit pages: 40 each 397 (791), 0 to 48
-// each 66 (85). With widths of 64, 0 to 48 each took 52 (45): a step's copies are
-// too small there for its waits. 200 users with 8 to 48 each, N up to 304: 44 (55); N
+// rows with 24 candidates each 256 (311), with 40 each 334 (533; the bytes alone take
+// 206), 16 users of 20000 rows with 40 each 176 (294), 64 users of 512 to 2048 rows with
+// 0 to 48 each 60 (64), with 16 each 49 (47). 8-bit pages: 40 each 405 (791), 0 to 48
+// each 68 (85). With widths of 64, 0 to 48 each took 52 (45): a step's copies are
+// too small there for its waits. 200 users with 8 to 48 each, N up to 304: 45 (55); N
 // up to 176, a step or two a CTA, of which an SM holds two here and three there: 38 (34).
 #pragma once
 
