@@ -529,7 +529,8 @@ def project_rows_bwd(dy, z, x, w, rows=None, want_dbias=True, ws=None, stream=No
 
 def set_handoff_limit_for_tests(limit_ns: int) -> None:
     """Test hook (hstu_attn_test_set_handoff_limit): shortens the attention
-    kernels' accumulator hand-off wait; 0 restores the normal limit."""
+    kernels' accumulator hand-off wait, and with 1 ns makes ``fwd_paged``'s waits
+    on tensor memory give up; 0 restores the normal limits."""
     _check(load().hstu_attn_test_set_handoff_limit(int(limit_ns)), "hstu_attn_test_set_handoff_limit")
 
 
