@@ -79,6 +79,8 @@ typedef enum {
 /* Input and output element types (all tensors of a call share one). */
 #define HSTU_DTYPE_BF16 0
 #define HSTU_DTYPE_F16 1
+/* Tables of hstu_attn_embed and gradients of hstu_attn_embed_bwd only. */
+#define HSTU_DTYPE_F32 2
 
 /* Size limits of a shape:
  *   - T < 2^31, since seq_offsets are int32 (else HSTU_ERR_INVALID_ARG);
@@ -498,6 +500,129 @@ HSTU_API hstu_status_t hstu_attn_fwd_paged(const void* q_c, int64_t q_stride, vo
                                            int32_t max_pages, const int32_t* cand_offsets, int64_t num_candidates,
                                            const int32_t* func_c, int32_t nfunc, int32_t max_seqlen, float alpha,
                                            void* ws, size_t ws_bytes, uint32_t flags, void* stream);
+
+/* ---- The rest of a layer: embedding rows, norms, products with an epilogue.
+ * Their rows are (rows, width) of bf16 or fp16, width a multiple of 8; inputs
+ * with a stride argument may have their rows that many elements apart (a
+ * multiple of 8, at least the width; slices of a wider projection), everything
+ * else is contiguous. Base addresses are 16-byte aligned. An output may not
+ * share memory with an input or another output (HSTU_ERR_INVALID_ARG) where
+ * nothing else is said. Sums are in 32 bits and no atomics order them: results are
+ * bitwise repeatable. */
+
+/* Embedding rows: out[t] = scale * table[ids[t]], rounded once. An id below 0 is
+ * padding: its row is 0.
+ *   table    DEVICE (vocab, dim) of table_dtype: that of the rows, or
+ *            HSTU_DTYPE_F32
+ *   ids      DEVICE (tokens), int32 or int64 (id_bytes 4 or 8)
+ *   out      DEVICE (tokens, dim) of dtype
+ *   ws       256 bytes or NULL: with it, an id of vocab or more sets
+ *            HSTU_ERR_DEVICE_INPUT in the error word; its row is 0 either way
+ * Limits: tokens and vocab below 2^31 - 1, dim a multiple of 8 up to 65536. */
+HSTU_API hstu_status_t hstu_attn_embed(const void* table, int32_t table_dtype, int64_t vocab, int32_t dim,
+                                       const void* ids, int32_t id_bytes, int64_t tokens, float scale, void* out,
+                                       int32_t dtype, void* ws, size_t ws_bytes, void* stream);
+
+/* Bytes of workspace of hstu_attn_embed_bwd; 0 if an argument is out of range. */
+HSTU_API size_t hstu_attn_embed_workspace_size(int64_t tokens, int64_t vocab, int32_t dim);
+
+/* Gradient of the table: dtable[v] = scale * the sum of dy[t] over the tokens t
+ * with ids[t] = v, in 32 bits and in the tokens' order, rounded once to grad_dtype
+ * (the rows' type, or HSTU_DTYPE_F32). Padding and ids of vocab or more are left
+ * out, the latter set HSTU_ERR_DEVICE_INPUT in ws. Rows that no token names
+ * are 0. With accumulate = 1 (HSTU_DTYPE_F32 only) the sums are added to what
+ * dtable holds, and rows that no token names are neither read nor written.
+ *   ws       hstu_attn_embed_workspace_size() bytes, 256-byte aligned, one for
+ *            each of the calls that may run at the same time */
+HSTU_API hstu_status_t hstu_attn_embed_bwd(const void* dy, int64_t dy_stride, int32_t dtype, const void* ids,
+                                           int32_t id_bytes, int64_t tokens, float scale, void* dtable,
+                                           int32_t grad_dtype, int64_t vocab, int32_t dim, int32_t accumulate, void* ws,
+                                           size_t ws_bytes, void* stream);
+
+/* Root-mean-square norm of rows, in front of a layer or behind its attention:
+ *     h = x + residual (rounded to dtype), rstd = 1 / sqrt(mean(h^2) + eps),
+ *     y = h rstd weight gate.
+ *   residual, gate  nullable; h is written where there is a residual, and may
+ *            then be the residual's or x's own rows (contiguous ones); it is NULL
+ *            without one
+ *   y        (rows, width) of dtype; with y_scale (rows) uint8, the rows' 8-bit
+ *            floats (e4m3) under the scale 2^(y_scale - 127) of their row, the
+ *            smallest power of two, 2^-127 at the least, that brings the row's
+ *            finite values to 448 or below; values that are not finite become NaN
+ *   rstd     (rows) fp32, NULL where no backward follows
+ * Limits: width a multiple of 8 up to 8192, eps >= 0. */
+HSTU_API hstu_status_t hstu_attn_rms_norm(const void* x, int64_t x_stride, const void* residual,
+                                          int64_t residual_stride, const void* gate, int64_t gate_stride,
+                                          const void* weight, int64_t rows, int32_t width, int32_t dtype, float eps,
+                                          void* y, uint8_t* y_scale, void* h, float* rstd, void* stream);
+
+/* Rows as 8-bit floats under a scale each, as hstu_attn_rms_norm writes them
+ * (for weights, once). Limits as there. */
+HSTU_API hstu_status_t hstu_attn_quantise_rows(const void* x, int64_t x_stride, int64_t rows, int32_t width,
+                                               int32_t dtype, uint8_t* codes, uint8_t* scale, void* stream);
+
+/* Bytes of workspace of hstu_attn_rms_norm_bwd; 0 if an argument is out of range. */
+HSTU_API size_t hstu_attn_rms_norm_workspace_size(int64_t rows, int32_t width);
+
+/* Gradients of hstu_attn_rms_norm (16-bit output): with u = h rstd and
+ * t = dy gate weight,
+ *     dx = rstd (t - u mean(t u)) + dh   (of x and of the residual alike),
+ *     dgate = dy u weight,  dweight = the sum over rows of dy gate u.
+ *   h, rstd  of the forward (h = x without a residual)
+ *   dh       the gradient that reaches h from its other uses, or NULL
+ *   dgate    written where there is a gate, else NULL; dweight (width) of dtype
+ *   ws       hstu_attn_rms_norm_workspace_size() bytes, 256-byte aligned, one
+ *            for each of the calls that may run at the same time (it holds no
+ *            error word) */
+HSTU_API hstu_status_t hstu_attn_rms_norm_bwd(const void* dy, int64_t dy_stride, const void* h, int64_t h_stride,
+                                              const float* rstd, const void* weight, const void* gate,
+                                              int64_t gate_stride, const void* dh, int64_t dh_stride, int64_t rows,
+                                              int32_t width, int32_t dtype, void* dx, void* dweight, void* dgate,
+                                              void* ws, size_t ws_bytes, void* stream);
+
+/* Activations of hstu_attn_linear: z; z sigmoid(z); z sigmoid(2 sqrt(2 / pi) (z + 0.044715
+ * z^3)), the tanh form of GELU; max(z, 0). */
+#define HSTU_ACT_NONE 0
+#define HSTU_ACT_SILU 1
+#define HSTU_ACT_GELU 2
+#define HSTU_ACT_RELU 3
+
+/* A linear map of rows with its epilogue: z = x w^T + bias, y = act(z) + residual,
+ * with fp32 sums and one rounding each of z and y.
+ *   x        (rows, d_in), w (d_out, d_in) contiguous: of dtype, x_scale and
+ *            w_scale NULL; or 8-bit floats (e4m3) of the rows of x and of w under
+ *            the scales 2^(x_scale - 127) (rows) and 2^(w_scale - 127) (d_out), as
+ *            hstu_attn_rms_norm and hstu_attn_quantise_rows write them
+ *   bias     (d_out) of dtype, or NULL; residual (rows, d_out) of dtype, or NULL
+ *   act      HSTU_ACT_*
+ *   y        (rows, d_out) of dtype; z the same or NULL (a backward with an
+ *            activation reads it)
+ *   ws       256 bytes or NULL: with it, a bounded in-kernel wait that gives up
+ *            sets HSTU_ERR_TIMEOUT in the error word (the rows of y and z are then
+ *            undefined)
+ * Limits: d_in and d_out multiples of 8 (d_in of 16 for 8-bit operands), up to
+ * 65536; the stride of 8-bit x a multiple of 16. */
+HSTU_API hstu_status_t hstu_attn_linear(const void* x, int64_t x_stride, const uint8_t* x_scale, const void* w,
+                                        const uint8_t* w_scale, const void* bias, const void* residual,
+                                        int64_t residual_stride, int64_t rows, int32_t d_in, int32_t d_out,
+                                        int32_t dtype, int32_t act, void* y, void* z, void* ws, size_t ws_bytes,
+                                        void* stream);
+
+/* Bytes of workspace of hstu_attn_linear_bwd; 0 if an argument is out of range. */
+HSTU_API size_t hstu_attn_linear_workspace_size(int64_t rows, int32_t d_in, int32_t d_out, int32_t act);
+
+/* Gradients of hstu_attn_linear with 16-bit operands: g = dy act'(z), rounded to
+ * dtype, dx = g w, dw = g^T x, dbias = the sum of g's rows. (The residual's
+ * gradient is dy.)
+ *   z        (rows, d_out) of the forward; NULL and not read with HSTU_ACT_NONE
+ *   dx       (rows, d_in), dw (d_out, d_in), dbias (d_out) or NULL, of dtype
+ *   ws       hstu_attn_linear_workspace_size() bytes, 256-byte aligned, one for
+ *            each of the calls that may run at the same time; its error word
+ *            as in hstu_attn_linear */
+HSTU_API hstu_status_t hstu_attn_linear_bwd(const void* dy, int64_t dy_stride, const void* z, const void* x,
+                                            int64_t x_stride, const void* w, int64_t rows, int32_t d_in, int32_t d_out,
+                                            int32_t dtype, int32_t act, void* dx, void* dw, void* dbias, void* ws,
+                                            size_t ws_bytes, void* stream);
 
 /* Synchronises the stream, then returns the status recorded in the
  * workspace error word (HSTU_OK, HSTU_ERR_DEVICE_INPUT, HSTU_ERR_TIMEOUT,

@@ -38,7 +38,9 @@ EXPORTED = (
     "hstu_attn_bwd_targets", "hstu_attn_project_workspace_size", "hstu_attn_project_rows",
     "hstu_attn_project_rows_bwd", "hstu_attn_test_set_handoff_limit", "hstu_attn_rope_table", "hstu_attn_rope",
     "hstu_attn_cache_write", "hstu_attn_cache_read", "hstu_attn_paged_workspace_size", "hstu_attn_fwd_paged",
-    "hstu_attn_cache_read_zeroed",
+    "hstu_attn_cache_read_zeroed", "hstu_attn_embed", "hstu_attn_embed_workspace_size", "hstu_attn_embed_bwd",
+    "hstu_attn_rms_norm", "hstu_attn_quantise_rows", "hstu_attn_rms_norm_workspace_size", "hstu_attn_rms_norm_bwd",
+    "hstu_attn_linear", "hstu_attn_linear_workspace_size", "hstu_attn_linear_bwd",
 )
 FUNC_CAUSAL, FUNC_SLA, FUNC_ONERANK = 0, 1, 2
 NOALLOC_SCRATCH_BYTES = 8 << 20
@@ -171,6 +173,21 @@ def load(path: str = None) -> ctypes.CDLL:
         "hstu_attn_paged_workspace_size": (sz, [vp, i32, i64, i32]),
         "hstu_attn_fwd_paged": (ctypes.c_int, [vp, i64, vp, vp, vp, i32, vp, i32, vp, i64, vp, i32, i32,
                                                ctypes.c_float, vp, sz, u32, vp]),
+        "hstu_attn_embed": (ctypes.c_int, [vp, i32, i64, i32, vp, i32, i64, ctypes.c_float, vp, i32, vp, sz, vp]),
+        "hstu_attn_embed_workspace_size": (sz, [i64, i64, i32]),
+        "hstu_attn_embed_bwd": (ctypes.c_int, [vp, i64, i32, vp, i32, i64, ctypes.c_float, vp, i32, i64, i32, i32, vp,
+                                               sz, vp]),
+        "hstu_attn_rms_norm": (ctypes.c_int, [vp, i64, vp, i64, vp, i64, vp, i64, i32, i32, ctypes.c_float, vp, vp, vp,
+                                              vp, vp]),
+        "hstu_attn_quantise_rows": (ctypes.c_int, [vp, i64, i64, i32, i32, vp, vp, vp]),
+        "hstu_attn_rms_norm_workspace_size": (sz, [i64, i32]),
+        "hstu_attn_rms_norm_bwd": (ctypes.c_int, [vp, i64, vp, i64, vp, vp, vp, i64, vp, i64, i64, i32, i32, vp, vp,
+                                                  vp, vp, sz, vp]),
+        "hstu_attn_linear": (ctypes.c_int, [vp, i64, vp, vp, vp, vp, vp, i64, i64, i32, i32, i32, i32, vp, vp, vp, sz,
+                                            vp]),
+        "hstu_attn_linear_workspace_size": (sz, [i64, i32, i32, i32]),
+        "hstu_attn_linear_bwd": (ctypes.c_int, [vp, i64, vp, vp, i64, vp, i64, i32, i32, i32, i32, vp, vp, vp, vp, sz,
+                                                vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -560,7 +577,11 @@ def load_extension():
             from . import _serving
             _ext_module = _serving
         names = ("rope", "cache_write", "cache_read", "paged_workspace_size", "fwd_paged", "cache_read_zeroed")
-        _ext_module.bind(*(ctypes.cast(getattr(lib, "hstu_attn_" + n), ctypes.c_void_p).value for n in names))
+        address = lambda n: ctypes.cast(getattr(lib, "hstu_attn_" + n), ctypes.c_void_p).value
+        _ext_module.bind(*map(address, names))
+        layer = ("embed", "embed_workspace_size", "embed_bwd", "rms_norm", "quantise_rows", "rms_norm_workspace_size",
+                 "rms_norm_bwd", "linear", "linear_workspace_size", "linear_bwd")
+        _ext_module.bind_layer(*map(address, layer))
         _ext_library = _active
     return _ext_module
 
@@ -722,4 +743,182 @@ def fwd_paged(q_c, cache: PagedCache, cache_lens, page_table, max_seqlen: int, a
                                    out)
     if type(r) is int:
         _check(r, "hstu_attn_fwd_paged")
+    return r
+
+
+# ------------------------------------------------------- the rest of a layer
+# Embedding rows, norms and linear maps of (rows, width) matrices, through the same
+# extension. Inputs may be slices of wider rows where the header gives them a
+# stride.
+
+_WIDE = {**DTYPES, torch.float32: 2}
+_ACTS = {"none": 0, "silu": 1, "gelu": 2, "relu": 3}
+
+
+def _dtype_code(dtype, codes, name: str) -> int:
+    if dtype not in codes:
+        raise ValueError(f"{name} must be one of {tuple(codes)}, got {dtype}")
+    return codes[dtype]
+
+
+def _act_code(act: str) -> int:
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}")
+    return _ACTS[act]
+
+
+def embed(table, ids, scale: float = 1.0, dtype=None, out=None, ws: Optional[torch.Tensor] = None, stream=None):
+    """(T, D): ``scale * table[ids]`` (hstu_attn_embed). The table is (V, D), of the
+    rows' type or float32 (the rows are then of ``dtype``, bf16 if it is not
+    given); ids are int32 or int64, below 0 for padding, whose rows are zeros.
+    With a ``ws`` (256 bytes) ids past the table are reported by
+    ``device_status``; their rows are zeros too."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return embed(table, ids, scale, dtype, out, ws)
+    if dtype is None:
+        dtype = torch.bfloat16 if table.dtype == torch.float32 else table.dtype
+    r = load_extension().embed(table, ids, scale, _dtype_code(dtype, DTYPES, "dtype"), out, ws)
+    if type(r) is int:
+        _check(r, "hstu_attn_embed")
+    return r
+
+
+def embed_workspace(tokens: int, vocab: int, dim: int, device="cuda") -> torch.Tensor:
+    """Workspace of ``embed_bwd``."""
+    n = int(load().hstu_attn_embed_workspace_size(tokens, vocab, dim))
+    if n == 0:
+        raise HstuError(2, "hstu_attn_embed_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def embed_bwd(dy, ids, vocab: int, scale: float = 1.0, dtype=torch.float32, out=None, accumulate: bool = False,
+              ws: Optional[torch.Tensor] = None, stream=None):
+    """The table's gradient (vocab, D) of sum(embed(table, ids, scale) * dy), of
+    ``dtype``: float32 or dy's (hstu_attn_embed_bwd). ``accumulate`` adds it to a
+    float32 ``out`` and leaves rows that no id names untouched."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return embed_bwd(dy, ids, vocab, scale, dtype, out, accumulate, ws)
+    r = load_extension().embed_bwd(dy, ids, vocab, scale, _dtype_code(dtype, _WIDE, "dtype"), out, bool(accumulate), ws)
+    if type(r) is int:
+        _check(r, "hstu_attn_embed_bwd")
+    return r
+
+
+class QuantisedRows:
+    """Rows of 8-bit floats (e4m3): ``codes`` (rows, width) and the exponent
+    bytes of their power-of-two scales, ``scale`` (rows,), both uint8. Made by
+    ``quantise_rows`` or ``rms_norm(..., quantise=True)``, taken by ``linear``."""
+
+    __slots__ = ("codes", "scale")
+
+    def __init__(self, codes: torch.Tensor, scale: torch.Tensor):
+        if codes.dtype != torch.uint8 or codes.dim() != 2:
+            raise ValueError(f"codes must be (rows, width) of torch.uint8, got {tuple(codes.shape)} of {codes.dtype}")
+        if scale.dtype != torch.uint8 or tuple(scale.shape) != (codes.shape[0],):
+            raise ValueError(f"scale must be ({codes.shape[0]},) of torch.uint8, got {tuple(scale.shape)} of "
+                             f"{scale.dtype}")
+        self.codes, self.scale = codes, scale
+
+
+def quantise_rows(x, stream=None) -> QuantisedRows:
+    """x (rows, width) as 8-bit floats under a power of two for each row
+    (hstu_attn_quantise_rows); a weight of ``linear`` once, before it is used."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return quantise_rows(x)
+    r = load_extension().quantise_rows(x)
+    if type(r) is int:
+        _check(r, "hstu_attn_quantise_rows")
+    return QuantisedRows(*r)
+
+
+def rms_norm(x, weight, residual=None, gate=None, eps: float = 1e-6, quantise: bool = False, want_rstd: bool = True,
+             outs=None, stream=None):
+    """(y, h, rstd): h = x + residual (None without one), rstd = 1 / rms(h) and
+    y = h * rstd * weight * gate (hstu_attn_rms_norm). y is QuantisedRows with
+    ``quantise``. ``outs`` may be (y, h), either None; h may be the residual
+    itself, which is then updated in place."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return rms_norm(x, weight, residual, gate, eps, quantise, want_rstd, outs)
+    y, h = (None, None) if outs is None else outs
+    if type(y) is QuantisedRows:
+        y, s = y.codes, y.scale
+    else:
+        s = None
+    r = load_extension().rms_norm(x, weight, residual, gate, eps, bool(quantise), bool(want_rstd), y, s, h)
+    if type(r) is int:
+        _check(r, "hstu_attn_rms_norm")
+    y, s, h, rstd = r
+    return (y if s is None else QuantisedRows(y, s)), h, rstd
+
+
+def rms_norm_workspace(rows: int, width: int, device="cuda") -> torch.Tensor:
+    """Workspace of ``rms_norm_bwd``."""
+    n = int(load().hstu_attn_rms_norm_workspace_size(rows, width))
+    if n == 0:
+        raise HstuError(2, "hstu_attn_rms_norm_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def rms_norm_bwd(dy, h, rstd, weight, gate=None, dh=None, ws: Optional[torch.Tensor] = None, stream=None):
+    """(dx, dweight, dgate) of sum(y * dy) for rms_norm, h and rstd those of the
+    forward (h is x where there was no residual; dx is the residual's gradient
+    too). ``dh``, the gradient of h's other uses, is added to dx; dgate is None
+    without a gate (hstu_attn_rms_norm_bwd)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return rms_norm_bwd(dy, h, rstd, weight, gate, dh, ws)
+    r = load_extension().rms_norm_bwd(dy, h, rstd, weight, gate, dh, ws)
+    if type(r) is int:
+        _check(r, "hstu_attn_rms_norm_bwd")
+    return r
+
+
+def linear(x, w, bias=None, act: str = "none", residual=None, want_z: bool = False, dtype=None, out=None,
+           ws: Optional[torch.Tensor] = None, stream=None):
+    """(y, z): z = x w^T + bias, y = act(z) + residual (hstu_attn_linear). x (T,
+    d_in) and w (d_out, d_in) are both bf16, both fp16, or both QuantisedRows (y
+    is then of ``dtype``, bf16 if it is not given). ``act`` is "none", "silu",
+    "gelu" (the tanh form) or "relu". z is None without ``want_z``; ``linear_bwd``
+    needs it where there is an activation. With a ``ws`` (256 bytes) a wait that
+    gave up is reported by ``device_status``."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return linear(x, w, bias, act, residual, want_z, dtype, out, ws)
+    xs = ws_ = None
+    if type(x) is QuantisedRows:
+        x, xs = x.codes, x.scale
+    if type(w) is QuantisedRows:
+        w, ws_ = w.codes, w.scale
+    if dtype is None:
+        dtype = x.dtype if xs is None else torch.bfloat16
+    r = load_extension().linear(x, xs, w, ws_, bias, _act_code(act), residual, _dtype_code(dtype, DTYPES, "dtype"),
+                                bool(want_z), out, ws)
+    if type(r) is int:
+        _check(r, "hstu_attn_linear")
+    return r
+
+
+def linear_workspace(rows: int, d_in: int, d_out: int, act: str = "none", device="cuda") -> torch.Tensor:
+    """Workspace of ``linear_bwd``."""
+    n = int(load().hstu_attn_linear_workspace_size(rows, d_in, d_out, _act_code(act)))
+    if n == 0:
+        raise HstuError(2, "hstu_attn_linear_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def linear_bwd(dy, z, x, w, act: str = "none", want_dbias: bool = True, ws: Optional[torch.Tensor] = None,
+               stream=None):
+    """(dx, dw, dbias) of sum(y * dy) for linear with 16-bit operands
+    (hstu_attn_linear_bwd); z is not read with act "none", and the residual's
+    gradient is dy."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return linear_bwd(dy, z, x, w, act, want_dbias, ws)
+    r = load_extension().linear_bwd(dy, z, x, w, _act_code(act), bool(want_dbias), ws)
+    if type(r) is int:
+        _check(r, "hstu_attn_linear_bwd")
     return r

@@ -6,7 +6,7 @@ work-list entry before using it (a debugging aid, results bit-identical).
 Every translation unit of both is compiled by nvcc in one parallel pool, then
 each set is linked into one shared library next to this file (the CUDA
 runtime is linked statically). ``_serving.so`` is the CPython extension of the
-serving calls, compiled beside them against the installed torch; the libraries
+serving and layer calls, compiled beside them against the installed torch; the libraries
 need neither torch nor Python's headers, and are built where it cannot be. A
 library newer than every source is not rebuilt, the extension only while torch
 and Python are those it was compiled against.
@@ -39,11 +39,11 @@ VARIANTS = {
 }
 SOURCES = ["plan.cu", "attn_fwd_bf16.cu", "attn_fwd_f16.cu", "attn_bwd_bf16.cu", "attn_bwd_f16.cu", "targets_only.cu", "api.cu", "noalloc.cu", "selftest.cu", "func_build.cu", "project.cu",
            "rope.cu", "cache.cu", "paged.cu", "paged_bf16.cu", "paged_f16.cu", "paged_bf16_e4m3.cu",
-           "paged_f16_e4m3.cu", "shard.cpp"]
+           "paged_f16_e4m3.cu", "embed.cu", "norm.cu", "linear.cu", "linear_bf16.cu", "linear_f16.cu", "shard.cpp"]
 # Sources without HSTU_CHECKED code: the checked library links the release's
 # objects of them.
 SHARED = {"rope.cu", "cache.cu", "paged.cu", "paged_bf16.cu", "paged_f16.cu", "paged_bf16_e4m3.cu",
-          "paged_f16_e4m3.cu"}
+          "paged_f16_e4m3.cu", "embed.cu", "norm.cu", "linear.cu", "linear_bf16.cu", "linear_f16.cu"}
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

@@ -1,0 +1,595 @@
+// Rows of an embedding table by id, and the table's gradient.
+//
+//   forward   y[t] = scale * table[ids[t]], zeros for an id below 0 (padding);
+//   backward  dtable[v] = scale * the sum of dy[t] over the tokens with ids[t]
+//             = v, in the tokens' order, summed in 32 bits without atomics, so
+//             that two runs agree bit for bit.
+//
+// The backward sorts the tokens by id (stable, by digits of at most 9 bits from
+// the lowest up), which puts the rows of one id next to each other, and then
+// sums runs:
+//   - the sorted tokens are cut into chunks of 16 to 128; a group of dim / 8
+//     threads (8 columns a thread) walks a chunk's rows and writes a row of the
+//     table at each change of id;
+//   - a run that crosses into the next chunk belongs to the chunk it begins
+//     in, unless it fills a whole chunk: such long runs (a few ids are most of
+//     all tokens) leave a sum for each chunk in the workspace, and a join
+//     kernel adds those in order;
+//   - rows of the table that no token names are zeroed by further blocks of the
+//     summing kernel, which know them by a bit a row that the first pass set;
+//     every row of the table is so written once.
+#include "layer.cuh"
+
+namespace hstu {
+namespace {
+
+constexpr int kEmbedThreads = 256;
+constexpr int kSortWarps = 16, kSortThreads = 32 * kSortWarps;
+constexpr int kMaxDigitBits = 9, kMaxBins = 1 << kMaxDigitBits;
+constexpr int kSortTiles = 152;  // at most one tile an SM
+constexpr int kFillRows = 64;    // rows of the table a zeroing block looks after
+constexpr int kJoinChunks = 8;   // chunks a joining block looks after
+
+// ------------------------------------------------------------------ forward
+
+struct EmbedParams {
+  const void* table;
+  const void* ids;
+  void* out;
+  int32_t* header;  // null: bad ids are not reported
+  int64_t vocab, tokens;
+  int32_t chunks;  // 8-column chunks of a row
+  int32_t rows;    // rows of a block
+  float scale;
+};
+
+// A block takes `rows` tokens' rows, a chunk a thread, U chunks in flight.
+template <typename TT, typename T, typename ID, int U>
+__global__ void __launch_bounds__(kEmbedThreads) embed_kernel(const EmbedParams p) {
+  chain();
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.rows;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(p.rows), p.tokens - t0));
+  const uint32_t units = static_cast<uint32_t>(rows) * p.chunks;
+  const ID* ids = static_cast<const ID*>(p.ids) + t0;
+  const TT* table = static_cast<const TT*>(p.table);
+  T* out = static_cast<T*>(p.out) + t0 * p.chunks * 8;
+  for (uint32_t u0 = threadIdx.x; u0 < units; u0 += U * kEmbedThreads) {
+    int64_t id[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const uint32_t u = u0 + i * kEmbedThreads;
+      id[i] = u < units ? static_cast<int64_t>(ids[u / p.chunks]) : -1;
+    }
+    float f[U][8];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const uint32_t u = u0 + i * kEmbedThreads;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[i][e] = 0.0f;
+      if (id[i] >= 0 && id[i] < p.vocab) load8(table + (id[i] * p.chunks + u % p.chunks) * 8, f[i]);
+      else if (id[i] >= p.vocab && p.header) atomicOr(p.header + kHdrErr, kErrInput);
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const uint32_t u = u0 + i * kEmbedThreads;
+      if (u >= units) break;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[i][e] *= p.scale;
+      store8(out + static_cast<int64_t>(u) * 8, f[i]);
+    }
+  }
+}
+
+template <typename TT, typename T, typename ID>
+cudaError_t launch_embed(EmbedParams p, cudaStream_t stream) {
+  // Four chunks a thread where that leaves eight blocks an SM, else one: a
+  // step's few rows are spread over as many SMs as they have chunks for.
+  const int64_t units = p.tokens * p.chunks;
+  const bool many = units >= int64_t{152} * 8 * kEmbedThreads * 4;
+  const int64_t per_block = kEmbedThreads * (many ? 4 : 1);
+  const int64_t rows = per_block / p.chunks;
+  p.rows = static_cast<int32_t>(rows < 1 ? 1 : rows);
+  const dim3 grid(static_cast<unsigned>((p.tokens + p.rows - 1) / p.rows));
+  return launch_chained(many ? embed_kernel<TT, T, ID, 4> : embed_kernel<TT, T, ID, 1>, grid, kEmbedThreads, 0, stream, p);
+}
+template <typename ID>
+cudaError_t launch_embed_typed(const EmbedParams& p, int table_dtype, int dtype, cudaStream_t stream) {
+  using B = __nv_bfloat16;
+  using H = __half;
+  if (table_dtype == HSTU_DTYPE_F32)
+    return dtype == HSTU_DTYPE_F16 ? launch_embed<float, H, ID>(p, stream) : launch_embed<float, B, ID>(p, stream);
+  return dtype == HSTU_DTYPE_F16 ? launch_embed<H, H, ID>(p, stream) : launch_embed<B, B, ID>(p, stream);
+}
+
+// --------------------------------------------------------------------- sort
+
+// One digit's pass over (id, token) pairs, from `ids` itself in the first.
+struct SortParams {
+  const void* ids;
+  const uint32_t* key_in;
+  const int32_t* val_in;
+  uint32_t* key_out;
+  int32_t* val_out;
+  uint32_t* counts;  // (tiles, bins)
+  uint32_t* named;   // first pass: a bit for each row of the table that a token names
+  int32_t* header;   // null: bad ids are not reported
+  int64_t vocab, n;
+  int32_t tile;  // pairs of a tile, a multiple of kSortThreads
+  int32_t tiles, shift, bits;
+};
+
+// Padding and ids past the table sort behind it, as `vocab`.
+template <typename ID, bool FIRST>
+__device__ __forceinline__ uint32_t sort_key(const SortParams& p, int64_t i) {
+  if (!FIRST) return p.key_in[i];
+  const int64_t id = static_cast<int64_t>(static_cast<const ID*>(p.ids)[i]);
+  return id >= 0 && id < p.vocab ? static_cast<uint32_t>(id) : static_cast<uint32_t>(p.vocab);
+}
+
+// How often each digit occurs in each tile.
+template <typename ID, bool FIRST>
+__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortParams p) {
+  chain();
+  __shared__ uint32_t count[kMaxBins];
+  const int bins = 1 << p.bits;
+  for (int b = threadIdx.x; b < bins; b += kSortThreads) count[b] = 0;
+  __syncthreads();
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * p.tile, i1 = min(i0 + p.tile, p.n);
+  for (int64_t i = i0 + threadIdx.x; i < i1; i += kSortThreads) {
+    const uint32_t key = sort_key<ID, FIRST>(p, i);
+    atomicAdd(&count[(key >> p.shift) & (bins - 1)], 1u);
+    if (FIRST) {
+      if (key < p.vocab) atomicOr(p.named + (key >> 5), 1u << (key & 31));
+      else if (p.header && static_cast<int64_t>(static_cast<const ID*>(p.ids)[i]) >= 0)
+        atomicOr(p.header + kHdrErr, kErrInput);
+    }
+  }
+  __syncthreads();
+  for (int b = threadIdx.x; b < bins; b += kSortThreads) p.counts[static_cast<int64_t>(blockIdx.x) * bins + b] = count[b];
+}
+
+// Moves each pair to its place: behind all pairs of a lower digit, those of its
+// digit in earlier tiles, and those of its digit before it in the tile. A tile's
+// warps own consecutive parts of it, so the order within a digit is kept.
+template <typename ID, bool FIRST>
+__global__ void __launch_bounds__(kSortThreads) sort_move_kernel(const SortParams p) {
+  chain();
+  __shared__ uint32_t place[kSortWarps][kMaxBins];
+  __shared__ uint32_t warp_sum[kSortWarps];
+  const int bins = 1 << p.bits, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < kSortWarps * kMaxBins; i += kSortThreads) (&place[0][0])[i] = 0;
+  __syncthreads();
+  const int part = p.tile / kSortWarps;
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * p.tile + static_cast<int64_t>(warp) * part;
+  for (int r = 0; r < part; r += 32) {
+    const int64_t i = i0 + r + lane;
+    if (i < p.n) atomicAdd(&place[warp][(sort_key<ID, FIRST>(p, i) >> p.shift) & (bins - 1)], 1u);
+  }
+  // Thread b (bins <= threads): digit b's pairs in all tiles and in those before this one.
+  uint32_t total = 0, before = 0;
+  if (threadIdx.x < bins)
+#pragma unroll 16
+    for (int t = 0; t < p.tiles; ++t) {
+      const uint32_t c = p.counts[static_cast<int64_t>(t) * bins + threadIdx.x];
+      total += c;
+      if (t < static_cast<int>(blockIdx.x)) before += c;
+    }
+  uint32_t sum = total;  // of digits up to this one
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const uint32_t o = __shfl_up_sync(0xffffffffu, sum, off);
+    if (lane >= off) sum += o;
+  }
+  if (lane == 31) warp_sum[warp] = sum;
+  __syncthreads();
+  uint32_t at = sum - total + before;
+  for (int w = 0; w < warp; ++w) at += warp_sum[w];
+  if (threadIdx.x < bins)
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) {
+      const uint32_t c = place[w][threadIdx.x];
+      place[w][threadIdx.x] = at;
+      at += c;
+    }
+  __syncthreads();
+  for (int r = 0; r < part; r += 32) {
+    const int64_t i = i0 + r + lane;
+    const uint32_t live = __ballot_sync(0xffffffffu, i < p.n);
+    if (i < p.n) {
+      const uint32_t key = sort_key<ID, FIRST>(p, i), digit = (key >> p.shift) & (bins - 1);
+      const uint32_t same = __match_any_sync(live, digit);
+      const uint32_t to = place[warp][digit] + __popc(same & ((1u << lane) - 1u));
+      __syncwarp(live);
+      if (lane == 31 - __clz(same)) place[warp][digit] = to + 1;
+      p.key_out[to] = key;
+      p.val_out[to] = FIRST ? static_cast<int32_t>(i) : p.val_in[i];
+    }
+    __syncwarp();
+  }
+}
+
+// ----------------------------------------------------------------- backward
+
+struct SumParams {
+  const void* dy;
+  int64_t dy_stride;
+  const uint32_t* key;  // sorted ids
+  const int32_t* val;   // their tokens
+  const uint32_t* named;
+  void* dtable;
+  float* part;  // (chunks, 2, dim): sums of long runs' chunks; [0] of a run from an earlier chunk, [1] of one that begins
+  int64_t n, vocab;
+  int32_t chunk, chunks, dim, accumulate;
+  int32_t sum_blocks;  // blocks that sum; the others zero
+  float scale;
+};
+
+// Whether chunk c holds one id alone.
+__device__ __forceinline__ bool one_id(const SumParams& p, int64_t c, uint32_t key) {
+  const int64_t i0 = c * p.chunk, i1 = min(i0 + p.chunk, p.n);
+  return i0 < i1 && p.key[i0] == key && p.key[i1 - 1] == key;
+}
+
+template <typename G>
+__device__ __forceinline__ void put_row(const SumParams& p, int64_t row, int col, float (&acc)[8]) {
+  G* dst = static_cast<G*>(p.dtable) + row * p.dim + col;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) acc[e] *= p.scale;
+  if (p.accumulate) {
+    float old[8];
+    load8(dst, old);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] += old[e];
+  }
+  store8(dst, acc);
+}
+
+template <typename T, typename G>
+__global__ void __launch_bounds__(kEmbedThreads) embed_sum_kernel(const SumParams p) {
+  chain();
+  const int col0 = blockIdx.y * kEmbedThreads * 8;
+  const int group = min(kEmbedThreads, (p.dim - col0) / 8);  // threads of a row
+  const int groups = kEmbedThreads / group, g = threadIdx.x / group;
+  const int col = col0 + (threadIdx.x % group) * 8;
+  if (g >= groups) return;
+  if (static_cast<int>(blockIdx.x) >= p.sum_blocks) {  // rows that no token names
+    const int64_t v0 = static_cast<int64_t>(blockIdx.x - p.sum_blocks) * kFillRows, v1 = min(v0 + kFillRows, p.vocab);
+    float zero[8] = {};
+    for (int64_t v = v0 + g; v < v1; v += groups)
+      if (((p.named[v >> 5] >> (v & 31)) & 1u) == 0) store8(static_cast<G*>(p.dtable) + v * p.dim + col, zero);
+    return;
+  }
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * groups + g;
+  if (c >= p.chunks) return;
+  const int64_t i0 = c * p.chunk, end = min(i0 + p.chunk, p.n);
+  const uint32_t first = p.key[i0], last = p.key[end - 1];
+  const bool from_before = i0 > 0 && p.key[i0 - 1] == first;
+  const bool whole = first == last;
+  if (first >= p.vocab) return;
+  int64_t i = i0, i1 = end;
+  // The run that comes from the chunk before: the whole of a chunk, or the end
+  // of a long run (one that fills the chunk before), is a partial sum;
+  // otherwise that chunk sums it.
+  const bool head_part = whole || (from_before && one_id(p, c - 1, first));
+  if (from_before && !head_part)
+    while (i < end && p.key[i] == first) ++i;
+  // The run that goes on into the next chunk: long if that chunk is full of it, else it is
+  // summed here to its end.
+  bool tail_part = false;
+  if (!whole && end < p.n && p.key[end] == last && last < p.vocab) {
+    tail_part = one_id(p, c + 1, last);
+    if (!tail_part)
+      while (i1 < p.n && p.key[i1] == last) ++i1;
+  }
+  // A whole chunk whose run is no longer than it: an ordinary row.
+  const bool alone = whole && !from_before && (end == p.n || p.key[end] != first);
+  const T* dy = static_cast<const T*>(p.dy) + col;
+  float acc[8] = {};
+  uint32_t cur = i < i1 ? p.key[i] : 0xffffffffu;
+  auto flush = [&](uint32_t row) {
+    if (row >= p.vocab) return;
+    if (!alone && head_part && row == first) {
+      store8(p.part + (c * 2) * p.dim + col, acc);
+    } else if (tail_part && row == last) {
+      store8(p.part + (c * 2 + 1) * p.dim + col, acc);
+    } else {
+      put_row<G>(p, row, col, acc);
+    }
+  };
+  constexpr int kAhead = 4;
+  while (i < i1) {
+    uint32_t key[kAhead];
+    uint4 v[kAhead];
+    const int m = static_cast<int>(min(static_cast<int64_t>(kAhead), i1 - i));
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      key[a] = a < m ? p.key[i + a] : 0xffffffffu;
+      if (a < m && key[a] < p.vocab)
+        v[a] = *reinterpret_cast<const uint4*>(dy + static_cast<int64_t>(p.val[i + a]) * p.dy_stride);
+    }
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      if (a >= m) break;
+      if (key[a] != cur) {
+        flush(cur);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
+        cur = key[a];
+      }
+      if (key[a] >= p.vocab) break;
+      float f[8];
+      unpack8<T>(v[a], f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] += f[e];
+    }
+    i += m;
+    if (cur >= p.vocab) return;  // padding sorts last
+  }
+  if (i0 < i1) flush(cur);
+}
+
+// Adds up the chunks of each long run: the end of the chunk before its first
+// whole one, the whole ones, and the beginning of the chunk behind. The groups
+// of a block take consecutive slices of the run, which are added in order.
+template <typename G>
+__global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(const SumParams p) {
+  chain();
+  __shared__ float slice[kEmbedThreads][8];
+  __shared__ int found[kJoinChunks];
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kJoinChunks;
+  if (threadIdx.x < kJoinChunks) {
+    const int64_t c = c0 + threadIdx.x;
+    int is = 0;
+    if (c < p.chunks) {
+      const int64_t i0 = c * p.chunk, end = min(i0 + p.chunk, p.n);
+      const uint32_t key = p.key[i0];
+      const bool before = i0 > 0 && p.key[i0 - 1] == key, after = end < p.n && p.key[end] == key;
+      is = key < p.vocab && p.key[end - 1] == key && (before || after) && !(c > 0 && one_id(p, c - 1, key));
+    }
+    found[threadIdx.x] = is;
+  }
+  __syncthreads();
+  const int col0 = blockIdx.y * kEmbedThreads * 8;
+  const int group = min(kEmbedThreads, (p.dim - col0) / 8);
+  const int groups = kEmbedThreads / group, g = threadIdx.x / group;
+  const int col = col0 + (threadIdx.x % group) * 8;
+  for (int k = 0; k < kJoinChunks; ++k) {
+    if (!found[k]) continue;
+    const int64_t c = c0 + k;
+    const uint32_t key = p.key[c * p.chunk];
+    const bool before = c > 0 && p.key[c * p.chunk - 1] == key;
+    // The last chunk that begins with the id.
+    int64_t lo = c, hi = p.chunks;
+    while (hi - lo > 1) {
+      const int64_t mid = lo + (hi - lo) / 2;
+      if (p.key[mid * p.chunk] == key) lo = mid;
+      else hi = mid;
+    }
+    const int64_t parts = lo - c + 1, per = (parts + groups - 1) / groups;
+    float acc[8] = {};
+    if (g < groups) {
+      const int64_t a = c + g * per, b = min(a + per, c + parts);
+      if (g == 0 && before) load8(p.part + ((c - 1) * 2 + 1) * p.dim + col, acc);
+#pragma unroll 4
+      for (int64_t x = a; x < b; ++x) {
+        float f[8];
+        load8(p.part + x * 2 * p.dim + col, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] += f[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) slice[threadIdx.x][e] = acc[e];
+    }
+    __syncthreads();
+    if (g == 0) {
+      for (int x = 1; x < groups; ++x)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] += slice[x * group + threadIdx.x][e];
+      put_row<G>(p, key, col, acc);
+    }
+    __syncthreads();
+  }
+}
+
+// No tokens: every row is zero.
+template <typename G>
+__global__ void __launch_bounds__(kEmbedThreads) embed_zero_kernel(G* out, int64_t units) {
+  chain();
+  const int64_t u = static_cast<int64_t>(blockIdx.x) * kEmbedThreads + threadIdx.x;
+  float zero[8] = {};
+  if (u < units) store8(out + u * 8, zero);
+}
+
+// A chunk's tokens: enough chunks to fill the GPU (2048 threads on each of 152 SMs), 16
+// to 128.
+int sum_chunk(int64_t n, int dim) {
+  const int64_t want = n * (dim / 8) / (152 * 2048);
+  int c = 16;
+  while (c < 128 && 2 * c <= want) c *= 2;
+  return c;
+}
+
+// Workspace: a 256-byte header (error word), a bit a row of the table, the two
+// buffers of (id, token), the digits' counts, and the long runs' sums.
+struct EmbedLayout {
+  size_t named = 0, key[2] = {}, val[2] = {}, counts = 0, part = 0, total = 0;
+};
+EmbedLayout embed_layout(int64_t n, int64_t vocab, int dim) {
+  EmbedLayout l;
+  l.named = kHdrWords * 4;
+  size_t at = l.named + align_up(static_cast<size_t>((vocab + 31) / 32) * 4, 256);
+  for (int i = 0; i < 2; ++i) {
+    l.key[i] = at;
+    at += align_up(static_cast<size_t>(n) * 4, 256);
+    l.val[i] = at;
+    at += align_up(static_cast<size_t>(n) * 4, 256);
+  }
+  l.counts = at;
+  at += static_cast<size_t>(kSortTiles) * kMaxBins * 4;
+  l.part = at;
+  const int c = sum_chunk(n, dim);
+  at += align_up(static_cast<size_t>((n + c - 1) / c) * 2 * dim * 4, 256);
+  l.total = at;
+  return l;
+}
+
+template <typename ID>
+cudaError_t launch_sort(SortParams p, uint8_t* base, const EmbedLayout& l, int& last, cudaStream_t stream) {
+  int bits = 1;
+  while ((p.vocab >> bits) != 0) ++bits;  // of the largest key, vocab
+  const int passes = (bits + kMaxDigitBits - 1) / kMaxDigitBits;
+  p.bits = (bits + passes - 1) / passes;
+  const int64_t rounds = (p.n + int64_t{kSortTiles} * kSortThreads - 1) / (int64_t{kSortTiles} * kSortThreads);
+  p.tile = static_cast<int32_t>(rounds * kSortThreads);
+  p.tiles = static_cast<int32_t>((p.n + p.tile - 1) / p.tile);
+  for (int s = 0; s < passes; ++s) {
+    p.shift = s * p.bits;
+    p.key_in = reinterpret_cast<const uint32_t*>(base + l.key[s & 1]);
+    p.val_in = reinterpret_cast<const int32_t*>(base + l.val[s & 1]);
+    p.key_out = reinterpret_cast<uint32_t*>(base + l.key[(s + 1) & 1]);
+    p.val_out = reinterpret_cast<int32_t*>(base + l.val[(s + 1) & 1]);
+    cudaError_t e = launch_chained(s == 0 ? sort_count_kernel<ID, true> : sort_count_kernel<ID, false>, dim3(p.tiles),
+                                   kSortThreads, 0, stream, p);
+    if (e != cudaSuccess) return e;
+    e = launch_chained(s == 0 ? sort_move_kernel<ID, true> : sort_move_kernel<ID, false>, dim3(p.tiles), kSortThreads, 0,
+                       stream, p);
+    if (e != cudaSuccess) return e;
+  }
+  last = passes & 1;
+  return cudaSuccess;
+}
+
+template <typename T, typename G>
+cudaError_t launch_sum(SumParams p, cudaStream_t stream) {
+  const int widest = p.dim < kEmbedThreads * 8 ? p.dim : kEmbedThreads * 8;
+  const int groups = kEmbedThreads / (widest / 8);
+  const unsigned ny = (p.dim + kEmbedThreads * 8 - 1) / (kEmbedThreads * 8);
+  p.sum_blocks = (p.chunks + groups - 1) / groups;
+  const int64_t fill = p.accumulate ? 0 : (p.vocab + kFillRows - 1) / kFillRows;
+  cudaError_t e = launch_chained(embed_sum_kernel<T, G>, dim3(static_cast<unsigned>(p.sum_blocks + fill), ny),
+                                 kEmbedThreads, 0, stream, p);
+  if (e != cudaSuccess) return e;
+  return launch_chained(embed_join_kernel<G>, dim3((p.chunks + kJoinChunks - 1) / kJoinChunks, ny), kEmbedThreads, 0,
+                        stream, p);
+}
+template <typename T>
+cudaError_t launch_sum_typed(const SumParams& p, int grad_dtype, cudaStream_t stream) {
+  return grad_dtype == HSTU_DTYPE_F32 ? launch_sum<T, float>(p, stream) : launch_sum<T, T>(p, stream);
+}
+
+hstu_status_t embed_checks(int64_t tokens, int64_t vocab, int dim) {
+  if (tokens < 0 || tokens > INT32_MAX || vocab < 1 || vocab >= INT32_MAX || dim < 1) return HSTU_ERR_INVALID_ARG;
+  if (dim % 8 != 0 || dim > 65536) return HSTU_ERR_UNSUPPORTED;
+  return HSTU_OK;
+}
+bool embed_types_ok(int dtype, int wide, int id_bytes) {
+  return row_dtype_ok(dtype) && (wide == dtype || wide == HSTU_DTYPE_F32) && (id_bytes == 4 || id_bytes == 8);
+}
+
+}  // namespace
+}  // namespace hstu
+
+extern "C" {
+
+HSTU_API hstu_status_t hstu_attn_embed(const void* table, int32_t table_dtype, int64_t vocab, int32_t dim,
+                                       const void* ids, int32_t id_bytes, int64_t tokens, float scale, void* out,
+                                       int32_t dtype, void* ws, size_t ws_bytes, void* stream) {
+  using namespace hstu;
+  const hstu_status_t st = embed_checks(tokens, vocab, dim);
+  if (st != HSTU_OK) return st;
+  if (!embed_types_ok(dtype, table_dtype, id_bytes)) return HSTU_ERR_UNSUPPORTED;
+  if (ws && (!aligned_to(ws, 256) || ws_bytes < kHdrWords * 4)) return HSTU_ERR_WORKSPACE;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (tokens > 0) {
+    if (!aligned_to(table, 16) || !aligned_to(out, 16) || !aligned_to(ids, id_bytes)) return HSTU_ERR_INVALID_ARG;
+    const int64_t written = tokens * dim * 2;
+    if (ranges_meet(out, written, table, vocab * dim * (table_dtype == HSTU_DTYPE_F32 ? 4 : 2)) ||
+        ranges_meet(out, written, ids, tokens * id_bytes))
+      return HSTU_ERR_INVALID_ARG;
+  }
+  if (ws && cudaMemsetAsync(ws, 0, kHdrWords * 4, cs) != cudaSuccess) return HSTU_ERR_CUDA;
+  if (tokens == 0) return HSTU_OK;
+  EmbedParams p{};
+  p.table = table;
+  p.ids = ids;
+  p.out = out;
+  p.header = static_cast<int32_t*>(ws);
+  p.vocab = vocab;
+  p.tokens = tokens;
+  p.chunks = dim / 8;
+  p.scale = scale;
+  const cudaError_t e = id_bytes == 8 ? launch_embed_typed<int64_t>(p, table_dtype, dtype, cs)
+                                      : launch_embed_typed<int32_t>(p, table_dtype, dtype, cs);
+  return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+}
+
+HSTU_API size_t hstu_attn_embed_workspace_size(int64_t tokens, int64_t vocab, int32_t dim) {
+  return hstu::embed_checks(tokens, vocab, dim) == HSTU_OK ? hstu::embed_layout(tokens, vocab, dim).total : 0;
+}
+
+HSTU_API hstu_status_t hstu_attn_embed_bwd(const void* dy, int64_t dy_stride, int32_t dtype, const void* ids,
+                                           int32_t id_bytes, int64_t tokens, float scale, void* dtable,
+                                           int32_t grad_dtype, int64_t vocab, int32_t dim, int32_t accumulate, void* ws,
+                                           size_t ws_bytes, void* stream) {
+  using namespace hstu;
+  const hstu_status_t st = embed_checks(tokens, vocab, dim);
+  if (st != HSTU_OK) return st;
+  if (!embed_types_ok(dtype, grad_dtype, id_bytes)) return HSTU_ERR_UNSUPPORTED;
+  if (accumulate != 0 && accumulate != 1) return HSTU_ERR_INVALID_ARG;
+  if (accumulate && grad_dtype != HSTU_DTYPE_F32) return HSTU_ERR_UNSUPPORTED;
+  if (!aligned_to(dtable, 16)) return HSTU_ERR_INVALID_ARG;
+  if (tokens > 0) {
+    if (!rows_ok(dy, dy_stride, 1, dim) || !aligned_to(ids, id_bytes)) return HSTU_ERR_INVALID_ARG;
+    const int64_t bytes = vocab * dim * (grad_dtype == HSTU_DTYPE_F32 ? 4 : 2);
+    if (ranges_meet(dtable, bytes, dy, ((tokens - 1) * dy_stride + dim) * 2) ||
+        ranges_meet(dtable, bytes, ids, tokens * id_bytes))
+      return HSTU_ERR_INVALID_ARG;
+  }
+  const EmbedLayout l = embed_layout(tokens, vocab, dim);
+  if (!aligned_to(ws, 256) || ws_bytes < l.total) return HSTU_ERR_WORKSPACE;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  // the error word and the bits of the rows
+  if (cudaMemsetAsync(base, 0, l.key[0], cs) != cudaSuccess) return HSTU_ERR_CUDA;
+  cudaError_t e = cudaSuccess;
+  if (tokens == 0) {
+    if (accumulate) return HSTU_OK;
+    const int64_t units = vocab * (dim / 8);
+    const dim3 grid(static_cast<unsigned>((units + kEmbedThreads - 1) / kEmbedThreads));
+    if (grad_dtype == HSTU_DTYPE_F32)
+      e = launch_chained(embed_zero_kernel<float>, grid, kEmbedThreads, 0, cs, static_cast<float*>(dtable), units);
+    else
+      e = launch_chained(embed_zero_kernel<__half>, grid, kEmbedThreads, 0, cs, static_cast<__half*>(dtable), units);
+    return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+  }
+  SortParams sp{};
+  sp.ids = ids;
+  sp.counts = reinterpret_cast<uint32_t*>(base + l.counts);
+  sp.named = reinterpret_cast<uint32_t*>(base + l.named);
+  sp.header = reinterpret_cast<int32_t*>(base);
+  sp.vocab = vocab;
+  sp.n = tokens;
+  int last = 0;
+  e = id_bytes == 8 ? launch_sort<int64_t>(sp, base, l, last, cs) : launch_sort<int32_t>(sp, base, l, last, cs);
+  if (e != cudaSuccess) return HSTU_ERR_CUDA;
+  SumParams p{};
+  p.dy = dy;
+  p.dy_stride = dy_stride;
+  p.key = reinterpret_cast<const uint32_t*>(base + l.key[last]);
+  p.val = reinterpret_cast<const int32_t*>(base + l.val[last]);
+  p.named = sp.named;
+  p.dtable = dtable;
+  p.part = reinterpret_cast<float*>(base + l.part);
+  p.n = tokens;
+  p.vocab = vocab;
+  p.dim = dim;
+  p.chunk = sum_chunk(tokens, dim);
+  p.chunks = static_cast<int32_t>((tokens + p.chunk - 1) / p.chunk);
+  p.accumulate = accumulate;
+  p.scale = scale;
+  e = dtype == HSTU_DTYPE_F16 ? launch_sum_typed<__half>(p, grad_dtype, cs)
+                              : launch_sum_typed<__nv_bfloat16>(p, grad_dtype, cs);
+  return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+}
+
+}  // extern "C"

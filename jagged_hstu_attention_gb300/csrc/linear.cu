@@ -1,0 +1,375 @@
+// Linear maps of rows with a fused epilogue, and their gradients.
+//
+//   forward   z = x w^T + bias, y = act(z) + residual: one tcgen05 product
+//             whose epilogue holds everything else, 16-bit or 8-bit operands;
+//   backward  g = dy act'(z) and the column sums of g (one elementwise kernel, parts
+//             of row chunks added in order), then dx = g w and dw = g^T x on
+//             tcgen05. Without an activation g is dy itself, read in place. dw,
+//             whose K is the number of rows, splits K over the SMs; its fp32
+//             parts are added in order.
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "layer.cuh"
+#include "linear.cuh"
+
+namespace hstu {
+namespace {
+
+constexpr int kGradThreads = 256;
+// Rows are split into at most kGradChunks chunks of at least kGradMinRows (one block
+// each); a chunk's column sums are the bias gradient's parts.
+constexpr int kGradChunks = 1216, kGradMinRows = 32;
+constexpr int kMaxKSplits = 16;
+constexpr int kPairs = 76;
+
+inline int grad_chunks(int64_t rows) {
+  const int64_t c = (rows + kGradMinRows - 1) / kGradMinRows;
+  return static_cast<int>(c < kGradChunks ? c : kGradChunks);
+}
+
+// act'(z)
+__device__ __forceinline__ float act_grad(float z, int act) {
+  if (act == HSTU_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
+  const bool gelu = act == HSTU_ACT_GELU;
+  const float u = gelu ? kGeluA * z * fmaf(kGeluB * z, z, 1.0f) : z;
+  const float du = gelu ? kGeluA * fmaf(3.0f * kGeluB * z, z, 1.0f) : 1.0f;
+  const float s = __fdividef(1.0f, 1.0f + __expf(-u));
+  return s * fmaf(z * (1.0f - s), du, 1.0f);
+}
+
+struct GradParams {
+  const void* dy;
+  const void* z;  // null: g = dy, nothing is written but the sums
+  void* g;
+  float* part;  // (chunks, cols)
+  int64_t dy_stride, rows;
+  int32_t cols, act;
+};
+
+// A block takes a chunk of rows; its threads cover as many rows of all columns at
+// a time as there are, 8 columns a thread (256 groups of columns a block where
+// there are more), two rows in flight.
+template <typename T>
+__global__ void __launch_bounds__(kGradThreads) linear_grad_kernel(const GradParams p) {
+  chain();
+  __shared__ float red[kGradThreads][8];
+  const int groups = p.cols / 8;
+  const int gy = groups >= kGradThreads ? kGradThreads : groups, rpi = kGradThreads / gy;
+  const int lane_row = threadIdx.x / gy, cg = blockIdx.y * gy + threadIdx.x % gy;
+  const bool active = lane_row < rpi && cg < groups;
+  const int col = cg * 8;
+  const int64_t per = (p.rows + gridDim.x - 1) / gridDim.x;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * per, r1 = min(r0 + per, p.rows);
+  float sum[8] = {};
+  auto one = [&](uint4 zv, uint4 dv, int64_t r) {
+    if (p.z) {
+      float z[8], d[8];
+      unpack8<T>(zv, z);
+      unpack8<T>(dv, d);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) d[e] *= act_grad(z[e], p.act);
+      dv = pack8<T>(d);
+      *reinterpret_cast<uint4*>(static_cast<T*>(p.g) + r * p.cols + col) = dv;
+    }
+    float d[8];
+    unpack8<T>(dv, d);  // the sums are those of the g that the products read
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] += d[e];
+  };
+  if (active) {
+    const T* dy = static_cast<const T*>(p.dy) + col;
+    const T* z = static_cast<const T*>(p.z) + (p.z ? col : 0);
+    auto load_z = [&](int64_t r) {
+      return p.z ? *reinterpret_cast<const uint4*>(z + r * p.cols) : make_uint4(0, 0, 0, 0);
+    };
+    int64_t r = r0 + lane_row;
+    for (; r + rpi < r1; r += 2 * rpi) {
+      const uint4 z0 = load_z(r), z1 = load_z(r + rpi);
+      const uint4 d0 = *reinterpret_cast<const uint4*>(dy + r * p.dy_stride);
+      const uint4 d1 = *reinterpret_cast<const uint4*>(dy + (r + rpi) * p.dy_stride);
+      one(z0, d0, r);
+      one(z1, d1, r + rpi);
+    }
+    if (r < r1) one(load_z(r), *reinterpret_cast<const uint4*>(dy + r * p.dy_stride), r);
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) red[threadIdx.x][e] = sum[e];
+  __syncthreads();
+  if (active && lane_row == 0) {
+    for (int l = 1; l < rpi; ++l)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] += red[l * gy + threadIdx.x][e];
+    store8(p.part + static_cast<int64_t>(blockIdx.x) * p.cols + col, sum);
+  }
+}
+
+// dbias[col]: the chunks' parts in order, 32 columns a block, a part in 32 a warp.
+template <typename T>
+__global__ void __launch_bounds__(1024) linear_bias_fold_kernel(const float* part, int chunks, int cols, void* dbias) {
+  chain();
+  __shared__ float red[32][33];
+  const int w = threadIdx.x >> 5, l = threadIdx.x & 31, col = blockIdx.x * 32 + l;
+  float s = 0.0f;
+  if (col < cols)
+#pragma unroll 8
+    for (int c = w; c < chunks; c += 32) s += part[static_cast<int64_t>(c) * cols + col];
+  red[w][l] = s;
+  __syncthreads();
+  if (w == 0 && col < cols) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int x = 0; x < 32; ++x) sum += red[x][l];
+    static_cast<uint16_t*>(dbias)[col] = static_cast<uint16_t>(Elem<T>::pack2(sum, 0.0f) & 0xffffu);
+  }
+}
+
+// dw: the fp32 parts of K's splits in order, 8 elements a thread.
+template <typename T>
+__global__ void __launch_bounds__(256) linear_split_fold_kernel(const float* part, int splits, int64_t elems, T* out) {
+  chain();
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
+  if (i >= elems) return;
+  float acc[8] = {};
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) {
+    float f[8];
+    load8(part + s * elems + i, f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] += f[e];
+  }
+  store8(out + i, acc);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
+// Boxes of 128 bytes x box_rows of a row-major (rows, cols) matrix; what lies outside it
+// reads as zeros and is not written.
+constexpr int kDtypeCodes = -1;  // 8-bit
+bool box_map(CUtensorMap* m, const void* ptr, int64_t rows, int64_t cols, int64_t stride, int dtype, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const bool codes = dtype == kDtypeCodes;
+  const CUtensorMapDataType type = codes                      ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : dtype == HSTU_DTYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                             : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * (codes ? 1 : 2)};
+  cuuint32_t box[2] = {codes ? 128u : 64u, static_cast<cuuint32_t>(box_rows)}, es[2] = {1, 1};
+  return fn(m, type, 2, const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+hstu_status_t linear_checks(int64_t rows, int d_in, int d_out, int act, bool codes) {
+  if (rows < 0 || rows > INT32_MAX - 1024 || d_in < 1 || d_out < 1) return HSTU_ERR_INVALID_ARG;
+  if (d_in % (codes ? 16 : 8) || d_out % 8 || d_in > 65536 || d_out > 65536) return HSTU_ERR_UNSUPPORTED;
+  if (act < HSTU_ACT_NONE || act > HSTU_ACT_RELU) return HSTU_ERR_UNSUPPORTED;
+  // tiles are numbered in 32 bits
+  const int64_t most = d_in > d_out ? d_in : d_out;
+  if ((rows / kTileM + 1) * (most / kTileN + 1) > INT32_MAX / 2) return HSTU_ERR_UNSUPPORTED;
+  return HSTU_OK;
+}
+
+// Splits of dw's K: those that leave the fewest tiles' time on the busiest pair, counting
+// each split's fp32 tile (written, read) as two of its 64-row blocks.
+int dw_splits(int64_t rows, int d_in, int d_out) {
+  const int64_t tiles = int64_t{(d_out + kTileM - 1) / kTileM} * ((d_in + kTileN - 1) / kTileN);
+  const int64_t nk = (rows + 63) / 64;
+  int best = 1;
+  int64_t least = INT64_MAX;
+  for (int s = 1; s <= kMaxKSplits && s <= nk; ++s) {
+    const int64_t per = (nk + s - 1) / s;
+    if ((s - 1) * per >= nk) continue;  // a split without rows
+    const int64_t cost = (tiles * s + kPairs - 1) / kPairs * (per + (s > 1 ? 4 : 0));
+    if (cost < least) least = cost, best = s;
+  }
+  return best;
+}
+
+// Workspace of the backward: a 256-byte header (error word), g, the bias gradient's
+// parts, dw's parts.
+struct LinearLayout {
+  size_t g = 0, part = 0, dw = 0, total = 0;
+};
+LinearLayout linear_layout(int64_t rows, int d_in, int d_out, int act) {
+  LinearLayout l;
+  l.g = kHdrWords * 4;
+  l.part = l.g + (act != HSTU_ACT_NONE ? align_up(static_cast<size_t>(rows) * d_out * 2, 256) : 0);
+  l.dw = l.part + align_up(static_cast<size_t>(grad_chunks(rows)) * d_out * 4, 256);
+  const int splits = dw_splits(rows, d_in, d_out);
+  l.total = l.dw + (splits > 1 ? align_up(static_cast<size_t>(splits) * d_out * d_in * 4, 256) : 0);
+  return l;
+}
+
+template <typename T>
+cudaError_t launch_grad(const GradParams& p, void* dbias, cudaStream_t stream) {
+  const int chunks = grad_chunks(p.rows);
+  const dim3 grid(chunks, (p.cols / 8 + kGradThreads - 1) / kGradThreads);
+  const cudaError_t e = launch_chained(linear_grad_kernel<T>, grid, kGradThreads, 0, stream, p);
+  if (e != cudaSuccess || !dbias) return e;
+  return launch_chained(linear_bias_fold_kernel<T>, dim3((p.cols + 31) / 32), 1024, 0, stream,
+                        static_cast<const float*>(p.part), chunks, p.cols, dbias);
+}
+
+}  // namespace
+}  // namespace hstu
+
+extern "C" {
+
+HSTU_API hstu_status_t hstu_attn_linear(const void* x, int64_t x_stride, const uint8_t* x_scale, const void* w,
+                                        const uint8_t* w_scale, const void* bias, const void* residual,
+                                        int64_t residual_stride, int64_t rows, int32_t d_in, int32_t d_out,
+                                        int32_t dtype, int32_t act, void* y, void* z, void* ws, size_t ws_bytes,
+                                        void* stream) {
+  using namespace hstu;
+  const bool codes = w_scale != nullptr;
+  const hstu_status_t st = linear_checks(rows, d_in, d_out, act, codes);
+  if (st != HSTU_OK) return st;
+  if (!row_dtype_ok(dtype)) return HSTU_ERR_UNSUPPORTED;
+  if (ws && (!aligned_to(ws, 256) || ws_bytes < kHdrWords * 4)) return HSTU_ERR_WORKSPACE;
+  const int xe = codes ? 1 : 2;
+  if (rows > 0) {
+    if (!aligned_to(x, 16) || x_stride < d_in || x_stride * xe % 16 != 0 || !aligned_to(w, 16) ||
+        (x_scale != nullptr) != codes || (bias && !aligned_to(bias, 16)) ||
+        (residual && !rows_ok(residual, residual_stride, 1, d_out)) || !aligned_to(y, 16) || (z && !aligned_to(z, 16)))
+      return HSTU_ERR_INVALID_ARG;
+    const int64_t yw = int64_t{d_out} * 2;
+    const RowSpan in[] = {{x, x_stride * xe, int64_t{d_in} * xe, rows},
+                          {w, int64_t{d_in} * xe * d_out, int64_t{d_in} * xe * d_out, 1},
+                          {x_scale, rows, rows, 1},
+                          {w_scale, d_out, d_out, 1},
+                          {bias, yw, yw, 1},
+                          {residual, 2 * residual_stride, yw, rows}},
+                  out[] = {{y, yw, yw, rows}, {z, yw, yw, rows}};
+    if (outputs_meet(in, out)) return HSTU_ERR_INVALID_ARG;
+  }
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (ws && cudaMemsetAsync(ws, 0, kHdrWords * 4, cs) != cudaSuccess) return HSTU_ERR_CUDA;
+  if (rows == 0) return HSTU_OK;
+  LinearParams p{};
+  const int type = codes ? kDtypeCodes : dtype;
+  if (!box_map(&p.tm_a, x, rows, d_in, x_stride, type, 128) || !box_map(&p.tm_b, w, d_out, d_in, d_in, type, 128) ||
+      !box_map(&p.tm_y, y, rows, d_out, d_out, dtype, 32) || (z && !box_map(&p.tm_z, z, rows, d_out, d_out, dtype, 32)) ||
+      (residual && !box_map(&p.tm_r, residual, rows, d_out, residual_stride, dtype, 32)))
+    return HSTU_ERR_CUDA;
+  p.bias = bias;
+  p.a_scale = x_scale;
+  p.b_scale = w_scale;
+  p.header = static_cast<int32_t*>(ws);
+  p.handoff_limit_ns = handoff_limit();
+  p.M = static_cast<int32_t>(rows);
+  p.N = d_out;
+  p.K = d_in;
+  p.k_splits = 1;
+  p.act = act;
+  p.has_z = z != nullptr;
+  p.has_r = residual != nullptr;
+  const cudaError_t e =
+      dtype == HSTU_DTYPE_F16 ? launch_linear_f16(p, codes, cs) : launch_linear_bf16(p, codes, cs);
+  return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+}
+
+HSTU_API size_t hstu_attn_linear_workspace_size(int64_t rows, int32_t d_in, int32_t d_out, int32_t act) {
+  if (hstu::linear_checks(rows, d_in, d_out, act, false) != HSTU_OK) return 0;
+  return hstu::linear_layout(rows, d_in, d_out, act).total;
+}
+
+HSTU_API hstu_status_t hstu_attn_linear_bwd(const void* dy, int64_t dy_stride, const void* z, const void* x,
+                                            int64_t x_stride, const void* w, int64_t rows, int32_t d_in, int32_t d_out,
+                                            int32_t dtype, int32_t act, void* dx, void* dw, void* dbias, void* ws,
+                                            size_t ws_bytes, void* stream) {
+  using namespace hstu;
+  const hstu_status_t st = linear_checks(rows, d_in, d_out, act, false);
+  if (st != HSTU_OK) return st;
+  if (!row_dtype_ok(dtype)) return HSTU_ERR_UNSUPPORTED;
+  const bool f16 = dtype == HSTU_DTYPE_F16;
+  if (!aligned_to(dw, 16) || (dbias && !aligned_to(dbias, 16))) return HSTU_ERR_INVALID_ARG;
+  const int64_t in_w = int64_t{d_in} * 2, out_w = int64_t{d_out} * 2;
+  if (rows > 0) {
+    if (!rows_ok(dy, dy_stride, 1, d_out) || !rows_ok(x, x_stride, 1, d_in) || !aligned_to(w, 16) ||
+        (act != HSTU_ACT_NONE && !aligned_to(z, 16)) || !aligned_to(dx, 16))
+      return HSTU_ERR_INVALID_ARG;
+    const RowSpan in[] = {{dy, 2 * dy_stride, out_w, rows},
+                          {act != HSTU_ACT_NONE ? z : nullptr, out_w, out_w, rows},
+                          {x, 2 * x_stride, in_w, rows},
+                          {w, in_w * d_out, in_w * d_out, 1}},
+                  out[] = {{dx, in_w, in_w, rows}, {dw, in_w * d_out, in_w * d_out, 1}, {dbias, out_w, out_w, 1}};
+    if (outputs_meet(in, out)) return HSTU_ERR_INVALID_ARG;
+  }
+  const LinearLayout l = linear_layout(rows, d_in, d_out, act);
+  if (!aligned_to(ws, 256) || ws_bytes < l.total) return HSTU_ERR_WORKSPACE;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  if (cudaMemsetAsync(base, 0, kHdrWords * 4, cs) != cudaSuccess) return HSTU_ERR_CUDA;
+  if (rows == 0) {  // no rows: dw and dbias are zero
+    if (cudaMemsetAsync(dw, 0, static_cast<size_t>(in_w) * d_out, cs) != cudaSuccess ||
+        (dbias && cudaMemsetAsync(dbias, 0, static_cast<size_t>(out_w), cs) != cudaSuccess))
+      return HSTU_ERR_CUDA;
+    return HSTU_OK;
+  }
+  const void* g = dy;
+  int64_t g_stride = dy_stride;
+  if (act != HSTU_ACT_NONE || dbias) {
+    GradParams gp{};
+    gp.dy = dy;
+    gp.z = act != HSTU_ACT_NONE ? z : nullptr;
+    gp.g = base + l.g;
+    gp.part = reinterpret_cast<float*>(base + l.part);
+    gp.dy_stride = dy_stride;
+    gp.rows = rows;
+    gp.cols = d_out;
+    gp.act = act;
+    if ((f16 ? launch_grad<__half>(gp, dbias, cs) : launch_grad<__nv_bfloat16>(gp, dbias, cs)) != cudaSuccess)
+      return HSTU_ERR_CUDA;
+    if (gp.z) {
+      g = gp.g;
+      g_stride = d_out;
+    }
+  }
+  LinearParams p{};
+  p.header = reinterpret_cast<int32_t*>(base);
+  p.handoff_limit_ns = handoff_limit();
+  p.k_splits = 1;
+  // dx (rows x d_in) = g (K = d_out along its rows) w (K down its columns)
+  if (!box_map(&p.tm_a, g, rows, d_out, g_stride, dtype, 128) || !box_map(&p.tm_b, w, d_out, d_in, d_in, dtype, 64) ||
+      !box_map(&p.tm_y, dx, rows, d_in, d_in, dtype, 32))
+    return HSTU_ERR_CUDA;
+  p.M = static_cast<int32_t>(rows);
+  p.N = d_in;
+  p.K = d_out;
+  if ((f16 ? launch_linear_dx_f16(p, cs) : launch_linear_dx_bf16(p, cs)) != cudaSuccess) return HSTU_ERR_CUDA;
+  // dw (d_out x d_in) = g^T x: K = rows, down the columns of both
+  if (!box_map(&p.tm_a, g, rows, d_out, g_stride, dtype, 64) || !box_map(&p.tm_b, x, rows, d_in, x_stride, dtype, 64) ||
+      !box_map(&p.tm_y, dw, d_out, d_in, d_in, dtype, 32))
+    return HSTU_ERR_CUDA;
+  p.M = d_out;
+  p.N = d_in;
+  p.K = static_cast<int32_t>(rows);
+  p.k_splits = dw_splits(rows, d_in, d_out);
+  p.part = reinterpret_cast<float*>(base + l.dw);
+  if ((f16 ? launch_linear_dw_f16(p, cs) : launch_linear_dw_bf16(p, cs)) != cudaSuccess) return HSTU_ERR_CUDA;
+  if (p.k_splits == 1) return HSTU_OK;
+  const int64_t elems = int64_t{d_out} * d_in;
+  const dim3 grid(static_cast<unsigned>((elems / 8 + 255) / 256));
+  const cudaError_t e = f16 ? launch_chained(linear_split_fold_kernel<__half>, grid, 256, 0, cs,
+                                             static_cast<const float*>(p.part), p.k_splits, elems, static_cast<__half*>(dw))
+                            : launch_chained(linear_split_fold_kernel<__nv_bfloat16>, grid, 256, 0, cs,
+                                             static_cast<const float*>(p.part), p.k_splits, elems,
+                                             static_cast<__nv_bfloat16*>(dw));
+  return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+}
+
+}  // extern "C"

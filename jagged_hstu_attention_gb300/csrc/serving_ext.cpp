@@ -1,5 +1,6 @@
 // Python calls of the serving entry points (rotation, paged cache, candidates
-// against it), as a CPython extension.
+// against it) and of the layer's row operators (layer_ext.h), as a CPython
+// extension.
 //
 // A decode step is a few microseconds on the GPU, and a call through ctypes
 // with its checks in Python took 13 us; here the same checks, the outputs'
@@ -385,6 +386,8 @@ PyObject* guarded(PyObject*, PyObject* const* args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+#include "layer_ext.h"
+
 template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
 constexpr PyMethodDef method(const char* name) {
   return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&guarded<F>)), METH_FASTCALL, nullptr};
@@ -396,6 +399,14 @@ PyMethodDef g_methods[] = {
     method<cache_write>("cache_write"),
     method<cache_read>("cache_read"),
     method<fwd_paged>("fwd_paged"),
+    method<layer::bind_layer>("bind_layer"),
+    method<layer::embed>("embed"),
+    method<layer::embed_bwd>("embed_bwd"),
+    method<layer::rms_norm>("rms_norm"),
+    method<layer::rms_norm_bwd>("rms_norm_bwd"),
+    method<layer::quantise_rows>("quantise_rows"),
+    method<layer::linear>("linear"),
+    method<layer::linear_bwd>("linear_bwd"),
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_serving", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
