@@ -505,7 +505,8 @@ HSTU_API hstu_status_t hstu_attn_fwd_paged(const void* q_c, int64_t q_stride, vo
  * Their rows are (rows, width) of bf16 or fp16, width a multiple of 8; inputs
  * with a stride argument may have their rows that many elements apart (a
  * multiple of 8, at least the width; slices of a wider projection), everything
- * else is contiguous. Base addresses are 16-byte aligned. An output may not
+ * else is contiguous. Base addresses are 16-byte aligned, those of fp32 tables and
+ * their gradients 32-byte. An output may not
  * share memory with an input or another output (HSTU_ERR_INVALID_ARG) where
  * nothing else is said. Sums are in 32 bits and no atomics order them: results are
  * bitwise repeatable. */

@@ -16,8 +16,11 @@
 //     all tokens) leave a sum for each chunk in the workspace, and a join
 //     kernel adds those in order;
 //   - rows of the table that no token names are zeroed by further blocks of the
-//     summing kernel, which know them by a bit a row that the first pass set;
-//     every row of the table is so written once.
+//     sorting and summing kernels, which know them by a bit a row that the first
+//     pass set; every row of the table is so written once, and the sort, which
+//     moves little, hides behind the zeros.
+#include <algorithm>
+
 #include "layer.cuh"
 
 namespace hstu {
@@ -27,8 +30,12 @@ constexpr int kEmbedThreads = 256;
 constexpr int kSortWarps = 16, kSortThreads = 32 * kSortWarps;
 constexpr int kMaxDigitBits = 9, kMaxBins = 1 << kMaxDigitBits;
 constexpr int kSortTiles = 152;  // at most one tile an SM
-constexpr int kFillRows = 64;    // rows of the table a zeroing block looks after
-constexpr int kJoinChunks = 8;   // chunks a joining block looks after
+constexpr int kSeenBits = 10, kSeen = 1 << kSeenBits;
+constexpr int kFillBytes = 1 << 16;  // of the table that a zeroing block looks after, about
+// What a sorting launch zeroes on the side, at most: about what the GPU writes in its time.
+constexpr int64_t kFillMove = 48 << 20, kFillCount = 16 << 20;
+constexpr int kJoinThreads = 1024, kJoinChunks = 32;  // chunks a joining block looks after
+constexpr int kShortRun = 16;  // chunks of a run that one group of threads joins alone
 
 // ------------------------------------------------------------------ forward
 
@@ -101,6 +108,31 @@ cudaError_t launch_embed_typed(const EmbedParams& p, int table_dtype, int dtype,
   return dtype == HSTU_DTYPE_F16 ? launch_embed<H, H, ID>(p, stream) : launch_embed<B, B, ID>(p, stream);
 }
 
+// ------------------------------------------------------------------ zeroing
+
+// Rows [row0, row1) of the table, those that no token names, as 16-byte units.
+struct FillParams {
+  void* table;
+  const uint32_t* named;  // a bit a row
+  int64_t row0, row1;
+  int32_t units;  // of a row
+  int32_t rows;   // of a block
+};
+__host__ __device__ inline int64_t fill_blocks(const FillParams& p) {
+  return p.row1 > p.row0 ? (p.row1 - p.row0 + p.rows - 1) / p.rows : 0;
+}
+__device__ __forceinline__ void fill_rows(const FillParams& p, int64_t block) {
+  const int threads = blockDim.x, group = min(threads, p.units), groups = threads / group, g = threadIdx.x / group;
+  if (g >= groups) return;
+  const int64_t v0 = p.row0 + block * p.rows, v1 = min(v0 + p.rows, p.row1);
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  for (int64_t v = v0 + g; v < v1; v += groups) {
+    if ((p.named[v >> 5] >> (v & 31)) & 1u) continue;
+    uint4* row = static_cast<uint4*>(p.table) + v * p.units;
+    for (int u = threadIdx.x % group; u < p.units; u += group) row[u] = zero;
+  }
+}
+
 // --------------------------------------------------------------------- sort
 
 // One digit's pass over (id, token) pairs, from `ids` itself in the first.
@@ -110,12 +142,13 @@ struct SortParams {
   const int32_t* val_in;
   uint32_t* key_out;
   int32_t* val_out;
-  uint32_t* counts;  // (tiles, bins)
+  uint32_t* counts;  // (tiles, kMaxBins)
   uint32_t* named;   // first pass: a bit for each row of the table that a token names
   int32_t* header;   // null: bad ids are not reported
   int64_t vocab, n;
   int32_t tile;  // pairs of a tile, a multiple of kSortThreads
   int32_t tiles, shift, bits;
+  FillParams fill;  // of the blocks behind the tiles'
 };
 
 // Padding and ids past the table sort behind it, as `vocab`.
@@ -130,22 +163,32 @@ __device__ __forceinline__ uint32_t sort_key(const SortParams& p, int64_t i) {
 template <typename ID, bool FIRST>
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortParams p) {
   chain();
+  if (static_cast<int>(blockIdx.x) >= p.tiles) return fill_rows(p.fill, blockIdx.x - p.tiles);
   __shared__ uint32_t count[kMaxBins];
+  // Ids whose bit a thread of the block has set or is about to: the most frequent ids
+  // would otherwise queue up at one word.
+  __shared__ volatile uint32_t seen[FIRST ? kSeen : 1];
   const int bins = 1 << p.bits;
   for (int b = threadIdx.x; b < bins; b += kSortThreads) count[b] = 0;
+  if (FIRST)
+    for (int b = threadIdx.x; b < kSeen; b += kSortThreads) seen[b] = 0xffffffffu;
   __syncthreads();
   const int64_t i0 = static_cast<int64_t>(blockIdx.x) * p.tile, i1 = min(i0 + p.tile, p.n);
   for (int64_t i = i0 + threadIdx.x; i < i1; i += kSortThreads) {
     const uint32_t key = sort_key<ID, FIRST>(p, i);
     atomicAdd(&count[(key >> p.shift) & (bins - 1)], 1u);
     if (FIRST) {
-      if (key < p.vocab) atomicOr(p.named + (key >> 5), 1u << (key & 31));
-      else if (p.header && static_cast<int64_t>(static_cast<const ID*>(p.ids)[i]) >= 0)
+      if (key < p.vocab) {
+        const uint32_t h = (key * 2654435761u) >> (32 - kSeenBits);
+        if (seen[h] == key) continue;
+        seen[h] = key;
+        atomicOr(p.named + (key >> 5), 1u << (key & 31));
+      } else if (p.header && static_cast<int64_t>(static_cast<const ID*>(p.ids)[i]) >= 0)
         atomicOr(p.header + kHdrErr, kErrInput);
     }
   }
   __syncthreads();
-  for (int b = threadIdx.x; b < bins; b += kSortThreads) p.counts[static_cast<int64_t>(blockIdx.x) * bins + b] = count[b];
+  for (int b = threadIdx.x; b < bins; b += kSortThreads) p.counts[static_cast<int64_t>(blockIdx.x) * kMaxBins + b] = count[b];
 }
 
 // Moves each pair to its place: behind all pairs of a lower digit, those of its
@@ -154,26 +197,44 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortPara
 template <typename ID, bool FIRST>
 __global__ void __launch_bounds__(kSortThreads) sort_move_kernel(const SortParams p) {
   chain();
-  __shared__ uint32_t place[kSortWarps][kMaxBins];
+  if (static_cast<int>(blockIdx.x) >= p.tiles) return fill_rows(p.fill, blockIdx.x - p.tiles);
+  __shared__ alignas(16) uint32_t place[kSortWarps][kMaxBins];
   __shared__ uint32_t warp_sum[kSortWarps];
   const int bins = 1 << p.bits, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // Digit b's pairs in all tiles and in those before this one. Groups of bins / 4 threads
+  // take the tiles in turn, four digits a thread; thread b adds up the groups' sums.
+  uint32_t total = 0, before = 0;
+  {
+    const int quads = max(bins / 4, 1), groups = min(kSortThreads / quads, kSortWarps / 2), g = threadIdx.x / quads;
+    uint4 all = make_uint4(0, 0, 0, 0), low = all;
+    if (g < groups) {
+      const uint32_t* counts = p.counts + threadIdx.x % quads * 4;
+#pragma unroll 8
+      for (int t = g; t < p.tiles; t += groups) {
+        const uint4 c = *reinterpret_cast<const uint4*>(counts + static_cast<int64_t>(t) * kMaxBins);
+        all.x += c.x, all.y += c.y, all.z += c.z, all.w += c.w;
+        if (t < static_cast<int>(blockIdx.x)) low.x += c.x, low.y += c.y, low.z += c.z, low.w += c.w;
+      }
+      *reinterpret_cast<uint4*>(&place[2 * g][threadIdx.x % quads * 4]) = all;
+      *reinterpret_cast<uint4*>(&place[2 * g + 1][threadIdx.x % quads * 4]) = low;
+    }
+    __syncthreads();
+    if (threadIdx.x < bins)
+      for (int x = 0; x < groups; ++x) {
+        total += place[2 * x][threadIdx.x];
+        before += place[2 * x + 1][threadIdx.x];
+      }
+    __syncthreads();
+  }
   for (int i = threadIdx.x; i < kSortWarps * kMaxBins; i += kSortThreads) (&place[0][0])[i] = 0;
   __syncthreads();
   const int part = p.tile / kSortWarps;
   const int64_t i0 = static_cast<int64_t>(blockIdx.x) * p.tile + static_cast<int64_t>(warp) * part;
+#pragma unroll 4
   for (int r = 0; r < part; r += 32) {
     const int64_t i = i0 + r + lane;
     if (i < p.n) atomicAdd(&place[warp][(sort_key<ID, FIRST>(p, i) >> p.shift) & (bins - 1)], 1u);
   }
-  // Thread b (bins <= threads): digit b's pairs in all tiles and in those before this one.
-  uint32_t total = 0, before = 0;
-  if (threadIdx.x < bins)
-#pragma unroll 16
-    for (int t = 0; t < p.tiles; ++t) {
-      const uint32_t c = p.counts[static_cast<int64_t>(t) * bins + threadIdx.x];
-      total += c;
-      if (t < static_cast<int>(blockIdx.x)) before += c;
-    }
   uint32_t sum = total;  // of digits up to this one
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -192,17 +253,26 @@ __global__ void __launch_bounds__(kSortThreads) sort_move_kernel(const SortParam
       at += c;
     }
   __syncthreads();
+  auto val_at = [&](int64_t i) { return FIRST ? static_cast<int32_t>(i) : p.val_in[i]; };
+  uint32_t next_key = i0 + lane < p.n ? sort_key<ID, FIRST>(p, i0 + lane) : 0;
+  int32_t next_val = i0 + lane < p.n ? val_at(i0 + lane) : 0;
   for (int r = 0; r < part; r += 32) {
     const int64_t i = i0 + r + lane;
     const uint32_t live = __ballot_sync(0xffffffffu, i < p.n);
+    const uint32_t key = next_key;
+    const int32_t val = next_val;
+    if (i + 32 < p.n && r + 32 < part) {
+      next_key = sort_key<ID, FIRST>(p, i + 32);
+      next_val = val_at(i + 32);
+    }
     if (i < p.n) {
-      const uint32_t key = sort_key<ID, FIRST>(p, i), digit = (key >> p.shift) & (bins - 1);
+      const uint32_t digit = (key >> p.shift) & (bins - 1);
       const uint32_t same = __match_any_sync(live, digit);
       const uint32_t to = place[warp][digit] + __popc(same & ((1u << lane) - 1u));
       __syncwarp(live);
       if (lane == 31 - __clz(same)) place[warp][digit] = to + 1;
       p.key_out[to] = key;
-      p.val_out[to] = FIRST ? static_cast<int32_t>(i) : p.val_in[i];
+      p.val_out[to] = val;
     }
     __syncwarp();
   }
@@ -215,13 +285,13 @@ struct SumParams {
   int64_t dy_stride;
   const uint32_t* key;  // sorted ids
   const int32_t* val;   // their tokens
-  const uint32_t* named;
   void* dtable;
   float* part;  // (chunks, 2, dim): sums of long runs' chunks; [0] of a run from an earlier chunk, [1] of one that begins
   int64_t n, vocab;
   int32_t chunk, chunks, dim, accumulate;
-  int32_t sum_blocks;  // blocks that sum; the others zero
+  int32_t sum_blocks;  // blocks that sum, spread evenly among those that zero
   float scale;
+  FillParams fill;
 };
 
 // Whether chunk c holds one id alone.
@@ -247,19 +317,17 @@ __device__ __forceinline__ void put_row(const SumParams& p, int64_t row, int col
 template <typename T, typename G>
 __global__ void __launch_bounds__(kEmbedThreads) embed_sum_kernel(const SumParams p) {
   chain();
+  const int64_t summed = static_cast<int64_t>(blockIdx.x) * p.sum_blocks / gridDim.x;  // summing blocks before this one
+  if ((static_cast<int64_t>(blockIdx.x) + 1) * p.sum_blocks / gridDim.x == summed) {
+    if (blockIdx.y == 0) fill_rows(p.fill, blockIdx.x - summed);
+    return;
+  }
   const int col0 = blockIdx.y * kEmbedThreads * 8;
   const int group = min(kEmbedThreads, (p.dim - col0) / 8);  // threads of a row
   const int groups = kEmbedThreads / group, g = threadIdx.x / group;
   const int col = col0 + (threadIdx.x % group) * 8;
   if (g >= groups) return;
-  if (static_cast<int>(blockIdx.x) >= p.sum_blocks) {  // rows that no token names
-    const int64_t v0 = static_cast<int64_t>(blockIdx.x - p.sum_blocks) * kFillRows, v1 = min(v0 + kFillRows, p.vocab);
-    float zero[8] = {};
-    for (int64_t v = v0 + g; v < v1; v += groups)
-      if (((p.named[v >> 5] >> (v & 31)) & 1u) == 0) store8(static_cast<G*>(p.dtable) + v * p.dim + col, zero);
-    return;
-  }
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * groups + g;
+  const int64_t c = summed * groups + g;
   if (c >= p.chunks) return;
   const int64_t i0 = c * p.chunk, end = min(i0 + p.chunk, p.n);
   const uint32_t first = p.key[i0], last = p.key[end - 1];
@@ -329,54 +397,84 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_sum_kernel(const SumParam
 }
 
 // Adds up the chunks of each long run: the end of the chunk before its first
-// whole one, the whole ones, and the beginning of the chunk behind. The groups
-// of a block take consecutive slices of the run, which are added in order.
+// whole one, the whole ones, and the beginning of the chunk behind. A run of a
+// few chunks is one group's, a longer one all groups': they take consecutive slices
+// of it, which are added in order.
 template <typename G>
-__global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(const SumParams p) {
+__global__ void __launch_bounds__(kJoinThreads) embed_join_kernel(const SumParams p) {
   chain();
-  __shared__ float slice[kEmbedThreads][8];
-  __shared__ int found[kJoinChunks];
+  __shared__ float slice[kJoinThreads][8];
+  __shared__ int64_t first[kJoinChunks];
+  __shared__ int runs[2];  // found; short ones among them, listed from the front, the others from the back
   const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kJoinChunks;
-  if (threadIdx.x < kJoinChunks) {
+  if (threadIdx.x < 32) {
     const int64_t c = c0 + threadIdx.x;
-    int is = 0;
+    bool is = false, brief = false;
     if (c < p.chunks) {
       const int64_t i0 = c * p.chunk, end = min(i0 + p.chunk, p.n);
       const uint32_t key = p.key[i0];
       const bool before = i0 > 0 && p.key[i0 - 1] == key, after = end < p.n && p.key[end] == key;
       is = key < p.vocab && p.key[end - 1] == key && (before || after) && !(c > 0 && one_id(p, c - 1, key));
+      brief = c + kShortRun >= p.chunks || p.key[(c + kShortRun) * p.chunk] != key;
     }
-    found[threadIdx.x] = is;
+    const uint32_t small = __ballot_sync(0xffffffffu, is && brief), large = __ballot_sync(0xffffffffu, is && !brief);
+    const uint32_t below = (1u << threadIdx.x) - 1u;
+    if (is && brief) first[__popc(small & below)] = c;
+    if (is && !brief) first[kJoinChunks - 1 - __popc(large & below)] = c;
+    if (threadIdx.x == 0) {
+      runs[0] = __popc(small);
+      runs[1] = __popc(large);
+    }
   }
   __syncthreads();
   const int col0 = blockIdx.y * kEmbedThreads * 8;
   const int group = min(kEmbedThreads, (p.dim - col0) / 8);
-  const int groups = kEmbedThreads / group, g = threadIdx.x / group;
+  const int groups = kJoinThreads / group, g = threadIdx.x / group;
   const int col = col0 + (threadIdx.x % group) * 8;
-  for (int k = 0; k < kJoinChunks; ++k) {
-    if (!found[k]) continue;
-    const int64_t c = c0 + k;
-    const uint32_t key = p.key[c * p.chunk];
-    const bool before = c > 0 && p.key[c * p.chunk - 1] == key;
-    // The last chunk that begins with the id.
-    int64_t lo = c, hi = p.chunks;
-    while (hi - lo > 1) {
-      const int64_t mid = lo + (hi - lo) / 2;
-      if (p.key[mid * p.chunk] == key) lo = mid;
-      else hi = mid;
+  // The sum of chunks [a, b) of a run; of the end of the chunk before too with `before`.
+  auto sum_of = [&](int64_t a, int64_t b, bool before, float (&acc)[8]) {
+    if (before) load8(p.part + ((a - 1) * 2 + 1) * p.dim + col, acc);
+#pragma unroll 8
+    for (int64_t x = a; x < b; ++x) {
+      float f[8];
+      load8(p.part + x * 2 * p.dim + col, f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] += f[e];
     }
-    const int64_t parts = lo - c + 1, per = (parts + groups - 1) / groups;
+  };
+  auto from_before = [&](int64_t c, uint32_t key) { return c > 0 && p.key[c * p.chunk - 1] == key; };
+  if (g < groups)
+    for (int k = g; k < runs[0]; k += groups) {
+      const int64_t c = first[k];
+      const uint32_t key = p.key[c * p.chunk];
+      int parts = 1;
+      bool on = true;
+#pragma unroll
+      for (int x = 1; x < kShortRun; ++x) {
+        on = c + x < p.chunks && p.key[(c + x) * p.chunk] == key && on;
+        parts += on;
+      }
+      float acc[8] = {};
+      sum_of(c, c + parts, from_before(c, key), acc);
+      put_row<G>(p, key, col, acc);
+    }
+  for (int k = 0; k < runs[1]; ++k) {
+    const int64_t c = first[kJoinChunks - 1 - k];
+    const uint32_t key = p.key[c * p.chunk];
+    // The last chunk that begins with the id: all threads look, at a step that
+    // shrinks a thousandfold.
+    int64_t last = c;
+    for (int64_t span = p.chunks - c; span > 1;) {
+      const int64_t step = (span - 1 + kJoinThreads - 1) / kJoinThreads, x = (threadIdx.x + 1) * step;
+      const int hits = __syncthreads_count(x < span && p.key[(last + x) * p.chunk] == key);
+      last += hits * step;
+      span = min(step, span - hits * step);
+    }
+    const int64_t parts = last - c + 1, per = (parts + groups - 1) / groups;
     float acc[8] = {};
     if (g < groups) {
-      const int64_t a = c + g * per, b = min(a + per, c + parts);
-      if (g == 0 && before) load8(p.part + ((c - 1) * 2 + 1) * p.dim + col, acc);
-#pragma unroll 4
-      for (int64_t x = a; x < b; ++x) {
-        float f[8];
-        load8(p.part + x * 2 * p.dim + col, f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] += f[e];
-      }
+      const int64_t a = c + min(g * per, parts), b = c + min((g + 1) * per, parts);
+      sum_of(a, b, g == 0 && from_before(c, key), acc);
 #pragma unroll
       for (int e = 0; e < 8; ++e) slice[threadIdx.x][e] = acc[e];
     }
@@ -392,12 +490,9 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(const SumPara
 }
 
 // No tokens: every row is zero.
-template <typename G>
-__global__ void __launch_bounds__(kEmbedThreads) embed_zero_kernel(G* out, int64_t units) {
+__global__ void __launch_bounds__(kEmbedThreads) embed_zero_kernel(const FillParams p) {
   chain();
-  const int64_t u = static_cast<int64_t>(blockIdx.x) * kEmbedThreads + threadIdx.x;
-  float zero[8] = {};
-  if (u < units) store8(out + u * 8, zero);
+  fill_rows(p, blockIdx.x);
 }
 
 // A chunk's tokens: enough chunks to fill the GPU (2048 threads on each of 152 SMs), 16
@@ -433,8 +528,20 @@ EmbedLayout embed_layout(int64_t n, int64_t vocab, int dim) {
   return l;
 }
 
+// Takes at most `bytes` of the rows still to be zeroed, and a quarter of `all` rows.
+FillParams fill_share(FillParams& rest, int64_t bytes, int64_t all) {
+  FillParams f = rest;
+  const int64_t rows = std::min(bytes / (int64_t{16} * f.units), all / 4);
+  f.row1 = std::min(f.row0 + std::max<int64_t>(rows, 0), rest.row1);
+  rest.row0 = f.row1;
+  return f;
+}
+
+// Leaves the rows still to be zeroed in `fill`.
 template <typename ID>
-cudaError_t launch_sort(SortParams p, uint8_t* base, const EmbedLayout& l, int& last, cudaStream_t stream) {
+cudaError_t launch_sort(SortParams p, FillParams& fill, uint8_t* base, const EmbedLayout& l, int& last,
+                        cudaStream_t stream) {
+  const int64_t all = fill.row1 - fill.row0;
   int bits = 1;
   while ((p.vocab >> bits) != 0) ++bits;  // of the largest key, vocab
   const int passes = (bits + kMaxDigitBits - 1) / kMaxDigitBits;
@@ -448,11 +555,14 @@ cudaError_t launch_sort(SortParams p, uint8_t* base, const EmbedLayout& l, int& 
     p.val_in = reinterpret_cast<const int32_t*>(base + l.val[s & 1]);
     p.key_out = reinterpret_cast<uint32_t*>(base + l.key[(s + 1) & 1]);
     p.val_out = reinterpret_cast<int32_t*>(base + l.val[(s + 1) & 1]);
-    cudaError_t e = launch_chained(s == 0 ? sort_count_kernel<ID, true> : sort_count_kernel<ID, false>, dim3(p.tiles),
-                                   kSortThreads, 0, stream, p);
+    // (the rows' bits are set by the first launch)
+    p.fill = fill_share(fill, s == 0 ? 0 : kFillCount, all);
+    cudaError_t e = launch_chained(s == 0 ? sort_count_kernel<ID, true> : sort_count_kernel<ID, false>,
+                                   dim3(static_cast<unsigned>(p.tiles + fill_blocks(p.fill))), kSortThreads, 0, stream, p);
     if (e != cudaSuccess) return e;
-    e = launch_chained(s == 0 ? sort_move_kernel<ID, true> : sort_move_kernel<ID, false>, dim3(p.tiles), kSortThreads, 0,
-                       stream, p);
+    p.fill = fill_share(fill, kFillMove, all);
+    e = launch_chained(s == 0 ? sort_move_kernel<ID, true> : sort_move_kernel<ID, false>,
+                       dim3(static_cast<unsigned>(p.tiles + fill_blocks(p.fill))), kSortThreads, 0, stream, p);
     if (e != cudaSuccess) return e;
   }
   last = passes & 1;
@@ -465,11 +575,10 @@ cudaError_t launch_sum(SumParams p, cudaStream_t stream) {
   const int groups = kEmbedThreads / (widest / 8);
   const unsigned ny = (p.dim + kEmbedThreads * 8 - 1) / (kEmbedThreads * 8);
   p.sum_blocks = (p.chunks + groups - 1) / groups;
-  const int64_t fill = p.accumulate ? 0 : (p.vocab + kFillRows - 1) / kFillRows;
-  cudaError_t e = launch_chained(embed_sum_kernel<T, G>, dim3(static_cast<unsigned>(p.sum_blocks + fill), ny),
+  cudaError_t e = launch_chained(embed_sum_kernel<T, G>, dim3(static_cast<unsigned>(p.sum_blocks + fill_blocks(p.fill)), ny),
                                  kEmbedThreads, 0, stream, p);
   if (e != cudaSuccess) return e;
-  return launch_chained(embed_join_kernel<G>, dim3((p.chunks + kJoinChunks - 1) / kJoinChunks, ny), kEmbedThreads, 0,
+  return launch_chained(embed_join_kernel<G>, dim3((p.chunks + kJoinChunks - 1) / kJoinChunks, ny), kJoinThreads, 0,
                         stream, p);
 }
 template <typename T>
@@ -501,7 +610,7 @@ HSTU_API hstu_status_t hstu_attn_embed(const void* table, int32_t table_dtype, i
   if (ws && (!aligned_to(ws, 256) || ws_bytes < kHdrWords * 4)) return HSTU_ERR_WORKSPACE;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (tokens > 0) {
-    if (!aligned_to(table, 16) || !aligned_to(out, 16) || !aligned_to(ids, id_bytes)) return HSTU_ERR_INVALID_ARG;
+    if (!aligned_to(table, table_dtype == HSTU_DTYPE_F32 ? 32 : 16) || !aligned_to(out, 16) || !aligned_to(ids, id_bytes)) return HSTU_ERR_INVALID_ARG;
     const int64_t written = tokens * dim * 2;
     if (ranges_meet(out, written, table, vocab * dim * (table_dtype == HSTU_DTYPE_F32 ? 4 : 2)) ||
         ranges_meet(out, written, ids, tokens * id_bytes))
@@ -537,7 +646,7 @@ HSTU_API hstu_status_t hstu_attn_embed_bwd(const void* dy, int64_t dy_stride, in
   if (!embed_types_ok(dtype, grad_dtype, id_bytes)) return HSTU_ERR_UNSUPPORTED;
   if (accumulate != 0 && accumulate != 1) return HSTU_ERR_INVALID_ARG;
   if (accumulate && grad_dtype != HSTU_DTYPE_F32) return HSTU_ERR_UNSUPPORTED;
-  if (!aligned_to(dtable, 16)) return HSTU_ERR_INVALID_ARG;
+  if (!aligned_to(dtable, grad_dtype == HSTU_DTYPE_F32 ? 32 : 16)) return HSTU_ERR_INVALID_ARG;
   if (tokens > 0) {
     if (!rows_ok(dy, dy_stride, 1, dim) || !aligned_to(ids, id_bytes)) return HSTU_ERR_INVALID_ARG;
     const int64_t bytes = vocab * dim * (grad_dtype == HSTU_DTYPE_F32 ? 4 : 2);
@@ -552,14 +661,15 @@ HSTU_API hstu_status_t hstu_attn_embed_bwd(const void* dy, int64_t dy_stride, in
   // the error word and the bits of the rows
   if (cudaMemsetAsync(base, 0, l.key[0], cs) != cudaSuccess) return HSTU_ERR_CUDA;
   cudaError_t e = cudaSuccess;
+  FillParams fill{};
+  fill.table = dtable;
+  fill.named = reinterpret_cast<const uint32_t*>(base + l.named);
+  fill.row1 = accumulate ? 0 : vocab;
+  fill.units = dim / (grad_dtype == HSTU_DTYPE_F32 ? 4 : 8);
+  fill.rows = std::max(1, kFillBytes / (16 * fill.units));
   if (tokens == 0) {
     if (accumulate) return HSTU_OK;
-    const int64_t units = vocab * (dim / 8);
-    const dim3 grid(static_cast<unsigned>((units + kEmbedThreads - 1) / kEmbedThreads));
-    if (grad_dtype == HSTU_DTYPE_F32)
-      e = launch_chained(embed_zero_kernel<float>, grid, kEmbedThreads, 0, cs, static_cast<float*>(dtable), units);
-    else
-      e = launch_chained(embed_zero_kernel<__half>, grid, kEmbedThreads, 0, cs, static_cast<__half*>(dtable), units);
+    e = launch_chained(embed_zero_kernel, dim3(static_cast<unsigned>(fill_blocks(fill))), kEmbedThreads, 0, cs, fill);
     return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
   }
   SortParams sp{};
@@ -570,14 +680,15 @@ HSTU_API hstu_status_t hstu_attn_embed_bwd(const void* dy, int64_t dy_stride, in
   sp.vocab = vocab;
   sp.n = tokens;
   int last = 0;
-  e = id_bytes == 8 ? launch_sort<int64_t>(sp, base, l, last, cs) : launch_sort<int32_t>(sp, base, l, last, cs);
+  e = id_bytes == 8 ? launch_sort<int64_t>(sp, fill, base, l, last, cs)
+                    : launch_sort<int32_t>(sp, fill, base, l, last, cs);
   if (e != cudaSuccess) return HSTU_ERR_CUDA;
   SumParams p{};
   p.dy = dy;
   p.dy_stride = dy_stride;
   p.key = reinterpret_cast<const uint32_t*>(base + l.key[last]);
   p.val = reinterpret_cast<const int32_t*>(base + l.val[last]);
-  p.named = sp.named;
+  p.fill = fill;
   p.dtable = dtable;
   p.part = reinterpret_cast<float*>(base + l.part);
   p.n = tokens;

@@ -8,7 +8,7 @@
 // takes tiles in turn, N fastest, so that pairs running together share A's rows and
 // B stays in L2. 128-byte deep K blocks (64 16-bit or 128 8-bit values) flow through
 // a ring of five TMA stages that runs on across tiles; two 256-column accumulators, so
-// that eight epilogue warps read one out while the next is computed.
+// that sixteen epilogue warps read one out while the next is computed.
 //
 // An operand is K-major when K runs along its tensor's rows, MN-major when K runs
 // down its columns (boxes of 64 columns x 64 rows, 16-bit only).
@@ -23,7 +23,7 @@ namespace hstu {
 constexpr int kTileM = 256, kTileN = 256;        // of a pair
 constexpr int kStages = 5;
 constexpr int kStageOperand = 128 * 128;         // bytes of A and of B in a stage of one CTA
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 16;
 constexpr int kGemmThreads2 = (kEpiWarps + 2) * 32;  // epilogue, TMA producer, MMA issuer
 
 // Epilogues.
@@ -33,7 +33,10 @@ constexpr int kEpiPartial32 = 2; // part[split] = acc in fp32 (split K)
 
 struct LinearParams {
   CUtensorMap tm_a, tm_b;
-  CUtensorMap tm_y, tm_z, tm_r;  // boxes of 64 columns x 32 rows
+  void* y;               // (M, N)
+  void* z;               // nullable, (M, N)
+  const void* residual;  // nullable, rows residual_stride apart
+  int64_t residual_stride;
   const void* bias;              // nullable, (N)
   const uint8_t* a_scale;        // 8-bit operands: exponent bytes of A's and B's rows
   const uint8_t* b_scale;
@@ -42,17 +45,15 @@ struct LinearParams {
   uint64_t handoff_limit_ns;     // of the wait for an accumulator to be read out
   int32_t M, N, K, k_splits;
   int32_t act;
-  bool has_z, has_r;
 };
 
 struct GemmSmem2 {
   alignas(1024) uint8_t a[kStages][kStageOperand];
   alignas(1024) uint8_t b[kStages][kStageOperand];
-  // Of each epilogue warp, 32 rows x 64 columns in the 128-byte swizzle of the maps:
-  // y on its way out; z on its way out, or residual rows on their way in.
-  alignas(1024) uint8_t stage_y[kEpiWarps][32 * 128];
-  alignas(1024) uint8_t stage_zr[kEpiWarps][32 * 128];
-  alignas(8) uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drain, res[kEpiWarps];
+  // 32 x 32 sums of each epilogue warp, turned from a row a lane to 8 columns of
+  // four rows a lane: row r's 16-byte piece j lies at piece j ^ (r % 8) of its line.
+  alignas(128) uint8_t turn[kEpiWarps][32 * 128];
+  alignas(8) uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drain;
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -86,23 +87,6 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void tma_load_own(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void tma_store_box(const CUtensorMap* map, uint32_t src, int x, int y) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(x), "r"(y), "r"(src)
-               : "memory");
-}
-__device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-__device__ __forceinline__ void store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
@@ -164,20 +148,94 @@ __device__ __forceinline__ uint64_t block_desc(uint32_t base, int kk) {
 }
 
 // ------------------------------------------------------------- activations
-// x / (1 + exp(-u)): u = x is SiLU; u = 2 sqrt(2 / pi) (x + 0.044715 x^3) the tanh form of GELU.
-__device__ __forceinline__ float gated(float x, float u) { return __fdividef(x, 1.0f + __expf(-u)); }
+// Two fp32 values in a register pair: one instruction works on both.
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void pair_split(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t pair_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t pair_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t pair_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float reciprocal_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// x / (1 + exp(-u)) of a pair: u = x is SiLU; u = 2 sqrt(2 / pi) (x + 0.044715 x^3) the tanh
+// form of GELU. The exponential is one of base 2, its argument m u, m = -log2(e).
+// (ex2 and rcp stay within 2 units of the exact values; where 1 + exp(-u) is above 2^126
+// the result is 0, less than 2^-119 off.)
 constexpr float kGeluA = 1.5957691216057308f, kGeluB = 0.044715f;  // 2 sqrt(2 / pi)
+constexpr float kLog2e = 1.4426950408889634f;
 template <int ACT>
-__device__ __forceinline__ float activate(float x) {
-  if (ACT == HSTU_ACT_SILU) return gated(x, x);
-  if (ACT == HSTU_ACT_GELU) return gated(x, kGeluA * x * fmaf(kGeluB * x, x, 1.0f));
-  if (ACT == HSTU_ACT_RELU) return x > 0.0f ? x : (x != x ? x : 0.0f);
-  return x;
+__device__ __forceinline__ uint64_t activate2(uint64_t x) {
+  if (ACT == HSTU_ACT_NONE) return x;
+  float a, b;
+  if (ACT == HSTU_ACT_RELU) {
+    pair_split(x, a, b);
+    asm("max.NaN.f32 %0, %0, 0f00000000;" : "+f"(a));
+    asm("max.NaN.f32 %0, %0, 0f00000000;" : "+f"(b));
+    return pair_of(a, b);
+  }
+  uint64_t m;
+  if (ACT == HSTU_ACT_SILU) {
+    m = pair_mul(x, pair_of(-kLog2e, -kLog2e));
+  } else {
+    const uint64_t sq = pair_mul(x, x);
+    const uint64_t poly = pair_fma(sq, pair_of(-kLog2e * kGeluA * kGeluB, -kLog2e * kGeluA * kGeluB),
+                                   pair_of(-kLog2e * kGeluA, -kLog2e * kGeluA));
+    m = pair_mul(x, poly);
+  }
+  pair_split(m, a, b);
+  pair_split(pair_add(pair_of(exp2_fast(a), exp2_fast(b)), pair_of(1.0f, 1.0f)), a, b);
+  return pair_mul(x, pair_of(reciprocal_fast(a), reciprocal_fast(b)));
 }
 template <int ACT>
-__device__ __forceinline__ void activate_all(float (&v)[64]) {
+__device__ __forceinline__ void activate_all(uint64_t (&v)[4]) {
 #pragma unroll
-  for (int e = 0; e < 64; ++e) v[e] = activate<ACT>(v[e]);
+  for (int e = 0; e < 4; ++e) v[e] = activate2<ACT>(v[e]);
+}
+__device__ __forceinline__ uint64_t pair_bits(uint32_t lo, uint32_t hi) {
+  return pair_of(__uint_as_float(lo), __uint_as_float(hi));
+}
+template <typename T>
+__device__ __forceinline__ uint64_t unpack_pair(uint32_t w) {
+  return pair_of(Elem<T>::lo(w), Elem<T>::hi(w));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack_pair(uint64_t v) {
+  float a, b;
+  pair_split(v, a, b);
+  return Elem<T>::pack2(a, b);
+}
+// Eight columns, rounded; nothing here reads them again.
+template <typename T>
+__device__ __forceinline__ void store_cols(T* dst, const uint64_t (&v)[4]) {
+  asm volatile("st.global.L1::no_allocate.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(dst), "r"(pack_pair<T>(v[0])),
+               "r"(pack_pair<T>(v[1])), "r"(pack_pair<T>(v[2])), "r"(pack_pair<T>(v[3]))
+               : "memory");
 }
 
 template <typename T, bool F8, bool A_MN, bool B_MN, int EPI>
@@ -192,7 +250,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads2, 1)
   const int tm = (p.M + kTileM - 1) / kTileM, tn = (p.N + kTileN - 1) / kTileN;
   const int n_tiles = tm * tn * p.k_splits;
   const int nk = (p.K + KB - 1) / KB, per = (nk + p.k_splits - 1) / p.k_splits;
-  // Tile t: K split t / (tm tn), then m tile, then n tile. Its K blocks are [kb0, kb1).
+  // Tile t: K split t / (tm tn), then m tile, then n tile. Its K blocks are [kb0, kb1), one
+  // at least.
   auto tile_of = [&](int t, int& m0, int& n0, int& split, int& kb0, int& kb1) {
     split = t / (tm * tn);
     const int rem = t - split * tm * tn;
@@ -212,7 +271,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads2, 1)
       mbar_init(smem_u32(&s.acc_empty[i]), 2 * kEpiWarps);  // of both CTAs
     }
     mbar_init(smem_u32(&s.drain), 1);
-    for (int i = 0; i < kEpiWarps; ++i) mbar_init(smem_u32(&s.res[i]), 1);
     fence_mbar_init();
   }
   if (warp == kEpiWarps + 1) {
@@ -305,180 +363,109 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads2, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue
-    // Warp w reads TMEM lanes 32 (w % 4) .. and columns 128 (w / 4) .., in two
-    // chunks of 64.
-    const int quarter = warp & 3, half = warp >> 2;
+    // Warp w reads TMEM lanes 32 (w % 4) .. and columns 64 (w / 4) .., in two
+    // parts of 32 columns, a row a lane, and turns them in shared memory: a lane then
+    // has 8 columns of rows lane / 4 + 8 k, so that its column's bias and scales are
+    // a few registers and a warp's loads and stores are runs of 64 bytes.
+    const int quarter = warp & 3, group = warp >> 2;
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t st_y = smem_u32(s.stage_y[warp]), st_zr = smem_u32(s.stage_zr[warp]);
-    const uint32_t res_bar = smem_u32(&s.res[warp]);
-    const bool has_z = EPI == kEpiLinear && p.has_z, has_r = EPI == kEpiLinear && p.has_r;
-    const bool ahead = has_r && !has_z;  // residual rows are loaded a chunk ahead
-    // The chunk behind (t, c) that has rows and columns of the matrix.
-    auto place = [&](int t, int c, int& row0, int& col) {
-      int m0, n0, split, kb0, kb1;
-      tile_of(t, m0, n0, split, kb0, kb1);
-      row0 = m0 + 128 * static_cast<int>(rank) + quarter * 32;
-      col = n0 + half * 128 + c * 64;
-      return row0 < p.M && col < p.N;
-    };
-    auto load_residual = [&](int row0, int col) {  // lane 0
-      mbar_expect_tx(res_bar, 32 * 128);
-      tma_load_own(st_zr, &p.tm_r, res_bar, col, row0);
-    };
-    auto load_next = [&](int t, int c) {  // lane 0: the first such chunk from (t, c) on
-      for (; t < n_tiles; t += pairs, c = 0)
-        for (; c < 2; ++c) {
-          int row0, col;
-          if (place(t, c, row0, col)) {
-            load_residual(row0, col);
-            return;
-          }
-        }
-    };
-    if (ahead && lane == 0) load_next(pair, 0);
-    uint32_t res_phase = 0;
-    bool pending = false, ok = true;  // lane 0: committed stores may still read the staging buffers
+    const uint32_t mine = smem_u32(s.turn[warp]);
+    const int sub_row = lane >> 2, sub_col = (lane & 3) * 8;
+    bool ok = true;
     int i = 0;
     for (int t = pair; ok && t < n_tiles; t += pairs, ++i) {
       int m0, n0, split, kb0, kb1;
       tile_of(t, m0, n0, split, kb0, kb1);
-      const int buf = i & 1;
+      const int row0 = m0 + 128 * static_cast<int>(rank) + quarter * 32, col0 = n0 + group * 64;
+      const int buf = i & 1, first_row = row0 + sub_row;
+      // What belongs to rows and columns is read while the accumulator is computed (the
+      // first part's) or the part before is worked on.
+      uint4 bias, residual[4];
+      uint2 col_scale;
+      float row_scale[4];
+      auto load_part = [&](int col) {
+        if constexpr (EPI == kEpiLinear) {
+          bias = make_uint4(0, 0, 0, 0);
+          col_scale = make_uint2(0, 0);
+          if (p.bias && col < p.N) bias = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.bias) + col);
+          if (F8 && col < p.N) col_scale = *reinterpret_cast<const uint2*>(p.b_scale + col);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            residual[k] = make_uint4(0, 0, 0, 0);
+            if (p.residual && col < p.N && first_row + 8 * k < p.M)
+              residual[k] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.residual) +
+                                                            (first_row + 8 * k) * p.residual_stride + col);
+          }
+        }
+      };
+      load_part(col0 + sub_col);
+      if (F8)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) row_scale[k] = first_row + 8 * k < p.M ? scale_value(p.a_scale[first_row + 8 * k]) : 0.0f;
       ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&s.acc_full[buf]), (i >> 1) & 1, abort_flag));
       if (!ok) break;
       tc_fence_after();
-      const bool none = kb1 == kb0;  // nothing accumulated: zeros
+#pragma unroll
       for (int c = 0; c < 2; ++c) {
-        int row0, col;
-        const bool live = place(t, c, row0, col);
-        const int row = row0 + lane;
-        if (!live) continue;  // the same for the whole warp
-        uint32_t a[32], b[32];
-        const uint32_t at = tbase + buf * kTileN + lane_addr + half * 128 + c * 64;
-        tmem_ld32(at, a);
-        tmem_ld32(at + 32, b);
-        float v[64];
-        // What belongs to the columns is read while the accumulators are.
-        uint4 bias[8];
-        if (EPI == kEpiLinear)
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            bias[q] = p.bias && col + 8 * q < p.N
-                          ? *reinterpret_cast<const uint4*>(static_cast<const T*>(p.bias) + col + 8 * q)
-                          : make_uint4(0, 0, 0, 0);
-        uint2 scale[8];
-        float row_scale = 1.0f;
-        if (F8) {
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            scale[q] = col + 8 * q < p.N ? *reinterpret_cast<const uint2*>(p.b_scale + col + 8 * q) : make_uint2(0, 0);
-          if (row < p.M) row_scale = scale_value(p.a_scale[row]);
-        }
+        if (row0 >= p.M || col0 + 32 * c >= p.N) break;  // the same for the whole warp
+        const int col = col0 + 32 * c + sub_col;
+        uint32_t a[32];
+        tmem_ld32(tbase + buf * kTileN + lane_addr + group * 64 + c * 32, a);
         tmem_ld_wait(a);
-        tmem_ld_wait(b);
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          v[e] = none ? 0.0f : __uint_as_float(a[e]);
-          v[32 + e] = none ? 0.0f : __uint_as_float(b[e]);
-        }
-        if (EPI == kEpiPartial32) {
-          if (row < p.M) {
-            float* dst = p.part + (static_cast<int64_t>(split) * p.M + row) * p.N + col;
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              if (col + 8 * q < p.N)
-                asm volatile("st.global.L1::no_allocate.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
-                                 dst + 8 * q),
-                             "f"(v[8 * q]), "f"(v[8 * q + 1]), "f"(v[8 * q + 2]), "f"(v[8 * q + 3]), "f"(v[8 * q + 4]),
-                             "f"(v[8 * q + 5]), "f"(v[8 * q + 6]), "f"(v[8 * q + 7])
-                             : "memory");
-          }
-          continue;
-        }
-        if (F8)
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const uint32_t byte = ((e < 4 ? scale[q].x : scale[q].y) >> (8 * (e & 3))) & 0xffu;
-              v[8 * q + e] = v[8 * q + e] * row_scale * scale_value(byte);
-            }
-        if (EPI == kEpiLinear)
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const uint32_t w[4] = {bias[q].x, bias[q].y, bias[q].z, bias[q].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              v[8 * q + 2 * e] += Elem<T>::lo(w[e]);
-              v[8 * q + 2 * e + 1] += Elem<T>::hi(w[e]);
-            }
-          }
-        // The stores of the chunk before have read the staging buffers.
-        if (lane == 0 && pending) store_wait_read();
-        __syncwarp();
-        // Row `lane`, 16-byte piece j lies at piece j ^ (lane & 7) of the row.
-        const uint32_t line = static_cast<uint32_t>(lane * 128);
-        if (EPI == kEpiLinear) {
-          uint4 z[8];
-          if (has_z)
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              z[j] = make_uint4(Elem<T>::pack2(v[8 * j], v[8 * j + 1]), Elem<T>::pack2(v[8 * j + 2], v[8 * j + 3]),
-                                Elem<T>::pack2(v[8 * j + 4], v[8 * j + 5]), Elem<T>::pack2(v[8 * j + 6], v[8 * j + 7]));
-          switch (p.act) {
-            case HSTU_ACT_SILU: activate_all<HSTU_ACT_SILU>(v); break;
-            case HSTU_ACT_GELU: activate_all<HSTU_ACT_GELU>(v); break;
-            case HSTU_ACT_RELU: activate_all<HSTU_ACT_RELU>(v); break;
-            default: break;
-          }
-          if (has_r) {
-            if (!ahead && lane == 0) load_residual(row0, col);
-            ok = __all_sync(0xffffffffu, mbar_wait(res_bar, res_phase, abort_flag));
-            if (!ok) break;
-            res_phase ^= 1u;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const uint4 r = lds128(st_zr + line + ((j ^ (lane & 7)) << 4));
-              const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                v[8 * j + 2 * e] += Elem<T>::lo(w[e]);
-                v[8 * j + 2 * e + 1] += Elem<T>::hi(w[e]);
-              }
-            }
-            __syncwarp();
-            if (ahead && lane == 0) {
-              fence_async_smem();  // the buffer has been read before the next copy into it
-              load_next(t, c + 1);
-            }
-          }
-          if (has_z)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sts128(st_zr + line + ((j ^ (lane & 7)) << 4), z[j].x, z[j].y, z[j].z, z[j].w);
-        }
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          sts128(st_y + line + ((j ^ (lane & 7)) << 4), Elem<T>::pack2(v[8 * j], v[8 * j + 1]),
-                 Elem<T>::pack2(v[8 * j + 2], v[8 * j + 3]), Elem<T>::pack2(v[8 * j + 4], v[8 * j + 5]),
-                 Elem<T>::pack2(v[8 * j + 6], v[8 * j + 7]));
-        fence_async_smem();
+          sts128(mine + lane * 128 + ((j ^ (lane & 7)) << 4), a[4 * j], a[4 * j + 1], a[4 * j + 2], a[4 * j + 3]);
         __syncwarp();
-        if (lane == 0) {  // rows and columns past the matrix are clipped by the map
-          tma_store_box(&p.tm_y, st_y, col, row0);
-          if (has_z) tma_store_box(&p.tm_z, st_zr, col, row0);
-          store_commit();
-          pending = true;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int r = sub_row + 8 * k;
+          const uint32_t line = mine + r * 128, piece = (lane & 3) * 2;
+          const uint4 lo = lds128(line + ((piece ^ (r & 7)) << 4)), hi = lds128(line + (((piece + 1) ^ (r & 7)) << 4));
+          const bool live = row0 + r < p.M && col < p.N;
+          const int64_t at = static_cast<int64_t>(row0 + r) * p.N + col;
+          if constexpr (EPI == kEpiPartial32) {
+            if (live)
+              asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                               p.part + static_cast<int64_t>(split) * p.M * p.N + at),
+                           "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w)
+                           : "memory");
+          } else {
+            uint64_t v[4] = {pair_bits(lo.x, lo.y), pair_bits(lo.z, lo.w), pair_bits(hi.x, hi.y), pair_bits(hi.z, hi.w)};
+            if constexpr (EPI == kEpiLinear) {
+              const uint32_t bw[4] = {bias.x, bias.y, bias.z, bias.w};
+              const uint64_t rs = pair_of(row_scale[k], row_scale[k]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if (F8) {
+                  const uint32_t w = (e < 2 ? col_scale.x : col_scale.y) >> (16 * (e & 1));
+                  v[e] = pair_mul(pair_mul(v[e], rs), pair_of(scale_value(w & 0xffu), scale_value((w >> 8) & 0xffu)));
+                }
+                v[e] = pair_add(v[e], unpack_pair<T>(bw[e]));
+              }
+              if (p.z && live) store_cols<T>(static_cast<T*>(p.z) + at, v);
+              switch (p.act) {
+                case HSTU_ACT_SILU: activate_all<HSTU_ACT_SILU>(v); break;
+                case HSTU_ACT_GELU: activate_all<HSTU_ACT_GELU>(v); break;
+                case HSTU_ACT_RELU: activate_all<HSTU_ACT_RELU>(v); break;
+                default: break;
+              }
+              if (p.residual) {
+                const uint32_t rw[4] = {residual[k].x, residual[k].y, residual[k].z, residual[k].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = pair_add(v[e], unpack_pair<T>(rw[e]));
+              }
+            }
+            if (live) store_cols<T>(static_cast<T*>(p.y) + at, v);
+          }
         }
+        if (c == 0) load_part(col + 32);
+        __syncwarp();  // the sums have been read before the next part's are written
       }
       tc_fence_before();
-      if (ok && lane == 0) arrive_cluster(in_cta(smem_u32(&s.acc_empty[buf]), 0));
+      if (lane == 0) arrive_cluster(in_cta(smem_u32(&s.acc_empty[buf]), 0));
       __syncwarp();
     }
-    if (!ok && lane == 0) {
-      store_cluster(peer_abort, 1);
-      // a residual copy in flight: the barrier's phase that has not been seen
-      if (has_r) mbar_wait_drain(res_bar, res_phase);
-    }
-    if (lane == 0 && pending) store_wait();  // every store done before the CTA ends
+    if (!ok && lane == 0) store_cluster(peer_abort, 1);
     __syncwarp();
   }
   tc_fence_before();

@@ -155,8 +155,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// Boxes of 128 bytes x box_rows of a row-major (rows, cols) matrix; what lies outside it
-// reads as zeros and is not written.
+// Boxes of 128 bytes x box_rows of a row-major (rows, cols) operand; what lies outside
+// it reads as zeros.
 constexpr int kDtypeCodes = -1;  // 8-bit
 bool box_map(CUtensorMap* m, const void* ptr, int64_t rows, int64_t cols, int64_t stride, int dtype, int box_rows) {
   auto fn = encode_fn();
@@ -261,10 +261,12 @@ HSTU_API hstu_status_t hstu_attn_linear(const void* x, int64_t x_stride, const u
   if (rows == 0) return HSTU_OK;
   LinearParams p{};
   const int type = codes ? kDtypeCodes : dtype;
-  if (!box_map(&p.tm_a, x, rows, d_in, x_stride, type, 128) || !box_map(&p.tm_b, w, d_out, d_in, d_in, type, 128) ||
-      !box_map(&p.tm_y, y, rows, d_out, d_out, dtype, 32) || (z && !box_map(&p.tm_z, z, rows, d_out, d_out, dtype, 32)) ||
-      (residual && !box_map(&p.tm_r, residual, rows, d_out, residual_stride, dtype, 32)))
+  if (!box_map(&p.tm_a, x, rows, d_in, x_stride, type, 128) || !box_map(&p.tm_b, w, d_out, d_in, d_in, type, 128))
     return HSTU_ERR_CUDA;
+  p.y = y;
+  p.z = z;
+  p.residual = residual;
+  p.residual_stride = residual_stride;
   p.bias = bias;
   p.a_scale = x_scale;
   p.b_scale = w_scale;
@@ -275,8 +277,6 @@ HSTU_API hstu_status_t hstu_attn_linear(const void* x, int64_t x_stride, const u
   p.K = d_in;
   p.k_splits = 1;
   p.act = act;
-  p.has_z = z != nullptr;
-  p.has_r = residual != nullptr;
   const cudaError_t e =
       dtype == HSTU_DTYPE_F16 ? launch_linear_f16(p, codes, cs) : launch_linear_bf16(p, codes, cs);
   return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
@@ -344,17 +344,17 @@ HSTU_API hstu_status_t hstu_attn_linear_bwd(const void* dy, int64_t dy_stride, c
   p.handoff_limit_ns = handoff_limit();
   p.k_splits = 1;
   // dx (rows x d_in) = g (K = d_out along its rows) w (K down its columns)
-  if (!box_map(&p.tm_a, g, rows, d_out, g_stride, dtype, 128) || !box_map(&p.tm_b, w, d_out, d_in, d_in, dtype, 64) ||
-      !box_map(&p.tm_y, dx, rows, d_in, d_in, dtype, 32))
+  if (!box_map(&p.tm_a, g, rows, d_out, g_stride, dtype, 128) || !box_map(&p.tm_b, w, d_out, d_in, d_in, dtype, 64))
     return HSTU_ERR_CUDA;
+  p.y = dx;
   p.M = static_cast<int32_t>(rows);
   p.N = d_in;
   p.K = d_out;
   if ((f16 ? launch_linear_dx_f16(p, cs) : launch_linear_dx_bf16(p, cs)) != cudaSuccess) return HSTU_ERR_CUDA;
   // dw (d_out x d_in) = g^T x: K = rows, down the columns of both
-  if (!box_map(&p.tm_a, g, rows, d_out, g_stride, dtype, 64) || !box_map(&p.tm_b, x, rows, d_in, x_stride, dtype, 64) ||
-      !box_map(&p.tm_y, dw, d_out, d_in, d_in, dtype, 32))
+  if (!box_map(&p.tm_a, g, rows, d_out, g_stride, dtype, 64) || !box_map(&p.tm_b, x, rows, d_in, x_stride, dtype, 64))
     return HSTU_ERR_CUDA;
+  p.y = dw;
   p.M = d_out;
   p.N = d_in;
   p.K = static_cast<int32_t>(rows);
