@@ -592,8 +592,8 @@ HSTU_API hstu_status_t hstu_attn_rms_norm_bwd(const void* dy, int64_t dy_stride,
  * with fp32 sums and one rounding each of z and y.
  *   x        (rows, d_in), w (d_out, d_in) contiguous: of dtype, x_scale and
  *            w_scale NULL; or 8-bit floats (e4m3) of the rows of x and of w under
- *            the scales 2^(x_scale - 127) (rows) and 2^(w_scale - 127) (d_out), as
- *            hstu_attn_rms_norm and hstu_attn_quantise_rows write them
+ *            the scales 2^(x_scale - 127) (rows) and 2^(w_scale - 127) (d_out, 16-byte
+ *            aligned), as hstu_attn_rms_norm and hstu_attn_quantise_rows write them
  *   bias     (d_out) of dtype, or NULL; residual (rows, d_out) of dtype, or NULL
  *   act      HSTU_ACT_*
  *   y        (rows, d_out) of dtype; z the same or NULL (a backward with an

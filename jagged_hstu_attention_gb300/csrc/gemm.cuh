@@ -14,6 +14,8 @@
 // down its columns (boxes of 64 columns x 64 rows, 16-bit only).
 #pragma once
 
+#include <type_traits>
+
 #include "../../include/hstu_attn.h"
 #include "cache.cuh"
 #include "internal.h"
@@ -73,8 +75,10 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// An arrival that orders nothing: what it reports, reads of TMEM, has completed (a
+// releasing one waits until the warp's stores of results have reached L2, 2700 cycles).
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void store_cluster(uint32_t addr, int v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
@@ -87,6 +91,8 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
+// This thread's shared-memory writes become visible to MMAs and bulk copies.
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
@@ -184,9 +190,10 @@ __device__ __forceinline__ float reciprocal_fast(float x) {
 }
 
 // x / (1 + exp(-u)) of a pair: u = x is SiLU; u = 2 sqrt(2 / pi) (x + 0.044715 x^3) the tanh
-// form of GELU. The exponential is one of base 2, its argument m u, m = -log2(e).
-// (ex2 and rcp stay within 2 units of the exact values; where 1 + exp(-u) is above 2^126
-// the result is 0, less than 2^-119 off.)
+// form of GELU. The exponentials are of base 2, their arguments m u, m = -log2(e),
+// at most 60 so that the product of the two sums below stays finite (past it the
+// result is 2^-60 x, for what is nearer to 0). One reciprocal serves both: 1 / a =
+// b / (a b). (ex2 runs at 32 a cycle and SM, rcp at 16.)
 constexpr float kGeluA = 1.5957691216057308f, kGeluB = 0.044715f;  // 2 sqrt(2 / pi)
 constexpr float kLog2e = 1.4426950408889634f;
 template <int ACT>
@@ -209,13 +216,11 @@ __device__ __forceinline__ uint64_t activate2(uint64_t x) {
     m = pair_mul(x, poly);
   }
   pair_split(m, a, b);
+  asm("min.NaN.f32 %0, %0, 0f42700000;" : "+f"(a));
+  asm("min.NaN.f32 %0, %0, 0f42700000;" : "+f"(b));
   pair_split(pair_add(pair_of(exp2_fast(a), exp2_fast(b)), pair_of(1.0f, 1.0f)), a, b);
-  return pair_mul(x, pair_of(reciprocal_fast(a), reciprocal_fast(b)));
-}
-template <int ACT>
-__device__ __forceinline__ void activate_all(uint64_t (&v)[4]) {
-#pragma unroll
-  for (int e = 0; e < 4; ++e) v[e] = activate2<ACT>(v[e]);
+  const float r = reciprocal_fast(a * b);
+  return pair_mul(x, pair_mul(pair_of(r, r), pair_of(b, a)));
 }
 __device__ __forceinline__ uint64_t pair_bits(uint32_t lo, uint32_t hi) {
   return pair_of(__uint_as_float(lo), __uint_as_float(hi));
@@ -365,12 +370,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads2, 1)
     // ------------------------------------------------------------ epilogue
     // Warp w reads TMEM lanes 32 (w % 4) .. and columns 64 (w / 4) .., in two
     // parts of 32 columns, a row a lane, and turns them in shared memory: a lane then
-    // has 8 columns of rows lane / 4 + 8 k, so that its column's bias and scales are
-    // a few registers and a warp's loads and stores are runs of 64 bytes.
+    // has 8 columns of rows lane / 4 + 8 k, so that its columns' bias and scales are
+    // a few registers and a warp's loads and stores are runs of 64 bytes. What the
+    // kernel is short of is shared memory's bandwidth: the operands alone take 4096 of
+    // its cycles a tile at K = 512, as long as their MMAs, and an epilogue 2000 more.
+    // (Of 40960 rows, K = 512, N = 2048, with z and SiLU: 80 us so; 87 us with 16-bit
+    // rows staged for TMA stores, 86 us with a row's 32-byte pieces stored by its
+    // lane; 58 us without any stores, 45 us without an epilogue.)
     const int quarter = warp & 3, group = warp >> 2;
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t mine = smem_u32(s.turn[warp]);
     const int sub_row = lane >> 2, sub_col = (lane & 3) * 8;
+    // The two pieces of a lane in line r = sub_row + 8 k: r % 8 is sub_row's.
+    const uint32_t piece = (lane & 3) * 2, from = mine + sub_row * 128;
+    const uint32_t lo_at = from + ((piece ^ (sub_row & 7)) << 4), hi_at = from + (((piece + 1) ^ (sub_row & 7)) << 4);
+    const int64_t skip = int64_t{8} * p.N;  // eight rows on
     bool ok = true;
     int i = 0;
     for (int t = pair; ok && t < n_tiles; t += pairs, ++i) {
@@ -378,6 +392,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads2, 1)
       tile_of(t, m0, n0, split, kb0, kb1);
       const int row0 = m0 + 128 * static_cast<int>(rank) + quarter * 32, col0 = n0 + group * 64;
       const int buf = i & 1, first_row = row0 + sub_row;
+      const int rows = min(max((p.M - first_row + 7) >> 3, 0), 4);  // of the lane's four
       // What belongs to rows and columns is read while the accumulator is computed (the
       // first part's) or the part before is worked on.
       uint4 bias, residual[4];
@@ -386,25 +401,68 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads2, 1)
       auto load_part = [&](int col) {
         if constexpr (EPI == kEpiLinear) {
           bias = make_uint4(0, 0, 0, 0);
-          col_scale = make_uint2(0, 0);
           if (p.bias && col < p.N) bias = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.bias) + col);
           if (F8 && col < p.N) col_scale = *reinterpret_cast<const uint2*>(p.b_scale + col);
+          if (p.residual && col < p.N) {
+            const T* from_row = static_cast<const T*>(p.residual) + first_row * p.residual_stride + col;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            residual[k] = make_uint4(0, 0, 0, 0);
-            if (p.residual && col < p.N && first_row + 8 * k < p.M)
-              residual[k] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.residual) +
-                                                            (first_row + 8 * k) * p.residual_stride + col);
+            for (int k = 0; k < 4; ++k)
+              if (k < rows) residual[k] = *reinterpret_cast<const uint4*>(from_row + 8 * k * p.residual_stride);
           }
         }
       };
       load_part(col0 + sub_col);
       if (F8)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) row_scale[k] = first_row + 8 * k < p.M ? scale_value(p.a_scale[first_row + 8 * k]) : 0.0f;
+        for (int k = 0; k < 4; ++k) row_scale[k] = k < rows ? scale_value(p.a_scale[first_row + 8 * k]) : 0.0f;
       ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&s.acc_full[buf]), (i >> 1) & 1, abort_flag));
       if (!ok) break;
       tc_fence_after();
+      bool held = true;  // the accumulator
+      auto release = [&] {
+        tc_fence_before();
+        if (lane == 0) arrive_cluster(in_cta(smem_u32(&s.acc_empty[buf]), 0));
+        held = false;
+      };
+      // Eight columns of the lane's four rows.
+      auto write_part = [&](auto act, int col) {
+        const int64_t at = static_cast<int64_t>(first_row) * p.N + col;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint4 lo = lds128(lo_at + 1024 * k), hi = lds128(hi_at + 1024 * k);
+          const bool live = k < rows && col < p.N;
+          if constexpr (EPI == kEpiPartial32) {
+            if (live)
+              asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                               p.part + static_cast<int64_t>(split) * p.M * p.N + at + k * skip),
+                           "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w)
+                           : "memory");
+          } else {
+            uint64_t v[4] = {pair_bits(lo.x, lo.y), pair_bits(lo.z, lo.w), pair_bits(hi.x, hi.y), pair_bits(hi.z, hi.w)};
+            if constexpr (EPI == kEpiLinear) {
+              const uint32_t bw[4] = {bias.x, bias.y, bias.z, bias.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if (F8) {
+                  const uint32_t w = (e < 2 ? col_scale.x : col_scale.y) >> (16 * (e & 1));
+                  v[e] = pair_mul(v[e], pair_of(row_scale[k], row_scale[k]));
+                  v[e] = pair_mul(v[e], pair_of(scale_value(w & 0xffu), scale_value((w >> 8) & 0xffu)));
+                }
+                v[e] = pair_add(v[e], unpack_pair<T>(bw[e]));
+              }
+              if (p.z && live) store_cols<T>(static_cast<T*>(p.z) + at + k * skip, v);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) v[e] = activate2<decltype(act)::value>(v[e]);
+              if (p.residual) {
+                const uint32_t rw[4] = {residual[k].x, residual[k].y, residual[k].z, residual[k].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = pair_add(v[e], unpack_pair<T>(rw[e]));
+              }
+            }
+            if (live) store_cols<T>(static_cast<T*>(p.y) + at + k * skip, v);
+          }
+        }
+      };
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         if (row0 >= p.M || col0 + 32 * c >= p.N) break;  // the same for the whole warp
@@ -412,57 +470,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads2, 1)
         uint32_t a[32];
         tmem_ld32(tbase + buf * kTileN + lane_addr + group * 64 + c * 32, a);
         tmem_ld_wait(a);
+        if (c == 1) release();
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           sts128(mine + lane * 128 + ((j ^ (lane & 7)) << 4), a[4 * j], a[4 * j + 1], a[4 * j + 2], a[4 * j + 3]);
         __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int r = sub_row + 8 * k;
-          const uint32_t line = mine + r * 128, piece = (lane & 3) * 2;
-          const uint4 lo = lds128(line + ((piece ^ (r & 7)) << 4)), hi = lds128(line + (((piece + 1) ^ (r & 7)) << 4));
-          const bool live = row0 + r < p.M && col < p.N;
-          const int64_t at = static_cast<int64_t>(row0 + r) * p.N + col;
-          if constexpr (EPI == kEpiPartial32) {
-            if (live)
-              asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
-                               p.part + static_cast<int64_t>(split) * p.M * p.N + at),
-                           "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w)
-                           : "memory");
-          } else {
-            uint64_t v[4] = {pair_bits(lo.x, lo.y), pair_bits(lo.z, lo.w), pair_bits(hi.x, hi.y), pair_bits(hi.z, hi.w)};
-            if constexpr (EPI == kEpiLinear) {
-              const uint32_t bw[4] = {bias.x, bias.y, bias.z, bias.w};
-              const uint64_t rs = pair_of(row_scale[k], row_scale[k]);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if (F8) {
-                  const uint32_t w = (e < 2 ? col_scale.x : col_scale.y) >> (16 * (e & 1));
-                  v[e] = pair_mul(pair_mul(v[e], rs), pair_of(scale_value(w & 0xffu), scale_value((w >> 8) & 0xffu)));
-                }
-                v[e] = pair_add(v[e], unpack_pair<T>(bw[e]));
-              }
-              if (p.z && live) store_cols<T>(static_cast<T*>(p.z) + at, v);
-              switch (p.act) {
-                case HSTU_ACT_SILU: activate_all<HSTU_ACT_SILU>(v); break;
-                case HSTU_ACT_GELU: activate_all<HSTU_ACT_GELU>(v); break;
-                case HSTU_ACT_RELU: activate_all<HSTU_ACT_RELU>(v); break;
-                default: break;
-              }
-              if (p.residual) {
-                const uint32_t rw[4] = {residual[k].x, residual[k].y, residual[k].z, residual[k].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = pair_add(v[e], unpack_pair<T>(rw[e]));
-              }
-            }
-            if (live) store_cols<T>(static_cast<T*>(p.y) + at, v);
+        if constexpr (EPI == kEpiLinear) {
+          switch (p.act) {
+            case HSTU_ACT_SILU: write_part(std::integral_constant<int, HSTU_ACT_SILU>{}, col); break;
+            case HSTU_ACT_GELU: write_part(std::integral_constant<int, HSTU_ACT_GELU>{}, col); break;
+            case HSTU_ACT_RELU: write_part(std::integral_constant<int, HSTU_ACT_RELU>{}, col); break;
+            default: write_part(std::integral_constant<int, HSTU_ACT_NONE>{}, col); break;
           }
+        } else {
+          write_part(std::integral_constant<int, HSTU_ACT_NONE>{}, col);
         }
         if (c == 0) load_part(col + 32);
         __syncwarp();  // the sums have been read before the next part's are written
       }
-      tc_fence_before();
-      if (lane == 0) arrive_cluster(in_cta(smem_u32(&s.acc_empty[buf]), 0));
+      if (held) release();
       __syncwarp();
     }
     if (!ok && lane == 0) store_cluster(peer_abort, 1);

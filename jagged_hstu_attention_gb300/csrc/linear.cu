@@ -155,8 +155,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// Boxes of 128 bytes x box_rows of a row-major (rows, cols) operand; what lies outside
-// it reads as zeros.
+// Boxes of 128 bytes x box_rows of a row-major (rows, cols) operand; what lies outside it
+// reads as zeros.
 constexpr int kDtypeCodes = -1;  // 8-bit
 bool box_map(CUtensorMap* m, const void* ptr, int64_t rows, int64_t cols, int64_t stride, int dtype, int box_rows) {
   auto fn = encode_fn();
@@ -181,6 +181,11 @@ hstu_status_t linear_checks(int64_t rows, int d_in, int d_out, int act, bool cod
   const int64_t most = d_in > d_out ? d_in : d_out;
   if ((rows / kTileM + 1) * (most / kTileN + 1) > INT32_MAX / 2) return HSTU_ERR_UNSUPPORTED;
   return HSTU_OK;
+}
+
+// Whether a product goes to the kernel for few rows.
+bool few_rows(int64_t rows, int d_out) {
+  return rows <= kFewRows;
 }
 
 // Splits of dw's K: those that leave the fewest tiles' time on the busiest pair, counting
@@ -243,7 +248,7 @@ HSTU_API hstu_status_t hstu_attn_linear(const void* x, int64_t x_stride, const u
   const int xe = codes ? 1 : 2;
   if (rows > 0) {
     if (!aligned_to(x, 16) || x_stride < d_in || x_stride * xe % 16 != 0 || !aligned_to(w, 16) ||
-        (x_scale != nullptr) != codes || (bias && !aligned_to(bias, 16)) ||
+        (x_scale != nullptr) != codes || (codes && !aligned_to(w_scale, 16)) || (bias && !aligned_to(bias, 16)) ||
         (residual && !rows_ok(residual, residual_stride, 1, d_out)) || !aligned_to(y, 16) || (z && !aligned_to(z, 16)))
       return HSTU_ERR_INVALID_ARG;
     const int64_t yw = int64_t{d_out} * 2;
@@ -259,6 +264,26 @@ HSTU_API hstu_status_t hstu_attn_linear(const void* x, int64_t x_stride, const u
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (ws && cudaMemsetAsync(ws, 0, kHdrWords * 4, cs) != cudaSuccess) return HSTU_ERR_CUDA;
   if (rows == 0) return HSTU_OK;
+  if (few_rows(rows, d_out)) {
+    FewParams p{};
+    p.x = x;
+    p.w = w;
+    p.bias = bias;
+    p.residual = residual;
+    p.x_scale = x_scale;
+    p.w_scale = w_scale;
+    p.y = y;
+    p.z = z;
+    p.header = static_cast<int32_t*>(ws);
+    p.x_stride = x_stride * xe;
+    p.residual_stride = residual_stride;
+    p.k_bytes = int64_t{d_in} * xe;
+    p.M = static_cast<int32_t>(rows);
+    p.N = d_out;
+    p.act = act;
+    const cudaError_t e = dtype == HSTU_DTYPE_F16 ? launch_few_f16(p, codes, cs) : launch_few_bf16(p, codes, cs);
+    return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+  }
   LinearParams p{};
   const int type = codes ? kDtypeCodes : dtype;
   if (!box_map(&p.tm_a, x, rows, d_in, x_stride, type, 128) || !box_map(&p.tm_b, w, d_out, d_in, d_in, type, 128))

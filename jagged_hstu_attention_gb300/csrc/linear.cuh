@@ -2,13 +2,16 @@
 // unit of their own.
 #pragma once
 
-#include "gemm.cuh"
+#include "gemm_few.cuh"
 
 namespace hstu {
 
 // kEpiLinear with K-major operands (8-bit with f8).
 cudaError_t launch_linear_bf16(const LinearParams& p, bool f8, cudaStream_t stream);
 cudaError_t launch_linear_f16(const LinearParams& p, bool f8, cudaStream_t stream);
+// The same for few rows.
+cudaError_t launch_few_bf16(const FewParams& p, bool f8, cudaStream_t stream);
+cudaError_t launch_few_f16(const FewParams& p, bool f8, cudaStream_t stream);
 // dx = g w: A K-major, B MN-major.
 cudaError_t launch_linear_dx_bf16(const LinearParams& p, cudaStream_t stream);
 cudaError_t launch_linear_dx_f16(const LinearParams& p, cudaStream_t stream);
@@ -36,6 +39,9 @@ cudaError_t launch_pair_gemm(const LinearParams& p, cudaStream_t stream) {
   cudaError_t launch_linear_##SUFFIX(const LinearParams& p, bool f8, cudaStream_t stream) {                 \
     return f8 ? launch_pair_gemm<T, true, false, false, kEpiLinear>(p, stream)                              \
               : launch_pair_gemm<T, false, false, false, kEpiLinear>(p, stream);                            \
+  }                                                                                                         \
+  cudaError_t launch_few_##SUFFIX(const FewParams& p, bool f8, cudaStream_t stream) {                       \
+    return f8 ? launch_few<T, true>(p, stream) : launch_few<T, false>(p, stream);                           \
   }                                                                                                         \
   cudaError_t launch_linear_dx_##SUFFIX(const LinearParams& p, cudaStream_t stream) {                       \
     return launch_pair_gemm<T, false, false, true, kEpiPlain>(p, stream);                                   \
