@@ -822,6 +822,13 @@ class QuantisedRows:
         self.codes, self.scale = codes, scale
 
 
+def _quantised(codes, scale) -> QuantisedRows:
+    """One of the extension's own outputs, which need no checks."""
+    q = object.__new__(QuantisedRows)
+    q.codes, q.scale = codes, scale
+    return q
+
+
 def quantise_rows(x, stream=None) -> QuantisedRows:
     """x (rows, width) as 8-bit floats under a power of two for each row
     (hstu_attn_quantise_rows); a weight of ``linear`` once, before it is used."""
@@ -831,7 +838,7 @@ def quantise_rows(x, stream=None) -> QuantisedRows:
     r = load_extension().quantise_rows(x)
     if type(r) is int:
         _check(r, "hstu_attn_quantise_rows")
-    return QuantisedRows(*r)
+    return _quantised(*r)
 
 
 def rms_norm(x, weight, residual=None, gate=None, eps: float = 1e-6, quantise: bool = False, want_rstd: bool = True,
@@ -852,7 +859,7 @@ def rms_norm(x, weight, residual=None, gate=None, eps: float = 1e-6, quantise: b
     if type(r) is int:
         _check(r, "hstu_attn_rms_norm")
     y, s, h, rstd = r
-    return (y if s is None else QuantisedRows(y, s)), h, rstd
+    return (y if s is None else _quantised(y, s)), h, rstd
 
 
 def rms_norm_workspace(rows: int, width: int, device="cuda") -> torch.Tensor:

@@ -31,11 +31,12 @@ constexpr int kSortWarps = 16, kSortThreads = 32 * kSortWarps;
 constexpr int kMaxDigitBits = 9, kMaxBins = 1 << kMaxDigitBits;
 constexpr int kSortTiles = 152;  // at most one tile an SM
 constexpr int kSeenBits = 10, kSeen = 1 << kSeenBits;
-constexpr int kFillBytes = 1 << 16;  // of the table that a zeroing block looks after, about
-// What a sorting launch zeroes on the side, at most: about what the GPU writes in its time.
-constexpr int64_t kFillMove = 48 << 20, kFillCount = 16 << 20;
-constexpr int kJoinThreads = 1024, kJoinChunks = 32;  // chunks a joining block looks after
+constexpr int kFillBytes = 1 << 17;     // of the table that a zeroing block looks after, about
+constexpr int kFillMostRows = 1 << 13;  // of them (rows are 16 bytes at least)
+constexpr int kJoinThreads = 1024, kJoinBlocks = 152;  // as many again for short runs
 constexpr int kShortRun = 16;  // chunks of a run that one group of threads joins alone
+// Header words: the long runs found, those of at most kShortRun chunks and the others.
+constexpr int kHdrShort = 1, kHdrLong = 2;
 
 // ------------------------------------------------------------------ forward
 
@@ -45,8 +46,9 @@ struct EmbedParams {
   void* out;
   int32_t* header;  // null: bad ids are not reported
   int64_t vocab, tokens;
-  int32_t chunks;  // 8-column chunks of a row
-  int32_t rows;    // rows of a block
+  uint64_t per_chunk;  // 2^32 / chunks, rounded up: u per_chunk / 2^32 is u / chunks for what a block has
+  int32_t chunks;      // 8-column chunks of a row, 2^13 at most
+  int32_t rows;        // rows of a block
   float scale;
 };
 
@@ -62,10 +64,12 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_kernel(const EmbedParams 
   T* out = static_cast<T*>(p.out) + t0 * p.chunks * 8;
   for (uint32_t u0 = threadIdx.x; u0 < units; u0 += U * kEmbedThreads) {
     int64_t id[U];
+    uint32_t row[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const uint32_t u = u0 + i * kEmbedThreads;
-      id[i] = u < units ? static_cast<int64_t>(ids[u / p.chunks]) : -1;
+      row[i] = static_cast<uint32_t>(u * p.per_chunk >> 32);
+      id[i] = u < units ? static_cast<int64_t>(ids[row[i]]) : -1;
     }
     float f[U][8];
 #pragma unroll
@@ -73,7 +77,7 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_kernel(const EmbedParams 
       const uint32_t u = u0 + i * kEmbedThreads;
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[i][e] = 0.0f;
-      if (id[i] >= 0 && id[i] < p.vocab) load8(table + (id[i] * p.chunks + u % p.chunks) * 8, f[i]);
+      if (id[i] >= 0 && id[i] < p.vocab) load8(table + (id[i] * p.chunks + (u - row[i] * p.chunks)) * 8, f[i]);
       else if (id[i] >= p.vocab && p.header) atomicOr(p.header + kHdrErr, kErrInput);
     }
 #pragma unroll
@@ -96,6 +100,7 @@ cudaError_t launch_embed(EmbedParams p, cudaStream_t stream) {
   const int64_t per_block = kEmbedThreads * (many ? 4 : 1);
   const int64_t rows = per_block / p.chunks;
   p.rows = static_cast<int32_t>(rows < 1 ? 1 : rows);
+  p.per_chunk = ((uint64_t{1} << 32) + p.chunks - 1) / p.chunks;
   const dim3 grid(static_cast<unsigned>((p.tokens + p.rows - 1) / p.rows));
   return launch_chained(many ? embed_kernel<TT, T, ID, 4> : embed_kernel<TT, T, ID, 1>, grid, kEmbedThreads, 0, stream, p);
 }
@@ -115,21 +120,26 @@ struct FillParams {
   void* table;
   const uint32_t* named;  // a bit a row
   int64_t row0, row1;
-  int32_t units;  // of a row
-  int32_t rows;   // of a block
+  uint64_t per_unit;  // 2^32 / units, rounded up: u per_unit / 2^32 is u / units for what a block has
+  int32_t units;      // of a row, 2^14 at most
+  int32_t rows;       // of a block
 };
 __host__ __device__ inline int64_t fill_blocks(const FillParams& p) {
   return p.row1 > p.row0 ? (p.row1 - p.row0 + p.rows - 1) / p.rows : 0;
 }
 __device__ __forceinline__ void fill_rows(const FillParams& p, int64_t block) {
-  const int threads = blockDim.x, group = min(threads, p.units), groups = threads / group, g = threadIdx.x / group;
-  if (g >= groups) return;
-  const int64_t v0 = p.row0 + block * p.rows, v1 = min(v0 + p.rows, p.row1);
+  __shared__ uint32_t bits[kFillMostRows / 32 + 1];
+  const int64_t v0 = p.row0 + block * p.rows, v1 = min(v0 + p.rows, p.row1), w0 = v0 >> 5;
+  // The rows' bits first, so that no store waits for a load.
+  for (int64_t w = w0 + threadIdx.x; w <= (v1 - 1) >> 5; w += blockDim.x) bits[w - w0] = p.named[w];
+  __syncthreads();
+  const uint32_t units = static_cast<uint32_t>(v1 - v0) * p.units, first = static_cast<uint32_t>(v0 & 31);
+  uint4* base = static_cast<uint4*>(p.table) + v0 * p.units;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int64_t v = v0 + g; v < v1; v += groups) {
-    if ((p.named[v >> 5] >> (v & 31)) & 1u) continue;
-    uint4* row = static_cast<uint4*>(p.table) + v * p.units;
-    for (int u = threadIdx.x % group; u < p.units; u += group) row[u] = zero;
+#pragma unroll 4
+  for (uint32_t u = threadIdx.x; u < units; u += blockDim.x) {
+    const uint32_t v = first + static_cast<uint32_t>(u * p.per_unit >> 32);
+    if (((bits[v >> 5] >> (v & 31)) & 1u) == 0) base[u] = zero;
   }
 }
 
@@ -174,6 +184,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortPara
     for (int b = threadIdx.x; b < kSeen; b += kSortThreads) seen[b] = 0xffffffffu;
   __syncthreads();
   const int64_t i0 = static_cast<int64_t>(blockIdx.x) * p.tile, i1 = min(i0 + p.tile, p.n);
+#pragma unroll 4
   for (int64_t i = i0 + threadIdx.x; i < i1; i += kSortThreads) {
     const uint32_t key = sort_key<ID, FIRST>(p, i);
     atomicAdd(&count[(key >> p.shift) & (bins - 1)], 1u);
@@ -287,6 +298,8 @@ struct SumParams {
   const int32_t* val;   // their tokens
   void* dtable;
   float* part;  // (chunks, 2, dim): sums of long runs' chunks; [0] of a run from an earlier chunk, [1] of one that begins
+  int32_t* header;
+  int32_t* runs;  // first whole chunks: of short runs from the front, of others from the back
   int64_t n, vocab;
   int32_t chunk, chunks, dim, accumulate;
   int32_t sum_blocks;  // blocks that sum, spread evenly among those that zero
@@ -315,7 +328,7 @@ __device__ __forceinline__ void put_row(const SumParams& p, int64_t row, int col
 }
 
 template <typename T, typename G>
-__global__ void __launch_bounds__(kEmbedThreads) embed_sum_kernel(const SumParams p) {
+__global__ void __launch_bounds__(kEmbedThreads, 4) embed_sum_kernel(const SumParams p) {
   chain();
   const int64_t summed = static_cast<int64_t>(blockIdx.x) * p.sum_blocks / gridDim.x;  // summing blocks before this one
   if ((static_cast<int64_t>(blockIdx.x) + 1) * p.sum_blocks / gridDim.x == summed) {
@@ -351,6 +364,13 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_sum_kernel(const SumParam
   }
   // A whole chunk whose run is no longer than it: an ordinary row.
   const bool alone = whole && !from_before && (end == p.n || p.key[end] != first);
+  // The first whole chunk of a run lists it for the join. (In whatever order: each
+  // run is added up by itself.)
+  if (whole && !alone && !(from_before && one_id(p, c - 1, first)) && blockIdx.y == 0 && threadIdx.x % group == 0) {
+    const bool brief = c + kShortRun >= p.chunks || p.key[(c + kShortRun) * p.chunk] != first;
+    const int at = atomicAdd(p.header + (brief ? kHdrShort : kHdrLong), 1);
+    p.runs[brief ? at : p.chunks - 1 - at] = static_cast<int32_t>(c);
+  }
   const T* dy = static_cast<const T*>(p.dy) + col;
   float acc[8] = {};
   uint32_t cur = i < i1 ? p.key[i] : 0xffffffffu;
@@ -364,36 +384,46 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_sum_kernel(const SumParam
       put_row<G>(p, row, col, acc);
     }
   };
+  // Four rows at a time; their ids and tokens are read while the four before are added.
   constexpr int kAhead = 4;
-  while (i < i1) {
-    uint32_t key[kAhead];
-    uint4 v[kAhead];
-    const int m = static_cast<int>(min(static_cast<int64_t>(kAhead), i1 - i));
+  uint32_t key[kAhead], next_key[kAhead];
+  int32_t val[kAhead], next_val[kAhead];
+  auto read_ids = [&](int64_t at, uint32_t (&k)[kAhead], int32_t (&t)[kAhead]) {
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
-      key[a] = a < m ? p.key[i + a] : 0xffffffffu;
-      if (a < m && key[a] < p.vocab)
-        v[a] = *reinterpret_cast<const uint4*>(dy + static_cast<int64_t>(p.val[i + a]) * p.dy_stride);
+      k[a] = at + a < i1 ? p.key[at + a] : 0xffffffffu;
+      t[a] = at + a < i1 ? p.val[at + a] : 0;
     }
+  };
+  read_ids(i, key, val);
+  while (i < i1) {
+    uint4 v[kAhead];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a)
+      if (key[a] < p.vocab) v[a] = *reinterpret_cast<const uint4*>(dy + static_cast<int64_t>(val[a]) * p.dy_stride);
+    read_ids(i + kAhead, next_key, next_val);
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
-      if (a >= m) break;
-      if (key[a] != cur) {
+      if (key[a] != cur) {  // past the last token too
         flush(cur);
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
         cur = key[a];
       }
-      if (key[a] >= p.vocab) break;
+      if (key[a] >= p.vocab) return;  // padding sorts last
       float f[8];
       unpack8<T>(v[a], f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) acc[e] += f[e];
     }
-    i += m;
-    if (cur >= p.vocab) return;  // padding sorts last
+    i += kAhead;
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      key[a] = next_key[a];
+      val[a] = next_val[a];
+    }
   }
-  if (i0 < i1) flush(cur);
+  flush(cur);
 }
 
 // Adds up the chunks of each long run: the end of the chunk before its first
@@ -404,29 +434,7 @@ template <typename G>
 __global__ void __launch_bounds__(kJoinThreads) embed_join_kernel(const SumParams p) {
   chain();
   __shared__ float slice[kJoinThreads][8];
-  __shared__ int64_t first[kJoinChunks];
-  __shared__ int runs[2];  // found; short ones among them, listed from the front, the others from the back
-  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kJoinChunks;
-  if (threadIdx.x < 32) {
-    const int64_t c = c0 + threadIdx.x;
-    bool is = false, brief = false;
-    if (c < p.chunks) {
-      const int64_t i0 = c * p.chunk, end = min(i0 + p.chunk, p.n);
-      const uint32_t key = p.key[i0];
-      const bool before = i0 > 0 && p.key[i0 - 1] == key, after = end < p.n && p.key[end] == key;
-      is = key < p.vocab && p.key[end - 1] == key && (before || after) && !(c > 0 && one_id(p, c - 1, key));
-      brief = c + kShortRun >= p.chunks || p.key[(c + kShortRun) * p.chunk] != key;
-    }
-    const uint32_t small = __ballot_sync(0xffffffffu, is && brief), large = __ballot_sync(0xffffffffu, is && !brief);
-    const uint32_t below = (1u << threadIdx.x) - 1u;
-    if (is && brief) first[__popc(small & below)] = c;
-    if (is && !brief) first[kJoinChunks - 1 - __popc(large & below)] = c;
-    if (threadIdx.x == 0) {
-      runs[0] = __popc(small);
-      runs[1] = __popc(large);
-    }
-  }
-  __syncthreads();
+  const int brief = p.header[kHdrShort], large = p.header[kHdrLong];
   const int col0 = blockIdx.y * kEmbedThreads * 8;
   const int group = min(kEmbedThreads, (p.dim - col0) / 8);
   const int groups = kJoinThreads / group, g = threadIdx.x / group;
@@ -444,8 +452,8 @@ __global__ void __launch_bounds__(kJoinThreads) embed_join_kernel(const SumParam
   };
   auto from_before = [&](int64_t c, uint32_t key) { return c > 0 && p.key[c * p.chunk - 1] == key; };
   if (g < groups)
-    for (int k = g; k < runs[0]; k += groups) {
-      const int64_t c = first[k];
+    for (int k = (blockIdx.x - kJoinBlocks) * groups + g; blockIdx.x >= kJoinBlocks && k < brief; k += kJoinBlocks * groups) {
+      const int64_t c = p.runs[k];
       const uint32_t key = p.key[c * p.chunk];
       int parts = 1;
       bool on = true;
@@ -458,8 +466,9 @@ __global__ void __launch_bounds__(kJoinThreads) embed_join_kernel(const SumParam
       sum_of(c, c + parts, from_before(c, key), acc);
       put_row<G>(p, key, col, acc);
     }
-  for (int k = 0; k < runs[1]; ++k) {
-    const int64_t c = first[kJoinChunks - 1 - k];
+  if (blockIdx.x >= kJoinBlocks) return;
+  for (int k = blockIdx.x; k < large; k += kJoinBlocks) {
+    const int64_t c = p.runs[p.chunks - 1 - k];
     const uint32_t key = p.key[c * p.chunk];
     // The last chunk that begins with the id: all threads look, at a step that
     // shrinks a thousandfold.
@@ -505,9 +514,9 @@ int sum_chunk(int64_t n, int dim) {
 }
 
 // Workspace: a 256-byte header (error word), a bit a row of the table, the two
-// buffers of (id, token), the digits' counts, and the long runs' sums.
+// buffers of (id, token), the digits' counts, and the long runs' list and sums.
 struct EmbedLayout {
-  size_t named = 0, key[2] = {}, val[2] = {}, counts = 0, part = 0, total = 0;
+  size_t named = 0, key[2] = {}, val[2] = {}, counts = 0, runs = 0, part = 0, total = 0;
 };
 EmbedLayout embed_layout(int64_t n, int64_t vocab, int dim) {
   EmbedLayout l;
@@ -521,22 +530,28 @@ EmbedLayout embed_layout(int64_t n, int64_t vocab, int dim) {
   }
   l.counts = at;
   at += static_cast<size_t>(kSortTiles) * kMaxBins * 4;
-  l.part = at;
   const int c = sum_chunk(n, dim);
-  at += align_up(static_cast<size_t>((n + c - 1) / c) * 2 * dim * 4, 256);
+  const size_t chunks = static_cast<size_t>((n + c - 1) / c);
+  l.runs = at;
+  at += align_up(chunks * 4, 256);
+  l.part = at;
+  at += align_up(chunks * 2 * dim * 4, 256);
   l.total = at;
   return l;
 }
 
-// Takes at most `bytes` of the rows still to be zeroed, and a quarter of `all` rows.
-FillParams fill_share(FillParams& rest, int64_t bytes, int64_t all) {
+// Takes `part` of `parts` of the table's rows from those still to be zeroed.
+FillParams fill_share(FillParams& rest, int64_t rows, int part, int parts) {
   FillParams f = rest;
-  const int64_t rows = std::min(bytes / (int64_t{16} * f.units), all / 4);
-  f.row1 = std::min(f.row0 + std::max<int64_t>(rows, 0), rest.row1);
+  f.row1 = std::min(f.row0 + rows * part / parts, rest.row1);
   rest.row0 = f.row1;
   return f;
 }
 
+// The launches that follow the first zero rows on the side: a move twice as many as
+// a count, which is about half as long, and the summing kernel, whose blocks hold more
+// registers and so write less at a time, as many as a move. (Zeroing 410 MB beside a
+// sort of 81920 tokens takes as long as the zeros alone.)
 // Leaves the rows still to be zeroed in `fill`.
 template <typename ID>
 cudaError_t launch_sort(SortParams p, FillParams& fill, uint8_t* base, const EmbedLayout& l, int& last,
@@ -546,6 +561,7 @@ cudaError_t launch_sort(SortParams p, FillParams& fill, uint8_t* base, const Emb
   while ((p.vocab >> bits) != 0) ++bits;  // of the largest key, vocab
   const int passes = (bits + kMaxDigitBits - 1) / kMaxDigitBits;
   p.bits = (bits + passes - 1) / passes;
+  const int parts = 2 * passes + (passes - 1) + 2;
   const int64_t rounds = (p.n + int64_t{kSortTiles} * kSortThreads - 1) / (int64_t{kSortTiles} * kSortThreads);
   p.tile = static_cast<int32_t>(rounds * kSortThreads);
   p.tiles = static_cast<int32_t>((p.n + p.tile - 1) / p.tile);
@@ -555,12 +571,11 @@ cudaError_t launch_sort(SortParams p, FillParams& fill, uint8_t* base, const Emb
     p.val_in = reinterpret_cast<const int32_t*>(base + l.val[s & 1]);
     p.key_out = reinterpret_cast<uint32_t*>(base + l.key[(s + 1) & 1]);
     p.val_out = reinterpret_cast<int32_t*>(base + l.val[(s + 1) & 1]);
-    // (the rows' bits are set by the first launch)
-    p.fill = fill_share(fill, s == 0 ? 0 : kFillCount, all);
+    p.fill = fill_share(fill, all, s == 0 ? 0 : 1, parts);  // (the first launch sets the rows' bits)
     cudaError_t e = launch_chained(s == 0 ? sort_count_kernel<ID, true> : sort_count_kernel<ID, false>,
                                    dim3(static_cast<unsigned>(p.tiles + fill_blocks(p.fill))), kSortThreads, 0, stream, p);
     if (e != cudaSuccess) return e;
-    p.fill = fill_share(fill, kFillMove, all);
+    p.fill = fill_share(fill, all, 2, parts);
     e = launch_chained(s == 0 ? sort_move_kernel<ID, true> : sort_move_kernel<ID, false>,
                        dim3(static_cast<unsigned>(p.tiles + fill_blocks(p.fill))), kSortThreads, 0, stream, p);
     if (e != cudaSuccess) return e;
@@ -578,8 +593,7 @@ cudaError_t launch_sum(SumParams p, cudaStream_t stream) {
   cudaError_t e = launch_chained(embed_sum_kernel<T, G>, dim3(static_cast<unsigned>(p.sum_blocks + fill_blocks(p.fill)), ny),
                                  kEmbedThreads, 0, stream, p);
   if (e != cudaSuccess) return e;
-  return launch_chained(embed_join_kernel<G>, dim3((p.chunks + kJoinChunks - 1) / kJoinChunks, ny), kJoinThreads, 0,
-                        stream, p);
+  return launch_chained(embed_join_kernel<G>, dim3(2 * kJoinBlocks, ny), kJoinThreads, 0, stream, p);
 }
 template <typename T>
 cudaError_t launch_sum_typed(const SumParams& p, int grad_dtype, cudaStream_t stream) {
@@ -666,7 +680,8 @@ HSTU_API hstu_status_t hstu_attn_embed_bwd(const void* dy, int64_t dy_stride, in
   fill.named = reinterpret_cast<const uint32_t*>(base + l.named);
   fill.row1 = accumulate ? 0 : vocab;
   fill.units = dim / (grad_dtype == HSTU_DTYPE_F32 ? 4 : 8);
-  fill.rows = std::max(1, kFillBytes / (16 * fill.units));
+  fill.per_unit = ((uint64_t{1} << 32) + fill.units - 1) / fill.units;
+  fill.rows = std::max(1, std::min(kFillBytes / (16 * fill.units), kFillMostRows));
   if (tokens == 0) {
     if (accumulate) return HSTU_OK;
     e = launch_chained(embed_zero_kernel, dim3(static_cast<unsigned>(fill_blocks(fill))), kEmbedThreads, 0, cs, fill);
@@ -691,6 +706,8 @@ HSTU_API hstu_status_t hstu_attn_embed_bwd(const void* dy, int64_t dy_stride, in
   p.fill = fill;
   p.dtable = dtable;
   p.part = reinterpret_cast<float*>(base + l.part);
+  p.header = reinterpret_cast<int32_t*>(base);
+  p.runs = reinterpret_cast<int32_t*>(base + l.runs);
   p.n = tokens;
   p.vocab = vocab;
   p.dim = dim;

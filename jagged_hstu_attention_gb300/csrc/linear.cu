@@ -20,7 +20,7 @@ namespace {
 constexpr int kGradThreads = 256;
 // Rows are split into at most kGradChunks chunks of at least kGradMinRows (one block
 // each); a chunk's column sums are the bias gradient's parts.
-constexpr int kGradChunks = 1216, kGradMinRows = 32;
+constexpr int kGradChunks = 152 * 4, kGradMinRows = 32;
 constexpr int kMaxKSplits = 16;
 constexpr int kPairs = 76;
 
@@ -85,14 +85,18 @@ __global__ void __launch_bounds__(kGradThreads) linear_grad_kernel(const GradPar
       return p.z ? *reinterpret_cast<const uint4*>(z + r * p.cols) : make_uint4(0, 0, 0, 0);
     };
     int64_t r = r0 + lane_row;
-    for (; r + rpi < r1; r += 2 * rpi) {
-      const uint4 z0 = load_z(r), z1 = load_z(r + rpi);
-      const uint4 d0 = *reinterpret_cast<const uint4*>(dy + r * p.dy_stride);
-      const uint4 d1 = *reinterpret_cast<const uint4*>(dy + (r + rpi) * p.dy_stride);
-      one(z0, d0, r);
-      one(z1, d1, r + rpi);
+    constexpr int kRows = 4;
+    for (; r + (kRows - 1) * rpi < r1; r += kRows * rpi) {
+      uint4 zv[kRows], dv[kRows];
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        zv[k] = load_z(r + k * rpi);
+        dv[k] = *reinterpret_cast<const uint4*>(dy + (r + k * rpi) * p.dy_stride);
+      }
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) one(zv[k], dv[k], r + k * rpi);
     }
-    if (r < r1) one(load_z(r), *reinterpret_cast<const uint4*>(dy + r * p.dy_stride), r);
+    for (; r < r1; r += rpi) one(load_z(r), *reinterpret_cast<const uint4*>(dy + r * p.dy_stride), r);
   }
 #pragma unroll
   for (int e = 0; e < 8; ++e) red[threadIdx.x][e] = sum[e];

@@ -17,6 +17,8 @@
 // above 1024 columns, shared memory. Sums are in 32 bits. The backward's blocks
 // take rows in turn and keep their part of dweight in registers; the blocks'
 // parts are added in order by a second kernel (no atomics).
+#include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "cache.cuh"
@@ -47,6 +49,7 @@ struct NormParams {
 };
 
 // Sum or maximum over the RT threads of a row; every thread of the block calls it.
+// `shared` has a value for each warp and is not in use by the reduction before.
 template <int RT, bool MAX>
 __device__ __forceinline__ float row_reduce(float v, float* shared) {
   auto join = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
@@ -55,7 +58,6 @@ __device__ __forceinline__ float row_reduce(float v, float* shared) {
   if (RT <= 32) return v;
   constexpr int kWarps = RT < 32 ? 1 : RT / 32;
   const int warp = threadIdx.x >> 5, first = warp / kWarps * kWarps;
-  __syncthreads();  // the values of the reduction before this one have been read
   if ((threadIdx.x & 31) == 0) shared[warp] = v;
   __syncthreads();
   v = shared[first];
@@ -71,7 +73,7 @@ constexpr int norm_threads() { return RT > 128 ? RT : 128; }
 template <typename T, int RT, int V, int OUT>
 __global__ void __launch_bounds__(norm_threads<RT>()) norm_kernel(const NormParams p) {
   chain();
-  __shared__ float shared[RT > 32 ? norm_threads<RT>() / 32 : 1];
+  __shared__ float shared[2][RT > 32 ? norm_threads<RT>() / 32 : 1];
   const int t = threadIdx.x % RT;
   const int64_t r = static_cast<int64_t>(blockIdx.x) * (norm_threads<RT>() / RT) + threadIdx.x / RT;
   const bool live = r < p.rows;
@@ -109,7 +111,7 @@ __global__ void __launch_bounds__(norm_threads<RT>()) norm_kernel(const NormPara
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum = fmaf(f[e], f[e], sum);
     }
-    sum = row_reduce<RT, false>(sum, shared);
+    sum = row_reduce<RT, false>(sum, shared[0]);
     rstd = 1.0f / sqrtf(sum / static_cast<float>(p.width) + p.eps);
     if (p.rstd && live && t == 0) p.rstd[r] = rstd;
   }
@@ -141,7 +143,7 @@ __global__ void __launch_bounds__(norm_threads<RT>()) norm_kernel(const NormPara
     }
   }
   if (OUT == kNorm16) return;
-  top = row_reduce<RT, true>(top, shared);
+  top = row_reduce<RT, true>(top, shared[1]);
   const uint32_t byte = scale_byte(top);
   const float inv = __uint_as_float((254u - byte) << 23);  // 2^(127 - byte), exact
 #pragma unroll
@@ -179,7 +181,7 @@ template <typename T, int RT, int V, bool GATE>
 __global__ void __launch_bounds__(norm_bwd_threads<RT>()) norm_bwd_kernel(const NormBwdParams p) {
   chain();
   constexpr int kThreads = norm_bwd_threads<RT>(), kGroups = kThreads / RT;
-  __shared__ float shared[kThreads / 32];
+  __shared__ float shared[2][kThreads / 32];  // in turn: one barrier a row
   __shared__ float red[kGroups > 1 ? RT * V * 8 : 1];
   const int t = threadIdx.x % RT, group = threadIdx.x / RT;
   uint4 wv[V];
@@ -194,8 +196,9 @@ __global__ void __launch_bounds__(norm_bwd_threads<RT>()) norm_bwd_kernel(const 
   }
   const float inv_width = 1.0f / static_cast<float>(p.width);
   // All groups of a block go around together: the reduction has barriers.
+  int turn = 0;
   for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kGroups; r0 < p.rows;
-       r0 += static_cast<int64_t>(gridDim.x) * kGroups) {
+       r0 += static_cast<int64_t>(gridDim.x) * kGroups, turn ^= 1) {
     const int64_t r = r0 + group;
     const bool live = r < p.rows;
     uint4 dv[V], hv[V], gv[V], ev[V];
@@ -229,7 +232,7 @@ __global__ void __launch_bounds__(norm_bwd_threads<RT>()) norm_bwd_kernel(const 
       const int col = (t + i * RT) * 8;
       if (GATE && live && col < p.width) store8(static_cast<T*>(p.dgate) + r * p.width + col, d);
     }
-    const float mean = row_reduce<RT, false>(sum, shared) * inv_width;
+    const float mean = row_reduce<RT, false>(sum, shared[turn]) * inv_width;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int col = (t + i * RT) * 8;
@@ -297,10 +300,13 @@ __global__ void __launch_bounds__(1024) norm_fold_kernel(const float* part, int 
   }
 }
 
-// Threads of a row and chunks a thread: the fewest threads whose registers hold the
-// row, so that reductions stay inside a warp up to 1024 columns; 8 and 16 threads
-// for heads, where a whole warp would leave most of its lanes without columns.
-template <typename F>
+// Threads of a row and chunks a thread. Forward: the fewest threads whose registers
+// hold the row, so that reductions stay inside a warp up to 1024 columns; 8 and 16
+// threads for heads, where a whole warp would leave most of its lanes without columns.
+// The backward holds up to four rows and its part of dweight besides: one or two
+// chunks a thread, so that several blocks fit an SM (32749 rows of 1024, with a gate:
+// 72 us with four chunks a lane and one block an SM).
+template <bool BACKWARD, typename F>
 cudaError_t by_width(int width, F&& f) {
   using std::integral_constant;
   auto call = [&](auto rt, auto v) { return f(rt, v); };
@@ -308,15 +314,22 @@ cudaError_t by_width(int width, F&& f) {
   if (width <= 128) return call(integral_constant<int, 16>{}, integral_constant<int, 1>{});
   if (width <= 256) return call(integral_constant<int, 32>{}, integral_constant<int, 1>{});
   if (width <= 512) return call(integral_constant<int, 32>{}, integral_constant<int, 2>{});
-  if (width <= 1024) return call(integral_constant<int, 32>{}, integral_constant<int, 4>{});
-  if (width <= 2048) return call(integral_constant<int, 128>{}, integral_constant<int, 2>{});
-  if (width <= 4096) return call(integral_constant<int, 128>{}, integral_constant<int, 4>{});
-  return call(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+  if constexpr (BACKWARD) {
+    if (width <= 1024) return call(integral_constant<int, 128>{}, integral_constant<int, 1>{});
+    if (width <= 2048) return call(integral_constant<int, 256>{}, integral_constant<int, 1>{});
+    if (width <= 4096) return call(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+    return call(integral_constant<int, 512>{}, integral_constant<int, 2>{});
+  } else {
+    if (width <= 1024) return call(integral_constant<int, 32>{}, integral_constant<int, 4>{});
+    if (width <= 2048) return call(integral_constant<int, 256>{}, integral_constant<int, 1>{});
+    if (width <= 4096) return call(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+    return call(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+  }
 }
 
 template <typename T, int OUT>
 cudaError_t launch_norm(const NormParams& p, cudaStream_t stream) {
-  return by_width(p.width, [&](auto rt, auto v) {
+  return by_width<false>(p.width, [&](auto rt, auto v) {
     constexpr int RT = decltype(rt)::value, V = decltype(v)::value;
     constexpr int per = norm_threads<RT>() / RT;
     return launch_chained(norm_kernel<T, RT, V, OUT>, dim3(static_cast<unsigned>((p.rows + per - 1) / per)),
@@ -331,13 +344,21 @@ cudaError_t launch_norm_typed(const NormParams& p, int dtype, cudaStream_t strea
 template <typename T>
 cudaError_t launch_norm_bwd(const NormBwdParams& p, void* dweight, cudaStream_t stream) {
   int blocks = 0;
-  cudaError_t e = by_width(p.width, [&](auto rt, auto v) {
+  cudaError_t e = by_width<true>(p.width, [&](auto rt, auto v) {
     constexpr int RT = decltype(rt)::value, V = decltype(v)::value;
     constexpr int threads = norm_bwd_threads<RT>(), per = threads / RT;
-    const int64_t want = (p.rows + per - 1) / per;
-    blocks = static_cast<int>(want < kNormMaxBlocks ? want : kNormMaxBlocks);
-    return launch_chained(p.gate ? norm_bwd_kernel<T, RT, V, true> : norm_bwd_kernel<T, RT, V, false>, dim3(blocks),
-                          threads, 0, stream, p);
+    auto kernel = p.gate ? norm_bwd_kernel<T, RT, V, true> : norm_bwd_kernel<T, RT, V, false>;
+    // as many blocks as run at a time
+    static std::atomic<int> resident[2];
+    int fit = resident[p.gate != nullptr].load();
+    if (fit == 0) {
+      const cudaError_t q = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, threads, 0);
+      if (q != cudaSuccess) return q;
+      fit = std::max(1, std::min(fit, kNormMaxBlocks / 152));
+      resident[p.gate != nullptr].store(fit);
+    }
+    blocks = static_cast<int>(std::min<int64_t>((p.rows + per - 1) / per, 152 * fit));
+    return launch_chained(kernel, dim3(blocks), threads, 0, stream, p);
   });
   if (e != cudaSuccess) return e;
   return launch_chained(norm_fold_kernel<T>, dim3((p.width + 31) / 32), 1024, 0, stream,
