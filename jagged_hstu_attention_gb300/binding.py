@@ -841,11 +841,12 @@ def quantise_rows(x, stream=None) -> QuantisedRows:
     return _quantised(*r)
 
 
-def rms_norm(x, weight, residual=None, gate=None, eps: float = 1e-6, quantise: bool = False, want_rstd: bool = True,
-             outs=None, stream=None):
+def rms_norm(x, weight, residual=None, gate=None, eps: float = 1e-6, quantise: bool = False,
+             want_rstd: Optional[bool] = None, outs=None, stream=None):
     """(y, h, rstd): h = x + residual (None without one), rstd = 1 / rms(h) and
     y = h * rstd * weight * gate (hstu_attn_rms_norm). y is QuantisedRows with
-    ``quantise``. ``outs`` may be (y, h), either None; h may be the residual
+    ``quantise``; rstd, which the backward reads, is then None unless asked for.
+    ``outs`` may be (y, h), either None; h may be the residual
     itself, which is then updated in place."""
     if stream is not None:
         with torch.cuda.stream(stream):
@@ -855,7 +856,8 @@ def rms_norm(x, weight, residual=None, gate=None, eps: float = 1e-6, quantise: b
         y, s = y.codes, y.scale
     else:
         s = None
-    r = load_extension().rms_norm(x, weight, residual, gate, eps, bool(quantise), bool(want_rstd), y, s, h)
+    rstd = not quantise if want_rstd is None else bool(want_rstd)
+    r = load_extension().rms_norm(x, weight, residual, gate, eps, bool(quantise), rstd, y, s, h)
     if type(r) is int:
         _check(r, "hstu_attn_rms_norm")
     y, s, h, rstd = r

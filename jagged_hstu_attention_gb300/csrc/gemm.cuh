@@ -189,38 +189,40 @@ __device__ __forceinline__ float reciprocal_fast(float x) {
   return y;
 }
 
-// x / (1 + exp(-u)) of a pair: u = x is SiLU; u = 2 sqrt(2 / pi) (x + 0.044715 x^3) the tanh
+// 1 / (1 + exp(-u)) of a pair; times x, u = x is SiLU, u = 2 sqrt(2 / pi) (x + 0.044715 x^3) the tanh
 // form of GELU. The exponentials are of base 2, their arguments m u, m = -log2(e),
 // at most 60 so that the product of the two sums below stays finite (past it the
-// result is 2^-60 x, for what is nearer to 0). One reciprocal serves both: 1 / a =
+// result is 2^-60, for what is nearer to 0). One reciprocal serves both: 1 / a =
 // b / (a b). (ex2 runs at 32 a cycle and SM, rcp at 16.)
 constexpr float kGeluA = 1.5957691216057308f, kGeluB = 0.044715f;  // 2 sqrt(2 / pi)
 constexpr float kLog2e = 1.4426950408889634f;
 template <int ACT>
-__device__ __forceinline__ uint64_t activate2(uint64_t x) {
-  if (ACT == HSTU_ACT_NONE) return x;
-  float a, b;
-  if (ACT == HSTU_ACT_RELU) {
-    pair_split(x, a, b);
-    asm("max.NaN.f32 %0, %0, 0f00000000;" : "+f"(a));
-    asm("max.NaN.f32 %0, %0, 0f00000000;" : "+f"(b));
-    return pair_of(a, b);
-  }
+__device__ __forceinline__ uint64_t sigmoid_of(uint64_t x) {
   uint64_t m;
   if (ACT == HSTU_ACT_SILU) {
     m = pair_mul(x, pair_of(-kLog2e, -kLog2e));
   } else {
-    const uint64_t sq = pair_mul(x, x);
-    const uint64_t poly = pair_fma(sq, pair_of(-kLog2e * kGeluA * kGeluB, -kLog2e * kGeluA * kGeluB),
+    const uint64_t poly = pair_fma(pair_mul(x, x), pair_of(-kLog2e * kGeluA * kGeluB, -kLog2e * kGeluA * kGeluB),
                                    pair_of(-kLog2e * kGeluA, -kLog2e * kGeluA));
     m = pair_mul(x, poly);
   }
+  float a, b;
   pair_split(m, a, b);
   asm("min.NaN.f32 %0, %0, 0f42700000;" : "+f"(a));
   asm("min.NaN.f32 %0, %0, 0f42700000;" : "+f"(b));
   pair_split(pair_add(pair_of(exp2_fast(a), exp2_fast(b)), pair_of(1.0f, 1.0f)), a, b);
   const float r = reciprocal_fast(a * b);
-  return pair_mul(x, pair_mul(pair_of(r, r), pair_of(b, a)));
+  return pair_mul(pair_of(r, r), pair_of(b, a));
+}
+template <int ACT>
+__device__ __forceinline__ uint64_t activate2(uint64_t x) {
+  if (ACT == HSTU_ACT_NONE) return x;
+  if (ACT != HSTU_ACT_RELU) return pair_mul(x, sigmoid_of<ACT>(x));
+  float a, b;
+  pair_split(x, a, b);
+  asm("max.NaN.f32 %0, %0, 0f00000000;" : "+f"(a));
+  asm("max.NaN.f32 %0, %0, 0f00000000;" : "+f"(b));
+  return pair_of(a, b);
 }
 __device__ __forceinline__ uint64_t pair_bits(uint32_t lo, uint32_t hi) {
   return pair_of(__uint_as_float(lo), __uint_as_float(hi));
@@ -412,6 +414,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads2, 1)
         }
       };
       load_part(col0 + sub_col);
+      if (EPI == kEpiLinear && p.residual && t + pairs < n_tiles) {
+        // The next tile's rows, one a lane, come from HBM while this tile is computed.
+        int m, n, sp, b0, b1;
+        tile_of(t + pairs, m, n, sp, b0, b1);
+        const int ahead = m + 128 * static_cast<int>(rank) + quarter * 32 + lane;
+        if (ahead < p.M && n + group * 64 < p.N)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const T*>(p.residual) + ahead * p.residual_stride + n +
+                                                        group * 64));
+      }
       if (F8)
 #pragma unroll
         for (int k = 0; k < 4; ++k) row_scale[k] = k < rows ? scale_value(p.a_scale[first_row + 8 * k]) : 0.0f;

@@ -31,6 +31,10 @@ struct FewParams {
   int32_t M, N, act;
 };
 
+inline int64_t few_tiles(int64_t rows, int outputs, int tile_rows) {
+  return (rows + tile_rows - 1) / tile_rows * ((outputs + kFewOutputs - 1) / kFewOutputs);
+}
+
 template <int NT>
 struct FewSmem {
   alignas(1024) uint8_t a[kFewStages][kFewOutputs * 128];
@@ -213,10 +217,12 @@ cudaError_t launch_few_rows(const FewParams& p, cudaStream_t stream) {
   auto kernel = few_rows_kernel<T, F8, NT>;
   const cudaError_t e = ensure_smem_limit(kernel, smem, configured);
   if (e != cudaSuccess) return e;
-  const int64_t nk = (p.k_bytes + 127) / 128, tiles = int64_t{(p.N + kFewOutputs - 1) / kFewOutputs} * ((p.M + NT - 1) / NT);
-  // K is split until every SM has two CTAs' worth of tiles, eight ways at most.
+  // K is split until there are as many CTAs as SMs, eight ways at most; twice as many
+  // where a CTA still has four blocks then (64 x 2048 x 2048: 7.7 us so, 8.3 us split
+  // four ways; 64 x 512 x 2048: 5.8 and 5.4).
+  const int64_t nk = (p.k_bytes + 127) / 128, tiles = few_tiles(p.M, p.N, NT);
   int split = 1;
-  while (split < 8 && 2 * split <= nk && tiles * split * 2 <= 2 * 152) split *= 2;
+  while (split < 8 && 2 * split <= nk && tiles * split * 2 <= (nk / (2 * split) >= 4 ? 2 * 152 : 152)) split *= 2;
   cudaLaunchAttribute attrs[2]{};
   attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attrs[0].val.programmaticStreamSerializationAllowed = 1;
@@ -231,10 +237,13 @@ cudaError_t launch_few_rows(const FewParams& p, cudaStream_t stream) {
   config.numAttrs = 2;
   return cudaLaunchKernelEx(&config, kernel, p);
 }
+// Fewer rows a tile, whose sums take less time to meet, where all tiles, split four
+// ways, still fit the SMs (64 x 512 x 2048: 5.4 us with tiles of 32 rows, 6.1 us with
+// 64; 64 x 4096 x 4096: 13.9 and 11.9).
 template <typename T, bool F8>
 cudaError_t launch_few(const FewParams& p, cudaStream_t stream) {
-  if (p.M <= 16) return launch_few_rows<T, F8, 16>(p, stream);
-  if (p.M <= 32) return launch_few_rows<T, F8, 32>(p, stream);
+  if (p.M <= 16 || 4 * few_tiles(p.M, p.N, 16) <= 152) return launch_few_rows<T, F8, 16>(p, stream);
+  if (p.M <= 32 || 4 * few_tiles(p.M, p.N, 32) <= 152) return launch_few_rows<T, F8, 32>(p, stream);
   return launch_few_rows<T, F8, 64>(p, stream);
 }
 

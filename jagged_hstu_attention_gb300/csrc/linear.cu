@@ -29,29 +29,37 @@ inline int grad_chunks(int64_t rows) {
   return static_cast<int>(c < kGradChunks ? c : kGradChunks);
 }
 
-// act'(z)
-__device__ __forceinline__ float act_grad(float z, int act) {
-  if (act == HSTU_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
-  const bool gelu = act == HSTU_ACT_GELU;
-  const float u = gelu ? kGeluA * z * fmaf(kGeluB * z, z, 1.0f) : z;
-  const float du = gelu ? kGeluA * fmaf(3.0f * kGeluB * z, z, 1.0f) : 1.0f;
-  const float s = __fdividef(1.0f, 1.0f + __expf(-u));
-  return s * fmaf(z * (1.0f - s), du, 1.0f);
+// dy act'(z) of a pair: with p = 1 / (1 + exp(-u)), act' = p (1 + z (1 - p) u').
+template <int ACT>
+__device__ __forceinline__ uint64_t act_grad2(uint64_t z, uint64_t dy) {
+  if (ACT == HSTU_ACT_NONE) return dy;
+  if (ACT == HSTU_ACT_RELU) {
+    float a, b, c, d;
+    pair_split(z, a, b);
+    pair_split(dy, c, d);
+    return pair_of(a > 0.0f ? c : 0.0f, b > 0.0f ? d : 0.0f);
+  }
+  const uint64_t p = sigmoid_of<ACT>(z), one = pair_of(1.0f, 1.0f);
+  uint64_t slope = pair_mul(z, pair_fma(p, pair_of(-1.0f, -1.0f), one));
+  if (ACT == HSTU_ACT_GELU)
+    slope = pair_mul(slope, pair_fma(pair_mul(z, z), pair_of(3.0f * kGeluA * kGeluB, 3.0f * kGeluA * kGeluB),
+                                     pair_of(kGeluA, kGeluA)));
+  return pair_mul(dy, pair_mul(p, pair_add(slope, one)));
 }
 
 struct GradParams {
   const void* dy;
-  const void* z;  // null: g = dy, nothing is written but the sums
+  const void* z;  // without an activation not read: g = dy, nothing is written but the sums
   void* g;
   float* part;  // (chunks, cols)
   int64_t dy_stride, rows;
-  int32_t cols, act;
+  int32_t cols;
 };
 
 // A block takes a chunk of rows; its threads cover as many rows of all columns at
 // a time as there are, 8 columns a thread (256 groups of columns a block where
 // there are more), two rows in flight.
-template <typename T>
+template <typename T, int ACT>
 __global__ void __launch_bounds__(kGradThreads) linear_grad_kernel(const GradParams p) {
   chain();
   __shared__ float red[kGradThreads][8];
@@ -62,27 +70,26 @@ __global__ void __launch_bounds__(kGradThreads) linear_grad_kernel(const GradPar
   const int col = cg * 8;
   const int64_t per = (p.rows + gridDim.x - 1) / gridDim.x;
   const int64_t r0 = static_cast<int64_t>(blockIdx.x) * per, r1 = min(r0 + per, p.rows);
-  float sum[8] = {};
+  uint64_t sums[4] = {};
   auto one = [&](uint4 zv, uint4 dv, int64_t r) {
-    if (p.z) {
-      float z[8], d[8];
-      unpack8<T>(zv, z);
-      unpack8<T>(dv, d);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) d[e] *= act_grad(z[e], p.act);
-      dv = pack8<T>(d);
+    if (ACT != HSTU_ACT_NONE) {
+      dv = make_uint4(pack_pair<T>(act_grad2<ACT>(unpack_pair<T>(zv.x), unpack_pair<T>(dv.x))),
+                      pack_pair<T>(act_grad2<ACT>(unpack_pair<T>(zv.y), unpack_pair<T>(dv.y))),
+                      pack_pair<T>(act_grad2<ACT>(unpack_pair<T>(zv.z), unpack_pair<T>(dv.z))),
+                      pack_pair<T>(act_grad2<ACT>(unpack_pair<T>(zv.w), unpack_pair<T>(dv.w))));
       *reinterpret_cast<uint4*>(static_cast<T*>(p.g) + r * p.cols + col) = dv;
     }
-    float d[8];
-    unpack8<T>(dv, d);  // the sums are those of the g that the products read
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sum[e] += d[e];
+    // the sums are those of the g that the products read
+    sums[0] = pair_add(sums[0], unpack_pair<T>(dv.x));
+    sums[1] = pair_add(sums[1], unpack_pair<T>(dv.y));
+    sums[2] = pair_add(sums[2], unpack_pair<T>(dv.z));
+    sums[3] = pair_add(sums[3], unpack_pair<T>(dv.w));
   };
   if (active) {
     const T* dy = static_cast<const T*>(p.dy) + col;
-    const T* z = static_cast<const T*>(p.z) + (p.z ? col : 0);
+    const T* z = static_cast<const T*>(p.z) + col;
     auto load_z = [&](int64_t r) {
-      return p.z ? *reinterpret_cast<const uint4*>(z + r * p.cols) : make_uint4(0, 0, 0, 0);
+      return ACT != HSTU_ACT_NONE ? *reinterpret_cast<const uint4*>(z + r * p.cols) : make_uint4(0, 0, 0, 0);
     };
     int64_t r = r0 + lane_row;
     constexpr int kRows = 4;
@@ -98,6 +105,9 @@ __global__ void __launch_bounds__(kGradThreads) linear_grad_kernel(const GradPar
     }
     for (; r < r1; r += rpi) one(load_z(r), *reinterpret_cast<const uint4*>(dy + r * p.dy_stride), r);
   }
+  float sum[8];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) pair_split(sums[e], sum[2 * e], sum[2 * e + 1]);
 #pragma unroll
   for (int e = 0; e < 8; ++e) red[threadIdx.x][e] = sum[e];
   __syncthreads();
@@ -109,41 +119,48 @@ __global__ void __launch_bounds__(kGradThreads) linear_grad_kernel(const GradPar
   }
 }
 
-// dbias[col]: the chunks' parts in order, 32 columns a block, a part in 32 a warp.
+// Ends the backward: dw from the fp32 parts of K's splits in order, 8 elements a
+// thread (blocks [0, dw_blocks)); dbias from the chunks' parts in order, 32 columns a
+// block, a part in 32 a warp (the blocks behind).
+constexpr int kFoldThreads = 1024;
+struct FoldParams {
+  const float* dw_part;
+  void* dw;
+  const float* bias_part;
+  void* dbias;
+  int64_t elems;  // of dw
+  int32_t splits, chunks, cols, dw_blocks;
+};
 template <typename T>
-__global__ void __launch_bounds__(1024) linear_bias_fold_kernel(const float* part, int chunks, int cols, void* dbias) {
+__global__ void __launch_bounds__(kFoldThreads) linear_fold_kernel(const FoldParams p) {
   chain();
+  if (static_cast<int>(blockIdx.x) < p.dw_blocks) {
+    const int64_t i = (static_cast<int64_t>(blockIdx.x) * kFoldThreads + threadIdx.x) * 8;
+    if (i >= p.elems) return;
+    float acc[8] = {};
+#pragma unroll 4
+    for (int s = 0; s < p.splits; ++s) {
+      float f[8];
+      load8(p.dw_part + s * p.elems + i, f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] += f[e];
+    }
+    return store8(static_cast<T*>(p.dw) + i, acc);
+  }
   __shared__ float red[32][33];
-  const int w = threadIdx.x >> 5, l = threadIdx.x & 31, col = blockIdx.x * 32 + l;
+  const int w = threadIdx.x >> 5, l = threadIdx.x & 31, col = (blockIdx.x - p.dw_blocks) * 32 + l;
   float s = 0.0f;
-  if (col < cols)
+  if (col < p.cols)
 #pragma unroll 8
-    for (int c = w; c < chunks; c += 32) s += part[static_cast<int64_t>(c) * cols + col];
+    for (int c = w; c < p.chunks; c += 32) s += p.bias_part[static_cast<int64_t>(c) * p.cols + col];
   red[w][l] = s;
   __syncthreads();
-  if (w == 0 && col < cols) {
+  if (w == 0 && col < p.cols) {
     float sum = 0.0f;
 #pragma unroll
     for (int x = 0; x < 32; ++x) sum += red[x][l];
-    static_cast<uint16_t*>(dbias)[col] = static_cast<uint16_t>(Elem<T>::pack2(sum, 0.0f) & 0xffffu);
+    static_cast<uint16_t*>(p.dbias)[col] = static_cast<uint16_t>(Elem<T>::pack2(sum, 0.0f) & 0xffffu);
   }
-}
-
-// dw: the fp32 parts of K's splits in order, 8 elements a thread.
-template <typename T>
-__global__ void __launch_bounds__(256) linear_split_fold_kernel(const float* part, int splits, int64_t elems, T* out) {
-  chain();
-  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
-  if (i >= elems) return;
-  float acc[8] = {};
-#pragma unroll 4
-  for (int s = 0; s < splits; ++s) {
-    float f[8];
-    load8(part + s * elems + i, f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] += f[e];
-  }
-  store8(out + i, acc);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -187,10 +204,10 @@ hstu_status_t linear_checks(int64_t rows, int d_in, int d_out, int act, bool cod
   return HSTU_OK;
 }
 
-// Whether a product goes to the kernel for few rows.
-bool few_rows(int64_t rows, int d_out) {
-  return rows <= kFewRows;
-}
+// Whether a product goes to the kernel for few rows: up to 64 always, more while its
+// tiles leave half of the SMs for K's splits. (512 x 2048: 256 rows take 7.3 us there and 7.7 us on pairs of
+// SMs, 384 rows 8.2 and 7.8; 2048 x 2048: 256 rows 11 and 15 us, 384 rows 15.4 and 14.9.)
+bool few_rows(int64_t rows, int d_out) { return rows <= kFewRows || few_tiles(rows, d_out, kFewRows) <= 152 / 2; }
 
 // Splits of dw's K: those that leave the fewest tiles' time on the busiest pair, counting
 // each split's fp32 tile (written, read) as two of its 64-row blocks.
@@ -224,13 +241,13 @@ LinearLayout linear_layout(int64_t rows, int d_in, int d_out, int act) {
 }
 
 template <typename T>
-cudaError_t launch_grad(const GradParams& p, void* dbias, cudaStream_t stream) {
-  const int chunks = grad_chunks(p.rows);
-  const dim3 grid(chunks, (p.cols / 8 + kGradThreads - 1) / kGradThreads);
-  const cudaError_t e = launch_chained(linear_grad_kernel<T>, grid, kGradThreads, 0, stream, p);
-  if (e != cudaSuccess || !dbias) return e;
-  return launch_chained(linear_bias_fold_kernel<T>, dim3((p.cols + 31) / 32), 1024, 0, stream,
-                        static_cast<const float*>(p.part), chunks, p.cols, dbias);
+cudaError_t launch_grad(const GradParams& p, int act, cudaStream_t stream) {
+  const dim3 grid(grad_chunks(p.rows), (p.cols / 8 + kGradThreads - 1) / kGradThreads);
+  auto kernel = act == HSTU_ACT_SILU   ? linear_grad_kernel<T, HSTU_ACT_SILU>
+                : act == HSTU_ACT_GELU ? linear_grad_kernel<T, HSTU_ACT_GELU>
+                : act == HSTU_ACT_RELU ? linear_grad_kernel<T, HSTU_ACT_RELU>
+                                       : linear_grad_kernel<T, HSTU_ACT_NONE>;
+  return launch_chained(kernel, grid, kGradThreads, 0, stream, p);
 }
 
 }  // namespace
@@ -360,8 +377,7 @@ HSTU_API hstu_status_t hstu_attn_linear_bwd(const void* dy, int64_t dy_stride, c
     gp.dy_stride = dy_stride;
     gp.rows = rows;
     gp.cols = d_out;
-    gp.act = act;
-    if ((f16 ? launch_grad<__half>(gp, dbias, cs) : launch_grad<__nv_bfloat16>(gp, dbias, cs)) != cudaSuccess)
+    if ((f16 ? launch_grad<__half>(gp, act, cs) : launch_grad<__nv_bfloat16>(gp, act, cs)) != cudaSuccess)
       return HSTU_ERR_CUDA;
     if (gp.z) {
       g = gp.g;
@@ -390,14 +406,20 @@ HSTU_API hstu_status_t hstu_attn_linear_bwd(const void* dy, int64_t dy_stride, c
   p.k_splits = dw_splits(rows, d_in, d_out);
   p.part = reinterpret_cast<float*>(base + l.dw);
   if ((f16 ? launch_linear_dw_f16(p, cs) : launch_linear_dw_bf16(p, cs)) != cudaSuccess) return HSTU_ERR_CUDA;
-  if (p.k_splits == 1) return HSTU_OK;
-  const int64_t elems = int64_t{d_out} * d_in;
-  const dim3 grid(static_cast<unsigned>((elems / 8 + 255) / 256));
-  const cudaError_t e = f16 ? launch_chained(linear_split_fold_kernel<__half>, grid, 256, 0, cs,
-                                             static_cast<const float*>(p.part), p.k_splits, elems, static_cast<__half*>(dw))
-                            : launch_chained(linear_split_fold_kernel<__nv_bfloat16>, grid, 256, 0, cs,
-                                             static_cast<const float*>(p.part), p.k_splits, elems,
-                                             static_cast<__nv_bfloat16*>(dw));
+  if (p.k_splits == 1 && !dbias) return HSTU_OK;
+  FoldParams fp{};
+  fp.dw_part = p.part;
+  fp.dw = dw;
+  fp.bias_part = reinterpret_cast<const float*>(base + l.part);
+  fp.dbias = dbias;
+  fp.elems = int64_t{d_out} * d_in;
+  fp.splits = p.k_splits;
+  fp.chunks = grad_chunks(rows);
+  fp.cols = d_out;
+  fp.dw_blocks = p.k_splits > 1 ? static_cast<int32_t>((fp.elems / 8 + kFoldThreads - 1) / kFoldThreads) : 0;
+  const dim3 grid(static_cast<unsigned>(fp.dw_blocks + (dbias ? (d_out + 31) / 32 : 0)));
+  const cudaError_t e = launch_chained(f16 ? linear_fold_kernel<__half> : linear_fold_kernel<__nv_bfloat16>, grid,
+                                       kFoldThreads, 0, cs, fp);
   return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
 }
 

@@ -116,11 +116,13 @@ def _check_codes(codes, scale, ref, slack):
 def test_eight_bits(D, dtype, T, residual, gate):
     x, w, r, g = _inputs(T, D, dtype, residual, gate, seed=3)
     x = x * torch.logspace(-3, 3, T, device="cuda")[:, None].to(dtype)
-    q, h, rstd = hb.rms_norm(x, w, residual=r, gate=g, quantise=True)
+    q, h, rstd = hb.rms_norm(x, w, residual=r, gate=g, quantise=True, want_rstd=True)
     kept = x if r is None else h
     ref, ref_rstd = lt.norm(lt.f64(kept), lt.f64(w), None if g is None else lt.f64(g))
     assert lt.worst(lt.f64(rstd), ref_rstd, lt.NORM_ERR * ref_rstd) <= 1.0
     _check_codes(q.codes, q.scale, ref, lt.NORM_ERR)
+    q2, _, none = hb.rms_norm(x, w, residual=r, gate=g, quantise=True)
+    assert none is None and torch.equal(q2.codes, q.codes) and torch.equal(q2.scale, q.scale)
 
 
 @pytest.mark.parametrize("D", WIDTHS)
