@@ -52,7 +52,8 @@ struct EmbedParams {
   float scale;
 };
 
-// A block takes `rows` tokens' rows, a chunk a thread, U chunks in flight.
+// A block takes `rows` tokens' rows, U chunks a thread at a time; the ids of the next
+// chunks are read while these are.
 template <typename TT, typename T, typename ID, int U>
 __global__ void __launch_bounds__(kEmbedThreads) embed_kernel(const EmbedParams p) {
   chain();
@@ -62,24 +63,27 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_kernel(const EmbedParams 
   const ID* ids = static_cast<const ID*>(p.ids) + t0;
   const TT* table = static_cast<const TT*>(p.table);
   T* out = static_cast<T*>(p.out) + t0 * p.chunks * 8;
-  for (uint32_t u0 = threadIdx.x; u0 < units; u0 += U * kEmbedThreads) {
-    int64_t id[U];
-    uint32_t row[U];
+  ID next[U];
+  auto read_ids = [&](uint32_t u0) {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const uint32_t u = u0 + i * kEmbedThreads;
-      row[i] = static_cast<uint32_t>(u * p.per_chunk >> 32);
-      id[i] = u < units ? static_cast<int64_t>(ids[row[i]]) : -1;
+      next[i] = u < units ? ids[static_cast<uint32_t>(u * p.per_chunk >> 32)] : static_cast<ID>(-1);
     }
+  };
+  read_ids(threadIdx.x);
+  for (uint32_t u0 = threadIdx.x; u0 < units; u0 += U * kEmbedThreads) {
     float f[U][8];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const uint32_t u = u0 + i * kEmbedThreads;
+      const uint32_t u = u0 + i * kEmbedThreads, col = u - static_cast<uint32_t>(u * p.per_chunk >> 32) * p.chunks;
+      const int64_t id = static_cast<int64_t>(next[i]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[i][e] = 0.0f;
-      if (id[i] >= 0 && id[i] < p.vocab) load8(table + (id[i] * p.chunks + (u - row[i] * p.chunks)) * 8, f[i]);
-      else if (id[i] >= p.vocab && p.header) atomicOr(p.header + kHdrErr, kErrInput);
+      if (id >= 0 && id < p.vocab) load8(table + (id * p.chunks + col) * 8, f[i]);
+      else if (id >= p.vocab && p.header) atomicOr(p.header + kHdrErr, kErrInput);
     }
+    read_ids(u0 + U * kEmbedThreads);
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const uint32_t u = u0 + i * kEmbedThreads;
@@ -93,13 +97,12 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_kernel(const EmbedParams 
 
 template <typename TT, typename T, typename ID>
 cudaError_t launch_embed(EmbedParams p, cudaStream_t stream) {
-  // Four chunks a thread where that leaves eight blocks an SM, else one: a
-  // step's few rows are spread over as many SMs as they have chunks for.
-  const int64_t units = p.tokens * p.chunks;
-  const bool many = units >= int64_t{152} * 8 * kEmbedThreads * 4;
-  const int64_t per_block = kEmbedThreads * (many ? 4 : 1);
-  const int64_t rows = per_block / p.chunks;
-  p.rows = static_cast<int32_t>(rows < 1 ? 1 : rows);
+  // Four chunks a thread at a time, and as many blocks as run at once, where that
+  // fills the GPU; else one: a step's few rows are spread over as many SMs as they
+  // have chunks for. (2^16 chunks a block at most, which per_chunk divides exactly.)
+  const bool many = p.tokens * p.chunks >= int64_t{152} * 8 * kEmbedThreads * 4;
+  const int64_t least = kEmbedThreads * (many ? 4 : 1) / p.chunks, even = many ? (p.tokens + 152 * 5 - 1) / (152 * 5) : 0;
+  p.rows = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(std::max(least, even), (1 << 16) / p.chunks)));
   p.per_chunk = ((uint64_t{1} << 32) + p.chunks - 1) / p.chunks;
   const dim3 grid(static_cast<unsigned>((p.tokens + p.rows - 1) / p.rows));
   return launch_chained(many ? embed_kernel<TT, T, ID, 4> : embed_kernel<TT, T, ID, 1>, grid, kEmbedThreads, 0, stream, p);
@@ -433,6 +436,10 @@ __global__ void __launch_bounds__(kEmbedThreads, 4) embed_sum_kernel(const SumPa
 template <typename G>
 __global__ void __launch_bounds__(kJoinThreads) embed_join_kernel(const SumParams p) {
   chain();
+  if (blockIdx.x >= 2 * kJoinBlocks) {
+    if (blockIdx.y == 0) fill_rows(p.fill, blockIdx.x - 2 * kJoinBlocks);
+    return;
+  }
   __shared__ float slice[kJoinThreads][8];
   const int brief = p.header[kHdrShort], large = p.header[kHdrLong];
   const int col0 = blockIdx.y * kEmbedThreads * 8;
@@ -548,10 +555,10 @@ FillParams fill_share(FillParams& rest, int64_t rows, int part, int parts) {
   return f;
 }
 
-// The launches that follow the first zero rows on the side: a move twice as many as
-// a count, which is about half as long, and the summing kernel, whose blocks hold more
-// registers and so write less at a time, as many as a move. (Zeroing 410 MB beside a
-// sort of 81920 tokens takes as long as the zeros alone.)
+// The launches that follow the first zero rows on the side: a move four parts, a
+// count, which is about half as long, two; the summing kernel, which moves as much
+// itself, and the join, which mostly waits, three each. (81920 tokens, 200003 rows of 512:
+// sort, sum and join take 65 us without zeros, the zeros alone 53 us.)
 // Leaves the rows still to be zeroed in `fill`.
 template <typename ID>
 cudaError_t launch_sort(SortParams p, FillParams& fill, uint8_t* base, const EmbedLayout& l, int& last,
@@ -561,7 +568,7 @@ cudaError_t launch_sort(SortParams p, FillParams& fill, uint8_t* base, const Emb
   while ((p.vocab >> bits) != 0) ++bits;  // of the largest key, vocab
   const int passes = (bits + kMaxDigitBits - 1) / kMaxDigitBits;
   p.bits = (bits + passes - 1) / passes;
-  const int parts = 2 * passes + (passes - 1) + 2;
+  const int parts = 4 * passes + 2 * (passes - 1) + 6;
   const int64_t rounds = (p.n + int64_t{kSortTiles} * kSortThreads - 1) / (int64_t{kSortTiles} * kSortThreads);
   p.tile = static_cast<int32_t>(rounds * kSortThreads);
   p.tiles = static_cast<int32_t>((p.n + p.tile - 1) / p.tile);
@@ -571,11 +578,11 @@ cudaError_t launch_sort(SortParams p, FillParams& fill, uint8_t* base, const Emb
     p.val_in = reinterpret_cast<const int32_t*>(base + l.val[s & 1]);
     p.key_out = reinterpret_cast<uint32_t*>(base + l.key[(s + 1) & 1]);
     p.val_out = reinterpret_cast<int32_t*>(base + l.val[(s + 1) & 1]);
-    p.fill = fill_share(fill, all, s == 0 ? 0 : 1, parts);  // (the first launch sets the rows' bits)
+    p.fill = fill_share(fill, all, s == 0 ? 0 : 2, parts);  // (the first launch sets the rows' bits)
     cudaError_t e = launch_chained(s == 0 ? sort_count_kernel<ID, true> : sort_count_kernel<ID, false>,
                                    dim3(static_cast<unsigned>(p.tiles + fill_blocks(p.fill))), kSortThreads, 0, stream, p);
     if (e != cudaSuccess) return e;
-    p.fill = fill_share(fill, all, 2, parts);
+    p.fill = fill_share(fill, all, 4, parts);
     e = launch_chained(s == 0 ? sort_move_kernel<ID, true> : sort_move_kernel<ID, false>,
                        dim3(static_cast<unsigned>(p.tiles + fill_blocks(p.fill))), kSortThreads, 0, stream, p);
     if (e != cudaSuccess) return e;
@@ -584,20 +591,24 @@ cudaError_t launch_sort(SortParams p, FillParams& fill, uint8_t* base, const Emb
   return cudaSuccess;
 }
 
+// The rows of the table still to be zeroed (`fill`) are shared with the join.
 template <typename T, typename G>
-cudaError_t launch_sum(SumParams p, cudaStream_t stream) {
+cudaError_t launch_sum(SumParams p, FillParams fill, cudaStream_t stream) {
   const int widest = p.dim < kEmbedThreads * 8 ? p.dim : kEmbedThreads * 8;
   const int groups = kEmbedThreads / (widest / 8);
   const unsigned ny = (p.dim + kEmbedThreads * 8 - 1) / (kEmbedThreads * 8);
   p.sum_blocks = (p.chunks + groups - 1) / groups;
+  p.fill = fill_share(fill, fill.row1 - fill.row0, 1, 2);
   cudaError_t e = launch_chained(embed_sum_kernel<T, G>, dim3(static_cast<unsigned>(p.sum_blocks + fill_blocks(p.fill)), ny),
                                  kEmbedThreads, 0, stream, p);
   if (e != cudaSuccess) return e;
-  return launch_chained(embed_join_kernel<G>, dim3(2 * kJoinBlocks, ny), kJoinThreads, 0, stream, p);
+  p.fill = fill;
+  return launch_chained(embed_join_kernel<G>, dim3(static_cast<unsigned>(2 * kJoinBlocks + fill_blocks(fill)), ny),
+                        kJoinThreads, 0, stream, p);
 }
 template <typename T>
-cudaError_t launch_sum_typed(const SumParams& p, int grad_dtype, cudaStream_t stream) {
-  return grad_dtype == HSTU_DTYPE_F32 ? launch_sum<T, float>(p, stream) : launch_sum<T, T>(p, stream);
+cudaError_t launch_sum_typed(const SumParams& p, const FillParams& fill, int grad_dtype, cudaStream_t stream) {
+  return grad_dtype == HSTU_DTYPE_F32 ? launch_sum<T, float>(p, fill, stream) : launch_sum<T, T>(p, fill, stream);
 }
 
 hstu_status_t embed_checks(int64_t tokens, int64_t vocab, int dim) {
@@ -703,7 +714,6 @@ HSTU_API hstu_status_t hstu_attn_embed_bwd(const void* dy, int64_t dy_stride, in
   p.dy_stride = dy_stride;
   p.key = reinterpret_cast<const uint32_t*>(base + l.key[last]);
   p.val = reinterpret_cast<const int32_t*>(base + l.val[last]);
-  p.fill = fill;
   p.dtable = dtable;
   p.part = reinterpret_cast<float*>(base + l.part);
   p.header = reinterpret_cast<int32_t*>(base);
@@ -715,8 +725,8 @@ HSTU_API hstu_status_t hstu_attn_embed_bwd(const void* dy, int64_t dy_stride, in
   p.chunks = static_cast<int32_t>((tokens + p.chunk - 1) / p.chunk);
   p.accumulate = accumulate;
   p.scale = scale;
-  e = dtype == HSTU_DTYPE_F16 ? launch_sum_typed<__half>(p, grad_dtype, cs)
-                              : launch_sum_typed<__nv_bfloat16>(p, grad_dtype, cs);
+  e = dtype == HSTU_DTYPE_F16 ? launch_sum_typed<__half>(p, fill, grad_dtype, cs)
+                              : launch_sum_typed<__nv_bfloat16>(p, fill, grad_dtype, cs);
   return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
 }
 
