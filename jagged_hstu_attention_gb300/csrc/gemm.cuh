@@ -19,6 +19,7 @@
 #include "../../include/hstu_attn.h"
 #include "cache.cuh"
 #include "internal.h"
+#include "pairs.cuh"
 
 namespace hstu {
 
@@ -154,30 +155,6 @@ __device__ __forceinline__ uint64_t block_desc(uint32_t base, int kk) {
 }
 
 // ------------------------------------------------------------- activations
-// Two fp32 values in a register pair: one instruction works on both.
-__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void pair_split(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t pair_add(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t pair_mul(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t pair_fma(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -189,15 +166,26 @@ __device__ __forceinline__ float reciprocal_fast(float x) {
   return y;
 }
 
-// 1 / (1 + exp(-u)) of a pair; times x, u = x is SiLU, u = 2 sqrt(2 / pi) (x + 0.044715 x^3) the tanh
-// form of GELU. The exponentials are of base 2, their arguments m u, m = -log2(e),
-// at most 60 so that the product of the two sums below stays finite (past it the
-// result is 2^-60, for what is nearer to 0). One reciprocal serves both: 1 / a =
-// b / (a b). (ex2 runs at 32 a cycle and SM, rcp at 16.)
+// 1 / (1 + exp(-u)) of a pair; times x, u = x is SiLU, u = 2 sqrt(2 / pi) (x + 0.044715 x^3)
+// the tanh form of GELU. The exponentials are of base 2 (argument m u, m = -log2(e)), and
+// one reciprocal serves both values: 1 / a = b / (a b). (ex2 runs at 32 a cycle and SM,
+// rcp at 16.) So that the product stays finite x counts as kLowest where it is
+// below that: SiLU and GELU are -4e-17 and -6e-17 there, nearer to 0 below. A NaN
+// stays with its own value.
 constexpr float kGeluA = 1.5957691216057308f, kGeluB = 0.044715f;  // 2 sqrt(2 / pi)
 constexpr float kLog2e = 1.4426950408889634f;
 template <int ACT>
-__device__ __forceinline__ uint64_t sigmoid_of(uint64_t x) {
+constexpr float kLowest = ACT == HSTU_ACT_GELU ? -7.3f : -41.5f;
+__device__ __forceinline__ float max_nan(float x, float low) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(low));
+  return r;
+}
+template <int ACT>
+__device__ __forceinline__ uint64_t sigmoid_of(uint64_t x, uint64_t& e) {  // e: exp(-u)
+  float a, b;
+  pair_split(x, a, b);
+  x = pair_of(fmaxf(a, kLowest<ACT>), fmaxf(b, kLowest<ACT>));  // NaN too
   uint64_t m;
   if (ACT == HSTU_ACT_SILU) {
     m = pair_mul(x, pair_of(-kLog2e, -kLog2e));
@@ -206,37 +194,23 @@ __device__ __forceinline__ uint64_t sigmoid_of(uint64_t x) {
                                    pair_of(-kLog2e * kGeluA, -kLog2e * kGeluA));
     m = pair_mul(x, poly);
   }
-  float a, b;
   pair_split(m, a, b);
-  asm("min.NaN.f32 %0, %0, 0f42700000;" : "+f"(a));
-  asm("min.NaN.f32 %0, %0, 0f42700000;" : "+f"(b));
-  pair_split(pair_add(pair_of(exp2_fast(a), exp2_fast(b)), pair_of(1.0f, 1.0f)), a, b);
+  e = pair_of(exp2_fast(a), exp2_fast(b));
+  pair_split(pair_add(e, pair_of(1.0f, 1.0f)), a, b);
   const float r = reciprocal_fast(a * b);
   return pair_mul(pair_of(r, r), pair_of(b, a));
 }
 template <int ACT>
 __device__ __forceinline__ uint64_t activate2(uint64_t x) {
   if (ACT == HSTU_ACT_NONE) return x;
-  if (ACT != HSTU_ACT_RELU) return pair_mul(x, sigmoid_of<ACT>(x));
   float a, b;
   pair_split(x, a, b);
-  asm("max.NaN.f32 %0, %0, 0f00000000;" : "+f"(a));
-  asm("max.NaN.f32 %0, %0, 0f00000000;" : "+f"(b));
-  return pair_of(a, b);
+  constexpr float low = ACT == HSTU_ACT_RELU ? 0.0f : kLowest<ACT>;
+  const uint64_t cut = pair_of(max_nan(a, low), max_nan(b, low));
+  uint64_t e;
+  return ACT == HSTU_ACT_RELU ? cut : pair_mul(cut, sigmoid_of<ACT>(x, e));
 }
-__device__ __forceinline__ uint64_t pair_bits(uint32_t lo, uint32_t hi) {
-  return pair_of(__uint_as_float(lo), __uint_as_float(hi));
-}
-template <typename T>
-__device__ __forceinline__ uint64_t unpack_pair(uint32_t w) {
-  return pair_of(Elem<T>::lo(w), Elem<T>::hi(w));
-}
-template <typename T>
-__device__ __forceinline__ uint32_t pack_pair(uint64_t v) {
-  float a, b;
-  pair_split(v, a, b);
-  return Elem<T>::pack2(a, b);
-}
+
 // Eight columns, rounded; nothing here reads them again.
 template <typename T>
 __device__ __forceinline__ void store_cols(T* dst, const uint64_t (&v)[4]) {

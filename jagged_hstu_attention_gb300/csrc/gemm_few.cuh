@@ -6,15 +6,20 @@
 // CTAs each fetch one 24 KB block, which is all the waiting there is. Operands come by
 // 16-byte asynchronous copies written where the MMA expects them (128-byte
 // swizzle), with no tensor maps to encode on the host. The CTAs' sums meet in
-// distributed shared memory: each CTA adds its part of the rows over the cluster, in
-// rank order, and runs their epilogue.
+// distributed shared memory: each CTA writes its sums of a part of the rows to the CTA
+// that owns the part, which adds them in rank order and runs the epilogue. (Read from
+// where they were computed instead, with a second barrier before anyone may leave: 64
+// rows, 512 x 2048, in 5.4 us.)
 #pragma once
 
 #include "gemm.cuh"
 
 namespace hstu {
 
-constexpr int kFewThreads = 256, kFewStages = 4, kFewOutputs = 128, kFewRows = 64;
+constexpr int kFewThreads = 256, kFewOutputs = 128, kFewRows = 64;
+// Two CTAs share an SM.
+template <int NT>
+constexpr int kFewStages = NT < 64 ? 4 : 3;
 
 struct FewParams {
   const void* x;
@@ -37,26 +42,24 @@ inline int64_t few_tiles(int64_t rows, int outputs, int tile_rows) {
 
 template <int NT>
 struct FewSmem {
-  alignas(1024) uint8_t a[kFewStages][kFewOutputs * 128];
-  alignas(1024) uint8_t b[kFewStages][NT * 128];
-  alignas(8) uint64_t done[kFewStages];
+  alignas(1024) uint8_t a[kFewStages<NT>][kFewOutputs * 128];
+  alignas(1024) uint8_t b[kFewStages<NT>][NT * 128];
+  float2 meet[NT / 2 * kFewOutputs];  // [CTA][pair of own rows][output]
+  alignas(8) uint64_t done[kFewStages<NT>];
   uint32_t tmem_base;
   int abort_flag;
 };
 
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-__device__ __forceinline__ float4 lds_cluster(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
+__device__ __forceinline__ void sts_cluster(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 template <bool F8>
 __device__ __forceinline__ void umma_one(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -87,6 +90,7 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams p
   extern __shared__ uint8_t smem_raw[];
   FewSmem<NT>& s = *reinterpret_cast<FewSmem<NT>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   constexpr int kColumns = NT < 32 ? 32 : NT;  // of TMEM
+  constexpr int kStagesHere = kFewStages<NT>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = gridDim.x, rank = blockIdx.x;  // the cluster lies along x
   const int n0 = blockIdx.y * kFewOutputs, m0 = blockIdx.z * NT;
@@ -95,7 +99,7 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams p
   const int blocks = static_cast<int>(static_cast<int64_t>(nk) * (rank + 1) / split) - kb0;  // one at least
   if (threadIdx.x == 0) {
     s.abort_flag = 0;
-    for (int i = 0; i < kFewStages; ++i) mbar_init(smem_u32(&s.done[i]), 1);
+    for (int i = 0; i < kStagesHere; ++i) mbar_init(smem_u32(&s.done[i]), 1);
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -111,101 +115,96 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams p
   const uint8_t *x = static_cast<const uint8_t*>(p.x), *w = static_cast<const uint8_t*>(p.w);
   auto load = [&](int j) {
     if (j < blocks) {
-      copy_block<kFewOutputs>(smem_u32(s.a[j % kFewStages]), w, p.k_bytes, n0, p.N, p.k_bytes, kb0 + j);
-      copy_block<NT>(smem_u32(s.b[j % kFewStages]), x, p.x_stride, m0, p.M, p.k_bytes, kb0 + j);
+      copy_block<kFewOutputs>(smem_u32(s.a[j % kStagesHere]), w, p.k_bytes, n0, p.N, p.k_bytes, kb0 + j);
+      copy_block<NT>(smem_u32(s.b[j % kStagesHere]), x, p.x_stride, m0, p.M, p.k_bytes, kb0 + j);
     }
     copy_commit();
   };
-  for (int j = 0; j < kFewStages - 1; ++j) load(j);
+  for (int j = 0; j < kStagesHere - 1; ++j) load(j);
   constexpr uint32_t idesc = idesc_f16kind(kFewOutputs, NT, false, false, F8 ? 0u : Elem<T>::kUmma);
   bool ok = true;
   for (int j = 0; j < blocks; ++j) {
-    copy_wait<kFewStages - 2>();
+    copy_wait<kStagesHere - 2>();
     fence_async_smem();
     ok = __syncthreads_and(ok);  // block j has arrived; all agree whether to go on
     if (!ok) break;
     if (warp == 0 && elect_one_sync()) {
-      const uint32_t a = smem_u32(s.a[j % kFewStages]), b = smem_u32(s.b[j % kFewStages]);
+      const uint32_t a = smem_u32(s.a[j % kStagesHere]), b = smem_u32(s.b[j % kStagesHere]);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
         umma_one<F8>(tacc, block_desc<false>(a, kk), block_desc<false>(b, kk), idesc, j > 0 || kk > 0 ? 1u : 0u);
-      umma_commit(smem_u32(&s.done[j % kFewStages]));
+      umma_commit(smem_u32(&s.done[j % kStagesHere]));
     }
     __syncwarp();
     // The block before has been multiplied: its stage takes the next one to come.
-    if (j > 0) ok = mbar_wait(smem_u32(&s.done[(j - 1) % kFewStages]), ((j - 1) / kFewStages) & 1, &s.abort_flag);
-    if (ok) load(j + kFewStages - 1);
+    if (j > 0) ok = mbar_wait(smem_u32(&s.done[(j - 1) % kStagesHere]), ((j - 1) / kStagesHere) & 1, &s.abort_flag);
+    if (ok) load(j + kStagesHere - 1);
   }
   copy_wait<0>();
-  if (ok) ok = mbar_wait(smem_u32(&s.done[(blocks - 1) % kFewStages]), ((blocks - 1) / kFewStages) & 1, &s.abort_flag);
+  if (ok) ok = mbar_wait(smem_u32(&s.done[(blocks - 1) % kStagesHere]), ((blocks - 1) / kStagesHere) & 1, &s.abort_flag);
   ok = __syncthreads_and(ok);
   tc_fence_after();
-  // The CTA's sums as [row][output], over the operands, which nothing reads any more.
-  const uint32_t part = smem_u32(s.a[0]);
-  static_assert(NT * kFewOutputs * 4 <= sizeof(s.a), "sums over the operands");
-  if (ok && warp < 4) {
+  // Rows [c own, (c + 1) own) of the tile are CTA c's: sums of pairs of rows, an output
+  // a lane; warps 4 to 7 take the second half of the columns.
+  const int own = NT / split;
+  if (ok) {
+    constexpr int kHalf = NT / 2;
+    const int c0 = warp < 4 ? 0 : kHalf, output = (warp & 3) * 32 + lane;
+    uint32_t a[32];
+    tmem_ld32(tacc + (static_cast<uint32_t>((warp & 3) * 32) << 16) + (NT < 64 ? 0 : c0), a);
+    tmem_ld_wait(a);
 #pragma unroll
-    for (int c = 0; c < NT; c += 32) {
-      uint32_t a[32];
-      tmem_ld32(tacc + (static_cast<uint32_t>(warp * 32) << 16) + c, a);
-      tmem_ld_wait(a);
-#pragma unroll
-      for (int e = 0; e < 32; ++e)
-        if (c + e < NT)
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(part + ((c + e) * kFewOutputs + warp * 32 + lane) * 4), "r"(a[e])
-                       : "memory");
+    for (int e = 0; e < kHalf; e += 2) {
+      const int row = c0 + e, at = rank * own + row % own;
+      const uint32_t lo = NT < 64 && warp >= 4 ? a[(kHalf + e) & 31] : a[e], hi = NT < 64 && warp >= 4 ? a[(kHalf + e + 1) & 31] : a[e + 1];
+      sts_cluster(in_cta(smem_u32(&s.meet[at / 2 * kFewOutputs + output]), row / own), lo, hi);
     }
   }
-  // Rows [rank NT / split, (rank + 1) NT / split) are this CTA's, four outputs a thread.
-  const int r0 = rank * NT / split, r1 = (rank + 1) * NT / split;
-  const int col = n0 + lane * 4;
-  uint2 bias = make_uint2(0, 0);
-  uint32_t col_scale = 0;
+  const int output = threadIdx.x % kFewOutputs, col = n0 + output;
+  float bias = 0.0f, col_scale = 1.0f;
   if (col < p.N) {
-    if (p.bias) bias = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.bias) + col);
-    if (F8) col_scale = *reinterpret_cast<const uint32_t*>(p.w_scale + col);
-  }
-  cluster_sync();  // all sums are in place
-  for (int r = r0 + warp; r < r1; r += kFewThreads / 32) {
-    const int row = m0 + r;
-    if (!ok || row >= p.M || col >= p.N) continue;
-    uint2 res = make_uint2(0, 0);
-    if (p.residual) res = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.residual) + row * p.residual_stride + col);
-    const float row_scale = F8 ? scale_value(p.x_scale[row]) : 1.0f;
-    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const uint32_t mine = part + (r * kFewOutputs + lane * 4) * 4;
-#pragma unroll 8
-    for (int c = 0; c < split; ++c) {
-      const float4 v = lds_cluster(in_cta(mine, c));
-      sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
-    }
-    uint64_t v[2] = {pair_of(sum.x, sum.y), pair_of(sum.z, sum.w)};
-    const uint32_t bw[2] = {bias.x, bias.y}, rw[2] = {res.x, res.y};
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      if (F8) {
-        const uint32_t b = col_scale >> (16 * e);
-        v[e] = pair_mul(pair_mul(v[e], pair_of(row_scale, row_scale)),
-                        pair_of(scale_value(b & 0xffu), scale_value((b >> 8) & 0xffu)));
-      }
-      v[e] = pair_add(v[e], unpack_pair<T>(bw[e]));
-    }
-    const int64_t at = static_cast<int64_t>(row) * p.N + col;
-    if (p.z) *reinterpret_cast<uint2*>(static_cast<T*>(p.z) + at) = make_uint2(pack_pair<T>(v[0]), pack_pair<T>(v[1]));
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      if (p.act == HSTU_ACT_SILU) v[e] = activate2<HSTU_ACT_SILU>(v[e]);
-      if (p.act == HSTU_ACT_GELU) v[e] = activate2<HSTU_ACT_GELU>(v[e]);
-      if (p.act == HSTU_ACT_RELU) v[e] = activate2<HSTU_ACT_RELU>(v[e]);
-      if (p.residual) v[e] = pair_add(v[e], unpack_pair<T>(rw[e]));
-    }
-    *reinterpret_cast<uint2*>(static_cast<T*>(p.y) + at) = make_uint2(pack_pair<T>(v[0]), pack_pair<T>(v[1]));
+    if (p.bias) bias = to_float(static_cast<const T*>(p.bias)[col]);
+    if (F8) col_scale = scale_value(p.w_scale[col]);
   }
   tc_fence_before();
-  cluster_sync();  // nobody leaves while another CTA reads its sums
+  cluster_sync();  // all sums are in place
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tacc, kColumns);
+  }
+  for (int j = threadIdx.x / kFewOutputs; j < own / 2; j += kFewThreads / kFewOutputs) {
+    const int row = m0 + rank * own + 2 * j;
+    if (!ok || row >= p.M || col >= p.N) continue;
+    const bool second = row + 1 < p.M;
+    const int64_t at = static_cast<int64_t>(row) * p.N + col;
+    float res[2] = {0.0f, 0.0f};
+    if (p.residual) {
+      const T* from = static_cast<const T*>(p.residual) + row * p.residual_stride + col;
+      res[0] = to_float(from[0]);
+      if (second) res[1] = to_float(from[p.residual_stride]);
+    }
+    uint64_t v = pair_of(0.0f, 0.0f);
+#pragma unroll 8
+    for (int c = 0; c < split; ++c) {
+      const float2 f = s.meet[(c * own / 2 + j) * kFewOutputs + output];
+      v = pair_add(v, pair_of(f.x, f.y));
+    }
+    if (F8)
+      v = pair_mul(pair_mul(v, pair_of(scale_value(p.x_scale[row]), second ? scale_value(p.x_scale[row + 1]) : 0.0f)),
+                   pair_of(col_scale, col_scale));
+    v = pair_add(v, pair_of(bias, bias));
+    auto store = [&](void* base, uint64_t values) {
+      const uint32_t w = pack_pair<T>(values);
+      uint16_t* to = static_cast<uint16_t*>(base) + at;
+      to[0] = static_cast<uint16_t>(w);
+      if (second) to[p.N] = static_cast<uint16_t>(w >> 16);
+    };
+    if (p.z) store(p.z, v);
+    if (p.act == HSTU_ACT_SILU) v = activate2<HSTU_ACT_SILU>(v);
+    if (p.act == HSTU_ACT_GELU) v = activate2<HSTU_ACT_GELU>(v);
+    if (p.act == HSTU_ACT_RELU) v = activate2<HSTU_ACT_RELU>(v);
+    if (p.residual) v = pair_add(v, pair_of(res[0], res[1]));
+    store(p.y, v);
   }
   if (threadIdx.x == 0 && s.abort_flag && p.header) atomicOr(p.header + kHdrErr, kErrTimeout);
 }

@@ -39,12 +39,19 @@ __device__ __forceinline__ uint64_t act_grad2(uint64_t z, uint64_t dy) {
     pair_split(dy, c, d);
     return pair_of(a > 0.0f ? c : 0.0f, b > 0.0f ? d : 0.0f);
   }
-  const uint64_t p = sigmoid_of<ACT>(z), one = pair_of(1.0f, 1.0f);
-  uint64_t slope = pair_mul(z, pair_fma(p, pair_of(-1.0f, -1.0f), one));
+  // (Past 64, where p is 1, z counts as 64: its square stays finite.)
+  float a, b;
+  pair_split(z, a, b);
+  asm("min.NaN.f32 %0, %0, 0f42800000;" : "+f"(a));
+  asm("min.NaN.f32 %0, %0, 0f42800000;" : "+f"(b));
+  z = pair_of(max_nan(a, kLowest<ACT>), max_nan(b, kLowest<ACT>));
+  uint64_t e;
+  const uint64_t p = sigmoid_of<ACT>(z, e);
+  uint64_t slope = pair_mul(z, pair_mul(e, p));  // 1 - p = p exp(-u), which nothing cancels in
   if (ACT == HSTU_ACT_GELU)
     slope = pair_mul(slope, pair_fma(pair_mul(z, z), pair_of(3.0f * kGeluA * kGeluB, 3.0f * kGeluA * kGeluB),
                                      pair_of(kGeluA, kGeluA)));
-  return pair_mul(dy, pair_mul(p, pair_add(slope, one)));
+  return pair_mul(dy, pair_mul(p, pair_add(slope, pair_of(1.0f, 1.0f))));
 }
 
 struct GradParams {

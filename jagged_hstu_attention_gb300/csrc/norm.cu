@@ -23,6 +23,7 @@
 
 #include "cache.cuh"
 #include "layer.cuh"
+#include "pairs.cuh"
 
 namespace hstu {
 namespace {
@@ -115,46 +116,69 @@ __global__ void __launch_bounds__(norm_threads<RT>()) norm_kernel(const NormPara
     rstd = 1.0f / sqrtf(sum / static_cast<float>(p.width) + p.eps);
     if (p.rstd && live && t == 0) p.rstd[r] = rstd;
   }
-  float y[V][8];
-  float top = 0.0f;
+  uint64_t y[V][4];
+  float top = 0.0f;  // largest magnitude; NaN is passed over
+  const uint64_t rr = pair_of(rstd, rstd);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    unpack8<T>(xv[i], y[i]);
-    if (OUT != kCodes) {
-      float w[8];
-      unpack8<T>(wv[i], w);
+    const uint32_t xw[4] = {xv[i].x, xv[i].y, xv[i].z, xv[i].w}, ww[4] = {wv[i].x, wv[i].y, wv[i].z, wv[i].w},
+                   gw[4] = {gv[i].x, gv[i].y, gv[i].z, gv[i].w};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[i][e] *= rstd * w[e];
-      if (p.gate) {
-        unpack8<T>(gv[i], w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[i][e] *= w[e];
+    for (int e = 0; e < 4; ++e) {
+      y[i][e] = unpack_pair<T>(xw[e]);
+      if (OUT != kCodes) {
+        y[i][e] = pair_mul(y[i][e], pair_mul(rr, unpack_pair<T>(ww[e])));
+        if (p.gate) y[i][e] = pair_mul(y[i][e], unpack_pair<T>(gw[e]));
+      }
+      if (OUT != kNorm16) {
+        float a, b;
+        pair_split(y[i][e], a, b);
+        top = fmaxf(top, fmaxf(fabsf(a), fabsf(b)));
       }
     }
-    if (OUT == kNorm16) {
-      const int col = (t + i * RT) * 8;
-      if (live && col < p.width) store8(static_cast<T*>(p.y) + r * p.width + col, y[i]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float a = fabsf(y[i][e]);
-        top = fmaxf(top, a <= kMaxFinite ? a : 0.0f);
-      }
-    }
+    const int col = (t + i * RT) * 8;
+    if (OUT == kNorm16 && live && col < p.width)
+      *reinterpret_cast<uint4*>(static_cast<T*>(p.y) + r * p.width + col) =
+          make_uint4(pack_pair<T>(y[i][0]), pack_pair<T>(y[i][1]), pack_pair<T>(y[i][2]), pack_pair<T>(y[i][3]));
   }
   if (OUT == kNorm16) return;
+  // The scale goes by the finite values: a row with an infinity looks for its largest again.
+  // (Every row of the block does then, for the barriers' sake; nothing changes for the others.)
   top = row_reduce<RT, true>(top, shared[1]);
+  const bool infinite = top > kMaxFinite;
+  const bool again = RT > 32 ? __syncthreads_or(infinite) : __any_sync(0xffffffffu, infinite);
+  if (again) {
+    top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float a, b;
+        pair_split(y[i][e], a, b);
+        top = fmaxf(top, fmaxf(fabsf(a) <= kMaxFinite ? fabsf(a) : 0.0f, fabsf(b) <= kMaxFinite ? fabsf(b) : 0.0f));
+      }
+    top = row_reduce<RT, true>(top, shared[0]);
+  }
   const uint32_t byte = scale_byte(top);
   const float inv = __uint_as_float((254u - byte) << 23);  // 2^(127 - byte), exact
+  const uint64_t ii = pair_of(inv, inv);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int col = (t + i * RT) * 8;
     if (!live || col >= p.width) continue;
-    float* f = y[i];
+    uint32_t c[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = fabsf(f[e]) <= kMaxFinite ? f[e] * inv : __uint_as_float(0x7fc00000u);
+    for (int e = 0; e < 4; ++e) {
+      float a, b;
+      pair_split(pair_mul(y[i][e], ii), a, b);
+      if (infinite) {  // infinities become NaN, as NaN does
+        a = fabsf(a) <= kMaxFinite ? a : __uint_as_float(0x7fc00000u);
+        b = fabsf(b) <= kMaxFinite ? b : __uint_as_float(0x7fc00000u);
+      }
+      c[e] = e4m3x2(a, b);
+    }
     *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.y) + r * p.width + col) =
-        make_uint2(e4m3x2(f[0], f[1]) | (e4m3x2(f[2], f[3]) << 16), e4m3x2(f[4], f[5]) | (e4m3x2(f[6], f[7]) << 16));
+        make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
   }
   if (live && t == 0) p.scale[r] = static_cast<uint8_t>(byte);
 }
@@ -195,24 +219,36 @@ __global__ void __launch_bounds__(norm_bwd_threads<RT>()) norm_bwd_kernel(const 
     for (int e = 0; e < 8; ++e) acc[i][e] = 0.0f;
   }
   const float inv_width = 1.0f / static_cast<float>(p.width);
-  // All groups of a block go around together: the reduction has barriers.
-  int turn = 0;
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kGroups; r0 < p.rows;
-       r0 += static_cast<int64_t>(gridDim.x) * kGroups, turn ^= 1) {
-    const int64_t r = r0 + group;
-    const bool live = r < p.rows;
-    uint4 dv[V], hv[V], gv[V], ev[V];
-    const float rstd = live ? p.rstd[r] : 0.0f;
+  // A row's loads are on their way while the row before is worked on (81920 rows of
+  // 512: 51 us, without 56 us); with a gate the registers for it cost more blocks than
+  // it gains (65 us without, 78 us).
+  constexpr bool kAhead = !GATE;
+  uint4 dv[V], hv[V], gv[V], ev[V];
+  float rstd = 0.0f;
+  auto read_row = [&](int64_t r, uint4 (&d)[V], uint4 (&h)[V], uint4 (&g)[V], uint4 (&e)[V], float& s) {
+    s = r < p.rows ? p.rstd[r] : 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int col = (t + i * RT) * 8;
-      dv[i] = hv[i] = gv[i] = ev[i] = make_uint4(0, 0, 0, 0);
-      if (!live || col >= p.width) continue;
-      dv[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.dy) + r * p.dy_stride + col);
-      hv[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.h) + r * p.h_stride + col);
-      if (GATE) gv[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.gate) + r * p.gate_stride + col);
-      if (p.dh) ev[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.dh) + r * p.dh_stride + col);
+      d[i] = h[i] = g[i] = e[i] = make_uint4(0, 0, 0, 0);
+      if (r >= p.rows || col >= p.width) continue;
+      d[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.dy) + r * p.dy_stride + col);
+      h[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.h) + r * p.h_stride + col);
+      if (GATE) g[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.gate) + r * p.gate_stride + col);
+      if (p.dh) e[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.dh) + r * p.dh_stride + col);
     }
+  };
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
+  if (kAhead) read_row(static_cast<int64_t>(blockIdx.x) * kGroups + group, dv, hv, gv, ev, rstd);
+  // All groups of a block go around together: the reduction has barriers.
+  int turn = 0;
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kGroups; r0 < p.rows; r0 += step, turn ^= 1) {
+    const int64_t r = r0 + group;
+    const bool live = r < p.rows;
+    uint4 next_d[V], next_h[V], next_g[V], next_e[V];
+    float next_rstd;
+    if (kAhead) read_row(r + step, next_d, next_h, next_g, next_e, next_rstd);
+    else read_row(r, dv, hv, gv, ev, rstd);
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -251,6 +287,10 @@ __global__ void __launch_bounds__(norm_bwd_threads<RT>()) norm_bwd_kernel(const 
       }
       store8(static_cast<T*>(p.dx) + r * p.width + col, x);
     }
+    if (!kAhead) continue;
+    rstd = next_rstd;
+#pragma unroll
+    for (int i = 0; i < V; ++i) dv[i] = next_d[i], hv[i] = next_h[i], gv[i] = next_g[i], ev[i] = next_e[i];
   }
   // The groups' sums, in their order.
   if (kGroups > 1) {

@@ -163,6 +163,34 @@ def test_values_that_are_not_finite_stay_in_their_row():
     assert torch.equal(y[rows], clean[rows]) and torch.isnan(y[7]).all()
 
 
+@pytest.mark.parametrize("T", [5, 200, 1500])
+@pytest.mark.parametrize("act", ["none", "silu", "gelu", "relu"])
+def test_extreme_columns(T, act):
+    """Outputs whose bias is the type's lowest or largest value, an infinity or NaN: the activation's
+    limits there, and nothing else changes."""
+    x, w, b, _ = _inputs(T, 64, 264, BF, seed=8)
+    clean = hb.linear(x, w, bias=b, act=act)[0]
+    low, top = torch.finfo(BF).min, torch.finfo(BF).max
+    at, values = [3, 64, 100, 131, 200, 263], [low, float("inf"), float("nan"), -1e4, -1e20, 3e38]
+    b = b.clone()
+    b[at] = torch.tensor(values, dtype=BF, device="cuda")
+    y, z = hb.linear(x, w, bias=b, act=act, want_z=True)
+    rest = torch.ones(264, dtype=torch.bool, device="cuda")
+    rest[at] = False
+    assert torch.equal(y[:, rest], clean[:, rest])
+    assert torch.isnan(y[:, 100]).all() and torch.isinf(y[:, 64]).all() and (y[:, 263].float() >= 2.9e38).all()
+    if act != "none":
+        assert (y[:, [3, 131, 200]].float().abs() <= 6e-17).all()
+    dy = lt.randn((T, 264), BF, 9)
+    dx, dw, db = hb.linear_bwd(dy, z, x, w, act=act)
+    # the gradient of a column that is not finite stays with it
+    assert torch.isfinite(dw[rest].float()).all() and torch.isfinite(db[rest].float()).all()
+    if act != "none":
+        assert (dw[[3, 131, 200]].float().abs() <= 1e-12 * T).all()
+        ones = hb.linear_bwd(dy, z, x, w)[2]  # slope 1 far above
+        assert torch.equal(db[263], ones[263])
+
+
 def test_no_rows():
     x, w, b, _ = _inputs(0, 64, 72, BF)
     y, z = hb.linear(x, w, bias=b, act="silu", want_z=True)
