@@ -83,6 +83,23 @@ def test_gradient_digits_and_wide_rows(T, V, D):
     _bwd_case(T, V, D, BF, F32 if V < 1000000 else BF, "skewed")
 
 
+def test_tables_past_two_to_the_32_values():
+    """Rows whose offsets pass 32 bits, in values and in bytes."""
+    V, D = 34000003, 128
+    table = torch.zeros((V, D), dtype=BF, device="cuda")
+    ids = torch.tensor([V - 1, 7, V - 2, V - 1, 20000001, V], dtype=torch.int64, device="cuda")
+    rows = lt.randn((6, D), BF, 3)
+    table[ids[:5]] = rows[:5]
+    y = hb.embed(table, ids, 2.0)
+    assert torch.equal(y[:5], 2 * table[ids[:5]]) and (y[5] == 0).all()
+    del table
+    d = hb.embed_bwd(rows, ids, V, dtype=BF)
+    assert torch.equal(d[V - 1], (rows[0].float() + rows[3].float()).to(BF)) and torch.equal(d[V - 2], rows[2])
+    assert torch.equal(d[20000001], rows[4]) and torch.equal(d[7], rows[1])
+    d[ids[:5]] = 0
+    assert int(torch.count_nonzero(d[V // 2:])) == 0 and int(torch.count_nonzero(d[:V // 2])) == 0
+
+
 def test_gradient_is_that_of_the_sum():
     """Along a random direction of the table, against differences of the 64-bit sum."""
     T, V, D, scale = 400, 60, 40, 1.5

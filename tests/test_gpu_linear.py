@@ -104,7 +104,8 @@ def test_eight_bit_rows_of_a_wider_matrix():
     assert torch.equal(a, hb.linear(hb.QuantisedRows(wide[:, 48:112], q.scale), qw)[0])
 
 
-@pytest.mark.parametrize("T,K,N", SIZES + [(5000, 264, 72), (20000, 40, 8)])
+@pytest.mark.parametrize("T,K,N", SIZES + [(5000, 264, 72), (20000, 40, 8), (9001, 512, 200), (41000, 256, 136),
+                                           (4097, 504, 328), (4500, 520, 96)])
 @pytest.mark.parametrize("act,dtype", [("none", BF), ("silu", BF), ("gelu", F16), ("relu", F16)])
 def test_gradients(T, K, N, act, dtype):
     x, w, b, _ = _inputs(T, K, N, dtype, seed=11, pad=8)
@@ -150,6 +151,17 @@ def test_gradients_are_those_of_the_sum(act):
         slope = ((f(s * v) - f(-s * v)) * DY).sum() / (2 * s)
         bound = ((err + half * np.abs(lt.f64(got)) * 1.01) * np.abs(v)).sum()
         assert abs((lt.f64(got) * v).sum() - slope) <= bound + 1e-6
+
+
+def test_rows_past_two_to_the_31_values():
+    """Inputs' and outputs' offsets past 32 bits: rows from both ends against the same rows alone."""
+    T, K, N = 1100000, 64, 2048
+    x, w, b, _ = _inputs(T, K, N, BF, seed=5)
+    y, _ = hb.linear(x, w, bias=b, act="silu")
+    dx, dw, _ = hb.linear_bwd(y, None, x, w, want_dbias=False)
+    for r in (slice(0, 300), slice(T - 300, T)):
+        assert torch.equal(y[r], hb.linear(x[r], w, bias=b, act="silu")[0])
+        assert torch.equal(dx[r], hb.linear_bwd(y[r], None, x[r], w, want_dbias=False)[0])
 
 
 def test_values_that_are_not_finite_stay_in_their_row():
@@ -211,6 +223,24 @@ def test_a_wait_that_gives_up_is_reported():
     finally:
         hb.set_handoff_limit_for_tests(0)
     assert torch.equal(want, hb.linear(x, w, bias=b, ws=ws)[0]) and hb.device_status(ws) == hb.HSTU_OK
+
+
+def test_a_wait_of_the_backward_that_gives_up_is_reported():
+    T, K, N = 45000, 640, 64
+    x, w, b, _ = _inputs(T, K, N, BF)
+    dy, z = lt.randn((T, N), BF, 1), lt.randn((T, N), BF, 2)
+    ws = hb.linear_workspace(T, K, N, "silu")
+    want = hb.linear_bwd(dy, z, x, w, act="silu", ws=ws)
+    assert hb.device_status(ws) == hb.HSTU_OK
+    hb.set_handoff_limit_for_tests(1)
+    try:
+        hb.linear_bwd(dy, z, x, w, act="silu", ws=ws)
+        assert hb.device_status(ws) == 6
+    finally:
+        hb.set_handoff_limit_for_tests(0)
+    for a, c in zip(want, hb.linear_bwd(dy, z, x, w, act="silu", ws=ws)):
+        assert torch.equal(a, c)
+    assert hb.device_status(ws) == hb.HSTU_OK
 
 
 def test_refusals():

@@ -176,6 +176,19 @@ def test_the_stream_updated_in_place():
     assert none is None and torch.equal(x2, h) and torch.equal(y3, y)
 
 
+def test_rows_past_two_to_the_31_values():
+    T, D = 540000, 4096
+    x, w = lt.randn((T, D), BF, 1), lt.randn((D,), BF, 2)
+    y, h, rstd = hb.rms_norm(x, w, residual=x)
+    dx, _, _ = hb.rms_norm_bwd(y, h, rstd, w)
+    q = hb.quantise_rows(x)
+    for r in (slice(0, 9), slice(T - 9, T)):
+        a, b, c = hb.rms_norm(x[r], w, residual=x[r])
+        assert torch.equal(y[r], a) and torch.equal(h[r], b) and torch.equal(rstd[r], c)
+        assert torch.equal(dx[r], hb.rms_norm_bwd(a, b, c, w)[0])
+        assert torch.equal(q.codes[r], hb.quantise_rows(x[r]).codes) and torch.equal(q.scale[r], hb.quantise_rows(x[r]).scale)
+
+
 def test_no_rows():
     x, w = lt.randn((0, 64), BF, 1), lt.randn((64,), BF, 2)
     y, h, rstd = hb.rms_norm(x, w)
