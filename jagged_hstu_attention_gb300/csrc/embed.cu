@@ -33,7 +33,10 @@ constexpr int kSortTiles = 152;  // at most one tile an SM
 constexpr int kSeenBits = 10, kSeen = 1 << kSeenBits;
 constexpr int kFillBytes = 1 << 17;     // of the table that a zeroing block looks after, about
 constexpr int kFillMostRows = 1 << 13;  // of them (rows are 16 bytes at least)
-constexpr int kJoinThreads = 1024, kJoinBlocks = 152;  // as many again for short runs
+// At most kJoinBlocks for long runs and for short ones: blocks that zero have the other half
+// of the SMs from the start.
+constexpr int kJoinThreads = 1024, kJoinBlocks = 76;
+constexpr int kJoinCols = 512;  // of a joining block: 16 groups of threads share a long run
 constexpr int kShortRun = 16;  // chunks of a run that one group of threads joins alone
 // Header words: the long runs found, those of at most kShortRun chunks and the others.
 constexpr int kHdrShort = 1, kHdrLong = 2;
@@ -178,9 +181,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortPara
   chain();
   if (static_cast<int>(blockIdx.x) >= p.tiles) return fill_rows(p.fill, blockIdx.x - p.tiles);
   __shared__ uint32_t count[kMaxBins];
-  // Ids whose bit a thread of the block has set or is about to: the most frequent ids
-  // would otherwise queue up at one word.
-  __shared__ volatile uint32_t seen[FIRST ? kSeen : 1];
+  // Ids whose bit a thread of the block sets: the most frequent ids would otherwise
+  // queue up at one word.
+  __shared__ uint32_t seen[FIRST ? kSeen : 1];
   const int bins = 1 << p.bits;
   for (int b = threadIdx.x; b < bins; b += kSortThreads) count[b] = 0;
   if (FIRST)
@@ -193,9 +196,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortPara
     atomicAdd(&count[(key >> p.shift) & (bins - 1)], 1u);
     if (FIRST) {
       if (key < p.vocab) {
-        const uint32_t h = (key * 2654435761u) >> (32 - kSeenBits);
-        if (seen[h] == key) continue;
-        seen[h] = key;
+        if (atomicExch(&seen[(key * 2654435761u) >> (32 - kSeenBits)], key) == key) continue;
         atomicOr(p.named + (key >> 5), 1u << (key & 31));
       } else if (p.header && static_cast<int64_t>(static_cast<const ID*>(p.ids)[i]) >= 0)
         atomicOr(p.header + kHdrErr, kErrInput);
@@ -292,6 +293,53 @@ __global__ void __launch_bounds__(kSortThreads) sort_move_kernel(const SortParam
   }
 }
 
+// Few tokens in one launch, 6 us for 208 (two for each digit take 10; 2048 tokens in a
+// block took 18): a block sorts (id, token) pairs as 64-bit numbers in shared
+// memory (a bitonic network; steps inside a warp's 64 pairs need no barrier), and sets the
+// rows' bits, which it clears itself where they are not too many.
+constexpr int kSmallTokens = 512, kSmallThreads = 256;
+constexpr int64_t kSmallBits = 1 << 18;
+template <typename ID>
+__global__ void __launch_bounds__(kSmallThreads) sort_small_kernel(const SortParams p, int count, bool clear) {
+  chain();
+  __shared__ uint64_t pairs[kSmallTokens];
+  if (clear) {
+    for (int64_t w = threadIdx.x; w < (p.vocab + 31) / 32; w += kSmallThreads) p.named[w] = 0;
+    if (threadIdx.x < kHdrWords) p.header[threadIdx.x] = 0;
+    __syncthreads();
+  }
+  for (int i = threadIdx.x; i < count; i += kSmallThreads) {
+    uint64_t pair = ~uint64_t{0};
+    if (i < p.n) {
+      const uint32_t key = sort_key<ID, true>(p, i);
+      pair = (static_cast<uint64_t>(key) << 32) | static_cast<uint32_t>(i);
+      if (key < p.vocab) atomicOr(p.named + (key >> 5), 1u << (key & 31));
+      else if (static_cast<int64_t>(static_cast<const ID*>(p.ids)[i]) >= 0) atomicOr(p.header + kHdrErr, kErrInput);
+    }
+    pairs[i] = pair;
+  }
+  __syncthreads();
+  for (int k = 2; k <= count; k *= 2)
+    for (int j = k / 2; j > 0; j /= 2) {
+      for (int t = threadIdx.x; t < count / 2; t += kSmallThreads) {
+        const int a = 2 * t - (t & (j - 1)), b = a + j;
+        const uint64_t x = pairs[a], y = pairs[b];
+        if ((x > y) == ((a & k) == 0)) {
+          pairs[a] = y;
+          pairs[b] = x;
+        }
+      }
+      // Steps of up to 32 stay within a warp's 64 pairs.
+      if (j >= 64 || (j == 1 && k >= 64)) __syncthreads();
+      else __syncwarp();
+    }
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.n; i += kSmallThreads) {
+    p.key_out[i] = static_cast<uint32_t>(pairs[i] >> 32);
+    p.val_out[i] = static_cast<int32_t>(pairs[i]);
+  }
+}
+
 // ----------------------------------------------------------------- backward
 
 struct SumParams {
@@ -305,16 +353,12 @@ struct SumParams {
   int32_t* runs;  // first whole chunks: of short runs from the front, of others from the back
   int64_t n, vocab;
   int32_t chunk, chunks, dim, accumulate;
+  int32_t groups;      // chunks of a summing block
+  int32_t long_blocks, short_blocks;  // of the join, for the runs of either kind
   int32_t sum_blocks;  // blocks that sum, spread evenly among those that zero
   float scale;
   FillParams fill;
 };
-
-// Whether chunk c holds one id alone.
-__device__ __forceinline__ bool one_id(const SumParams& p, int64_t c, uint32_t key) {
-  const int64_t i0 = c * p.chunk, i1 = min(i0 + p.chunk, p.n);
-  return i0 < i1 && p.key[i0] == key && p.key[i1 - 1] == key;
-}
 
 template <typename G>
 __device__ __forceinline__ void put_row(const SumParams& p, int64_t row, int col, float (&acc)[8]) {
@@ -331,7 +375,7 @@ __device__ __forceinline__ void put_row(const SumParams& p, int64_t row, int col
 }
 
 template <typename T, typename G>
-__global__ void __launch_bounds__(kEmbedThreads, 4) embed_sum_kernel(const SumParams p) {
+__global__ void __launch_bounds__(kEmbedThreads) embed_sum_kernel(const SumParams p) {
   chain();
   const int64_t summed = static_cast<int64_t>(blockIdx.x) * p.sum_blocks / gridDim.x;  // summing blocks before this one
   if ((static_cast<int64_t>(blockIdx.x) + 1) * p.sum_blocks / gridDim.x == summed) {
@@ -340,37 +384,54 @@ __global__ void __launch_bounds__(kEmbedThreads, 4) embed_sum_kernel(const SumPa
   }
   const int col0 = blockIdx.y * kEmbedThreads * 8;
   const int group = min(kEmbedThreads, (p.dim - col0) / 8);  // threads of a row
-  const int groups = kEmbedThreads / group, g = threadIdx.x / group;
+  const int groups = p.groups, g = threadIdx.x / group;
   const int col = col0 + (threadIdx.x % group) * 8;
   if (g >= groups) return;
   const int64_t c = summed * groups + g;
   if (c >= p.chunks) return;
-  const int64_t i0 = c * p.chunk, end = min(i0 + p.chunk, p.n);
+  // The ids at the chunk's ends and its neighbours', all read at once: kNoId where there
+  // is none.
+  constexpr uint32_t kNoId = 0xffffffffu;
+  const int64_t i0 = c * p.chunk, end = min(i0 + p.chunk, p.n), far = i0 + static_cast<int64_t>(kShortRun) * p.chunk;
   const uint32_t first = p.key[i0], last = p.key[end - 1];
-  const bool from_before = i0 > 0 && p.key[i0 - 1] == first;
-  const bool whole = first == last;
+  const uint32_t before = c > 0 ? p.key[i0 - 1] : kNoId, before_first = c > 0 ? p.key[i0 - p.chunk] : kNoId;
+  const uint32_t after = end < p.n ? p.key[end] : kNoId;
+  const uint32_t after_last = end < p.n ? p.key[min(end + p.chunk, p.n) - 1] : kNoId;
+  const uint32_t far_first = far < p.n ? p.key[far] : kNoId;
   if (first >= p.vocab) return;
+  const bool whole = first == last, from_before = before == first;
+  // How many of the ids from `at` on, a chunk's at most, are `id`.
+  auto run_of = [&](int64_t at, int64_t limit, uint32_t id) {
+    int n = 0;
+    for (int part = 0; part < p.chunk; part += 16) {
+      int same = 0;
+#pragma unroll
+      for (int u = 0; u < 16; ++u) {
+        const int64_t x = at + part + u;
+        same += x < limit && p.key[x] == id;
+      }
+      n += same;
+      if (same < 16) break;
+    }
+    return n;
+  };
   int64_t i = i0, i1 = end;
   // The run that comes from the chunk before: the whole of a chunk, or the end
   // of a long run (one that fills the chunk before), is a partial sum;
   // otherwise that chunk sums it.
-  const bool head_part = whole || (from_before && one_id(p, c - 1, first));
-  if (from_before && !head_part)
-    while (i < end && p.key[i] == first) ++i;
+  const bool long_before = from_before && before_first == first;
+  const bool head_part = whole || long_before;
+  if (from_before && !head_part) i += run_of(i0, end, first);
   // The run that goes on into the next chunk: long if that chunk is full of it, else it is
   // summed here to its end.
-  bool tail_part = false;
-  if (!whole && end < p.n && p.key[end] == last && last < p.vocab) {
-    tail_part = one_id(p, c + 1, last);
-    if (!tail_part)
-      while (i1 < p.n && p.key[i1] == last) ++i1;
-  }
+  const bool goes_on = !whole && after == last && last < p.vocab, tail_part = goes_on && after_last == last;
+  if (goes_on && !tail_part) i1 += run_of(end, p.n, last);
   // A whole chunk whose run is no longer than it: an ordinary row.
-  const bool alone = whole && !from_before && (end == p.n || p.key[end] != first);
+  const bool alone = whole && !from_before && after != first;
   // The first whole chunk of a run lists it for the join. (In whatever order: each
   // run is added up by itself.)
-  if (whole && !alone && !(from_before && one_id(p, c - 1, first)) && blockIdx.y == 0 && threadIdx.x % group == 0) {
-    const bool brief = c + kShortRun >= p.chunks || p.key[(c + kShortRun) * p.chunk] != first;
+  if (whole && !alone && !long_before && blockIdx.y == 0 && threadIdx.x % group == 0) {
+    const bool brief = far_first != first;
     const int at = atomicAdd(p.header + (brief ? kHdrShort : kHdrLong), 1);
     p.runs[brief ? at : p.chunks - 1 - at] = static_cast<int32_t>(c);
   }
@@ -436,14 +497,15 @@ __global__ void __launch_bounds__(kEmbedThreads, 4) embed_sum_kernel(const SumPa
 template <typename G>
 __global__ void __launch_bounds__(kJoinThreads) embed_join_kernel(const SumParams p) {
   chain();
-  if (blockIdx.x >= 2 * kJoinBlocks) {
-    if (blockIdx.y == 0) fill_rows(p.fill, blockIdx.x - 2 * kJoinBlocks);
+  const int joining = p.long_blocks + p.short_blocks;
+  if (static_cast<int>(blockIdx.x) >= joining) {
+    if (blockIdx.y == 0) fill_rows(p.fill, blockIdx.x - joining);
     return;
   }
   __shared__ float slice[kJoinThreads][8];
   const int brief = p.header[kHdrShort], large = p.header[kHdrLong];
-  const int col0 = blockIdx.y * kEmbedThreads * 8;
-  const int group = min(kEmbedThreads, (p.dim - col0) / 8);
+  const int col0 = blockIdx.y * kJoinCols;
+  const int group = min(kJoinCols, p.dim - col0) / 8;
   const int groups = kJoinThreads / group, g = threadIdx.x / group;
   const int col = col0 + (threadIdx.x % group) * 8;
   // The sum of chunks [a, b) of a run; of the end of the chunk before too with `before`.
@@ -459,7 +521,7 @@ __global__ void __launch_bounds__(kJoinThreads) embed_join_kernel(const SumParam
   };
   auto from_before = [&](int64_t c, uint32_t key) { return c > 0 && p.key[c * p.chunk - 1] == key; };
   if (g < groups)
-    for (int k = (blockIdx.x - kJoinBlocks) * groups + g; blockIdx.x >= kJoinBlocks && k < brief; k += kJoinBlocks * groups) {
+    for (int k = (static_cast<int>(blockIdx.x) - p.long_blocks) * groups + g; k >= 0 && k < brief; k += p.short_blocks * groups) {
       const int64_t c = p.runs[k];
       const uint32_t key = p.key[c * p.chunk];
       int parts = 1;
@@ -473,8 +535,8 @@ __global__ void __launch_bounds__(kJoinThreads) embed_join_kernel(const SumParam
       sum_of(c, c + parts, from_before(c, key), acc);
       put_row<G>(p, key, col, acc);
     }
-  if (blockIdx.x >= kJoinBlocks) return;
-  for (int k = blockIdx.x; k < large; k += kJoinBlocks) {
+  if (static_cast<int>(blockIdx.x) >= p.long_blocks) return;
+  for (int k = blockIdx.x; k < large; k += p.long_blocks) {
     const int64_t c = p.runs[p.chunks - 1 - k];
     const uint32_t key = p.key[c * p.chunk];
     // The last chunk that begins with the id: all threads look, at a step that
@@ -564,6 +626,14 @@ template <typename ID>
 cudaError_t launch_sort(SortParams p, FillParams& fill, uint8_t* base, const EmbedLayout& l, int& last,
                         cudaStream_t stream) {
   const int64_t all = fill.row1 - fill.row0;
+  if (p.n <= kSmallTokens) {
+    int count = 2;
+    while (count < p.n) count *= 2;
+    p.key_out = reinterpret_cast<uint32_t*>(base + l.key[0]);
+    p.val_out = reinterpret_cast<int32_t*>(base + l.val[0]);
+    last = 0;
+    return launch_chained(sort_small_kernel<ID>, dim3(1), kSmallThreads, 0, stream, p, count, p.vocab <= kSmallBits);
+  }
   int bits = 1;
   while ((p.vocab >> bits) != 0) ++bits;  // of the largest key, vocab
   const int passes = (bits + kMaxDigitBits - 1) / kMaxDigitBits;
@@ -595,15 +665,25 @@ cudaError_t launch_sort(SortParams p, FillParams& fill, uint8_t* base, const Emb
 template <typename T, typename G>
 cudaError_t launch_sum(SumParams p, FillParams fill, cudaStream_t stream) {
   const int widest = p.dim < kEmbedThreads * 8 ? p.dim : kEmbedThreads * 8;
-  const int groups = kEmbedThreads / (widest / 8);
+  // As many chunks as fit a block, and no more threads than they need (a row of 1128
+  // columns takes 141: one chunk, 160 threads).
+  p.groups = kEmbedThreads / (widest / 8);
+  const int threads = (p.groups * (widest / 8) + 31) / 32 * 32;
   const unsigned ny = (p.dim + kEmbedThreads * 8 - 1) / (kEmbedThreads * 8);
-  p.sum_blocks = (p.chunks + groups - 1) / groups;
-  p.fill = fill_share(fill, fill.row1 - fill.row0, 1, 2);
+  p.sum_blocks = (p.chunks + p.groups - 1) / p.groups;
+  const bool join = p.chunks > 1;  // a chunk alone has no runs into others
+  p.fill = fill_share(fill, fill.row1 - fill.row0, 1, join ? 2 : 1);
   cudaError_t e = launch_chained(embed_sum_kernel<T, G>, dim3(static_cast<unsigned>(p.sum_blocks + fill_blocks(p.fill)), ny),
-                                 kEmbedThreads, 0, stream, p);
-  if (e != cudaSuccess) return e;
+                                 threads, 0, stream, p);
+  if (e != cudaSuccess || !join) return e;
   p.fill = fill;
-  return launch_chained(embed_join_kernel<G>, dim3(static_cast<unsigned>(2 * kJoinBlocks + fill_blocks(fill)), ny),
+  // No more blocks than there can be runs.
+  const int join_groups = kJoinThreads / (std::min(kJoinCols, p.dim) / 8);
+  p.long_blocks = std::min(kJoinBlocks, (p.chunks + kShortRun - 1) / kShortRun);
+  p.short_blocks = std::min(kJoinBlocks, (p.chunks + join_groups - 1) / join_groups);
+  return launch_chained(embed_join_kernel<G>,
+                        dim3(static_cast<unsigned>(p.long_blocks + p.short_blocks + fill_blocks(fill)),
+                             (p.dim + kJoinCols - 1) / kJoinCols),
                         kJoinThreads, 0, stream, p);
 }
 template <typename T>
@@ -683,8 +763,10 @@ HSTU_API hstu_status_t hstu_attn_embed_bwd(const void* dy, int64_t dy_stride, in
   if (!aligned_to(ws, 256) || ws_bytes < l.total) return HSTU_ERR_WORKSPACE;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(ws);
-  // the error word and the bits of the rows
-  if (cudaMemsetAsync(base, 0, l.key[0], cs) != cudaSuccess) return HSTU_ERR_CUDA;
+  // The error word and the bits of the rows. (A sort in one block clears few of them itself.)
+  if ((tokens == 0 || tokens > kSmallTokens || vocab > kSmallBits) &&
+      cudaMemsetAsync(base, 0, l.key[0], cs) != cudaSuccess)
+    return HSTU_ERR_CUDA;
   cudaError_t e = cudaSuccess;
   FillParams fill{};
   fill.table = dtable;

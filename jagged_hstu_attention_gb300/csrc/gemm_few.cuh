@@ -85,7 +85,21 @@ __device__ __forceinline__ void copy_block(uint32_t dst, const uint8_t* src, int
   }
 }
 
-template <typename T, bool F8, int NT>
+// The same of a matrix whose columns are the outputs (MN-major): columns [col0, col0 + 128) of
+// rows [64 kb, 64 kb + 64), as [64-column group][row][128 bytes].
+__device__ __forceinline__ void copy_block_mn(uint32_t dst, const uint8_t* src, int col0, int cols, int64_t rows, int kb) {
+#pragma unroll
+  for (int i = threadIdx.x; i < 64 * 16; i += kFewThreads) {
+    const int r = i >> 4, c = i & 15;
+    const int64_t row = int64_t{64} * kb + r;
+    const bool valid = row < rows && col0 + 8 * c < cols;
+    copy16(dst + (c >> 3) * 64 * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+           valid ? src + (row * cols + col0 + 8 * c) * 2 : src, valid);
+  }
+}
+
+// W_MN: w is (K, N), its columns the outputs (the gradient of the rows).
+template <typename T, bool F8, bool W_MN, int NT>
 __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams p) {
   extern __shared__ uint8_t smem_raw[];
   FewSmem<NT>& s = *reinterpret_cast<FewSmem<NT>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -115,13 +129,14 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams p
   const uint8_t *x = static_cast<const uint8_t*>(p.x), *w = static_cast<const uint8_t*>(p.w);
   auto load = [&](int j) {
     if (j < blocks) {
-      copy_block<kFewOutputs>(smem_u32(s.a[j % kStagesHere]), w, p.k_bytes, n0, p.N, p.k_bytes, kb0 + j);
+      if (W_MN) copy_block_mn(smem_u32(s.a[j % kStagesHere]), w, n0, p.N, p.k_bytes / 2, kb0 + j);
+      else copy_block<kFewOutputs>(smem_u32(s.a[j % kStagesHere]), w, p.k_bytes, n0, p.N, p.k_bytes, kb0 + j);
       copy_block<NT>(smem_u32(s.b[j % kStagesHere]), x, p.x_stride, m0, p.M, p.k_bytes, kb0 + j);
     }
     copy_commit();
   };
   for (int j = 0; j < kStagesHere - 1; ++j) load(j);
-  constexpr uint32_t idesc = idesc_f16kind(kFewOutputs, NT, false, false, F8 ? 0u : Elem<T>::kUmma);
+  constexpr uint32_t idesc = idesc_f16kind(kFewOutputs, NT, W_MN, false, F8 ? 0u : Elem<T>::kUmma);
   bool ok = true;
   for (int j = 0; j < blocks; ++j) {
     copy_wait<kStagesHere - 2>();
@@ -132,7 +147,7 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams p
       const uint32_t a = smem_u32(s.a[j % kStagesHere]), b = smem_u32(s.b[j % kStagesHere]);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        umma_one<F8>(tacc, block_desc<false>(a, kk), block_desc<false>(b, kk), idesc, j > 0 || kk > 0 ? 1u : 0u);
+        umma_one<F8>(tacc, block_desc<W_MN>(a, kk), block_desc<false>(b, kk), idesc, j > 0 || kk > 0 ? 1u : 0u);
       umma_commit(smem_u32(&s.done[j % kStagesHere]));
     }
     __syncwarp();
@@ -209,11 +224,11 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams p
   if (threadIdx.x == 0 && s.abort_flag && p.header) atomicOr(p.header + kHdrErr, kErrTimeout);
 }
 
-template <typename T, bool F8, int NT>
+template <typename T, bool F8, bool W_MN, int NT>
 cudaError_t launch_few_rows(const FewParams& p, cudaStream_t stream) {
   const int smem = static_cast<int>(sizeof(FewSmem<NT>)) + 1024;
   static std::atomic<uint64_t> configured{0};
-  auto kernel = few_rows_kernel<T, F8, NT>;
+  auto kernel = few_rows_kernel<T, F8, W_MN, NT>;
   const cudaError_t e = ensure_smem_limit(kernel, smem, configured);
   if (e != cudaSuccess) return e;
   // K is split until there are as many CTAs as SMs, eight ways at most; twice as many
@@ -239,11 +254,11 @@ cudaError_t launch_few_rows(const FewParams& p, cudaStream_t stream) {
 // Fewer rows a tile, whose sums take less time to meet, where all tiles, split four
 // ways, still fit the SMs (64 x 512 x 2048: 5.4 us with tiles of 32 rows, 6.1 us with
 // 64; 64 x 4096 x 4096: 13.9 and 11.9).
-template <typename T, bool F8>
+template <typename T, bool F8, bool W_MN>
 cudaError_t launch_few(const FewParams& p, cudaStream_t stream) {
-  if (p.M <= 16 || 4 * few_tiles(p.M, p.N, 16) <= 152) return launch_few_rows<T, F8, 16>(p, stream);
-  if (p.M <= 32 || 4 * few_tiles(p.M, p.N, 32) <= 152) return launch_few_rows<T, F8, 32>(p, stream);
-  return launch_few_rows<T, F8, 64>(p, stream);
+  if (p.M <= 16 || 4 * few_tiles(p.M, p.N, 16) <= 152) return launch_few_rows<T, F8, W_MN, 16>(p, stream);
+  if (p.M <= 32 || 4 * few_tiles(p.M, p.N, 32) <= 152) return launch_few_rows<T, F8, W_MN, 32>(p, stream);
+  return launch_few_rows<T, F8, W_MN, 64>(p, stream);
 }
 
 }  // namespace hstu

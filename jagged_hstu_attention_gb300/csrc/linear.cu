@@ -59,6 +59,7 @@ struct GradParams {
   const void* z;  // without an activation not read: g = dy, nothing is written but the sums
   void* g;
   float* part;  // (chunks, cols)
+  int32_t* header;
   int64_t dy_stride, rows;
   int32_t cols;
 };
@@ -69,6 +70,7 @@ struct GradParams {
 template <typename T, int ACT>
 __global__ void __launch_bounds__(kGradThreads) linear_grad_kernel(const GradParams p) {
   chain();
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) p.header[kHdrErr] = 0;  // the products behind may set it
   __shared__ float red[kGradThreads][8];
   const int groups = p.cols / 8;
   const int gy = groups >= kGradThreads ? kGradThreads : groups, rpi = kGradThreads / gy;
@@ -366,7 +368,8 @@ HSTU_API hstu_status_t hstu_attn_linear_bwd(const void* dy, int64_t dy_stride, c
   if (!aligned_to(ws, 256) || ws_bytes < l.total) return HSTU_ERR_WORKSPACE;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(ws);
-  if (cudaMemsetAsync(base, 0, kHdrWords * 4, cs) != cudaSuccess) return HSTU_ERR_CUDA;
+  const bool grads = act != HSTU_ACT_NONE || dbias;  // the kernel that makes g or its sums clears the error word
+  if ((rows == 0 || !grads) && cudaMemsetAsync(base, 0, kHdrWords * 4, cs) != cudaSuccess) return HSTU_ERR_CUDA;
   if (rows == 0) {  // no rows: dw and dbias are zero
     if (cudaMemsetAsync(dw, 0, static_cast<size_t>(in_w) * d_out, cs) != cudaSuccess ||
         (dbias && cudaMemsetAsync(dbias, 0, static_cast<size_t>(out_w), cs) != cudaSuccess))
@@ -375,8 +378,9 @@ HSTU_API hstu_status_t hstu_attn_linear_bwd(const void* dy, int64_t dy_stride, c
   }
   const void* g = dy;
   int64_t g_stride = dy_stride;
-  if (act != HSTU_ACT_NONE || dbias) {
+  if (grads) {
     GradParams gp{};
+    gp.header = reinterpret_cast<int32_t*>(base);
     gp.dy = dy;
     gp.z = act != HSTU_ACT_NONE ? z : nullptr;
     gp.g = base + l.g;
@@ -396,13 +400,27 @@ HSTU_API hstu_status_t hstu_attn_linear_bwd(const void* dy, int64_t dy_stride, c
   p.handoff_limit_ns = handoff_limit();
   p.k_splits = 1;
   // dx (rows x d_in) = g (K = d_out along its rows) w (K down its columns)
-  if (!box_map(&p.tm_a, g, rows, d_out, g_stride, dtype, 128) || !box_map(&p.tm_b, w, d_out, d_in, d_in, dtype, 64))
-    return HSTU_ERR_CUDA;
-  p.y = dx;
-  p.M = static_cast<int32_t>(rows);
-  p.N = d_in;
-  p.K = d_out;
-  if ((f16 ? launch_linear_dx_f16(p, cs) : launch_linear_dx_bf16(p, cs)) != cudaSuccess) return HSTU_ERR_CUDA;
+  if (few_rows(rows, d_in)) {
+    FewParams fp{};
+    fp.x = g;
+    fp.w = w;
+    fp.y = dx;
+    fp.header = p.header;
+    fp.x_stride = g_stride * 2;
+    fp.k_bytes = int64_t{d_out} * 2;
+    fp.M = static_cast<int32_t>(rows);
+    fp.N = d_in;
+    fp.act = HSTU_ACT_NONE;
+    if ((f16 ? launch_few_dx_f16(fp, cs) : launch_few_dx_bf16(fp, cs)) != cudaSuccess) return HSTU_ERR_CUDA;
+  } else {
+    if (!box_map(&p.tm_a, g, rows, d_out, g_stride, dtype, 128) || !box_map(&p.tm_b, w, d_out, d_in, d_in, dtype, 64))
+      return HSTU_ERR_CUDA;
+    p.y = dx;
+    p.M = static_cast<int32_t>(rows);
+    p.N = d_in;
+    p.K = d_out;
+    if ((f16 ? launch_linear_dx_f16(p, cs) : launch_linear_dx_bf16(p, cs)) != cudaSuccess) return HSTU_ERR_CUDA;
+  }
   // dw (d_out x d_in) = g^T x: K = rows, down the columns of both
   if (!box_map(&p.tm_a, g, rows, d_out, g_stride, dtype, 64) || !box_map(&p.tm_b, x, rows, d_in, x_stride, dtype, 64))
     return HSTU_ERR_CUDA;

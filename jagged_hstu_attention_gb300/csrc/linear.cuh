@@ -12,6 +12,8 @@ cudaError_t launch_linear_f16(const LinearParams& p, bool f8, cudaStream_t strea
 // The same for few rows.
 cudaError_t launch_few_bf16(const FewParams& p, bool f8, cudaStream_t stream);
 cudaError_t launch_few_f16(const FewParams& p, bool f8, cudaStream_t stream);
+cudaError_t launch_few_dx_bf16(const FewParams& p, cudaStream_t stream);
+cudaError_t launch_few_dx_f16(const FewParams& p, cudaStream_t stream);
 // dx = g w: A K-major, B MN-major.
 cudaError_t launch_linear_dx_bf16(const LinearParams& p, cudaStream_t stream);
 cudaError_t launch_linear_dx_f16(const LinearParams& p, cudaStream_t stream);
@@ -41,7 +43,10 @@ cudaError_t launch_pair_gemm(const LinearParams& p, cudaStream_t stream) {
               : launch_pair_gemm<T, false, false, false, kEpiLinear>(p, stream);                            \
   }                                                                                                         \
   cudaError_t launch_few_##SUFFIX(const FewParams& p, bool f8, cudaStream_t stream) {                       \
-    return f8 ? launch_few<T, true>(p, stream) : launch_few<T, false>(p, stream);                           \
+    return f8 ? launch_few<T, true, false>(p, stream) : launch_few<T, false, false>(p, stream);             \
+  }                                                                                                         \
+  cudaError_t launch_few_dx_##SUFFIX(const FewParams& p, cudaStream_t stream) {                             \
+    return launch_few<T, false, true>(p, stream);                                                           \
   }                                                                                                         \
   cudaError_t launch_linear_dx_##SUFFIX(const LinearParams& p, cudaStream_t stream) {                       \
     return launch_pair_gemm<T, false, false, true, kEpiPlain>(p, stream);                                   \

@@ -77,9 +77,11 @@ def test_gradient_types(dtype, grad, T, V, D, kind):
     _bwd_case(T, V, D, dtype, grad, kind, torch.int64, stride=D + 24)
 
 
-@pytest.mark.parametrize("T,V,D", [(3000, 300000, 8), (2500, 20000000, 8), (500, 511, 2056), (80000, 7, 8)])
+@pytest.mark.parametrize("T,V,D", [(3000, 300000, 8), (2500, 20000000, 8), (500, 511, 2056), (80000, 7, 8),
+                                   (4096, 4096, 16), (4097, 300, 1128), (4500, 300000, 8), (5000, 20000000, 8),
+                                   (9000, 3, 520)])
 def test_gradient_digits_and_wide_rows(T, V, D):
-    """One to three digits, rows wider than a block, long runs that a block joins."""
+    """One block's sort and one to three digits, rows wider than a block, long runs that a block joins."""
     _bwd_case(T, V, D, BF, F32 if V < 1000000 else BF, "skewed")
 
 

@@ -161,7 +161,12 @@ def test_rows_past_two_to_the_31_values():
     dx, dw, _ = hb.linear_bwd(y, None, x, w, want_dbias=False)
     for r in (slice(0, 300), slice(T - 300, T)):
         assert torch.equal(y[r], hb.linear(x[r], w, bias=b, act="silu")[0])
-        assert torch.equal(dx[r], hb.linear_bwd(y[r], None, x[r], w, want_dbias=False)[0])
+        # few rows are summed in another order: each within the bound of its sums, and rounded
+        Y, W = lt.f64(y[r]), lt.f64(w)
+        ref = Y @ W
+        err = lt.product_err(Y, W)
+        for got in (dx[r], hb.linear_bwd(y[r], None, x[r], w, want_dbias=False)[0]):
+            assert lt.worst(lt.f64(got), ref, err + _round(BF, np.abs(ref) + err)) <= 1.0
 
 
 def test_values_that_are_not_finite_stay_in_their_row():
