@@ -17,9 +17,16 @@
 namespace hstu {
 
 constexpr int kFewThreads = 256, kFewOutputs = 128, kFewRows = 64;
-// Two CTAs share an SM.
+constexpr int kFewMostStages = 5;
 template <int NT>
-constexpr int kFewStages = NT < 64 ? 4 : 3;
+constexpr int kFewStageBytes = (kFewOutputs + NT) * 128;
+template <int NT>
+constexpr int kFewMeetBytes = NT * kFewOutputs * 4;
+// K blocks in shared memory, where a CTA has as many: two CTAs share an SM up to 64
+// rows. (A block takes a CTA about 0.55 us however many are on their way, so that two
+// CTAs with three stages beat one with seven: 64 x 4096 x 4096 11.9 and 15.2 us.)
+template <int NT>
+constexpr int kFewStages = NT == 16 ? 5 : NT == 32 ? 4 : 3;
 
 struct FewParams {
   const void* x;
@@ -34,21 +41,19 @@ struct FewParams {
   int64_t x_stride, residual_stride;  // bytes; elements
   int64_t k_bytes;                    // of a row
   int32_t M, N, act;
+  int32_t stages;
 };
 
 inline int64_t few_tiles(int64_t rows, int outputs, int tile_rows) {
   return (rows + tile_rows - 1) / tile_rows * ((outputs + kFewOutputs - 1) / kFewOutputs);
 }
 
-template <int NT>
-struct FewSmem {
-  alignas(1024) uint8_t a[kFewStages<NT>][kFewOutputs * 128];
-  alignas(1024) uint8_t b[kFewStages<NT>][NT * 128];
-  float2 meet[NT / 2 * kFewOutputs];  // [CTA][pair of own rows][output]
-  alignas(8) uint64_t done[kFewStages<NT>];
+struct FewSmem {  // the stages and the sums of others lie behind
+  uint64_t done[kFewMostStages];
   uint32_t tmem_base;
   int abort_flag;
 };
+static_assert(sizeof(FewSmem) <= 256, "the space in front of the stages");
 
 __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
@@ -56,8 +61,15 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool valid
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// Waits until at most `n` of the groups committed last are on their way.
+__device__ __forceinline__ void copy_wait_all_but(int n) {
+  switch (n) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+  }
+}
 __device__ __forceinline__ void sts_cluster(uint32_t addr, uint32_t a, uint32_t b) {
   asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
@@ -102,9 +114,11 @@ __device__ __forceinline__ void copy_block_mn(uint32_t dst, const uint8_t* src, 
 template <typename T, bool F8, bool W_MN, int NT>
 __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams p) {
   extern __shared__ uint8_t smem_raw[];
-  FewSmem<NT>& s = *reinterpret_cast<FewSmem<NT>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // [stages: A 16 KB, B], sums [CTA][pair of own rows][output], barriers
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float2* meet = reinterpret_cast<float2*>(base + p.stages * kFewStageBytes<NT>);
+  FewSmem& s = *reinterpret_cast<FewSmem*>(reinterpret_cast<uint8_t*>(meet) + kFewMeetBytes<NT>);
   constexpr int kColumns = NT < 32 ? 32 : NT;  // of TMEM
-  constexpr int kStagesHere = kFewStages<NT>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = gridDim.x, rank = blockIdx.x;  // the cluster lies along x
   const int n0 = blockIdx.y * kFewOutputs, m0 = blockIdx.z * NT;
@@ -113,7 +127,7 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams p
   const int blocks = static_cast<int>(static_cast<int64_t>(nk) * (rank + 1) / split) - kb0;  // one at least
   if (threadIdx.x == 0) {
     s.abort_flag = 0;
-    for (int i = 0; i < kStagesHere; ++i) mbar_init(smem_u32(&s.done[i]), 1);
+    for (int i = 0; i < p.stages; ++i) mbar_init(smem_u32(&s.done[i]), 1);
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -127,36 +141,46 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams p
   chain();
 
   const uint8_t *x = static_cast<const uint8_t*>(p.x), *w = static_cast<const uint8_t*>(p.w);
-  auto load = [&](int j) {
-    if (j < blocks) {
-      if (W_MN) copy_block_mn(smem_u32(s.a[j % kStagesHere]), w, n0, p.N, p.k_bytes / 2, kb0 + j);
-      else copy_block<kFewOutputs>(smem_u32(s.a[j % kStagesHere]), w, p.k_bytes, n0, p.N, p.k_bytes, kb0 + j);
-      copy_block<NT>(smem_u32(s.b[j % kStagesHere]), x, p.x_stride, m0, p.M, p.k_bytes, kb0 + j);
+  const uint32_t ring = smem_u32(base);
+  auto stage_of = [&](int st) { return ring + st * kFewStageBytes<NT>; };
+  int loaded = 0, load_st = 0;  // blocks on their way; the stage of the next
+  auto load = [&] {
+    if (loaded < blocks) {
+      const uint32_t a = stage_of(load_st);
+      if (W_MN) copy_block_mn(a, w, n0, p.N, p.k_bytes / 2, kb0 + loaded);
+      else copy_block<kFewOutputs>(a, w, p.k_bytes, n0, p.N, p.k_bytes, kb0 + loaded);
+      copy_block<NT>(a + kFewOutputs * 128, x, p.x_stride, m0, p.M, p.k_bytes, kb0 + loaded);
     }
+    ++loaded;
+    if (++load_st == p.stages) load_st = 0;
     copy_commit();
   };
-  for (int j = 0; j < kStagesHere - 1; ++j) load(j);
+  for (int j = 0; j < p.stages - 1; ++j) load();
   constexpr uint32_t idesc = idesc_f16kind(kFewOutputs, NT, W_MN, false, F8 ? 0u : Elem<T>::kUmma);
   bool ok = true;
+  int st = 0, phase = 0, before = 0, before_phase = 0;  // of this block and the one before
   for (int j = 0; j < blocks; ++j) {
-    copy_wait<kStagesHere - 2>();
+    copy_wait_all_but(p.stages - 2);
     fence_async_smem();
     ok = __syncthreads_and(ok);  // block j has arrived; all agree whether to go on
     if (!ok) break;
     if (warp == 0 && elect_one_sync()) {
-      const uint32_t a = smem_u32(s.a[j % kStagesHere]), b = smem_u32(s.b[j % kStagesHere]);
+      const uint32_t a = stage_of(st), b = a + kFewOutputs * 128;
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
         umma_one<F8>(tacc, block_desc<W_MN>(a, kk), block_desc<false>(b, kk), idesc, j > 0 || kk > 0 ? 1u : 0u);
-      umma_commit(smem_u32(&s.done[j % kStagesHere]));
+      umma_commit(smem_u32(&s.done[st]));
     }
     __syncwarp();
     // The block before has been multiplied: its stage takes the next one to come.
-    if (j > 0) ok = mbar_wait(smem_u32(&s.done[(j - 1) % kStagesHere]), ((j - 1) / kStagesHere) & 1, &s.abort_flag);
-    if (ok) load(j + kStagesHere - 1);
+    if (j > 0) ok = mbar_wait(smem_u32(&s.done[before]), before_phase, &s.abort_flag);
+    if (ok) load();
+    before = st;
+    before_phase = phase;
+    if (++st == p.stages) st = 0, phase ^= 1;
   }
-  copy_wait<0>();
-  if (ok) ok = mbar_wait(smem_u32(&s.done[(blocks - 1) % kStagesHere]), ((blocks - 1) / kStagesHere) & 1, &s.abort_flag);
+  copy_wait_all_but(0);
+  if (ok) ok = mbar_wait(smem_u32(&s.done[before]), before_phase, &s.abort_flag);
   ok = __syncthreads_and(ok);
   tc_fence_after();
   // Rows [c own, (c + 1) own) of the tile are CTA c's: sums of pairs of rows, an output
@@ -171,8 +195,9 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams p
 #pragma unroll
     for (int e = 0; e < kHalf; e += 2) {
       const int row = c0 + e, at = rank * own + row % own;
-      const uint32_t lo = NT < 64 && warp >= 4 ? a[(kHalf + e) & 31] : a[e], hi = NT < 64 && warp >= 4 ? a[(kHalf + e + 1) & 31] : a[e + 1];
-      sts_cluster(in_cta(smem_u32(&s.meet[at / 2 * kFewOutputs + output]), row / own), lo, hi);
+      const bool second = NT < 64 && warp >= 4;  // the columns of both halves were read
+      sts_cluster(in_cta(smem_u32(&meet[at / 2 * kFewOutputs + output]), row / own), second ? a[(kHalf + e) & 31] : a[e],
+                  second ? a[(kHalf + e + 1) & 31] : a[e + 1]);
     }
   }
   const int output = threadIdx.x % kFewOutputs, col = n0 + output;
@@ -201,7 +226,7 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams p
     uint64_t v = pair_of(0.0f, 0.0f);
 #pragma unroll 8
     for (int c = 0; c < split; ++c) {
-      const float2 f = s.meet[(c * own / 2 + j) * kFewOutputs + output];
+      const float2 f = meet[(c * own / 2 + j) * kFewOutputs + output];
       v = pair_add(v, pair_of(f.x, f.y));
     }
     if (F8)
@@ -224,19 +249,41 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams p
   if (threadIdx.x == 0 && s.abort_flag && p.header) atomicOr(p.header + kHdrErr, kErrTimeout);
 }
 
+// Rows of a tile, and K's splits over a cluster, eight at most: until there is a CTA for
+// each SM, or two where a CTA keeps four blocks. The cost is a model of the measured time
+// in units of 10 ns: launch, meeting sums, blocks one after the other, slower where two
+// CTAs share an SM. (64 rows: 512 x 2048 takes 5.1 us with tiles of 32 rows, 6.0 us with 64;
+// 4096 x 4096 13.7 and 11.8. Tiles of 128 rows gained nothing: 384 x 8192 x 1024 26.1 us, 26.0 with 64.)
+struct FewPlan {
+  int rows_tile = 0, split = 1;
+  int64_t cost = INT64_MAX;
+};
+inline FewPlan few_plan(int64_t rows, int outputs, int64_t k_bytes) {
+  FewPlan best;
+  const int64_t nk = (k_bytes + 127) / 128;
+  for (int nt = 16; nt <= kFewRows; nt *= 2) {
+    const int64_t tiles = few_tiles(rows, outputs, nt);
+    int split = 1;
+    while (split < 8 && 2 * split <= nk && tiles * split * 2 <= (nk / (2 * split) >= 4 ? 304 : 152)) split *= 2;
+    const int64_t ctas = tiles * split, blocks = (nk + split - 1) / split, waves = (ctas + 303) / 304;
+    const int64_t block = (nt < 64 ? 55 : 70) * (ctas > 152 ? 13 : 10) / 10;
+    const int64_t cost = 330 + waves * ((nt <= 32 ? 3 * nt - 15 : 185) + blocks * block);
+    if (cost < best.cost) best = FewPlan{nt, split, cost};
+  }
+  return best;
+}
+
 template <typename T, bool F8, bool W_MN, int NT>
-cudaError_t launch_few_rows(const FewParams& p, cudaStream_t stream) {
-  const int smem = static_cast<int>(sizeof(FewSmem<NT>)) + 1024;
+cudaError_t launch_few_rows(const FewParams& given, int split, cudaStream_t stream) {
+  FewParams p = given;
+  const int64_t nk = (p.k_bytes + 127) / 128, blocks = (nk + split - 1) / split;
+  p.stages = static_cast<int>(blocks < 2 ? 2 : (blocks < kFewStages<NT> ? blocks : kFewStages<NT>));
+  const int smem = p.stages * kFewStageBytes<NT> + kFewMeetBytes<NT> + 256 + 1024;
   static std::atomic<uint64_t> configured{0};
   auto kernel = few_rows_kernel<T, F8, W_MN, NT>;
-  const cudaError_t e = ensure_smem_limit(kernel, smem, configured);
+  const cudaError_t e =
+      ensure_smem_limit(kernel, kFewStages<NT> * kFewStageBytes<NT> + kFewMeetBytes<NT> + 256 + 1024, configured);
   if (e != cudaSuccess) return e;
-  // K is split until there are as many CTAs as SMs, eight ways at most; twice as many
-  // where a CTA still has four blocks then (64 x 2048 x 2048: 7.7 us so, 8.3 us split
-  // four ways; 64 x 512 x 2048: 5.8 and 5.4).
-  const int64_t nk = (p.k_bytes + 127) / 128, tiles = few_tiles(p.M, p.N, NT);
-  int split = 1;
-  while (split < 8 && 2 * split <= nk && tiles * split * 2 <= (nk / (2 * split) >= 4 ? 2 * 152 : 152)) split *= 2;
   cudaLaunchAttribute attrs[2]{};
   attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attrs[0].val.programmaticStreamSerializationAllowed = 1;
@@ -251,14 +298,14 @@ cudaError_t launch_few_rows(const FewParams& p, cudaStream_t stream) {
   config.numAttrs = 2;
   return cudaLaunchKernelEx(&config, kernel, p);
 }
-// Fewer rows a tile, whose sums take less time to meet, where all tiles, split four
-// ways, still fit the SMs (64 x 512 x 2048: 5.4 us with tiles of 32 rows, 6.1 us with
-// 64; 64 x 4096 x 4096: 13.9 and 11.9).
 template <typename T, bool F8, bool W_MN>
 cudaError_t launch_few(const FewParams& p, cudaStream_t stream) {
-  if (p.M <= 16 || 4 * few_tiles(p.M, p.N, 16) <= 152) return launch_few_rows<T, F8, W_MN, 16>(p, stream);
-  if (p.M <= 32 || 4 * few_tiles(p.M, p.N, 32) <= 152) return launch_few_rows<T, F8, W_MN, 32>(p, stream);
-  return launch_few_rows<T, F8, W_MN, 64>(p, stream);
+  const FewPlan plan = few_plan(p.M, p.N, p.k_bytes);
+  switch (plan.rows_tile) {
+    case 16: return launch_few_rows<T, F8, W_MN, 16>(p, plan.split, stream);
+    case 32: return launch_few_rows<T, F8, W_MN, 32>(p, plan.split, stream);
+    default: return launch_few_rows<T, F8, W_MN, 64>(p, plan.split, stream);
+  }
 }
 
 }  // namespace hstu

@@ -213,10 +213,16 @@ hstu_status_t linear_checks(int64_t rows, int d_in, int d_out, int act, bool cod
   return HSTU_OK;
 }
 
-// Whether a product goes to the kernel for few rows: up to 64 always, more while its
-// tiles leave half of the SMs for K's splits. (512 x 2048: 256 rows take 7.3 us there and 7.7 us on pairs of
-// SMs, 384 rows 8.2 and 7.8; 2048 x 2048: 256 rows 11 and 15 us, 384 rows 15.4 and 14.9.)
-bool few_rows(int64_t rows, int d_out) { return rows <= kFewRows || few_tiles(rows, d_out, kFewRows) <= 152 / 2; }
+// Whether a product goes to the kernel for few rows: where its model of the time is below
+// that of pairs of SMs (512 x 2048: 64 rows take 5.3 us there and 6.5 us on pairs, 512 rows 12.7
+// and 7.7; 4096 x 4096: 64 rows 11.9 and 23 us, 384 rows 49 and 24), and its tiles run
+// at the same time, or there are no more rows than one tile may have.
+bool few_rows(int64_t rows, int outputs, int64_t k_bytes) {
+  const int64_t tiles = (rows + kTileM - 1) / kTileM * ((outputs + kTileN - 1) / kTileN), nk = (k_bytes + 127) / 128;
+  const int64_t pairs = 330 + (tiles + kPairs - 1) / kPairs * (150 + 31 * nk);
+  const FewPlan plan = few_plan(rows, outputs, k_bytes);
+  return plan.cost <= pairs && (rows <= kFewRows || few_tiles(rows, outputs, plan.rows_tile) <= 152);
+}
 
 // Splits of dw's K: those that leave the fewest tiles' time on the busiest pair, counting
 // each split's fp32 tile (written, read) as two of its 64-row blocks.
@@ -294,7 +300,7 @@ HSTU_API hstu_status_t hstu_attn_linear(const void* x, int64_t x_stride, const u
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (ws && cudaMemsetAsync(ws, 0, kHdrWords * 4, cs) != cudaSuccess) return HSTU_ERR_CUDA;
   if (rows == 0) return HSTU_OK;
-  if (few_rows(rows, d_out)) {
+  if (few_rows(rows, d_out, int64_t{d_in} * xe)) {
     FewParams p{};
     p.x = x;
     p.w = w;
@@ -400,7 +406,7 @@ HSTU_API hstu_status_t hstu_attn_linear_bwd(const void* dy, int64_t dy_stride, c
   p.handoff_limit_ns = handoff_limit();
   p.k_splits = 1;
   // dx (rows x d_in) = g (K = d_out along its rows) w (K down its columns)
-  if (few_rows(rows, d_in)) {
+  if (few_rows(rows, d_in, int64_t{d_out} * 2)) {
     FewParams fp{};
     fp.x = g;
     fp.w = w;
