@@ -18,7 +18,8 @@
 //   - rows of the table that no token names are zeroed by further blocks of the
 //     sorting and summing kernels, which know them by a bit a row that the first
 //     pass set; every row of the table is so written once, and the sort, which
-//     moves little, hides behind the zeros.
+//     moves little, hides behind the zeros;
+//   - up to 4096 tokens are sorted by one block of one launch.
 #include <algorithm>
 
 #include "layer.cuh"
@@ -124,7 +125,7 @@ cudaError_t launch_embed_typed(const EmbedParams& p, int table_dtype, int dtype,
 // Rows [row0, row1) of the table, those that no token names, as 16-byte units.
 struct FillParams {
   void* table;
-  const uint32_t* named;  // a bit a row
+  const uint32_t* named;  // a bit a row; null: all rows
   int64_t row0, row1;
   uint64_t per_unit;  // 2^32 / units, rounded up: u per_unit / 2^32 is u / units for what a block has
   int32_t units;      // of a row, 2^14 at most
@@ -137,7 +138,7 @@ __device__ __forceinline__ void fill_rows(const FillParams& p, int64_t block) {
   __shared__ uint32_t bits[kFillMostRows / 32 + 1];
   const int64_t v0 = p.row0 + block * p.rows, v1 = min(v0 + p.rows, p.row1), w0 = v0 >> 5;
   // The rows' bits first, so that no store waits for a load.
-  for (int64_t w = w0 + threadIdx.x; w <= (v1 - 1) >> 5; w += blockDim.x) bits[w - w0] = p.named[w];
+  for (int64_t w = w0 + threadIdx.x; w <= (v1 - 1) >> 5; w += blockDim.x) bits[w - w0] = p.named ? p.named[w] : 0u;
   __syncthreads();
   const uint32_t units = static_cast<uint32_t>(v1 - v0) * p.units, first = static_cast<uint32_t>(v0 & 31);
   uint4* base = static_cast<uint4*>(p.table) + v0 * p.units;
@@ -293,51 +294,101 @@ __global__ void __launch_bounds__(kSortThreads) sort_move_kernel(const SortParam
   }
 }
 
-// Few tokens in one launch, 6 us for 208 (two for each digit take 10; 2048 tokens in a
-// block took 18): a block sorts (id, token) pairs as 64-bit numbers in shared
-// memory (a bitonic network; steps inside a warp's 64 pairs need no barrier), and sets the
-// rows' bits, which it clears itself where they are not too many.
-constexpr int kSmallTokens = 512, kSmallThreads = 256;
-constexpr int64_t kSmallBits = 1 << 18;
+// Few tokens in one launch (1889 tokens forward and backward take 20 us, 29 us with two
+// launches a digit): a block keeps its pairs in registers, kBlockRounds a thread, and
+// turns them over in shared memory once a digit. A pair's place is that of its digit and
+// warp plus the number of the warp's pairs of the digit before it. The other blocks zero
+// the table, named rows too, which are few and are written after.
+constexpr int kBlockThreads = 1024, kBlockWarps = kBlockThreads / 32, kBlockRounds = 4;
+constexpr int kBlockTokens = kBlockThreads * kBlockRounds;
+constexpr int kBlockSmem = kBlockTokens * 8 + kBlockWarps * kMaxBins * 2;
 template <typename ID>
-__global__ void __launch_bounds__(kSmallThreads) sort_small_kernel(const SortParams p, int count, bool clear) {
+__global__ void __launch_bounds__(kBlockThreads) sort_block_kernel(const SortParams p, int passes) {
   chain();
-  __shared__ uint64_t pairs[kSmallTokens];
-  if (clear) {
-    for (int64_t w = threadIdx.x; w < (p.vocab + 31) / 32; w += kSmallThreads) p.named[w] = 0;
-    if (threadIdx.x < kHdrWords) p.header[threadIdx.x] = 0;
+  if (blockIdx.x > 0) return fill_rows(p.fill, blockIdx.x - 1);
+  extern __shared__ uint4 sort_smem[];
+  uint16_t(*place)[kMaxBins] = reinterpret_cast<uint16_t(*)[kMaxBins]>(sort_smem);
+  uint2* pairs = reinterpret_cast<uint2*>(sort_smem + kBlockWarps * kMaxBins * 2 / 16);
+  __shared__ uint32_t warp_sum[kBlockWarps];
+  const int n = static_cast<int>(p.n), rounds = (n + kBlockThreads - 1) / kBlockThreads;
+  const int bins = 1 << p.bits, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int i0 = warp * rounds * 32 + lane;
+  if (threadIdx.x < kHdrWords) p.header[threadIdx.x] = 0;
+  uint32_t key[kBlockRounds];
+  int32_t val[kBlockRounds];
+  bool past = false;  // an id past the table
+#pragma unroll
+  for (int r = 0; r < kBlockRounds; ++r) {
+    const int i = i0 + 32 * r;
+    val[r] = i;
+    key[r] = 0;
+    if (r < rounds && i < n) {
+      key[r] = sort_key<ID, true>(p, i);
+      past |= key[r] == p.vocab && static_cast<int64_t>(static_cast<const ID*>(p.ids)[i]) >= 0;
+    }
+  }
+  for (int s = 0; s < passes; ++s) {
+    for (int i = threadIdx.x; i < kBlockWarps * kMaxBins * 2 / 16; i += kBlockThreads) sort_smem[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
-  }
-  for (int i = threadIdx.x; i < count; i += kSmallThreads) {
-    uint64_t pair = ~uint64_t{0};
-    if (i < p.n) {
-      const uint32_t key = sort_key<ID, true>(p, i);
-      pair = (static_cast<uint64_t>(key) << 32) | static_cast<uint32_t>(i);
-      if (key < p.vocab) atomicOr(p.named + (key >> 5), 1u << (key & 31));
-      else if (static_cast<int64_t>(static_cast<const ID*>(p.ids)[i]) >= 0) atomicOr(p.header + kHdrErr, kErrInput);
-    }
-    pairs[i] = pair;
-  }
-  __syncthreads();
-  for (int k = 2; k <= count; k *= 2)
-    for (int j = k / 2; j > 0; j /= 2) {
-      for (int t = threadIdx.x; t < count / 2; t += kSmallThreads) {
-        const int a = 2 * t - (t & (j - 1)), b = a + j;
-        const uint64_t x = pairs[a], y = pairs[b];
-        if ((x > y) == ((a & k) == 0)) {
-          pairs[a] = y;
-          pairs[b] = x;
-        }
+    uint32_t digit[kBlockRounds], nth[kBlockRounds];
+#pragma unroll
+    for (int r = 0; r < kBlockRounds; ++r) {
+      const bool mine = r < rounds && i0 + 32 * r < n;
+      const uint32_t live = __ballot_sync(0xffffffffu, mine);
+      digit[r] = nth[r] = 0;
+      if (mine) {
+        digit[r] = (key[r] >> (s * p.bits)) & (bins - 1);
+        const uint32_t same = __match_any_sync(live, digit[r]);
+        nth[r] = place[warp][digit[r]] + __popc(same & ((1u << lane) - 1u));
+        __syncwarp(live);
+        if (lane == 31 - __clz(same)) place[warp][digit[r]] = static_cast<uint16_t>(nth[r] + 1);
       }
-      // Steps of up to 32 stay within a warp's 64 pairs.
-      if (j >= 64 || (j == 1 && k >= 64)) __syncthreads();
-      else __syncwarp();
+      __syncwarp();
     }
-  __syncthreads();
-  for (int i = threadIdx.x; i < p.n; i += kSmallThreads) {
-    p.key_out[i] = static_cast<uint32_t>(pairs[i] >> 32);
-    p.val_out[i] = static_cast<int32_t>(pairs[i]);
+    __syncthreads();
+    // Thread b: where digit b's pairs of each warp begin.
+    uint32_t total = 0;
+    if (threadIdx.x < bins)
+#pragma unroll
+      for (int w = 0; w < kBlockWarps; ++w) total += place[w][threadIdx.x];
+    uint32_t sum = total;  // of digits up to this one
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const uint32_t o = __shfl_up_sync(0xffffffffu, sum, off);
+      if (lane >= off) sum += o;
+    }
+    if (lane == 31) warp_sum[warp] = sum;
+    __syncthreads();
+    uint32_t at = sum - total;
+    if (threadIdx.x < bins) {
+      for (int w = 0; w < warp; ++w) at += warp_sum[w];
+#pragma unroll
+      for (int w = 0; w < kBlockWarps; ++w) {
+        const uint32_t c = place[w][threadIdx.x];
+        place[w][threadIdx.x] = static_cast<uint16_t>(at);
+        at += c;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kBlockRounds; ++r)
+      if (r < rounds && i0 + 32 * r < n) pairs[place[warp][digit[r]] + nth[r]] = make_uint2(key[r], static_cast<uint32_t>(val[r]));
+    __syncthreads();
+    if (s + 1 < passes)
+#pragma unroll
+      for (int r = 0; r < kBlockRounds; ++r)
+        if (r < rounds && i0 + 32 * r < n) {
+          const uint2 q = pairs[i0 + 32 * r];
+          key[r] = q.x;
+          val[r] = static_cast<int32_t>(q.y);
+        }
   }
+  for (int i = threadIdx.x; i < n; i += kBlockThreads) {
+    const uint2 q = pairs[i];
+    p.key_out[i] = q.x;
+    p.val_out[i] = static_cast<int32_t>(q.y);
+  }
+  if (past) atomicOr(p.header + kHdrErr, kErrInput);
 }
 
 // ----------------------------------------------------------------- backward
@@ -626,18 +677,23 @@ template <typename ID>
 cudaError_t launch_sort(SortParams p, FillParams& fill, uint8_t* base, const EmbedLayout& l, int& last,
                         cudaStream_t stream) {
   const int64_t all = fill.row1 - fill.row0;
-  if (p.n <= kSmallTokens) {
-    int count = 2;
-    while (count < p.n) count *= 2;
-    p.key_out = reinterpret_cast<uint32_t*>(base + l.key[0]);
-    p.val_out = reinterpret_cast<int32_t*>(base + l.val[0]);
-    last = 0;
-    return launch_chained(sort_small_kernel<ID>, dim3(1), kSmallThreads, 0, stream, p, count, p.vocab <= kSmallBits);
-  }
   int bits = 1;
   while ((p.vocab >> bits) != 0) ++bits;  // of the largest key, vocab
   const int passes = (bits + kMaxDigitBits - 1) / kMaxDigitBits;
   p.bits = (bits + passes - 1) / passes;
+  if (p.n <= kBlockTokens) {
+    p.key_out = reinterpret_cast<uint32_t*>(base + l.key[0]);
+    p.val_out = reinterpret_cast<int32_t*>(base + l.val[0]);
+    last = 0;
+    static std::atomic<uint64_t> configured{0};
+    const cudaError_t e = ensure_smem_limit(sort_block_kernel<ID>, kBlockSmem, configured);
+    if (e != cudaSuccess) return e;
+    p.fill = fill;
+    p.fill.named = nullptr;
+    fill.row0 = fill.row1;
+    return launch_chained(sort_block_kernel<ID>, dim3(static_cast<unsigned>(1 + fill_blocks(p.fill))), kBlockThreads,
+                          kBlockSmem, stream, p, passes);
+  }
   const int parts = 4 * passes + 2 * (passes - 1) + 6;
   const int64_t rounds = (p.n + int64_t{kSortTiles} * kSortThreads - 1) / (int64_t{kSortTiles} * kSortThreads);
   p.tile = static_cast<int32_t>(rounds * kSortThreads);
@@ -763,9 +819,8 @@ HSTU_API hstu_status_t hstu_attn_embed_bwd(const void* dy, int64_t dy_stride, in
   if (!aligned_to(ws, 256) || ws_bytes < l.total) return HSTU_ERR_WORKSPACE;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(ws);
-  // The error word and the bits of the rows. (A sort in one block clears few of them itself.)
-  if ((tokens == 0 || tokens > kSmallTokens || vocab > kSmallBits) &&
-      cudaMemsetAsync(base, 0, l.key[0], cs) != cudaSuccess)
+  // The error word and the bits of the rows. (A sort in one block needs no bits.)
+  if ((tokens == 0 || tokens > kBlockTokens) && cudaMemsetAsync(base, 0, l.key[0], cs) != cudaSuccess)
     return HSTU_ERR_CUDA;
   cudaError_t e = cudaSuccess;
   FillParams fill{};
