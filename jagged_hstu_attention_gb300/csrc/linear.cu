@@ -9,7 +9,9 @@
 //             parts are added in order.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "layer.cuh"
 #include "linear.cuh"
@@ -18,15 +20,33 @@ namespace hstu {
 namespace {
 
 constexpr int kGradThreads = 256;
-// Rows are split into at most kGradChunks chunks of at least kGradMinRows (one block
-// each); a chunk's column sums are the bias gradient's parts.
-constexpr int kGradChunks = 152 * 4, kGradMinRows = 32;
+constexpr int kGradChunks = 152 * 4;
+constexpr int kGradRows = 4;  // of a thread, on their way at once
 constexpr int kMaxKSplits = 16;
 constexpr int kPairs = 76;
 
-inline int grad_chunks(int64_t rows) {
-  const int64_t c = (rows + kGradMinRows - 1) / kGradMinRows;
-  return static_cast<int>(c < kGradChunks ? c : kGradChunks);
+// The blocks of the activation's gradient: rows in chunks of at least kGradRows a thread,
+// all columns a block where those are blocks enough, else columns evenly in parts of 512, and
+// chunks of fewer rows until there is a block for each SM. (33047 rows of 3584 columns
+// take 109 us in whole rows and 115 us in parts, 61 rows of 2584 columns 23 us and 3.9. Half as many
+// chunks of 3584 columns, all on their way at once, took the backward 240 us, not 202.) A chunk's
+// column sums are one part of the bias gradient.
+struct GradGrid {
+  int col_blocks, groups, rows_at_once, chunks;
+};
+inline GradGrid grad_grid(int64_t rows, int cols) {
+  auto up = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
+  GradGrid g;
+  for (int widest = kGradThreads; widest >= kGradThreads / 4; widest /= 4) {
+    g.col_blocks = static_cast<int>(up(cols / 8, widest));
+    g.groups = static_cast<int>(up(cols / 8, g.col_blocks));
+    g.rows_at_once = kGradThreads / g.groups;
+    const int64_t few = std::max(152 / g.col_blocks, 1);
+    const int64_t full = up(rows, kGradRows * g.rows_at_once), thin = std::min(up(rows, g.rows_at_once), few);
+    g.chunks = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kGradChunks, std::max(full, thin))));
+    if (full * g.col_blocks >= kGradChunks) break;
+  }
+  return g;
 }
 
 // dy act'(z) of a pair: with p = 1 / (1 + exp(-u)), act' = p (1 + z (1 - p) u').
@@ -62,22 +82,19 @@ struct GradParams {
   int32_t* header;
   int64_t dy_stride, rows;
   int32_t cols;
+  int32_t groups, rows_at_once;
 };
 
-// A block takes a chunk of rows; its threads cover as many rows of all columns at
-// a time as there are, 8 columns a thread (256 groups of columns a block where
-// there are more), two rows in flight.
+// A block takes a chunk of rows of its columns, 8 columns a thread, kGradRows rows on their way.
 template <typename T, int ACT>
-__global__ void __launch_bounds__(kGradThreads) linear_grad_kernel(const GradParams p) {
+__global__ void __launch_bounds__(kGradThreads, 4) linear_grad_kernel(const GradParams p) {
   chain();
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) p.header[kHdrErr] = 0;  // the products behind may set it
-  __shared__ float red[kGradThreads][8];
-  const int groups = p.cols / 8;
-  const int gy = groups >= kGradThreads ? kGradThreads : groups, rpi = kGradThreads / gy;
-  const int lane_row = threadIdx.x / gy, cg = blockIdx.y * gy + threadIdx.x % gy;
-  const bool active = lane_row < rpi && cg < groups;
-  const int col = cg * 8;
-  const int64_t per = (p.rows + gridDim.x - 1) / gridDim.x;
+  __shared__ float red[8][kGradThreads];
+  const int gy = p.groups, rpi = p.rows_at_once;
+  const int lane_row = threadIdx.x / gy, col = (blockIdx.y * gy + threadIdx.x % gy) * 8;
+  const bool active = lane_row < rpi && col < p.cols;
+  const int64_t step = int64_t{rpi} * gridDim.x, per = (p.rows + step - 1) / step * rpi;
   const int64_t r0 = static_cast<int64_t>(blockIdx.x) * per, r1 = min(r0 + per, p.rows);
   uint64_t sums[4] = {};
   auto one = [&](uint4 zv, uint4 dv, int64_t r) {
@@ -100,32 +117,37 @@ __global__ void __launch_bounds__(kGradThreads) linear_grad_kernel(const GradPar
     auto load_z = [&](int64_t r) {
       return ACT != HSTU_ACT_NONE ? *reinterpret_cast<const uint4*>(z + r * p.cols) : make_uint4(0, 0, 0, 0);
     };
-    int64_t r = r0 + lane_row;
-    constexpr int kRows = 4;
-    for (; r + (kRows - 1) * rpi < r1; r += kRows * rpi) {
-      uint4 zv[kRows], dv[kRows];
+    auto some = [&](int64_t r, auto all) {  // kGradRows rows, or those there are
+      uint4 zv[kGradRows], dv[kGradRows];
 #pragma unroll
-      for (int k = 0; k < kRows; ++k) {
-        zv[k] = load_z(r + k * rpi);
-        dv[k] = *reinterpret_cast<const uint4*>(dy + (r + k * rpi) * p.dy_stride);
+      for (int k = 0; k < kGradRows; ++k) {
+        const int64_t row = r + k * rpi;
+        if (!all && row >= r1) break;
+        zv[k] = load_z(row);
+        dv[k] = *reinterpret_cast<const uint4*>(dy + row * p.dy_stride);
       }
 #pragma unroll
-      for (int k = 0; k < kRows; ++k) one(zv[k], dv[k], r + k * rpi);
-    }
-    for (; r < r1; r += rpi) one(load_z(r), *reinterpret_cast<const uint4*>(dy + r * p.dy_stride), r);
+      for (int k = 0; k < kGradRows; ++k)
+        if (all || r + k * rpi < r1) one(zv[k], dv[k], r + k * rpi);
+    };
+    int64_t r = r0 + lane_row;
+    for (; r + (kGradRows - 1) * rpi < r1; r += kGradRows * rpi) some(r, std::true_type{});
+    if (r < r1) some(r, std::false_type{});
   }
   float sum[8];
 #pragma unroll
   for (int e = 0; e < 4; ++e) pair_split(sums[e], sum[2 * e], sum[2 * e + 1]);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) red[threadIdx.x][e] = sum[e];
+  for (int e = 0; e < 8; ++e) red[e][threadIdx.x] = sum[e];
   __syncthreads();
-  if (active && lane_row == 0) {
-    for (int l = 1; l < rpi; ++l)
+  // Rows of threads meet in halves (32163 rows of 16 columns have 128 of them).
+  for (int s = 1 << (31 - __clz(max(rpi - 1, 1))); s > 0; s >>= 1) {
+    if (lane_row < s && lane_row + s < rpi)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum[e] += red[l * gy + threadIdx.x][e];
-    store8(p.part + static_cast<int64_t>(blockIdx.x) * p.cols + col, sum);
+      for (int e = 0; e < 8; ++e) red[e][threadIdx.x] = sum[e] += red[e][threadIdx.x + s * gy];
+    __syncthreads();
   }
+  if (active && lane_row == 0) store8(p.part + static_cast<int64_t>(blockIdx.x) * p.cols + col, sum);
 }
 
 // Ends the backward: dw from the fp32 parts of K's splits in order, 8 elements a
@@ -249,15 +271,18 @@ LinearLayout linear_layout(int64_t rows, int d_in, int d_out, int act) {
   LinearLayout l;
   l.g = kHdrWords * 4;
   l.part = l.g + (act != HSTU_ACT_NONE ? align_up(static_cast<size_t>(rows) * d_out * 2, 256) : 0);
-  l.dw = l.part + align_up(static_cast<size_t>(grad_chunks(rows)) * d_out * 4, 256);
+  l.dw = l.part + align_up(static_cast<size_t>(grad_grid(rows, d_out).chunks) * d_out * 4, 256);
   const int splits = dw_splits(rows, d_in, d_out);
   l.total = l.dw + (splits > 1 ? align_up(static_cast<size_t>(splits) * d_out * d_in * 4, 256) : 0);
   return l;
 }
 
 template <typename T>
-cudaError_t launch_grad(const GradParams& p, int act, cudaStream_t stream) {
-  const dim3 grid(grad_chunks(p.rows), (p.cols / 8 + kGradThreads - 1) / kGradThreads);
+cudaError_t launch_grad(GradParams p, int act, cudaStream_t stream) {
+  const GradGrid g = grad_grid(p.rows, p.cols);
+  p.groups = g.groups;
+  p.rows_at_once = g.rows_at_once;
+  const dim3 grid(g.chunks, g.col_blocks);
   auto kernel = act == HSTU_ACT_SILU   ? linear_grad_kernel<T, HSTU_ACT_SILU>
                 : act == HSTU_ACT_GELU ? linear_grad_kernel<T, HSTU_ACT_GELU>
                 : act == HSTU_ACT_RELU ? linear_grad_kernel<T, HSTU_ACT_RELU>
@@ -445,7 +470,7 @@ HSTU_API hstu_status_t hstu_attn_linear_bwd(const void* dy, int64_t dy_stride, c
   fp.dbias = dbias;
   fp.elems = int64_t{d_out} * d_in;
   fp.splits = p.k_splits;
-  fp.chunks = grad_chunks(rows);
+  fp.chunks = grad_grid(rows, d_out).chunks;
   fp.cols = d_out;
   fp.dw_blocks = p.k_splits > 1 ? static_cast<int32_t>((fp.elems / 8 + kFoldThreads - 1) / kFoldThreads) : 0;
   const dim3 grid(static_cast<unsigned>(fp.dw_blocks + (dbias ? (d_out + 31) / 32 : 0)));

@@ -105,7 +105,7 @@ def test_eight_bit_rows_of_a_wider_matrix():
 
 
 @pytest.mark.parametrize("T,K,N", SIZES + [(5000, 264, 72), (20000, 40, 8), (9001, 512, 200), (41000, 256, 136),
-                                           (4097, 504, 328), (4500, 520, 96)])
+                                           (4097, 504, 328), (4500, 520, 96), (61, 72, 2584), (700, 16, 1056)])
 @pytest.mark.parametrize("act,dtype", [("none", BF), ("silu", BF), ("gelu", F16), ("relu", F16)])
 def test_gradients(T, K, N, act, dtype):
     x, w, b, _ = _inputs(T, K, N, dtype, seed=11, pad=8)
