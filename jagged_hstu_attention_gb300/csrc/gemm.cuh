@@ -8,7 +8,8 @@
 // takes tiles in turn, N fastest, so that pairs running together share A's rows and
 // B stays in L2. 128-byte deep K blocks (64 16-bit or 128 8-bit values) flow through
 // a ring of five TMA stages that runs on across tiles; two 256-column accumulators, so
-// that sixteen epilogue warps read one out while the next is computed.
+// that sixteen epilogue warps read one out while the next is computed. Products of few
+// tiles take tiles of 256 x 128, which more pairs share.
 //
 // An operand is K-major when K runs along its tensor's rows, MN-major when K runs
 // down its columns (boxes of 64 columns x 64 rows, 16-bit only).
@@ -23,9 +24,12 @@
 
 namespace hstu {
 
-constexpr int kTileM = 256, kTileN = 256;        // of a pair
-constexpr int kStages = 5;
-constexpr int kStageOperand = 128 * 128;         // bytes of A and of B in a stage of one CTA
+constexpr int kTileM = 256, kTileN = 256;  // of a pair; kTileN / 2 columns in the narrow form
+template <int TN>
+constexpr int kStages = TN == kTileN ? 5 : 6;
+constexpr int kStageA = 128 * 128;  // bytes of a stage of one CTA
+template <int TN>
+constexpr int kStageB = TN / 2 * 128;
 constexpr int kEpiWarps = 16;
 constexpr int kGemmThreads2 = (kEpiWarps + 2) * 32;  // epilogue, TMA producer, MMA issuer
 
@@ -48,19 +52,21 @@ struct LinearParams {
   uint64_t handoff_limit_ns;     // of the wait for an accumulator to be read out
   int32_t M, N, K, k_splits;
   int32_t act;
+  int32_t narrow;  // tiles of kTileN / 2 columns
 };
 
+template <int TN>
 struct GemmSmem2 {
-  alignas(1024) uint8_t a[kStages][kStageOperand];
-  alignas(1024) uint8_t b[kStages][kStageOperand];
+  alignas(1024) uint8_t a[kStages<TN>][kStageA];
+  alignas(1024) uint8_t b[kStages<TN>][kStageB<TN>];
   // 32 x 32 sums of each epilogue warp, turned from a row a lane to 8 columns of
   // four rows a lane: row r's 16-byte piece j lies at piece j ^ (r % 8) of its line.
   alignas(128) uint8_t turn[kEpiWarps][32 * 128];
-  alignas(8) uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drain;
+  alignas(8) uint64_t full[kStages<TN>], empty[kStages<TN>], acc_full[2], acc_empty[2], drain;
   uint32_t tmem_base;
   int abort_flag;
 };
-static_assert(sizeof(GemmSmem2) + 1024 <= 232448, "over the shared memory of a CTA");
+static_assert(sizeof(GemmSmem2<256>) + 1024 <= 232448 && sizeof(GemmSmem2<128>) + 1024 <= 232448, "over a CTA's shared memory");
 
 // ---------------------------------------------------------- cluster helpers
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -138,12 +144,12 @@ __device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
       : "memory");
 }
 
-// Loads 128 rows (K-major) or columns (MN-major) of an operand, one K block deep.
-template <bool MN, int KB>
+// Loads ROWS rows (K-major, a box) or columns (MN-major) of an operand, one K block deep.
+template <bool MN, int KB, int ROWS>
 __device__ __forceinline__ void load_block(uint32_t dst, const CUtensorMap* map, uint32_t bar, int mn, int kb) {
   if (MN) {  // [64-column group][K row][128 bytes]
     tma_load_pair(dst, map, bar, mn, kb * KB);
-    tma_load_pair(dst + 64 * 128, map, bar, mn + 64, kb * KB);
+    if (ROWS > 64) tma_load_pair(dst + 64 * 128, map, bar, mn + 64, kb * KB);
   } else {
     tma_load_pair(dst, map, bar, kb * KB, mn);
   }
@@ -219,16 +225,17 @@ __device__ __forceinline__ void store_cols(T* dst, const uint64_t (&v)[4]) {
                : "memory");
 }
 
-template <typename T, bool F8, bool A_MN, bool B_MN, int EPI>
+template <typename T, bool F8, bool A_MN, bool B_MN, int EPI, int TN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads2, 1)
     pair_gemm_kernel(const __grid_constant__ LinearParams p) {
   extern __shared__ uint8_t smem_raw[];
-  GemmSmem2& s = *reinterpret_cast<GemmSmem2*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  GemmSmem2<TN>& s = *reinterpret_cast<GemmSmem2<TN>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   constexpr int KB = F8 ? 128 : 64;  // K values of a block
+  constexpr int kRing = kStages<TN>, kGroup = TN / 4;  // columns of an epilogue warp
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  const int tm = (p.M + kTileM - 1) / kTileM, tn = (p.N + kTileN - 1) / kTileN;
+  const int tm = (p.M + kTileM - 1) / kTileM, tn = (p.N + TN - 1) / TN;
   const int n_tiles = tm * tn * p.k_splits;
   const int nk = (p.K + KB - 1) / KB, per = (nk + p.k_splits - 1) / p.k_splits;
   // Tile t: K split t / (tm tn), then m tile, then n tile. Its K blocks are [kb0, kb1), one
@@ -237,13 +244,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads2, 1)
     split = t / (tm * tn);
     const int rem = t - split * tm * tn;
     m0 = (rem / tn) * kTileM;
-    n0 = (rem % tn) * kTileN;
+    n0 = (rem % tn) * TN;
     kb0 = min(split * per, nk);
     kb1 = min(kb0 + per, nk);
   };
   if (threadIdx.x == 0) {
     s.abort_flag = 0;
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kRing; ++i) {
       mbar_init(smem_u32(&s.full[i]), 1);
       mbar_init(smem_u32(&s.empty[i]), 1);
     }
@@ -255,7 +262,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads2, 1)
     fence_mbar_init();
   }
   if (warp == kEpiWarps + 1) {
-    tmem_alloc_pair(smem_u32(&s.tmem_base), 2 * kTileN);
+    tmem_alloc_pair(smem_u32(&s.tmem_base), 2 * TN);
     tmem_relinquish_pair();
   }
   tc_fence_before();
@@ -272,25 +279,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads2, 1)
     if (lane == 0) {
       tma_prefetch_map(&p.tm_a);
       tma_prefetch_map(&p.tm_b);
-      int last[kStages];
-      for (int st = 0; st < kStages; ++st) last[st] = -1;
+      int last[kRing];
+      for (int st = 0; st < kRing; ++st) last[st] = -1;
       int g = 0;
       bool ok = true;
       for (int t = pair; ok && t < n_tiles; t += pairs) {
         int m0, n0, split, kb0, kb1;
         tile_of(t, m0, n0, split, kb0, kb1);
         for (int kb = kb0; kb < kb1; ++kb, ++g) {
-          const int st = g % kStages, use = g / kStages;
+          const int st = g % kRing, use = g / kRing;
           if (use > 0 && !mbar_wait(smem_u32(&s.empty[st]), (use - 1) & 1, abort_flag)) {
             store_cluster(peer_abort, 1);
             ok = false;
             break;
           }
           // The leader's barrier counts the bytes of both CTAs.
-          if (rank == 0) mbar_expect_tx(smem_u32(&s.full[st]), 4 * kStageOperand);
+          if (rank == 0) mbar_expect_tx(smem_u32(&s.full[st]), 2 * (kStageA + kStageB<TN>));
           const uint32_t bar = in_cta(smem_u32(&s.full[st]), 0);
-          load_block<A_MN, KB>(smem_u32(s.a[st]), &p.tm_a, bar, m0 + 128 * rank, kb);
-          load_block<B_MN, KB>(smem_u32(s.b[st]), &p.tm_b, bar, n0 + 128 * rank, kb);
+          load_block<A_MN, KB, 128>(smem_u32(s.a[st]), &p.tm_a, bar, m0 + 128 * rank, kb);
+          load_block<B_MN, KB, TN / 2>(smem_u32(s.b[st]), &p.tm_b, bar, n0 + TN / 2 * rank, kb);
           last[st] = use;
         }
       }
@@ -298,7 +305,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads2, 1)
       // the cluster barrier at the end keeps the other one.
       if (rank == 0) {
         const uint64_t t0 = globaltimer_ns();  // one limit for all: the other CTA may have stopped before a stage
-        for (int st = 0; st < kStages; ++st)
+        for (int st = 0; st < kRing; ++st)
           while (last[st] >= 0 && !mbar_test(smem_u32(&s.full[st]), last[st] & 1) &&
                  globaltimer_ns() - t0 < kWaitLimitNs) {
           }
@@ -308,7 +315,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads2, 1)
   } else if (warp == kEpiWarps + 1) {
     // ------------------------------------------------------------ MMA issuer
     if (rank == 0 && elect_one_sync()) {
-      constexpr uint32_t idesc = idesc_f16kind(kTileM, kTileN, A_MN, B_MN, F8 ? 0u : Elem<T>::kUmma);
+      constexpr uint32_t idesc = idesc_f16kind(kTileM, TN, A_MN, B_MN, F8 ? 0u : Elem<T>::kUmma);
       int g = 0, i = 0;
       bool ok = true;
       for (int t = pair; ok && t < n_tiles; t += pairs, ++i) {
@@ -321,10 +328,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads2, 1)
           break;
         }
         tc_fence_after();
-        const uint32_t tacc = tbase + buf * kTileN;
+        const uint32_t tacc = tbase + buf * TN;
         for (int kb = kb0; kb < kb1; ++kb, ++g) {
-          const int st = g % kStages;
-          if (!mbar_wait(smem_u32(&s.full[st]), (g / kStages) & 1, abort_flag)) {
+          const int st = g % kRing;
+          if (!mbar_wait(smem_u32(&s.full[st]), (g / kRing) & 1, abort_flag)) {
             ok = false;
             break;
           }
@@ -344,8 +351,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads2, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue
-    // Warp w reads TMEM lanes 32 (w % 4) .. and columns 64 (w / 4) .., in two
-    // parts of 32 columns, a row a lane, and turns them in shared memory: a lane then
+    // Warp w reads TMEM lanes 32 (w % 4) .. and columns TN / 4 (w / 4) .., in parts
+    // of 32 columns, a row a lane, and turns them in shared memory: a lane then
     // has 8 columns of rows lane / 4 + 8 k, so that its columns' bias and scales are
     // a few registers and a warp's loads and stores are runs of 64 bytes. What the
     // kernel is short of is shared memory's bandwidth: the operands alone take 4096 of
@@ -366,7 +373,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads2, 1)
     for (int t = pair; ok && t < n_tiles; t += pairs, ++i) {
       int m0, n0, split, kb0, kb1;
       tile_of(t, m0, n0, split, kb0, kb1);
-      const int row0 = m0 + 128 * static_cast<int>(rank) + quarter * 32, col0 = n0 + group * 64;
+      const int row0 = m0 + 128 * static_cast<int>(rank) + quarter * 32, col0 = n0 + group * kGroup;
       const int buf = i & 1, first_row = row0 + sub_row;
       const int rows = min(max((p.M - first_row + 7) >> 3, 0), 4);  // of the lane's four
       // What belongs to rows and columns is read while the accumulator is computed (the
@@ -393,9 +400,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads2, 1)
         int m, n, sp, b0, b1;
         tile_of(t + pairs, m, n, sp, b0, b1);
         const int ahead = m + 128 * static_cast<int>(rank) + quarter * 32 + lane;
-        if (ahead < p.M && n + group * 64 < p.N)
+        if (ahead < p.M && n + group * kGroup < p.N)
           asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const T*>(p.residual) + ahead * p.residual_stride + n +
-                                                        group * 64));
+                                                        group * kGroup));
       }
       if (F8)
 #pragma unroll
@@ -449,13 +456,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads2, 1)
         }
       };
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < kGroup / 32; ++c) {
         if (row0 >= p.M || col0 + 32 * c >= p.N) break;  // the same for the whole warp
         const int col = col0 + 32 * c + sub_col;
         uint32_t a[32];
-        tmem_ld32(tbase + buf * kTileN + lane_addr + group * 64 + c * 32, a);
+        tmem_ld32(tbase + buf * TN + lane_addr + group * kGroup + c * 32, a);
         tmem_ld_wait(a);
-        if (c == 1) release();
+        if (c == kGroup / 32 - 1) release();
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           sts128(mine + lane * 128 + ((j ^ (lane & 7)) << 4), a[4 * j], a[4 * j + 1], a[4 * j + 2], a[4 * j + 3]);
@@ -470,7 +477,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads2, 1)
         } else {
           write_part(std::integral_constant<int, HSTU_ACT_NONE>{}, col);
         }
-        if (c == 0) load_part(col + 32);
+        if (c < kGroup / 32 - 1) load_part(col + 32);
         __syncwarp();  // the sums have been read before the next part's are written
       }
       if (held) release();
@@ -487,7 +494,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads2, 1)
   cluster_sync();  // nobody leaves while the other CTA's MMAs, copies or arrivals may reach it
   if (warp == kEpiWarps + 1) {
     tc_fence_after();
-    tmem_dealloc_pair(tbase, 2 * kTileN);
+    tmem_dealloc_pair(tbase, 2 * TN);
   }
   if (threadIdx.x == 0 && s.abort_flag && p.header) atomicOr(p.header + kHdrErr, kErrTimeout);
 }

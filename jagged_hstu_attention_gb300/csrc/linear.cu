@@ -235,15 +235,25 @@ hstu_status_t linear_checks(int64_t rows, int d_in, int d_out, int act, bool cod
   return HSTU_OK;
 }
 
+// A model of the time of a product on pairs of SMs, in units of 10 ns. Tiles of half the
+// columns take three quarters of a whole one's time, and so pay while there are pairs
+// left for twice as many (512 x 4096 x 4096: 19.0 and 25.6 us; 2000 rows 63 and 44).
+int64_t pairs_cost(int64_t rows, int outputs, int64_t k_bytes, bool narrow) {
+  const int tn = narrow ? kTileN / 2 : kTileN;
+  const int64_t tiles = (rows + kTileM - 1) / kTileM * ((outputs + tn - 1) / tn), nk = (k_bytes + 127) / 128;
+  return 330 + (tiles + kPairs - 1) / kPairs * (narrow ? 110 + 23 * nk : 150 + 31 * nk);
+}
+bool narrow_tiles(int64_t rows, int outputs, int64_t k_bytes) {
+  return pairs_cost(rows, outputs, k_bytes, true) < pairs_cost(rows, outputs, k_bytes, false);
+}
 // Whether a product goes to the kernel for few rows: where its model of the time is below
-// that of pairs of SMs (512 x 2048: 64 rows take 5.3 us there and 6.5 us on pairs, 512 rows 12.7
-// and 7.7; 4096 x 4096: 64 rows 11.9 and 23 us, 384 rows 49 and 24), and its tiles run
+// that of pairs of SMs (512 x 2048: 64 rows take 5.1 us there and 6.4 us on pairs, 512 rows 9.8
+// and 7.6; 4096 x 4096: 64 rows 11.8 and 23 us, 384 rows 49 and 24), and its tiles run
 // at the same time, or there are no more rows than one tile may have.
 bool few_rows(int64_t rows, int outputs, int64_t k_bytes) {
-  const int64_t tiles = (rows + kTileM - 1) / kTileM * ((outputs + kTileN - 1) / kTileN), nk = (k_bytes + 127) / 128;
-  const int64_t pairs = 330 + (tiles + kPairs - 1) / kPairs * (150 + 31 * nk);
   const FewPlan plan = few_plan(rows, outputs, k_bytes);
-  return plan.cost <= pairs && (rows <= kFewRows || few_tiles(rows, outputs, plan.rows_tile) <= 152);
+  return plan.cost <= std::min(pairs_cost(rows, outputs, k_bytes, false), pairs_cost(rows, outputs, k_bytes, true)) &&
+         (rows <= kFewRows || few_tiles(rows, outputs, plan.rows_tile) <= 152);
 }
 
 // Splits of dw's K: those that leave the fewest tiles' time on the busiest pair, counting
@@ -346,8 +356,9 @@ HSTU_API hstu_status_t hstu_attn_linear(const void* x, int64_t x_stride, const u
     return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
   }
   LinearParams p{};
+  p.narrow = narrow_tiles(rows, d_out, int64_t{d_in} * xe);
   const int type = codes ? kDtypeCodes : dtype;
-  if (!box_map(&p.tm_a, x, rows, d_in, x_stride, type, 128) || !box_map(&p.tm_b, w, d_out, d_in, d_in, type, 128))
+  if (!box_map(&p.tm_a, x, rows, d_in, x_stride, type, 128) || !box_map(&p.tm_b, w, d_out, d_in, d_in, type, p.narrow ? 64 : 128))
     return HSTU_ERR_CUDA;
   p.y = y;
   p.z = z;
@@ -446,6 +457,7 @@ HSTU_API hstu_status_t hstu_attn_linear_bwd(const void* dy, int64_t dy_stride, c
   } else {
     if (!box_map(&p.tm_a, g, rows, d_out, g_stride, dtype, 128) || !box_map(&p.tm_b, w, d_out, d_in, d_in, dtype, 64))
       return HSTU_ERR_CUDA;
+    p.narrow = narrow_tiles(rows, d_in, int64_t{d_out} * 2);
     p.y = dx;
     p.M = static_cast<int32_t>(rows);
     p.N = d_in;

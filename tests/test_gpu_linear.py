@@ -11,7 +11,7 @@ BF, F16 = torch.bfloat16, torch.float16
 
 # rows, d_in, d_out: tails of the tiles and of the K blocks, single rows, several tiles a CTA
 SIZES = [(1, 8, 8), (1, 512, 2048), (3, 24, 40), (64, 512, 264), (65, 72, 520), (127, 136, 64), (129, 64, 128),
-         (256, 128, 256), (257, 200, 264), (300, 1032, 1000)]
+         (256, 128, 256), (257, 200, 264), (300, 1032, 1000), (5000, 72, 1032)]
 
 
 def _inputs(T, K, N, dtype, seed=0, pad=0):
