@@ -22,7 +22,7 @@ namespace {
 constexpr int kGradThreads = 256;
 constexpr int kGradChunks = 152 * 4;
 constexpr int kGradRows = 4;  // of a thread, on their way at once
-constexpr int kMaxKSplits = 16;
+constexpr int kMaxKSplits = 76;
 constexpr int kPairs = 76;
 
 // The blocks of the activation's gradient: rows in chunks of at least kGradRows a thread,
@@ -150,33 +150,50 @@ __global__ void __launch_bounds__(kGradThreads, 4) linear_grad_kernel(const Grad
   if (active && lane_row == 0) store8(p.part + static_cast<int64_t>(blockIdx.x) * p.cols + col, sum);
 }
 
-// Ends the backward: dw from the fp32 parts of K's splits in order, 8 elements a
-// thread (blocks [0, dw_blocks)); dbias from the chunks' parts in order, 32 columns a
-// block, a part in 32 a warp (the blocks behind).
-constexpr int kFoldThreads = 1024;
+// Ends the backward: dw from the fp32 parts of K's splits, 8 elements a thread (blocks
+// [0, dw_blocks)), where there are many splits `slices` threads that take a part of them
+// each; dbias from the chunks' parts in order, 32 columns a block, a part in 32 a warp (the
+// blocks behind).
+constexpr int kFoldThreads = 1024, kFoldSplits = 8;  // of a slice, about
 struct FoldParams {
   const float* dw_part;
   void* dw;
   const float* bias_part;
   void* dbias;
   int64_t elems;  // of dw
-  int32_t splits, chunks, cols, dw_blocks;
+  int32_t splits, slices, chunks, cols, dw_blocks;
 };
 template <typename T>
 __global__ void __launch_bounds__(kFoldThreads) linear_fold_kernel(const FoldParams p) {
   chain();
   if (static_cast<int>(blockIdx.x) < p.dw_blocks) {
-    const int64_t i = (static_cast<int64_t>(blockIdx.x) * kFoldThreads + threadIdx.x) * 8;
-    if (i >= p.elems) return;
+    __shared__ float4 slice[kFoldThreads][2];
+    const int width = kFoldThreads / p.slices, q = threadIdx.x / width;
+    const int64_t i = (static_cast<int64_t>(blockIdx.x) * width + threadIdx.x % width) * 8;
     float acc[8] = {};
+    if (i < p.elems) {
+      const int s1 = p.splits * (q + 1) / p.slices;
 #pragma unroll 4
-    for (int s = 0; s < p.splits; ++s) {
-      float f[8];
-      load8(p.dw_part + s * p.elems + i, f);
+      for (int s = p.splits * q / p.slices; s < s1; ++s) {
+        float f[8];
+        load8(p.dw_part + s * p.elems + i, f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] += f[e];
+        for (int e = 0; e < 8; ++e) acc[e] += f[e];
+      }
     }
-    return store8(static_cast<T*>(p.dw) + i, acc);
+    if (p.slices > 1) {
+      slice[threadIdx.x][0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      slice[threadIdx.x][1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+      __syncthreads();
+      if (q > 0) return;
+      for (int x = 1; x < p.slices; ++x) {
+        const float4 lo = slice[x * width + threadIdx.x][0], hi = slice[x * width + threadIdx.x][1];
+        acc[0] += lo.x, acc[1] += lo.y, acc[2] += lo.z, acc[3] += lo.w;
+        acc[4] += hi.x, acc[5] += hi.y, acc[6] += hi.z, acc[7] += hi.w;
+      }
+    }
+    if (i < p.elems) store8(static_cast<T*>(p.dw) + i, acc);
+    return;
   }
   __shared__ float red[32][33];
   const int w = threadIdx.x >> 5, l = threadIdx.x & 31, col = (blockIdx.x - p.dw_blocks) * 32 + l;
@@ -256,17 +273,19 @@ bool few_rows(int64_t rows, int outputs, int64_t k_bytes) {
          (rows <= kFewRows || few_tiles(rows, outputs, plan.rows_tile) <= 152);
 }
 
-// Splits of dw's K: those that leave the fewest tiles' time on the busiest pair, counting
-// each split's fp32 tile (written, read) as two of its 64-row blocks.
+// Splits of dw's K: those that take the least time, in 64-row blocks: the tiles of the
+// busiest pair, each split's fp32 tile counting as four blocks, and the sums' way through
+// the fold, at some 400000 values a block. (46120 rows of 152 and 200 columns: 45 us for the
+// backward with 16 splits, 37 with 73; 81920 of 512 and 2048: 410 with 14, 399 with 9.)
 int dw_splits(int64_t rows, int d_in, int d_out) {
   const int64_t tiles = int64_t{(d_out + kTileM - 1) / kTileM} * ((d_in + kTileN - 1) / kTileN);
-  const int64_t nk = (rows + 63) / 64;
+  const int64_t nk = (rows + 63) / 64, elems = int64_t{d_in} * d_out;
   int best = 1;
   int64_t least = INT64_MAX;
   for (int s = 1; s <= kMaxKSplits && s <= nk; ++s) {
     const int64_t per = (nk + s - 1) / s;
     if ((s - 1) * per >= nk) continue;  // a split without rows
-    const int64_t cost = (tiles * s + kPairs - 1) / kPairs * (per + (s > 1 ? 4 : 0));
+    const int64_t cost = (tiles * s + kPairs - 1) / kPairs * (per + (s > 1 ? 4 : 0)) + (s > 1 ? 8 + s * elems / 400000 : 0);
     if (cost < least) least = cost, best = s;
   }
   return best;
@@ -484,7 +503,10 @@ HSTU_API hstu_status_t hstu_attn_linear_bwd(const void* dy, int64_t dy_stride, c
   fp.splits = p.k_splits;
   fp.chunks = grad_grid(rows, d_out).chunks;
   fp.cols = d_out;
-  fp.dw_blocks = p.k_splits > 1 ? static_cast<int32_t>((fp.elems / 8 + kFoldThreads - 1) / kFoldThreads) : 0;
+  fp.slices = 1;
+  while (fp.slices * kFoldSplits < fp.splits) fp.slices *= 2;
+  const int64_t width = kFoldThreads / fp.slices;
+  fp.dw_blocks = p.k_splits > 1 ? static_cast<int32_t>((fp.elems / 8 + width - 1) / width) : 0;
   const dim3 grid(static_cast<unsigned>(fp.dw_blocks + (dbias ? (d_out + 31) / 32 : 0)));
   const cudaError_t e = launch_chained(f16 ? linear_fold_kernel<__half> : linear_fold_kernel<__nv_bfloat16>, grid,
                                        kFoldThreads, 0, cs, fp);
