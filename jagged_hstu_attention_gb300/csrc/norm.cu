@@ -146,7 +146,9 @@ __global__ void __launch_bounds__(norm_threads<RT>()) norm_kernel(const NormPara
   // (Every row of the block does then, for the barriers' sake; nothing changes for the others.)
   top = row_reduce<RT, true>(top, shared[1]);
   const bool infinite = top > kMaxFinite;
-  const bool again = RT > 32 ? __syncthreads_or(infinite) : __any_sync(0xffffffffu, infinite);
+  const bool again = RT == norm_threads<RT>() ? infinite  // a row a block
+                     : RT > 32                ? __syncthreads_or(infinite)
+                                              : __any_sync(0xffffffffu, infinite);
   if (again) {
     top = 0.0f;
 #pragma unroll
@@ -341,11 +343,14 @@ __global__ void __launch_bounds__(1024) norm_fold_kernel(const float* part, int 
 }
 
 // Threads of a row and chunks a thread. Forward: the fewest threads whose registers
-// hold the row, so that reductions stay inside a warp up to 1024 columns; 8 and 16
-// threads for heads, where a whole warp would leave most of its lanes without columns.
+// hold the row, so that reductions stay inside a warp up to 1024 columns and take few
+// warps above (16381 rows of 2048 with a residual into 8 bits: 36 us, 42 us with a chunk
+// a thread); 8 and 16 threads for heads, where a whole warp would leave most of its
+// lanes without columns.
 // The backward holds up to four rows and its part of dweight besides: one or two
 // chunks a thread, so that several blocks fit an SM (32749 rows of 1024, with a gate:
-// 72 us with four chunks a lane and one block an SM).
+// 72 us with four chunks a lane and one block an SM, 65 us with a chunk a thread, 62 us with
+// two; 16381 rows of 2048 with dh 46 us so, 51 us with a chunk a thread).
 template <bool BACKWARD, typename F>
 cudaError_t by_width(int width, F&& f) {
   using std::integral_constant;
@@ -355,14 +360,14 @@ cudaError_t by_width(int width, F&& f) {
   if (width <= 256) return call(integral_constant<int, 32>{}, integral_constant<int, 1>{});
   if (width <= 512) return call(integral_constant<int, 32>{}, integral_constant<int, 2>{});
   if constexpr (BACKWARD) {
-    if (width <= 1024) return call(integral_constant<int, 128>{}, integral_constant<int, 1>{});
-    if (width <= 2048) return call(integral_constant<int, 256>{}, integral_constant<int, 1>{});
+    if (width <= 1024) return call(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+    if (width <= 2048) return call(integral_constant<int, 128>{}, integral_constant<int, 2>{});
     if (width <= 4096) return call(integral_constant<int, 256>{}, integral_constant<int, 2>{});
     return call(integral_constant<int, 512>{}, integral_constant<int, 2>{});
   } else {
     if (width <= 1024) return call(integral_constant<int, 32>{}, integral_constant<int, 4>{});
-    if (width <= 2048) return call(integral_constant<int, 256>{}, integral_constant<int, 1>{});
-    if (width <= 4096) return call(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+    if (width <= 2048) return call(integral_constant<int, 64>{}, integral_constant<int, 4>{});
+    if (width <= 4096) return call(integral_constant<int, 128>{}, integral_constant<int, 4>{});
     return call(integral_constant<int, 256>{}, integral_constant<int, 4>{});
   }
 }
