@@ -7,7 +7,7 @@
 // block instead of the 384 that a 128 x 256 tile of its own takes. Persistent: a pair
 // takes tiles in turn, N fastest, so that pairs running together share A's rows and
 // B stays in L2. 128-byte deep K blocks (64 16-bit or 128 8-bit values) flow through
-// a ring of five TMA stages that runs on across tiles; two 256-column accumulators, so
+// a ring of seven TMA stages that runs on across tiles; two 256-column accumulators, so
 // that sixteen epilogue warps read one out while the next is computed. Products of few
 // tiles take tiles of 256 x 128, which more pairs share.
 //
@@ -26,7 +26,7 @@ namespace hstu {
 
 constexpr int kTileM = 256, kTileN = 256;  // of a pair; kTileN / 2 columns in the narrow form
 template <int TN>
-constexpr int kStages = TN == kTileN ? 5 : 6;
+constexpr int kStages = TN == kTileN ? 7 : 9;
 constexpr int kStageA = 128 * 128;  // bytes of a stage of one CTA
 template <int TN>
 constexpr int kStageB = TN / 2 * 128;
@@ -59,9 +59,6 @@ template <int TN>
 struct GemmSmem2 {
   alignas(1024) uint8_t a[kStages<TN>][kStageA];
   alignas(1024) uint8_t b[kStages<TN>][kStageB<TN>];
-  // 32 x 32 sums of each epilogue warp, turned from a row a lane to 8 columns of
-  // four rows a lane: row r's 16-byte piece j lies at piece j ^ (r % 8) of its line.
-  alignas(128) uint8_t turn[kEpiWarps][32 * 128];
   alignas(8) uint64_t full[kStages<TN>], empty[kStages<TN>], acc_full[2], acc_empty[2], drain;
   uint32_t tmem_base;
   int abort_flag;
@@ -100,13 +97,27 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
 }
 // This thread's shared-memory writes become visible to MMAs and bulk copies.
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+// 32 columns of 16 lanes of TMEM: value 4 g + 2 h + e of a lane of the warp is row
+// lane / 4 + 8 h, column 8 g + 2 (lane % 4) + e.
+__device__ __forceinline__ void tmem_ld_rows16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
 }
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-  return v;
+// Word i of lane q of four becomes word q of lane i.
+__device__ __forceinline__ void quad_transpose(uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d, int q) {
+  auto trade = [](uint32_t& low, uint32_t& high, bool upper, int with) {
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? low : high, with);
+    low = upper ? got : low;
+    high = upper ? high : got;
+  };
+  trade(a, b, q & 1, 1);
+  trade(c, d, q & 1, 1);
+  trade(a, c, q & 2, 2);
+  trade(b, d, q & 2, 2);
 }
 
 // ------------------------------------------------------------ pair of CTAs
@@ -217,11 +228,9 @@ __device__ __forceinline__ uint64_t activate2(uint64_t x) {
   return ACT == HSTU_ACT_RELU ? cut : pair_mul(cut, sigmoid_of<ACT>(x, e));
 }
 
-// Eight columns, rounded; nothing here reads them again.
-template <typename T>
-__device__ __forceinline__ void store_cols(T* dst, const uint64_t (&v)[4]) {
-  asm volatile("st.global.L1::no_allocate.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(dst), "r"(pack_pair<T>(v[0])),
-               "r"(pack_pair<T>(v[1])), "r"(pack_pair<T>(v[2])), "r"(pack_pair<T>(v[3]))
+// Eight columns; nothing here reads them again.
+__device__ __forceinline__ void store_cols(void* dst, uint4 v) {
+  asm volatile("st.global.L1::no_allocate.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                : "memory");
 }
 
@@ -352,21 +361,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads2, 1)
   } else {
     // ------------------------------------------------------------ epilogue
     // Warp w reads TMEM lanes 32 (w % 4) .. and columns TN / 4 (w / 4) .., in parts
-    // of 32 columns, a row a lane, and turns them in shared memory: a lane then
-    // has 8 columns of rows lane / 4 + 8 k, so that its columns' bias and scales are
-    // a few registers and a warp's loads and stores are runs of 64 bytes. What the
-    // kernel is short of is shared memory's bandwidth: the operands alone take 4096 of
-    // its cycles a tile at K = 512, as long as their MMAs, and an epilogue 2000 more.
-    // (Of 40960 rows, K = 512, N = 2048, with z and SiLU: 80 us so; 87 us with 16-bit
-    // rows staged for TMA stores, 86 us with a row's 32-byte pieces stored by its
-    // lane; 58 us without any stores, 45 us without an epilogue.)
+    // of 32 columns: a lane gets two columns of each 8 of rows lane / 4 + 8 k, and the
+    // lanes of four trade rounded results so that each has 8 columns of the rows; a
+    // warp's loads and stores are runs of 64 bytes. Of 40960 rows, K = 512, N = 2048, with z
+    // and SiLU: 75.6 us so, 78.9 us with the sums turned in shared memory, whose
+    // bandwidth the operands take already (4096 of its cycles a tile, as long as their
+    // MMAs); 87 us with 16-bit rows staged for TMA stores, 86 us with a row's 32-byte pieces
+    // stored by its lane; 58 us without any stores, 45 us without an epilogue. What
+    // it is short of now is the way out of the SM (requests to L2 69% of the cycles)
+    // and, at 55%, issue slots.
     const int quarter = warp & 3, group = warp >> 2;
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t mine = smem_u32(s.turn[warp]);
-    const int sub_row = lane >> 2, sub_col = (lane & 3) * 8;
-    // The two pieces of a lane in line r = sub_row + 8 k: r % 8 is sub_row's.
-    const uint32_t piece = (lane & 3) * 2, from = mine + sub_row * 128;
-    const uint32_t lo_at = from + ((piece ^ (sub_row & 7)) << 4), hi_at = from + (((piece + 1) ^ (sub_row & 7)) << 4);
+    const int quad = lane & 3, sub_row = lane >> 2, sub_col = quad * 8;
     const int64_t skip = int64_t{8} * p.N;  // eight rows on
     bool ok = true;
     int i = 0;
@@ -379,13 +385,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads2, 1)
       // What belongs to rows and columns is read while the accumulator is computed (the
       // first part's) or the part before is worked on.
       uint4 bias, residual[4];
-      uint2 col_scale;
+      uint32_t col_scale[4];
       float row_scale[4];
       auto load_part = [&](int col) {
         if constexpr (EPI == kEpiLinear) {
           bias = make_uint4(0, 0, 0, 0);
           if (p.bias && col < p.N) bias = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.bias) + col);
-          if (F8 && col < p.N) col_scale = *reinterpret_cast<const uint2*>(p.b_scale + col);
+          if (F8)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {  // of the lane's two columns of each eight
+              const int at = col - sub_col + 8 * g;
+              col_scale[g] = at < p.N ? *reinterpret_cast<const uint16_t*>(p.b_scale + at + 2 * quad) : 0u;
+            }
           if (p.residual && col < p.N) {
             const T* from_row = static_cast<const T*>(p.residual) + first_row * p.residual_stride + col;
 #pragma unroll
@@ -416,42 +427,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads2, 1)
         if (lane == 0) arrive_cluster(in_cta(smem_u32(&s.acc_empty[buf]), 0));
         held = false;
       };
-      // Eight columns of the lane's four rows.
-      auto write_part = [&](auto act, int col) {
+      // Two columns of each eight of the lane's four rows (a: as read), eight stored.
+      auto write_part = [&](auto act, int col, const uint32_t (&a)[32]) {
         const int64_t at = static_cast<int64_t>(first_row) * p.N + col;
+        if constexpr (EPI == kEpiLinear) quad_transpose(bias.x, bias.y, bias.z, bias.w, quad);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint4 lo = lds128(lo_at + 1024 * k), hi = lds128(hi_at + 1024 * k);
-          const bool live = k < rows && col < p.N;
+          [[maybe_unused]] const bool live = k < rows && col < p.N;
+          const uint32_t* of = a + 16 * (k >> 1) + 2 * (k & 1);
           if constexpr (EPI == kEpiPartial32) {
-            if (live)
-              asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
-                               p.part + static_cast<int64_t>(split) * p.M * p.N + at + k * skip),
-                           "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w)
-                           : "memory");
+            float* dst = p.part + static_cast<int64_t>(split) * p.M * p.N + at - sub_col + 2 * quad + k * skip;
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              if (k < rows && col - sub_col + 8 * g < p.N)
+                asm volatile("st.global.L1::no_allocate.v2.b32 [%0], {%1, %2};" ::"l"(dst + 8 * g), "r"(of[4 * g]),
+                             "r"(of[4 * g + 1])
+                             : "memory");
           } else {
-            uint64_t v[4] = {pair_bits(lo.x, lo.y), pair_bits(lo.z, lo.w), pair_bits(hi.x, hi.y), pair_bits(hi.z, hi.w)};
+            uint64_t v[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) v[g] = pair_bits(of[4 * g], of[4 * g + 1]);
+            auto store = [&](void* dst) {
+              uint4 w = make_uint4(pack_pair<T>(v[0]), pack_pair<T>(v[1]), pack_pair<T>(v[2]), pack_pair<T>(v[3]));
+              quad_transpose(w.x, w.y, w.z, w.w, quad);
+              if (live) store_cols(static_cast<T*>(dst) + at + k * skip, w);
+            };
             if constexpr (EPI == kEpiLinear) {
               const uint32_t bw[4] = {bias.x, bias.y, bias.z, bias.w};
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
+              for (int g = 0; g < 4; ++g) {
                 if (F8) {
-                  const uint32_t w = (e < 2 ? col_scale.x : col_scale.y) >> (16 * (e & 1));
-                  v[e] = pair_mul(v[e], pair_of(row_scale[k], row_scale[k]));
-                  v[e] = pair_mul(v[e], pair_of(scale_value(w & 0xffu), scale_value((w >> 8) & 0xffu)));
+                  v[g] = pair_mul(v[g], pair_of(row_scale[k], row_scale[k]));
+                  v[g] = pair_mul(v[g], pair_of(scale_value(col_scale[g] & 0xffu), scale_value(col_scale[g] >> 8)));
                 }
-                v[e] = pair_add(v[e], unpack_pair<T>(bw[e]));
+                v[g] = pair_add(v[g], unpack_pair<T>(bw[g]));
               }
-              if (p.z && live) store_cols<T>(static_cast<T*>(p.z) + at + k * skip, v);
+              if (p.z) store(p.z);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) v[e] = activate2<decltype(act)::value>(v[e]);
+              for (int g = 0; g < 4; ++g) v[g] = activate2<decltype(act)::value>(v[g]);
               if (p.residual) {
-                const uint32_t rw[4] = {residual[k].x, residual[k].y, residual[k].z, residual[k].w};
+                uint4& w = residual[k];
+                quad_transpose(w.x, w.y, w.z, w.w, quad);
+                const uint32_t rw[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = pair_add(v[e], unpack_pair<T>(rw[e]));
+                for (int g = 0; g < 4; ++g) v[g] = pair_add(v[g], unpack_pair<T>(rw[g]));
               }
             }
-            if (live) store_cols<T>(static_cast<T*>(p.y) + at + k * skip, v);
+            store(p.y);
           }
         }
       };
@@ -460,25 +482,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads2, 1)
         if (row0 >= p.M || col0 + 32 * c >= p.N) break;  // the same for the whole warp
         const int col = col0 + 32 * c + sub_col;
         uint32_t a[32];
-        tmem_ld32(tbase + buf * TN + lane_addr + group * kGroup + c * 32, a);
+        const uint32_t from = tbase + buf * TN + lane_addr + group * kGroup + c * 32;
+        tmem_ld_rows16(from, a);
+        tmem_ld_rows16(from + (16u << 16), a + 16);
         tmem_ld_wait(a);
         if (c == kGroup / 32 - 1) release();
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          sts128(mine + lane * 128 + ((j ^ (lane & 7)) << 4), a[4 * j], a[4 * j + 1], a[4 * j + 2], a[4 * j + 3]);
-        __syncwarp();
         if constexpr (EPI == kEpiLinear) {
           switch (p.act) {
-            case HSTU_ACT_SILU: write_part(std::integral_constant<int, HSTU_ACT_SILU>{}, col); break;
-            case HSTU_ACT_GELU: write_part(std::integral_constant<int, HSTU_ACT_GELU>{}, col); break;
-            case HSTU_ACT_RELU: write_part(std::integral_constant<int, HSTU_ACT_RELU>{}, col); break;
-            default: write_part(std::integral_constant<int, HSTU_ACT_NONE>{}, col); break;
+            case HSTU_ACT_SILU: write_part(std::integral_constant<int, HSTU_ACT_SILU>{}, col, a); break;
+            case HSTU_ACT_GELU: write_part(std::integral_constant<int, HSTU_ACT_GELU>{}, col, a); break;
+            case HSTU_ACT_RELU: write_part(std::integral_constant<int, HSTU_ACT_RELU>{}, col, a); break;
+            default: write_part(std::integral_constant<int, HSTU_ACT_NONE>{}, col, a); break;
           }
         } else {
-          write_part(std::integral_constant<int, HSTU_ACT_NONE>{}, col);
+          write_part(std::integral_constant<int, HSTU_ACT_NONE>{}, col, a);
         }
         if (c < kGroup / 32 - 1) load_part(col + 32);
-        __syncwarp();  // the sums have been read before the next part's are written
       }
       if (held) release();
       __syncwarp();
