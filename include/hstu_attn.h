@@ -524,7 +524,8 @@ HSTU_API hstu_status_t hstu_attn_embed(const void* table, int32_t table_dtype, i
                                        const void* ids, int32_t id_bytes, int64_t tokens, float scale, void* out,
                                        int32_t dtype, void* ws, size_t ws_bytes, void* stream);
 
-/* Bytes of workspace of hstu_attn_embed_bwd; 0 if an argument is out of range. */
+/* Bytes of workspace of hstu_attn_embed_bwd, enough for fewer tokens too; 0 if an argument
+ * is out of range. */
 HSTU_API size_t hstu_attn_embed_workspace_size(int64_t tokens, int64_t vocab, int32_t dim);
 
 /* Gradient of the table: dtable[v] = scale * the sum of dy[t] over the tokens t
@@ -562,7 +563,8 @@ HSTU_API hstu_status_t hstu_attn_rms_norm(const void* x, int64_t x_stride, const
 HSTU_API hstu_status_t hstu_attn_quantise_rows(const void* x, int64_t x_stride, int64_t rows, int32_t width,
                                                int32_t dtype, uint8_t* codes, uint8_t* scale, void* stream);
 
-/* Bytes of workspace of hstu_attn_rms_norm_bwd; 0 if an argument is out of range. */
+/* Bytes of workspace of hstu_attn_rms_norm_bwd, enough for fewer rows too; 0 if an argument
+ * is out of range. */
 HSTU_API size_t hstu_attn_rms_norm_workspace_size(int64_t rows, int32_t width);
 
 /* Gradients of hstu_attn_rms_norm (16-bit output): with u = h rstd and
@@ -602,14 +604,16 @@ HSTU_API hstu_status_t hstu_attn_rms_norm_bwd(const void* dy, int64_t dy_stride,
  *            sets HSTU_ERR_TIMEOUT in the error word (the rows of y and z are then
  *            undefined)
  * Limits: d_in and d_out multiples of 8 (d_in of 16 for 8-bit operands), up to
- * 65536; the stride of 8-bit x a multiple of 16. */
+ * 65536; the stride of 8-bit x a multiple of 16; rows up to 2^31 - 1025, and
+ * (rows / 256 + 1) (max(d_in, d_out) / 256 + 1) up to 2^30 - 1. */
 HSTU_API hstu_status_t hstu_attn_linear(const void* x, int64_t x_stride, const uint8_t* x_scale, const void* w,
                                         const uint8_t* w_scale, const void* bias, const void* residual,
                                         int64_t residual_stride, int64_t rows, int32_t d_in, int32_t d_out,
                                         int32_t dtype, int32_t act, void* y, void* z, void* ws, size_t ws_bytes,
                                         void* stream);
 
-/* Bytes of workspace of hstu_attn_linear_bwd; 0 if an argument is out of range. */
+/* Bytes of workspace of hstu_attn_linear_bwd, enough for fewer rows too; 0 if an argument
+ * is out of range. */
 HSTU_API size_t hstu_attn_linear_workspace_size(int64_t rows, int32_t d_in, int32_t d_out, int32_t act);
 
 /* Gradients of hstu_attn_linear with 16-bit operands: g = dy act'(z), rounded to

@@ -785,7 +785,7 @@ def embed(table, ids, scale: float = 1.0, dtype=None, out=None, ws: Optional[tor
 
 
 def embed_workspace(tokens: int, vocab: int, dim: int, device="cuda") -> torch.Tensor:
-    """Workspace of ``embed_bwd``."""
+    """Workspace of ``embed_bwd``, for up to so many tokens."""
     n = int(load().hstu_attn_embed_workspace_size(tokens, vocab, dim))
     if n == 0:
         raise HstuError(2, "hstu_attn_embed_workspace_size")
@@ -865,7 +865,7 @@ def rms_norm(x, weight, residual=None, gate=None, eps: float = 1e-6, quantise: b
 
 
 def rms_norm_workspace(rows: int, width: int, device="cuda") -> torch.Tensor:
-    """Workspace of ``rms_norm_bwd``."""
+    """Workspace of ``rms_norm_bwd``, for up to so many rows."""
     n = int(load().hstu_attn_rms_norm_workspace_size(rows, width))
     if n == 0:
         raise HstuError(2, "hstu_attn_rms_norm_workspace_size")
@@ -912,7 +912,7 @@ def linear(x, w, bias=None, act: str = "none", residual=None, want_z: bool = Fal
 
 
 def linear_workspace(rows: int, d_in: int, d_out: int, act: str = "none", device="cuda") -> torch.Tensor:
-    """Workspace of ``linear_bwd``."""
+    """Workspace of ``linear_bwd``, for up to so many rows."""
     n = int(load().hstu_attn_linear_workspace_size(rows, d_in, d_out, _act_code(act)))
     if n == 0:
         raise HstuError(2, "hstu_attn_linear_workspace_size")

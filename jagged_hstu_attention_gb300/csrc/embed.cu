@@ -633,6 +633,16 @@ int sum_chunk(int64_t n, int dim) {
   return c;
 }
 
+// The most chunks of up to n tokens, so that a workspace serves calls of fewer.
+int64_t most_chunks(int64_t n, int dim) {
+  int64_t most = 0;
+  for (int c = 16; c <= sum_chunk(n, dim); c *= 2) {
+    const int64_t last = c < 128 ? std::min(n, (int64_t{2} * c * 152 * 2048 - 1) / (dim / 8)) : n;  // with chunks of c
+    most = std::max(most, (last + c - 1) / c);
+  }
+  return most;
+}
+
 // Workspace: a 256-byte header (error word), a bit a row of the table, the two
 // buffers of (id, token), the digits' counts, and the long runs' list and sums.
 struct EmbedLayout {
@@ -650,8 +660,7 @@ EmbedLayout embed_layout(int64_t n, int64_t vocab, int dim) {
   }
   l.counts = at;
   at += static_cast<size_t>(kSortTiles) * kMaxBins * 4;
-  const int c = sum_chunk(n, dim);
-  const size_t chunks = static_cast<size_t>((n + c - 1) / c);
+  const size_t chunks = static_cast<size_t>(most_chunks(n, dim));
   l.runs = at;
   at += align_up(chunks * 4, 256);
   l.part = at;

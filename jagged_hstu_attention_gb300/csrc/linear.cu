@@ -22,7 +22,6 @@ namespace {
 constexpr int kGradThreads = 256;
 constexpr int kGradChunks = 152 * 4;
 constexpr int kGradRows = 4;  // of a thread, on their way at once
-constexpr int kMaxKSplits = 76;
 constexpr int kPairs = 76;
 
 // The blocks of the activation's gradient: rows in chunks of at least kGradRows a thread,
@@ -277,12 +276,20 @@ bool few_rows(int64_t rows, int outputs, int64_t k_bytes) {
 // busiest pair, each split's fp32 tile counting as four blocks, and the sums' way through
 // the fold, at some 400000 values a block. (46120 rows of 152 and 200 columns: 45 us for the
 // backward with 16 splits, 37 with 73; 81920 of 512 and 2048: 410 with 14, 399 with 9.)
+int64_t dw_tiles(int d_in, int d_out) {
+  return int64_t{(d_out + kTileM - 1) / kTileM} * ((d_in + kTileN - 1) / kTileN);
+}
+// Two turns of the pairs at the most.
+int most_splits(int64_t rows, int d_in, int d_out) {
+  const int64_t fit = std::min<int64_t>(kPairs, std::max<int64_t>(1, 2 * kPairs / dw_tiles(d_in, d_out)));
+  return static_cast<int>(std::max<int64_t>(1, std::min(fit, (rows + 63) / 64)));
+}
 int dw_splits(int64_t rows, int d_in, int d_out) {
-  const int64_t tiles = int64_t{(d_out + kTileM - 1) / kTileM} * ((d_in + kTileN - 1) / kTileN);
-  const int64_t nk = (rows + 63) / 64, elems = int64_t{d_in} * d_out;
+  const int64_t tiles = dw_tiles(d_in, d_out), nk = (rows + 63) / 64, elems = int64_t{d_in} * d_out;
+  const int most = most_splits(rows, d_in, d_out);
   int best = 1;
   int64_t least = INT64_MAX;
-  for (int s = 1; s <= kMaxKSplits && s <= nk; ++s) {
+  for (int s = 1; s <= most; ++s) {
     const int64_t per = (nk + s - 1) / s;
     if ((s - 1) * per >= nk) continue;  // a split without rows
     const int64_t cost = (tiles * s + kPairs - 1) / kPairs * (per + (s > 1 ? 4 : 0)) + (s > 1 ? 8 + s * elems / 400000 : 0);
@@ -292,7 +299,7 @@ int dw_splits(int64_t rows, int d_in, int d_out) {
 }
 
 // Workspace of the backward: a 256-byte header (error word), g, the bias gradient's
-// parts, dw's parts.
+// parts, dw's parts, as many as fewer rows may have.
 struct LinearLayout {
   size_t g = 0, part = 0, dw = 0, total = 0;
 };
@@ -301,7 +308,7 @@ LinearLayout linear_layout(int64_t rows, int d_in, int d_out, int act) {
   l.g = kHdrWords * 4;
   l.part = l.g + (act != HSTU_ACT_NONE ? align_up(static_cast<size_t>(rows) * d_out * 2, 256) : 0);
   l.dw = l.part + align_up(static_cast<size_t>(grad_grid(rows, d_out).chunks) * d_out * 4, 256);
-  const int splits = dw_splits(rows, d_in, d_out);
+  const int splits = most_splits(rows, d_in, d_out);
   l.total = l.dw + (splits > 1 ? align_up(static_cast<size_t>(splits) * d_out * d_in * 4, 256) : 0);
   return l;
 }

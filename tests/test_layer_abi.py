@@ -120,3 +120,17 @@ def test_linear_bwd_refusals(lib):
     size = lib.hstu_attn_linear_workspace_size
     assert size(-1, 64, 64, 0) == 0 and size(5, 60, 64, 0) == 0 and size(5, 64, 64, 7) == 0
     assert 0 < size(0, 8, 8, 0) <= size(1000, 64, 64, 0) < size(1000, 64, 64, 1)
+
+
+@pytest.mark.parametrize("dims", [(8, 8), (16, 40), (64, 512), (512, 64), (504, 2056), (512, 2048), (1128, 640),
+                                  (2048, 2048), (2048, 8192), (8192, 200), (65536, 8), (8, 65536)])
+def test_workspaces_of_more_rows_serve_fewer(lib, dims):
+    """Sizes never fall as the rows grow, one by one at first and across the larger counts."""
+    a, b = dims
+    counts = list(range(1, 700)) + sorted({int(700 * 1.013 ** k) + d for k in range(560) for d in (-1, 0, 1)})
+    for size in (lambda n: lib.hstu_attn_linear_workspace_size(n, a, b, 1),
+                 lambda n: lib.hstu_attn_linear_workspace_size(n, a, b, 0),
+                 lambda n: lib.hstu_attn_embed_workspace_size(n, 1000, a),
+                 lambda n: lib.hstu_attn_rms_norm_workspace_size(n, min(a, 8192))):
+        sizes = [size(n) for n in counts]
+        assert sizes[0] > 0 and all(x <= y for x, y in zip(sizes, sizes[1:]))
