@@ -3,6 +3,7 @@ projection, attention, gated norm, output projection with the layer's input
 added, and all their gradients; the same through 8 bits; captured into graphs, on
 other streams and from several workspaces at once."""
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -156,6 +157,49 @@ def test_two_streams_at_once():
     for a, b in zip(got, want):
         for n in b:
             assert torch.equal(a[n], b[n]), n
+
+
+def test_threads_at_once():
+    """Threads with a stream each, whose calls take every kind of product and sort: pairs with whole and half tiles,
+    few rows, one block's sort and several."""
+    sizes = [(4500, 136, 528), (5000, 72, 1040), (64, 512, 1024), (600, 264, 336)]
+
+    def work(i):
+        T, K, N = sizes[i]
+        x, w, dy = lt.randn((T, K), BF, i), lt.randn((N, K), BF, 10 + i, K ** -0.5), lt.randn((T, N), BF, 20 + i)
+        ids = torch.randint(-1, 500, (T,), generator=torch.Generator("cuda").manual_seed(i), device="cuda")
+        q, qw = hb.quantise_rows(dy), hb.quantise_rows(w.t().contiguous())
+        nw = lt.randn((K,), BF, 30 + i)
+        torch.cuda.current_stream().synchronize()
+
+        def once():
+            a, _, rstd = hb.rms_norm(x, nw)
+            y, z = hb.linear(a, w, act="silu", want_z=True)
+            dx, dw, db = hb.linear_bwd(dy, z, a, w, act="silu")
+            back, dn, _ = hb.rms_norm_bwd(dx, x, rstd, nw)
+            return [y, dx, dw, db, back, dn, hb.embed_bwd(back, ids, 500), hb.linear(q, qw)[0]]
+        return once
+    calls = [work(i) for i in range(len(sizes))]
+    want = [once() for once in calls]
+    torch.cuda.synchronize()
+    got, errors = [None] * len(calls), []
+
+    def run(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    got[i] = calls[i]()
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for a, b in zip(got, want):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
 def test_a_stream_given():
