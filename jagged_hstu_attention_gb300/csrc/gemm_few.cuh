@@ -55,8 +55,6 @@ struct FewSmem {  // the stages and the sums of others lie behind
 };
 static_assert(sizeof(FewSmem) <= 256, "the space in front of the stages");
 
-__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
 }
@@ -70,6 +68,9 @@ __device__ __forceinline__ void copy_wait_all_but(int n) {
     default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
   }
 }
+// The halves of a cluster barrier; the arrival orders nothing.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void sts_cluster(uint32_t addr, uint32_t a, uint32_t b) {
   asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
@@ -114,6 +115,7 @@ __device__ __forceinline__ void copy_block_mn(uint32_t dst, const uint8_t* src, 
 template <typename T, bool F8, bool W_MN, int NT>
 __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams p) {
   extern __shared__ uint8_t smem_raw[];
+  cluster_arrive();  // this CTA has started: what the others wait for before they write here
   // [stages: A 16 KB, B], sums [CTA][pair of own rows][output], barriers
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float2* meet = reinterpret_cast<float2*>(base + p.stages * kFewStageBytes<NT>);
@@ -186,6 +188,7 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams p
   // Rows [c own, (c + 1) own) of the tile are CTA c's: sums of pairs of rows, an output
   // a lane; warps 4 to 7 take the second half of the columns.
   const int own = NT / split;
+  cluster_wait();  // all CTAs have started
   if (ok) {
     constexpr int kHalf = NT / 2;
     const int c0 = warp < 4 ? 0 : kHalf, output = (warp & 3) * 32 + lane;
@@ -201,28 +204,41 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams p
     }
   }
   const int output = threadIdx.x % kFewOutputs, col = n0 + output;
-  float bias = 0.0f, col_scale = 1.0f;
-  if (col < p.N) {
-    if (p.bias) bias = to_float(static_cast<const T*>(p.bias)[col]);
-    if (F8) col_scale = scale_value(p.w_scale[col]);
-  }
   tc_fence_before();
-  cluster_sync();  // all sums are in place
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  // What the rows and columns need is read while the sums meet: behind the arrival, which
+  // would wait for it (0.2 us), and as it lies in memory.
+  uint16_t bias_bits = 0, next_res[2] = {0, 0};
+  uint8_t col_byte = 0, next_byte[2] = {0, 0};
+  if (col < p.N) {
+    if (p.bias) bias_bits = static_cast<const uint16_t*>(p.bias)[col];
+    if (F8) col_byte = p.w_scale[col];
+  }
+  auto read_rows = [&](int j) {
+    const int row = m0 + rank * own + 2 * j;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (j >= own / 2 || row + e >= p.M || col >= p.N) continue;
+      if (p.residual) next_res[e] = static_cast<const uint16_t*>(p.residual)[(row + e) * p.residual_stride + col];
+      if (F8) next_byte[e] = p.x_scale[row + e];
+    }
+  };
+  constexpr int kRowStep = kFewThreads / kFewOutputs;
+  read_rows(threadIdx.x / kFewOutputs);
+  cluster_wait();  // all sums are in place
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tacc, kColumns);
   }
-  for (int j = threadIdx.x / kFewOutputs; j < own / 2; j += kFewThreads / kFewOutputs) {
+  const uint64_t bias = unpack_pair<T>(bias_bits * 0x10001u);
+  for (int j = threadIdx.x / kFewOutputs; j < own / 2; j += kRowStep) {
     const int row = m0 + rank * own + 2 * j;
+    const uint32_t res = next_res[0] | static_cast<uint32_t>(next_res[1]) << 16;
+    const uint8_t row_byte[2] = {next_byte[0], next_byte[1]};
+    read_rows(j + kRowStep);
     if (!ok || row >= p.M || col >= p.N) continue;
     const bool second = row + 1 < p.M;
     const int64_t at = static_cast<int64_t>(row) * p.N + col;
-    float res[2] = {0.0f, 0.0f};
-    if (p.residual) {
-      const T* from = static_cast<const T*>(p.residual) + row * p.residual_stride + col;
-      res[0] = to_float(from[0]);
-      if (second) res[1] = to_float(from[p.residual_stride]);
-    }
     uint64_t v = pair_of(0.0f, 0.0f);
 #pragma unroll 8
     for (int c = 0; c < split; ++c) {
@@ -230,9 +246,9 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams p
       v = pair_add(v, pair_of(f.x, f.y));
     }
     if (F8)
-      v = pair_mul(pair_mul(v, pair_of(scale_value(p.x_scale[row]), second ? scale_value(p.x_scale[row + 1]) : 0.0f)),
-                   pair_of(col_scale, col_scale));
-    v = pair_add(v, pair_of(bias, bias));
+      v = pair_mul(pair_mul(v, pair_of(scale_value(row_byte[0]), scale_value(row_byte[1]))),
+                   pair_of(scale_value(col_byte), scale_value(col_byte)));
+    v = pair_add(v, bias);
     auto store = [&](void* base, uint64_t values) {
       const uint32_t w = pack_pair<T>(values);
       uint16_t* to = static_cast<uint16_t*>(base) + at;
@@ -243,7 +259,7 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams p
     if (p.act == HSTU_ACT_SILU) v = activate2<HSTU_ACT_SILU>(v);
     if (p.act == HSTU_ACT_GELU) v = activate2<HSTU_ACT_GELU>(v);
     if (p.act == HSTU_ACT_RELU) v = activate2<HSTU_ACT_RELU>(v);
-    if (p.residual) v = pair_add(v, pair_of(res[0], res[1]));
+    if (p.residual) v = pair_add(v, unpack_pair<T>(res));
     store(p.y, v);
   }
   if (threadIdx.x == 0 && s.abort_flag && p.header) atomicOr(p.header + kHdrErr, kErrTimeout);

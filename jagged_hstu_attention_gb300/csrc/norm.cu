@@ -12,7 +12,7 @@
 //             dx = rstd (t - u mean(t u)) + dh,  dgate = dy u weight,
 //             dweight = the sum over rows of dy gate u.
 //
-// A row lies in the registers of the 8 to 256 threads that share it, so it is
+// A row lies in the registers of the 8 to 512 threads that share it, so it is
 // read and written once, with one reduction (two for 8 bits) by shuffles and,
 // above 1024 columns, shared memory. Sums are in 32 bits. The backward's blocks
 // take rows in turn and keep their part of dweight in registers; the blocks'
