@@ -4,9 +4,10 @@
 //             whose epilogue holds everything else, 16-bit or 8-bit operands;
 //   backward  g = dy act'(z) and the column sums of g (one elementwise kernel, parts
 //             of row chunks added in order), then dx = g w and dw = g^T x on
-//             tcgen05. Without an activation g is dy itself, read in place. dw,
-//             whose K is the number of rows, splits K over the SMs; its fp32
-//             parts are added in order.
+//             tcgen05, whose operands have 16 bits: g is rounded to them, half a
+//             step of relative error in each term of the sums. Without an
+//             activation g is dy itself, read in place. dw, whose K is the number
+//             of rows, splits K over the SMs; its fp32 parts are added in order.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
