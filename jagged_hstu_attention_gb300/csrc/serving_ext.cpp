@@ -24,6 +24,8 @@
 
 #include <optional>
 #include <string>
+#include <tuple>
+#include <utility>
 
 #include "../../include/hstu_attn.h"
 

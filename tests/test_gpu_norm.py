@@ -223,3 +223,18 @@ def test_refusals():
         with pytest.raises(hb.HstuError) as e:
             call()
         assert e.value.status == status
+
+
+def test_codes_and_scales_outlive_each_other():
+    """They share a piece of memory, which either keeps; a later call's lie elsewhere."""
+    x = lt.randn((37, 48), BF, 5)
+    q = hb.quantise_rows(x)
+    codes, scale = q.codes.clone(), q.scale.clone()
+    later = [hb.quantise_rows(-x) for _ in range(20)]
+    assert torch.equal(q.codes, codes) and torch.equal(q.scale, scale)
+    assert q.codes.is_contiguous() and q.scale.is_contiguous() and q.scale.data_ptr() % 16 == 0
+    only_scale, only_codes = q.scale, later[0].codes
+    want = only_codes.clone()
+    del q, later
+    filler = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in (100, 37, 2000, 4000)]
+    assert torch.equal(only_scale, scale) and torch.equal(only_codes, want) and len(filler) == 4
