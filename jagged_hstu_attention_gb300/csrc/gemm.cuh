@@ -64,6 +64,7 @@ struct GemmSmem2 {
   alignas(8) uint64_t full[kStages<TN>], empty[kStages<TN>], acc_full[2], acc_empty[2], drain;
   uint32_t tmem_base;
   int abort_flag;
+  int issued[2];  // the leader's: stages that either CTA's producer loaded into
 };
 static_assert(sizeof(GemmSmem2<256>) + 1024 <= 232448 && sizeof(GemmSmem2<128>) + 1024 <= 232448, "over a CTA's shared memory");
 
@@ -88,6 +89,10 @@ __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
 }
 __device__ __forceinline__ void store_cluster(uint32_t addr, int v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+// Counts bytes that no copy brings as having come.
+__device__ __forceinline__ void mbar_complete_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 // 2-D load whose bytes are counted by a barrier of either CTA of the pair.
 __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
@@ -155,6 +160,24 @@ __device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
       "h"(static_cast<uint16_t>(3))
       : "memory");
+}
+
+// Waits until what the two producers loaded has landed, after an abort, which may have
+// stopped them a stage apart: the leader arms a stage for the bytes of both CTAs, and either
+// may be the one that issued its half alone. (No more than a stage of each barrier: a
+// stage is loaded again only after both halves of its last load were multiplied.)
+template <int RING>
+__device__ __forceinline__ void settle_copies(uint64_t* full, const int* issued, uint32_t half) {
+  const uint64_t t0 = globaltimer_ns();
+  for (int st = 0; st < RING; ++st) {
+    const uint32_t bar = smem_u32(&full[st]);
+    const int leader = (issued[0] - st + RING - 1) / RING, other = (issued[1] - st + RING - 1) / RING;  // loads
+    if (other > leader) mbar_expect_tx(bar, half);
+    if (other < leader) mbar_complete_tx(bar, half);
+    const int loads = max(leader, other);
+    while (loads > 0 && !mbar_test(bar, (loads - 1) & 1) && globaltimer_ns() - t0 < kWaitLimitNs) {
+    }
+  }
 }
 
 // Loads ROWS rows (K-major, a box) or columns (MN-major) of an operand, one K block deep.
@@ -290,8 +313,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads2, 1)
     if (lane == 0) {
       tma_prefetch_map(&p.tm_a);
       tma_prefetch_map(&p.tm_b);
-      int last[kRing];
-      for (int st = 0; st < kRing; ++st) last[st] = -1;
       int g = 0;
       bool ok = true;
       for (int t = pair; ok && t < n_tiles; t += pairs) {
@@ -309,18 +330,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads2, 1)
           const uint32_t bar = in_cta(smem_u32(&s.full[st]), 0);
           load_block<A_MN, KB, 128>(smem_u32(s.a[st]), &p.tm_a, bar, m0 + 128 * rank, kb);
           load_block<B_MN, KB, TN / 2>(smem_u32(s.b[st]), &p.tm_b, bar, n0 + TN / 2 * rank, kb);
-          last[st] = use;
         }
       }
-      // Never leave with a copy in flight: the leader waits for both CTAs', and
-      // the cluster barrier at the end keeps the other one.
-      if (rank == 0) {
-        const uint64_t t0 = globaltimer_ns();  // one limit for all: the other CTA may have stopped before a stage
-        for (int st = 0; st < kRing; ++st)
-          while (last[st] >= 0 && !mbar_test(smem_u32(&s.full[st]), last[st] & 1) &&
-                 globaltimer_ns() - t0 < kWaitLimitNs) {
-          }
-      }
+      store_cluster(in_cta(smem_u32(&s.issued[rank]), 0), g);
     }
     __syncwarp();
   } else if (warp == kEpiWarps + 1) {
@@ -333,10 +345,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads2, 1)
         int m0, n0, split, kb0, kb1;
         tile_of(t, m0, n0, split, kb0, kb1);
         const int buf = i & 1;
-        // accumulator buf is free once both CTAs have read out tile i - 2
-        if (i >= 2 && !mbar_wait(smem_u32(&s.acc_empty[buf]), ((i >> 1) - 1) & 1, abort_flag, p.handoff_limit_ns)) {
-          ok = false;
-          break;
+        // accumulator buf is free once both CTAs have read out tile i - 2 (a limit of 1 ns, set only by a
+        // test, gives up at once, with copies and MMAs in flight)
+        if (i >= 2) {
+          if (p.handoff_limit_ns <= 1) *abort_flag = 1;
+          ok = p.handoff_limit_ns > 1 && mbar_wait(smem_u32(&s.acc_empty[buf]), ((i >> 1) - 1) & 1, abort_flag, p.handoff_limit_ns);
+          if (!ok) break;
         }
         tc_fence_after();
         const uint32_t tacc = tbase + buf * TN;
@@ -509,10 +523,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads2, 1)
   }
   tc_fence_before();
   __syncthreads();
-  // The last arrival that the leader's MMAs send here.
-  if (rank == 1 && threadIdx.x == 0) mbar_wait_drain(smem_u32(&s.drain), 0);
+  if (threadIdx.x == 0) {
+    if (rank == 1) mbar_wait_drain(smem_u32(&s.drain), 0);  // the last arrival that the leader's MMAs send here
+    if (*abort_flag) store_cluster(peer_abort, 1);
+  }
   __syncthreads();
-  cluster_sync();  // nobody leaves while the other CTA's MMAs, copies or arrivals may reach it
+  cluster_sync();  // nobody leaves while the other CTA's MMAs or arrivals may reach it; the flags are equal
+  if (*abort_flag) {
+    // Never leave with a copy in flight. (Without an abort the MMAs have waited for every one.)
+    if (rank == 0 && threadIdx.x == 0) settle_copies<kRing>(s.full, s.issued, kStageA + kStageB<TN>);
+    cluster_sync();
+  }
   if (warp == kEpiWarps + 1) {
     tc_fence_after();
     tmem_dealloc_pair(tbase, 2 * TN);
