@@ -42,6 +42,7 @@ struct FewParams {
   int64_t k_bytes;                    // of a row
   int32_t M, N, act;
   int32_t stages;
+  bool give_up;  // a test's: waits for products give up at once, with copies and MMAs in flight
 };
 
 inline int64_t few_tiles(int64_t rows, int outputs, int tile_rows) {
@@ -49,7 +50,7 @@ inline int64_t few_tiles(int64_t rows, int outputs, int tile_rows) {
 }
 
 struct FewSmem {  // the stages and the sums of others lie behind
-  uint64_t done[kFewMostStages];
+  uint64_t done[kFewMostStages], drain;
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -130,6 +131,7 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams p
   if (threadIdx.x == 0) {
     s.abort_flag = 0;
     for (int i = 0; i < p.stages; ++i) mbar_init(smem_u32(&s.done[i]), 1);
+    mbar_init(smem_u32(&s.drain), 1);
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -175,15 +177,23 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams p
     }
     __syncwarp();
     // The block before has been multiplied: its stage takes the next one to come.
-    if (j > 0) ok = mbar_wait(smem_u32(&s.done[before]), before_phase, &s.abort_flag);
+    if (j > 0) ok = !p.give_up && mbar_wait(smem_u32(&s.done[before]), before_phase, &s.abort_flag);
     if (ok) load();
     before = st;
     before_phase = phase;
     if (++st == p.stages) st = 0, phase ^= 1;
   }
   copy_wait_all_but(0);
-  if (ok) ok = mbar_wait(smem_u32(&s.done[before]), before_phase, &s.abort_flag);
+  if (ok) ok = !p.give_up && mbar_wait(smem_u32(&s.done[before]), before_phase, &s.abort_flag);
   ok = __syncthreads_and(ok);
+  if (!ok) {  // MMAs may be on their way still
+    if (warp == 0 && elect_one_sync()) {
+      s.abort_flag = 1;
+      umma_commit(smem_u32(&s.drain));
+      mbar_wait_drain(smem_u32(&s.drain), 0);
+    }
+    __syncthreads();
+  }
   tc_fence_after();
   // Rows [c own, (c + 1) own) of the tile are CTA c's: sums of pairs of rows, an output
   // a lane; warps 4 to 7 take the second half of the columns.

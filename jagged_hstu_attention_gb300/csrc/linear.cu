@@ -376,6 +376,7 @@ HSTU_API hstu_status_t hstu_attn_linear(const void* x, int64_t x_stride, const u
     p.x_stride = x_stride * xe;
     p.residual_stride = residual_stride;
     p.k_bytes = int64_t{d_in} * xe;
+    p.give_up = handoff_limit() <= 1;
     p.M = static_cast<int32_t>(rows);
     p.N = d_out;
     p.act = act;
@@ -477,6 +478,7 @@ HSTU_API hstu_status_t hstu_attn_linear_bwd(const void* dy, int64_t dy_stride, c
     fp.header = p.header;
     fp.x_stride = g_stride * 2;
     fp.k_bytes = int64_t{d_out} * 2;
+    fp.give_up = handoff_limit() <= 1;
     fp.M = static_cast<int32_t>(rows);
     fp.N = d_in;
     fp.act = HSTU_ACT_NONE;

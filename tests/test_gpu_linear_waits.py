@@ -55,3 +55,31 @@ def test_a_backward_that_gives_up_leaves_together():
     for a, b in zip(want, call()):
         assert torch.equal(a, b)
     assert hb.device_status(ws) == hb.HSTU_OK
+
+
+# A CTA or several to a cluster, a K block to a CTA or more than it has stages for, tiles of 16, 32 and 64 rows.
+@pytest.mark.parametrize("T,K,N,codes", [(1, 64, 8, False), (64, 512, 2048, False), (7, 8192, 264, False),
+                                         (64, 4096, 4096, False), (33, 4096, 1032, True)])
+def test_few_rows_that_give_up(T, K, N, codes):
+    x, w = lt.randn((T, K), F16, 1), lt.randn((N, K), F16, 2, K ** -0.5)
+    if codes:
+        x, w = hb.quantise_rows(x), hb.quantise_rows(w)
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    call = lambda: hb.linear(x, w, act="gelu", dtype=F16, ws=ws)[0]  # noqa: E731
+    want = call()
+    assert hb.device_status(ws) == hb.HSTU_OK
+    assert _given_up(call, ws, 20) < 1.0
+    assert torch.equal(want, call()) and hb.device_status(ws) == hb.HSTU_OK
+
+
+@pytest.mark.parametrize("T,K,N", [(1, 64, 8), (64, 512, 2048), (40, 2048, 1000)])
+def test_a_backward_of_few_rows_that_gives_up(T, K, N):
+    x, w, dy = lt.randn((T, K), BF, 1), lt.randn((N, K), BF, 2, K ** -0.5), lt.randn((T, N), BF, 3)
+    ws = hb.linear_workspace(T, K, N)
+    call = lambda: hb.linear_bwd(dy, None, x, w, ws=ws)  # noqa: E731
+    want = call()
+    assert hb.device_status(ws) == hb.HSTU_OK
+    assert _given_up(call, ws, 20) < 1.0
+    for a, b in zip(want, call()):
+        assert torch.equal(a, b)
+    assert hb.device_status(ws) == hb.HSTU_OK
