@@ -616,9 +616,9 @@ HSTU_API hstu_status_t hstu_attn_linear(const void* x, int64_t x_stride, const u
  * is out of range. */
 HSTU_API size_t hstu_attn_linear_workspace_size(int64_t rows, int32_t d_in, int32_t d_out, int32_t act);
 
-/* Gradients of hstu_attn_linear with 16-bit operands: g = dy act'(z), rounded to
- * dtype, dx = g w, dw = g^T x, dbias = the sum of g's rows. (The residual's
- * gradient is dy.)
+/* Gradients of hstu_attn_linear with 16-bit operands: g = dy act'(z), dx = g w and
+ * dw = g^T x with g rounded to dtype, dbias = the sum of g's rows in 32 bits. (The
+ * residual's gradient is dy.)
  *   z        (rows, d_out) of the forward; NULL and not read with HSTU_ACT_NONE
  *   dx       (rows, d_in), dw (d_out, d_in), dbias (d_out) or NULL, of dtype
  *   ws       hstu_attn_linear_workspace_size() bytes, 256-byte aligned, one for

@@ -5,7 +5,8 @@
 //   backward  g = dy act'(z) and the column sums of g (one elementwise kernel, parts
 //             of row chunks added in order), then dx = g w and dw = g^T x on
 //             tcgen05, whose operands have 16 bits: g is rounded to them, half a
-//             step of relative error in each term of the sums. Without an
+//             step of relative error in each term of their sums. (The column sums, the bias
+//             gradient, are of g in 32 bits.) Without an
 //             activation g is dy itself, read in place. dw, whose K is the number
 //             of rows, splits K over the SMs; its fp32 parts are added in order.
 #include <cudaTypedefs.h>
@@ -97,42 +98,43 @@ __global__ void __launch_bounds__(kGradThreads, 4) linear_grad_kernel(const Grad
   const int64_t step = int64_t{rpi} * gridDim.x, per = (p.rows + step - 1) / step * rpi;
   const int64_t r0 = static_cast<int64_t>(blockIdx.x) * per, r1 = min(r0 + per, p.rows);
   uint64_t sums[4] = {};
-  auto one = [&](uint4 zv, uint4 dv, int64_t r) {
-    if (ACT != HSTU_ACT_NONE) {
-      dv = make_uint4(pack_pair<T>(act_grad2<ACT>(unpack_pair<T>(zv.x), unpack_pair<T>(dv.x))),
-                      pack_pair<T>(act_grad2<ACT>(unpack_pair<T>(zv.y), unpack_pair<T>(dv.y))),
-                      pack_pair<T>(act_grad2<ACT>(unpack_pair<T>(zv.z), unpack_pair<T>(dv.z))),
-                      pack_pair<T>(act_grad2<ACT>(unpack_pair<T>(zv.w), unpack_pair<T>(dv.w))));
-      *reinterpret_cast<uint4*>(static_cast<T*>(p.g) + r * p.cols + col) = dv;
-    }
-    // the sums are those of the g that the products read
-    sums[0] = pair_add(sums[0], unpack_pair<T>(dv.x));
-    sums[1] = pair_add(sums[1], unpack_pair<T>(dv.y));
-    sums[2] = pair_add(sums[2], unpack_pair<T>(dv.z));
-    sums[3] = pair_add(sums[3], unpack_pair<T>(dv.w));
-  };
-  if (active) {
-    const T* dy = static_cast<const T*>(p.dy) + col;
-    const T* z = static_cast<const T*>(p.z) + col;
-    auto load_z = [&](int64_t r) {
-      return ACT != HSTU_ACT_NONE ? *reinterpret_cast<const uint4*>(z + r * p.cols) : make_uint4(0, 0, 0, 0);
+  auto one = [&](uint4 zv, uint4 dv, int64_t to) {
+    // the sums are those of g in 32 bits; only the products' operand is rounded
+    auto two = [&](int e, uint32_t zw, uint32_t dw) {
+      const uint64_t g = act_grad2<ACT>(unpack_pair<T>(zw), unpack_pair<T>(dw));
+      sums[e] = pair_add(sums[e], g);
+      return pack_pair<T>(g);
     };
-    auto some = [&](int64_t r, auto all) {  // kGradRows rows, or those there are
+    dv.x = two(0, zv.x, dv.x);
+    dv.y = two(1, zv.y, dv.y);
+    dv.z = two(2, zv.z, dv.z);
+    dv.w = two(3, zv.w, dv.w);
+    if (ACT != HSTU_ACT_NONE) *reinterpret_cast<uint4*>(static_cast<T*>(p.g) + to) = dv;
+  };
+  if (active && r0 + lane_row < r1) {
+    // Of the thread's next row; its rows are rpi apart.
+    int64_t at = (r0 + lane_row) * p.cols + col, dy_at = (r0 + lane_row) * p.dy_stride + col;
+    const int64_t at_step = int64_t{rpi} * p.cols, dy_step = rpi * p.dy_stride;
+    int left = static_cast<int>((r1 - r0 - lane_row + rpi - 1) / rpi);
+    auto some = [&](auto all) {  // kGradRows rows, or those there are
       uint4 zv[kGradRows], dv[kGradRows];
 #pragma unroll
       for (int k = 0; k < kGradRows; ++k) {
-        const int64_t row = r + k * rpi;
-        if (!all && row >= r1) break;
-        zv[k] = load_z(row);
-        dv[k] = *reinterpret_cast<const uint4*>(dy + row * p.dy_stride);
+        if (!all && k >= left) break;
+        zv[k] = make_uint4(0, 0, 0, 0);
+        if (ACT != HSTU_ACT_NONE) zv[k] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.z) + at + k * at_step);
+        dv[k] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.dy) + dy_at + k * dy_step);
       }
 #pragma unroll
       for (int k = 0; k < kGradRows; ++k)
-        if (all || r + k * rpi < r1) one(zv[k], dv[k], r + k * rpi);
+        if (all || k < left) one(zv[k], dv[k], at + k * at_step);
     };
-    int64_t r = r0 + lane_row;
-    for (; r + (kGradRows - 1) * rpi < r1; r += kGradRows * rpi) some(r, std::true_type{});
-    if (r < r1) some(r, std::false_type{});
+    for (; left >= kGradRows; left -= kGradRows) {
+      some(std::true_type{});
+      at += kGradRows * at_step;
+      dy_at += kGradRows * dy_step;
+    }
+    if (left > 0) some(std::false_type{});
   }
   float sum[8];
 #pragma unroll
