@@ -516,6 +516,7 @@ HSTU_API hstu_status_t hstu_attn_fwd_paged(const void* q_c, int64_t q_stride, vo
  *   table    DEVICE (vocab, dim) of table_dtype: that of the rows, or
  *            HSTU_DTYPE_F32
  *   ids      DEVICE (tokens), int32 or int64 (id_bytes 4 or 8)
+ *   scale    finite
  *   out      DEVICE (tokens, dim) of dtype
  *   ws       256 bytes or NULL: with it, an id of vocab or more sets
  *            HSTU_ERR_DEVICE_INPUT in the error word; its row is 0 either way

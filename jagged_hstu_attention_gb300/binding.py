@@ -770,7 +770,8 @@ def _act_code(act: str) -> int:
 def embed(table, ids, scale: float = 1.0, dtype=None, out=None, ws: Optional[torch.Tensor] = None, stream=None):
     """(T, D): ``scale * table[ids]`` (hstu_attn_embed). The table is (V, D), of the
     rows' type or float32 (the rows are then of ``dtype``, bf16 if it is not
-    given); ids are int32 or int64, below 0 for padding, whose rows are zeros.
+    given); ids are int32 or int64, below 0 for padding, whose rows are zeros; the
+    scale is finite.
     With a ``ws`` (256 bytes) ids past the table are reported by
     ``device_status``; their rows are zeros too."""
     if stream is not None:
