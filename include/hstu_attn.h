@@ -596,7 +596,9 @@ HSTU_API hstu_status_t hstu_attn_rms_norm_bwd(const void* dy, int64_t dy_stride,
  *   x        (rows, d_in), w (d_out, d_in) contiguous: of dtype, x_scale and
  *            w_scale NULL; or 8-bit floats (e4m3) of the rows of x and of w under
  *            the scales 2^(x_scale - 127) (rows) and 2^(w_scale - 127) (d_out, 16-byte
- *            aligned), as hstu_attn_rms_norm and hstu_attn_quantise_rows write them
+ *            aligned), as hstu_attn_rms_norm and hstu_attn_quantise_rows write them;
+ *            the sums take w's scale first, in fp32: exact for w_scale of 19 to 221
+ *            (2^-108 to 2^94; rows of zeros have 0), whatever x_scale is
  *   bias     (d_out) of dtype, or NULL; residual (rows, d_out) of dtype, or NULL
  *   act      HSTU_ACT_*
  *   y        (rows, d_out) of dtype; z the same or NULL (a backward with an

@@ -472,9 +472,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads2, 1)
               const uint32_t bw[4] = {bias.x, bias.y, bias.z, bias.w};
 #pragma unroll
               for (int g = 0; g < 4; ++g) {
-                if (F8) {
-                  v[g] = pair_mul(v[g], pair_of(row_scale[k], row_scale[k]));
+                if (F8) {  // by w's scale first: a row of x may hold a mask's lowest value, which alone passes 2^127
                   v[g] = pair_mul(v[g], pair_of(scale_value(col_scale[g] & 0xffu), scale_value(col_scale[g] >> 8)));
+                  v[g] = pair_mul(v[g], pair_of(row_scale[k], row_scale[k]));
                 }
                 v[g] = pair_add(v[g], unpack_pair<T>(bw[g]));
               }

@@ -255,9 +255,9 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams p
       const float2 f = meet[(c * own / 2 + j) * kFewOutputs + output];
       v = pair_add(v, pair_of(f.x, f.y));
     }
-    if (F8)
-      v = pair_mul(pair_mul(v, pair_of(scale_value(row_byte[0]), scale_value(row_byte[1]))),
-                   pair_of(scale_value(col_byte), scale_value(col_byte)));
+    if (F8)  // by w's scale first, as in the pair kernel
+      v = pair_mul(pair_mul(v, pair_of(scale_value(col_byte), scale_value(col_byte))),
+                   pair_of(scale_value(row_byte[0]), scale_value(row_byte[1])));
     v = pair_add(v, bias);
     auto store = [&](void* base, uint64_t values) {
       const uint32_t w = pack_pair<T>(values);
