@@ -37,3 +37,42 @@ def test_bias_gradient_of_terms_below_the_smallest_half():
     db = lt.f64(hb.linear_bwd(dy, z, x, w, act="silu")[2])
     ref = T * 2.0 ** -24 * float(lt.act_grad(np.float64(-0.5), "silu"))  # 6.3e-5, a normal fp16 number
     assert np.abs(db - ref).max() <= 2.0 ** -11 * ref + 1e-5 * ref
+
+
+def _whole(shape, top, dtype, seed, stride=None):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    wide = torch.randint(-top, top + 1, (shape[0], stride or shape[1]), generator=g, device="cuda").to(dtype)
+    return wide[:, :shape[1]]
+
+
+# rows, d_in, d_out: splits of dw's K from 1 to 65 and slices of the fold from 1 to 16, chunks of the bias
+# gradient from 1 to 608, K blocks and tiles that are not full; few rows and many.
+WHOLE = [(41000, 256, 136), (20000, 40, 8), (9001, 512, 200), (5000, 72, 1032), (4500, 520, 96), (4097, 504, 328),
+         (81920, 64, 64), (61, 72, 2584), (700, 16, 1056), (64, 512, 2048), (1, 8, 8), (65, 4096, 264)]
+
+
+@pytest.mark.parametrize("T,K,N", WHOLE)
+@pytest.mark.parametrize("act,dtype", [("none", BF), ("relu", F16), ("relu", BF)])
+def test_gradients_of_whole_numbers(T, K, N, act, dtype):
+    """Every sum is below 2^24 in magnitude, term by term, and so exact in fp32 in any order: one
+    rounding, the output's, is all that may differ, and a lost or doubled row shows."""
+    x, w = _whole((T, K), 2, dtype, 1, K + 8), _whole((N, K), 2, dtype, 2)
+    dy, z = _whole((T, N), 2, dtype, 3, N + 16), _whole((T, N), 1, dtype, 4)
+    assert 4 * max(T, N) < 1 << 24
+    dx, dw, db = hb.linear_bwd(dy, z, x, w, act=act)
+    g = dy.double() * (z > 0) if act == "relu" else dy.double()
+    assert torch.equal(dx, (g @ w.double()).to(dtype))
+    assert torch.equal(dw, (g.t() @ x.double()).to(dtype))
+    assert torch.equal(db, g.sum(0).to(dtype))
+
+
+@pytest.mark.parametrize("T,K,N", [(1, 8, 8), (64, 512, 2048), (7, 8192, 264), (64, 4096, 1032), (300, 1032, 1000),
+                                   (5000, 72, 1032), (1000, 8192, 520), (40000, 264, 136)])
+@pytest.mark.parametrize("dtype", [BF, F16])
+def test_products_of_whole_numbers(T, K, N, dtype):
+    x, w, b, r = _whole((T, K), 2, dtype, 5, K + 8), _whole((N, K), 2, dtype, 6), _whole((1, N), 9, dtype, 7)[0], \
+        _whole((T, N), 9, dtype, 8, N + 8)
+    y, z = hb.linear(x, w, bias=b, act="relu", residual=r, want_z=True)
+    ref = x.double() @ w.double().t() + b.double()
+    assert torch.equal(z, ref.to(dtype)) and torch.equal(y, (ref.clamp(min=0) + r.double()).to(dtype))
