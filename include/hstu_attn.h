@@ -530,8 +530,9 @@ HSTU_API hstu_status_t hstu_attn_embed(const void* table, int32_t table_dtype, i
 HSTU_API size_t hstu_attn_embed_workspace_size(int64_t tokens, int64_t vocab, int32_t dim);
 
 /* Gradient of the table: dtable[v] = scale * the sum of dy[t] over the tokens t
- * with ids[t] = v, in 32 bits and in the tokens' order, rounded once to grad_dtype
- * (the rows' type, or HSTU_DTYPE_F32). Padding and ids of vocab or more are left
+ * with ids[t] = v, in 32 bits, rounded once to grad_dtype (the rows' type, or
+ * HSTU_DTYPE_F32). The order of the sum is fixed by ids, tokens and dim: that of the
+ * tokens, in parts of 16 to 128 that are added in theirs where there are many. Padding and ids of vocab or more are left
  * out, the latter set HSTU_ERR_DEVICE_INPUT in ws. Rows that no token names
  * are 0. With accumulate = 1 (HSTU_DTYPE_F32 only) the sums are added to what
  * dtable holds, and rows that no token names are neither read nor written.
@@ -670,9 +671,10 @@ HSTU_API hstu_status_t hstu_attn_test_wait_timeout(void* ws, int32_t limit_ms, v
  * then raises its abort flag, every role drains what it issued (bounded
  * waits), TMEM is freed and the workspace error word gets HSTU_ERR_TIMEOUT --
  * no fault, no hang, the context stays usable.
- * With 1 ns hstu_attn_fwd_paged's waits for products on tensor memory give up
- * too, in each sequence's last group of 64 candidates; longer limits leave
- * them as they are.
+ * It is also the limit of the wait for an accumulator in hstu_attn_linear and
+ * hstu_attn_linear_bwd. With 1 ns their waits for products of few rows give up too,
+ * and those of hstu_attn_fwd_paged for products on tensor memory, in each
+ * sequence's last group of 64 candidates; longer limits leave these as they are.
  *   limit_ns: 1 .. 2e9; 0 restores the kernels' normal limit (2 s).
  * Process-wide and meant for tests only; returns HSTU_ERR_INVALID_ARG above
  * 2e9. */

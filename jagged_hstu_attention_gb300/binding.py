@@ -504,7 +504,8 @@ def project_workspace(num_rows: int, d_in: int, d_out: int, backward: bool, devi
 
 def project_rows(x, w, rows=None, bias=None, want_z=True, ws=None, stream=None):
     """(y, z) = (silu(x[rows] w^T + bias), x[rows] w^T + bias) on the
-    listed rows of x (all rows if ``rows`` is None), hstu_attn_project_rows.
+    listed rows of x (all rows if ``rows`` is None, which ``linear`` with act
+    "silu" does faster), hstu_attn_project_rows.
     x (T, d_in), w (d_out, d_in), one dtype (bf16 or fp16)."""
     _need(x, _FLOATS, "x")
     _need(w, _FLOATS, "w")
@@ -546,8 +547,9 @@ def project_rows_bwd(dy, z, x, w, rows=None, want_dbias=True, ws=None, stream=No
 
 def set_handoff_limit_for_tests(limit_ns: int) -> None:
     """Test hook (hstu_attn_test_set_handoff_limit): shortens the attention
-    kernels' accumulator hand-off wait, and with 1 ns makes ``fwd_paged``'s waits
-    on tensor memory give up; 0 restores the normal limits."""
+    kernels' and the linear maps' accumulator hand-off wait, and with 1 ns makes the
+    waits of ``fwd_paged`` and of ``linear`` of few rows on tensor memory give up;
+    0 restores the normal limits."""
     _check(load().hstu_attn_test_set_handoff_limit(int(limit_ns)), "hstu_attn_test_set_handoff_limit")
 
 

@@ -96,8 +96,8 @@ bool make_map(CUtensorMap* m, const void* ptr, int64_t tokens, int heads, int di
 
 hstu_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA; }
 
-// Limit of the attention kernels' accumulator hand-off wait; 0 = the
-// kernels' normal limit. Only hstu_attn_test_set_handoff_limit changes it.
+// Limit of the attention kernels' and the linear maps' accumulator hand-off
+// wait; 0 = the kernels' normal limit. Only hstu_attn_test_set_handoff_limit changes it.
 std::atomic<uint64_t> g_handoff_limit_ns{0};
 
 // Upper bound on the number of (sequence, tile) work items.

@@ -2,8 +2,8 @@
 //
 //   forward   y[t] = scale * table[ids[t]], zeros for an id below 0 (padding);
 //   backward  dtable[v] = scale * the sum of dy[t] over the tokens with ids[t]
-//             = v, in the tokens' order, summed in 32 bits without atomics, so
-//             that two runs agree bit for bit.
+//             = v, summed in 32 bits in an order that the sorted tokens fix,
+//             without atomics, so that two runs agree bit for bit.
 //
 // The backward sorts the tokens by id (stable, by digits of at most 9 bits from
 // the lowest up), which puts the rows of one id next to each other, and then

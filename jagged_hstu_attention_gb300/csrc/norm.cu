@@ -345,8 +345,9 @@ __global__ void __launch_bounds__(1024) norm_fold_kernel(const float* part, int 
 // Threads of a row and chunks a thread. Forward: the fewest threads whose registers
 // hold the row, so that reductions stay inside a warp up to 1024 columns and take few
 // warps above (16381 rows of 2048 with a residual into 8 bits: 36 us, 42 us with a chunk
-// a thread); 8 and 16 threads for heads, where a whole warp would leave most of its
-// lanes without columns.
+// a thread); 8 and 16 threads for narrow rows (heads of 64 and 128, of a contiguous (T, H, D)
+// tensor seen as T H rows), where a whole warp would leave most of its lanes without
+// columns.
 // The backward holds up to four rows and its part of dweight besides: one or two
 // chunks a thread, so that several blocks fit an SM (32749 rows of 1024, with a gate:
 // 72 us with four chunks a lane and one block an SM, 65 us with a chunk a thread, 62 us with
