@@ -76,3 +76,21 @@ def test_products_of_whole_numbers(T, K, N, dtype):
     y, z = hb.linear(x, w, bias=b, act="relu", residual=r, want_z=True)
     ref = x.double() @ w.double().t() + b.double()
     assert torch.equal(z, ref.to(dtype)) and torch.equal(y, (ref.clamp(min=0) + r.double()).to(dtype))
+
+
+def test_gradients_of_whole_numbers_past_two_to_the_31_values():
+    """With an activation, whose g and column sums have offsets past 32 bits too."""
+    T, K, N = 1100000, 16, 2048
+    g = torch.Generator(device="cuda").manual_seed(9)
+    dy = torch.randint(-1, 2, (T, N), generator=g, device="cuda", dtype=torch.int8).to(BF)
+    z = torch.randint(-1, 2, (T, N), generator=g, device="cuda", dtype=torch.int8).to(BF)
+    x, w = _whole((T, K), 1, BF, 10), _whole((N, K), 2, BF, 11)
+    dx, dw, db = hb.linear_bwd(dy, z, x, w, act="relu")
+    sums, products = torch.zeros(N, dtype=torch.float64, device="cuda"), torch.zeros((N, K), dtype=torch.float64, device="cuda")
+    for t in range(0, T, 100000):
+        part = slice(t, t + 100000)
+        d = dy[part].double() * (z[part] > 0)
+        sums += d.sum(0)
+        products += d.t() @ x[part].double()
+        assert torch.equal(dx[part], (d @ w.double()).to(BF))
+    assert torch.equal(db, sums.to(BF)) and torch.equal(dw, products.to(BF))
