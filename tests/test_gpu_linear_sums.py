@@ -94,3 +94,16 @@ def test_gradients_of_whole_numbers_past_two_to_the_31_values():
         products += d.t() @ x[part].double()
         assert torch.equal(dx[part], (d @ w.double()).to(BF))
     assert torch.equal(db, sums.to(BF)) and torch.equal(dw, products.to(BF))
+
+
+@pytest.mark.parametrize("T,K,N", [(1, 16, 8), (64, 512, 2048), (7, 8192, 264), (300, 1040, 1000), (1000, 8192, 520),
+                                   (20000, 2064, 136)])
+def test_eight_bit_products_of_whole_numbers(T, K, N):
+    """Under scales of powers of two that differ from row to row."""
+    codes = lambda shape, seed: _whole(shape, 8, F16, seed).to(torch.float8_e4m3fn).view(torch.uint8)  # noqa: E731
+    g = torch.Generator(device="cuda").manual_seed(12)
+    scale = lambda n: torch.randint(120, 135, (n,), generator=g, device="cuda", dtype=torch.uint8)  # noqa: E731
+    qx, qw = hb.QuantisedRows(codes((T, K), 13), scale(T)), hb.QuantisedRows(codes((N, K), 14), scale(N))
+    value = lambda q: q.codes.view(torch.float8_e4m3fn).double() * torch.exp2(q.scale.double() - 127)[:, None]  # noqa: E731
+    y, _ = hb.linear(qx, qw, dtype=BF)
+    assert torch.equal(y, (value(qx) @ value(qw).t()).float().to(BF))
