@@ -532,10 +532,11 @@ HSTU_API size_t hstu_attn_embed_workspace_size(int64_t tokens, int64_t vocab, in
 /* Gradient of the table: dtable[v] = scale * the sum of dy[t] over the tokens t
  * with ids[t] = v, in 32 bits, rounded once to grad_dtype (the rows' type, or
  * HSTU_DTYPE_F32). The order of the sum is fixed by ids, tokens and dim: that of the
- * tokens, in parts of 16 to 128 that are added in theirs where there are many. Padding and ids of vocab or more are left
- * out, the latter set HSTU_ERR_DEVICE_INPUT in ws. Rows that no token names
- * are 0. With accumulate = 1 (HSTU_DTYPE_F32 only) the sums are added to what
- * dtable holds, and rows that no token names are neither read nor written.
+ * tokens, in parts of 16 to 128 that are added in theirs where there are many.
+ * Padding and ids of vocab or more are left out, the latter set
+ * HSTU_ERR_DEVICE_INPUT in ws. Rows that no token names are 0. With
+ * accumulate = 1 (HSTU_DTYPE_F32 only) the sums are added to what dtable holds, and
+ * rows that no token names are neither read nor written.
  *   ws       hstu_attn_embed_workspace_size() bytes, 256-byte aligned, one for
  *            each of the calls that may run at the same time */
 HSTU_API hstu_status_t hstu_attn_embed_bwd(const void* dy, int64_t dy_stride, int32_t dtype, const void* ids,

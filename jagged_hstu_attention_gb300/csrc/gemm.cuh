@@ -348,8 +348,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads2, 1)
         // accumulator buf is free once both CTAs have read out tile i - 2 (a limit of 1 ns, set only by a
         // test, gives up at once, with copies and MMAs in flight)
         if (i >= 2) {
-          if (p.handoff_limit_ns <= 1) *abort_flag = 1;
-          ok = p.handoff_limit_ns > 1 && mbar_wait(smem_u32(&s.acc_empty[buf]), ((i >> 1) - 1) & 1, abort_flag, p.handoff_limit_ns);
+          ok = p.handoff_limit_ns > 1;
+          if (!ok) *abort_flag = 1;
+          ok = ok && mbar_wait(smem_u32(&s.acc_empty[buf]), ((i >> 1) - 1) & 1, abort_flag, p.handoff_limit_ns);
           if (!ok) break;
         }
         tc_fence_after();
@@ -472,7 +473,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads2, 1)
               const uint32_t bw[4] = {bias.x, bias.y, bias.z, bias.w};
 #pragma unroll
               for (int g = 0; g < 4; ++g) {
-                if (F8) {  // by w's scale first: a row of x may hold a mask's lowest value, which alone passes 2^127
+                if (F8) {  // w's scale first: that of a row with a mask's lowest value is 2^120, too much for a sum
                   v[g] = pair_mul(v[g], pair_of(scale_value(col_scale[g] & 0xffu), scale_value(col_scale[g] >> 8)));
                   v[g] = pair_mul(v[g], pair_of(row_scale[k], row_scale[k]));
                 }
