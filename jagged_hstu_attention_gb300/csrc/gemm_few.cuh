@@ -42,7 +42,7 @@ struct FewParams {
   int64_t k_bytes;                    // of a row
   int32_t M, N, act;
   int32_t stages;
-  bool give_up;  // a test's: waits for products give up at once, with copies and MMAs in flight
+  bool give_up;  // a test's: the wait for the last products gives up at once, with MMAs in flight
 };
 
 inline int64_t few_tiles(int64_t rows, int outputs, int tile_rows) {
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams p
     }
     __syncwarp();
     // The block before has been multiplied: its stage takes the next one to come.
-    if (j > 0) ok = !p.give_up && mbar_wait(smem_u32(&s.done[before]), before_phase, &s.abort_flag);
+    if (j > 0) ok = mbar_wait(smem_u32(&s.done[before]), before_phase, &s.abort_flag);
     if (ok) load();
     before = st;
     before_phase = phase;
